@@ -337,6 +337,13 @@ int fill_device_args(GemmArgs &g) {
     g.encode = g_encode;
     return SGEMM_OK;
 }
+
+int stream_workspace(size_t bytes, cudaStream_t s, void **out) {
+    float *p = nullptr;
+    const int rc = workspace(bytes, s, &p);
+    if (rc == SGEMM_OK) *out = p;
+    return rc;
+}
 }  // namespace sgemm_gb300
 
 extern "C" {
@@ -399,8 +406,8 @@ const char *sgemm_status_string(int status) {
             return "the stream is being captured and the call needs a larger workspace; "
                    "run one call of this shape eagerly on the stream first";
         case SGEMM_ERR_TOO_LARGE:
-            return "problem needs more than the fixed scratch of sgemm_noalloc "
-                   "(K * round_up(M, 4) floats > 16777216)";
+            return "problem beyond a fixed limit of the entry point: the fixed scratch of sgemm_noalloc "
+                   "(K * round_up(M, 4) floats > 16777216), or sgemm_q8_moe's tokens, experts or top_k";
         default: return "unknown status";
     }
 }
@@ -497,6 +504,6 @@ int sgemm_kernel_timing_result(double *total_ms, int64_t *launches) {
     return kernel_timing_result(total_ms, launches) ? SGEMM_OK : SGEMM_ERR_CUDA;
 }
 
-int sgemm_version(void) { return 100; }
+int sgemm_version(void) { return 200; }
 
 }  // extern "C"

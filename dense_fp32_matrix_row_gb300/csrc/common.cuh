@@ -125,6 +125,9 @@ bool release_host_paths();
 // Fills g.err, g.wait_ns, g.sm_count and g.encode for the current device
 // (setting the device up on first use); returns an SGEMM_* status.
 int fill_device_args(GemmArgs &g);
+// The workspace of (current device, s), at least `bytes` large and 256-byte
+// aligned; returns an SGEMM_* status.
+int stream_workspace(size_t bytes, cudaStream_t s, void **out);
 
 
 #ifdef __CUDACC__

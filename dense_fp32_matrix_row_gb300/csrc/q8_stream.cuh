@@ -1,0 +1,171 @@
+// q8_stream.cuh -- one warp's share of an 8-bit product that streams 16 weight
+// rows past a few token rows (used by the linear product at few tokens and by
+// the expert layer).
+//
+// mma.sync m16n8k16 on FP16 operands expanded from the 8-bit values in
+// registers (exact, see q8_to_f16), FP32 accumulation flushed into 32-bit
+// integers every 1024 k: up to there |sum| <= 1024 * 128 * 128 = 2^24, so
+// every FP32 partial sum is exact.
+//
+// The order of k inside an MMA is free as long as both operands share it.
+// Lane t of a quad therefore takes 16 consecutive bytes of its row per step of
+// 64 k (one 128-bit load each of weight rows g and g + 8 and of token g), and
+// word s of those bytes feeds MMA s of the step: no shared memory, no shuffles.
+#pragma once
+
+#include "q8.cuh"
+
+namespace sgemm_gb300 {
+
+#ifdef __CUDACC__
+
+constexpr int kQ8Step = 64;          // k per step
+constexpr int kQ8ExactSteps = 16;    // steps per exact FP32 chunk (1024 k)
+
+__device__ __forceinline__ uint4 ldg_stream_u4(const void *p) {
+    uint4 v;
+    asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                 : "l"(p));
+    return v;
+}
+
+// Up to 16 bytes from p, byte by byte; bytes at and past `valid` are 0.
+__device__ __forceinline__ uint4 load16_bytes(const int8_t *p, int valid) {
+    uint32_t w[4] = {0u, 0u, 0u, 0u};
+#pragma unroll
+    for (int i = 0; i < 16; ++i)
+        if (i < valid) w[i >> 2] |= (uint32_t)(uint8_t)p[i] << (8 * (i & 3));
+    return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+// 16 bytes from p of any alignment, all of them inside [.., end): the five
+// aligned words around them, shifted together, where those lie inside
+// [begin, end) as well; byte by byte at the two ends of the array.
+__device__ __forceinline__ uint4 load16_unaligned(const int8_t *p, const int8_t *begin,
+                                                  const int8_t *end) {
+    const int8_t *a = reinterpret_cast<const int8_t *>(reinterpret_cast<uintptr_t>(p) & ~uintptr_t(3));
+    if (a < begin || a + 20 > end) return load16_bytes(p, 16);
+    const uint32_t *w = reinterpret_cast<const uint32_t *>(a);
+    const int sh = 8 * (int)(reinterpret_cast<uintptr_t>(p) & 3);
+    const uint32_t w0 = __ldg(w), w1 = __ldg(w + 1), w2 = __ldg(w + 2), w3 = __ldg(w + 3), w4 = __ldg(w + 4);
+    return make_uint4(__funnelshift_r(w0, w1, sh), __funnelshift_r(w1, w2, sh),
+                      __funnelshift_r(w2, w3, sh), __funnelshift_r(w3, w4, sh));
+}
+
+__device__ __forceinline__ void mma_f16(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+        "{%0, %1, %2, %3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+// Products of one step: weight rows g (wa) and g + 8 (wb), tokens x[0..NB).
+template <int NB>
+__device__ __forceinline__ void q8_step(float (&acc)[NB][4], const uint4 &wa, const uint4 &wb,
+                                        const uint4 (&x)[NB]) {
+    const uint32_t ra[4] = {wa.x, wa.y, wa.z, wa.w}, rb[4] = {wb.x, wb.y, wb.z, wb.w};
+#pragma unroll
+    for (int s = 0; s < 4; ++s) {
+        uint32_t a[4];
+        q8_to_f16(ra[s], a[0], a[2]);
+        q8_to_f16(rb[s], a[1], a[3]);
+#pragma unroll
+        for (int n = 0; n < NB; ++n) {
+            const uint32_t w = s == 0 ? x[n].x : s == 1 ? x[n].y : s == 2 ? x[n].z : x[n].w;
+            uint32_t b0, b1;
+            q8_to_f16(w, b0, b1);
+            mma_f16(acc[n], a, b0, b1);
+        }
+    }
+}
+
+template <int NB>
+__device__ __forceinline__ void q8_flush(int (&sum)[NB][4], float (&acc)[NB][4]) {
+#pragma unroll
+    for (int n = 0; n < NB; ++n)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            sum[n][i] += __float2int_rn(acc[n][i]);
+            acc[n][i] = 0.0f;
+        }
+}
+
+// Adds into `sum` the dot products over steps [s0, s1) of a row of K values.
+//   wa, wb     this lane's two weight rows (g and g + 8 of the 16), at k = 0
+//   x[n]       this lane's token row of block n (token 8n + g), at k = 0
+//   VEC        all those rows are 16-byte aligned; otherwise wbegin/wend and
+//              xbegin/xend bound the two arrays
+//   COHERENT   the token rows were written by other blocks of this kernel (VEC
+//              only): they are read from L2, and are padded with zeros to whole
+//              steps
+// sum[n][0..3]: rows g, g, g+8, g+8 and tokens 8n + 2t, +1, 2t, +1.
+template <int NB, bool VEC, int U, bool COHERENT = false>
+__device__ __forceinline__ void q8_dot(int (&sum)[NB][4], const int8_t *wa, const int8_t *wb,
+                                       const int8_t *const (&x)[NB], int64_t K, int s0, int s1,
+                                       const int8_t *wbegin, const int8_t *wend,
+                                       const int8_t *xbegin, const int8_t *xend) {
+    const int t = (int)(threadIdx.x & 3);
+    const int full = (int)(K / kQ8Step);
+    const int sf = s1 < full ? s1 : full;
+    float acc[NB][4];
+#pragma unroll
+    for (int n = 0; n < NB; ++n)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) acc[n][i] = 0.0f;
+    auto wload = [&](const int8_t *row, int s) {
+        const int8_t *p = row + (int64_t)s * kQ8Step + 16 * t;
+        return VEC ? ldg_stream_u4(p) : load16_unaligned(p, wbegin, wend);
+    };
+    auto xload = [&](const int8_t *row, int s) {
+        const int8_t *p = row + (int64_t)s * kQ8Step + 16 * t;
+        if (COHERENT) return __ldcg(reinterpret_cast<const uint4 *>(p));
+        return VEC ? __ldg(reinterpret_cast<const uint4 *>(p)) : load16_unaligned(p, xbegin, xend);
+    };
+    int s = s0, since = 0;
+    static_assert(kQ8ExactSteps % U == 0, "an exact chunk is whole unrolled rounds");
+    for (; s + U <= sf; s += U) {
+        uint4 a[U], b[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            a[u] = wload(wa, s + u);
+            b[u] = wload(wb, s + u);
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            uint4 xv[NB];
+#pragma unroll
+            for (int n = 0; n < NB; ++n) xv[n] = xload(x[n], s + u);
+            q8_step<NB>(acc, a[u], b[u], xv);
+        }
+        since += U;
+        if (since == kQ8ExactSteps) {
+            q8_flush<NB>(sum, acc);
+            since = 0;
+        }
+    }
+    for (; s < sf; ++s) {   // at most U - 1 steps, in the chunk the last round left open
+        uint4 xv[NB];
+        const uint4 a = wload(wa, s), b = wload(wb, s);
+#pragma unroll
+        for (int n = 0; n < NB; ++n) xv[n] = xload(x[n], s);
+        q8_step<NB>(acc, a, b, xv);
+    }
+    q8_flush<NB>(sum, acc);
+    if (s < s1) {   // the row's last K % 64 values
+        const int64_t k = (int64_t)s * kQ8Step + 16 * t;
+        const int valid = (int)(K - k < 0 ? 0 : K - k > 16 ? 16 : K - k);
+        uint4 xv[NB];
+        const uint4 a = load16_bytes(wa + k, valid), b = load16_bytes(wb + k, valid);
+#pragma unroll
+        for (int n = 0; n < NB; ++n)
+            xv[n] = COHERENT ? __ldcg(reinterpret_cast<const uint4 *>(x[n] + k)) : load16_bytes(x[n] + k, valid);
+        q8_step<NB>(acc, a, b, xv);
+        q8_flush<NB>(sum, acc);
+    }
+}
+
+#endif  // __CUDACC__
+
+}  // namespace sgemm_gb300

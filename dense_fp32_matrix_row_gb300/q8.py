@@ -1,0 +1,211 @@
+"""Python binding of the 8-bit serving operators (``sgemm_q8_*`` in
+``include/sgemm_gb300.h``): row quantisation, RMS norm with quantisation, the
+8-bit linear product and the expert layer for a few tokens.
+
+Like the rest of the package it only marshals torch CUDA tensors into the C
+ABI: outputs are the caller's, calls are enqueued on ``stream`` (default: the
+current torch stream of the output's device) and return without waiting.
+"""
+
+from __future__ import annotations
+
+import ctypes
+
+import torch
+
+_i64, _vp, _int, _f32 = ctypes.c_int64, ctypes.c_void_p, ctypes.c_int, ctypes.c_float
+TYPE_FP32, TYPE_BF16 = 0, 1
+_TYPES = {torch.float32: TYPE_FP32, torch.bfloat16: TYPE_BF16}
+ACTIVATIONS = {"none": 0, "relu": 1, "gelu": 2, "silu": 3}
+
+_SIGNATURES = {
+    "sgemm_q8_quantize": [_i64, _i64, _vp, _i64, _int, _vp, _i64, _vp, _vp],
+    "sgemm_q8_rmsnorm": [_i64, _i64, _vp, _i64, _vp, _i64, _int, _vp, _f32, _vp, _i64, _vp, _i64,
+                         _vp, _i64, _vp, _vp],
+    "sgemm_q8_linear": [_i64, _i64, _i64, _vp, _i64, _vp, _vp, _i64, _vp, _vp, _int, _vp, _i64,
+                        _int, _vp],
+    "sgemm_q8_moe": [_i64] * 5 + [_vp, _i64, _int, _vp, _i64, _vp, _i64, _vp, _vp, _i64, _vp, _int,
+                                  _vp, _i64, _vp, _vp, _vp],
+}
+_fn = {}
+
+
+def _entry(name):
+    f = _fn.get(name)
+    if f is None:
+        from . import lib
+        f = getattr(lib(), name)
+        f.argtypes, f.restype = _SIGNATURES[name], _int
+        _fn[name] = f
+    return f
+
+
+def _call(name, *args):
+    rc = _entry(name)(*args)
+    if rc:
+        from . import SgemmError
+        raise SgemmError(rc, name)
+
+
+def _stream(stream, device):
+    if stream is None:
+        return torch.cuda.current_stream(device).cuda_stream if device.type == "cuda" else 0
+    return stream if isinstance(stream, int) else stream.cuda_stream
+
+
+def _matrix(t, name, dtypes, shape, device):
+    """Checks a 2-D operand; its row stride."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch tensor")
+    if t.dtype not in dtypes:
+        raise TypeError(f"{name} must be of type {' or '.join(str(d) for d in dtypes)}, not {t.dtype}")
+    if t.dim() != 2 or (shape is not None and tuple(t.shape) != shape):
+        raise ValueError(f"{name} must have shape {shape}, not {tuple(t.shape)}" if shape is not None
+                         else f"{name} must be 2-D")
+    rows, cols = t.shape
+    if t.numel() == 0:
+        return max(cols, 1)
+    if t.device != device or device.type != "cuda":
+        raise TypeError(f"{name} must live on the same CUDA device as the output")
+    if cols > 1 and t.stride(1) != 1:
+        raise ValueError(f"{name} must be row-major with contiguous rows (stride(1) == 1)")
+    return max(t.stride(0), cols) if rows == 1 else t.stride(0)
+
+
+def _packed(t, name, dtype, shape, device):
+    """Checks a contiguous operand of exactly this type and shape."""
+    if not isinstance(t, torch.Tensor) or t.dtype != dtype:
+        raise TypeError(f"{name} must be a torch tensor of type {dtype}")
+    if tuple(t.shape) != shape:
+        raise ValueError(f"{name} must have shape {shape}, not {tuple(t.shape)}")
+    if t.numel() and (t.device != device or device.type != "cuda"):
+        raise TypeError(f"{name} must live on the same CUDA device as the output")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+
+
+def _on(device):
+    """The library works on the current device."""
+    return torch.cuda.device(device)
+
+
+_FLOATS = (torch.float32, torch.bfloat16)
+_INT8 = (torch.int8,)
+
+
+def _launch(device, name, *args):
+    if device.type != "cuda" or device.index == torch.cuda.current_device():
+        _call(name, *args)
+    else:
+        with _on(device):
+            _call(name, *args)
+
+
+def quantize_q8(x, q, scale, stream=None) -> None:
+    """Each row of ``x`` (M, K; float32 or bfloat16) as 8-bit whole numbers
+    ``q`` (M, K; int8) and one ``scale`` (M; float32): x is about q * scale,
+    scale = max|row| / 127.  Rows of ``x`` and ``q`` may be strided."""
+    dev = q.device
+    ldx = _matrix(x, "x", _FLOATS, None, dev)
+    M, K = x.shape
+    ldq = _matrix(q, "q", _INT8, (M, K), dev)
+    _packed(scale, "scale", torch.float32, (M,), dev)
+    _launch(dev, "sgemm_q8_quantize", M, K, x.data_ptr(), ldx, _TYPES[x.dtype], q.data_ptr(), ldq,
+            scale.data_ptr(), _stream(stream, dev))
+
+
+def rmsnorm_q8(x, weight, q, scale, residual=None, h=None, y=None, eps: float = 1e-6,
+               stream=None) -> None:
+    """h = x + residual; y = h * weight / sqrt(mean(h^2) + eps); ``q`` and
+    ``scale`` are y's 8-bit rows.
+
+    ``x``, ``residual``, ``h`` and ``y`` are (M, K) of one type (float32 or
+    bfloat16), ``weight`` K float32 values.  ``residual``, ``h`` and ``y`` may
+    be left out; ``h`` may be ``x`` or ``residual`` itself."""
+    dev = q.device
+    ldx = _matrix(x, "x", _FLOATS, None, dev)
+    M, K = x.shape
+    ldq = _matrix(q, "q", _INT8, (M, K), dev)
+    _packed(weight, "weight", torch.float32, (K,), dev)
+    _packed(scale, "scale", torch.float32, (M,), dev)
+    more = []
+    for t, name in ((residual, "residual"), (h, "h"), (y, "y")):
+        if t is None:
+            more.append((None, 0))
+        else:
+            ld = _matrix(t, name, (x.dtype,), (M, K), dev)
+            more.append((t.data_ptr(), ld))
+    (pr, ldr), (ph, ldh), (py, ldy) = more
+    _launch(dev, "sgemm_q8_rmsnorm", M, K, x.data_ptr(), ldx, pr, ldr, _TYPES[x.dtype],
+            weight.data_ptr(), eps, ph, ldh, py, ldy, q.data_ptr(), ldq, scale.data_ptr(),
+            _stream(stream, dev))
+
+
+def linear_q8(xq, xs, wq, ws, out, bias=None, activation: str = "none", stream=None) -> None:
+    """out = act((xq @ wq^T) * xs[:, None] * ws[None, :] + bias).
+
+    ``xq`` (M, K) and ``wq`` (N, K) are int8 with the float32 scales ``xs``
+    (M) and ``ws`` (N); ``out`` (M, N) is float32 or bfloat16; ``bias`` is N
+    float32 values or None; ``activation`` is a key of ``ACTIVATIONS``."""
+    act = ACTIVATIONS.get(activation)
+    if act is None:
+        raise ValueError(f"unknown activation {activation!r}; one of {sorted(ACTIVATIONS)}")
+    dev = out.device
+    ldx = _matrix(xq, "xq", _INT8, None, dev)
+    ldw = _matrix(wq, "wq", _INT8, None, dev)
+    M, K = xq.shape
+    N = wq.shape[0]
+    if wq.shape[1] != K:
+        raise ValueError(f"shape mismatch: xq {tuple(xq.shape)}, wq {tuple(wq.shape)}")
+    ldc = _matrix(out, "out", _FLOATS, (M, N), dev)
+    _packed(xs, "xs", torch.float32, (M,), dev)
+    _packed(ws, "ws", torch.float32, (N,), dev)
+    if bias is not None:
+        _packed(bias, "bias", torch.float32, (N,), dev)
+    _launch(dev, "sgemm_q8_linear", M, N, K, xq.data_ptr(), ldx, xs.data_ptr(), wq.data_ptr(), ldw,
+            ws.data_ptr(), None if bias is None else bias.data_ptr(), act, out.data_ptr(), ldc,
+            _TYPES[out.dtype], _stream(stream, dev))
+
+
+def moe_q8(x, router, w_up, s_up, w_down, s_down, out, top_k: int, renormalize: bool = True,
+           ids=None, gates=None, stream=None) -> None:
+    """A mixture-of-experts layer for up to 64 tokens.
+
+    ``x`` and ``out`` (T, H) are float32 or bfloat16 alike; ``router`` (E, H)
+    float32; ``w_up`` (E, 2I, H) and ``w_down`` (E, H, I) int8 with the float32
+    scales ``s_up`` (E, 2I) and ``s_down`` (E, H).  The first I rows of an
+    expert's ``w_up`` are its gate, the last I its up projection:
+    out[t] = sum over the top_k experts of gate * down(silu(gate) * up), with
+    the token and the hidden row in 8 bits.  ``ids`` (T, top_k; int32) and
+    ``gates`` (T, top_k; float32) take the routing if given."""
+    dev = out.device
+    ldx = _matrix(x, "x", _FLOATS, None, dev)
+    T, H = x.shape
+    ldo = _matrix(out, "out", (x.dtype,), (T, H), dev)
+    ldr = _matrix(router, "router", (torch.float32,), None, dev)
+    E = router.shape[0]
+    if router.shape[1] != H:
+        raise ValueError(f"router must have shape (E, {H}), not {tuple(router.shape)}")
+    for t, name in ((w_up, "w_up"), (w_down, "w_down")):
+        if not isinstance(t, torch.Tensor) or t.dtype != torch.int8:
+            raise TypeError(f"{name} must be a torch tensor of type torch.int8")
+        if t.dim() != 3 or t.shape[0] != E:
+            raise ValueError(f"{name} must have three dimensions, the first of them {E}, not {tuple(t.shape)}")
+        if not t.is_contiguous():
+            raise ValueError(f"{name} must be contiguous")
+    inner = w_down.shape[2]
+    if tuple(w_up.shape) != (E, 2 * inner, H) or w_down.shape[1] != H:
+        raise ValueError(f"shape mismatch: w_up {tuple(w_up.shape)}, w_down {tuple(w_down.shape)}, H = {H}")
+    _packed(w_up, "w_up", torch.int8, (E, 2 * inner, H), dev)
+    _packed(w_down, "w_down", torch.int8, (E, H, inner), dev)
+    _packed(s_up, "s_up", torch.float32, (E, 2 * inner), dev)
+    _packed(s_down, "s_down", torch.float32, (E, H), dev)
+    if ids is not None:
+        _packed(ids, "ids", torch.int32, (T, top_k), dev)
+    if gates is not None:
+        _packed(gates, "gates", torch.float32, (T, top_k), dev)
+    _launch(dev, "sgemm_q8_moe", T, E, top_k, H, inner, x.data_ptr(), ldx, _TYPES[x.dtype],
+            router.data_ptr(), ldr, w_up.data_ptr(), H, s_up.data_ptr(), w_down.data_ptr(), inner,
+            s_down.data_ptr(), 1 if renormalize else 0, out.data_ptr(), ldo,
+            None if ids is None else ids.data_ptr(), None if gates is None else gates.data_ptr(),
+            _stream(stream, dev))

@@ -67,7 +67,7 @@ extern "C" {
 #define SGEMM_ERR_DEVICE     -6   /* the current device is not an sm_103 GPU */
 #define SGEMM_ERR_TIMEOUT    -7   /* a device-side bounded wait ran out (from sgemm_status) */
 #define SGEMM_ERR_BAD_ARG    -8   /* any other invalid argument */
-#define SGEMM_ERR_TOO_LARGE  -9   /* beyond sgemm_noalloc's fixed scratch */
+#define SGEMM_ERR_TOO_LARGE  -9   /* beyond sgemm_noalloc's fixed scratch or a limit of sgemm_q8_moe */
 #define SGEMM_ERR_CAPTURE   -10   /* the stream is being captured and the call would allocate */
 
 /* Kernel identifiers, for sgemm_select_kernel and sgemm_force_kernel. */
@@ -218,6 +218,109 @@ int sgemm_fused(int64_t M, int64_t N, int64_t K, float alpha,
                 const float *A, int64_t lda, const float *B, int64_t ldb,
                 float beta, float *C, int64_t ldc, const float *bias, int activation,
                 int mode, void *stream);
+
+/*
+ * 8-bit serving operators: the feed-forward chain of "GPU GEMM 优化完全拆解（一）",
+ * section "LLM 推理本质上是 GEMM 的串联", with weights and activations held as
+ * 8-bit whole numbers and one FP32 scale per row (a token's row of X, an output
+ * channel's row of W): value = whole number * scale.
+ *
+ * The conventions above hold (device pointers, row-major, any stride >= the
+ * row length, asynchronous on `stream`, argument errors before anything is
+ * enqueued, outputs not overlapping inputs or one another: SGEMM_ERR_ALIAS),
+ * with these additions.
+ * Types       `type` is SGEMM_TYPE_FP32 or SGEMM_TYPE_BF16 (another value:
+ *             SGEMM_ERR_BAD_ARG) and names the element type of the `void *`
+ *             arrays.  Pointers are aligned to their elements
+ *             (SGEMM_ERR_BAD_ARG).  All arithmetic is FP32 or integer; a BF16
+ *             output is rounded once, to nearest even.
+ * Rounding    Quantising a row p: m = max|p_k|, q_k = rint(p_k * (127/m)), ties
+ *             to even, in [-127, 127].  A row of zeros has q = 0, scale 0; a
+ *             row that holds a NaN or an infinity has q = 0, scale NaN, so
+ *             that every value it stands for is NaN.
+ * Alignment   Any.  16-byte aligned bases and row strides (in bytes) run
+ *             fastest.
+ * Results     are the same bits on every call on the same GPU model.
+ */
+#define SGEMM_TYPE_FP32  0
+#define SGEMM_TYPE_BF16  1
+
+/*
+ * sgemm_q8_quantize -- rows of x (M x K) to q (M x K) and scale (M floats):
+ * scale = m/127.  For weights (one scale per output channel) and activations
+ * (one per token) alike.  K == 0 gives scale 0.
+ */
+int sgemm_q8_quantize(int64_t M, int64_t K, const void *x, int64_t ldx, int type, int8_t *q,
+                      int64_t ldq, float *scale, void *stream);
+
+/*
+ * sgemm_q8_rmsnorm -- residual addition, RMS norm and quantisation of each row:
+ *
+ *     h = x + residual                          (residual NULL: h = x)
+ *     y = h * weight / sqrt(mean(h^2) + eps)
+ *     q, scale = the 8-bit form of y: p = h * weight quantised as above,
+ *                scale = (m/127) / sqrt(mean(h^2) + eps)
+ *
+ * h is summed and y formed in FP32 from the unrounded h.
+ *   weight      K floats; eps >= 0 (else SGEMM_ERR_BAD_ARG)
+ *   h, y        optional outputs (NULL: not written) of type `type`; h may be x
+ *               or residual itself (the same pointer and stride)
+ *   q, scale    required
+ */
+int sgemm_q8_rmsnorm(int64_t M, int64_t K, const void *x, int64_t ldx, const void *residual,
+                     int64_t ldr, int type, const float *weight, float eps, void *h, int64_t ldh,
+                     void *y, int64_t ldy, int8_t *q, int64_t ldq, float *scale, void *stream);
+
+/*
+ * sgemm_q8_linear -- the 8-bit product with a fused epilogue:
+ *
+ *     C[m][n] = act(xs[m] * ws[n] * sum_k X[m][k] * W[n][k] + bias[n])
+ *
+ *   X, xs       M x K token rows and their M scales
+ *   W, ws       N x K weights, one row per output channel, and their N scales
+ *   bias        N floats or NULL;  activation  SGEMM_ACT_*
+ *   C           M x N of type `type`
+ * The whole-number sums are exact while every partial sum stays within 2^24
+ * in magnitude (always up to K = 1024, and for ordinary data far beyond), and
+ * rounded to FP32 from there.  K <= 131071 (SGEMM_ERR_BAD_DIM).  K == 0 gives
+ * act(bias).
+ */
+int sgemm_q8_linear(int64_t M, int64_t N, int64_t K, const int8_t *X, int64_t ldx, const float *xs,
+                    const int8_t *W, int64_t ldw, const float *ws, const float *bias, int activation,
+                    void *C, int64_t ldc, int type, void *stream);
+
+/*
+ * sgemm_q8_moe -- a whole mixture-of-experts layer for a few tokens:
+ *
+ *     logits = x @ router^T                               (FP32, T x E)
+ *     ids[t][0..top_k)  the experts of the largest logits, largest first;
+ *                       equal logits: the lower index; a NaN logit counts as
+ *                       the largest
+ *     gates[t][j] = exp(logits[t][ids[t][j]]) / the sum of exp(logits[t][.])
+ *                   over all experts, or (renormalize != 0) over the chosen
+ *     out[t] = sum_j gates[t][j] * expert_{ids[t][j]}(x[t])
+ *
+ * where an expert is the gated feed-forward block in 8 bits: with xq, sx the
+ * quantised token, g and u its products with the first I and the last I rows
+ * of w_up (each times sx and s_up), hid = g / (1 + exp(-g)) * u, then the
+ * quantised hid times w_down (times its scale and s_down).
+ *   x, out      T x H of type `type`
+ *   router      E x H floats, row stride ldr
+ *   w_up, s_up      E x 2I rows of H bytes (row stride ldu) and E x 2I scales
+ *   w_down, s_down  E x H rows of I bytes (row stride ldd) and E x H scales
+ *   ids, gates  optional outputs, T x top_k, contiguous
+ * 1 <= top_k <= E; T <= 64, E <= 512 and top_k <= 16 (SGEMM_ERR_TOO_LARGE
+ * beyond: more tokens are work for sgemm_q8_linear); H, I <= 131071.
+ * Uses the stream's workspace (tokens, hidden rows and the experts' results:
+ * about 9 * T * top_k * max(H, I) bytes), grown like sgemm()'s; the same rule
+ * for stream capture holds.  One of its kernels waits for its own earlier
+ * blocks (bounded, see sgemm_status).
+ */
+int sgemm_q8_moe(int64_t T, int64_t E, int64_t top_k, int64_t H, int64_t I, const void *x,
+                 int64_t ldx, int type, const float *router, int64_t ldr, const int8_t *w_up,
+                 int64_t ldu, const float *s_up, const int8_t *w_down, int64_t ldd,
+                 const float *s_down, int renormalize, void *out, int64_t ldo, int32_t *ids,
+                 float *gates, void *stream);
 
 /*
  * sgemm_status -- wait for `stream`, then report and clear the current
