@@ -132,16 +132,25 @@ int stream_workspace(size_t bytes, cudaStream_t s, void **out);
 
 #ifdef __CUDACC__
 
+// The epilogue's activations.  GELU is the tanh form
+// x/2 * (1 + tanh(sqrt(2/pi) * (x + 0.044715 x^3))), SiLU is x / (1 + e^-x);
+// CUDA's tanhf and expf.  ReLU keeps NaN.
+template <int ACT>
+__device__ __forceinline__ float activate(float v) {
+    if constexpr (ACT == kActRelu) return v < 0.0f ? 0.0f : v;
+    else if constexpr (ACT == kActGelu)
+        return 0.5f * v * (1.0f + tanhf(0.7978845608028654f * fmaf(0.044715f * v, v * v, v)));
+    else if constexpr (ACT == kActSilu) return v / (1.0f + expf(-v));
+    else return v;
+}
+
 // act(v + bias[col]): the part of the epilogue after alpha*acc + beta*C.
-// GELU is the tanh form x/2 * (1 + tanh(sqrt(2/pi) * (x + 0.044715 x^3))),
-// SiLU is x / (1 + e^-x); CUDA's tanhf and expf.  ReLU keeps NaN.
 __device__ __forceinline__ float epilogue_tail(const Epilogue &e, float v, int64_t col) {
     if (e.bias != nullptr) v += __ldg(e.bias + col);
     switch (e.act) {
-        case kActRelu: return v < 0.0f ? 0.0f : v;
-        case kActGelu:
-            return 0.5f * v * (1.0f + tanhf(0.7978845608028654f * fmaf(0.044715f * v, v * v, v)));
-        case kActSilu: return v / (1.0f + expf(-v));
+        case kActRelu: return activate<kActRelu>(v);
+        case kActGelu: return activate<kActGelu>(v);
+        case kActSilu: return activate<kActSilu>(v);
         default: return v;
     }
 }

@@ -60,6 +60,10 @@ struct Q8MoeArgs {
 
 cudaError_t launch_q8_rows(const Q8RowsArgs &a);
 cudaError_t launch_q8_stream(const Q8LinearArgs &a);
+// The tensor-core form, for more tokens than the streaming kernel is for.
+bool q8_mma_can_run(const Q8LinearArgs &a);
+size_t q8_mma_workspace_bytes(const Q8LinearArgs &a);
+cudaError_t launch_q8_mma(const Q8LinearArgs &a, void *workspace);
 cudaError_t launch_q8_moe(const Q8MoeArgs &a, void *workspace);
 size_t q8_moe_workspace_bytes(int T, int E, int top_k, int H, int I);
 

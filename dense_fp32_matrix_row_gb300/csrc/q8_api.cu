@@ -10,6 +10,8 @@ using namespace sgemm_gb300;
 namespace {
 
 constexpr int64_t kMaxElems = int64_t(1) << 40;
+// Products of at most this many tokens run the streaming kernel.
+constexpr int64_t kStreamTokens = 16;
 
 size_t type_size(int type) { return type == SGEMM_TYPE_BF16 ? 2 : 4; }
 bool known_type(int type) { return type == SGEMM_TYPE_FP32 || type == SGEMM_TYPE_BF16; }
@@ -146,7 +148,11 @@ int sgemm_q8_linear(int64_t M, int64_t N, int64_t K, const int8_t *X, int64_t ld
     a.stream = static_cast<cudaStream_t>(stream);
     rc = device_args(&a.err, &a.wait_ns, &a.sm_count, &a.encode);
     if (rc != SGEMM_OK) return rc;
-    return launch_status(launch_q8_stream(a));
+    if (M <= kStreamTokens || !q8_mma_can_run(a)) return launch_status(launch_q8_stream(a));
+    void *work = nullptr;
+    rc = stream_workspace(q8_mma_workspace_bytes(a), a.stream, &work);
+    if (rc != SGEMM_OK) return rc;
+    return launch_status(launch_q8_mma(a, work));
 }
 
 int sgemm_q8_moe(int64_t T, int64_t E, int64_t top_k, int64_t H, int64_t I, const void *x, int64_t ldx, int type,

@@ -1,0 +1,745 @@
+// q8_mma.cu -- 8-bit linear product on the tcgen05 tensor cores, exactly:
+//
+//     C[m][n] = act(xs[m] * ws[n] * sum_k X[m][k] * W[n][k] + bias[n])
+//
+// sm_103a has no fast 8-bit integer MMA (and no tcgen05 kind::i8).  But an
+// 8-bit whole number is exact in FP16, a product of two is at most 2^14, and a
+// sum of 1024 of them at most 2^24: the FP16 tensor cores with FP32
+// accumulators give the integer sum exactly, as long as the accumulator is
+// emptied every 1024 k.  The chunk sums are added in FP32 registers, exact
+// while they stay within 2^24 and rounded once per chunk beyond.
+//
+// Roles are swapped against a usual product: the 128 lanes of the accumulator
+// are rows of W (output channels), its columns are tokens, so a few tokens
+// waste nothing and C's rows are stored 32 channels at a time.
+//
+//   W   travels and rests in 8 bits.  TMA brings 64 k of 128 rows into a
+//       shared-memory ring; eight converter warps read a row per thread, expand
+//       it to FP16 in registers and store it to tensor memory, from where the
+//       MMA takes its A operand.  The 16-bit form of W never touches shared
+//       memory, whose bandwidth is what bounds such a kernel (8 KB written and
+//       read per stage and SM for W, where 16-bit tiles would move 16 and 16).
+//   X   is expanded to FP16 once, by a kernel before (2 bytes of L2 traffic per
+//       element), and comes in by TMA as the B operand, 64 k per stage.
+//   MMA one thread issues four tcgen05.mma kind::f16 per stage.
+//   The converter warps also empty the accumulator, add the chunks and store.
+//
+// PAIR: two SMs share a tile of 256 W rows x NT tokens (cta_group::2), each
+// with its own 128 rows of W and half of the tokens' X.
+//
+// When the tiles do not fill the GPU, K is divided into `ks` parts per tile;
+// the parts' sums go to the workspace and the last warp to arrive adds them in
+// part order.
+//
+// Every wait is bounded; on a time-out the roles record it and wind down.
+#include <cuda_fp16.h>
+
+#include <atomic>
+
+#include "q8.cuh"
+#include "tcgen05.cuh"
+
+namespace sgemm_gb300 {
+namespace {
+
+constexpr int CONV_WARPS = 8;
+constexpr int PRODUCER_WARP = CONV_WARPS, MMA_WARP = CONV_WARPS + 1;
+constexpr int THREADS = (CONV_WARPS + 2) * 32;
+constexpr int KT = 64;                        // k per stage
+constexpr int CHUNK = 16;                     // stages per accumulation chunk: 1024 k
+constexpr uint32_t W_STAGE = 128 * KT;        // bytes
+constexpr uint64_t DRAIN_NS = 1000000000ull;
+
+template <int NT_, bool PAIR_>
+struct Cfg {
+    static constexpr int NT = NT_;                         // tokens per tile
+    static constexpr bool PAIR = PAIR_;
+    static constexpr int NL = PAIR ? NT / 2 : NT;          // tokens staged by one SM
+    static constexpr int ROWS = PAIR ? 256 : 128;          // W rows per tile
+    static constexpr int DB = NT <= 128 ? 2 : 1;           // accumulators
+    static constexpr int ST = 8;                           // X and A stages
+    static constexpr int WST = NT <= 64 ? 14 : 8;          // W stages
+    static constexpr uint32_t X_STAGE = NL * 128;          // bytes: 64 FP16 per token
+    static constexpr uint32_t A_COL = DB * NT;             // tensor-memory column of A stage 0
+    static constexpr int COLS = NT / 2;                    // columns per converter thread
+    static constexpr int LEAD = ST - 2;                    // stages converted ahead of a drain
+    static constexpr size_t SMEM = 1024 + (size_t)ST * X_STAGE + (size_t)WST * W_STAGE + 512;
+    // kind::f16, FP16 operands (format 0), FP32 accumulator, both K-major
+    static constexpr uint32_t IDESC = (1u << 4) | ((uint32_t)(NT >> 3) << 17) | ((uint32_t)(ROWS >> 4) << 24);
+    static_assert(A_COL + ST * (KT / 2) <= 512, "tensor memory");
+    static_assert(SMEM <= 227 * 1024, "shared memory per block");
+    static_assert(X_STAGE % 1024 == 0 && W_STAGE % 1024 == 0, "stages keep 1024-byte alignment");
+    static_assert(COLS % 16 == 0, "the drain reads 16 columns at a time");
+};
+
+// The division of the product into units: tile (W rows, tokens) and part of K.
+struct Plan {
+    int nt, mt;      // tiles along W rows and along tokens
+    int ks, per;     // parts of K per tile, stages per part
+    int stages;
+    __host__ __device__ int units() const { return nt * mt * ks; }
+};
+
+constexpr int RASTER = 8;   // W tiles walked together over the tokens (L2 reuse)
+
+__device__ __forceinline__ void plan_unit(const Plan &p, int u, int &tn, int &tm, int &s0, int &s1) {
+    const int tile = u / p.ks, part = u - tile * p.ks;
+    const int per_group = RASTER * p.mt;
+    const int first = (tile / per_group) * RASTER;
+    const int gsz = min(RASTER, p.nt - first);
+    tn = first + (tile % per_group) % gsz;
+    tm = (tile % per_group) / gsz;
+    s0 = part * p.per;
+    s1 = min(s0 + p.per, p.stages);
+}
+
+template <bool PAIR>
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+    if constexpr (PAIR)
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t"
+            "setp.ne.b32 p, %4, 0;\n\t"
+            "tcgen05.mma.cta_group::2.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+            "r"(a), "l"(b), "r"(idesc), "r"(accumulate)
+            : "memory");
+    else
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t"
+            "setp.ne.b32 p, %4, 0;\n\t"
+            "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+            "r"(a), "l"(b), "r"(idesc), "r"(accumulate)
+            : "memory");
+}
+
+__device__ __forceinline__ void tc_st32(uint32_t taddr, const uint32_t (&r)[32]) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], "
+        "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, "
+        "%17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32};" ::"r"(taddr),
+        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]),
+        "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]),
+        "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]),
+        "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
+        : "memory");
+    asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+}
+
+__device__ __forceinline__ uint4 lds128(uint32_t a) {
+    uint4 v;
+    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a));
+    return v;
+}
+
+// Arrive on the barrier at offset `bar` of CTA `cta` of the cluster.  Relaxed:
+// what it hands over is tensor memory alone, which the completed tcgen05
+// operations and tcgen05.fence before it order.  (A release at cluster scope
+// waits about 1500 cycles here, once per stage and warp: the 8192 x 14336 x
+// 4096 product took 1209 us with it.)
+__device__ __forceinline__ void arrive_relaxed(uint32_t bar, uint32_t cta) {
+    asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr(bar, cta))
+                 : "memory");
+}
+
+// Whether a phase has completed, without the pause that try_wait may take.
+__device__ __forceinline__ bool mbar_test(uint32_t bar, uint32_t parity) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(bar), "r"(parity)
+        : "memory");
+    return ok != 0;
+}
+
+// Lane 0 waits for the whole warp; the others then see the completed phase.
+__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, uint64_t limit_ns) {
+    const int lane = threadIdx.x & 31;
+    int ok = lane == 0 ? (int)mbar_wait(bar, parity, limit_ns) : 0;
+    ok = __shfl_sync(0xffffffffu, ok, 0);
+    if (!ok) return false;
+    mbar_wait(bar, parity, DRAIN_NS);
+    return true;
+}
+
+template <typename C, typename OutT>
+__global__ void __launch_bounds__(THREADS, 1)
+q8_mma_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmX, int M, int N,
+              Plan plan, const float *__restrict__ xs, const float *__restrict__ ws, Epilogue ep,
+              OutT *__restrict__ out, int64_t ldc, float *part, uint32_t *counters, unsigned *err,
+              uint64_t wait_ns) {
+    constexpr bool PAIR = C::PAIR;
+    constexpr int ST = C::ST, WST = C::WST, NT = C::NT, COLS = C::COLS;
+    extern __shared__ unsigned char smem_raw[];
+    const uintptr_t base = (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023);
+    unsigned char *xring = reinterpret_cast<unsigned char *>(base);
+    unsigned char *wring = xring + (size_t)ST * C::X_STAGE;
+    uint64_t *wfull = reinterpret_cast<uint64_t *>(wring + (size_t)WST * W_STAGE);
+    uint64_t *wempty = wfull + WST;
+    uint64_t *xfull = wempty + WST;     // even SM of a pair: both SMs' bytes
+    uint64_t *afull = xfull + ST;       // even SM of a pair: both SMs' converters
+    uint64_t *empty = afull + ST;       // the MMAs that read X and A stage s are done
+    uint64_t *dfull = empty + ST;       // [2] accumulator holds a finished chunk
+    uint64_t *dempty = dfull + 2;       // [2] accumulator has been read
+    uint64_t *drainbar = dempty + 2;
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(drainbar + 1);
+
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    uint32_t rank = 0;
+    if constexpr (PAIR) asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(rank));
+    const bool lead = rank == 0;
+    const int worker = PAIR ? (int)(blockIdx.x >> 1) : (int)blockIdx.x;
+    const int workers = PAIR ? (int)(gridDim.x >> 1) : (int)gridDim.x;
+    const int units = plan.units();
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < WST; ++s) {
+            mbar_init(smem_u32(&wfull[s]), 1);
+            mbar_init(smem_u32(&wempty[s]), CONV_WARPS / 2);
+        }
+        for (int s = 0; s < ST; ++s) {
+            mbar_init(smem_u32(&xfull[s]), 1);
+            mbar_init(smem_u32(&afull[s]), (PAIR ? 2 : 1) * CONV_WARPS / 2);
+            mbar_init(smem_u32(&empty[s]), 1);
+        }
+        for (int b = 0; b < 2; ++b) {
+            mbar_init(smem_u32(&dfull[b]), 1);
+            mbar_init(smem_u32(&dempty[b]), (PAIR ? 2 : 1) * CONV_WARPS);
+        }
+        mbar_init(smem_u32(drainbar), 1);
+        mbar_fence_init();
+    }
+    if (warp == 0) {
+        __syncwarp();
+        if constexpr (PAIR) {
+            asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
+                             smem_u32(tmem_slot)), "r"(512u) : "memory");
+            asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+        } else {
+            asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
+                             smem_u32(tmem_slot)), "r"(512u) : "memory");
+            asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    if constexpr (PAIR) cluster_sync_all();
+    tc_fence_after();
+    const uint32_t tmem = *reinterpret_cast<volatile uint32_t *>(tmem_slot);
+
+    if (warp == PRODUCER_WARP) {
+        if (lane == 0) {
+            tma_prefetch_desc(&tmW);
+            tma_prefetch_desc(&tmX);
+            // Two rings filled by one thread: whichever has a free stage next.
+            // W may be read before the preceding kernel (the expansion of X)
+            // has finished: that kernel itself waited for all earlier work.
+            struct Cursor {
+                int u, s, s1, row;
+                uint32_t g;
+                bool done;
+            };
+            auto open = [&](Cursor &c, bool w) {
+                if (c.u >= units) {
+                    c.done = true;
+                    return;
+                }
+                int tn, tm;
+                plan_unit(plan, c.u, tn, tm, c.s, c.s1);
+                c.row = w ? tn * C::ROWS + 128 * (int)rank : tm * NT + C::NL * (int)rank;
+            };
+            auto step = [&](Cursor &c, bool w) {
+                ++c.g;
+                if (++c.s == c.s1) {
+                    c.u += workers;
+                    open(c, w);
+                }
+            };
+            Cursor w{worker, 0, 0, 0, 0u, false}, x{worker, 0, 0, 0, 0u, false};
+            open(w, true);
+            open(x, false);
+            bool ok = true, waited = false;
+            uint64_t t0 = 0;
+            int idle = 0;
+            while (!w.done || !x.done) {
+                bool moved = false;
+                if (!w.done) {
+                    const int s = (int)(w.g % WST);
+                    if (w.g < (uint32_t)WST || mbar_test(smem_u32(&wempty[s]), (w.g / WST - 1) & 1)) {
+                        const uint32_t bar = smem_u32(&wfull[s]);
+                        mbar_arrive_expect_tx(bar, W_STAGE);
+                        tma_load_2d(smem_u32(wring + (size_t)s * W_STAGE), &tmW, bar, w.s * KT, w.row);
+                        step(w, true);
+                        moved = true;
+                    }
+                }
+                if (!x.done && (waited || !moved || w.g >= (uint32_t)WST)) {
+                    if (!waited) {
+                        pdl_wait();   // the expanded X is there from here on
+                        asm volatile("fence.proxy.async;" ::: "memory");
+                        waited = true;
+                    }
+                    const int s = (int)(x.g % ST);
+                    if (x.g < (uint32_t)ST || mbar_test(smem_u32(&empty[s]), (x.g / ST - 1) & 1)) {
+                        const uint32_t dst = smem_u32(xring + (size_t)s * C::X_STAGE);
+                        if constexpr (PAIR) {
+                            if (lead) mbar_arrive_expect_tx(smem_u32(&xfull[s]), 2 * C::X_STAGE);
+                            tma_load_2d_pair(dst, &tmX, cluster_addr(smem_u32(&xfull[s]), 0), x.s * KT, x.row);
+                        } else {
+                            mbar_arrive_expect_tx(smem_u32(&xfull[s]), C::X_STAGE);
+                            tma_load_2d(dst, &tmX, smem_u32(&xfull[s]), x.s * KT, x.row);
+                        }
+                        step(x, false);
+                        moved = true;
+                    }
+                }
+                if (moved) {
+                    idle = 0;
+                } else if ((++idle & 255) == 0) {   // the clock is slow to read
+                    const uint64_t now = globaltimer_ns();
+                    if (idle == 256) t0 = now;
+                    else if (now - t0 > wait_ns) {
+                        ok = false;
+                        break;
+                    }
+                }
+            }
+            if (!ok) {   // wait for the copies still in flight
+                record_error(err, kErrWaitTimeout);
+                for (uint32_t q = (w.g > (uint32_t)WST ? w.g - WST : 0); q < w.g; ++q)
+                    mbar_wait(smem_u32(&wfull[q % WST]), (q / WST) & 1, DRAIN_NS);
+                if (lead) {
+                    for (uint32_t q = (x.g > (uint32_t)ST ? x.g - ST : 0); q < x.g; ++q)
+                        mbar_wait(smem_u32(&xfull[q % ST]), (q / ST) & 1, DRAIN_NS);
+                } else {
+                    // copies of the odd SM complete on the even SM's barriers,
+                    // possibly in phases it gave up on: give them time to land
+                    const uint64_t d0 = globaltimer_ns();
+                    while (globaltimer_ns() - d0 < 200000ull) {
+                    }
+                }
+            }
+        }
+    } else if (warp == MMA_WARP) {
+        if (lane == 0 && lead) {
+            auto wait = [&](uint64_t *bar, uint32_t parity) {
+                return PAIR ? mbar_wait_cluster(smem_u32(bar), parity, wait_ns)
+                            : mbar_wait(smem_u32(bar), parity, wait_ns);
+            };
+            auto commit = [&](uint64_t *bar) {
+                if constexpr (PAIR) tc2_commit_both(smem_u32(bar));
+                else tc_commit(smem_u32(bar));
+            };
+            bool ok = true, issued = false;
+            uint32_t g = 0, gc = 0;
+            for (int u = worker; u < units && ok; u += workers) {
+                int tn, tm, s0, s1;
+                plan_unit(plan, u, tn, tm, s0, s1);
+                for (int c0 = s0; c0 < s1 && ok; c0 += CHUNK, ++gc) {
+                    const int b = (int)(gc % C::DB);
+                    if (gc >= (uint32_t)C::DB && !wait(&dempty[b], (gc / C::DB - 1) & 1)) {
+                        ok = false;
+                        break;
+                    }
+                    tc_fence_after();
+                    const uint32_t d = tmem + (uint32_t)(b * NT);
+                    const int c1 = min(c0 + CHUNK, s1);
+                    for (int k = c0; k < c1; ++k, ++g) {
+                        const int s = (int)(g % ST);
+                        const uint32_t par = (g / ST) & 1;
+                        if (!wait(&xfull[s], par) || !wait(&afull[s], par)) {
+                            ok = false;
+                            break;
+                        }
+                        tc_fence_after();
+                        const uint32_t a = tmem + C::A_COL + (uint32_t)(s * (KT / 2));
+                        const uint32_t xb = smem_u32(xring + (size_t)s * C::X_STAGE);
+#pragma unroll
+                        for (int kk = 0; kk < KT / 16; ++kk)
+                            mma_ts<PAIR>(d, a + kk * 8, smem_desc<128>(xb + kk * 32), C::IDESC,
+                                         (k != c0 || kk != 0) ? 1u : 0u);
+                        issued = true;
+                        commit(&empty[s]);
+                    }
+                    if (ok) commit(&dfull[b]);
+                }
+            }
+            if (!ok) {
+                record_error(err, kErrWaitTimeout);
+                if (issued) {
+                    if constexpr (PAIR)
+                        asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(
+                                         smem_u32(drainbar)) : "memory");
+                    else
+                        tc_commit(smem_u32(drainbar));
+                    mbar_wait(smem_u32(drainbar), 0, DRAIN_NS);
+                }
+            }
+        }
+    } else {
+        // Converter warp w: tensor-memory lanes 32 * (w % 4) .. + 31 (a W row
+        // each); stages of parity w / 4; accumulator columns (w / 4) * COLS ..
+        const int half = warp >> 2, lane_base = (warp & 3) * 32;
+        const int row = lane_base + lane;
+        const uint32_t lane_addr = tmem + ((uint32_t)lane_base << 16);
+        uint32_t total = 0;
+        for (int u = worker; u < units; u += workers) {
+            int tn, tm, s0, s1;
+            plan_unit(plan, u, tn, tm, s0, s1);
+            total += (uint32_t)(s1 - s0);
+        }
+        bool ok = true;
+        uint32_t g = (uint32_t)half;     // next stage to expand
+        auto expand_until = [&](uint32_t end) {
+            for (; g < end; g += 2) {
+                const int w = (int)(g % WST), s = (int)(g % ST);
+                if (!warp_wait(smem_u32(&wfull[w]), (g / WST) & 1, wait_ns)) {
+                    ok = false;
+                    return;
+                }
+                const uint32_t src = smem_u32(wring + (size_t)w * W_STAGE) + (uint32_t)row * 64;
+                const uint32_t swz = (uint32_t)((row >> 1) & 3);   // the 64-byte swizzle of this row
+                uint4 q[4];
+#pragma unroll
+                for (int c = 0; c < 4; ++c) q[c] = lds128(src + (((uint32_t)c ^ swz) << 4));
+                uint32_t r[32];
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                    q8_to_f16(q[c].x, r[8 * c], r[8 * c + 1]);
+                    q8_to_f16(q[c].y, r[8 * c + 2], r[8 * c + 3]);
+                    q8_to_f16(q[c].z, r[8 * c + 4], r[8 * c + 5]);
+                    q8_to_f16(q[c].w, r[8 * c + 6], r[8 * c + 7]);
+                }
+                __syncwarp();
+                if (lane == 0) mbar_arrive(smem_u32(&wempty[w]));
+                if (g >= (uint32_t)ST) {
+                    if (!warp_wait(smem_u32(&empty[s]), (g / ST - 1) & 1, wait_ns)) {
+                        ok = false;
+                        return;
+                    }
+                    tc_fence_after();
+                }
+                tc_st32(lane_addr + C::A_COL + (uint32_t)(s * (KT / 2)), r);
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) {
+                    if constexpr (PAIR) arrive_relaxed(smem_u32(&afull[s]), 0);
+                    else mbar_arrive(smem_u32(&afull[s]));
+                }
+            }
+        };
+        uint32_t gc = 0, end = 0;
+        for (int u = worker; u < units && ok; u += workers) {
+            int tn, tm, s0, s1;
+            plan_unit(plan, u, tn, tm, s0, s1);
+            float acc[COLS];
+#pragma unroll
+            for (int j = 0; j < COLS; ++j) acc[j] = 0.0f;
+            for (int c0 = s0; c0 < s1; c0 += CHUNK, ++gc) {
+                end += (uint32_t)(min(c0 + CHUNK, s1) - c0);
+                expand_until(min(end + C::LEAD, total));
+                if (!ok) break;
+                const int b = (int)(gc % C::DB);
+                if (!warp_wait(smem_u32(&dfull[b]), (gc / C::DB) & 1, wait_ns)) {
+                    ok = false;
+                    break;
+                }
+                tc_fence_after();
+                const uint32_t d = lane_addr + (uint32_t)(b * NT + half * COLS);
+#pragma unroll
+                for (int piece = 0; piece < COLS / 16; ++piece) {
+                    float v[16];
+                    __syncwarp();
+                    tc_ld16(d + (uint32_t)(piece * 16), v);
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) acc[piece * 16 + i] += v[i];
+                }
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) {
+                    if constexpr (PAIR) arrive_relaxed(smem_u32(&dempty[b]), 0);
+                    else mbar_arrive(smem_u32(&dempty[b]));
+                }
+            }
+            if (!ok) break;
+            pdl_wait();   // returns at once: X's stages could not have come before
+            if (!PAIR && plan.ks > 1) {
+                // this unit's sums to the workspace; the last part's warp adds them all
+                const int tile = u / plan.ks, own = u - tile * plan.ks;
+                float *slot = part + ((int64_t)u * NT + half * COLS) * 128 + row;
+#pragma unroll
+                for (int j = 0; j < COLS; ++j) __stcg(slot + j * 128, acc[j]);
+                __threadfence();
+                __syncwarp();
+                uint32_t arrived = 0;
+                if (lane == 0) arrived = atomicAdd(counters + tile * CONV_WARPS + warp, 1u);
+                arrived = __shfl_sync(0xffffffffu, arrived, 0);
+                if (arrived != (uint32_t)(plan.ks - 1)) continue;
+                __threadfence();
+                float sum[COLS];
+#pragma unroll
+                for (int j = 0; j < COLS; ++j) sum[j] = 0.0f;
+                for (int p = 0; p < plan.ks; ++p) {
+                    const float *o = slot + (int64_t)(p - own) * NT * 128;
+#pragma unroll
+                    for (int j = 0; j < COLS; ++j) sum[j] += __ldcg(o + j * 128);
+                }
+#pragma unroll
+                for (int j = 0; j < COLS; ++j) acc[j] = sum[j];
+            }
+            // Column j of the accumulator is token m0 + j, this thread channel n:
+            // a warp stores 32 channels of one token at a time.
+            const int n = tn * C::ROWS + 128 * (int)rank + row;
+            const int m0 = tm * NT + half * COLS;
+            const float wsn = __ldg(ws + min(n, N - 1));
+            const float bias = ep.bias != nullptr ? __ldg(ep.bias + min(n, N - 1)) : 0.0f;
+            float xv[(COLS + 31) / 32];       // lane l holds the scale of token 32 i + l
+#pragma unroll
+            for (int i = 0; i < (COLS + 31) / 32; ++i) xv[i] = __ldg(xs + min(m0 + 32 * i + lane, M - 1));
+            OutT *o = out + (int64_t)m0 * ldc + n;
+            auto store = [&](auto act) {
+#pragma unroll
+                for (int j = 0; j < COLS; ++j) {
+                    const float x = __shfl_sync(0xffffffffu, xv[j / 32], j % 32);
+                    if (n < N && m0 + j < M)
+                        o[(int64_t)j * ldc] = from_f32<OutT>(act(acc[j] * x * wsn + bias));
+                }
+            };
+            switch (ep.act) {
+                case kActRelu: store([](float v) { return activate<kActRelu>(v); }); break;
+                case kActGelu: store([](float v) { return activate<kActGelu>(v); }); break;
+                case kActSilu: store([](float v) { return activate<kActSilu>(v); }); break;
+                default: store([](float v) { return v; });
+            }
+        }
+        if (!ok && lane == 0) record_error(err, kErrWaitTimeout);
+    }
+
+    tc_fence_before();
+    __syncthreads();
+    if constexpr (PAIR) cluster_sync_all();
+    if (warp == 0) {
+        __syncwarp();
+        tc_fence_after();
+        if constexpr (PAIR)
+            asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512u) : "memory");
+        else
+            asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512u) : "memory");
+    }
+}
+
+// X (any alignment and stride) as FP16 [M][ldh], ldh a multiple of 16, zeros
+// past K; also clears `nzero` words.
+__global__ void __launch_bounds__(256)
+q8_expand_kernel(int M, int K, const int8_t *__restrict__ X, int64_t ldx, int vec, uint16_t *__restrict__ H,
+                 int64_t ldh, uint32_t *zero, int nzero) {
+    pdl_wait();
+    pdl_trigger();
+    const int64_t i0 = (int64_t)blockIdx.x * blockDim.x + threadIdx.x, stride = (int64_t)gridDim.x * blockDim.x;
+    for (int64_t i = i0; i < nzero; i += stride) zero[i] = 0u;
+    const int64_t per_row = ldh / 16, total = per_row * M;
+    for (int64_t i = i0; i < total; i += stride) {
+        const int64_t m = i / per_row, k = (i - m * per_row) * 16;
+        const int8_t *p = X + m * ldx + k;
+        uint32_t w[4] = {0u, 0u, 0u, 0u};
+        if (vec && k + 16 <= K) {
+            const uint4 v = *reinterpret_cast<const uint4 *>(p);
+            w[0] = v.x; w[1] = v.y; w[2] = v.z; w[3] = v.w;
+        } else {
+#pragma unroll
+            for (int j = 0; j < 16; ++j)
+                if (k + j < K) w[j >> 2] |= (uint32_t)(uint8_t)p[j] << (8 * (j & 3));
+        }
+        uint32_t r[8];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) q8_to_f16(w[j], r[2 * j], r[2 * j + 1]);
+        uint4 *o = reinterpret_cast<uint4 *>(H + m * ldh + k);
+        o[0] = make_uint4(r[0], r[1], r[2], r[3]);
+        o[1] = make_uint4(r[4], r[5], r[6], r[7]);
+    }
+}
+
+// Rows of W at any alignment to 16-byte aligned rows (ldo a multiple of 16,
+// zeros past K).
+__global__ void __launch_bounds__(256)
+q8_align_kernel(int N, int K, const int8_t *__restrict__ W, int64_t ldw, int8_t *__restrict__ O, int64_t ldo) {
+    pdl_wait();
+    pdl_trigger();
+    const int64_t per_row = ldo / 16, total = per_row * N;
+    for (int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; i < total; i += (int64_t)gridDim.x * blockDim.x) {
+        const int64_t n = i / per_row, k = (i - n * per_row) * 16;
+        const int8_t *p = W + n * ldw + k;
+        uint32_t w[4] = {0u, 0u, 0u, 0u};
+#pragma unroll
+        for (int j = 0; j < 16; ++j)
+            if (k + j < K) w[j >> 2] |= (uint32_t)(uint8_t)p[j] << (8 * (j & 3));
+        *reinterpret_cast<uint4 *>(O + n * ldo + k) = make_uint4(w[0], w[1], w[2], w[3]);
+    }
+}
+
+bool encode_bytes(EncodeTiledFn enc, CUtensorMap *map, const int8_t *base, int64_t inner, int64_t rows, int64_t ld,
+                  uint32_t box_inner, uint32_t box_rows) {
+    if (enc == nullptr) return false;
+    const cuuint64_t dims[2] = {(cuuint64_t)inner, (cuuint64_t)rows};
+    const cuuint64_t strides[1] = {(cuuint64_t)ld};
+    const cuuint32_t box[2] = {box_inner, box_rows};
+    const cuuint32_t estr[2] = {1, 1};
+    return enc(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<int8_t *>(base), dims, strides, box, estr,
+               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_64B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <typename... P, typename... A>
+cudaError_t launch_with(void (*kern)(P...), unsigned grid, int threads, size_t smem, int cluster, cudaStream_t s,
+                        A... args) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(grid, 1, 1);
+    cfg.blockDim = dim3((unsigned)threads, 1, 1);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = (unsigned)cluster;
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = cluster > 1 ? 2 : 1;
+    return cudaLaunchKernelEx(&cfg, kern, args...);
+}
+
+constexpr int64_t round16(int64_t v) { return (v + 15) / 16 * 16; }
+constexpr size_t round256(size_t v) { return (v + 255) / 256 * 256; }
+
+// Which tile a product runs on, and its division.
+struct Choice {
+    int nt;          // tokens per tile: 32, 64, 128, or 256 (pair)
+    Plan plan;
+    int workers;     // CTAs, or pairs of them
+};
+
+Choice choose(int64_t M, int64_t N, int64_t K, int sms) {
+    Choice c{};
+    const int stages = (int)((K + KT - 1) / KT);
+    c.nt = M <= 32 ? 32 : M <= 64 ? 64 : 128;
+    const int64_t pair_tiles = ((N + 255) / 256) * ((M + 255) / 256);
+    if (M > 128 && pair_tiles >= sms / 4) c.nt = 256;
+    const int rows = c.nt == 256 ? 256 : 128;
+    Plan &p = c.plan;
+    p.nt = (int)((N + rows - 1) / rows);
+    p.mt = (int)((M + c.nt - 1) / c.nt);
+    p.stages = stages;
+    p.ks = 1;
+    if (c.nt != 256) {
+        // the number of parts that ends soonest: rounds of units, each its
+        // stages and a fixed cost (set-up and the exchange of sums)
+        const int64_t tiles = (int64_t)p.nt * p.mt;
+        int64_t best = INT64_MAX;
+        for (int ks = 1; ks <= 16 && ks <= stages; ++ks) {
+            const int64_t per = (stages + ks - 1) / ks;
+            const int64_t rounds = (tiles * ks + sms - 1) / sms;
+            const int64_t cost = rounds * (per + 2) + (ks > 1 ? 6 : 0);
+            if (cost < best) {
+                best = cost;
+                p.ks = ks;
+            }
+        }
+    }
+    p.per = (stages + p.ks - 1) / p.ks;
+    p.ks = (stages + p.per - 1) / p.per;
+    const int w = c.nt == 256 ? sms / 2 : sms;
+    c.workers = p.units() < w ? p.units() : w;
+    return c;
+}
+
+struct Layout {
+    int64_t ldh, ldw;
+    size_t x, w, part, counters, total;
+    int ncounters;
+};
+
+Layout layout(const Q8LinearArgs &a, const Choice &c, bool copy_w) {
+    Layout l{};
+    l.ldh = round16(a.K);
+    l.ldw = copy_w ? round16(a.K) : a.ldw;
+    size_t at = 0;
+    l.x = at; at += round256((size_t)a.M * l.ldh * 2);
+    l.w = at; at += copy_w ? round256((size_t)a.N * l.ldw) : 0;
+    l.part = at; at += c.plan.ks > 1 ? round256((size_t)c.plan.units() * c.nt * 128 * 4) : 0;
+    l.ncounters = c.plan.ks > 1 ? c.plan.nt * c.plan.mt * CONV_WARPS : 0;
+    l.counters = at; at += round256((size_t)l.ncounters * 4);
+    l.total = at;
+    return l;
+}
+
+template <typename C, typename OutT>
+cudaError_t launch_c(const Q8LinearArgs &a, const Choice &c, const Layout &l, unsigned char *ws, const int8_t *W) {
+    alignas(64) CUtensorMap tW, tX;
+    if (!encode_bytes(a.encode, &tW, W, a.K, a.N, l.ldw, KT, 128) ||
+        !encode_tma_2d_bf16(a.encode, &tX, ws + l.x, l.ldh, a.M, l.ldh, KT, C::NL, CU_TENSOR_MAP_SWIZZLE_128B))
+        return cudaErrorInvalidValue;
+    auto kern = q8_mma_kernel<C, OutT>;
+    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)C::SMEM);
+    if (e != cudaSuccess) return e;
+    const unsigned grid = (unsigned)(C::PAIR ? 2 * c.workers : c.workers);
+    return launch_with(kern, grid, THREADS, C::SMEM, C::PAIR ? 2 : 1, a.stream, tW, tX, (int)a.M, (int)a.N, c.plan,
+                       a.xs, a.ws, Epilogue{1.0f, 0.0f, a.bias, a.act}, (OutT *)a.C, a.ldc,
+                       reinterpret_cast<float *>(ws + l.part), reinterpret_cast<uint32_t *>(ws + l.counters), a.err,
+                       a.wait_ns);
+}
+
+template <typename OutT>
+cudaError_t launch_o(const Q8LinearArgs &a, const Choice &c, const Layout &l, unsigned char *ws, const int8_t *W) {
+    switch (c.nt) {
+        case 32: return launch_c<Cfg<32, false>, OutT>(a, c, l, ws, W);
+        case 64: return launch_c<Cfg<64, false>, OutT>(a, c, l, ws, W);
+        case 128: return launch_c<Cfg<128, false>, OutT>(a, c, l, ws, W);
+        default: return launch_c<Cfg<256, true>, OutT>(a, c, l, ws, W);
+    }
+}
+
+bool w_aligned(const Q8LinearArgs &a) {
+    return reinterpret_cast<uintptr_t>(a.W) % 16 == 0 && a.ldw % 16 == 0;
+}
+
+unsigned grid_for(int64_t items, int sms) {
+    const int64_t blocks = (items + 255) / 256, most = (int64_t)sms * 8;
+    return (unsigned)(blocks < 1 ? 1 : blocks < most ? blocks : most);
+}
+
+}  // namespace
+
+bool q8_mma_can_run(const Q8LinearArgs &a) {
+    if (a.K < 1) return false;
+    const int64_t tiles = ((a.N + 127) / 128) * ((a.M + 31) / 32);
+    return tiles <= (INT32_MAX >> 6);
+}
+
+size_t q8_mma_workspace_bytes(const Q8LinearArgs &a) {
+    return layout(a, choose(a.M, a.N, a.K, a.sm_count), !w_aligned(a)).total;
+}
+
+cudaError_t launch_q8_mma(const Q8LinearArgs &a, void *workspace) {
+    unsigned char *ws = static_cast<unsigned char *>(workspace);
+    const bool copy_w = !w_aligned(a);
+    const Choice c = choose(a.M, a.N, a.K, a.sm_count);
+    const Layout l = layout(a, c, copy_w);
+    const int8_t *W = a.W;
+    if (copy_w) {
+        int8_t *o = reinterpret_cast<int8_t *>(ws + l.w);
+        const cudaError_t e = launch_with(q8_align_kernel, grid_for(a.N * (l.ldw / 16), a.sm_count), 256, 0, 1,
+                                          a.stream, (int)a.N, (int)a.K, a.W, a.ldw, o, l.ldw);
+        if (e != cudaSuccess) return e;
+        W = o;
+    }
+    const int vec = reinterpret_cast<uintptr_t>(a.X) % 16 == 0 && a.ldx % 16 == 0;
+    const cudaError_t e = launch_with(q8_expand_kernel, grid_for(a.M * (l.ldh / 16), a.sm_count), 256, 0, 1, a.stream,
+                                      (int)a.M, (int)a.K, a.X, a.ldx, vec, reinterpret_cast<uint16_t *>(ws + l.x),
+                                      l.ldh, reinterpret_cast<uint32_t *>(ws + l.counters), l.ncounters);
+    if (e != cudaSuccess) return e;
+    return a.type == kTypeBf16 ? launch_o<__nv_bfloat16>(a, c, l, ws, W) : launch_o<float>(a, c, l, ws, W);
+}
+
+}  // namespace sgemm_gb300
