@@ -14,7 +14,7 @@
 // waste nothing and C's rows are stored 32 channels at a time.
 //
 //   W   travels and rests in 8 bits.  TMA brings 64 k of 128 rows into a
-//       shared-memory ring; eight converter warps read a row per thread, expand
+//       shared-memory ring; four converter warps read a row per thread, expand
 //       it to FP16 in registers and store it to tensor memory, from where the
 //       MMA takes its A operand.  The 16-bit form of W never touches shared
 //       memory, whose bandwidth is what bounds such a kernel (8 KB written and
@@ -22,7 +22,9 @@
 //   X   is expanded to FP16 once, by a kernel before (2 bytes of L2 traffic per
 //       element), and comes in by TMA as the B operand, 64 k per stage.
 //   MMA one thread issues four tcgen05.mma kind::f16 per stage.
-//   The converter warps also empty the accumulator, add the chunks and store.
+//   Eight more warps empty the accumulator, add the chunks and store.  The
+//       warpgroups trade registers (setmaxnreg), so that each of these threads
+//       can hold its 128 sums.
 //
 // PAIR: two SMs share a tile of 256 W rows x NT tokens (cta_group::2), each
 // with its own 128 rows of W and half of the tokens' X.
@@ -42,9 +44,16 @@
 namespace sgemm_gb300 {
 namespace {
 
-constexpr int CONV_WARPS = 8;
-constexpr int PRODUCER_WARP = CONV_WARPS, MMA_WARP = CONV_WARPS + 1;
-constexpr int THREADS = (CONV_WARPS + 2) * 32;
+// Warpgroups: two that empty the accumulator, one of converters, and one whose
+// first two warps are the producer and the MMA issuer.
+constexpr int EPI_WARPS = 8, CONV_WARPS = 4;
+constexpr int PRODUCER_WARP = EPI_WARPS + CONV_WARPS, MMA_WARP = PRODUCER_WARP + 1;
+constexpr int THREADS = (EPI_WARPS + CONV_WARPS + 4) * 32;
+// Registers per thread: at launch, and what each warpgroup takes.  The shares
+// have to add up to no more than the launch's, or setmaxnreg.inc would wait.
+constexpr int REGS = 128, EPI_REGS = 176, CONV_REGS = 96, OTHER_REGS = 64;
+static_assert(EPI_REGS * EPI_WARPS + CONV_REGS * CONV_WARPS + OTHER_REGS * 4 <= REGS * (THREADS / 32),
+              "register shares");
 constexpr int KT = 64;                        // k per stage
 constexpr int CHUNK = 16;                     // stages per accumulation chunk: 1024 k
 constexpr uint32_t W_STAGE = 128 * KT;        // bytes
@@ -61,8 +70,7 @@ struct Cfg {
     static constexpr int WST = NT <= 64 ? 14 : 8;          // W stages
     static constexpr uint32_t X_STAGE = NL * 128;          // bytes: 64 FP16 per token
     static constexpr uint32_t A_COL = DB * NT;             // tensor-memory column of A stage 0
-    static constexpr int COLS = NT / 2;                    // columns per converter thread
-    static constexpr int LEAD = ST - 2;                    // stages converted ahead of a drain
+    static constexpr int COLS = NT / 2;                    // columns per epilogue thread
     static constexpr size_t SMEM = 1024 + (size_t)ST * X_STAGE + (size_t)WST * W_STAGE + 512;
     // kind::f16, FP16 operands (format 0), FP32 accumulator, both K-major
     static constexpr uint32_t IDESC = (1u << 4) | ((uint32_t)(NT >> 3) << 17) | ((uint32_t)(ROWS >> 4) << 24);
@@ -121,8 +129,8 @@ __device__ __forceinline__ void tc_st32(uint32_t taddr, const uint32_t (&r)[32])
         "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]),
         "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
         : "memory");
-    asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
 }
+__device__ __forceinline__ void tc_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
 __device__ __forceinline__ uint4 lds128(uint32_t a) {
     uint4 v;
@@ -153,14 +161,15 @@ __device__ __forceinline__ bool mbar_test(uint32_t bar, uint32_t parity) {
     return ok != 0;
 }
 
-// Lane 0 waits for the whole warp; the others then see the completed phase.
+// The whole warp waits, and agrees on whether the phase completed.
 __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, uint64_t limit_ns) {
-    const int lane = threadIdx.x & 31;
-    int ok = lane == 0 ? (int)mbar_wait(bar, parity, limit_ns) : 0;
-    ok = __shfl_sync(0xffffffffu, ok, 0);
-    if (!ok) return false;
-    mbar_wait(bar, parity, DRAIN_NS);
-    return true;
+    return __all_sync(0xffffffffu, mbar_wait(bar, parity, limit_ns)) != 0;
+}
+
+template <int N, bool UP>
+__device__ __forceinline__ void set_registers() {
+    if constexpr (UP) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+    else asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
 }
 
 template <typename C, typename OutT>
@@ -196,16 +205,16 @@ q8_mma_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ C
     if (threadIdx.x == 0) {
         for (int s = 0; s < WST; ++s) {
             mbar_init(smem_u32(&wfull[s]), 1);
-            mbar_init(smem_u32(&wempty[s]), CONV_WARPS / 2);
+            mbar_init(smem_u32(&wempty[s]), CONV_WARPS);
         }
         for (int s = 0; s < ST; ++s) {
             mbar_init(smem_u32(&xfull[s]), 1);
-            mbar_init(smem_u32(&afull[s]), (PAIR ? 2 : 1) * CONV_WARPS / 2);
+            mbar_init(smem_u32(&afull[s]), (PAIR ? 2 : 1) * CONV_WARPS);
             mbar_init(smem_u32(&empty[s]), 1);
         }
         for (int b = 0; b < 2; ++b) {
             mbar_init(smem_u32(&dfull[b]), 1);
-            mbar_init(smem_u32(&dempty[b]), (PAIR ? 2 : 1) * CONV_WARPS);
+            mbar_init(smem_u32(&dempty[b]), (PAIR ? 2 : 1) * EPI_WARPS);
         }
         mbar_init(smem_u32(drainbar), 1);
         mbar_fence_init();
@@ -228,208 +237,15 @@ q8_mma_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ C
     tc_fence_after();
     const uint32_t tmem = *reinterpret_cast<volatile uint32_t *>(tmem_slot);
 
-    if (warp == PRODUCER_WARP) {
-        if (lane == 0) {
-            tma_prefetch_desc(&tmW);
-            tma_prefetch_desc(&tmX);
-            // Two rings filled by one thread: whichever has a free stage next.
-            // W may be read before the preceding kernel (the expansion of X)
-            // has finished: that kernel itself waited for all earlier work.
-            struct Cursor {
-                int u, s, s1, row;
-                uint32_t g;
-                bool done;
-            };
-            auto open = [&](Cursor &c, bool w) {
-                if (c.u >= units) {
-                    c.done = true;
-                    return;
-                }
-                int tn, tm;
-                plan_unit(plan, c.u, tn, tm, c.s, c.s1);
-                c.row = w ? tn * C::ROWS + 128 * (int)rank : tm * NT + C::NL * (int)rank;
-            };
-            auto step = [&](Cursor &c, bool w) {
-                ++c.g;
-                if (++c.s == c.s1) {
-                    c.u += workers;
-                    open(c, w);
-                }
-            };
-            Cursor w{worker, 0, 0, 0, 0u, false}, x{worker, 0, 0, 0, 0u, false};
-            open(w, true);
-            open(x, false);
-            bool ok = true, waited = false;
-            uint64_t t0 = 0;
-            int idle = 0;
-            while (!w.done || !x.done) {
-                bool moved = false;
-                if (!w.done) {
-                    const int s = (int)(w.g % WST);
-                    if (w.g < (uint32_t)WST || mbar_test(smem_u32(&wempty[s]), (w.g / WST - 1) & 1)) {
-                        const uint32_t bar = smem_u32(&wfull[s]);
-                        mbar_arrive_expect_tx(bar, W_STAGE);
-                        tma_load_2d(smem_u32(wring + (size_t)s * W_STAGE), &tmW, bar, w.s * KT, w.row);
-                        step(w, true);
-                        moved = true;
-                    }
-                }
-                if (!x.done && (waited || !moved || w.g >= (uint32_t)WST)) {
-                    if (!waited) {
-                        pdl_wait();   // the expanded X is there from here on
-                        asm volatile("fence.proxy.async;" ::: "memory");
-                        waited = true;
-                    }
-                    const int s = (int)(x.g % ST);
-                    if (x.g < (uint32_t)ST || mbar_test(smem_u32(&empty[s]), (x.g / ST - 1) & 1)) {
-                        const uint32_t dst = smem_u32(xring + (size_t)s * C::X_STAGE);
-                        if constexpr (PAIR) {
-                            if (lead) mbar_arrive_expect_tx(smem_u32(&xfull[s]), 2 * C::X_STAGE);
-                            tma_load_2d_pair(dst, &tmX, cluster_addr(smem_u32(&xfull[s]), 0), x.s * KT, x.row);
-                        } else {
-                            mbar_arrive_expect_tx(smem_u32(&xfull[s]), C::X_STAGE);
-                            tma_load_2d(dst, &tmX, smem_u32(&xfull[s]), x.s * KT, x.row);
-                        }
-                        step(x, false);
-                        moved = true;
-                    }
-                }
-                if (moved) {
-                    idle = 0;
-                } else if ((++idle & 255) == 0) {   // the clock is slow to read
-                    const uint64_t now = globaltimer_ns();
-                    if (idle == 256) t0 = now;
-                    else if (now - t0 > wait_ns) {
-                        ok = false;
-                        break;
-                    }
-                }
-            }
-            if (!ok) {   // wait for the copies still in flight
-                record_error(err, kErrWaitTimeout);
-                for (uint32_t q = (w.g > (uint32_t)WST ? w.g - WST : 0); q < w.g; ++q)
-                    mbar_wait(smem_u32(&wfull[q % WST]), (q / WST) & 1, DRAIN_NS);
-                if (lead) {
-                    for (uint32_t q = (x.g > (uint32_t)ST ? x.g - ST : 0); q < x.g; ++q)
-                        mbar_wait(smem_u32(&xfull[q % ST]), (q / ST) & 1, DRAIN_NS);
-                } else {
-                    // copies of the odd SM complete on the even SM's barriers,
-                    // possibly in phases it gave up on: give them time to land
-                    const uint64_t d0 = globaltimer_ns();
-                    while (globaltimer_ns() - d0 < 200000ull) {
-                    }
-                }
-            }
-        }
-    } else if (warp == MMA_WARP) {
-        if (lane == 0 && lead) {
-            auto wait = [&](uint64_t *bar, uint32_t parity) {
-                return PAIR ? mbar_wait_cluster(smem_u32(bar), parity, wait_ns)
-                            : mbar_wait(smem_u32(bar), parity, wait_ns);
-            };
-            auto commit = [&](uint64_t *bar) {
-                if constexpr (PAIR) tc2_commit_both(smem_u32(bar));
-                else tc_commit(smem_u32(bar));
-            };
-            bool ok = true, issued = false;
-            uint32_t g = 0, gc = 0;
-            for (int u = worker; u < units && ok; u += workers) {
-                int tn, tm, s0, s1;
-                plan_unit(plan, u, tn, tm, s0, s1);
-                for (int c0 = s0; c0 < s1 && ok; c0 += CHUNK, ++gc) {
-                    const int b = (int)(gc % C::DB);
-                    if (gc >= (uint32_t)C::DB && !wait(&dempty[b], (gc / C::DB - 1) & 1)) {
-                        ok = false;
-                        break;
-                    }
-                    tc_fence_after();
-                    const uint32_t d = tmem + (uint32_t)(b * NT);
-                    const int c1 = min(c0 + CHUNK, s1);
-                    for (int k = c0; k < c1; ++k, ++g) {
-                        const int s = (int)(g % ST);
-                        const uint32_t par = (g / ST) & 1;
-                        if (!wait(&xfull[s], par) || !wait(&afull[s], par)) {
-                            ok = false;
-                            break;
-                        }
-                        tc_fence_after();
-                        const uint32_t a = tmem + C::A_COL + (uint32_t)(s * (KT / 2));
-                        const uint32_t xb = smem_u32(xring + (size_t)s * C::X_STAGE);
-#pragma unroll
-                        for (int kk = 0; kk < KT / 16; ++kk)
-                            mma_ts<PAIR>(d, a + kk * 8, smem_desc<128>(xb + kk * 32), C::IDESC,
-                                         (k != c0 || kk != 0) ? 1u : 0u);
-                        issued = true;
-                        commit(&empty[s]);
-                    }
-                    if (ok) commit(&dfull[b]);
-                }
-            }
-            if (!ok) {
-                record_error(err, kErrWaitTimeout);
-                if (issued) {
-                    if constexpr (PAIR)
-                        asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(
-                                         smem_u32(drainbar)) : "memory");
-                    else
-                        tc_commit(smem_u32(drainbar));
-                    mbar_wait(smem_u32(drainbar), 0, DRAIN_NS);
-                }
-            }
-        }
-    } else {
-        // Converter warp w: tensor-memory lanes 32 * (w % 4) .. + 31 (a W row
-        // each); stages of parity w / 4; accumulator columns (w / 4) * COLS ..
+    if (warp < EPI_WARPS) {
+        // Epilogue warp w: tensor-memory lanes 32 * (w % 4) .. + 31 (a W row
+        // each), accumulator columns (w / 4) * COLS .. + COLS (tokens).
+        set_registers<EPI_REGS, true>();
         const int half = warp >> 2, lane_base = (warp & 3) * 32;
         const int row = lane_base + lane;
         const uint32_t lane_addr = tmem + ((uint32_t)lane_base << 16);
-        uint32_t total = 0;
-        for (int u = worker; u < units; u += workers) {
-            int tn, tm, s0, s1;
-            plan_unit(plan, u, tn, tm, s0, s1);
-            total += (uint32_t)(s1 - s0);
-        }
         bool ok = true;
-        uint32_t g = (uint32_t)half;     // next stage to expand
-        auto expand_until = [&](uint32_t end) {
-            for (; g < end; g += 2) {
-                const int w = (int)(g % WST), s = (int)(g % ST);
-                if (!warp_wait(smem_u32(&wfull[w]), (g / WST) & 1, wait_ns)) {
-                    ok = false;
-                    return;
-                }
-                const uint32_t src = smem_u32(wring + (size_t)w * W_STAGE) + (uint32_t)row * 64;
-                const uint32_t swz = (uint32_t)((row >> 1) & 3);   // the 64-byte swizzle of this row
-                uint4 q[4];
-#pragma unroll
-                for (int c = 0; c < 4; ++c) q[c] = lds128(src + (((uint32_t)c ^ swz) << 4));
-                uint32_t r[32];
-#pragma unroll
-                for (int c = 0; c < 4; ++c) {
-                    q8_to_f16(q[c].x, r[8 * c], r[8 * c + 1]);
-                    q8_to_f16(q[c].y, r[8 * c + 2], r[8 * c + 3]);
-                    q8_to_f16(q[c].z, r[8 * c + 4], r[8 * c + 5]);
-                    q8_to_f16(q[c].w, r[8 * c + 6], r[8 * c + 7]);
-                }
-                __syncwarp();
-                if (lane == 0) mbar_arrive(smem_u32(&wempty[w]));
-                if (g >= (uint32_t)ST) {
-                    if (!warp_wait(smem_u32(&empty[s]), (g / ST - 1) & 1, wait_ns)) {
-                        ok = false;
-                        return;
-                    }
-                    tc_fence_after();
-                }
-                tc_st32(lane_addr + C::A_COL + (uint32_t)(s * (KT / 2)), r);
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) {
-                    if constexpr (PAIR) arrive_relaxed(smem_u32(&afull[s]), 0);
-                    else mbar_arrive(smem_u32(&afull[s]));
-                }
-            }
-        };
-        uint32_t gc = 0, end = 0;
+        uint32_t gc = 0;
         for (int u = worker; u < units && ok; u += workers) {
             int tn, tm, s0, s1;
             plan_unit(plan, u, tn, tm, s0, s1);
@@ -437,9 +253,6 @@ q8_mma_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ C
 #pragma unroll
             for (int j = 0; j < COLS; ++j) acc[j] = 0.0f;
             for (int c0 = s0; c0 < s1; c0 += CHUNK, ++gc) {
-                end += (uint32_t)(min(c0 + CHUNK, s1) - c0);
-                expand_until(min(end + C::LEAD, total));
-                if (!ok) break;
                 const int b = (int)(gc % C::DB);
                 if (!warp_wait(smem_u32(&dfull[b]), (gc / C::DB) & 1, wait_ns)) {
                     ok = false;
@@ -473,7 +286,7 @@ q8_mma_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ C
                 __threadfence();
                 __syncwarp();
                 uint32_t arrived = 0;
-                if (lane == 0) arrived = atomicAdd(counters + tile * CONV_WARPS + warp, 1u);
+                if (lane == 0) arrived = atomicAdd(counters + tile * EPI_WARPS + warp, 1u);
                 arrived = __shfl_sync(0xffffffffu, arrived, 0);
                 if (arrived != (uint32_t)(plan.ks - 1)) continue;
                 __threadfence();
@@ -514,6 +327,213 @@ q8_mma_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ C
             }
         }
         if (!ok && lane == 0) record_error(err, kErrWaitTimeout);
+    } else if (warp < PRODUCER_WARP) {
+        // Converter warp w: W rows (tensor-memory lanes) 32 * (w % 4) .. + 31,
+        // every stage.  The next stage's bytes are read before this one's are
+        // handed over.
+        set_registers<CONV_REGS, false>();
+        const int lane_base = (warp & 3) * 32;
+        const int row = lane_base + lane;
+        const uint32_t a_addr = tmem + ((uint32_t)lane_base << 16) + C::A_COL;
+        const uint32_t swz = (uint32_t)((row >> 1) & 3);   // the 64-byte swizzle of this row
+        uint32_t total = 0;
+        for (int u = worker; u < units; u += workers) {
+            int tn, tm, s0, s1;
+            plan_unit(plan, u, tn, tm, s0, s1);
+            total += (uint32_t)(s1 - s0);
+        }
+        uint4 q[4];
+        auto fetch = [&](uint32_t g) {
+            const int w = (int)(g % WST);
+            if (!warp_wait(smem_u32(&wfull[w]), (g / WST) & 1, wait_ns)) return false;
+            const uint32_t src = smem_u32(wring + (size_t)w * W_STAGE) + (uint32_t)row * 64;
+#pragma unroll
+            for (int c = 0; c < 4; ++c) q[c] = lds128(src + (((uint32_t)c ^ swz) << 4));
+            return true;
+        };
+        bool ok = total == 0 || fetch(0);
+        for (uint32_t g = 0; g < total && ok; ++g) {
+            const int s = (int)(g % ST);
+            uint32_t r[32];
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+                q8_to_f16(q[c].x, r[8 * c], r[8 * c + 1]);
+                q8_to_f16(q[c].y, r[8 * c + 2], r[8 * c + 3]);
+                q8_to_f16(q[c].z, r[8 * c + 4], r[8 * c + 5]);
+                q8_to_f16(q[c].w, r[8 * c + 6], r[8 * c + 7]);
+            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(smem_u32(&wempty[g % WST]));
+            if (g >= (uint32_t)ST) {
+                if (!warp_wait(smem_u32(&empty[s]), (g / ST - 1) & 1, wait_ns)) {
+                    ok = false;
+                    break;
+                }
+                tc_fence_after();
+            }
+            tc_st32(a_addr + (uint32_t)(s * (KT / 2)), r);
+            if (g + 1 < total) ok = fetch(g + 1);
+            tc_st_wait();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) {
+                if constexpr (PAIR) arrive_relaxed(smem_u32(&afull[s]), 0);
+                else mbar_arrive(smem_u32(&afull[s]));
+            }
+        }
+        if (!ok && lane == 0) record_error(err, kErrWaitTimeout);
+    } else {
+        set_registers<OTHER_REGS, false>();
+        if (warp == PRODUCER_WARP) {
+            if (lane == 0) {
+                tma_prefetch_desc(&tmW);
+                tma_prefetch_desc(&tmX);
+                // Two rings filled by one thread: whichever has a free stage next.
+                // W may be read before the preceding kernel (the expansion of X)
+                // has finished: that kernel itself waited for all earlier work.
+                struct Cursor {
+                    int u, s, s1, row;
+                    uint32_t g;
+                    bool done;
+                };
+                auto open = [&](Cursor &c, bool w) {
+                    if (c.u >= units) {
+                        c.done = true;
+                        return;
+                    }
+                    int tn, tm;
+                    plan_unit(plan, c.u, tn, tm, c.s, c.s1);
+                    c.row = w ? tn * C::ROWS + 128 * (int)rank : tm * NT + C::NL * (int)rank;
+                };
+                auto step = [&](Cursor &c, bool w) {
+                    ++c.g;
+                    if (++c.s == c.s1) {
+                        c.u += workers;
+                        open(c, w);
+                    }
+                };
+                Cursor w{worker, 0, 0, 0, 0u, false}, x{worker, 0, 0, 0, 0u, false};
+                open(w, true);
+                open(x, false);
+                bool ok = true, waited = false;
+                uint64_t t0 = 0;
+                int idle = 0;
+                while (!w.done || !x.done) {
+                    bool moved = false;
+                    if (!w.done) {
+                        const int s = (int)(w.g % WST);
+                        if (w.g < (uint32_t)WST || mbar_test(smem_u32(&wempty[s]), (w.g / WST - 1) & 1)) {
+                            const uint32_t bar = smem_u32(&wfull[s]);
+                            mbar_arrive_expect_tx(bar, W_STAGE);
+                            tma_load_2d(smem_u32(wring + (size_t)s * W_STAGE), &tmW, bar, w.s * KT, w.row);
+                            step(w, true);
+                            moved = true;
+                        }
+                    }
+                    if (!x.done && (waited || !moved || w.g >= (uint32_t)WST)) {
+                        if (!waited) {
+                            pdl_wait();   // the expanded X is there from here on
+                            asm volatile("fence.proxy.async;" ::: "memory");
+                            waited = true;
+                        }
+                        const int s = (int)(x.g % ST);
+                        if (x.g < (uint32_t)ST || mbar_test(smem_u32(&empty[s]), (x.g / ST - 1) & 1)) {
+                            const uint32_t dst = smem_u32(xring + (size_t)s * C::X_STAGE);
+                            if constexpr (PAIR) {
+                                if (lead) mbar_arrive_expect_tx(smem_u32(&xfull[s]), 2 * C::X_STAGE);
+                                tma_load_2d_pair(dst, &tmX, cluster_addr(smem_u32(&xfull[s]), 0), x.s * KT, x.row);
+                            } else {
+                                mbar_arrive_expect_tx(smem_u32(&xfull[s]), C::X_STAGE);
+                                tma_load_2d(dst, &tmX, smem_u32(&xfull[s]), x.s * KT, x.row);
+                            }
+                            step(x, false);
+                            moved = true;
+                        }
+                    }
+                    if (moved) {
+                        idle = 0;
+                    } else if ((++idle & 255) == 0) {   // the clock is slow to read
+                        const uint64_t now = globaltimer_ns();
+                        if (idle == 256) t0 = now;
+                        else if (now - t0 > wait_ns) {
+                            ok = false;
+                            break;
+                        }
+                    }
+                }
+                if (!ok) {   // wait for the copies still in flight
+                    record_error(err, kErrWaitTimeout);
+                    for (uint32_t q = (w.g > (uint32_t)WST ? w.g - WST : 0); q < w.g; ++q)
+                        mbar_wait(smem_u32(&wfull[q % WST]), (q / WST) & 1, DRAIN_NS);
+                    if (lead) {
+                        for (uint32_t q = (x.g > (uint32_t)ST ? x.g - ST : 0); q < x.g; ++q)
+                            mbar_wait(smem_u32(&xfull[q % ST]), (q / ST) & 1, DRAIN_NS);
+                    } else {
+                        // copies of the odd SM complete on the even SM's barriers,
+                        // possibly in phases it gave up on: give them time to land
+                        const uint64_t d0 = globaltimer_ns();
+                        while (globaltimer_ns() - d0 < 200000ull) {
+                        }
+                    }
+                }
+            }
+        } else if (warp == MMA_WARP) {
+            if (lane == 0 && lead) {
+                auto wait = [&](uint64_t *bar, uint32_t parity) {
+                    return PAIR ? mbar_wait_cluster(smem_u32(bar), parity, wait_ns)
+                                : mbar_wait(smem_u32(bar), parity, wait_ns);
+                };
+                auto commit = [&](uint64_t *bar) {
+                    if constexpr (PAIR) tc2_commit_both(smem_u32(bar));
+                    else tc_commit(smem_u32(bar));
+                };
+                bool ok = true, issued = false;
+                uint32_t g = 0, gc = 0;
+                for (int u = worker; u < units && ok; u += workers) {
+                    int tn, tm, s0, s1;
+                    plan_unit(plan, u, tn, tm, s0, s1);
+                    for (int c0 = s0; c0 < s1 && ok; c0 += CHUNK, ++gc) {
+                        const int b = (int)(gc % C::DB);
+                        if (gc >= (uint32_t)C::DB && !wait(&dempty[b], (gc / C::DB - 1) & 1)) {
+                            ok = false;
+                            break;
+                        }
+                        tc_fence_after();
+                        const uint32_t d = tmem + (uint32_t)(b * NT);
+                        const int c1 = min(c0 + CHUNK, s1);
+                        for (int k = c0; k < c1; ++k, ++g) {
+                            const int s = (int)(g % ST);
+                            const uint32_t par = (g / ST) & 1;
+                            if (!wait(&xfull[s], par) || !wait(&afull[s], par)) {
+                                ok = false;
+                                break;
+                            }
+                            tc_fence_after();
+                            const uint32_t a = tmem + C::A_COL + (uint32_t)(s * (KT / 2));
+                            const uint32_t xb = smem_u32(xring + (size_t)s * C::X_STAGE);
+    #pragma unroll
+                            for (int kk = 0; kk < KT / 16; ++kk)
+                                mma_ts<PAIR>(d, a + kk * 8, smem_desc<128>(xb + kk * 32), C::IDESC,
+                                             (k != c0 || kk != 0) ? 1u : 0u);
+                            issued = true;
+                            commit(&empty[s]);
+                        }
+                        if (ok) commit(&dfull[b]);
+                    }
+                }
+                if (!ok) {
+                    record_error(err, kErrWaitTimeout);
+                    if (issued) {
+                        if constexpr (PAIR)
+                            asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(
+                                             smem_u32(drainbar)) : "memory");
+                        else
+                            tc_commit(smem_u32(drainbar));
+                        mbar_wait(smem_u32(drainbar), 0, DRAIN_NS);
+                    }
+                }
+            }
+        }
     }
 
     tc_fence_before();
@@ -668,7 +688,7 @@ Layout layout(const Q8LinearArgs &a, const Choice &c, bool copy_w) {
     l.x = at; at += round256((size_t)a.M * l.ldh * 2);
     l.w = at; at += copy_w ? round256((size_t)a.N * l.ldw) : 0;
     l.part = at; at += c.plan.ks > 1 ? round256((size_t)c.plan.units() * c.nt * 128 * 4) : 0;
-    l.ncounters = c.plan.ks > 1 ? c.plan.nt * c.plan.mt * CONV_WARPS : 0;
+    l.ncounters = c.plan.ks > 1 ? c.plan.nt * c.plan.mt * EPI_WARPS : 0;
     l.counters = at; at += round256((size_t)l.ncounters * 4);
     l.total = at;
     return l;
@@ -683,6 +703,12 @@ cudaError_t launch_c(const Q8LinearArgs &a, const Choice &c, const Layout &l, un
     auto kern = q8_mma_kernel<C, OutT>;
     const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)C::SMEM);
     if (e != cudaSuccess) return e;
+    // the warpgroups' register shares need the launch to bring REGS per thread
+    static const bool regs_ok = [kern] {
+        cudaFuncAttributes at;
+        return cudaFuncGetAttributes(&at, kern) == cudaSuccess && at.numRegs >= REGS;
+    }();
+    if (!regs_ok) return cudaErrorInvalidConfiguration;
     const unsigned grid = (unsigned)(C::PAIR ? 2 * c.workers : c.workers);
     return launch_with(kern, grid, THREADS, C::SMEM, C::PAIR ? 2 : 1, a.stream, tW, tX, (int)a.M, (int)a.N, c.plan,
                        a.xs, a.ws, Epilogue{1.0f, 0.0f, a.bias, a.act}, (OutT *)a.C, a.ldc,
