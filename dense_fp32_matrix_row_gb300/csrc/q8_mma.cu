@@ -13,21 +13,28 @@
 // are rows of W (output channels), its columns are tokens, so a few tokens
 // waste nothing and C's rows are stored 32 channels at a time.
 //
-//   W   travels and rests in 8 bits.  TMA brings 64 k of 128 rows into a
-//       shared-memory ring; four converter warps read a row per thread, expand
+//   W   travels and rests in 8 bits.  TMA brings 128 k of 128 rows into a
+//       shared-memory ring; eight converter warps, four to a stage, read a row per thread, expand
 //       it to FP16 in registers and store it to tensor memory, from where the
 //       MMA takes its A operand.  The 16-bit form of W never touches shared
-//       memory, whose bandwidth is what bounds such a kernel (8 KB written and
-//       read per stage and SM for W, where 16-bit tiles would move 16 and 16).
+//       memory, whose bandwidth is what bounds such a kernel (16 KB written and
+//       read per stage and SM for W, where 16-bit tiles would move 32 and 32).
 //   X   is expanded to FP16 once, by a kernel before (2 bytes of L2 traffic per
-//       element), and comes in by TMA as the B operand, 64 k per stage.
-//   MMA one thread issues four tcgen05.mma kind::f16 per stage.
+//       element), and comes in by TMA as the B operand, 128 k per stage.
+//   MMA one thread issues eight tcgen05.mma kind::f16 per stage.
 //   Eight more warps empty the accumulator, add the chunks and store.  The
 //       warpgroups trade registers (setmaxnreg), so that each of these threads
 //       can hold its 128 sums.
 //
 // PAIR: two SMs share a tile of 256 W rows x NT tokens (cta_group::2), each
 // with its own 128 rows of W and half of the tokens' X.
+//
+// Emptying an accumulator must not stop the MMAs.  Up to 128 tokens there are
+// two accumulators, used in turn.  At 256 tokens one fills tensor memory
+// beside the A stages; it is used as two halves of 128 columns, and the MMAs
+// of two stages at a time are issued for one half, then for the other, so
+// that a half is emptied while the other is computed (8192 x 14336 x 4096:
+// 600 us when each chunk stopped for the whole accumulator).
 //
 // When the tiles do not fill the GPU, K is divided into `ks` parts per tile;
 // the parts' sums go to the workspace and the last warp to arrive adds them in
@@ -38,24 +45,25 @@
 
 #include <atomic>
 
-#include "q8.cuh"
+#include "q8_stream.cuh"
 #include "tcgen05.cuh"
 
 namespace sgemm_gb300 {
 namespace {
 
-// Warpgroups: two that empty the accumulator, one of converters, and one whose
-// first two warps are the producer and the MMA issuer.
-constexpr int EPI_WARPS = 8, CONV_WARPS = 4;
-constexpr int PRODUCER_WARP = EPI_WARPS + CONV_WARPS, MMA_WARP = PRODUCER_WARP + 1;
+// Warpgroups: two that empty the accumulator, two of converters (stages of
+// either parity), and one whose first three warps load W, issue the MMAs and
+// load X.
+constexpr int EPI_WARPS = 8, CONV_WARPS = 8;
+constexpr int W_WARP = EPI_WARPS + CONV_WARPS, MMA_WARP = W_WARP + 1, X_WARP = W_WARP + 2;
 constexpr int THREADS = (EPI_WARPS + CONV_WARPS + 4) * 32;
 // Registers per thread: at launch, and what each warpgroup takes.  The shares
 // have to add up to no more than the launch's, or setmaxnreg.inc would wait.
-constexpr int REGS = 128, EPI_REGS = 176, CONV_REGS = 96, OTHER_REGS = 64;
+constexpr int REGS = 96, EPI_REGS = 152, CONV_REGS = 64, OTHER_REGS = 48;
 static_assert(EPI_REGS * EPI_WARPS + CONV_REGS * CONV_WARPS + OTHER_REGS * 4 <= REGS * (THREADS / 32),
               "register shares");
-constexpr int KT = 64;                        // k per stage
-constexpr int CHUNK = 16;                     // stages per accumulation chunk: 1024 k
+constexpr int KT = 128;                       // k per stage
+constexpr int CHUNK = 8;                      // stages per accumulation chunk: 1024 k
 constexpr uint32_t W_STAGE = 128 * KT;        // bytes
 constexpr uint64_t DRAIN_NS = 1000000000ull;
 
@@ -65,18 +73,22 @@ struct Cfg {
     static constexpr bool PAIR = PAIR_;
     static constexpr int NL = PAIR ? NT / 2 : NT;          // tokens staged by one SM
     static constexpr int ROWS = PAIR ? 256 : 128;          // W rows per tile
-    static constexpr int DB = NT <= 128 ? 2 : 1;           // accumulators
-    static constexpr int ST = 8;                           // X and A stages
-    static constexpr int WST = NT <= 64 ? 14 : 8;          // W stages
-    static constexpr uint32_t X_STAGE = NL * 128;          // bytes: 64 FP16 per token
+    static constexpr bool HALVES = NT == 256;              // one accumulator, emptied by halves
+    static constexpr int DB = HALVES ? 1 : 2;              // accumulators
+    static constexpr int NM = HALVES ? NT / 2 : NT;        // columns of an MMA
+    static constexpr int R = PAIR ? 2 : 1;                 // SMs per tile
+    static constexpr int ST = 4;                           // X and A stages
+    static constexpr int WST = NT <= 64 ? 8 : 4;           // W stages
+    static constexpr uint32_t X_HALF = NL * 128;           // bytes: 64 FP16 per token
+    static constexpr uint32_t X_STAGE = 2 * X_HALF;
     static constexpr uint32_t A_COL = DB * NT;             // tensor-memory column of A stage 0
     static constexpr int COLS = NT / 2;                    // columns per epilogue thread
     static constexpr size_t SMEM = 1024 + (size_t)ST * X_STAGE + (size_t)WST * W_STAGE + 512;
     // kind::f16, FP16 operands (format 0), FP32 accumulator, both K-major
-    static constexpr uint32_t IDESC = (1u << 4) | ((uint32_t)(NT >> 3) << 17) | ((uint32_t)(ROWS >> 4) << 24);
+    static constexpr uint32_t IDESC = (1u << 4) | ((uint32_t)(NM >> 3) << 17) | ((uint32_t)(ROWS >> 4) << 24);
     static_assert(A_COL + ST * (KT / 2) <= 512, "tensor memory");
     static_assert(SMEM <= 227 * 1024, "shared memory per block");
-    static_assert(X_STAGE % 1024 == 0 && W_STAGE % 1024 == 0, "stages keep 1024-byte alignment");
+    static_assert(X_HALF % 1024 == 0 && W_STAGE % 1024 == 0, "stages keep 1024-byte alignment");
     static_assert(COLS % 16 == 0, "the drain reads 16 columns at a time");
 };
 
@@ -148,22 +160,34 @@ __device__ __forceinline__ void arrive_relaxed(uint32_t bar, uint32_t cta) {
                  : "memory");
 }
 
-// Whether a phase has completed, without the pause that try_wait may take.
-__device__ __forceinline__ bool mbar_test(uint32_t bar, uint32_t parity) {
-    uint32_t ok;
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
-        "selp.u32 %0, 1, 0, p;\n\t}"
-        : "=r"(ok)
-        : "r"(bar), "r"(parity)
-        : "memory");
-    return ok != 0;
+// One stage of X: 128 k of NL tokens as two 64-wide halves, through a map whose
+// dimensions are (k % 64, token, k / 64).
+template <bool PAIR>
+__device__ __forceinline__ void tma_load_x(uint32_t dst, const CUtensorMap *map, uint32_t bar, int token, int k64) {
+    if constexpr (PAIR)
+        asm volatile(
+            "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes"
+            " [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(dst),
+            "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(0), "r"(token), "r"(k64)
+            : "memory");
+    else
+        asm volatile(
+            "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes"
+            " [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(dst),
+            "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(0), "r"(token), "r"(k64)
+            : "memory");
 }
 
 // The whole warp waits, and agrees on whether the phase completed.
 __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, uint64_t limit_ns) {
     return __all_sync(0xffffffffu, mbar_wait(bar, parity, limit_ns)) != 0;
+}
+
+// One lane of the converged warp, the same on every call.
+__device__ __forceinline__ bool elect_one() {
+    uint32_t p;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
+    return p != 0;
 }
 
 template <int N, bool UP>
@@ -205,16 +229,16 @@ q8_mma_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ C
     if (threadIdx.x == 0) {
         for (int s = 0; s < WST; ++s) {
             mbar_init(smem_u32(&wfull[s]), 1);
-            mbar_init(smem_u32(&wempty[s]), CONV_WARPS);
+            mbar_init(smem_u32(&wempty[s]), CONV_WARPS / 2);
         }
         for (int s = 0; s < ST; ++s) {
             mbar_init(smem_u32(&xfull[s]), 1);
-            mbar_init(smem_u32(&afull[s]), (PAIR ? 2 : 1) * CONV_WARPS);
+            mbar_init(smem_u32(&afull[s]), C::R * CONV_WARPS / 2);
             mbar_init(smem_u32(&empty[s]), 1);
         }
         for (int b = 0; b < 2; ++b) {
             mbar_init(smem_u32(&dfull[b]), 1);
-            mbar_init(smem_u32(&dempty[b]), (PAIR ? 2 : 1) * EPI_WARPS);
+            mbar_init(smem_u32(&dempty[b]), C::R * EPI_WARPS / (C::HALVES ? 2 : 1));
         }
         mbar_init(smem_u32(drainbar), 1);
         mbar_fence_init();
@@ -253,13 +277,13 @@ q8_mma_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ C
 #pragma unroll
             for (int j = 0; j < COLS; ++j) acc[j] = 0.0f;
             for (int c0 = s0; c0 < s1; c0 += CHUNK, ++gc) {
-                const int b = (int)(gc % C::DB);
+                const int b = C::HALVES ? half : (int)(gc % C::DB);
                 if (!warp_wait(smem_u32(&dfull[b]), (gc / C::DB) & 1, wait_ns)) {
                     ok = false;
                     break;
                 }
                 tc_fence_after();
-                const uint32_t d = lane_addr + (uint32_t)(b * NT + half * COLS);
+                const uint32_t d = lane_addr + (uint32_t)((C::HALVES ? 0 : b * NT) + half * COLS);
 #pragma unroll
                 for (int piece = 0; piece < COLS / 16; ++piece) {
                     float v[16];
@@ -277,16 +301,16 @@ q8_mma_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ C
             }
             if (!ok) break;
             pdl_wait();   // returns at once: X's stages could not have come before
-            if (!PAIR && plan.ks > 1) {
+            if (NT <= 128 && plan.ks > 1) {
                 // this unit's sums to the workspace; the last part's warp adds them all
                 const int tile = u / plan.ks, own = u - tile * plan.ks;
-                float *slot = part + ((int64_t)u * NT + half * COLS) * 128 + row;
+                float *slot = part + (((int64_t)u * C::R + rank) * NT + half * COLS) * 128 + row;
 #pragma unroll
                 for (int j = 0; j < COLS; ++j) __stcg(slot + j * 128, acc[j]);
                 __threadfence();
                 __syncwarp();
                 uint32_t arrived = 0;
-                if (lane == 0) arrived = atomicAdd(counters + tile * EPI_WARPS + warp, 1u);
+                if (lane == 0) arrived = atomicAdd(counters + (tile * C::R + (int)rank) * EPI_WARPS + warp, 1u);
                 arrived = __shfl_sync(0xffffffffu, arrived, 0);
                 if (arrived != (uint32_t)(plan.ks - 1)) continue;
                 __threadfence();
@@ -294,76 +318,77 @@ q8_mma_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ C
 #pragma unroll
                 for (int j = 0; j < COLS; ++j) sum[j] = 0.0f;
                 for (int p = 0; p < plan.ks; ++p) {
-                    const float *o = slot + (int64_t)(p - own) * NT * 128;
+                    const float *o = slot + (int64_t)(p - own) * C::R * NT * 128;
 #pragma unroll
                     for (int j = 0; j < COLS; ++j) sum[j] += __ldcg(o + j * 128);
                 }
 #pragma unroll
                 for (int j = 0; j < COLS; ++j) acc[j] = sum[j];
             }
-            // Column j of the accumulator is token m0 + j, this thread channel n:
-            // a warp stores 32 channels of one token at a time.
+            // Column j of this thread's sums is token m0 + at(j), the thread channel
+            // n: a warp stores 32 channels of one token at a time.  (A half of the
+            // accumulator holds 64 tokens of each SM's 128.)
+            constexpr auto at = [](int j) { return C::HALVES ? j + (j >= 64 ? 64 : 0) : j; };
             const int n = tn * C::ROWS + 128 * (int)rank + row;
-            const int m0 = tm * NT + half * COLS;
+            const int m0 = tm * NT + half * (C::HALVES ? 64 : COLS);
             const float wsn = __ldg(ws + min(n, N - 1));
             const float bias = ep.bias != nullptr ? __ldg(ep.bias + min(n, N - 1)) : 0.0f;
-            float xv[(COLS + 31) / 32];       // lane l holds the scale of token 32 i + l
+            float xv[(COLS + 31) / 32];       // lane l holds the scale of column 32 i + l
 #pragma unroll
-            for (int i = 0; i < (COLS + 31) / 32; ++i) xv[i] = __ldg(xs + min(m0 + 32 * i + lane, M - 1));
-            OutT *o = out + (int64_t)m0 * ldc + n;
-            auto store = [&](auto act) {
+            for (int i = 0; i < (COLS + 31) / 32; ++i) xv[i] = __ldg(xs + min(m0 + at(32 * i) + lane, M - 1));
+            // In place first, then the stores: next to the sums there are few
+            // registers, and one pass over both ran one dependent chain per column
+            // (110 cycles each, longer than a chunk's MMAs).
+            auto finish = [&](auto act) {
 #pragma unroll
-                for (int j = 0; j < COLS; ++j) {
-                    const float x = __shfl_sync(0xffffffffu, xv[j / 32], j % 32);
-                    if (n < N && m0 + j < M)
-                        o[(int64_t)j * ldc] = from_f32<OutT>(act(acc[j] * x * wsn + bias));
-                }
+                for (int j = 0; j < COLS; ++j)
+                    acc[j] = act(fmaf(acc[j] * __shfl_sync(0xffffffffu, xv[j / 32], j % 32), wsn, bias));
             };
             switch (ep.act) {
-                case kActRelu: store([](float v) { return activate<kActRelu>(v); }); break;
-                case kActGelu: store([](float v) { return activate<kActGelu>(v); }); break;
-                case kActSilu: store([](float v) { return activate<kActSilu>(v); }); break;
-                default: store([](float v) { return v; });
+                case kActRelu: finish([](float v) { return activate<kActRelu>(v); }); break;
+                case kActGelu: finish([](float v) { return activate<kActGelu>(v); }); break;
+                case kActSilu: finish([](float v) { return activate<kActSilu>(v); }); break;
+                default: finish([](float v) { return v; });
+            }
+            OutT *o = out + (int64_t)m0 * ldc + n;
+            if (n - lane + 32 <= N && m0 + at(COLS - 1) < M) {
+#pragma unroll
+                for (int j = 0; j < COLS; ++j) {
+                    *o = from_f32<OutT>(acc[j]);
+                    if (j + 1 < COLS) o += ldc * (at(j + 1) - at(j));
+                }
+            } else {
+#pragma unroll
+                for (int j = 0; j < COLS; ++j)
+                    if (n < N && m0 + at(j) < M) o[(int64_t)at(j) * ldc] = from_f32<OutT>(acc[j]);
             }
         }
         if (!ok && lane == 0) record_error(err, kErrWaitTimeout);
-    } else if (warp < PRODUCER_WARP) {
-        // Converter warp w: W rows (tensor-memory lanes) 32 * (w % 4) .. + 31,
-        // every stage.  The next stage's bytes are read before this one's are
-        // handed over.
+    } else if (warp < W_WARP) {
+        // Converter warp w: W rows (tensor-memory lanes) 32 * (w % 4) .. + 31 of
+        // the stages of parity (w / 4) % 2.
         set_registers<CONV_REGS, false>();
         const int lane_base = (warp & 3) * 32;
         const int row = lane_base + lane;
         const uint32_t a_addr = tmem + ((uint32_t)lane_base << 16) + C::A_COL;
-        const uint32_t swz = (uint32_t)((row >> 1) & 3);   // the 64-byte swizzle of this row
+        const uint32_t swz = (uint32_t)(row & 7);   // the 128-byte swizzle of this row
         uint32_t total = 0;
         for (int u = worker; u < units; u += workers) {
             int tn, tm, s0, s1;
             plan_unit(plan, u, tn, tm, s0, s1);
             total += (uint32_t)(s1 - s0);
         }
-        uint4 q[4];
-        auto fetch = [&](uint32_t g) {
-            const int w = (int)(g % WST);
-            if (!warp_wait(smem_u32(&wfull[w]), (g / WST) & 1, wait_ns)) return false;
-            const uint32_t src = smem_u32(wring + (size_t)w * W_STAGE) + (uint32_t)row * 64;
+        bool ok = true;
+        for (uint32_t g = (uint32_t)(warp >> 2) & 1; g < total; g += 2) {
+            const int w = (int)(g % WST), s = (int)(g % ST);
+            if (!warp_wait(smem_u32(&wfull[w]), (g / WST) & 1, wait_ns)) {
+                ok = false;
+                break;
+            }
+            const uint32_t src = smem_u32(wring + (size_t)w * W_STAGE) + (uint32_t)row * 128;
+            uint4 q[4];
 #pragma unroll
             for (int c = 0; c < 4; ++c) q[c] = lds128(src + (((uint32_t)c ^ swz) << 4));
-            return true;
-        };
-        bool ok = total == 0 || fetch(0);
-        for (uint32_t g = 0; g < total && ok; ++g) {
-            const int s = (int)(g % ST);
-            uint32_t r[32];
-#pragma unroll
-            for (int c = 0; c < 4; ++c) {
-                q8_to_f16(q[c].x, r[8 * c], r[8 * c + 1]);
-                q8_to_f16(q[c].y, r[8 * c + 2], r[8 * c + 3]);
-                q8_to_f16(q[c].z, r[8 * c + 4], r[8 * c + 5]);
-                q8_to_f16(q[c].w, r[8 * c + 6], r[8 * c + 7]);
-            }
-            __syncwarp();
-            if (lane == 0) mbar_arrive(smem_u32(&wempty[g % WST]));
             if (g >= (uint32_t)ST) {
                 if (!warp_wait(smem_u32(&empty[s]), (g / ST - 1) & 1, wait_ns)) {
                     ok = false;
@@ -371,8 +396,24 @@ q8_mma_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ C
                 }
                 tc_fence_after();
             }
-            tc_st32(a_addr + (uint32_t)(s * (KT / 2)), r);
-            if (g + 1 < total) ok = fetch(g + 1);
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {      // 64 k at a time
+                uint32_t r[32];
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                    q8_to_f16(q[c].x, r[8 * c], r[8 * c + 1]);
+                    q8_to_f16(q[c].y, r[8 * c + 2], r[8 * c + 3]);
+                    q8_to_f16(q[c].z, r[8 * c + 4], r[8 * c + 5]);
+                    q8_to_f16(q[c].w, r[8 * c + 6], r[8 * c + 7]);
+                }
+                if (h == 0) {
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) q[c] = lds128(src + (((uint32_t)(c + 4) ^ swz) << 4));
+                }
+                tc_st32(a_addr + (uint32_t)(s * (KT / 2) + 32 * h), r);
+            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(smem_u32(&wempty[w]));
             tc_st_wait();
             tc_fence_before();
             __syncwarp();
@@ -384,153 +425,154 @@ q8_mma_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ C
         if (!ok && lane == 0) record_error(err, kErrWaitTimeout);
     } else {
         set_registers<OTHER_REGS, false>();
-        if (warp == PRODUCER_WARP) {
-            if (lane == 0) {
-                tma_prefetch_desc(&tmW);
-                tma_prefetch_desc(&tmX);
-                // Two rings filled by one thread: whichever has a free stage next.
-                // W may be read before the preceding kernel (the expansion of X)
-                // has finished: that kernel itself waited for all earlier work.
-                struct Cursor {
-                    int u, s, s1, row;
-                    uint32_t g;
-                    bool done;
-                };
-                auto open = [&](Cursor &c, bool w) {
-                    if (c.u >= units) {
-                        c.done = true;
-                        return;
+        if (warp == W_WARP || warp == X_WARP) {
+            // One warp fills each ring.  W may be read before the preceding
+            // kernel (the expansion of X) has finished: that kernel itself
+            // waited for all earlier work.
+            const bool is_w = warp == W_WARP;
+            const int depth = is_w ? WST : ST;
+            uint64_t *freed = is_w ? wempty : empty;
+            if (lane == 0) tma_prefetch_desc(is_w ? &tmW : &tmX);
+            if (!is_w) {
+                pdl_wait();
+                asm volatile("fence.proxy.async;" ::: "memory");
+            }
+            bool ok = true;
+            uint32_t g = 0;
+            for (int u = worker; u < units && ok; u += workers) {
+                int tn, tm, s0, s1;
+                plan_unit(plan, u, tn, tm, s0, s1);
+                for (int k = s0; k < s1; ++k, ++g) {
+                    const int s = (int)(g % (uint32_t)depth);
+                    if (g >= (uint32_t)depth &&
+                        !warp_wait(smem_u32(&freed[s]), (g / (uint32_t)depth - 1) & 1, wait_ns)) {
+                        ok = false;
+                        break;
                     }
-                    int tn, tm;
-                    plan_unit(plan, c.u, tn, tm, c.s, c.s1);
-                    c.row = w ? tn * C::ROWS + 128 * (int)rank : tm * NT + C::NL * (int)rank;
-                };
-                auto step = [&](Cursor &c, bool w) {
-                    ++c.g;
-                    if (++c.s == c.s1) {
-                        c.u += workers;
-                        open(c, w);
-                    }
-                };
-                Cursor w{worker, 0, 0, 0, 0u, false}, x{worker, 0, 0, 0, 0u, false};
-                open(w, true);
-                open(x, false);
-                bool ok = true, waited = false;
-                uint64_t t0 = 0;
-                int idle = 0;
-                while (!w.done || !x.done) {
-                    bool moved = false;
-                    if (!w.done) {
-                        const int s = (int)(w.g % WST);
-                        if (w.g < (uint32_t)WST || mbar_test(smem_u32(&wempty[s]), (w.g / WST - 1) & 1)) {
+                    if (elect_one()) {
+                        if (is_w) {
                             const uint32_t bar = smem_u32(&wfull[s]);
                             mbar_arrive_expect_tx(bar, W_STAGE);
-                            tma_load_2d(smem_u32(wring + (size_t)s * W_STAGE), &tmW, bar, w.s * KT, w.row);
-                            step(w, true);
-                            moved = true;
+                            tma_load_2d(smem_u32(wring + (size_t)s * W_STAGE), &tmW, bar, k * KT,
+                                        tn * C::ROWS + 128 * (int)rank);
+                        } else {
+                            const uint32_t bar = smem_u32(&xfull[s]);
+                            if (lead) mbar_arrive_expect_tx(bar, (PAIR ? 2 : 1) * C::X_STAGE);
+                            tma_load_x<PAIR>(smem_u32(xring + (size_t)s * C::X_STAGE), &tmX,
+                                             PAIR ? cluster_addr(bar, 0) : bar, tm * NT + C::NL * (int)rank, 2 * k);
                         }
                     }
-                    if (!x.done && (waited || !moved || w.g >= (uint32_t)WST)) {
-                        if (!waited) {
-                            pdl_wait();   // the expanded X is there from here on
-                            asm volatile("fence.proxy.async;" ::: "memory");
-                            waited = true;
-                        }
-                        const int s = (int)(x.g % ST);
-                        if (x.g < (uint32_t)ST || mbar_test(smem_u32(&empty[s]), (x.g / ST - 1) & 1)) {
-                            const uint32_t dst = smem_u32(xring + (size_t)s * C::X_STAGE);
-                            if constexpr (PAIR) {
-                                if (lead) mbar_arrive_expect_tx(smem_u32(&xfull[s]), 2 * C::X_STAGE);
-                                tma_load_2d_pair(dst, &tmX, cluster_addr(smem_u32(&xfull[s]), 0), x.s * KT, x.row);
-                            } else {
-                                mbar_arrive_expect_tx(smem_u32(&xfull[s]), C::X_STAGE);
-                                tma_load_2d(dst, &tmX, smem_u32(&xfull[s]), x.s * KT, x.row);
-                            }
-                            step(x, false);
-                            moved = true;
-                        }
-                    }
-                    if (moved) {
-                        idle = 0;
-                    } else if ((++idle & 255) == 0) {   // the clock is slow to read
-                        const uint64_t now = globaltimer_ns();
-                        if (idle == 256) t0 = now;
-                        else if (now - t0 > wait_ns) {
-                            ok = false;
-                            break;
-                        }
+                    __syncwarp();
+                }
+            }
+            if (!ok && lane == 0) {   // wait for the copies still in flight
+                record_error(err, kErrWaitTimeout);
+                if (is_w || lead) {
+                    for (uint32_t q = g > (uint32_t)depth ? g - (uint32_t)depth : 0; q < g; ++q)
+                        mbar_wait(smem_u32(&(is_w ? wfull : xfull)[q % (uint32_t)depth]), (q / (uint32_t)depth) & 1,
+                                  DRAIN_NS);
+                } else {
+                    // copies of the odd SM complete on the even SM's barriers,
+                    // possibly in phases it gave up on: give them time to land
+                    const uint64_t d0 = globaltimer_ns();
+                    while (globaltimer_ns() - d0 < 200000ull) {
                     }
                 }
-                if (!ok) {   // wait for the copies still in flight
-                    record_error(err, kErrWaitTimeout);
-                    for (uint32_t q = (w.g > (uint32_t)WST ? w.g - WST : 0); q < w.g; ++q)
-                        mbar_wait(smem_u32(&wfull[q % WST]), (q / WST) & 1, DRAIN_NS);
-                    if (lead) {
-                        for (uint32_t q = (x.g > (uint32_t)ST ? x.g - ST : 0); q < x.g; ++q)
-                            mbar_wait(smem_u32(&xfull[q % ST]), (q / ST) & 1, DRAIN_NS);
+            }
+        } else if (warp == MMA_WARP && lead) {
+            // The whole warp walks the stages and one elected lane issues: the
+            // operands then stay in uniform registers (23 cycles per MMA of 32
+            // tokens, against 54 from a loop that a single lane runs).
+            auto wait = [&](uint64_t *bar, uint32_t parity) {
+                const bool done = PAIR ? mbar_wait_cluster(smem_u32(bar), parity, wait_ns)
+                                       : mbar_wait(smem_u32(bar), parity, wait_ns);
+                return __all_sync(0xffffffffu, done) != 0;
+            };
+            auto commit = [&](uint64_t *bar) {
+                if constexpr (PAIR) tc2_commit_both(smem_u32(bar));
+                else tc_commit(smem_u32(bar));
+            };
+            const uint64_t xdesc = smem_desc<128>(smem_u32(xring));   // addresses count in 16 bytes
+            bool ok = true, issued = false;
+            uint32_t g = 0, gc = 0;
+            for (int u = worker; u < units && ok; u += workers) {
+                int tn, tm, s0, s1;
+                plan_unit(plan, u, tn, tm, s0, s1);
+                for (int c0 = s0; c0 < s1 && ok; c0 += CHUNK, ++gc) {
+                    const int c1 = min(c0 + CHUNK, s1);
+                    // the accumulator (or half) b is free for this chunk
+                    auto acquire = [&](int b) {
+                        if (gc >= (uint32_t)C::DB && !wait(&dempty[b], (gc / C::DB - 1) & 1)) ok = false;
+                        tc_fence_after();
+                        return ok;
+                    };
+                    auto staged = [&](uint32_t at) {   // X and A of stage `at` are there
+                        const uint32_t par = (at / ST) & 1;
+                        if (!wait(&xfull[at % ST], par) || !wait(&afull[at % ST], par)) ok = false;
+                        tc_fence_after();
+                        return ok;
+                    };
+                    // the eight MMAs of stage `at` into the accumulator columns at d
+                    auto issue = [&](uint32_t d, uint32_t at, uint32_t rows, bool first) {
+                        const uint32_t s = at % ST;
+                        const uint32_t a = tmem + C::A_COL + s * (KT / 2);
+                        const uint64_t x = xdesc + (uint64_t)(s * (C::X_STAGE >> 4) + rows * 8);
+#pragma unroll
+                        for (int kk = 0; kk < KT / 16; ++kk)
+                            mma_ts<PAIR>(d, a + kk * 8, x + (kk >> 2) * (C::X_HALF >> 4) + (kk & 3) * 2, C::IDESC,
+                                         (!first || kk != 0) ? 1u : 0u);
+                    };
+                    if constexpr (C::HALVES) {
+                        for (int k = c0; k < c1; k += 2) {
+                            const int two = min(2, c1 - k);
+                            if (!staged(g) || (two > 1 && !staged(g + 1))) break;
+#pragma unroll
+                            for (int h = 0; h < 2; ++h) {
+                                if (k == c0 && !acquire(h)) break;
+                                if (elect_one()) {
+                                    issue(tmem + (uint32_t)(h * C::NM), g, (uint32_t)h * 64, k == c0);
+                                    if (h == 1) commit(&empty[g % ST]);
+                                    if (two > 1) {
+                                        issue(tmem + (uint32_t)(h * C::NM), g + 1, (uint32_t)h * 64, false);
+                                        if (h == 1) commit(&empty[(g + 1) % ST]);
+                                    }
+                                    if (k + 2 >= c1) commit(&dfull[h]);
+                                }
+                                __syncwarp();
+                                issued = true;
+                            }
+                            if (!ok) break;
+                            g += (uint32_t)two;
+                        }
                     } else {
-                        // copies of the odd SM complete on the even SM's barriers,
-                        // possibly in phases it gave up on: give them time to land
-                        const uint64_t d0 = globaltimer_ns();
-                        while (globaltimer_ns() - d0 < 200000ull) {
+                        const int b = (int)(gc % C::DB);
+                        if (!acquire(b)) break;
+                        for (int k = c0; k < c1; ++k, ++g) {
+                            if (!staged(g)) break;
+                            if (elect_one()) {
+                                issue(tmem + (uint32_t)(b * NT), g, 0u, k == c0);
+                                commit(&empty[g % ST]);
+                                if (k + 1 == c1) commit(&dfull[b]);
+                            }
+                            __syncwarp();
+                            issued = true;
                         }
                     }
                 }
             }
-        } else if (warp == MMA_WARP) {
-            if (lane == 0 && lead) {
-                auto wait = [&](uint64_t *bar, uint32_t parity) {
-                    return PAIR ? mbar_wait_cluster(smem_u32(bar), parity, wait_ns)
-                                : mbar_wait(smem_u32(bar), parity, wait_ns);
-                };
-                auto commit = [&](uint64_t *bar) {
-                    if constexpr (PAIR) tc2_commit_both(smem_u32(bar));
-                    else tc_commit(smem_u32(bar));
-                };
-                bool ok = true, issued = false;
-                uint32_t g = 0, gc = 0;
-                for (int u = worker; u < units && ok; u += workers) {
-                    int tn, tm, s0, s1;
-                    plan_unit(plan, u, tn, tm, s0, s1);
-                    for (int c0 = s0; c0 < s1 && ok; c0 += CHUNK, ++gc) {
-                        const int b = (int)(gc % C::DB);
-                        if (gc >= (uint32_t)C::DB && !wait(&dempty[b], (gc / C::DB - 1) & 1)) {
-                            ok = false;
-                            break;
-                        }
-                        tc_fence_after();
-                        const uint32_t d = tmem + (uint32_t)(b * NT);
-                        const int c1 = min(c0 + CHUNK, s1);
-                        for (int k = c0; k < c1; ++k, ++g) {
-                            const int s = (int)(g % ST);
-                            const uint32_t par = (g / ST) & 1;
-                            if (!wait(&xfull[s], par) || !wait(&afull[s], par)) {
-                                ok = false;
-                                break;
-                            }
-                            tc_fence_after();
-                            const uint32_t a = tmem + C::A_COL + (uint32_t)(s * (KT / 2));
-                            const uint32_t xb = smem_u32(xring + (size_t)s * C::X_STAGE);
-    #pragma unroll
-                            for (int kk = 0; kk < KT / 16; ++kk)
-                                mma_ts<PAIR>(d, a + kk * 8, smem_desc<128>(xb + kk * 32), C::IDESC,
-                                             (k != c0 || kk != 0) ? 1u : 0u);
-                            issued = true;
-                            commit(&empty[s]);
-                        }
-                        if (ok) commit(&dfull[b]);
-                    }
-                }
-                if (!ok) {
-                    record_error(err, kErrWaitTimeout);
-                    if (issued) {
+            if (!ok) {
+                if (lane == 0) record_error(err, kErrWaitTimeout);
+                if (issued) {
+                    if (elect_one()) {
                         if constexpr (PAIR)
-                            asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(
-                                             smem_u32(drainbar)) : "memory");
+                            asm volatile(
+                                "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(
+                                    smem_u32(drainbar)) : "memory");
                         else
                             tc_commit(smem_u32(drainbar));
-                        mbar_wait(smem_u32(drainbar), 0, DRAIN_NS);
                     }
+                    __syncwarp();
+                    mbar_wait(smem_u32(drainbar), 0, DRAIN_NS);
                 }
             }
         }
@@ -549,7 +591,7 @@ q8_mma_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ C
     }
 }
 
-// X (any alignment and stride) as FP16 [M][ldh], ldh a multiple of 16, zeros
+// X (any alignment and stride) as FP16 [M][ldh], ldh a multiple of 64, zeros
 // past K; also clears `nzero` words.
 __global__ void __launch_bounds__(256)
 q8_expand_kernel(int M, int K, const int8_t *__restrict__ X, int64_t ldx, int vec, uint16_t *__restrict__ H,
@@ -562,15 +604,11 @@ q8_expand_kernel(int M, int K, const int8_t *__restrict__ X, int64_t ldx, int ve
     for (int64_t i = i0; i < total; i += stride) {
         const int64_t m = i / per_row, k = (i - m * per_row) * 16;
         const int8_t *p = X + m * ldx + k;
-        uint32_t w[4] = {0u, 0u, 0u, 0u};
-        if (vec && k + 16 <= K) {
-            const uint4 v = *reinterpret_cast<const uint4 *>(p);
-            w[0] = v.x; w[1] = v.y; w[2] = v.z; w[3] = v.w;
-        } else {
-#pragma unroll
-            for (int j = 0; j < 16; ++j)
-                if (k + j < K) w[j >> 2] |= (uint32_t)(uint8_t)p[j] << (8 * (j & 3));
-        }
+        uint4 v;
+        if (k + 16 > K) v = load16_bytes(p, (int)max((int64_t)0, K - k));
+        else if (vec) v = *reinterpret_cast<const uint4 *>(p);
+        else v = load16_unaligned(p, X, X + (int64_t)(M - 1) * ldx + K);
+        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
         uint32_t r[8];
 #pragma unroll
         for (int j = 0; j < 4; ++j) q8_to_f16(w[j], r[2 * j], r[2 * j + 1]);
@@ -590,11 +628,8 @@ q8_align_kernel(int N, int K, const int8_t *__restrict__ W, int64_t ldw, int8_t 
     for (int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; i < total; i += (int64_t)gridDim.x * blockDim.x) {
         const int64_t n = i / per_row, k = (i - n * per_row) * 16;
         const int8_t *p = W + n * ldw + k;
-        uint32_t w[4] = {0u, 0u, 0u, 0u};
-#pragma unroll
-        for (int j = 0; j < 16; ++j)
-            if (k + j < K) w[j >> 2] |= (uint32_t)(uint8_t)p[j] << (8 * (j & 3));
-        *reinterpret_cast<uint4 *>(O + n * ldo + k) = make_uint4(w[0], w[1], w[2], w[3]);
+        *reinterpret_cast<uint4 *>(O + n * ldo + k) =
+            k + 16 > K ? load16_bytes(p, (int)(K - k)) : load16_unaligned(p, W, W + (int64_t)(N - 1) * ldw + K);
     }
 }
 
@@ -606,7 +641,20 @@ bool encode_bytes(EncodeTiledFn enc, CUtensorMap *map, const int8_t *base, int64
     const cuuint32_t box[2] = {box_inner, box_rows};
     const cuuint32_t estr[2] = {1, 1};
     return enc(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<int8_t *>(base), dims, strides, box, estr,
-               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_64B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// X expanded, FP16 [rows][ld] (ld a multiple of 64), in boxes of 128 k of
+// `box_rows` tokens.
+bool encode_x(EncodeTiledFn enc, CUtensorMap *map, void *base, int64_t ld, int64_t rows, uint32_t box_rows) {
+    if (enc == nullptr) return false;
+    const cuuint64_t dims[3] = {64, (cuuint64_t)rows, (cuuint64_t)(ld / 64)};
+    const cuuint64_t strides[2] = {(cuuint64_t)ld * 2, 128};
+    const cuuint32_t box[3] = {64, box_rows, 2};
+    const cuuint32_t estr[3] = {1, 1, 1};
+    return enc(map, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3, base, dims, strides, box, estr,
+               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
@@ -635,7 +683,7 @@ constexpr size_t round256(size_t v) { return (v + 255) / 256 * 256; }
 
 // Which tile a product runs on, and its division.
 struct Choice {
-    int nt;          // tokens per tile: 32, 64, 128, or 256 (pair)
+    int nt;          // tokens per tile: 32 (one SM), 64, 128 or 256 (a pair of SMs)
     Plan plan;
     int workers;     // CTAs, or pairs of them
 };
@@ -643,10 +691,10 @@ struct Choice {
 Choice choose(int64_t M, int64_t N, int64_t K, int sms) {
     Choice c{};
     const int stages = (int)((K + KT - 1) / KT);
-    c.nt = M <= 32 ? 32 : M <= 64 ? 64 : 128;
     const int64_t pair_tiles = ((N + 255) / 256) * ((M + 255) / 256);
-    if (M > 128 && pair_tiles >= sms / 4) c.nt = 256;
-    const int rows = c.nt == 256 ? 256 : 128;
+    c.nt = M <= 32 ? 32 : M <= 64 ? 64 : M <= 128 || pair_tiles < sms / 4 ? 128 : 256;
+    const int rows = c.nt == 32 ? 128 : 256;
+    const int workers = c.nt == 32 ? sms : sms / 2;
     Plan &p = c.plan;
     p.nt = (int)((N + rows - 1) / rows);
     p.mt = (int)((M + c.nt - 1) / c.nt);
@@ -659,8 +707,8 @@ Choice choose(int64_t M, int64_t N, int64_t K, int sms) {
         int64_t best = INT64_MAX;
         for (int ks = 1; ks <= 16 && ks <= stages; ++ks) {
             const int64_t per = (stages + ks - 1) / ks;
-            const int64_t rounds = (tiles * ks + sms - 1) / sms;
-            const int64_t cost = rounds * (per + 2) + (ks > 1 ? 6 : 0);
+            const int64_t rounds = (tiles * ks + workers - 1) / workers;
+            const int64_t cost = rounds * (per + (ks > 1 ? 10 : 2));
             if (cost < best) {
                 best = cost;
                 p.ks = ks;
@@ -669,8 +717,7 @@ Choice choose(int64_t M, int64_t N, int64_t K, int sms) {
     }
     p.per = (stages + p.ks - 1) / p.ks;
     p.ks = (stages + p.per - 1) / p.per;
-    const int w = c.nt == 256 ? sms / 2 : sms;
-    c.workers = p.units() < w ? p.units() : w;
+    c.workers = p.units() < workers ? p.units() : workers;
     return c;
 }
 
@@ -682,13 +729,13 @@ struct Layout {
 
 Layout layout(const Q8LinearArgs &a, const Choice &c, bool copy_w) {
     Layout l{};
-    l.ldh = round16(a.K);
+    l.ldh = (a.K + 63) / 64 * 64;
     l.ldw = copy_w ? round16(a.K) : a.ldw;
     size_t at = 0;
     l.x = at; at += round256((size_t)a.M * l.ldh * 2);
     l.w = at; at += copy_w ? round256((size_t)a.N * l.ldw) : 0;
-    l.part = at; at += c.plan.ks > 1 ? round256((size_t)c.plan.units() * c.nt * 128 * 4) : 0;
-    l.ncounters = c.plan.ks > 1 ? c.plan.nt * c.plan.mt * EPI_WARPS : 0;
+    l.part = at; at += c.plan.ks > 1 ? round256((size_t)c.plan.units() * (c.nt == 32 ? 1 : 2) * c.nt * 128 * 4) : 0;
+    l.ncounters = c.plan.ks > 1 ? c.plan.nt * c.plan.mt * (c.nt == 32 ? 1 : 2) * EPI_WARPS : 0;
     l.counters = at; at += round256((size_t)l.ncounters * 4);
     l.total = at;
     return l;
@@ -698,7 +745,7 @@ template <typename C, typename OutT>
 cudaError_t launch_c(const Q8LinearArgs &a, const Choice &c, const Layout &l, unsigned char *ws, const int8_t *W) {
     alignas(64) CUtensorMap tW, tX;
     if (!encode_bytes(a.encode, &tW, W, a.K, a.N, l.ldw, KT, 128) ||
-        !encode_tma_2d_bf16(a.encode, &tX, ws + l.x, l.ldh, a.M, l.ldh, KT, C::NL, CU_TENSOR_MAP_SWIZZLE_128B))
+        !encode_x(a.encode, &tX, ws + l.x, l.ldh, a.M, C::NL))
         return cudaErrorInvalidValue;
     auto kern = q8_mma_kernel<C, OutT>;
     const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)C::SMEM);
@@ -720,8 +767,8 @@ template <typename OutT>
 cudaError_t launch_o(const Q8LinearArgs &a, const Choice &c, const Layout &l, unsigned char *ws, const int8_t *W) {
     switch (c.nt) {
         case 32: return launch_c<Cfg<32, false>, OutT>(a, c, l, ws, W);
-        case 64: return launch_c<Cfg<64, false>, OutT>(a, c, l, ws, W);
-        case 128: return launch_c<Cfg<128, false>, OutT>(a, c, l, ws, W);
+        case 64: return launch_c<Cfg<64, true>, OutT>(a, c, l, ws, W);
+        case 128: return launch_c<Cfg<128, true>, OutT>(a, c, l, ws, W);
         default: return launch_c<Cfg<256, true>, OutT>(a, c, l, ws, W);
     }
 }
