@@ -19,7 +19,7 @@
 //       MMA takes its A operand.  The 16-bit form of W never touches shared
 //       memory, whose bandwidth is what bounds such a kernel (16 KB written and
 //       read per stage and SM for W, where 16-bit tiles would move 32 and 32).
-//   X   is expanded to FP16 once, by a kernel before (2 bytes of L2 traffic per
+//   X   is expanded to FP16 once, by q8_prepare_kernel (2 bytes of L2 traffic per
 //       element), and comes in by TMA as the B operand, 128 k per stage.
 //   MMA one thread issues eight tcgen05.mma kind::f16 per stage.
 //   Eight more warps empty the accumulator, add the chunks and store.  The
@@ -43,7 +43,7 @@
 // Every wait is bounded; on a time-out the roles record it and wind down.
 #include <cuda_fp16.h>
 
-#include <atomic>
+#include <algorithm>
 
 #include "q8_stream.cuh"
 #include "tcgen05.cuh"
@@ -201,7 +201,7 @@ __global__ void __launch_bounds__(THREADS, 1)
 q8_mma_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmX, int M, int N,
               Plan plan, const float *__restrict__ xs, const float *__restrict__ ws, Epilogue ep,
               OutT *__restrict__ out, int64_t ldc, float *part, uint32_t *counters, unsigned *err,
-              uint64_t wait_ns) {
+              uint64_t wait_ns, int w_copied) {
     constexpr bool PAIR = C::PAIR;
     constexpr int ST = C::ST, WST = C::WST, NT = C::NT, COLS = C::COLS;
     extern __shared__ unsigned char smem_raw[];
@@ -426,14 +426,14 @@ q8_mma_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ C
     } else {
         set_registers<OTHER_REGS, false>();
         if (warp == W_WARP || warp == X_WARP) {
-            // One warp fills each ring.  W may be read before the preceding
-            // kernel (the expansion of X) has finished: that kernel itself
-            // waited for all earlier work.
+            // One warp fills each ring.  The caller's W may be read before the
+            // preceding kernel (q8_prepare_kernel) has finished: that kernel
+            // itself waited for all earlier work.
             const bool is_w = warp == W_WARP;
             const int depth = is_w ? WST : ST;
             uint64_t *freed = is_w ? wempty : empty;
             if (lane == 0) tma_prefetch_desc(is_w ? &tmW : &tmX);
-            if (!is_w) {
+            if (!is_w || w_copied) {
                 pdl_wait();
                 asm volatile("fence.proxy.async;" ::: "memory");
             }
@@ -591,18 +591,21 @@ q8_mma_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ C
     }
 }
 
-// X (any alignment and stride) as FP16 [M][ldh], ldh a multiple of 64, zeros
-// past K; also clears `nzero` words.
+// What has to be laid out before the product: X (any alignment and stride) as
+// FP16 [M][ldh], ldh a multiple of 64, zeros past K; rows of W that TMA cannot
+// address (O not NULL) as [N][ldo], ldo a multiple of 16, zeros past K; and
+// `nzero` counters cleared.
 __global__ void __launch_bounds__(256)
-q8_expand_kernel(int M, int K, const int8_t *__restrict__ X, int64_t ldx, int vec, uint16_t *__restrict__ H,
-                 int64_t ldh, uint32_t *zero, int nzero) {
+q8_prepare_kernel(int M, int N, int K, const int8_t *__restrict__ X, int64_t ldx, int vec, uint16_t *__restrict__ H,
+                  int64_t ldh, const int8_t *__restrict__ W, int64_t ldw, int8_t *__restrict__ O, int64_t ldo,
+                  uint32_t *zero, int nzero) {
     pdl_wait();
     pdl_trigger();
     const int64_t i0 = (int64_t)blockIdx.x * blockDim.x + threadIdx.x, stride = (int64_t)gridDim.x * blockDim.x;
     for (int64_t i = i0; i < nzero; i += stride) zero[i] = 0u;
-    const int64_t per_row = ldh / 16, total = per_row * M;
-    for (int64_t i = i0; i < total; i += stride) {
-        const int64_t m = i / per_row, k = (i - m * per_row) * 16;
+    const int64_t xrow = ldh / 16, xtotal = xrow * M;
+    for (int64_t i = i0; i < xtotal; i += stride) {
+        const int64_t m = i / xrow, k = (i - m * xrow) * 16;
         const int8_t *p = X + m * ldx + k;
         uint4 v;
         if (k + 16 > K) v = load16_bytes(p, (int)max((int64_t)0, K - k));
@@ -616,17 +619,10 @@ q8_expand_kernel(int M, int K, const int8_t *__restrict__ X, int64_t ldx, int ve
         o[0] = make_uint4(r[0], r[1], r[2], r[3]);
         o[1] = make_uint4(r[4], r[5], r[6], r[7]);
     }
-}
-
-// Rows of W at any alignment to 16-byte aligned rows (ldo a multiple of 16,
-// zeros past K).
-__global__ void __launch_bounds__(256)
-q8_align_kernel(int N, int K, const int8_t *__restrict__ W, int64_t ldw, int8_t *__restrict__ O, int64_t ldo) {
-    pdl_wait();
-    pdl_trigger();
-    const int64_t per_row = ldo / 16, total = per_row * N;
-    for (int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; i < total; i += (int64_t)gridDim.x * blockDim.x) {
-        const int64_t n = i / per_row, k = (i - n * per_row) * 16;
+    if (O == nullptr) return;
+    const int64_t wrow = ldo / 16, wtotal = wrow * N;
+    for (int64_t i = i0; i < wtotal; i += stride) {
+        const int64_t n = i / wrow, k = (i - n * wrow) * 16;
         const int8_t *p = W + n * ldw + k;
         *reinterpret_cast<uint4 *>(O + n * ldo + k) =
             k + 16 > K ? load16_bytes(p, (int)(K - k)) : load16_unaligned(p, W, W + (int64_t)(N - 1) * ldw + K);
@@ -760,7 +756,7 @@ cudaError_t launch_c(const Q8LinearArgs &a, const Choice &c, const Layout &l, un
     return launch_with(kern, grid, THREADS, C::SMEM, C::PAIR ? 2 : 1, a.stream, tW, tX, (int)a.M, (int)a.N, c.plan,
                        a.xs, a.ws, Epilogue{1.0f, 0.0f, a.bias, a.act}, (OutT *)a.C, a.ldc,
                        reinterpret_cast<float *>(ws + l.part), reinterpret_cast<uint32_t *>(ws + l.counters), a.err,
-                       a.wait_ns);
+                       a.wait_ns, W != a.W);
 }
 
 template <typename OutT>
@@ -799,18 +795,14 @@ cudaError_t launch_q8_mma(const Q8LinearArgs &a, void *workspace) {
     const bool copy_w = !w_aligned(a);
     const Choice c = choose(a.M, a.N, a.K, a.sm_count);
     const Layout l = layout(a, c, copy_w);
-    const int8_t *W = a.W;
-    if (copy_w) {
-        int8_t *o = reinterpret_cast<int8_t *>(ws + l.w);
-        const cudaError_t e = launch_with(q8_align_kernel, grid_for(a.N * (l.ldw / 16), a.sm_count), 256, 0, 1,
-                                          a.stream, (int)a.N, (int)a.K, a.W, a.ldw, o, l.ldw);
-        if (e != cudaSuccess) return e;
-        W = o;
-    }
+    int8_t *copy = copy_w ? reinterpret_cast<int8_t *>(ws + l.w) : nullptr;
+    const int8_t *W = copy_w ? copy : a.W;
     const int vec = reinterpret_cast<uintptr_t>(a.X) % 16 == 0 && a.ldx % 16 == 0;
-    const cudaError_t e = launch_with(q8_expand_kernel, grid_for(a.M * (l.ldh / 16), a.sm_count), 256, 0, 1, a.stream,
-                                      (int)a.M, (int)a.K, a.X, a.ldx, vec, reinterpret_cast<uint16_t *>(ws + l.x),
-                                      l.ldh, reinterpret_cast<uint32_t *>(ws + l.counters), l.ncounters);
+    const int64_t items = std::max(a.M * (l.ldh / 16), copy_w ? a.N * (l.ldw / 16) : 0);
+    const cudaError_t e = launch_with(q8_prepare_kernel, grid_for(items, a.sm_count), 256, 0, 1, a.stream, (int)a.M,
+                                      (int)a.N, (int)a.K, a.X, a.ldx, vec, reinterpret_cast<uint16_t *>(ws + l.x),
+                                      l.ldh, a.W, a.ldw, copy, l.ldw, reinterpret_cast<uint32_t *>(ws + l.counters),
+                                      l.ncounters);
     if (e != cudaSuccess) return e;
     return a.type == kTypeBf16 ? launch_o<__nv_bfloat16>(a, c, l, ws, W) : launch_o<float>(a, c, l, ws, W);
 }

@@ -40,75 +40,97 @@ def _entry(name):
     return f
 
 
-def _call(name, *args):
-    rc = _entry(name)(*args)
+def _launch(index, name, *args):
+    """Calls an entry point with the tensors' device current."""
+    f = _fn.get(name) or _entry(name)
+    if index < 0 or index == _current_device():
+        rc = f(*args)
+    else:
+        with torch.cuda.device(index):
+            rc = f(*args)
     if rc:
         from . import SgemmError
         raise SgemmError(rc, name)
 
 
-def _stream(stream, device):
+# torch's own accessors behind torch.cuda.current_stream and current_device,
+# without the objects those make (2 us a call); the public ones otherwise
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+_current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+
+
+def _stream(stream, index):
     if stream is None:
-        return torch.cuda.current_stream(device).cuda_stream if device.type == "cuda" else 0
+        if index < 0:
+            return 0
+        return _raw_stream(index) if _raw_stream else torch.cuda.current_stream(index).cuda_stream
     return stream if isinstance(stream, int) else stream.cuda_stream
 
 
-def _matrix(t, name, dtypes, shape, device):
-    """Checks a 2-D operand; its row stride."""
+def _matrix(t, name, dtypes, shape, index):
+    """Checks a 2-D operand on CUDA device `index` (-1: the output is not on
+    one) of this shape; its row stride."""
+    if (type(t) is torch.Tensor and t.dtype in dtypes and t.shape == shape and t.get_device() == index >= 0
+            and t.is_contiguous()):
+        return shape[1] or 1
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch tensor")
     if t.dtype not in dtypes:
         raise TypeError(f"{name} must be of type {' or '.join(str(d) for d in dtypes)}, not {t.dtype}")
-    if t.dim() != 2 or (shape is not None and tuple(t.shape) != shape):
-        raise ValueError(f"{name} must have shape {shape}, not {tuple(t.shape)}" if shape is not None
-                         else f"{name} must be 2-D")
+    if t.dim() != 2 or t.shape != shape:
+        raise ValueError(f"{name} must have shape {tuple(shape)}, not {tuple(t.shape)}")
     rows, cols = t.shape
     if t.numel() == 0:
         return max(cols, 1)
-    if t.device != device or device.type != "cuda":
+    if index < 0 or t.get_device() != index:
         raise TypeError(f"{name} must live on the same CUDA device as the output")
     if cols > 1 and t.stride(1) != 1:
         raise ValueError(f"{name} must be row-major with contiguous rows (stride(1) == 1)")
     return max(t.stride(0), cols) if rows == 1 else t.stride(0)
 
 
-def _packed(t, name, dtype, shape, device):
+def _packed(t, name, dtype, shape, index):
     """Checks a contiguous operand of exactly this type and shape."""
+    if (type(t) is torch.Tensor and t.dtype is dtype and t.shape == shape and t.get_device() == index >= 0
+            and t.is_contiguous()):
+        return
     if not isinstance(t, torch.Tensor) or t.dtype != dtype:
         raise TypeError(f"{name} must be a torch tensor of type {dtype}")
-    if tuple(t.shape) != shape:
-        raise ValueError(f"{name} must have shape {shape}, not {tuple(t.shape)}")
-    if t.numel() and (t.device != device or device.type != "cuda"):
+    if t.shape != shape:
+        raise ValueError(f"{name} must have shape {tuple(shape)}, not {tuple(t.shape)}")
+    if t.numel() and (index < 0 or t.get_device() != index):
         raise TypeError(f"{name} must live on the same CUDA device as the output")
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
 
 
-def _on(device):
-    """The library works on the current device."""
-    return torch.cuda.device(device)
+def _shape2(t, name):
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch tensor")
+    if t.dim() != 2:
+        raise ValueError(f"{name} must be 2-D")
+    return t.shape
+
+
+def _index(t, name):
+    """CUDA device of an output (-1: on none)."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch tensor")
+    return t.get_device()
 
 
 _FLOATS = (torch.float32, torch.bfloat16)
 _INT8 = (torch.int8,)
 
 
-def _launch(device, name, *args):
-    if device.type != "cuda" or device.index == torch.cuda.current_device():
-        _call(name, *args)
-    else:
-        with _on(device):
-            _call(name, *args)
-
-
 def quantize_q8(x, q, scale, stream=None) -> None:
     """Each row of ``x`` (M, K; float32 or bfloat16) as 8-bit whole numbers
     ``q`` (M, K; int8) and one ``scale`` (M; float32): x is about q * scale,
     scale = max|row| / 127.  Rows of ``x`` and ``q`` may be strided."""
-    dev = q.device
-    ldx = _matrix(x, "x", _FLOATS, None, dev)
-    M, K = x.shape
-    ldq = _matrix(q, "q", _INT8, (M, K), dev)
+    dev, shape = _index(q, "q"), _shape2(x, "x")
+    M, K = shape
+    ldx = _matrix(x, "x", _FLOATS, shape, dev)
+    ldq = _matrix(q, "q", _INT8, shape, dev)
     _packed(scale, "scale", torch.float32, (M,), dev)
     _launch(dev, "sgemm_q8_quantize", M, K, x.data_ptr(), ldx, _TYPES[x.dtype], q.data_ptr(), ldq,
             scale.data_ptr(), _stream(stream, dev))
@@ -122,20 +144,21 @@ def rmsnorm_q8(x, weight, q, scale, residual=None, h=None, y=None, eps: float = 
     ``x``, ``residual``, ``h`` and ``y`` are (M, K) of one type (float32 or
     bfloat16), ``weight`` K float32 values.  ``residual``, ``h`` and ``y`` may
     be left out; ``h`` may be ``x`` or ``residual`` itself."""
-    dev = q.device
-    ldx = _matrix(x, "x", _FLOATS, None, dev)
-    M, K = x.shape
-    ldq = _matrix(q, "q", _INT8, (M, K), dev)
+    dev, shape = _index(q, "q"), _shape2(x, "x")
+    M, K = shape
+    ldx = _matrix(x, "x", _FLOATS, shape, dev)
+    ldq = _matrix(q, "q", _INT8, shape, dev)
     _packed(weight, "weight", torch.float32, (K,), dev)
     _packed(scale, "scale", torch.float32, (M,), dev)
-    more = []
-    for t, name in ((residual, "residual"), (h, "h"), (y, "y")):
-        if t is None:
-            more.append((None, 0))
-        else:
-            ld = _matrix(t, name, (x.dtype,), (M, K), dev)
-            more.append((t.data_ptr(), ld))
-    (pr, ldr), (ph, ldh), (py, ldy) = more
+    pr = ph = py = None
+    ldr = ldh = ldy = 0
+    like = (x.dtype,)
+    if residual is not None:
+        ldr, pr = _matrix(residual, "residual", like, shape, dev), residual.data_ptr()
+    if h is not None:
+        ldh, ph = _matrix(h, "h", like, shape, dev), h.data_ptr()
+    if y is not None:
+        ldy, py = _matrix(y, "y", like, shape, dev), y.data_ptr()
     _launch(dev, "sgemm_q8_rmsnorm", M, K, x.data_ptr(), ldx, pr, ldr, _TYPES[x.dtype],
             weight.data_ptr(), eps, ph, ldh, py, ldy, q.data_ptr(), ldq, scale.data_ptr(),
             _stream(stream, dev))
@@ -150,13 +173,13 @@ def linear_q8(xq, xs, wq, ws, out, bias=None, activation: str = "none", stream=N
     act = ACTIVATIONS.get(activation)
     if act is None:
         raise ValueError(f"unknown activation {activation!r}; one of {sorted(ACTIVATIONS)}")
-    dev = out.device
-    ldx = _matrix(xq, "xq", _INT8, None, dev)
-    ldw = _matrix(wq, "wq", _INT8, None, dev)
-    M, K = xq.shape
-    N = wq.shape[0]
-    if wq.shape[1] != K:
-        raise ValueError(f"shape mismatch: xq {tuple(xq.shape)}, wq {tuple(wq.shape)}")
+    dev, xshape, wshape = _index(out, "out"), _shape2(xq, "xq"), _shape2(wq, "wq")
+    M, K = xshape
+    N = wshape[0]
+    if wshape[1] != K:
+        raise ValueError(f"shape mismatch: xq {tuple(xshape)}, wq {tuple(wshape)}")
+    ldx = _matrix(xq, "xq", _INT8, xshape, dev)
+    ldw = _matrix(wq, "wq", _INT8, wshape, dev)
     ldc = _matrix(out, "out", _FLOATS, (M, N), dev)
     _packed(xs, "xs", torch.float32, (M,), dev)
     _packed(ws, "ws", torch.float32, (N,), dev)
@@ -178,24 +201,18 @@ def moe_q8(x, router, w_up, s_up, w_down, s_down, out, top_k: int, renormalize: 
     out[t] = sum over the top_k experts of gate * down(silu(gate) * up), with
     the token and the hidden row in 8 bits.  ``ids`` (T, top_k; int32) and
     ``gates`` (T, top_k; float32) take the routing if given."""
-    dev = out.device
-    ldx = _matrix(x, "x", _FLOATS, None, dev)
-    T, H = x.shape
-    ldo = _matrix(out, "out", (x.dtype,), (T, H), dev)
-    ldr = _matrix(router, "router", (torch.float32,), None, dev)
-    E = router.shape[0]
-    if router.shape[1] != H:
-        raise ValueError(f"router must have shape (E, {H}), not {tuple(router.shape)}")
+    dev, shape, rshape = _index(out, "out"), _shape2(x, "x"), _shape2(router, "router")
+    T, H = shape
+    E = rshape[0]
+    if rshape[1] != H:
+        raise ValueError(f"router must have shape (E, {H}), not {tuple(rshape)}")
+    ldx = _matrix(x, "x", _FLOATS, shape, dev)
+    ldo = _matrix(out, "out", (x.dtype,), shape, dev)
+    ldr = _matrix(router, "router", (torch.float32,), rshape, dev)
     for t, name in ((w_up, "w_up"), (w_down, "w_down")):
-        if not isinstance(t, torch.Tensor) or t.dtype != torch.int8:
-            raise TypeError(f"{name} must be a torch tensor of type torch.int8")
-        if t.dim() != 3 or t.shape[0] != E:
-            raise ValueError(f"{name} must have three dimensions, the first of them {E}, not {tuple(t.shape)}")
-        if not t.is_contiguous():
-            raise ValueError(f"{name} must be contiguous")
+        if not isinstance(t, torch.Tensor) or t.dim() != 3:
+            raise ValueError(f"{name} must be a torch tensor of three dimensions")
     inner = w_down.shape[2]
-    if tuple(w_up.shape) != (E, 2 * inner, H) or w_down.shape[1] != H:
-        raise ValueError(f"shape mismatch: w_up {tuple(w_up.shape)}, w_down {tuple(w_down.shape)}, H = {H}")
     _packed(w_up, "w_up", torch.int8, (E, 2 * inner, H), dev)
     _packed(w_down, "w_down", torch.int8, (E, H, inner), dev)
     _packed(s_up, "s_up", torch.float32, (E, 2 * inner), dev)
