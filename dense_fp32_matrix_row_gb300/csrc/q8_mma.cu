@@ -144,12 +144,6 @@ __device__ __forceinline__ void tc_st32(uint32_t taddr, const uint32_t (&r)[32])
 }
 __device__ __forceinline__ void tc_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
-__device__ __forceinline__ uint4 lds128(uint32_t a) {
-    uint4 v;
-    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a));
-    return v;
-}
-
 // Arrive on the barrier at offset `bar` of CTA `cta` of the cluster.  Relaxed:
 // what it hands over is tensor memory alone, which the completed tcgen05
 // operations and tcgen05.fence before it order.  (A release at cluster scope
@@ -176,18 +170,6 @@ __device__ __forceinline__ void tma_load_x(uint32_t dst, const CUtensorMap *map,
             " [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(dst),
             "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(0), "r"(token), "r"(k64)
             : "memory");
-}
-
-// The whole warp waits, and agrees on whether the phase completed.
-__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, uint64_t limit_ns) {
-    return __all_sync(0xffffffffu, mbar_wait(bar, parity, limit_ns)) != 0;
-}
-
-// One lane of the converged warp, the same on every call.
-__device__ __forceinline__ bool elect_one() {
-    uint32_t p;
-    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
-    return p != 0;
 }
 
 template <int N, bool UP>

@@ -17,9 +17,10 @@
 
 namespace sgemm_gb300 {
 
+constexpr int kQ8Step = 64;          // k per step
+
 #ifdef __CUDACC__
 
-constexpr int kQ8Step = 64;          // k per step
 constexpr int kQ8ExactSteps = 16;    // steps per exact FP32 chunk (1024 k)
 
 __device__ __forceinline__ uint4 ldg_stream_u4(const void *p) {
@@ -77,6 +78,27 @@ __device__ __forceinline__ void q8_step(float (&acc)[NB][4], const uint4 &wa, co
             uint32_t b0, b1;
             q8_to_f16(w, b0, b1);
             mma_f16(acc[n], a, b0, b1);
+        }
+    }
+}
+
+// The same for RW pairs of weight rows that share the tokens.
+template <int RW, int NB>
+__device__ __forceinline__ void q8_step_rows(float (&acc)[RW][NB][4], const uint4 (&wa)[RW], const uint4 (&wb)[RW],
+                                             const uint4 (&x)[NB]) {
+#pragma unroll
+    for (int s = 0; s < 4; ++s) {
+        uint32_t b[NB][2];
+#pragma unroll
+        for (int n = 0; n < NB; ++n)
+            q8_to_f16(s == 0 ? x[n].x : s == 1 ? x[n].y : s == 2 ? x[n].z : x[n].w, b[n][0], b[n][1]);
+#pragma unroll
+        for (int r = 0; r < RW; ++r) {
+            uint32_t a[4];
+            q8_to_f16(s == 0 ? wa[r].x : s == 1 ? wa[r].y : s == 2 ? wa[r].z : wa[r].w, a[0], a[2]);
+            q8_to_f16(s == 0 ? wb[r].x : s == 1 ? wb[r].y : s == 2 ? wb[r].z : wb[r].w, a[1], a[3]);
+#pragma unroll
+            for (int n = 0; n < NB; ++n) mma_f16(acc[r][n], a, b[n][0], b[n][1]);
         }
     }
 }
@@ -164,6 +186,74 @@ __device__ __forceinline__ void q8_dot(int (&sum)[NB][4], const int8_t *wa, cons
         q8_step<NB>(acc, a, b, xv);
         q8_flush<NB>(sum, acc);
     }
+}
+
+// ---- the same product from a ring of bulk copies ----------------------------------
+//
+// One stage is RT 16-row tiles of KB steps (64 k each).  A row's share of it is
+// one bulk copy (4 KB at RT = 1: a 64-byte-wide TMA box ran at half the rate), a
+// tile's are issued by a warp of their own.  Rows lie 64 bytes further apart
+// than they are long, so that the 128-bit reads of a fragment, rows g and g + 1
+// together, meet no bank conflict.  Sixteen consumer warps take STEPS steps
+// each, of RW tiles.  Their sums of a tile, integers, meet in shared memory
+// (as 16-byte stores and one pass of reads: 256 shared-memory atomics a tile
+// took as long as its products).
+//
+// Up to 8 tokens the products are 8-bit MMAs (mma.sync m16n8k32 s8): exact
+// without any expansion, and although sm_103a runs them at a sixteenth of the
+// FP16 rate per byte, 31 bytes of W per cycle and SM is more than memory brings
+// (23).  For 16 tokens that halves, and the FP16 form takes over; there a warp
+// takes RW = 2 row tiles, so that the tokens' bytes, which would otherwise be as
+// many as W's, are fetched and expanded half as often.
+constexpr int kQ8Consumers = 16;
+template <int RT, int RW, int STEPS_>
+struct Q8Stage {
+    static constexpr int STEPS = STEPS_, ROWS = 16 * RT;
+    static constexpr int KW = kQ8Consumers / (RT / RW);   // warps that divide a tile's steps
+    static constexpr int KB = KW * STEPS;
+    static constexpr uint32_t LD = KB * kQ8Step + 64;
+    static constexpr uint32_t BYTES = ROWS * LD;
+    static_assert(RT % RW == 0 && kQ8ExactSteps % STEPS == 0, "the warps cover the stage");
+};
+
+__device__ __forceinline__ void mma_s8(int (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                       uint32_t b1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k32.row.col.s32.s8.s8.s32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+        "{%0, %1, %2, %3};"
+        : "+r"(c[0]), "+r"(c[1]), "+r"(c[2]), "+r"(c[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// q8_step with 8-bit MMAs: as there, words of the 16 bytes are fed in pairs.
+__device__ __forceinline__ void q8_step_s8(int (&sum)[4], const uint4 &wa, const uint4 &wb, const uint4 &x) {
+    mma_s8(sum, wa.x, wb.x, wa.y, wb.y, x.x, x.y);
+    mma_s8(sum, wa.z, wb.z, wa.w, wb.w, x.z, x.w);
+}
+
+// Bulk copy into shared memory: 16-byte aligned addresses and size.
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void *src, uint32_t bytes, uint32_t bar) {
+    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
+                 "l"(src), "r"(bytes), "r"(bar)
+                 : "memory");
+}
+
+__device__ __forceinline__ uint4 lds128(uint32_t a) {
+    uint4 v;
+    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a));
+    return v;
+}
+
+// One lane of the converged warp, the same on every call.
+__device__ __forceinline__ bool elect_one() {
+    uint32_t p;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
+    return p != 0;
+}
+
+// The whole warp waits, and agrees on whether the phase completed.
+__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, uint64_t limit_ns) {
+    return __all_sync(0xffffffffu, mbar_wait(bar, parity, limit_ns)) != 0;
 }
 
 #endif  // __CUDACC__
