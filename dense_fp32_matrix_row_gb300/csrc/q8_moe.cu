@@ -21,6 +21,8 @@
 // the hidden rows into 8 bits, and the one that finishes the last down unit
 // of an output range adds the experts' results, in slot order: nothing
 // depends on timing, and results repeat bit for bit.
+#include <type_traits>
+
 #include "q8_stream.cuh"
 
 namespace sgemm_gb300 {
@@ -32,13 +34,13 @@ constexpr int kMaxPairs = kMoeMaxTokens * kMoeMaxTopK;
 
 // The layer's workspace: byte offsets of its arrays.
 struct MoeLayout {
-    int P, Hp, Ip, dmax;      // pairs (token, slot); row strides; down groups at most
+    int P, Hp, Ip, dmax;      // pairs (token, slot); row strides (whole cache lines); down groups at most
     size_t logits, xs, xq, hidden, hs, hq, part, zero, total;
     int nzero;                // words to clear: ticket, ready[P], flag[P], hmax[P], done[dmax]
     __host__ __device__ MoeLayout(int T, int E, int top_k, int H, int I) {
         P = T * top_k;
-        Hp = (H + kQ8Step - 1) / kQ8Step * kQ8Step;
-        Ip = (I + kQ8Step - 1) / kQ8Step * kQ8Step;
+        Hp = (H + 127) / 128 * 128;
+        Ip = (I + 127) / 128 * 128;
         dmax = (H + 15) / 16;
         size_t at = 0;
         auto take = [&](size_t bytes) {
@@ -65,7 +67,7 @@ struct MoeLayout {
 template <typename T>
 __global__ void __launch_bounds__(RTHREADS)
 q8_route_kernel(int ntok, int E, int top_k, int H, int I, const T *__restrict__ x, int64_t ldx,
-                const float *__restrict__ router, int64_t ldr, unsigned char *__restrict__ ws) {
+                const float *__restrict__ router, int64_t ldr, int vec, unsigned char *__restrict__ ws) {
     __shared__ uint32_t red[64];
     __shared__ float lsum[RTHREADS / 32][8];
     const MoeLayout L(ntok, E, top_k, H, I);
@@ -80,11 +82,24 @@ q8_route_kernel(int ntok, int E, int top_k, int H, int I, const T *__restrict__ 
             float acc[8];
 #pragma unroll
             for (int j = 0; j < 8; ++j) acc[j] = 0.0f;
-            for (int k = threadIdx.x; k < H; k += RTHREADS) {
-                const float wk = __ldg(w + k);
+            if (vec) {
+                for (int k = 4 * (int)threadIdx.x; k < H; k += 4 * RTHREADS) {
+                    const float4 w4 = __ldg(reinterpret_cast<const float4 *>(w + k));
 #pragma unroll
-                for (int j = 0; j < 8; ++j)
-                    if (t0 + j < ntok) acc[j] = fmaf(to_f32<T>(x[(int64_t)(t0 + j) * ldx + k]), wk, acc[j]);
+                    for (int j = 0; j < 8; ++j)
+                        if (t0 + j < ntok) {
+                            float v[4];
+                            load_vec<T, 4>(x + (int64_t)(t0 + j) * ldx + k, v);
+                            acc[j] = fmaf(v[0], w4.x, fmaf(v[1], w4.y, fmaf(v[2], w4.z, fmaf(v[3], w4.w, acc[j]))));
+                        }
+                }
+            } else {
+                for (int k = threadIdx.x; k < H; k += RTHREADS) {
+                    const float wk = __ldg(w + k);
+#pragma unroll
+                    for (int j = 0; j < 8; ++j)
+                        if (t0 + j < ntok) acc[j] = fmaf(to_f32<T>(x[(int64_t)(t0 + j) * ldx + k]), wk, acc[j]);
+                }
             }
 #pragma unroll
             for (int j = 0; j < 8; ++j)
@@ -112,12 +127,29 @@ q8_route_kernel(int ntok, int E, int top_k, int H, int I, const T *__restrict__ 
     const T *xr = x + (int64_t)t * ldx;
     uint32_t mx = 0;
     float none = 0.0f;
-    for (int k = threadIdx.x; k < H; k += RTHREADS) mx = max(mx, abs_bits(to_f32<T>(xr[k])));
+    int8_t *q = reinterpret_cast<int8_t *>(ws + L.xq) + (int64_t)t * L.Hp;
+    if (vec) {
+        for (int k = 4 * (int)threadIdx.x; k < H; k += 4 * RTHREADS) {
+            float v[4];
+            load_vec<T, 4>(xr + k, v);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) mx = max(mx, abs_bits(v[i]));
+        }
+    } else {
+        for (int k = threadIdx.x; k < H; k += RTHREADS) mx = max(mx, abs_bits(to_f32<T>(xr[k])));
+    }
     block_max_sum(mx, none, red);
     const RowQuant rq(mx);
-    int8_t *q = reinterpret_cast<int8_t *>(ws + L.xq) + (int64_t)t * L.Hp;
-    for (int k = threadIdx.x; k < L.Hp; k += RTHREADS)
-        q[k] = k < H ? (int8_t)rq(to_f32<T>(xr[k])) : (int8_t)0;
+    if (vec) {
+        for (int k = 4 * (int)threadIdx.x; k < L.Hp; k += 4 * RTHREADS) {
+            float v[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+            if (k < H) load_vec<T, 4>(xr + k, v);
+            store_q<4>(q + k, rq, v);
+        }
+    } else {
+        for (int k = threadIdx.x; k < L.Hp; k += RTHREADS)
+            q[k] = k < H ? (int8_t)rq(to_f32<T>(xr[k])) : (int8_t)0;
+    }
     if (threadIdx.x == 0) reinterpret_cast<float *>(ws + L.xs)[t] = rq.step * rq.unpre;
 }
 
@@ -147,17 +179,19 @@ struct MoeShared {
     int count[kMoeMaxExperts];
     int first[kMoeMaxExperts], first_chunk[kMoeMaxExperts];
     int nchunks;
+};
+
+struct MoeBlock : MoeShared {
     int ticket[2];
     int flag;
     int part[MWARPS][16][17];
 };
 
-// The routing of all tokens, the same in every block: top_k experts and gates
-// of each token, then each expert's pairs and their chunks of up to 16.
-__device__ void moe_route(MoeShared &S, int ntok, int E, int top_k, int renorm, const float *logits) {
+// top_k experts and gates of every token; E <= 32 * PER.
+template <int PER>
+__device__ void moe_choose(MoeShared &S, int ntok, int E, int top_k, int renorm, const float *logits) {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    constexpr int PER = kMoeMaxExperts / 32;
-    for (int t = warp; t < ntok; t += MWARPS) {
+    for (int t = warp; t < ntok; t += (int)(blockDim.x >> 5)) {
         float l[PER];
         uint32_t key[PER];
 #pragma unroll
@@ -205,9 +239,19 @@ __device__ void moe_route(MoeShared &S, int ntok, int E, int top_k, int renorm, 
             S.gates[t * top_k + lane] = mine / (renorm ? chosen : all);
         }
     }
+}
+
+// The routing of all tokens, the same in every block: top_k experts and gates
+// of each token, then each expert's pairs and their chunks of up to 16.
+__device__ void moe_route(MoeShared &S, int ntok, int E, int top_k, int renorm, const float *logits) {
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    if (E <= 32) moe_choose<1>(S, ntok, E, top_k, renorm, logits);
+    else if (E <= 64) moe_choose<2>(S, ntok, E, top_k, renorm, logits);
+    else if (E <= 128) moe_choose<4>(S, ntok, E, top_k, renorm, logits);
+    else moe_choose<kMoeMaxExperts / 32>(S, ntok, E, top_k, renorm, logits);
     __syncthreads();
     const int P = ntok * top_k;
-    for (int e = threadIdx.x; e < E; e += MTHREADS) {
+    for (int e = threadIdx.x; e < E; e += (int)blockDim.x) {
         int c = 0;
         for (int p = 0; p < P; ++p) c += S.ids[p] == e;
         S.count[e] = c;
@@ -237,7 +281,7 @@ __device__ void moe_route(MoeShared &S, int ntok, int E, int top_k, int renorm, 
         if (lane == 0) S.nchunks = chunks;
     }
     __syncthreads();
-    for (int e = threadIdx.x; e < E; e += MTHREADS) {
+    for (int e = threadIdx.x; e < E; e += (int)blockDim.x) {
         int at = S.first[e];
         if (S.count[e])
             for (int p = 0; p < P; ++p)
@@ -253,7 +297,7 @@ __device__ void moe_route(MoeShared &S, int ntok, int E, int top_k, int renorm, 
 
 // One block's sums for 16-row tiles `tile` of a weight matrix into S.part.
 template <int NB, bool VEC, bool COHERENT>
-__device__ __forceinline__ void moe_dot(MoeShared &S, const int8_t *wa, const int8_t *wb, const int8_t *xbase,
+__device__ __forceinline__ void moe_dot(MoeBlock &S, const int8_t *wa, const int8_t *wb, const int8_t *xbase,
                                         const int (&xrow)[2], int64_t xld, int K, int kw, const int8_t *wbegin,
                                         const int8_t *wend, const int8_t *xend) {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
@@ -279,14 +323,16 @@ __device__ __forceinline__ void moe_dot(MoeShared &S, const int8_t *wa, const in
     }
 }
 
-template <typename T, bool VEC>
+// ---- any alignment -------------------------------------------------------------
+
+template <typename T>
 __global__ void __launch_bounds__(MTHREADS, 2)
 q8_expert_kernel(int ntok, int E, int top_k, int H, int I, int renorm, const int8_t *__restrict__ w_up,
                  int64_t ldu, const float *__restrict__ s_up, const int8_t *__restrict__ w_down,
                  int64_t ldd, const float *__restrict__ s_down, T *__restrict__ out, int64_t ldo,
                  int *__restrict__ ids, float *__restrict__ gates, unsigned char *ws, int kw_up,
                  int kw_down, unsigned *err, uint64_t wait_ns) {
-    __shared__ MoeShared S;
+    __shared__ MoeBlock S;
     const MoeLayout L(ntok, E, top_k, H, I);
     const float *xs = reinterpret_cast<const float *>(ws + L.xs);
     const int8_t *xq = reinterpret_cast<const int8_t *>(ws + L.xq);
@@ -331,8 +377,8 @@ q8_expert_kernel(int ntok, int E, int top_k, int H, int I, int renorm, const int
             const int8_t *wb = wa + (int64_t)I * ldu;
             const int xrow[2] = {pa / top_k, pb / top_k};
             const int8_t *xend = xq + (int64_t)ntok * L.Hp;
-            if (n <= 8) moe_dot<1, VEC, true>(S, wa, wb, xq, xrow, L.Hp, H, kw_up, w_up, up_end, xend);
-            else moe_dot<2, VEC, true>(S, wa, wb, xq, xrow, L.Hp, H, kw_up, w_up, up_end, xend);
+            if (n <= 8) moe_dot<1, false, true>(S, wa, wb, xq, xrow, L.Hp, H, kw_up, w_up, up_end, xend);
+            else moe_dot<2, false, true>(S, wa, wb, xq, xrow, L.Hp, H, kw_up, w_up, up_end, xend);
             __syncthreads();
             const int tok = n <= 8 ? 8 : 16;
             for (int o = tid; o < 8 * rt_up * tok; o += MTHREADS) {   // whole warps: 8 * tok * rt_up is a multiple of 32
@@ -394,8 +440,8 @@ q8_expert_kernel(int ntok, int E, int top_k, int H, int I, int renorm, const int
             const int8_t *wb = w_down + ((int64_t)e * H + min(n0 + g + 8, H - 1)) * ldd;
             const int xrow[2] = {pa, pb};
             const int8_t *xend = hq + (int64_t)L.P * L.Ip;
-            if (n <= 8) moe_dot<1, VEC, true>(S, wa, wb, hq, xrow, L.Ip, I, kw_down, w_down, down_end, xend);
-            else moe_dot<2, VEC, true>(S, wa, wb, hq, xrow, L.Ip, I, kw_down, w_down, down_end, xend);
+            if (n <= 8) moe_dot<1, false, true>(S, wa, wb, hq, xrow, L.Ip, I, kw_down, w_down, down_end, xend);
+            else moe_dot<2, false, true>(S, wa, wb, hq, xrow, L.Ip, I, kw_down, w_down, down_end, xend);
             __syncthreads();
             for (int o = tid; o < 16 * rt_down * n; o += MTHREADS) {
                 const int r = o & 15, tl = (o >> 4) % rt_down, j = (o >> 4) / rt_down;
@@ -427,6 +473,495 @@ q8_expert_kernel(int ntok, int E, int top_k, int H, int I, int renorm, const int
     }
 }
 
+// ---- the persistent kernel for weights whose arrays are 16-byte aligned -----------
+//
+// Roles of a block (one per SM):
+//   producer   one warp draws units from the counter and brings each unit's
+//              weights into a ring of bulk copies (see q8_stream.cuh), running
+//              ahead into later units, down projections too: weights depend on
+//              the routing alone;
+//   consumers  two groups of eight warps take units in turn, multiply (dp4a up
+//              to 4 tokens, then 8-bit MMAs) and add their integer sums in a
+//              buffer;
+//   finishers  a warp for each group turns sums into hidden values, quantises
+//              complete hidden rows and adds the experts' results (units of their
+//              own after the gate/up and after the down projections).
+// A unit is up to four 16-row tiles (of the gate/up projection, 8 gate and 8 up
+// rows each), 33 to 70 KB: its chain of waits, token loads and hand-overs takes as
+// long as 33 KB do at the memory's rate, hence the groups, the finishers and the
+// size; larger units leave blocks idle at the end of a projection.
+// Rows whose length is no multiple of 16 (SHIFT) are copied from the 16-byte
+// boundary below and shifted as the fragments are read.
+constexpr int FINISHERS = 2;                               // one per consumer group
+constexpr int E_PRODUCER = kQ8Consumers + FINISHERS;
+constexpr int ETHREADS = (E_PRODUCER + 1) * 32;
+constexpr int ERING = 5, EBUFS = 4;                        // stages; buffers of sums, two per group
+constexpr int EGROUP = kQ8Consumers / 2;                   // warps of a consumer group
+constexpr int ESTEPS = 4;                                  // steps per consumer warp and stage
+constexpr int ETILES = 4;                                  // 16-row tiles of a unit, at most
+constexpr uint32_t ESTAGE = 64 * (8 * kQ8Step + 64 + 16);  // the largest geometry (RT = 4)
+constexpr int EPART = ETILES * 2 * 128;                    // one unit's sums: [tile][token block][word][lane]
+constexpr int QSEG = 1024;                                 // hidden values a quantising unit takes
+constexpr int CSEG = 128;                                  // results an adding unit takes
+
+struct EGeom {       // one projection's division
+    int K, rt, kw, kb, blocks, stages, sub, groups;
+    uint32_t ld;
+    // `rows` results, `per_tile` of them to a tile; `experts` of them are wanted at most
+    __host__ __device__ EGeom(int K_, int rows, int per_tile, bool shift, int chunks, int blocks_of_grid) : K(K_) {
+        const int steps = (K + kQ8Step - 1) / kQ8Step;
+        rt = steps <= 8 ? 4 : steps <= 16 ? 2 : 1;
+        kw = EGROUP / rt;
+        kb = kw * ESTEPS;
+        // whole steps that the ring brings; shifted rows leave 15 bytes at their end alone
+        blocks = shift ? (K > 15 ? (K - 15) / kQ8Step : 0) : K / kQ8Step;
+        stages = blocks > 0 ? (blocks + kb - 1) / kb : 1;
+        // two stages to a unit, if that leaves every block eight units
+        const int64_t all = (int64_t)((rows + per_tile * rt - 1) / (per_tile * rt)) * chunks;
+        sub = stages == 1 && rt <= 2 && all >= (int64_t)16 * blocks_of_grid ? 2 : 1;
+        groups = (rows + per_tile * rt * sub - 1) / (per_tile * rt * sub);
+        ld = (uint32_t)(kb * kQ8Step + 64 + (shift ? 16 : 0));
+    }
+};
+
+struct EShared {
+    MoeShared route;
+    int unit[ERING];                  // unit a stage belongs to
+    int done[EBUFS];                  // unit a buffer of sums belongs to
+    uint64_t full[ERING], empty[ERING], bfull[EBUFS], bempty[EBUFS];
+};
+constexpr size_t EOFF_PART = (size_t)ERING * ESTAGE;
+constexpr size_t EOFF_SHARED = EOFF_PART + (size_t)EBUFS * EPART * 4;
+constexpr size_t ESMEM = 128 + EOFF_SHARED + sizeof(EShared);
+static_assert(ESMEM <= 227 * 1024, "shared memory per block");
+
+// 16 bytes at any address of shared memory.
+__device__ __forceinline__ uint4 lds_shifted(uint32_t addr) {
+    const uint32_t a = addr & ~3u;
+    const int sh = 8 * (int)(addr & 3);
+    uint32_t w[5];
+#pragma unroll
+    for (int i = 0; i < 5; ++i) asm volatile("ld.shared.u32 %0, [%1];" : "=r"(w[i]) : "r"(a + 4 * i));
+    return make_uint4(__funnelshift_r(w[0], w[1], sh), __funnelshift_r(w[1], w[2], sh),
+                      __funnelshift_r(w[2], w[3], sh), __funnelshift_r(w[3], w[4], sh));
+}
+
+// Lane 0 polls a counter until it reaches `want` (bounded); the warp agrees.
+__device__ __forceinline__ bool warp_poll(const uint32_t *p, uint32_t want, uint64_t wait_ns) {
+    int ok = 1;
+    if ((threadIdx.x & 31) == 0 && ld_acquire(p) < want) {
+        const uint64_t t0 = globaltimer_ns();
+        do {
+            ok = ld_acquire(p) >= want;
+        } while (!ok && globaltimer_ns() - t0 <= wait_ns);
+    }
+    ok = __shfl_sync(0xffffffffu, ok, 0);
+    __syncwarp();
+    return ok != 0;
+}
+
+template <typename T, bool SHIFT>
+__global__ void __launch_bounds__(ETHREADS, 1)
+q8_expert_ring_kernel(int ntok, int E, int top_k, int H, int I, int renorm, const int8_t *__restrict__ w_up,
+                      int64_t ldu, const float *__restrict__ s_up, const int8_t *__restrict__ w_down, int64_t ldd,
+                      const float *__restrict__ s_down, T *__restrict__ out, int64_t ldo, int *__restrict__ ids,
+                      float *__restrict__ gates, unsigned char *ws, unsigned *err, uint64_t wait_ns) {
+    extern __shared__ unsigned char smem_raw[];
+    unsigned char *smem = reinterpret_cast<unsigned char *>((reinterpret_cast<uintptr_t>(smem_raw) + 127) & ~uintptr_t(127));
+    int *part = reinterpret_cast<int *>(smem + EOFF_PART);
+    EShared &S = *reinterpret_cast<EShared *>(smem + EOFF_SHARED);
+    MoeShared &R = S.route;
+    const MoeLayout L(ntok, E, top_k, H, I);
+    const float *xs = reinterpret_cast<const float *>(ws + L.xs);
+    const int8_t *xq = reinterpret_cast<const int8_t *>(ws + L.xq);
+    float *hidden = reinterpret_cast<float *>(ws + L.hidden);
+    float *hs = reinterpret_cast<float *>(ws + L.hs);
+    int8_t *hq = reinterpret_cast<int8_t *>(ws + L.hq);
+    float *res = reinterpret_cast<float *>(ws + L.part);
+    uint32_t *ticket = reinterpret_cast<uint32_t *>(ws + L.zero);
+    uint32_t *ready = ticket + 1, *quantised = ready + L.P, *hmax = quantised + L.P, *done = hmax + L.P;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+
+    if (tid == 0) {
+        for (int s = 0; s < ERING; ++s) {
+            mbar_init(smem_u32(&S.full[s]), 1);
+            mbar_init(smem_u32(&S.empty[s]), kQ8Consumers);
+        }
+        for (int b = 0; b < EBUFS; ++b) {
+            mbar_init(smem_u32(&S.bfull[b]), EGROUP);
+            mbar_init(smem_u32(&S.bempty[b]), 1);
+        }
+        mbar_fence_init();
+    }
+    for (int i = tid; i < EBUFS * EPART; i += ETHREADS) part[i] = 0;
+    pdl_wait();
+    moe_route(R, ntok, E, top_k, renorm, reinterpret_cast<const float *>(ws + L.logits));   // ends with a barrier
+    if (blockIdx.x == 0) {
+        for (int p = tid; p < L.P; p += ETHREADS) {
+            if (ids) ids[p] = R.ids[p];
+            if (gates) gates[p] = R.gates[p];
+        }
+    }
+    const EGeom gu(H, I, 8, SHIFT, R.nchunks, (int)gridDim.x), gd(I, H, 16, SHIFT, R.nchunks, (int)gridDim.x);
+    const int segs = (L.Ip + QSEG - 1) / QSEG;                 // quantising units of one pair
+    const int up_units = R.nchunks * gu.groups, q_units = L.P * segs;
+    const int down_end_unit = up_units + q_units + R.nchunks * gd.groups;
+    const int csegs = (H + CSEG - 1) / CSEG;                   // adding units of one token
+    const int units = down_end_unit + ntok * csegs;
+    // what a unit does: 0 up, 1 quantise, 2 down, 3 add (1 and 3 have no weights)
+    auto kind_of = [&](int u) {
+        return u < up_units ? 0 : u < up_units + q_units ? 1 : u < down_end_unit ? 2 : 3;
+    };
+
+    if (warp == E_PRODUCER) {
+        bool ok = true;
+        uint32_t g = 0;
+        auto slot = [&](int &r) {
+            r = (int)(g % ERING);
+            return g < (uint32_t)ERING || warp_wait(smem_u32(&S.empty[r]), (g / ERING - 1) & 1, wait_ns);
+        };
+        int next = lane == 0 ? (int)atomicAdd(ticket, 1u) : 0;
+        while (ok) {
+            const int u = __shfl_sync(0xffffffffu, next, 0);
+            if (lane == 0) next = (int)atomicAdd(ticket, 1u);   // on its way while this unit is brought
+            const int kind = u >= units ? 1 : kind_of(u);
+            if (kind & 1) {      // nothing to bring: a finisher's unit, or the end
+                int r;
+                if (!(ok = slot(r))) break;
+                if (lane == 0) {
+                    S.unit[r] = u;
+                    mbar_arrive(smem_u32(&S.full[r]));
+                }
+                ++g;
+                if (u >= units) break;
+                continue;
+            }
+            const bool up = kind == 0;
+            const int groups = up ? gu.groups : gd.groups, rt = up ? gu.rt : gd.rt, sub = up ? gu.sub : gd.sub;
+            const int stages = up ? gu.stages : gd.stages, kb = up ? gu.kb : gd.kb;
+            const int blocks = up ? gu.blocks : gd.blocks;
+            const uint32_t ld = up ? gu.ld : gd.ld;
+            const int v = up ? u : u - up_units - q_units;
+            const int c = v / groups, grp = v - c * groups, e = R.chunk_e[c];
+            const int8_t *row0 = up ? w_up + (int64_t)e * 2 * I * ldu : w_down + (int64_t)e * H * ldd;
+            for (int t = 0; t < sub && ok; ++t) {
+                // this lane's rows of the stage (rows past the end read the last one)
+                const int8_t *row[2] = {nullptr, nullptr};
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const int q = lane + 32 * h, tile = (grp * sub + t) * rt + (q >> 4);
+                    if (q < 16 * rt) {
+                        const int i = min(tile * 8 + (q & 7), I - 1) + ((q >> 3) & 1) * I;
+                        row[h] = row0 + (up ? (int64_t)i * ldu : (int64_t)min(tile * 16 + (q & 15), H - 1) * ldd);
+                    }
+                }
+                for (int s = 0; s < stages; ++s, ++g) {
+                    int r;
+                    if (!(ok = slot(r))) break;
+                    const uint32_t bar = smem_u32(&S.full[r]);
+                    const uint32_t base = smem_u32(smem) + (uint32_t)r * ESTAGE;
+                    const int len = max(0, min(kb, blocks - s * kb)) * kQ8Step;
+                    const int8_t *src[2];
+                    uint32_t bytes[2], total = 0;
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        bytes[h] = 0;
+                        src[h] = row[h] + (int64_t)s * kb * kQ8Step;
+                        if (row[h] != nullptr && len > 0) {
+                            bytes[h] = (uint32_t)len;
+                            if (SHIFT) {
+                                const uint32_t off = (uint32_t)(reinterpret_cast<uintptr_t>(src[h]) & 15);
+                                src[h] -= off;
+                                bytes[h] = (bytes[h] + off + 15) / 16 * 16;
+                            }
+                            total += bytes[h];
+                        }
+                    }
+                    total = __reduce_add_sync(0xffffffffu, total);
+                    if (lane == 0) {
+                        S.unit[r] = u;
+                        if (total > 0) mbar_arrive_expect_tx(bar, total);
+                        else mbar_arrive(bar);
+                    }
+                    __syncwarp();
+#pragma unroll
+                    for (int h = 0; h < 2; ++h)
+                        if (bytes[h] > 0) bulk_load(base + (uint32_t)(lane + 32 * h) * ld, src[h], bytes[h], bar);
+                    __syncwarp();
+                }
+            }
+        }
+        if (!ok && lane == 0) {
+            record_error(err, kErrWaitTimeout);
+            for (uint32_t q = g > (uint32_t)ERING ? g - ERING : 0; q < g; ++q)
+                mbar_wait(smem_u32(&S.full[q % ERING]), (q / ERING) & 1, 1000000000ull);
+        }
+    } else if (warp < kQ8Consumers) {
+        const int g = lane >> 2, t4 = lane & 3;
+        const int group = warp / EGROUP, cw = warp % EGROUP;
+        uint32_t used = 0;
+        bool ok = true;
+        for (uint32_t count = 0;; ++count) {
+            int r = (int)(used % ERING);
+            if (!(ok = warp_wait(smem_u32(&S.full[r]), (used / ERING) & 1, wait_ns))) break;
+            const int u = S.unit[r];
+            const int kind = u >= units ? 1 : kind_of(u);
+            const bool mine = (int)(count & 1) == group;
+            const bool up = kind == 0;
+            const int stages = up ? gu.stages : gd.stages, sub = up ? gu.sub : gd.sub;
+            if (!mine || (kind & 1)) {     // the other group's unit, or one without weights
+                const int all = (kind & 1) ? 1 : stages * sub;
+                for (int s = 0; s < all; ++s, ++used) {
+                    r = (int)(used % ERING);
+                    if (s > 0 && !(ok = warp_wait(smem_u32(&S.full[r]), (used / ERING) & 1, wait_ns))) break;
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(smem_u32(&S.empty[r]));
+                }
+                if (!ok) break;
+                if (!mine && u < units) continue;
+            } else {
+                const int b = (int)(count % EBUFS);
+                const int K = up ? H : I, groups = up ? gu.groups : gd.groups, rt = up ? gu.rt : gd.rt;
+                const int kw = up ? gu.kw : gd.kw, kb = up ? gu.kb : gd.kb, blocks = up ? gu.blocks : gd.blocks;
+                const uint32_t ld = up ? gu.ld : gd.ld;
+                const int v = up ? u : u - up_units - q_units;
+                const int c = v / groups, grp = v - c * groups;
+                const int e = R.chunk_e[c], at = R.chunk_at[c], n = R.chunk_n[c];
+                // down: the chunk's hidden rows are there in 8 bits
+                if (!up && !(ok = warp_poll(quantised + c, (uint32_t)(n * segs), wait_ns))) break;
+                const int tl = cw / kw, kpart = cw % kw;      // this warp's tile of a stage, its share of the steps
+                const int step0 = kpart * ESTEPS;
+                const int8_t *xbase = up ? xq : hq;
+                const int64_t xld = up ? L.Hp : L.Ip;
+                // token row of the chunk's pair j (past the end: the last one)
+                auto token = [&](int j) {
+                    const int p = R.list[at + min(j, n - 1)];
+                    return xbase + (int64_t)(up ? p / top_k : p) * xld + 16 * t4;
+                };
+                // the buffer is free (its finisher has read and cleared it)
+                if (count >= (uint32_t)EBUFS &&
+                    !(ok = warp_wait(smem_u32(&S.bempty[b]), (count / EBUFS - 1) & 1, wait_ns)))
+                    break;
+                // DP: NT tokens by dp4a, each lane with every token's bytes; otherwise
+                // NT blocks of 8 tokens by MMA, lane row g with token g of each.
+                auto multiply = [&](auto nt, auto dp) {
+                    constexpr int NT = decltype(nt)::value;
+                    constexpr bool DP = decltype(dp)::value;
+                    const int8_t *x[NT];
+#pragma unroll
+                    for (int j = 0; j < NT; ++j) x[j] = token(DP ? j : 8 * j + g);
+                    for (int t = 0; t < sub && ok; ++t) {
+                        // the two weight rows of this lane, and where they lie in a stage
+                        const int tile = (grp * sub + t) * rt + tl;
+                        const int8_t *wa, *wb;
+                        if (up) {
+                            wa = w_up + ((int64_t)e * 2 * I + min(tile * 8 + g, I - 1)) * ldu;
+                            wb = wa + (int64_t)I * ldu;
+                        } else {
+                            wa = w_down + ((int64_t)e * H + min(tile * 16 + g, H - 1)) * ldd;
+                            wb = w_down + ((int64_t)e * H + min(tile * 16 + g + 8, H - 1)) * ldd;
+                        }
+                        const uint32_t oa = (uint32_t)(tl * 16 + g) * ld + (uint32_t)(step0 * kQ8Step + 16 * t4) +
+                                            (SHIFT ? (uint32_t)(reinterpret_cast<uintptr_t>(wa) & 15) : 0u);
+                        const uint32_t ob = (uint32_t)(tl * 16 + g + 8) * ld + (uint32_t)(step0 * kQ8Step + 16 * t4) +
+                                            (SHIFT ? (uint32_t)(reinterpret_cast<uintptr_t>(wb) & 15) : 0u);
+                        int sum[NT][DP ? 2 : 4];
+#pragma unroll
+                        for (int j = 0; j < NT; ++j)
+#pragma unroll
+                            for (int i = 0; i < (DP ? 2 : 4); ++i) sum[j][i] = 0;
+                        auto step = [&](const uint4 &a, const uint4 &d, int64_t k) {
+                            uint4 xv[NT];
+#pragma unroll
+                            for (int j = 0; j < NT; ++j) xv[j] = *reinterpret_cast<const uint4 *>(x[j] + k);
+                            if constexpr (DP) {
+                                q8_step_dp<NT>(sum, a, d, xv);
+                            } else {
+#pragma unroll
+                                for (int j = 0; j < NT; ++j) q8_step_s8(sum[j], a, d, xv[j]);
+                            }
+                        };
+                        for (int s = 0; s < stages; ++s, ++used) {
+                            r = (int)(used % ERING);
+                            if (s + t > 0 && !(ok = warp_wait(smem_u32(&S.full[r]), (used / ERING) & 1, wait_ns))) break;
+                            const uint32_t stage = smem_u32(smem) + (uint32_t)r * ESTAGE;
+#pragma unroll
+                            for (int k = 0; k < ESTEPS; ++k)
+                                if (s * kb + step0 + k < blocks)
+                                    step(SHIFT ? lds_shifted(stage + oa + k * kQ8Step) : lds128(stage + oa + k * kQ8Step),
+                                         SHIFT ? lds_shifted(stage + ob + k * kQ8Step) : lds128(stage + ob + k * kQ8Step),
+                                         (int64_t)(s * kb + step0 + k) * kQ8Step);
+                            __syncwarp();
+                            if (lane == 0) mbar_arrive(smem_u32(&S.empty[r]));
+                        }
+                        if (!ok) break;
+                        if (kpart == 0)
+                            for (int k0 = blocks * kQ8Step; k0 < K; k0 += kQ8Step) {   // the rows' last values
+                                const int valid = min(16, max(0, K - k0 - 16 * t4));
+                                step(load16_bytes(wa + k0 + 16 * t4, valid), load16_bytes(wb + k0 + 16 * t4, valid), k0);
+                            }
+                        // whole numbers: the order of these additions does not matter
+                        int *to = part + b * EPART + (t * rt + tl) * 256;
+                        if constexpr (DP) {
+#pragma unroll
+                            for (int j = 0; j < NT; ++j)
+#pragma unroll
+                                for (int i = 0; i < 2; ++i) {
+                                    int v2 = sum[j][i];
+                                    v2 += __shfl_xor_sync(0xffffffffu, v2, 1);
+                                    v2 += __shfl_xor_sync(0xffffffffu, v2, 2);
+                                    // one lane of the quad: where the MMA would leave (row, token j)
+                                    if (t4 == (j >> 1)) atomicAdd(to + (2 * i + (j & 1)) * 32 + lane, v2);
+                                }
+                        } else {
+#pragma unroll
+                            for (int j = 0; j < NT; ++j)
+#pragma unroll
+                                for (int i = 0; i < 4; ++i) atomicAdd(to + j * 128 + 32 * i + lane, sum[j][i]);
+                        }
+                    }
+                };
+                using std::integral_constant;
+                if (n == 1) multiply(integral_constant<int, 1>{}, std::true_type{});
+                else if (n == 2) multiply(integral_constant<int, 2>{}, std::true_type{});
+                else if (n <= 4) multiply(integral_constant<int, 4>{}, std::true_type{});
+                else if (n <= 8) multiply(integral_constant<int, 1>{}, std::false_type{});
+                else multiply(integral_constant<int, 2>{}, std::false_type{});
+                if (!ok) break;
+            }
+            // hand the sums over; the end goes to every finisher, each group telling
+            // those whose buffers it fills (it alone knows their turn)
+            const uint32_t last = u < units ? count : count + 1;
+            for (uint32_t q = count; q <= last; ++q) {
+                if ((int)(q & 1) != group) continue;
+                const int o = (int)(q % EBUFS);
+                if ((kind & 1) && q >= (uint32_t)EBUFS &&
+                    !(ok = warp_wait(smem_u32(&S.bempty[o]), (q / EBUFS - 1) & 1, wait_ns)))
+                    break;
+                if (cw == 0 && lane == 0) S.done[o] = u;
+                __syncwarp();
+                if (lane == 0) mbar_arrive(smem_u32(&S.bfull[o]));
+            }
+            if (!ok || u >= units) break;
+        }
+        if (!ok && lane == 0) record_error(err, kErrWaitTimeout);
+    } else {
+        bool ok = true;
+        for (uint32_t count = (uint32_t)(warp - kQ8Consumers);; count += FINISHERS) {
+            const int b = (int)(count % EBUFS);       // this finisher's buffer
+            if (!(ok = warp_wait(smem_u32(&S.bfull[b]), (count / EBUFS) & 1, wait_ns))) break;
+            const int u = S.done[b];
+            if (u >= units) break;
+            const int kind = kind_of(u);
+            int *sums = part + b * EPART;
+            auto sum_at = [&](int tile, int row, int tok) {
+                return sums[tile * 256 + (tok >> 3) * 128 + (((row >> 3) << 1) + (tok & 1)) * 32 + (row & 7) * 4 +
+                            ((tok & 7) >> 1)];
+            };
+            if (kind == 1) {
+                if (lane == 0) mbar_arrive(smem_u32(&S.bempty[b]));
+                const int v = u - up_units, q = v / segs, seg = v - q * segs;
+                const int p = R.list[q];            // pairs in the order of their chunks
+                int c = 0;
+                {
+                    const int e = R.ids[p];
+                    c = R.first_chunk[e] + (q - R.first[e]) / 16;
+                }
+                if (!(ok = warp_poll(ready + c, (uint32_t)gu.groups, wait_ns))) break;
+                const RowQuant rq(__ldcg(hmax + p));
+                const int lo = seg * QSEG, hi = min(lo + QSEG, L.Ip);
+                const float *hr = hidden + (int64_t)p * I;
+                int8_t *qr = hq + (int64_t)p * L.Ip;
+#pragma unroll 4
+                for (int i = lo + 4 * lane; i < hi; i += 4 * 32) {
+                    float h4[4];
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) h4[k] = i + k < I ? __ldcg(hr + i + k) : 0.0f;
+                    *reinterpret_cast<uint32_t *>(qr + i) = pack4(rq(h4[0]), rq(h4[1]), rq(h4[2]), rq(h4[3]));
+                }
+                if (seg == 0 && lane == 0) hs[p] = rq.step * rq.unpre;
+                __threadfence();
+                __syncwarp();
+                if (lane == 0) atomicAdd(quantised + c, 1u);
+                continue;
+            }
+            if (kind == 3) {      // one token's sum over its experts, in slot order
+                if (lane == 0) mbar_arrive(smem_u32(&S.bempty[b]));
+                const int v = u - down_end_unit, t = v / csegs, c0 = (v - t * csegs) * CSEG;
+                const int cols = 16 * gd.rt * gd.sub, g0 = c0 / cols, g1 = (min(c0 + CSEG, H) - 1) / cols;
+                for (int q = g0; q <= g1 && ok; ++q) ok = warp_poll(done + q, (uint32_t)R.nchunks, wait_ns);
+                if (!ok) break;
+                const int col = c0 + 4 * lane;
+                float y[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+                const float *rr = res + (int64_t)t * top_k * H + col;
+#pragma unroll 4
+                for (int j = 0; j < top_k; ++j) {
+                    float w4[4];
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) w4[k] = col + k < H ? __ldcg(rr + (int64_t)j * H + k) : 0.0f;
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) y[k] = fmaf(R.gates[t * top_k + j], w4[k], y[k]);
+                }
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                    if (col + k < H) out[(int64_t)t * ldo + col + k] = from_f32<T>(y[k]);
+                continue;
+            }
+            const bool up = kind == 0;
+            const int groups = up ? gu.groups : gd.groups;
+            const int tiles = up ? gu.rt * gu.sub : gd.rt * gd.sub;     // of the unit
+            const int v = up ? u : u - up_units - q_units;
+            const int c = v / groups, grp = v - c * groups;
+            const int e = R.chunk_e[c], at = R.chunk_at[c], n = R.chunk_n[c];
+            auto clear = [&] {      // the sums have been read: the buffer goes back empty
+                __syncwarp();
+                for (int i = lane; i < tiles * 64; i += 32) reinterpret_cast<int4 *>(sums)[i] = make_int4(0, 0, 0, 0);
+                __syncwarp();
+                if (lane == 0) mbar_arrive(smem_u32(&S.bempty[b]));
+            };
+            if (up) {
+                for (int o0 = 0; o0 < 8 * tiles * n; o0 += 32) {
+                    const int o = o0 + lane, row = o & 7, tl = (o >> 3) % tiles, j = (o >> 3) / tiles;
+                    const int i = (grp * tiles + tl) * 8 + row;
+                    uint32_t mb = 0;
+                    int p = 0;
+                    if (j < n && i < I) {
+                        p = R.list[at + j];
+                        const float s = __ldg(xs + p / top_k);
+                        const float gv = (float)sum_at(tl, row, j) * s * __ldg(s_up + (int64_t)e * 2 * I + i);
+                        const float uv = (float)sum_at(tl, row + 8, j) * s * __ldg(s_up + (int64_t)e * 2 * I + I + i);
+                        const float hv = __fdiv_rn(gv, 1.0f + expf(-gv)) * uv;
+                        __stcg(hidden + (int64_t)p * I + i, hv);
+                        mb = abs_bits(hv);
+                    }
+#pragma unroll
+                    for (int d = 1; d < 8; d <<= 1) mb = max(mb, __shfl_xor_sync(0xffffffffu, mb, d));
+                    if (row == 0 && j < n && mb != 0u) atomicMax(hmax + p, mb);
+                }
+                clear();
+                __threadfence();
+                __syncwarp();
+                if (lane == 0) atomicAdd(ready + c, 1u);
+            } else {
+                for (int o = lane; o < 16 * tiles * n; o += 32) {
+                    const int row = o & 15, tl = (o >> 4) % tiles, j = (o >> 4) / tiles;
+                    const int col = (grp * tiles + tl) * 16 + row;
+                    if (col < H) {
+                        const int p = R.list[at + j];
+                        __stcg(res + (int64_t)p * H + col,
+                               (float)sum_at(tl, row, j) * __ldcg(hs + p) * __ldg(s_down + (int64_t)e * H + col));
+                    }
+                }
+                clear();
+                __threadfence();
+                __syncwarp();
+                if (lane == 0) atomicAdd(done + grp, 1u);
+            }
+        }
+        if (!ok && lane == 0) record_error(err, kErrWaitTimeout);
+    }
+}
+
 // Warps that share one 16-row tile's K: at least 4 steps each.
 int warps_per_tile(int K) {
     const int steps = (K + kQ8Step - 1) / kQ8Step;
@@ -436,10 +971,11 @@ int warps_per_tile(int K) {
 }
 
 template <typename K, typename... A>
-cudaError_t launch_pdl(K kern, int grid, int threads, cudaStream_t s, A... args) {
+cudaError_t launch_pdl(K kern, int grid, int threads, size_t smem, cudaStream_t s, A... args) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)grid, 1, 1);
     cfg.blockDim = dim3((unsigned)threads, 1, 1);
+    cfg.dynamicSmemBytes = smem;
     cfg.stream = s;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -451,18 +987,27 @@ cudaError_t launch_pdl(K kern, int grid, int threads, cudaStream_t s, A... args)
 
 template <typename T>
 cudaError_t launch_t(const Q8MoeArgs &a, unsigned char *ws) {
-    cudaError_t e = launch_pdl(q8_route_kernel<T>, a.E + a.T, RTHREADS, a.stream, a.T, a.E, a.top_k, a.H, a.I,
-                               (const T *)a.x, a.ldx, a.router, a.ldr, ws);
+    // four elements at a time: one aligned access of each array, H a multiple of 4
+    const int vec = a.H % 4 == 0 && a.ldx % 4 == 0 && a.ldr % 4 == 0 &&
+                    reinterpret_cast<uintptr_t>(a.x) % (4 * sizeof(T)) == 0 &&
+                    reinterpret_cast<uintptr_t>(a.router) % 16 == 0;
+    cudaError_t e = launch_pdl(q8_route_kernel<T>, a.E + a.T, RTHREADS, 0, a.stream, a.T, a.E, a.top_k, a.H, a.I,
+                               (const T *)a.x, a.ldx, a.router, a.ldr, vec, ws);
     if (e != cudaSuccess) return e;
-    const bool vec = reinterpret_cast<uintptr_t>(a.w_up) % 16 == 0 && a.ldu % 16 == 0 &&
-                     reinterpret_cast<uintptr_t>(a.w_down) % 16 == 0 && a.ldd % 16 == 0;
+    if (reinterpret_cast<uintptr_t>(a.w_up) % 16 == 0 && reinterpret_cast<uintptr_t>(a.w_down) % 16 == 0) {
+        auto kern = a.ldu % 16 == 0 && a.ldd % 16 == 0 ? q8_expert_ring_kernel<T, false>
+                                                       : q8_expert_ring_kernel<T, true>;
+        e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)ESMEM);
+        if (e != cudaSuccess) return e;
+        return launch_pdl(kern, a.sm_count > 0 ? a.sm_count : 1, ETHREADS, ESMEM, a.stream, a.T, a.E, a.top_k, a.H,
+                          a.I, a.renormalize, a.w_up, a.ldu, a.s_up, a.w_down, a.ldd, a.s_down, (T *)a.out, a.ldo,
+                          a.ids, a.gates, ws, a.err, a.wait_ns);
+    }
     const int kw_up = warps_per_tile(a.H), kw_down = warps_per_tile(a.I);
-    // no more blocks than units: at most one chunk per pair and one per expert and 16 pairs
     const int grid = 2 * (a.sm_count > 0 ? a.sm_count : 1);
-    auto kern = vec ? q8_expert_kernel<T, true> : q8_expert_kernel<T, false>;
-    return launch_pdl(kern, grid, MTHREADS, a.stream, a.T, a.E, a.top_k, a.H, a.I, a.renormalize, a.w_up, a.ldu,
-                      a.s_up, a.w_down, a.ldd, a.s_down, (T *)a.out, a.ldo, a.ids, a.gates, ws, kw_up, kw_down,
-                      a.err, a.wait_ns);
+    return launch_pdl(q8_expert_kernel<T>, grid, MTHREADS, 0, a.stream, a.T, a.E, a.top_k, a.H, a.I, a.renormalize,
+                      a.w_up, a.ldu, a.s_up, a.w_down, a.ldd, a.s_down, (T *)a.out, a.ldo, a.ids, a.gates, ws, kw_up,
+                      kw_down, a.err, a.wait_ns);
 }
 
 }  // namespace

@@ -231,6 +231,25 @@ __device__ __forceinline__ void q8_step_s8(int (&sum)[4], const uint4 &wa, const
     mma_s8(sum, wa.z, wb.z, wa.w, wb.w, x.z, x.w);
 }
 
+// The same for NT single tokens without an MMA: sum[j][0], sum[j][1] take this
+// lane's 16 bytes of rows g and g + 8 times token j's; the four lanes of a quad
+// hold parts of one sum.  8 NT dp4a a step (half rate) against two 8-bit MMAs at
+// 17 cycles of the SM each: the cheaper way up to 4 tokens.
+template <int NT>
+__device__ __forceinline__ void q8_step_dp(int (&sum)[NT][2], const uint4 &wa, const uint4 &wb, const uint4 (&x)[NT]) {
+#pragma unroll
+    for (int j = 0; j < NT; ++j) {
+        sum[j][0] = __dp4a((int)wa.x, (int)x[j].x, sum[j][0]);
+        sum[j][1] = __dp4a((int)wb.x, (int)x[j].x, sum[j][1]);
+        sum[j][0] = __dp4a((int)wa.y, (int)x[j].y, sum[j][0]);
+        sum[j][1] = __dp4a((int)wb.y, (int)x[j].y, sum[j][1]);
+        sum[j][0] = __dp4a((int)wa.z, (int)x[j].z, sum[j][0]);
+        sum[j][1] = __dp4a((int)wb.z, (int)x[j].z, sum[j][1]);
+        sum[j][0] = __dp4a((int)wa.w, (int)x[j].w, sum[j][0]);
+        sum[j][1] = __dp4a((int)wb.w, (int)x[j].w, sum[j][1]);
+    }
+}
+
 // Bulk copy into shared memory: 16-byte aligned addresses and size.
 __device__ __forceinline__ void bulk_load(uint32_t dst, const void *src, uint32_t bytes, uint32_t bar) {
     asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
