@@ -56,6 +56,7 @@ struct Q8MoeArgs {
     unsigned *err;
     uint64_t wait_ns;
     int sm_count;
+    EncodeTiledFn encode;
 };
 
 cudaError_t launch_q8_rows(const Q8RowsArgs &a);

@@ -191,7 +191,7 @@ int sgemm_q8_moe(int64_t T, int64_t E, int64_t top_k, int64_t H, int64_t I, cons
     a.renormalize = renormalize != 0;
     a.out = out; a.ldo = ldo; a.ids = ids; a.gates = gates;
     a.stream = static_cast<cudaStream_t>(stream);
-    rc = device_args(&a.err, &a.wait_ns, &a.sm_count, nullptr);
+    rc = device_args(&a.err, &a.wait_ns, &a.sm_count, &a.encode);
     if (rc != SGEMM_OK) return rc;
     void *work = nullptr;
     rc = stream_workspace(q8_moe_workspace_bytes(a.T, a.E, a.top_k, a.H, a.I), a.stream, &work);

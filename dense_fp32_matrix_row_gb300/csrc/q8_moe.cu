@@ -51,7 +51,7 @@ struct MoeLayout {
         logits = take((size_t)T * E * 4);
         xs = take((size_t)T * 4);
         xq = take((size_t)T * Hp);
-        hidden = take((size_t)P * I * 4);
+        hidden = take((size_t)P * I * 4);    // rows of I floats: 16-byte aligned where I % 4 == 0
         hs = take((size_t)P * 4);
         hq = take((size_t)P * Ip);
         part = take((size_t)P * H * 4);
@@ -253,6 +253,7 @@ __device__ void moe_route(MoeShared &S, int ntok, int E, int top_k, int renorm, 
     const int P = ntok * top_k;
     for (int e = threadIdx.x; e < E; e += (int)blockDim.x) {
         int c = 0;
+#pragma unroll 8
         for (int p = 0; p < P; ++p) c += S.ids[p] == e;
         S.count[e] = c;
     }
@@ -284,6 +285,7 @@ __device__ void moe_route(MoeShared &S, int ntok, int E, int top_k, int renorm, 
     for (int e = threadIdx.x; e < E; e += (int)blockDim.x) {
         int at = S.first[e];
         if (S.count[e])
+#pragma unroll 8
             for (int p = 0; p < P; ++p)
                 if (S.ids[p] == e) S.list[at++] = (unsigned short)p;
         for (int c = 0; c * 16 < S.count[e]; ++c) {
@@ -490,8 +492,12 @@ q8_expert_kernel(int ntok, int E, int top_k, int H, int I, int renorm, const int
 // rows each), 33 to 70 KB: its chain of waits, token loads and hand-overs takes as
 // long as 33 KB do at the memory's rate, hence the groups, the finishers and the
 // size; larger units leave blocks idle at the end of a projection.
-// Rows whose length is no multiple of 16 (SHIFT) are copied from the 16-byte
-// boundary below and shifted as the fragments are read.
+// Eight rows of a stage are one TMA box of 8-byte elements, 2 KB a row at most:
+// as 16 bulk copies, a stage took its warp 2000 cycles to issue, 13 bytes a
+// cycle.  (Rows then lie a multiple of 512 bytes apart and the 128-bit reads of
+// a fragment meet a two-way bank conflict, which costs nothing here.)  Rows whose
+// length is no multiple of 16 (SHIFT) have no TMA map; they are copied one by one
+// from the 16-byte boundary below and shifted as the fragments are read.
 constexpr int FINISHERS = 2;                               // one per consumer group
 constexpr int E_PRODUCER = kQ8Consumers + FINISHERS;
 constexpr int ETHREADS = (E_PRODUCER + 1) * 32;
@@ -501,7 +507,7 @@ constexpr int ESTEPS = 4;                                  // steps per consumer
 constexpr int ETILES = 4;                                  // 16-row tiles of a unit, at most
 constexpr uint32_t ESTAGE = 64 * (8 * kQ8Step + 64 + 16);  // the largest geometry (RT = 4)
 constexpr int EPART = ETILES * 2 * 128;                    // one unit's sums: [tile][token block][word][lane]
-constexpr int QSEG = 1024;                                 // hidden values a quantising unit takes
+constexpr int QSEG = 512;                                  // hidden values a quantising unit takes
 constexpr int CSEG = 128;                                  // results an adding unit takes
 
 struct EGeom {       // one projection's division
@@ -520,7 +526,7 @@ struct EGeom {       // one projection's division
         const int64_t all = (int64_t)((rows + per_tile * rt - 1) / (per_tile * rt)) * chunks;
         sub = stages == 1 && rt <= 2 && all >= (int64_t)16 * blocks_of_grid ? 2 : 1;
         groups = (rows + per_tile * rt * sub - 1) / (per_tile * rt * sub);
-        ld = (uint32_t)(kb * kQ8Step + 64 + (shift ? 16 : 0));
+        ld = (uint32_t)(kb * kQ8Step + (shift ? 80 : 0));
     }
 };
 
@@ -560,9 +566,22 @@ __device__ __forceinline__ bool warp_poll(const uint32_t *p, uint32_t want, uint
     return ok != 0;
 }
 
+// The same for `count` <= 32 counters, one a lane.
+__device__ __forceinline__ bool warp_poll_all(const uint32_t *p, int count, uint32_t want, uint64_t wait_ns) {
+    const int lane = threadIdx.x & 31;
+    bool ok = lane >= count || ld_acquire(p + lane) >= want;
+    if (!ok) {
+        const uint64_t t0 = globaltimer_ns();
+        do {
+            ok = ld_acquire(p + lane) >= want;
+        } while (!ok && globaltimer_ns() - t0 <= wait_ns);
+    }
+    return __all_sync(0xffffffffu, ok) != 0;
+}
+
 template <typename T, bool SHIFT>
 __global__ void __launch_bounds__(ETHREADS, 1)
-q8_expert_ring_kernel(int ntok, int E, int top_k, int H, int I, int renorm, const int8_t *__restrict__ w_up,
+q8_expert_ring_kernel(const __grid_constant__ CUtensorMap map_up, const __grid_constant__ CUtensorMap map_down, int ntok, int E, int top_k, int H, int I, int renorm, const int8_t *__restrict__ w_up,
                       int64_t ldu, const float *__restrict__ s_up, const int8_t *__restrict__ w_down, int64_t ldd,
                       const float *__restrict__ s_down, T *__restrict__ out, int64_t ldo, int *__restrict__ ids,
                       float *__restrict__ gates, unsigned char *ws, unsigned *err, uint64_t wait_ns) {
@@ -595,6 +614,8 @@ q8_expert_ring_kernel(int ntok, int E, int top_k, int H, int I, int renorm, cons
     }
     for (int i = tid; i < EBUFS * EPART; i += ETHREADS) part[i] = 0;
     pdl_wait();
+    int next = 0;       // the producer's first unit, asked for before the routing
+    if (warp == E_PRODUCER && lane == 0) next = (int)atomicAdd(ticket, 1u);
     moe_route(R, ntok, E, top_k, renorm, reinterpret_cast<const float *>(ws + L.logits));   // ends with a barrier
     if (blockIdx.x == 0) {
         for (int p = tid; p < L.P; p += ETHREADS) {
@@ -620,7 +641,6 @@ q8_expert_ring_kernel(int ntok, int E, int top_k, int H, int I, int renorm, cons
             r = (int)(g % ERING);
             return g < (uint32_t)ERING || warp_wait(smem_u32(&S.empty[r]), (g / ERING - 1) & 1, wait_ns);
         };
-        int next = lane == 0 ? (int)atomicAdd(ticket, 1u) : 0;
         while (ok) {
             const int u = __shfl_sync(0xffffffffu, next, 0);
             if (lane == 0) next = (int)atomicAdd(ticket, 1u);   // on its way while this unit is brought
@@ -643,8 +663,30 @@ q8_expert_ring_kernel(int ntok, int E, int top_k, int H, int I, int renorm, cons
             const uint32_t ld = up ? gu.ld : gd.ld;
             const int v = up ? u : u - up_units - q_units;
             const int c = v / groups, grp = v - c * groups, e = R.chunk_e[c];
-            const int8_t *row0 = up ? w_up + (int64_t)e * 2 * I * ldu : w_down + (int64_t)e * H * ldd;
             for (int t = 0; t < sub && ok; ++t) {
+                if constexpr (!SHIFT) {
+                    // lane q brings rows 8 (q % 2) .. + 7 of row tile q / 2 (rows past the
+                    // projection's end are others' or zero; their results are dropped)
+                    const int tile = (grp * sub + t) * rt + (lane >> 1);
+                    const int row = up ? e * 2 * I + (lane & 1) * I + tile * 8 : e * H + tile * 16 + 8 * (lane & 1);
+                    for (int s = 0; s < stages; ++s, ++g) {
+                        int r;
+                        if (!(ok = slot(r))) break;
+                        const uint32_t bar = smem_u32(&S.full[r]);
+                        if (lane == 0) {
+                            S.unit[r] = u;
+                            if (blocks > 0) mbar_arrive_expect_tx(bar, 16u * rt * ld);
+                            else mbar_arrive(bar);
+                        }
+                        __syncwarp();
+                        if (lane < 2 * rt && blocks > 0)
+                            tma_load_2d(smem_u32(smem) + (uint32_t)r * ESTAGE + (uint32_t)lane * 8 * ld,
+                                        up ? &map_up : &map_down, bar, s * kb * (kQ8Step / 8), row);
+                        __syncwarp();
+                    }
+                    continue;
+                }
+                const int8_t *row0 = up ? w_up + (int64_t)e * 2 * I * ldu : w_down + (int64_t)e * H * ldd;
                 // this lane's rows of the stage (rows past the end read the last one)
                 const int8_t *row[2] = {nullptr, nullptr};
 #pragma unroll
@@ -699,6 +741,7 @@ q8_expert_ring_kernel(int ntok, int E, int top_k, int H, int I, int renorm, cons
     } else if (warp < kQ8Consumers) {
         const int g = lane >> 2, t4 = lane & 3;
         const int group = warp / EGROUP, cw = warp % EGROUP;
+        int open_chunk = -1;              // the chunk whose hidden rows were last seen complete
         uint32_t used = 0;
         bool ok = true;
         for (uint32_t count = 0;; ++count) {
@@ -728,7 +771,10 @@ q8_expert_ring_kernel(int ntok, int E, int top_k, int H, int I, int renorm, cons
                 const int c = v / groups, grp = v - c * groups;
                 const int e = R.chunk_e[c], at = R.chunk_at[c], n = R.chunk_n[c];
                 // down: the chunk's hidden rows are there in 8 bits
-                if (!up && !(ok = warp_poll(quantised + c, (uint32_t)(n * segs), wait_ns))) break;
+                if (!up && c != open_chunk) {
+                    if (!(ok = warp_poll(quantised + c, (uint32_t)(n * segs), wait_ns))) break;
+                    open_chunk = c;
+                }
                 const int tl = cw / kw, kpart = cw % kw;      // this warp's tile of a stage, its share of the steps
                 const int step0 = kpart * ESTEPS;
                 const int8_t *xbase = up ? xq : hq;
@@ -868,16 +914,27 @@ q8_expert_ring_kernel(int ntok, int E, int top_k, int H, int I, int renorm, cons
                     c = R.first_chunk[e] + (q - R.first[e]) / 16;
                 }
                 if (!(ok = warp_poll(ready + c, (uint32_t)gu.groups, wait_ns))) break;
-                const RowQuant rq(__ldcg(hmax + p));
                 const int lo = seg * QSEG, hi = min(lo + QSEG, L.Ip);
                 const float *hr = hidden + (int64_t)p * I;
                 int8_t *qr = hq + (int64_t)p * L.Ip;
-#pragma unroll 4
-                for (int i = lo + 4 * lane; i < hi; i += 4 * 32) {
-                    float h4[4];
+                float h4[QSEG / 128][4];        // all loads at once
 #pragma unroll
-                    for (int k = 0; k < 4; ++k) h4[k] = i + k < I ? __ldcg(hr + i + k) : 0.0f;
-                    *reinterpret_cast<uint32_t *>(qr + i) = pack4(rq(h4[0]), rq(h4[1]), rq(h4[2]), rq(h4[3]));
+                for (int q4 = 0; q4 < QSEG / 128; ++q4) {
+                    const int i = lo + 128 * q4 + 4 * lane;
+                    if (I % 4 == 0 && i < I) {
+                        const float4 v4 = __ldcg(reinterpret_cast<const float4 *>(hr + i));
+                        h4[q4][0] = v4.x; h4[q4][1] = v4.y; h4[q4][2] = v4.z; h4[q4][3] = v4.w;
+                    } else {
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) h4[q4][k] = i + k < I ? __ldcg(hr + i + k) : 0.0f;
+                    }
+                }
+                const RowQuant rq(__ldcg(hmax + p));
+#pragma unroll
+                for (int q4 = 0; q4 < QSEG / 128; ++q4) {
+                    const int i = lo + 128 * q4 + 4 * lane;
+                    if (i < hi)
+                        *reinterpret_cast<uint32_t *>(qr + i) = pack4(rq(h4[q4][0]), rq(h4[q4][1]), rq(h4[q4][2]), rq(h4[q4][3]));
                 }
                 if (seg == 0 && lane == 0) hs[p] = rq.step * rq.unpre;
                 __threadfence();
@@ -889,8 +946,7 @@ q8_expert_ring_kernel(int ntok, int E, int top_k, int H, int I, int renorm, cons
                 if (lane == 0) mbar_arrive(smem_u32(&S.bempty[b]));
                 const int v = u - down_end_unit, t = v / csegs, c0 = (v - t * csegs) * CSEG;
                 const int cols = 16 * gd.rt * gd.sub, g0 = c0 / cols, g1 = (min(c0 + CSEG, H) - 1) / cols;
-                for (int q = g0; q <= g1 && ok; ++q) ok = warp_poll(done + q, (uint32_t)R.nchunks, wait_ns);
-                if (!ok) break;
+                if (!(ok = warp_poll_all(done + g0, g1 - g0 + 1, (uint32_t)R.nchunks, wait_ns))) break;
                 const int col = c0 + 4 * lane;
                 float y[4] = {0.0f, 0.0f, 0.0f, 0.0f};
                 const float *rr = res + (int64_t)t * top_k * H + col;
@@ -962,6 +1018,20 @@ q8_expert_ring_kernel(int ntok, int E, int top_k, int H, int I, int renorm, cons
     }
 }
 
+// Map of rows of `K` bytes in 8-byte elements, for boxes of 8 rows as long as a
+// stage is deep (K >= 64).
+bool encode_rows8(EncodeTiledFn enc, CUtensorMap *map, const int8_t *base, int K, int64_t rows, int64_t ld) {
+    if (enc == nullptr) return false;
+    const EGeom g(K, 1, 1, false, 1, 1);
+    const cuuint64_t dims[2] = {(cuuint64_t)(K / 8), (cuuint64_t)rows};
+    const cuuint64_t strides[1] = {(cuuint64_t)ld};
+    const cuuint32_t box[2] = {(cuuint32_t)(g.kb * kQ8Step / 8), 8};
+    const cuuint32_t estr[2] = {1, 1};
+    return enc(map, CU_TENSOR_MAP_DATA_TYPE_FLOAT64, 2, const_cast<int8_t *>(base), dims, strides, box, estr,
+               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 // Warps that share one 16-row tile's K: at least 4 steps each.
 int warps_per_tile(int K) {
     const int steps = (K + kQ8Step - 1) / kQ8Step;
@@ -999,7 +1069,12 @@ cudaError_t launch_t(const Q8MoeArgs &a, unsigned char *ws) {
                                                        : q8_expert_ring_kernel<T, true>;
         e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)ESMEM);
         if (e != cudaSuccess) return e;
-        return launch_pdl(kern, a.sm_count > 0 ? a.sm_count : 1, ETHREADS, ESMEM, a.stream, a.T, a.E, a.top_k, a.H,
+        alignas(64) CUtensorMap up = {}, down = {};
+        if (a.ldu % 16 == 0 && a.ldd % 16 == 0 &&
+            ((a.H >= kQ8Step && !encode_rows8(a.encode, &up, a.w_up, a.H, (int64_t)a.E * 2 * a.I, a.ldu)) ||
+             (a.I >= kQ8Step && !encode_rows8(a.encode, &down, a.w_down, a.I, (int64_t)a.E * a.H, a.ldd))))
+            return cudaErrorInvalidValue;
+        return launch_pdl(kern, a.sm_count > 0 ? a.sm_count : 1, ETHREADS, ESMEM, a.stream, up, down, a.T, a.E, a.top_k, a.H,
                           a.I, a.renormalize, a.w_up, a.ldu, a.s_up, a.w_down, a.ldd, a.s_down, (T *)a.out, a.ldo,
                           a.ids, a.gates, ws, a.err, a.wait_ns);
     }
