@@ -501,7 +501,7 @@ q8_expert_kernel(int ntok, int E, int top_k, int H, int I, int renorm, const int
 constexpr int FINISHERS = 2;                               // one per consumer group
 constexpr int E_PRODUCER = kQ8Consumers + FINISHERS;
 constexpr int ETHREADS = (E_PRODUCER + 1) * 32;
-constexpr int ERING = 5, EBUFS = 4;                        // stages; buffers of sums, two per group
+constexpr int ERING = 4, EBUFS = 4;                        // stages; buffers of sums, two per group
 constexpr int EGROUP = kQ8Consumers / 2;                   // warps of a consumer group
 constexpr int ESTEPS = 4;                                  // steps per consumer warp and stage
 constexpr int ETILES = 4;                                  // 16-row tiles of a unit, at most
@@ -513,6 +513,7 @@ constexpr int CSEG = 128;                                  // results an adding 
 struct EGeom {       // one projection's division
     int K, rt, kw, kb, blocks, stages, sub, groups;
     uint32_t ld;
+    EGeom() = default;
     // `rows` results, `per_tile` of them to a tile; `experts` of them are wanted at most
     __host__ __device__ EGeom(int K_, int rows, int per_tile, bool shift, int chunks, int blocks_of_grid) : K(K_) {
         const int steps = (K + kQ8Step - 1) / kQ8Step;
@@ -530,8 +531,36 @@ struct EGeom {       // one projection's division
     }
 };
 
+// What the roles work on; in shared memory, so that none of it occupies the
+// registers of a role that does not need it (what they spill comes back from L2:
+// next to 200 KB of shared memory L1 is small).
+struct EArgs {
+    const int8_t *w_up, *w_down;
+    int64_t ldu, ldd;
+    const float *s_up, *s_down;
+    void *out;
+    int64_t ldo;
+    const float *xs;
+    const int8_t *xq;
+    float *hidden, *hs, *res;
+    int8_t *hq;
+    uint32_t *ticket, *ready, *quantised, *hmax, *done;
+    unsigned *err;
+    uint64_t wait_ns;
+    int ntok, top_k, H, I, Hp, Ip;
+    int segs, csegs;                          // quantising units of a pair, adding units of a token
+    int up_units, quant_end, down_end, units; // units: gate/up, quantise, down, add
+
+    // what unit u does: 0 gate/up, 1 quantise, 2 down, 3 add, -1 nothing (the end)
+    __device__ __forceinline__ int kind(int u) const {
+        return u < up_units ? 0 : u < quant_end ? 1 : u < down_end ? 2 : u < units ? 3 : -1;
+    }
+};
+
 struct EShared {
     MoeShared route;
+    EArgs a;
+    EGeom geom[2];                    // gate/up, down
     int unit[ERING];                  // unit a stage belongs to
     int done[EBUFS];                  // unit a buffer of sums belongs to
     uint64_t full[ERING], empty[ERING], bfull[EBUFS], bempty[EBUFS];
@@ -579,27 +608,418 @@ __device__ __forceinline__ bool warp_poll_all(const uint32_t *p, int count, uint
     return __all_sync(0xffffffffu, ok) != 0;
 }
 
+// The products of one unit by one warp of a consumer group, into the buffer
+// `sums`; false when a wait ran out.  DP: NT tokens by dp4a, each lane with every
+// token's bytes; otherwise NT blocks of 8 tokens by MMA, lane row g with token g
+// of each.
+template <int NT, bool DP, bool SHIFT>
+__device__ __forceinline__ bool unit_products(EShared &S, uint32_t ring, int *sums, int c, int grp, bool up,
+                                           uint32_t used) {
+    const EArgs &A = S.a;
+    const MoeShared &R = S.route;
+    const EGeom &G = S.geom[up ? 0 : 1];
+    const int lane = threadIdx.x & 31, cw = (int)(threadIdx.x >> 5) % EGROUP;
+    const int g = lane >> 2, t4 = lane & 3;
+    const int kb = G.kb, blocks = G.blocks, stages = G.stages, sub = G.sub, rt = G.rt;
+    const uint32_t ld = G.ld;
+    const int tl = cw / G.kw, kpart = cw % G.kw;      // this warp's tile of a stage, its share of the steps
+    const int step0 = kpart * ESTEPS;
+    const int8_t *x[NT];
+#pragma unroll
+    for (int j = 0; j < NT; ++j) {                    // tokens past the chunk's end: the last one
+        const int p = R.list[R.chunk_at[c] + min(DP ? j : 8 * j + g, (int)R.chunk_n[c] - 1)];
+        x[j] = (up ? A.xq + (int64_t)(p / A.top_k) * A.Hp : A.hq + (int64_t)p * A.Ip) + 16 * t4;
+    }
+    for (int t = 0; t < sub; ++t) {
+        // the two weight rows of this lane
+        const int tile = (grp * sub + t) * rt + tl, e = R.chunk_e[c];
+        const int8_t *wa, *wb;
+        if (up) {
+            wa = A.w_up + ((int64_t)e * 2 * A.I + min(tile * 8 + g, A.I - 1)) * A.ldu;
+            wb = wa + (int64_t)A.I * A.ldu;
+        } else {
+            wa = A.w_down + ((int64_t)e * A.H + min(tile * 16 + g, A.H - 1)) * A.ldd;
+            wb = A.w_down + ((int64_t)e * A.H + min(tile * 16 + g + 8, A.H - 1)) * A.ldd;
+        }
+        // and where they lie in a stage
+        uint32_t oa = (uint32_t)(tl * 16 + g) * ld + (uint32_t)(step0 * kQ8Step + 16 * t4), ob = oa + 8 * ld;
+        if (SHIFT) {
+            oa += (uint32_t)(reinterpret_cast<uintptr_t>(wa) & 15);
+            ob += (uint32_t)(reinterpret_cast<uintptr_t>(wb) & 15);
+        }
+        int sum[NT][DP ? 2 : 4];
+#pragma unroll
+        for (int j = 0; j < NT; ++j)
+#pragma unroll
+            for (int i = 0; i < (DP ? 2 : 4); ++i) sum[j][i] = 0;
+        auto step = [&](const uint4 &a, const uint4 &d, const uint4 (&xv)[NT]) {
+            if constexpr (DP) {
+                q8_step_dp<NT>(sum, a, d, xv);
+            } else {
+#pragma unroll
+                for (int j = 0; j < NT; ++j) q8_step_s8(sum[j], a, d, xv[j]);
+            }
+        };
+        for (int s = 0; s < stages; ++s, ++used) {
+            const int r = (int)(used % ERING);
+            const int first = s * kb + step0;
+            const int here = min(ESTEPS, blocks - first);    // this warp's steps of the stage
+            // The tokens of a batch of steps are asked for together, the first ahead of
+            // the wait for the weights.  (A step past the last reads the last one's
+            // tokens and is not used.)
+            constexpr int BATCH = NT <= 2 ? ESTEPS : ESTEPS / 2;
+            uint4 xv[BATCH][NT];
+            auto xload = [&](int k0) {
+#pragma unroll
+                for (int k = 0; k < BATCH; ++k)
+#pragma unroll
+                    for (int j = 0; j < NT; ++j)
+                        xv[k][j] = *reinterpret_cast<const uint4 *>(x[j] + (int64_t)max(0, min(first + k0 + k, blocks - 1)) * kQ8Step);
+            };
+            xload(0);
+            if (s + t > 0 && !warp_wait(smem_u32(&S.full[r]), (used / ERING) & 1, A.wait_ns)) return false;
+            const uint32_t stage = ring + (uint32_t)r * ESTAGE;
+#pragma unroll
+            for (int k0 = 0; k0 < ESTEPS; k0 += BATCH) {
+                if (k0 > 0) xload(k0);
+#pragma unroll
+                for (int k = 0; k < BATCH; ++k)
+                    if (k0 + k < here) {
+                        const uint32_t o = stage + (uint32_t)(k0 + k) * kQ8Step;
+                        step(SHIFT ? lds_shifted(o + oa) : lds128(o + oa), SHIFT ? lds_shifted(o + ob) : lds128(o + ob), xv[k]);
+                    }
+            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(smem_u32(&S.empty[r]));
+        }
+        if (kpart == 0)
+            for (int k0 = blocks * kQ8Step; k0 < G.K; k0 += kQ8Step) {   // the rows' last values
+                const int valid = min(16, max(0, G.K - k0 - 16 * t4));
+                uint4 xv[NT];
+#pragma unroll
+                for (int j = 0; j < NT; ++j) xv[j] = *reinterpret_cast<const uint4 *>(x[j] + k0);
+                step(load16_bytes(wa + k0 + 16 * t4, valid), load16_bytes(wb + k0 + 16 * t4, valid), xv);
+            }
+        // whole numbers: the order of these additions does not matter
+        int *to = sums + (t * rt + tl) * 256;
+        if constexpr (DP) {
+#pragma unroll
+            for (int j = 0; j < NT; ++j)
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    int v2 = sum[j][i];
+                    v2 += __shfl_xor_sync(0xffffffffu, v2, 1);
+                    v2 += __shfl_xor_sync(0xffffffffu, v2, 2);
+                    // one lane of the quad: where the MMA would leave (row, token j)
+                    if (t4 == (j >> 1)) atomicAdd(to + (2 * i + (j & 1)) * 32 + lane, v2);
+                }
+        } else {
+#pragma unroll
+            for (int j = 0; j < NT; ++j)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) atomicAdd(to + j * 128 + 32 * i + lane, sum[j][i]);
+        }
+    }
+    return true;
+}
+
+template <bool SHIFT>
+__device__ __noinline__ void produce(EShared &S, uint32_t ring, const CUtensorMap *map_up,
+                                     const CUtensorMap *map_down, int next) {
+    const EArgs &A = S.a;
+    const int lane = threadIdx.x & 31;
+    bool ok = true;
+    uint32_t g = 0;
+    auto slot = [&](int &r) {
+        r = (int)(g % ERING);
+        return g < (uint32_t)ERING || warp_wait(smem_u32(&S.empty[r]), (g / ERING - 1) & 1, A.wait_ns);
+    };
+    while (ok) {
+        const int u = __shfl_sync(0xffffffffu, next, 0);
+        if (lane == 0) next = (int)atomicAdd(A.ticket, 1u);   // on its way while this unit is brought
+        const int kind = A.kind(u);
+        if (kind & 1) {      // nothing to bring: a finisher's unit, or the end
+            int r;
+            if (!(ok = slot(r))) break;
+            if (lane == 0) {
+                S.unit[r] = u;
+                mbar_arrive(smem_u32(&S.full[r]));
+            }
+            ++g;
+            if (kind < 0) break;
+            continue;
+        }
+        const bool up = kind == 0;
+        const EGeom &G = S.geom[up ? 0 : 1];
+        const int v = up ? u : u - A.quant_end;
+        const int c = v / G.groups, grp = v - c * G.groups, e = S.route.chunk_e[c];
+        const int rt = G.rt, stages = G.stages, kb = G.kb, blocks = G.blocks;
+        const uint32_t ld = G.ld;
+        for (int t = 0; t < G.sub && ok; ++t) {
+            const int tile0 = (grp * G.sub + t) * rt;
+            for (int s = 0; s < stages; ++s, ++g) {
+                int r;
+                if (!(ok = slot(r))) break;
+                const uint32_t bar = smem_u32(&S.full[r]), base = ring + (uint32_t)r * ESTAGE;
+                if constexpr (!SHIFT) {
+                    // lane q brings rows 8 (q % 2) .. + 7 of row tile q / 2 (rows past the
+                    // projection's end are others' or zero; their results are dropped)
+                    const int tile = tile0 + (lane >> 1);
+                    const int row = up ? e * 2 * A.I + (lane & 1) * A.I + tile * 8 : e * A.H + tile * 16 + 8 * (lane & 1);
+                    if (lane == 0) {
+                        S.unit[r] = u;
+                        if (blocks > 0) mbar_arrive_expect_tx(bar, 16u * rt * ld);
+                        else mbar_arrive(bar);
+                    }
+                    __syncwarp();
+                    if (lane < 2 * rt && blocks > 0)
+                        tma_load_2d(base + (uint32_t)lane * 8 * ld, up ? map_up : map_down, bar, s * kb * (kQ8Step / 8), row);
+                } else {
+                    const int len = max(0, min(kb, blocks - s * kb)) * kQ8Step;
+                    const int8_t *src[2];
+                    uint32_t bytes[2], total = 0;
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        const int q = lane + 32 * h, tile = tile0 + (q >> 4);
+                        bytes[h] = 0;
+                        src[h] = nullptr;
+                        if (q < 16 * rt && len > 0) {   // rows past the end read the last one
+                            const int64_t row = up ? (int64_t)e * 2 * A.I + min(tile * 8 + (q & 7), A.I - 1) + ((q >> 3) & 1) * A.I
+                                                   : (int64_t)e * A.H + min(tile * 16 + (q & 15), A.H - 1);
+                            src[h] = (up ? A.w_up + row * A.ldu : A.w_down + row * A.ldd) + (int64_t)s * kb * kQ8Step;
+                            const uint32_t off = (uint32_t)(reinterpret_cast<uintptr_t>(src[h]) & 15);
+                            src[h] -= off;
+                            bytes[h] = ((uint32_t)len + off + 15) / 16 * 16;
+                            total += bytes[h];
+                        }
+                    }
+                    total = __reduce_add_sync(0xffffffffu, total);
+                    if (lane == 0) {
+                        S.unit[r] = u;
+                        if (total > 0) mbar_arrive_expect_tx(bar, total);
+                        else mbar_arrive(bar);
+                    }
+                    __syncwarp();
+#pragma unroll
+                    for (int h = 0; h < 2; ++h)
+                        if (bytes[h] > 0) bulk_load(base + (uint32_t)(lane + 32 * h) * ld, src[h], bytes[h], bar);
+                }
+                __syncwarp();
+            }
+        }
+    }
+    if (!ok && lane == 0) {
+        record_error(A.err, kErrWaitTimeout);
+        for (uint32_t q = g > (uint32_t)ERING ? g - ERING : 0; q < g; ++q)
+            mbar_wait(smem_u32(&S.full[q % ERING]), (q / ERING) & 1, 1000000000ull);
+    }
+}
+
+template <bool SHIFT>
+__device__ __noinline__ void consume(EShared &S, uint32_t ring, int *part) {
+    const EArgs &A = S.a;
+    const MoeShared &R = S.route;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int group = warp / EGROUP, cw = warp % EGROUP;
+    int open_chunk = -1;              // the chunk whose hidden rows were last seen complete
+    uint32_t used = 0;
+    bool ok = true;
+    for (uint32_t count = 0;; ++count) {
+        int r = (int)(used % ERING);
+        if (!(ok = warp_wait(smem_u32(&S.full[r]), (used / ERING) & 1, A.wait_ns))) break;
+        const int u = S.unit[r];
+        const int kind = A.kind(u);
+        const bool mine = (int)(count & 1) == group, up = kind == 0;
+        const EGeom &G = S.geom[up ? 0 : 1];
+        if (!mine || (kind & 1)) {     // the other group's unit, or one without weights
+            const int all = (kind & 1) ? 1 : G.stages * G.sub;
+            for (int s = 0; s < all; ++s, ++used) {
+                r = (int)(used % ERING);
+                if (s > 0 && !(ok = warp_wait(smem_u32(&S.full[r]), (used / ERING) & 1, A.wait_ns))) break;
+                __syncwarp();
+                if (lane == 0) mbar_arrive(smem_u32(&S.empty[r]));
+            }
+            if (!ok) break;
+            if (!mine && kind >= 0) continue;
+        } else {
+            const int b = (int)(count % EBUFS);
+            const int v = up ? u : u - A.quant_end;
+            const int c = v / G.groups, grp = v - c * G.groups, n = R.chunk_n[c];
+            // down: the chunk's hidden rows are there in 8 bits
+            if (!up && c != open_chunk) {
+                if (!(ok = warp_poll(A.quantised + c, (uint32_t)(n * A.segs), A.wait_ns))) break;
+                open_chunk = c;
+            }
+            // the buffer is free (its finisher has read and cleared it)
+            if (count >= (uint32_t)EBUFS &&
+                !(ok = warp_wait(smem_u32(&S.bempty[b]), (count / EBUFS - 1) & 1, A.wait_ns)))
+                break;
+            int *sums = part + b * EPART;
+            if (n == 1) ok = unit_products<1, true, SHIFT>(S, ring, sums, c, grp, up, used);
+            else if (n == 2) ok = unit_products<2, true, SHIFT>(S, ring, sums, c, grp, up, used);
+            else if (n <= 4) ok = unit_products<4, true, SHIFT>(S, ring, sums, c, grp, up, used);
+            else if (n <= 8) ok = unit_products<1, false, SHIFT>(S, ring, sums, c, grp, up, used);
+            else ok = unit_products<2, false, SHIFT>(S, ring, sums, c, grp, up, used);
+            if (!ok) break;
+            used += (uint32_t)(G.stages * G.sub);
+        }
+        // hand the sums over; the end goes to every finisher, each group telling
+        // the one whose buffers it fills (it alone knows their turn)
+        const uint32_t last = kind >= 0 ? count : count + 1;
+        for (uint32_t q = count; q <= last; ++q) {
+            if ((int)(q & 1) != group) continue;
+            const int o = (int)(q % EBUFS);
+            if ((kind & 1) && q >= (uint32_t)EBUFS &&
+                !(ok = warp_wait(smem_u32(&S.bempty[o]), (q / EBUFS - 1) & 1, A.wait_ns)))
+                break;
+            if (cw == 0 && lane == 0) S.done[o] = u;
+            __syncwarp();
+            if (lane == 0) mbar_arrive(smem_u32(&S.bfull[o]));
+        }
+        if (!ok || kind < 0) break;
+    }
+    if (!ok && lane == 0) record_error(A.err, kErrWaitTimeout);
+}
+
+template <typename T>
+__device__ __noinline__ void finish(EShared &S, int *part) {
+    const EArgs &A = S.a;
+    const MoeShared &R = S.route;
+    const int lane = threadIdx.x & 31;
+    const int H = A.H, I = A.I, top_k = A.top_k;
+    bool ok = true;
+    for (uint32_t count = (threadIdx.x >> 5) - kQ8Consumers;; count += FINISHERS) {
+        const int b = (int)(count % EBUFS);       // one of this finisher's buffers
+        if (!(ok = warp_wait(smem_u32(&S.bfull[b]), (count / EBUFS) & 1, A.wait_ns))) break;
+        const int u = S.done[b];
+        const int kind = A.kind(u);
+        if (kind < 0) break;
+        int *sums = part + b * EPART;
+        auto sum_at = [&](int tile, int row, int tok) {
+            return sums[tile * 256 + (tok >> 3) * 128 + (((row >> 3) << 1) + (tok & 1)) * 32 + (row & 7) * 4 + ((tok & 7) >> 1)];
+        };
+        if (kind & 1) {
+            __syncwarp();
+            if (lane == 0) mbar_arrive(smem_u32(&S.bempty[b]));
+        }
+        if (kind == 1) {
+            const int v = u - A.up_units, q = v / A.segs, seg = v - q * A.segs;
+            const int p = R.list[q];            // pairs in the order of their chunks
+            const int e = R.ids[p], c = R.first_chunk[e] + (q - R.first[e]) / 16;
+            if (!(ok = warp_poll(A.ready + c, (uint32_t)S.geom[0].groups, A.wait_ns))) break;
+            const int lo = seg * QSEG, hi = min(lo + QSEG, A.Ip);
+            const float *hr = A.hidden + (int64_t)p * I;
+            int8_t *qr = A.hq + (int64_t)p * A.Ip;
+            float h4[QSEG / 128][4];        // all loads at once
+#pragma unroll
+            for (int q4 = 0; q4 < QSEG / 128; ++q4) {
+                const int i = lo + 128 * q4 + 4 * lane;
+                if (I % 4 == 0 && i < I) {
+                    const float4 v4 = __ldcg(reinterpret_cast<const float4 *>(hr + i));
+                    h4[q4][0] = v4.x; h4[q4][1] = v4.y; h4[q4][2] = v4.z; h4[q4][3] = v4.w;
+                } else {
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) h4[q4][k] = i + k < I ? __ldcg(hr + i + k) : 0.0f;
+                }
+            }
+            const RowQuant rq(__ldcg(A.hmax + p));
+#pragma unroll
+            for (int q4 = 0; q4 < QSEG / 128; ++q4) {
+                const int i = lo + 128 * q4 + 4 * lane;
+                if (i < hi)
+                    *reinterpret_cast<uint32_t *>(qr + i) = pack4(rq(h4[q4][0]), rq(h4[q4][1]), rq(h4[q4][2]), rq(h4[q4][3]));
+            }
+            if (seg == 0 && lane == 0) A.hs[p] = rq.step * rq.unpre;
+            __threadfence();
+            __syncwarp();
+            if (lane == 0) atomicAdd(A.quantised + c, 1u);
+            continue;
+        }
+        if (kind == 3) {      // one token's sum over its experts, in slot order
+            const int v = u - A.down_end, t = v / A.csegs, c0 = (v - t * A.csegs) * CSEG;
+            const int cols = 16 * S.geom[1].rt * S.geom[1].sub, g0 = c0 / cols, g1 = (min(c0 + CSEG, H) - 1) / cols;
+            if (!(ok = warp_poll_all(A.done + g0, g1 - g0 + 1, (uint32_t)R.nchunks, A.wait_ns))) break;
+            const int col = c0 + 4 * lane;
+            float y[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+            const float *rr = A.res + (int64_t)t * top_k * H + col;
+#pragma unroll 4
+            for (int j = 0; j < top_k; ++j) {
+                float w4[4];
+#pragma unroll
+                for (int k = 0; k < 4; ++k) w4[k] = col + k < H ? __ldcg(rr + (int64_t)j * H + k) : 0.0f;
+#pragma unroll
+                for (int k = 0; k < 4; ++k) y[k] = fmaf(R.gates[t * top_k + j], w4[k], y[k]);
+            }
+            T *o = static_cast<T *>(A.out) + (int64_t)t * A.ldo + col;
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+                if (col + k < H) o[k] = from_f32<T>(y[k]);
+            continue;
+        }
+        const bool up = kind == 0;
+        const EGeom &G = S.geom[up ? 0 : 1];
+        const int tiles = G.rt * G.sub;     // of the unit
+        const int v = up ? u : u - A.quant_end;
+        const int c = v / G.groups, grp = v - c * G.groups;
+        const int e = R.chunk_e[c], at = R.chunk_at[c], n = R.chunk_n[c];
+        if (up) {
+            for (int o0 = 0; o0 < 8 * tiles * n; o0 += 32) {
+                const int o = o0 + lane, row = o & 7, tl = (o >> 3) % tiles, j = (o >> 3) / tiles;
+                const int i = (grp * tiles + tl) * 8 + row;
+                uint32_t mb = 0;
+                int p = 0;
+                if (j < n && i < I) {
+                    p = R.list[at + j];
+                    const float s = __ldg(A.xs + p / top_k);
+                    const float sg = __ldg(A.s_up + (int64_t)e * 2 * I + i), su = __ldg(A.s_up + (int64_t)e * 2 * I + I + i);
+                    const float gv = (float)sum_at(tl, row, j) * s * sg;
+                    const float uv = (float)sum_at(tl, row + 8, j) * s * su;
+                    const float hv = __fdiv_rn(gv, 1.0f + expf(-gv)) * uv;
+                    __stcg(A.hidden + (int64_t)p * I + i, hv);
+                    mb = abs_bits(hv);
+                }
+#pragma unroll
+                for (int d = 1; d < 8; d <<= 1) mb = max(mb, __shfl_xor_sync(0xffffffffu, mb, d));
+                if (row == 0 && j < n && mb != 0u) atomicMax(A.hmax + p, mb);
+            }
+        } else {
+            for (int o = lane; o < 16 * tiles * n; o += 32) {
+                const int row = o & 15, tl = (o >> 4) % tiles, j = (o >> 4) / tiles;
+                const int col = (grp * tiles + tl) * 16 + row;
+                if (col < H) {
+                    const int p = R.list[at + j];
+                    __stcg(A.res + (int64_t)p * H + col,
+                           (float)sum_at(tl, row, j) * __ldcg(A.hs + p) * __ldg(A.s_down + (int64_t)e * H + col));
+                }
+            }
+        }
+        // the sums have been read: the buffer goes back empty
+        __syncwarp();
+        for (int i = lane; i < tiles * 64; i += 32) reinterpret_cast<int4 *>(sums)[i] = make_int4(0, 0, 0, 0);
+        __threadfence();
+        __syncwarp();
+        if (lane == 0) {
+            mbar_arrive(smem_u32(&S.bempty[b]));
+            atomicAdd(up ? A.ready + c : A.done + grp, 1u);
+        }
+    }
+    if (!ok && lane == 0) record_error(A.err, kErrWaitTimeout);
+}
+
 template <typename T, bool SHIFT>
 __global__ void __launch_bounds__(ETHREADS, 1)
-q8_expert_ring_kernel(const __grid_constant__ CUtensorMap map_up, const __grid_constant__ CUtensorMap map_down, int ntok, int E, int top_k, int H, int I, int renorm, const int8_t *__restrict__ w_up,
-                      int64_t ldu, const float *__restrict__ s_up, const int8_t *__restrict__ w_down, int64_t ldd,
-                      const float *__restrict__ s_down, T *__restrict__ out, int64_t ldo, int *__restrict__ ids,
-                      float *__restrict__ gates, unsigned char *ws, unsigned *err, uint64_t wait_ns) {
+q8_expert_ring_kernel(const __grid_constant__ CUtensorMap map_up, const __grid_constant__ CUtensorMap map_down,
+                      int ntok, int E, int top_k, int H, int I, int renorm, const int8_t *w_up, int64_t ldu,
+                      const float *s_up, const int8_t *w_down, int64_t ldd, const float *s_down, T *out, int64_t ldo,
+                      int *__restrict__ ids, float *__restrict__ gates, unsigned char *ws, unsigned *err,
+                      uint64_t wait_ns) {
     extern __shared__ unsigned char smem_raw[];
     unsigned char *smem = reinterpret_cast<unsigned char *>((reinterpret_cast<uintptr_t>(smem_raw) + 127) & ~uintptr_t(127));
     int *part = reinterpret_cast<int *>(smem + EOFF_PART);
     EShared &S = *reinterpret_cast<EShared *>(smem + EOFF_SHARED);
     MoeShared &R = S.route;
-    const MoeLayout L(ntok, E, top_k, H, I);
-    const float *xs = reinterpret_cast<const float *>(ws + L.xs);
-    const int8_t *xq = reinterpret_cast<const int8_t *>(ws + L.xq);
-    float *hidden = reinterpret_cast<float *>(ws + L.hidden);
-    float *hs = reinterpret_cast<float *>(ws + L.hs);
-    int8_t *hq = reinterpret_cast<int8_t *>(ws + L.hq);
-    float *res = reinterpret_cast<float *>(ws + L.part);
-    uint32_t *ticket = reinterpret_cast<uint32_t *>(ws + L.zero);
-    uint32_t *ready = ticket + 1, *quantised = ready + L.P, *hmax = quantised + L.P, *done = hmax + L.P;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const MoeLayout L(ntok, E, top_k, H, I);
 
     if (tid == 0) {
         for (int s = 0; s < ERING; ++s) {
@@ -614,408 +1034,46 @@ q8_expert_ring_kernel(const __grid_constant__ CUtensorMap map_up, const __grid_c
     }
     for (int i = tid; i < EBUFS * EPART; i += ETHREADS) part[i] = 0;
     pdl_wait();
+    uint32_t *ticket = reinterpret_cast<uint32_t *>(ws + L.zero);
     int next = 0;       // the producer's first unit, asked for before the routing
     if (warp == E_PRODUCER && lane == 0) next = (int)atomicAdd(ticket, 1u);
     moe_route(R, ntok, E, top_k, renorm, reinterpret_cast<const float *>(ws + L.logits));   // ends with a barrier
+    if (tid == 0) {
+        EArgs &A = S.a;
+        A.w_up = w_up; A.w_down = w_down; A.ldu = ldu; A.ldd = ldd; A.s_up = s_up; A.s_down = s_down;
+        A.out = out; A.ldo = ldo;
+        A.xs = reinterpret_cast<const float *>(ws + L.xs);
+        A.xq = reinterpret_cast<const int8_t *>(ws + L.xq);
+        A.hidden = reinterpret_cast<float *>(ws + L.hidden);
+        A.hs = reinterpret_cast<float *>(ws + L.hs);
+        A.hq = reinterpret_cast<int8_t *>(ws + L.hq);
+        A.res = reinterpret_cast<float *>(ws + L.part);
+        A.ticket = ticket;
+        A.ready = ticket + 1;
+        A.quantised = A.ready + L.P;
+        A.hmax = A.quantised + L.P;
+        A.done = A.hmax + L.P;
+        A.err = err; A.wait_ns = wait_ns;
+        A.ntok = ntok; A.top_k = top_k; A.H = H; A.I = I; A.Hp = L.Hp; A.Ip = L.Ip;
+        S.geom[0] = EGeom(H, I, 8, SHIFT, R.nchunks, (int)gridDim.x);
+        S.geom[1] = EGeom(I, H, 16, SHIFT, R.nchunks, (int)gridDim.x);
+        A.segs = (L.Ip + QSEG - 1) / QSEG;
+        A.csegs = (H + CSEG - 1) / CSEG;
+        A.up_units = R.nchunks * S.geom[0].groups;
+        A.quant_end = A.up_units + L.P * A.segs;
+        A.down_end = A.quant_end + R.nchunks * S.geom[1].groups;
+        A.units = A.down_end + ntok * A.csegs;
+    }
     if (blockIdx.x == 0) {
         for (int p = tid; p < L.P; p += ETHREADS) {
             if (ids) ids[p] = R.ids[p];
             if (gates) gates[p] = R.gates[p];
         }
     }
-    const EGeom gu(H, I, 8, SHIFT, R.nchunks, (int)gridDim.x), gd(I, H, 16, SHIFT, R.nchunks, (int)gridDim.x);
-    const int segs = (L.Ip + QSEG - 1) / QSEG;                 // quantising units of one pair
-    const int up_units = R.nchunks * gu.groups, q_units = L.P * segs;
-    const int down_end_unit = up_units + q_units + R.nchunks * gd.groups;
-    const int csegs = (H + CSEG - 1) / CSEG;                   // adding units of one token
-    const int units = down_end_unit + ntok * csegs;
-    // what a unit does: 0 up, 1 quantise, 2 down, 3 add (1 and 3 have no weights)
-    auto kind_of = [&](int u) {
-        return u < up_units ? 0 : u < up_units + q_units ? 1 : u < down_end_unit ? 2 : 3;
-    };
-
-    if (warp == E_PRODUCER) {
-        bool ok = true;
-        uint32_t g = 0;
-        auto slot = [&](int &r) {
-            r = (int)(g % ERING);
-            return g < (uint32_t)ERING || warp_wait(smem_u32(&S.empty[r]), (g / ERING - 1) & 1, wait_ns);
-        };
-        while (ok) {
-            const int u = __shfl_sync(0xffffffffu, next, 0);
-            if (lane == 0) next = (int)atomicAdd(ticket, 1u);   // on its way while this unit is brought
-            const int kind = u >= units ? 1 : kind_of(u);
-            if (kind & 1) {      // nothing to bring: a finisher's unit, or the end
-                int r;
-                if (!(ok = slot(r))) break;
-                if (lane == 0) {
-                    S.unit[r] = u;
-                    mbar_arrive(smem_u32(&S.full[r]));
-                }
-                ++g;
-                if (u >= units) break;
-                continue;
-            }
-            const bool up = kind == 0;
-            const int groups = up ? gu.groups : gd.groups, rt = up ? gu.rt : gd.rt, sub = up ? gu.sub : gd.sub;
-            const int stages = up ? gu.stages : gd.stages, kb = up ? gu.kb : gd.kb;
-            const int blocks = up ? gu.blocks : gd.blocks;
-            const uint32_t ld = up ? gu.ld : gd.ld;
-            const int v = up ? u : u - up_units - q_units;
-            const int c = v / groups, grp = v - c * groups, e = R.chunk_e[c];
-            for (int t = 0; t < sub && ok; ++t) {
-                if constexpr (!SHIFT) {
-                    // lane q brings rows 8 (q % 2) .. + 7 of row tile q / 2 (rows past the
-                    // projection's end are others' or zero; their results are dropped)
-                    const int tile = (grp * sub + t) * rt + (lane >> 1);
-                    const int row = up ? e * 2 * I + (lane & 1) * I + tile * 8 : e * H + tile * 16 + 8 * (lane & 1);
-                    for (int s = 0; s < stages; ++s, ++g) {
-                        int r;
-                        if (!(ok = slot(r))) break;
-                        const uint32_t bar = smem_u32(&S.full[r]);
-                        if (lane == 0) {
-                            S.unit[r] = u;
-                            if (blocks > 0) mbar_arrive_expect_tx(bar, 16u * rt * ld);
-                            else mbar_arrive(bar);
-                        }
-                        __syncwarp();
-                        if (lane < 2 * rt && blocks > 0)
-                            tma_load_2d(smem_u32(smem) + (uint32_t)r * ESTAGE + (uint32_t)lane * 8 * ld,
-                                        up ? &map_up : &map_down, bar, s * kb * (kQ8Step / 8), row);
-                        __syncwarp();
-                    }
-                    continue;
-                }
-                const int8_t *row0 = up ? w_up + (int64_t)e * 2 * I * ldu : w_down + (int64_t)e * H * ldd;
-                // this lane's rows of the stage (rows past the end read the last one)
-                const int8_t *row[2] = {nullptr, nullptr};
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    const int q = lane + 32 * h, tile = (grp * sub + t) * rt + (q >> 4);
-                    if (q < 16 * rt) {
-                        const int i = min(tile * 8 + (q & 7), I - 1) + ((q >> 3) & 1) * I;
-                        row[h] = row0 + (up ? (int64_t)i * ldu : (int64_t)min(tile * 16 + (q & 15), H - 1) * ldd);
-                    }
-                }
-                for (int s = 0; s < stages; ++s, ++g) {
-                    int r;
-                    if (!(ok = slot(r))) break;
-                    const uint32_t bar = smem_u32(&S.full[r]);
-                    const uint32_t base = smem_u32(smem) + (uint32_t)r * ESTAGE;
-                    const int len = max(0, min(kb, blocks - s * kb)) * kQ8Step;
-                    const int8_t *src[2];
-                    uint32_t bytes[2], total = 0;
-#pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        bytes[h] = 0;
-                        src[h] = row[h] + (int64_t)s * kb * kQ8Step;
-                        if (row[h] != nullptr && len > 0) {
-                            bytes[h] = (uint32_t)len;
-                            if (SHIFT) {
-                                const uint32_t off = (uint32_t)(reinterpret_cast<uintptr_t>(src[h]) & 15);
-                                src[h] -= off;
-                                bytes[h] = (bytes[h] + off + 15) / 16 * 16;
-                            }
-                            total += bytes[h];
-                        }
-                    }
-                    total = __reduce_add_sync(0xffffffffu, total);
-                    if (lane == 0) {
-                        S.unit[r] = u;
-                        if (total > 0) mbar_arrive_expect_tx(bar, total);
-                        else mbar_arrive(bar);
-                    }
-                    __syncwarp();
-#pragma unroll
-                    for (int h = 0; h < 2; ++h)
-                        if (bytes[h] > 0) bulk_load(base + (uint32_t)(lane + 32 * h) * ld, src[h], bytes[h], bar);
-                    __syncwarp();
-                }
-            }
-        }
-        if (!ok && lane == 0) {
-            record_error(err, kErrWaitTimeout);
-            for (uint32_t q = g > (uint32_t)ERING ? g - ERING : 0; q < g; ++q)
-                mbar_wait(smem_u32(&S.full[q % ERING]), (q / ERING) & 1, 1000000000ull);
-        }
-    } else if (warp < kQ8Consumers) {
-        const int g = lane >> 2, t4 = lane & 3;
-        const int group = warp / EGROUP, cw = warp % EGROUP;
-        int open_chunk = -1;              // the chunk whose hidden rows were last seen complete
-        uint32_t used = 0;
-        bool ok = true;
-        for (uint32_t count = 0;; ++count) {
-            int r = (int)(used % ERING);
-            if (!(ok = warp_wait(smem_u32(&S.full[r]), (used / ERING) & 1, wait_ns))) break;
-            const int u = S.unit[r];
-            const int kind = u >= units ? 1 : kind_of(u);
-            const bool mine = (int)(count & 1) == group;
-            const bool up = kind == 0;
-            const int stages = up ? gu.stages : gd.stages, sub = up ? gu.sub : gd.sub;
-            if (!mine || (kind & 1)) {     // the other group's unit, or one without weights
-                const int all = (kind & 1) ? 1 : stages * sub;
-                for (int s = 0; s < all; ++s, ++used) {
-                    r = (int)(used % ERING);
-                    if (s > 0 && !(ok = warp_wait(smem_u32(&S.full[r]), (used / ERING) & 1, wait_ns))) break;
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(smem_u32(&S.empty[r]));
-                }
-                if (!ok) break;
-                if (!mine && u < units) continue;
-            } else {
-                const int b = (int)(count % EBUFS);
-                const int K = up ? H : I, groups = up ? gu.groups : gd.groups, rt = up ? gu.rt : gd.rt;
-                const int kw = up ? gu.kw : gd.kw, kb = up ? gu.kb : gd.kb, blocks = up ? gu.blocks : gd.blocks;
-                const uint32_t ld = up ? gu.ld : gd.ld;
-                const int v = up ? u : u - up_units - q_units;
-                const int c = v / groups, grp = v - c * groups;
-                const int e = R.chunk_e[c], at = R.chunk_at[c], n = R.chunk_n[c];
-                // down: the chunk's hidden rows are there in 8 bits
-                if (!up && c != open_chunk) {
-                    if (!(ok = warp_poll(quantised + c, (uint32_t)(n * segs), wait_ns))) break;
-                    open_chunk = c;
-                }
-                const int tl = cw / kw, kpart = cw % kw;      // this warp's tile of a stage, its share of the steps
-                const int step0 = kpart * ESTEPS;
-                const int8_t *xbase = up ? xq : hq;
-                const int64_t xld = up ? L.Hp : L.Ip;
-                // token row of the chunk's pair j (past the end: the last one)
-                auto token = [&](int j) {
-                    const int p = R.list[at + min(j, n - 1)];
-                    return xbase + (int64_t)(up ? p / top_k : p) * xld + 16 * t4;
-                };
-                // the buffer is free (its finisher has read and cleared it)
-                if (count >= (uint32_t)EBUFS &&
-                    !(ok = warp_wait(smem_u32(&S.bempty[b]), (count / EBUFS - 1) & 1, wait_ns)))
-                    break;
-                // DP: NT tokens by dp4a, each lane with every token's bytes; otherwise
-                // NT blocks of 8 tokens by MMA, lane row g with token g of each.
-                auto multiply = [&](auto nt, auto dp) {
-                    constexpr int NT = decltype(nt)::value;
-                    constexpr bool DP = decltype(dp)::value;
-                    const int8_t *x[NT];
-#pragma unroll
-                    for (int j = 0; j < NT; ++j) x[j] = token(DP ? j : 8 * j + g);
-                    for (int t = 0; t < sub && ok; ++t) {
-                        // the two weight rows of this lane, and where they lie in a stage
-                        const int tile = (grp * sub + t) * rt + tl;
-                        const int8_t *wa, *wb;
-                        if (up) {
-                            wa = w_up + ((int64_t)e * 2 * I + min(tile * 8 + g, I - 1)) * ldu;
-                            wb = wa + (int64_t)I * ldu;
-                        } else {
-                            wa = w_down + ((int64_t)e * H + min(tile * 16 + g, H - 1)) * ldd;
-                            wb = w_down + ((int64_t)e * H + min(tile * 16 + g + 8, H - 1)) * ldd;
-                        }
-                        const uint32_t oa = (uint32_t)(tl * 16 + g) * ld + (uint32_t)(step0 * kQ8Step + 16 * t4) +
-                                            (SHIFT ? (uint32_t)(reinterpret_cast<uintptr_t>(wa) & 15) : 0u);
-                        const uint32_t ob = (uint32_t)(tl * 16 + g + 8) * ld + (uint32_t)(step0 * kQ8Step + 16 * t4) +
-                                            (SHIFT ? (uint32_t)(reinterpret_cast<uintptr_t>(wb) & 15) : 0u);
-                        int sum[NT][DP ? 2 : 4];
-#pragma unroll
-                        for (int j = 0; j < NT; ++j)
-#pragma unroll
-                            for (int i = 0; i < (DP ? 2 : 4); ++i) sum[j][i] = 0;
-                        auto step = [&](const uint4 &a, const uint4 &d, int64_t k) {
-                            uint4 xv[NT];
-#pragma unroll
-                            for (int j = 0; j < NT; ++j) xv[j] = *reinterpret_cast<const uint4 *>(x[j] + k);
-                            if constexpr (DP) {
-                                q8_step_dp<NT>(sum, a, d, xv);
-                            } else {
-#pragma unroll
-                                for (int j = 0; j < NT; ++j) q8_step_s8(sum[j], a, d, xv[j]);
-                            }
-                        };
-                        for (int s = 0; s < stages; ++s, ++used) {
-                            r = (int)(used % ERING);
-                            if (s + t > 0 && !(ok = warp_wait(smem_u32(&S.full[r]), (used / ERING) & 1, wait_ns))) break;
-                            const uint32_t stage = smem_u32(smem) + (uint32_t)r * ESTAGE;
-#pragma unroll
-                            for (int k = 0; k < ESTEPS; ++k)
-                                if (s * kb + step0 + k < blocks)
-                                    step(SHIFT ? lds_shifted(stage + oa + k * kQ8Step) : lds128(stage + oa + k * kQ8Step),
-                                         SHIFT ? lds_shifted(stage + ob + k * kQ8Step) : lds128(stage + ob + k * kQ8Step),
-                                         (int64_t)(s * kb + step0 + k) * kQ8Step);
-                            __syncwarp();
-                            if (lane == 0) mbar_arrive(smem_u32(&S.empty[r]));
-                        }
-                        if (!ok) break;
-                        if (kpart == 0)
-                            for (int k0 = blocks * kQ8Step; k0 < K; k0 += kQ8Step) {   // the rows' last values
-                                const int valid = min(16, max(0, K - k0 - 16 * t4));
-                                step(load16_bytes(wa + k0 + 16 * t4, valid), load16_bytes(wb + k0 + 16 * t4, valid), k0);
-                            }
-                        // whole numbers: the order of these additions does not matter
-                        int *to = part + b * EPART + (t * rt + tl) * 256;
-                        if constexpr (DP) {
-#pragma unroll
-                            for (int j = 0; j < NT; ++j)
-#pragma unroll
-                                for (int i = 0; i < 2; ++i) {
-                                    int v2 = sum[j][i];
-                                    v2 += __shfl_xor_sync(0xffffffffu, v2, 1);
-                                    v2 += __shfl_xor_sync(0xffffffffu, v2, 2);
-                                    // one lane of the quad: where the MMA would leave (row, token j)
-                                    if (t4 == (j >> 1)) atomicAdd(to + (2 * i + (j & 1)) * 32 + lane, v2);
-                                }
-                        } else {
-#pragma unroll
-                            for (int j = 0; j < NT; ++j)
-#pragma unroll
-                                for (int i = 0; i < 4; ++i) atomicAdd(to + j * 128 + 32 * i + lane, sum[j][i]);
-                        }
-                    }
-                };
-                using std::integral_constant;
-                if (n == 1) multiply(integral_constant<int, 1>{}, std::true_type{});
-                else if (n == 2) multiply(integral_constant<int, 2>{}, std::true_type{});
-                else if (n <= 4) multiply(integral_constant<int, 4>{}, std::true_type{});
-                else if (n <= 8) multiply(integral_constant<int, 1>{}, std::false_type{});
-                else multiply(integral_constant<int, 2>{}, std::false_type{});
-                if (!ok) break;
-            }
-            // hand the sums over; the end goes to every finisher, each group telling
-            // those whose buffers it fills (it alone knows their turn)
-            const uint32_t last = u < units ? count : count + 1;
-            for (uint32_t q = count; q <= last; ++q) {
-                if ((int)(q & 1) != group) continue;
-                const int o = (int)(q % EBUFS);
-                if ((kind & 1) && q >= (uint32_t)EBUFS &&
-                    !(ok = warp_wait(smem_u32(&S.bempty[o]), (q / EBUFS - 1) & 1, wait_ns)))
-                    break;
-                if (cw == 0 && lane == 0) S.done[o] = u;
-                __syncwarp();
-                if (lane == 0) mbar_arrive(smem_u32(&S.bfull[o]));
-            }
-            if (!ok || u >= units) break;
-        }
-        if (!ok && lane == 0) record_error(err, kErrWaitTimeout);
-    } else {
-        bool ok = true;
-        for (uint32_t count = (uint32_t)(warp - kQ8Consumers);; count += FINISHERS) {
-            const int b = (int)(count % EBUFS);       // this finisher's buffer
-            if (!(ok = warp_wait(smem_u32(&S.bfull[b]), (count / EBUFS) & 1, wait_ns))) break;
-            const int u = S.done[b];
-            if (u >= units) break;
-            const int kind = kind_of(u);
-            int *sums = part + b * EPART;
-            auto sum_at = [&](int tile, int row, int tok) {
-                return sums[tile * 256 + (tok >> 3) * 128 + (((row >> 3) << 1) + (tok & 1)) * 32 + (row & 7) * 4 +
-                            ((tok & 7) >> 1)];
-            };
-            if (kind == 1) {
-                if (lane == 0) mbar_arrive(smem_u32(&S.bempty[b]));
-                const int v = u - up_units, q = v / segs, seg = v - q * segs;
-                const int p = R.list[q];            // pairs in the order of their chunks
-                int c = 0;
-                {
-                    const int e = R.ids[p];
-                    c = R.first_chunk[e] + (q - R.first[e]) / 16;
-                }
-                if (!(ok = warp_poll(ready + c, (uint32_t)gu.groups, wait_ns))) break;
-                const int lo = seg * QSEG, hi = min(lo + QSEG, L.Ip);
-                const float *hr = hidden + (int64_t)p * I;
-                int8_t *qr = hq + (int64_t)p * L.Ip;
-                float h4[QSEG / 128][4];        // all loads at once
-#pragma unroll
-                for (int q4 = 0; q4 < QSEG / 128; ++q4) {
-                    const int i = lo + 128 * q4 + 4 * lane;
-                    if (I % 4 == 0 && i < I) {
-                        const float4 v4 = __ldcg(reinterpret_cast<const float4 *>(hr + i));
-                        h4[q4][0] = v4.x; h4[q4][1] = v4.y; h4[q4][2] = v4.z; h4[q4][3] = v4.w;
-                    } else {
-#pragma unroll
-                        for (int k = 0; k < 4; ++k) h4[q4][k] = i + k < I ? __ldcg(hr + i + k) : 0.0f;
-                    }
-                }
-                const RowQuant rq(__ldcg(hmax + p));
-#pragma unroll
-                for (int q4 = 0; q4 < QSEG / 128; ++q4) {
-                    const int i = lo + 128 * q4 + 4 * lane;
-                    if (i < hi)
-                        *reinterpret_cast<uint32_t *>(qr + i) = pack4(rq(h4[q4][0]), rq(h4[q4][1]), rq(h4[q4][2]), rq(h4[q4][3]));
-                }
-                if (seg == 0 && lane == 0) hs[p] = rq.step * rq.unpre;
-                __threadfence();
-                __syncwarp();
-                if (lane == 0) atomicAdd(quantised + c, 1u);
-                continue;
-            }
-            if (kind == 3) {      // one token's sum over its experts, in slot order
-                if (lane == 0) mbar_arrive(smem_u32(&S.bempty[b]));
-                const int v = u - down_end_unit, t = v / csegs, c0 = (v - t * csegs) * CSEG;
-                const int cols = 16 * gd.rt * gd.sub, g0 = c0 / cols, g1 = (min(c0 + CSEG, H) - 1) / cols;
-                if (!(ok = warp_poll_all(done + g0, g1 - g0 + 1, (uint32_t)R.nchunks, wait_ns))) break;
-                const int col = c0 + 4 * lane;
-                float y[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-                const float *rr = res + (int64_t)t * top_k * H + col;
-#pragma unroll 4
-                for (int j = 0; j < top_k; ++j) {
-                    float w4[4];
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) w4[k] = col + k < H ? __ldcg(rr + (int64_t)j * H + k) : 0.0f;
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) y[k] = fmaf(R.gates[t * top_k + j], w4[k], y[k]);
-                }
-#pragma unroll
-                for (int k = 0; k < 4; ++k)
-                    if (col + k < H) out[(int64_t)t * ldo + col + k] = from_f32<T>(y[k]);
-                continue;
-            }
-            const bool up = kind == 0;
-            const int groups = up ? gu.groups : gd.groups;
-            const int tiles = up ? gu.rt * gu.sub : gd.rt * gd.sub;     // of the unit
-            const int v = up ? u : u - up_units - q_units;
-            const int c = v / groups, grp = v - c * groups;
-            const int e = R.chunk_e[c], at = R.chunk_at[c], n = R.chunk_n[c];
-            auto clear = [&] {      // the sums have been read: the buffer goes back empty
-                __syncwarp();
-                for (int i = lane; i < tiles * 64; i += 32) reinterpret_cast<int4 *>(sums)[i] = make_int4(0, 0, 0, 0);
-                __syncwarp();
-                if (lane == 0) mbar_arrive(smem_u32(&S.bempty[b]));
-            };
-            if (up) {
-                for (int o0 = 0; o0 < 8 * tiles * n; o0 += 32) {
-                    const int o = o0 + lane, row = o & 7, tl = (o >> 3) % tiles, j = (o >> 3) / tiles;
-                    const int i = (grp * tiles + tl) * 8 + row;
-                    uint32_t mb = 0;
-                    int p = 0;
-                    if (j < n && i < I) {
-                        p = R.list[at + j];
-                        const float s = __ldg(xs + p / top_k);
-                        const float gv = (float)sum_at(tl, row, j) * s * __ldg(s_up + (int64_t)e * 2 * I + i);
-                        const float uv = (float)sum_at(tl, row + 8, j) * s * __ldg(s_up + (int64_t)e * 2 * I + I + i);
-                        const float hv = __fdiv_rn(gv, 1.0f + expf(-gv)) * uv;
-                        __stcg(hidden + (int64_t)p * I + i, hv);
-                        mb = abs_bits(hv);
-                    }
-#pragma unroll
-                    for (int d = 1; d < 8; d <<= 1) mb = max(mb, __shfl_xor_sync(0xffffffffu, mb, d));
-                    if (row == 0 && j < n && mb != 0u) atomicMax(hmax + p, mb);
-                }
-                clear();
-                __threadfence();
-                __syncwarp();
-                if (lane == 0) atomicAdd(ready + c, 1u);
-            } else {
-                for (int o = lane; o < 16 * tiles * n; o += 32) {
-                    const int row = o & 15, tl = (o >> 4) % tiles, j = (o >> 4) / tiles;
-                    const int col = (grp * tiles + tl) * 16 + row;
-                    if (col < H) {
-                        const int p = R.list[at + j];
-                        __stcg(res + (int64_t)p * H + col,
-                               (float)sum_at(tl, row, j) * __ldcg(hs + p) * __ldg(s_down + (int64_t)e * H + col));
-                    }
-                }
-                clear();
-                __threadfence();
-                __syncwarp();
-                if (lane == 0) atomicAdd(done + grp, 1u);
-            }
-        }
-        if (!ok && lane == 0) record_error(err, kErrWaitTimeout);
-    }
+    __syncthreads();
+    if (warp == E_PRODUCER) produce<SHIFT>(S, smem_u32(smem), &map_up, &map_down, next);
+    else if (warp < kQ8Consumers) consume<SHIFT>(S, smem_u32(smem), part);
+    else finish<T>(S, part);
 }
 
 // Map of rows of `K` bytes in 8-byte elements, for boxes of 8 rows as long as a
