@@ -29,6 +29,7 @@ namespace sgemm_gb300 {
 namespace {
 
 constexpr int RTHREADS = 256;
+constexpr int kRouteTokens = 16;       // tokens a router block takes at a time
 constexpr int MWARPS = 8, MTHREADS = MWARPS * 32;
 constexpr int kMaxPairs = kMoeMaxTokens * kMoeMaxTopK;
 
@@ -69,7 +70,7 @@ __global__ void __launch_bounds__(RTHREADS)
 q8_route_kernel(int ntok, int E, int top_k, int H, int I, const T *__restrict__ x, int64_t ldx,
                 const float *__restrict__ router, int64_t ldr, int vec, unsigned char *__restrict__ ws) {
     __shared__ uint32_t red[64];
-    __shared__ float lsum[RTHREADS / 32][8];
+    __shared__ float lsum[RTHREADS / 32][kRouteTokens];
     const MoeLayout L(ntok, E, top_k, H, I);
     pdl_wait();
     pdl_trigger();
@@ -78,15 +79,15 @@ q8_route_kernel(int ntok, int E, int top_k, int H, int I, const T *__restrict__ 
         const int e = (int)blockIdx.x;
         const float *w = router + (int64_t)e * ldr;
         float *logits = reinterpret_cast<float *>(ws + L.logits);
-        for (int t0 = 0; t0 < ntok; t0 += 8) {
-            float acc[8];
+        for (int t0 = 0; t0 < ntok; t0 += kRouteTokens) {
+            float acc[kRouteTokens];
 #pragma unroll
-            for (int j = 0; j < 8; ++j) acc[j] = 0.0f;
+            for (int j = 0; j < kRouteTokens; ++j) acc[j] = 0.0f;
             if (vec) {
                 for (int k = 4 * (int)threadIdx.x; k < H; k += 4 * RTHREADS) {
                     const float4 w4 = __ldg(reinterpret_cast<const float4 *>(w + k));
 #pragma unroll
-                    for (int j = 0; j < 8; ++j)
+                    for (int j = 0; j < kRouteTokens; ++j)
                         if (t0 + j < ntok) {
                             float v[4];
                             load_vec<T, 4>(x + (int64_t)(t0 + j) * ldx + k, v);
@@ -97,20 +98,20 @@ q8_route_kernel(int ntok, int E, int top_k, int H, int I, const T *__restrict__ 
                 for (int k = threadIdx.x; k < H; k += RTHREADS) {
                     const float wk = __ldg(w + k);
 #pragma unroll
-                    for (int j = 0; j < 8; ++j)
+                    for (int j = 0; j < kRouteTokens; ++j)
                         if (t0 + j < ntok) acc[j] = fmaf(to_f32<T>(x[(int64_t)(t0 + j) * ldx + k]), wk, acc[j]);
                 }
             }
 #pragma unroll
-            for (int j = 0; j < 8; ++j)
+            for (int j = 0; j < kRouteTokens; ++j)
 #pragma unroll
                 for (int o = 16; o > 0; o >>= 1) acc[j] += __shfl_xor_sync(0xffffffffu, acc[j], o);
             __syncthreads();
             if (lane == 0)
 #pragma unroll
-                for (int j = 0; j < 8; ++j) lsum[warp][j] = acc[j];
+                for (int j = 0; j < kRouteTokens; ++j) lsum[warp][j] = acc[j];
             __syncthreads();
-            if (threadIdx.x < 8 && t0 + (int)threadIdx.x < ntok) {
+            if (threadIdx.x < kRouteTokens && t0 + (int)threadIdx.x < ntok) {
                 float s = 0.0f;
 #pragma unroll
                 for (int v = 0; v < RTHREADS / 32; ++v) s += lsum[v][threadIdx.x];
@@ -505,7 +506,7 @@ constexpr int ERING = 4, EBUFS = 4;                        // stages; buffers of
 constexpr int EGROUP = kQ8Consumers / 2;                   // warps of a consumer group
 constexpr int ESTEPS = 4;                                  // steps per consumer warp and stage
 constexpr int ETILES = 4;                                  // 16-row tiles of a unit, at most
-constexpr uint32_t ESTAGE = 64 * (8 * kQ8Step + 64 + 16);  // the largest geometry (RT = 4)
+constexpr uint32_t ESTAGE = 64 * (2 * ESTEPS * kQ8Step + 80);  // the largest geometry (RT = 4)
 constexpr int EPART = ETILES * 2 * 128;                    // one unit's sums: [tile][token block][word][lane]
 constexpr int QSEG = 512;                                  // hidden values a quantising unit takes
 constexpr int CSEG = 128;                                  // results an adding unit takes
@@ -523,9 +524,11 @@ struct EGeom {       // one projection's division
         // whole steps that the ring brings; shifted rows leave 15 bytes at their end alone
         blocks = shift ? (K > 15 ? (K - 15) / kQ8Step : 0) : K / kQ8Step;
         stages = blocks > 0 ? (blocks + kb - 1) / kb : 1;
-        // two stages to a unit, if that leaves every block eight units
+        // as many tiles to a unit as leave every block six units (at 8, 12 and 16 the
+        // layer for one token took 74, 82 and 82 us, at 4 73)
         const int64_t all = (int64_t)((rows + per_tile * rt - 1) / (per_tile * rt)) * chunks;
-        sub = stages == 1 && rt <= 2 && all >= (int64_t)16 * blocks_of_grid ? 2 : 1;
+        sub = ETILES / rt;
+        while (sub > 1 && all < (int64_t)6 * sub * blocks_of_grid) sub /= 2;
         groups = (rows + per_tile * rt * sub - 1) / (per_tile * rt * sub);
         ld = (uint32_t)(kb * kQ8Step + (shift ? 80 : 0));
     }
@@ -667,7 +670,7 @@ __device__ __forceinline__ bool unit_products(EShared &S, uint32_t ring, int *su
             // The tokens of a batch of steps are asked for together, the first ahead of
             // the wait for the weights.  (A step past the last reads the last one's
             // tokens and is not used.)
-            constexpr int BATCH = NT <= 2 ? ESTEPS : ESTEPS / 2;
+            constexpr int BATCH = NT <= 2 || ESTEPS <= 2 ? ESTEPS : ESTEPS / 2;
             uint4 xv[BATCH][NT];
             auto xload = [&](int k0) {
 #pragma unroll
@@ -723,7 +726,7 @@ __device__ __forceinline__ bool unit_products(EShared &S, uint32_t ring, int *su
     return true;
 }
 
-template <bool SHIFT>
+template <bool SU, bool SD>
 __device__ __noinline__ void produce(EShared &S, uint32_t ring, const CUtensorMap *map_up,
                                      const CUtensorMap *map_down, int next) {
     const EArgs &A = S.a;
@@ -761,7 +764,7 @@ __device__ __noinline__ void produce(EShared &S, uint32_t ring, const CUtensorMa
                 int r;
                 if (!(ok = slot(r))) break;
                 const uint32_t bar = smem_u32(&S.full[r]), base = ring + (uint32_t)r * ESTAGE;
-                if constexpr (!SHIFT) {
+                if (!(up ? SU : SD)) {
                     // lane q brings rows 8 (q % 2) .. + 7 of row tile q / 2 (rows past the
                     // projection's end are others' or zero; their results are dropped)
                     const int tile = tile0 + (lane >> 1);
@@ -815,7 +818,7 @@ __device__ __noinline__ void produce(EShared &S, uint32_t ring, const CUtensorMa
     }
 }
 
-template <bool SHIFT>
+template <bool SU, bool SD>
 __device__ __noinline__ void consume(EShared &S, uint32_t ring, int *part) {
     const EArgs &A = S.a;
     const MoeShared &R = S.route;
@@ -855,11 +858,16 @@ __device__ __noinline__ void consume(EShared &S, uint32_t ring, int *part) {
                 !(ok = warp_wait(smem_u32(&S.bempty[b]), (count / EBUFS - 1) & 1, A.wait_ns)))
                 break;
             int *sums = part + b * EPART;
-            if (n == 1) ok = unit_products<1, true, SHIFT>(S, ring, sums, c, grp, up, used);
-            else if (n == 2) ok = unit_products<2, true, SHIFT>(S, ring, sums, c, grp, up, used);
-            else if (n <= 4) ok = unit_products<4, true, SHIFT>(S, ring, sums, c, grp, up, used);
-            else if (n <= 8) ok = unit_products<1, false, SHIFT>(S, ring, sums, c, grp, up, used);
-            else ok = unit_products<2, false, SHIFT>(S, ring, sums, c, grp, up, used);
+            auto products = [&](auto shift) {
+                constexpr bool SHIFT = decltype(shift)::value;
+                if (n == 1) return unit_products<1, true, SHIFT>(S, ring, sums, c, grp, up, used);
+                if (n == 2) return unit_products<2, true, SHIFT>(S, ring, sums, c, grp, up, used);
+                if (n <= 4) return unit_products<4, true, SHIFT>(S, ring, sums, c, grp, up, used);
+                if (n <= 8) return unit_products<1, false, SHIFT>(S, ring, sums, c, grp, up, used);
+                return unit_products<2, false, SHIFT>(S, ring, sums, c, grp, up, used);
+            };
+            if (SU == SD || up) ok = products(std::bool_constant<SU>{});
+            else ok = products(std::bool_constant<SD>{});
             if (!ok) break;
             used += (uint32_t)(G.stages * G.sub);
         }
@@ -963,27 +971,44 @@ __device__ __noinline__ void finish(EShared &S, int *part) {
         const int c = v / G.groups, grp = v - c * G.groups;
         const int e = R.chunk_e[c], at = R.chunk_at[c], n = R.chunk_n[c];
         if (up) {
-            for (int o0 = 0; o0 < 8 * tiles * n; o0 += 32) {
-                const int o = o0 + lane, row = o & 7, tl = (o >> 3) % tiles, j = (o >> 3) / tiles;
-                const int i = (grp * tiles + tl) * 8 + row;
-                uint32_t mb = 0;
-                int p = 0;
-                if (j < n && i < I) {
-                    p = R.list[at + j];
-                    const float s = __ldg(A.xs + p / top_k);
-                    const float sg = __ldg(A.s_up + (int64_t)e * 2 * I + i), su = __ldg(A.s_up + (int64_t)e * 2 * I + I + i);
-                    const float gv = (float)sum_at(tl, row, j) * s * sg;
-                    const float uv = (float)sum_at(tl, row + 8, j) * s * su;
-                    const float hv = __fdiv_rn(gv, 1.0f + expf(-gv)) * uv;
-                    __stcg(A.hidden + (int64_t)p * I + i, hv);
-                    mb = abs_bits(hv);
+            const int all = 8 * tiles * n;
+            for (int o0 = 0; o0 < all; o0 += 128) {     // four rounds' scales at once
+                float sx[4], sg[4], su[4];
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    const int o = o0 + 32 * q + lane, tl = (o >> 3) % tiles, j = (o >> 3) / tiles;
+                    const int i = (grp * tiles + tl) * 8 + (o & 7);
+                    sx[q] = sg[q] = su[q] = 0.0f;
+                    if (o < all && i < I) {
+                        sx[q] = __ldg(A.xs + R.list[at + j] / top_k);
+                        sg[q] = __ldg(A.s_up + (int64_t)e * 2 * I + i);
+                        su[q] = __ldg(A.s_up + (int64_t)e * 2 * I + I + i);
+                    }
                 }
 #pragma unroll
-                for (int d = 1; d < 8; d <<= 1) mb = max(mb, __shfl_xor_sync(0xffffffffu, mb, d));
-                if (row == 0 && j < n && mb != 0u) atomicMax(A.hmax + p, mb);
+                for (int q = 0; q < 4; ++q) {
+                    if (o0 + 32 * q >= all) break;
+                    const int o = o0 + 32 * q + lane, row = o & 7, tl = (o >> 3) % tiles, j = (o >> 3) / tiles;
+                    const int i = (grp * tiles + tl) * 8 + row;
+                    uint32_t mb = 0;
+                    int p = 0;
+                    if (o < all && i < I) {
+                        p = R.list[at + j];
+                        const float gv = (float)sum_at(tl, row, j) * sx[q] * sg[q];
+                        const float uv = (float)sum_at(tl, row + 8, j) * sx[q] * su[q];
+                        const float hv = __fdiv_rn(gv, 1.0f + expf(-gv)) * uv;
+                        __stcg(A.hidden + (int64_t)p * I + i, hv);
+                        mb = abs_bits(hv);
+                    }
+#pragma unroll
+                    for (int d = 1; d < 8; d <<= 1) mb = max(mb, __shfl_xor_sync(0xffffffffu, mb, d));
+                    if (row == 0 && mb != 0u) atomicMax(A.hmax + p, mb);
+                }
             }
         } else {
-            for (int o = lane; o < 16 * tiles * n; o += 32) {
+            const int all = 16 * tiles * n;
+#pragma unroll 4
+            for (int o = lane; o < all; o += 32) {
                 const int row = o & 15, tl = (o >> 4) % tiles, j = (o >> 4) / tiles;
                 const int col = (grp * tiles + tl) * 16 + row;
                 if (col < H) {
@@ -1006,7 +1031,7 @@ __device__ __noinline__ void finish(EShared &S, int *part) {
     if (!ok && lane == 0) record_error(A.err, kErrWaitTimeout);
 }
 
-template <typename T, bool SHIFT>
+template <typename T, bool SU, bool SD>
 __global__ void __launch_bounds__(ETHREADS, 1)
 q8_expert_ring_kernel(const __grid_constant__ CUtensorMap map_up, const __grid_constant__ CUtensorMap map_down,
                       int ntok, int E, int top_k, int H, int I, int renorm, const int8_t *w_up, int64_t ldu,
@@ -1033,12 +1058,8 @@ q8_expert_ring_kernel(const __grid_constant__ CUtensorMap map_up, const __grid_c
         mbar_fence_init();
     }
     for (int i = tid; i < EBUFS * EPART; i += ETHREADS) part[i] = 0;
-    pdl_wait();
     uint32_t *ticket = reinterpret_cast<uint32_t *>(ws + L.zero);
-    int next = 0;       // the producer's first unit, asked for before the routing
-    if (warp == E_PRODUCER && lane == 0) next = (int)atomicAdd(ticket, 1u);
-    moe_route(R, ntok, E, top_k, renorm, reinterpret_cast<const float *>(ws + L.logits));   // ends with a barrier
-    if (tid == 0) {
+    if (tid == 32) {
         EArgs &A = S.a;
         A.w_up = w_up; A.w_down = w_down; A.ldu = ldu; A.ldd = ldd; A.s_up = s_up; A.s_down = s_down;
         A.out = out; A.ldo = ldo;
@@ -1055,14 +1076,20 @@ q8_expert_ring_kernel(const __grid_constant__ CUtensorMap map_up, const __grid_c
         A.done = A.hmax + L.P;
         A.err = err; A.wait_ns = wait_ns;
         A.ntok = ntok; A.top_k = top_k; A.H = H; A.I = I; A.Hp = L.Hp; A.Ip = L.Ip;
-        S.geom[0] = EGeom(H, I, 8, SHIFT, R.nchunks, (int)gridDim.x);
-        S.geom[1] = EGeom(I, H, 16, SHIFT, R.nchunks, (int)gridDim.x);
-        A.segs = (L.Ip + QSEG - 1) / QSEG;
-        A.csegs = (H + CSEG - 1) / CSEG;
+    }
+    pdl_wait();
+    int next = 0;       // the producer's first unit, asked for before the routing
+    if (warp == E_PRODUCER && lane == 0) next = (int)atomicAdd(ticket, 1u);
+    moe_route(R, ntok, E, top_k, renorm, reinterpret_cast<const float *>(ws + L.logits));   // ends with a barrier
+    EArgs &A = S.a;
+    if (tid == 0) {
+        S.geom[0] = EGeom(H, I, 8, SU, R.nchunks, (int)gridDim.x);
         A.up_units = R.nchunks * S.geom[0].groups;
-        A.quant_end = A.up_units + L.P * A.segs;
-        A.down_end = A.quant_end + R.nchunks * S.geom[1].groups;
-        A.units = A.down_end + ntok * A.csegs;
+    } else if (tid == 32) {
+        S.geom[1] = EGeom(I, H, 16, SD, R.nchunks, (int)gridDim.x);
+        A.csegs = (H + CSEG - 1) / CSEG;
+    } else if (tid == 64) {
+        A.segs = (L.Ip + QSEG - 1) / QSEG;
     }
     if (blockIdx.x == 0) {
         for (int p = tid; p < L.P; p += ETHREADS) {
@@ -1071,8 +1098,14 @@ q8_expert_ring_kernel(const __grid_constant__ CUtensorMap map_up, const __grid_c
         }
     }
     __syncthreads();
-    if (warp == E_PRODUCER) produce<SHIFT>(S, smem_u32(smem), &map_up, &map_down, next);
-    else if (warp < kQ8Consumers) consume<SHIFT>(S, smem_u32(smem), part);
+    if (tid == 0) {
+        A.quant_end = A.up_units + L.P * A.segs;
+        A.down_end = A.quant_end + R.nchunks * S.geom[1].groups;
+        A.units = A.down_end + ntok * A.csegs;
+    }
+    __syncthreads();
+    if (warp == E_PRODUCER) produce<SU, SD>(S, smem_u32(smem), &map_up, &map_down, next);
+    else if (warp < kQ8Consumers) consume<SU, SD>(S, smem_u32(smem), part);
     else finish<T>(S, part);
 }
 
@@ -1123,14 +1156,14 @@ cudaError_t launch_t(const Q8MoeArgs &a, unsigned char *ws) {
                                (const T *)a.x, a.ldx, a.router, a.ldr, vec, ws);
     if (e != cudaSuccess) return e;
     if (reinterpret_cast<uintptr_t>(a.w_up) % 16 == 0 && reinterpret_cast<uintptr_t>(a.w_down) % 16 == 0) {
-        auto kern = a.ldu % 16 == 0 && a.ldd % 16 == 0 ? q8_expert_ring_kernel<T, false>
-                                                       : q8_expert_ring_kernel<T, true>;
+        const bool su = a.ldu % 16 != 0, sd = a.ldd % 16 != 0;
+        auto kern = su ? (sd ? q8_expert_ring_kernel<T, true, true> : q8_expert_ring_kernel<T, true, false>)
+                       : (sd ? q8_expert_ring_kernel<T, false, true> : q8_expert_ring_kernel<T, false, false>);
         e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)ESMEM);
         if (e != cudaSuccess) return e;
         alignas(64) CUtensorMap up = {}, down = {};
-        if (a.ldu % 16 == 0 && a.ldd % 16 == 0 &&
-            ((a.H >= kQ8Step && !encode_rows8(a.encode, &up, a.w_up, a.H, (int64_t)a.E * 2 * a.I, a.ldu)) ||
-             (a.I >= kQ8Step && !encode_rows8(a.encode, &down, a.w_down, a.I, (int64_t)a.E * a.H, a.ldd))))
+        if ((!su && a.H >= kQ8Step && !encode_rows8(a.encode, &up, a.w_up, a.H, (int64_t)a.E * 2 * a.I, a.ldu)) ||
+            (!sd && a.I >= kQ8Step && !encode_rows8(a.encode, &down, a.w_down, a.I, (int64_t)a.E * a.H, a.ldd)))
             return cudaErrorInvalidValue;
         return launch_pdl(kern, a.sm_count > 0 ? a.sm_count : 1, ETHREADS, ESMEM, a.stream, up, down, a.T, a.E, a.top_k, a.H,
                           a.I, a.renormalize, a.w_up, a.ldu, a.s_up, a.w_down, a.ldd, a.s_down, (T *)a.out, a.ldo,
