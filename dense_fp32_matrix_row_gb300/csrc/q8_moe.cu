@@ -512,11 +512,13 @@ constexpr int QSEG = 512;                                  // hidden values a qu
 constexpr int CSEG = 128;                                  // results an adding unit takes
 
 struct EGeom {       // one projection's division
-    int K, rt, kw, kb, blocks, stages, sub, groups;
+    int K, rt, kw, kb, blocks, stages;
     uint32_t ld;
+    int tiles;       // groups of rt row tiles that the projection has
+    int sub, groups; // groups of rt tiles to a unit (a power of two), units; set on the device
     EGeom() = default;
-    // `rows` results, `per_tile` of them to a tile; `experts` of them are wanted at most
-    __host__ __device__ EGeom(int K_, int rows, int per_tile, bool shift, int chunks, int blocks_of_grid) : K(K_) {
+    // `rows` results, `per_tile` of them to a tile
+    EGeom(int K_, int rows, int per_tile, bool shift) : K(K_) {
         const int steps = (K + kQ8Step - 1) / kQ8Step;
         rt = steps <= 8 ? 4 : steps <= 16 ? 2 : 1;
         kw = EGROUP / rt;
@@ -524,15 +526,21 @@ struct EGeom {       // one projection's division
         // whole steps that the ring brings; shifted rows leave 15 bytes at their end alone
         blocks = shift ? (K > 15 ? (K - 15) / kQ8Step : 0) : K / kQ8Step;
         stages = blocks > 0 ? (blocks + kb - 1) / kb : 1;
-        // as many tiles to a unit as leave every block six units (at 8, 12 and 16 the
-        // layer for one token took 74, 82 and 82 us, at 4 73)
-        const int64_t all = (int64_t)((rows + per_tile * rt - 1) / (per_tile * rt)) * chunks;
-        sub = ETILES / rt;
-        while (sub > 1 && all < (int64_t)6 * sub * blocks_of_grid) sub /= 2;
-        groups = (rows + per_tile * rt * sub - 1) / (per_tile * rt * sub);
         ld = (uint32_t)(kb * kQ8Step + (shift ? 80 : 0));
+        tiles = (rows + per_tile * rt - 1) / (per_tile * rt);
+        sub = 1;
+        groups = tiles;
+    }
+    // as many tiles to a unit as leave every block six units (at 8, 12 and 16 the
+    // layer for one token took 74, 82 and 82 us, at 4 73)
+    __device__ __forceinline__ void divide(int chunks, int blocks_of_grid) {
+        const int64_t all = (int64_t)tiles * chunks;
+        sub = rt == 1 ? 4 : rt == 2 ? 2 : 1;
+        while (sub > 1 && all < (int64_t)6 * sub * blocks_of_grid) sub >>= 1;
+        groups = (tiles + sub - 1) >> (sub == 4 ? 2 : sub == 2 ? 1 : 0);
     }
 };
+static_assert(ETILES == 4, "rt * sub tiles of a unit");
 
 // What the roles work on; in shared memory, so that none of it occupies the
 // registers of a role that does not need it (what they spill comes back from L2:
@@ -966,7 +974,7 @@ __device__ __noinline__ void finish(EShared &S, int *part) {
         }
         const bool up = kind == 0;
         const EGeom &G = S.geom[up ? 0 : 1];
-        const int tiles = G.rt * G.sub;     // of the unit
+        const int tiles = G.rt * G.sub, tsh = tiles == 4 ? 2 : tiles == 2 ? 1 : 0;     // of the unit
         const int v = up ? u : u - A.quant_end;
         const int c = v / G.groups, grp = v - c * G.groups;
         const int e = R.chunk_e[c], at = R.chunk_at[c], n = R.chunk_n[c];
@@ -976,7 +984,7 @@ __device__ __noinline__ void finish(EShared &S, int *part) {
                 float sx[4], sg[4], su[4];
 #pragma unroll
                 for (int q = 0; q < 4; ++q) {
-                    const int o = o0 + 32 * q + lane, tl = (o >> 3) % tiles, j = (o >> 3) / tiles;
+                    const int o = o0 + 32 * q + lane, tl = (o >> 3) & (tiles - 1), j = (o >> 3) >> tsh;
                     const int i = (grp * tiles + tl) * 8 + (o & 7);
                     sx[q] = sg[q] = su[q] = 0.0f;
                     if (o < all && i < I) {
@@ -988,7 +996,7 @@ __device__ __noinline__ void finish(EShared &S, int *part) {
 #pragma unroll
                 for (int q = 0; q < 4; ++q) {
                     if (o0 + 32 * q >= all) break;
-                    const int o = o0 + 32 * q + lane, row = o & 7, tl = (o >> 3) % tiles, j = (o >> 3) / tiles;
+                    const int o = o0 + 32 * q + lane, row = o & 7, tl = (o >> 3) & (tiles - 1), j = (o >> 3) >> tsh;
                     const int i = (grp * tiles + tl) * 8 + row;
                     uint32_t mb = 0;
                     int p = 0;
@@ -1009,7 +1017,7 @@ __device__ __noinline__ void finish(EShared &S, int *part) {
             const int all = 16 * tiles * n;
 #pragma unroll 4
             for (int o = lane; o < all; o += 32) {
-                const int row = o & 15, tl = (o >> 4) % tiles, j = (o >> 4) / tiles;
+                const int row = o & 15, tl = (o >> 4) & (tiles - 1), j = (o >> 4) >> tsh;
                 const int col = (grp * tiles + tl) * 16 + row;
                 if (col < H) {
                     const int p = R.list[at + j];
@@ -1034,7 +1042,7 @@ __device__ __noinline__ void finish(EShared &S, int *part) {
 template <typename T, bool SU, bool SD>
 __global__ void __launch_bounds__(ETHREADS, 1)
 q8_expert_ring_kernel(const __grid_constant__ CUtensorMap map_up, const __grid_constant__ CUtensorMap map_down,
-                      int ntok, int E, int top_k, int H, int I, int renorm, const int8_t *w_up, int64_t ldu,
+                      const EGeom g_up, const EGeom g_down, int ntok, int E, int top_k, int H, int I, int renorm, const int8_t *w_up, int64_t ldu,
                       const float *s_up, const int8_t *w_down, int64_t ldd, const float *s_down, T *out, int64_t ldo,
                       int *__restrict__ ids, float *__restrict__ gates, unsigned char *ws, unsigned *err,
                       uint64_t wait_ns) {
@@ -1083,10 +1091,12 @@ q8_expert_ring_kernel(const __grid_constant__ CUtensorMap map_up, const __grid_c
     moe_route(R, ntok, E, top_k, renorm, reinterpret_cast<const float *>(ws + L.logits));   // ends with a barrier
     EArgs &A = S.a;
     if (tid == 0) {
-        S.geom[0] = EGeom(H, I, 8, SU, R.nchunks, (int)gridDim.x);
+        S.geom[0] = g_up;
+        S.geom[0].divide(R.nchunks, (int)gridDim.x);
         A.up_units = R.nchunks * S.geom[0].groups;
     } else if (tid == 32) {
-        S.geom[1] = EGeom(I, H, 16, SD, R.nchunks, (int)gridDim.x);
+        S.geom[1] = g_down;
+        S.geom[1].divide(R.nchunks, (int)gridDim.x);
         A.csegs = (H + CSEG - 1) / CSEG;
     } else if (tid == 64) {
         A.segs = (L.Ip + QSEG - 1) / QSEG;
@@ -1113,7 +1123,7 @@ q8_expert_ring_kernel(const __grid_constant__ CUtensorMap map_up, const __grid_c
 // stage is deep (K >= 64).
 bool encode_rows8(EncodeTiledFn enc, CUtensorMap *map, const int8_t *base, int K, int64_t rows, int64_t ld) {
     if (enc == nullptr) return false;
-    const EGeom g(K, 1, 1, false, 1, 1);
+    const EGeom g(K, 1, 1, false);
     const cuuint64_t dims[2] = {(cuuint64_t)(K / 8), (cuuint64_t)rows};
     const cuuint64_t strides[1] = {(cuuint64_t)ld};
     const cuuint32_t box[2] = {(cuuint32_t)(g.kb * kQ8Step / 8), 8};
@@ -1165,7 +1175,8 @@ cudaError_t launch_t(const Q8MoeArgs &a, unsigned char *ws) {
         if ((!su && a.H >= kQ8Step && !encode_rows8(a.encode, &up, a.w_up, a.H, (int64_t)a.E * 2 * a.I, a.ldu)) ||
             (!sd && a.I >= kQ8Step && !encode_rows8(a.encode, &down, a.w_down, a.I, (int64_t)a.E * a.H, a.ldd)))
             return cudaErrorInvalidValue;
-        return launch_pdl(kern, a.sm_count > 0 ? a.sm_count : 1, ETHREADS, ESMEM, a.stream, up, down, a.T, a.E, a.top_k, a.H,
+        return launch_pdl(kern, a.sm_count > 0 ? a.sm_count : 1, ETHREADS, ESMEM, a.stream, up, down,
+                          EGeom(a.H, a.I, 8, su), EGeom(a.I, a.H, 16, sd), a.T, a.E, a.top_k, a.H,
                           a.I, a.renormalize, a.w_up, a.ldu, a.s_up, a.w_down, a.ldd, a.s_down, (T *)a.out, a.ldo,
                           a.ids, a.gates, ws, a.err, a.wait_ns);
     }
