@@ -57,7 +57,7 @@ int launch_status(cudaError_t e) {
     return SGEMM_ERR_CUDA;
 }
 
-int rows_call(const Q8RowsArgs &a) {
+int rows_call(Q8RowsArgs a) {
     if (a.M < 0 || a.K < 0) return SGEMM_ERR_BAD_DIM;
     if (!known_type(a.type)) return SGEMM_ERR_BAD_ARG;
     if (a.M == 0) return SGEMM_OK;
@@ -85,7 +85,7 @@ int rows_call(const Q8RowsArgs &a) {
             if (o->overlaps(*i) && !(o == &h && (i == &x || i == &r) && o->same(*i))) return SGEMM_ERR_ALIAS;
     if (h.overlaps(y) || h.overlaps(q) || h.overlaps(s) || y.overlaps(q) || y.overlaps(s) || q.overlaps(s))
         return SGEMM_ERR_ALIAS;
-    const int rc = device_args(nullptr, nullptr, nullptr, nullptr);
+    const int rc = device_args(nullptr, nullptr, &a.sm_count, nullptr);
     if (rc != SGEMM_OK) return rc;
     return launch_status(launch_q8_rows(a));
 }

@@ -12,9 +12,17 @@
 // once, to the stored h.
 //
 // Bound by memory: each of x, residual, h, y is touched once and q written
-// once.  One block takes one row and keeps it in registers between the
-// reduction and the store (rows up to 16384 elements); longer rows are read
-// twice.
+// once.  A row stays in registers between its reduction and its stores.  Which
+// kernel a call runs:
+//   q8_rows_warp   rows of at most 64 vectors, many of them: a warp a row, no
+//                  block barriers (at 128 vectors both take 20 us for 16384 rows);
+//   q8_rows        longer rows, few rows, any alignment: a block a row, all its
+//                  loads issued at once;
+//   q8_rows_long   rows beyond registers: read twice.
+// Measured and not kept for long rows (8192 x 4096, 4096 x 8192 in FP32, 2048 x
+// 16384, with residual: 46, 69 and 42 us with a block a row): persistent blocks
+// that prefetch the next row into registers 46, 89 and 44 us, into shared memory
+// with bulk copies 49, 122 and 64 us.
 #include "q8.cuh"
 
 namespace sgemm_gb300 {
@@ -43,63 +51,85 @@ __device__ __forceinline__ float row_scale(const RowQuant &rq, float lift, float
     return rq.step == 0.0f ? 0.0f : rq.step * (rq.unpre * lift) * r;
 }
 
-// One row per block, NV vectors of V elements per thread held in registers.
-template <typename T, int V, int NV>
-__global__ void __launch_bounds__(512)
-q8_rows_kernel(int64_t K, const T *x, int64_t ldx, const T *residual,
-               int64_t ldr, const float *__restrict__ weight, float eps, T *h, int64_t ldh, T *y,
-               int64_t ldy, int8_t *__restrict__ q, int64_t ldq, float *__restrict__ scale) {
-    __shared__ uint32_t red[64];
-    const int64_t row = blockIdx.x;
-    pdl_wait();
-    const T *xr = x + row * ldx;
-    const T *rr = residual ? residual + row * ldr : nullptr;
-    const int nvec = (int)(K / V);
-    float v[NV][V];
+// V elements as they come from memory, in one aligned access (two for 32 bytes).
+template <typename T, int V>
+struct Raw {
+    static constexpr int WORDS = V * (int)sizeof(T) / 4;
+    uint32_t w[WORDS];
+    __device__ __forceinline__ void load(const T *p) {
+        if constexpr (WORDS >= 4) {
 #pragma unroll
-    for (int i = 0; i < NV; ++i) {
-        const int c = threadIdx.x + i * (int)blockDim.x;
-        if (c < nvec) {
-            load_vec<T, V>(xr + (int64_t)c * V, v[i]);
+            for (int i = 0; i < WORDS / 4; ++i) {
+                const uint4 u = reinterpret_cast<const uint4 *>(p)[i];
+                w[4 * i] = u.x; w[4 * i + 1] = u.y; w[4 * i + 2] = u.z; w[4 * i + 3] = u.w;
+            }
         } else {
-#pragma unroll
-            for (int e = 0; e < V; ++e) v[i][e] = 0.0f;
+            const uint2 u = *reinterpret_cast<const uint2 *>(p);
+            w[0] = u.x; w[1] = u.y;
         }
     }
-    if (rr) {
-#pragma unroll
-        for (int i = 0; i < NV; ++i) {
-            const int c = threadIdx.x + i * (int)blockDim.x;
-            if (c < nvec) {
-                float t[V];
-                load_vec<T, V>(rr + (int64_t)c * V, t);
-#pragma unroll
-                for (int e = 0; e < V; ++e) v[i][e] += t[e];
-            }
-        }
+    __device__ __forceinline__ float operator[](int i) const {
+        if constexpr (sizeof(T) == 4) return __uint_as_float(w[i]);
+        else return __uint_as_float((i & 1) ? w[i >> 1] & 0xffff0000u : w[i >> 1] << 16);
     }
-    uint32_t mx = 0;
-    float ss = 0.0f;
+};
+template <typename T>
+struct Raw<T, 1> {
+    T v;
+    __device__ __forceinline__ void load(const T *p) { v = *p; }
+    __device__ __forceinline__ float operator[](int) const { return to_f32<T>(v); }
+};
+
+// The arrays of a call, and what happens to one row once its sums are known.
+template <typename T>
+struct Rows {
+    int64_t M, K;
+    const T *x;
+    int64_t ldx;
+    const T *residual;
+    int64_t ldr;
+    const float *weight;
+    float eps;
+    T *h;
+    int64_t ldh;
+    T *y;
+    int64_t ldy;
+    int8_t *q;
+    int64_t ldq;
+    float *scale;
+};
+
+// One vector's part in the row's sums: v = x (+ residual), h stored, the largest
+// |p| and the sum of squares extended.
+template <typename T, int V>
+__device__ __forceinline__ void take_vector(const Rows<T> &a, int64_t row, int c, float (&v)[V], uint32_t &mx,
+                                            float &ss) {
+    if (a.h) store_vec<T, V>(a.h + row * a.ldh + (int64_t)c * V, v);
+    if (a.weight) {
+        float w[V];
+        load_vec<float, V>(a.weight + (int64_t)c * V, w);
 #pragma unroll
-    for (int i = 0; i < NV; ++i) {
-        const int c = threadIdx.x + i * (int)blockDim.x;
-        if (c < nvec) {
-            if (h) store_vec<T, V>(h + row * ldh + (int64_t)c * V, v[i]);
-            float w[V];
-            if (weight) load_vec<float, V>(weight + (int64_t)c * V, w);
-#pragma unroll
-            for (int e = 0; e < V; ++e) {
-                ss = fmaf(v[i][e], v[i][e], ss);
-                mx = max(mx, abs_bits(weight ? v[i][e] * w[e] : v[i][e]));
-            }
+        for (int e = 0; e < V; ++e) {
+            ss = fmaf(v[e], v[e], ss);
+            mx = max(mx, abs_bits(v[e] * w[e]));
         }
+    } else {
+#pragma unroll
+        for (int e = 0; e < V; ++e) mx = max(mx, abs_bits(v[e]));
     }
-    block_max_sum(mx, ss, red);
+}
+
+// The row's results from its vectors c = first, first + step, ... in registers;
+// `reduce` sums over the threads that share the row.
+template <typename T, int V, int NV, typename Reduce>
+__device__ __forceinline__ void finish_row(const Rows<T> &a, int64_t row, int first, int step, float (&v)[NV][V],
+                                           uint32_t mx, float ss, Reduce reduce) {
+    const int nvec = (int)(a.K / V);
     const RowQuant rq(mx);
     float r = 1.0f, lift = 1.0f;
-    if (weight) {
-        r = inv_rms(ss, K, eps);   // 0 for an infinite row, NaN for one with a NaN
-        lift = norm_lift(ss, K, eps, mx);
+    if (a.weight) {
+        r = inv_rms(ss, a.K, a.eps);   // 0 for an infinite row, NaN for one with a NaN
+        lift = norm_lift(ss, a.K, a.eps, mx);
         if (lift != 1.0f) {
             float s2 = 0.0f;
 #pragma unroll
@@ -110,29 +140,94 @@ q8_rows_kernel(int64_t K, const T *x, int64_t ldx, const T *residual,
                     s2 = fmaf(t, t, s2);
                 }
             uint32_t none = 0;
-            block_max_sum(none, s2, red);
-            r = inv_rms(s2, K, lift > 1.0f ? eps * lift * lift : 0.0f);
+            reduce(none, s2);
+            r = inv_rms(s2, a.K, lift > 1.0f ? a.eps * lift * lift : 0.0f);
         }
     }
-    if (threadIdx.x == 0) scale[row] = row_scale(rq, lift, r);
+    if (first == 0) a.scale[row] = row_scale(rq, lift, r);
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-        const int c = threadIdx.x + i * (int)blockDim.x;
+        const int c = first + i * step;
         if (c < nvec) {
-            if (weight) {
+            if (a.weight) {
                 float w[V];
-                load_vec<float, V>(weight + (int64_t)c * V, w);
+                load_vec<float, V>(a.weight + (int64_t)c * V, w);
 #pragma unroll
                 for (int e = 0; e < V; ++e) v[i][e] *= w[e];
-                if (y) {
+                if (a.y) {
                     float t[V];
 #pragma unroll
-                    for (int e = 0; e < V; ++e) t[e] = v[i][e] * lift * r;
-                    store_vec<T, V>(y + row * ldy + (int64_t)c * V, t);
+                    for (int e = 0; e < V; ++e) t[e] = lift == 1.0f ? v[i][e] * r : v[i][e] * lift * r;
+                    store_vec<T, V>(a.y + row * a.ldy + (int64_t)c * V, t);
                 }
             }
-            store_q<V>(q + row * ldq + (int64_t)c * V, rq, v[i]);
+            store_q<V>(a.q + row * a.ldq + (int64_t)c * V, rq, v[i]);
         }
+    }
+}
+
+// A row's vectors straight from memory, all loads issued before the first use.
+template <typename T, int V, int NV>
+__device__ __forceinline__ void load_row(const Rows<T> &a, int64_t row, int first, int step, float (&v)[NV][V],
+                                         uint32_t &mx, float &ss) {
+    const int nvec = (int)(a.K / V);
+    Raw<T, V> rx[NV], rr[NV];
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+        const int c = first + i * step;
+        if (c < nvec) {
+            rx[i].load(a.x + row * a.ldx + (int64_t)c * V);
+            if (a.residual) rr[i].load(a.residual + row * a.ldr + (int64_t)c * V);
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+        const int c = first + i * step;
+#pragma unroll
+        for (int e = 0; e < V; ++e) v[i][e] = 0.0f;
+        if (c < nvec) {
+#pragma unroll
+            for (int e = 0; e < V; ++e) {
+                v[i][e] = rx[i][e];
+                if (a.residual) v[i][e] += rr[i][e];
+            }
+            take_vector<T, V>(a, row, c, v[i], mx, ss);
+        }
+    }
+}
+
+// A block per row.
+template <typename T, int V, int NV>
+__global__ void __launch_bounds__(512) q8_rows_kernel(const Rows<T> a) {
+    __shared__ uint32_t red[64];
+    pdl_wait();
+    float v[NV][V];
+    uint32_t mx = 0;
+    float ss = 0.0f;
+    load_row<T, V, NV>(a, blockIdx.x, threadIdx.x, blockDim.x, v, mx, ss);
+    block_max_sum(mx, ss, red);
+    finish_row<T, V, NV>(a, blockIdx.x, threadIdx.x, blockDim.x, v, mx, ss,
+                         [&](uint32_t &m, float &s) { block_max_sum(m, s, red); });
+}
+
+// A warp per row.
+constexpr int WARP_ROWS = 8;    // warps of a block
+template <typename T, int V, int NV>
+__global__ void __launch_bounds__(WARP_ROWS * 32, 4) q8_rows_warp_kernel(const Rows<T> a) {
+    pdl_wait();
+    const int lane = threadIdx.x & 31;
+    auto reduce = [](uint32_t &m, float &s) {
+        m = __reduce_max_sync(0xffffffffu, m);
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+    };
+    for (int64_t row = (int64_t)blockIdx.x * WARP_ROWS + (threadIdx.x >> 5); row < a.M; row += (int64_t)gridDim.x * WARP_ROWS) {
+        float v[NV][V];
+        uint32_t mx = 0;
+        float ss = 0.0f;
+        load_row<T, V, NV>(a, row, lane, 32, v, mx, ss);
+        reduce(mx, ss);
+        finish_row<T, V, NV>(a, row, lane, 32, v, mx, ss, reduce);
     }
 }
 
@@ -185,10 +280,11 @@ q8_rows_long_kernel(int64_t K, const T *x, int64_t ldx, const T *residual, int64
 }
 
 template <typename K, typename... A>
-cudaError_t launch_rows_pdl(K kern, dim3 grid, int threads, cudaStream_t s, A... args) {
+cudaError_t launch_rows_pdl(K kern, dim3 grid, int threads, size_t smem, cudaStream_t s, A... args) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = grid;
     cfg.blockDim = dim3((unsigned)threads, 1, 1);
+    cfg.dynamicSmemBytes = smem;
     cfg.stream = s;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -198,33 +294,53 @@ cudaError_t launch_rows_pdl(K kern, dim3 grid, int threads, cudaStream_t s, A...
     return cudaLaunchKernelEx(&cfg, kern, args...);
 }
 
-template <typename T, int V, int NV>
-cudaError_t launch_reg(const Q8RowsArgs &a, int threads) {
-    return launch_rows_pdl(q8_rows_kernel<T, V, NV>, dim3((unsigned)a.M), threads, a.stream, a.K,
-                           (const T *)a.x, a.ldx, (const T *)a.residual, a.ldr, a.weight, a.eps,
-                           (T *)a.h, a.ldh, (T *)a.y, a.ldy, a.q, a.ldq, a.scale);
+template <typename T>
+Rows<T> rows_of(const Q8RowsArgs &a) {
+    return {a.M, a.K, (const T *)a.x, a.ldx, (const T *)a.residual, a.ldr, a.weight, a.eps, (T *)a.h, a.ldh,
+            (T *)a.y, a.ldy, a.q, a.ldq, a.scale};
 }
 
-// Vectors per thread: as few as 512 threads a row allow.
+// Vectors per thread: as few as `most` threads a row allow; 0 if it takes more than 16.
+int vectors_per_thread(int64_t nvec, int most) {
+    for (int nv = 1; nv <= 16; nv *= 2)
+        if (nvec <= (int64_t)most * nv) return nv;
+    return 0;
+}
+int threads_for(int64_t nvec, int nv) {
+    const int t = (int)(((nvec + nv - 1) / nv + 31) / 32 * 32);
+    return t < 32 ? 32 : t;
+}
+
 template <typename T, int V>
-cudaError_t launch_v(const Q8RowsArgs &a) {
+cudaError_t launch_block(const Q8RowsArgs &a) {
     const int64_t nvec = a.K / V;
-    const int nv = nvec <= 512 ? 1 : nvec <= 1024 ? 2 : nvec <= 2048 ? 4 : nvec <= 4096 ? 8 : 16;
-    int threads = (int)((((nvec + nv - 1) / nv) + 31) / 32 * 32);
-    if (threads < 32) threads = 32;
+    const int nv = vectors_per_thread(nvec, 512), threads = threads_for(nvec, nv);
+    const dim3 grid((unsigned)a.M);
+    const Rows<T> r = rows_of<T>(a);
     switch (nv) {
-        case 1: return launch_reg<T, V, 1>(a, threads);
-        case 2: return launch_reg<T, V, 2>(a, threads);
-        case 4: return launch_reg<T, V, 4>(a, threads);
+        case 1: return launch_rows_pdl(q8_rows_kernel<T, V, 1>, grid, threads, 0, a.stream, r);
+        case 2: return launch_rows_pdl(q8_rows_kernel<T, V, 2>, grid, threads, 0, a.stream, r);
+        case 4: return launch_rows_pdl(q8_rows_kernel<T, V, 4>, grid, threads, 0, a.stream, r);
         default: break;
     }
     if constexpr (V <= 4) {
-        if (nv == 8) return launch_reg<T, V, 8>(a, threads);
+        if (nv == 8) return launch_rows_pdl(q8_rows_kernel<T, V, 8>, grid, threads, 0, a.stream, r);
     }
     if constexpr (V == 1) {
-        if (nv == 16) return launch_reg<T, V, 16>(a, threads);
+        if (nv == 16) return launch_rows_pdl(q8_rows_kernel<T, V, 16>, grid, threads, 0, a.stream, r);
     }
     return cudaErrorInvalidValue;
+}
+
+template <typename T, int V>
+cudaError_t launch_warp(const Q8RowsArgs &a) {
+    const int64_t blocks = (a.M + WARP_ROWS - 1) / WARP_ROWS, most = (int64_t)a.sm_count * 8;
+    const dim3 grid((unsigned)(blocks < most ? blocks : most));
+    const Rows<T> r = rows_of<T>(a);
+    switch (vectors_per_thread(a.K / V, 32)) {
+        case 1: return launch_rows_pdl(q8_rows_warp_kernel<T, V, 1>, grid, WARP_ROWS * 32, 0, a.stream, r);
+        default: return launch_rows_pdl(q8_rows_warp_kernel<T, V, 2>, grid, WARP_ROWS * 32, 0, a.stream, r);
+    }
 }
 
 template <typename T>
@@ -240,10 +356,12 @@ cudaError_t launch_t(const Q8RowsArgs &a) {
                ok(a.h, a.ldh, sizeof(T), v) && ok(a.y, a.ldy, sizeof(T), v) && ok(a.q, a.ldq, 1, v) &&
                ok(a.weight, 0, 4, v);
     };
-    if (a.K <= 16384 && fits(8)) return launch_v<T, 8>(a);
-    if (a.K <= 16384 && fits(4)) return launch_v<T, 4>(a);
-    if (a.K <= 8192) return launch_v<T, 1>(a);
-    return launch_rows_pdl(q8_rows_long_kernel<T>, dim3((unsigned)a.M), 1024, a.stream, a.K,
+    constexpr int V16 = 16 / (int)sizeof(T);       // elements of a 16-byte access
+    if (a.K > 0 && a.K <= 64 * V16 && fits(V16) && a.M > 2 * (int64_t)a.sm_count) return launch_warp<T, V16>(a);
+    if (a.K <= 16384 && fits(8)) return launch_block<T, 8>(a);
+    if (a.K <= 16384 && fits(4)) return launch_block<T, 4>(a);
+    if (a.K <= 8192) return launch_block<T, 1>(a);
+    return launch_rows_pdl(q8_rows_long_kernel<T>, dim3((unsigned)a.M), 1024, 0, a.stream, a.K,
                            (const T *)a.x, a.ldx, (const T *)a.residual, a.ldr, a.weight, a.eps,
                            (T *)a.h, a.ldh, (T *)a.y, a.ldy, a.q, a.ldq, a.scale);
 }
