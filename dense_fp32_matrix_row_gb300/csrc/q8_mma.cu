@@ -577,38 +577,39 @@ q8_mma_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ C
 // FP16 [M][ldh], ldh a multiple of 64, zeros past K; rows of W that TMA cannot
 // address (O not NULL) as [N][ldo], ldo a multiple of 16, zeros past K; and
 // `nzero` counters cleared.
+// Blocks of 256 threads, `wide` of them (a power of two, 1 << shift) to a row.
 __global__ void __launch_bounds__(256)
 q8_prepare_kernel(int M, int N, int K, const int8_t *__restrict__ X, int64_t ldx, int vec, uint16_t *__restrict__ H,
                   int64_t ldh, const int8_t *__restrict__ W, int64_t ldw, int8_t *__restrict__ O, int64_t ldo,
-                  uint32_t *zero, int nzero) {
+                  int shift, uint32_t *zero, int nzero) {
     pdl_wait();
     pdl_trigger();
-    const int64_t i0 = (int64_t)blockIdx.x * blockDim.x + threadIdx.x, stride = (int64_t)gridDim.x * blockDim.x;
-    for (int64_t i = i0; i < nzero; i += stride) zero[i] = 0u;
-    const int64_t xrow = ldh / 16, xtotal = xrow * M;
-    for (int64_t i = i0; i < xtotal; i += stride) {
-        const int64_t m = i / xrow, k = (i - m * xrow) * 16;
-        const int8_t *p = X + m * ldx + k;
-        uint4 v;
-        if (k + 16 > K) v = load16_bytes(p, (int)max((int64_t)0, K - k));
-        else if (vec) v = *reinterpret_cast<const uint4 *>(p);
-        else v = load16_unaligned(p, X, X + (int64_t)(M - 1) * ldx + K);
-        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-        uint32_t r[8];
+    const int64_t row0 = ((int64_t)blockIdx.x << (8 - shift)) + (threadIdx.x >> shift);
+    const int64_t rows = (int64_t)gridDim.x << (8 - shift);
+    const int c0 = 16 * (int)(threadIdx.x & ((1u << shift) - 1)), step = 16 << shift;
+    for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < nzero; i += (int64_t)gridDim.x * 256) zero[i] = 0u;
+    for (int64_t m = row0; m < M; m += rows)
+        for (int k = c0; k < ldh; k += step) {
+            const int8_t *p = X + m * ldx + k;
+            uint4 v;
+            if (k + 16 > K) v = load16_bytes(p, max(0, K - k));
+            else if (vec) v = *reinterpret_cast<const uint4 *>(p);
+            else v = load16_unaligned(p, X, X + (int64_t)(M - 1) * ldx + K);
+            const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+            uint32_t r[8];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) q8_to_f16(w[j], r[2 * j], r[2 * j + 1]);
-        uint4 *o = reinterpret_cast<uint4 *>(H + m * ldh + k);
-        o[0] = make_uint4(r[0], r[1], r[2], r[3]);
-        o[1] = make_uint4(r[4], r[5], r[6], r[7]);
-    }
+            for (int j = 0; j < 4; ++j) q8_to_f16(w[j], r[2 * j], r[2 * j + 1]);
+            uint4 *o = reinterpret_cast<uint4 *>(H + m * ldh + k);
+            o[0] = make_uint4(r[0], r[1], r[2], r[3]);
+            o[1] = make_uint4(r[4], r[5], r[6], r[7]);
+        }
     if (O == nullptr) return;
-    const int64_t wrow = ldo / 16, wtotal = wrow * N;
-    for (int64_t i = i0; i < wtotal; i += stride) {
-        const int64_t n = i / wrow, k = (i - n * wrow) * 16;
-        const int8_t *p = W + n * ldw + k;
-        *reinterpret_cast<uint4 *>(O + n * ldo + k) =
-            k + 16 > K ? load16_bytes(p, (int)(K - k)) : load16_unaligned(p, W, W + (int64_t)(N - 1) * ldw + K);
-    }
+    for (int64_t n = row0; n < N; n += rows)
+        for (int k = c0; k < ldo; k += step) {
+            const int8_t *p = W + n * ldw + k;
+            *reinterpret_cast<uint4 *>(O + n * ldo + k) =
+                k + 16 > K ? load16_bytes(p, K - k) : load16_unaligned(p, W, W + (int64_t)(N - 1) * ldw + K);
+        }
 }
 
 bool encode_bytes(EncodeTiledFn enc, CUtensorMap *map, const int8_t *base, int64_t inner, int64_t rows, int64_t ld,
@@ -755,11 +756,6 @@ bool w_aligned(const Q8LinearArgs &a) {
     return reinterpret_cast<uintptr_t>(a.W) % 16 == 0 && a.ldw % 16 == 0;
 }
 
-unsigned grid_for(int64_t items, int sms) {
-    const int64_t blocks = (items + 255) / 256, most = (int64_t)sms * 8;
-    return (unsigned)(blocks < 1 ? 1 : blocks < most ? blocks : most);
-}
-
 }  // namespace
 
 bool q8_mma_can_run(const Q8LinearArgs &a) {
@@ -780,11 +776,15 @@ cudaError_t launch_q8_mma(const Q8LinearArgs &a, void *workspace) {
     int8_t *copy = copy_w ? reinterpret_cast<int8_t *>(ws + l.w) : nullptr;
     const int8_t *W = copy_w ? copy : a.W;
     const int vec = reinterpret_cast<uintptr_t>(a.X) % 16 == 0 && a.ldx % 16 == 0;
-    const int64_t items = std::max(a.M * (l.ldh / 16), copy_w ? a.N * (l.ldw / 16) : 0);
-    const cudaError_t e = launch_with(q8_prepare_kernel, grid_for(items, a.sm_count), 256, 0, 1, a.stream, (int)a.M,
-                                      (int)a.N, (int)a.K, a.X, a.ldx, vec, reinterpret_cast<uint16_t *>(ws + l.x),
-                                      l.ldh, a.W, a.ldw, copy, l.ldw, reinterpret_cast<uint32_t *>(ws + l.counters),
-                                      l.ncounters);
+    // threads to a row: a 16-byte piece each, up to a whole block
+    int shift = 2;
+    while (shift < 8 && (16 << shift) < a.K) ++shift;
+    const int64_t rows = std::max(a.M, copy_w ? a.N : 0), blocks = (rows + (256 >> shift) - 1) >> (8 - shift);
+    const int64_t most = (int64_t)(a.sm_count > 0 ? a.sm_count : 1) * 8;
+    const cudaError_t e = launch_with(q8_prepare_kernel, (unsigned)(blocks < most ? blocks : most), 256, 0, 1, a.stream,
+                                      (int)a.M, (int)a.N, (int)a.K, a.X, a.ldx, vec,
+                                      reinterpret_cast<uint16_t *>(ws + l.x), l.ldh, a.W, a.ldw, copy, l.ldw, shift,
+                                      reinterpret_cast<uint32_t *>(ws + l.counters), l.ncounters);
     if (e != cudaSuccess) return e;
     return a.type == kTypeBf16 ? launch_o<__nv_bfloat16>(a, c, l, ws, W) : launch_o<float>(a, c, l, ws, W);
 }

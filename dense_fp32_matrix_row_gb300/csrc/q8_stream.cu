@@ -71,16 +71,17 @@ q8_stream_kernel(int M, int N, int K, const int8_t *__restrict__ X, int64_t ldx,
 // ---- the ring ------------------------------------------------------------------
 
 constexpr uint64_t DRAIN_NS = 1000000000ull;
-
-// NB blocks of 8 tokens; RT 16-row tiles per stage, RW of them per warp.
-template <int NB_, int RT_, int RW_, int STEPS_, int RING_>
+// NB blocks of 8 tokens; RT 16-row tiles per stage, RW of them per warp.  DP > 0: at
+// most DP tokens, by dp4a.
+template <int DP_, int NB_, int RT_, int RW_, int STEPS_, int RING_>
 struct RingCfg {
     using S = Q8Stage<RT_, RW_, STEPS_>;
-    static constexpr int NB = NB_, RT = RT_, RW = RW_, RING = RING_;
+    static constexpr int DP = DP_, NB = NB_, RT = RT_, RW = RW_, RING = RING_;
+    static constexpr int XN = DP > 0 ? DP : NB;                      // token rows a lane reads
+    static_assert(DP == 0 || (NB == 1 && RW == 1 && DP <= 8), "dp4a takes one block of tokens");
     static constexpr int TOK = NB * 8, TILE = S::ROWS * TOK;
     static constexpr int THREADS = (kQ8Consumers + RT) * 32;         // RT producer warps
-    static constexpr int PART = kQ8Consumers * RW * NB * 32;         // int4 of one tile's sums
-    static constexpr size_t SMEM = 128 + (size_t)RING * S::BYTES + 2 * (size_t)PART * 16 + 256;
+    static constexpr size_t SMEM = 128 + (size_t)RING * S::BYTES + 2 * (size_t)TILE * 4 + 256;
     static_assert(SMEM <= 227 * 1024, "shared memory per block");
 };
 
@@ -91,13 +92,13 @@ q8_ring_kernel(int M, int N, int K, const int8_t *__restrict__ X,
                const float *__restrict__ ws, Epilogue ep, OutT *__restrict__ out, int64_t ldc, unsigned *err,
                uint64_t wait_ns) {
     using S = typename C::S;
-    constexpr int NB = C::NB, RT = C::RT, RW = C::RW, RING = C::RING;
+    constexpr int DP = C::DP, XN = C::XN, NB = C::NB, RT = C::RT, RW = C::RW, RING = C::RING;
     constexpr int TOK = C::TOK, ROWS = S::ROWS, KB = S::KB, KW = S::KW, STEPS = S::STEPS;
     extern __shared__ unsigned char smem_raw[];
     const uintptr_t base = (reinterpret_cast<uintptr_t>(smem_raw) + 127) & ~uintptr_t(127);
     unsigned char *ring = reinterpret_cast<unsigned char *>(base);
-    int4 *sums = reinterpret_cast<int4 *>(ring + (size_t)RING * S::BYTES);   // [2][warp][RW][NB][lane]
-    uint64_t *full = reinterpret_cast<uint64_t *>(sums + 2 * C::PART);
+    int *sums = reinterpret_cast<int *>(ring + (size_t)RING * S::BYTES);   // [2][row tile][NB][word][lane]
+    uint64_t *full = reinterpret_cast<uint64_t *>(sums + 2 * C::TILE);
     uint64_t *empty = full + RING;
     uint64_t *tdone = empty + RING;                       // [2] all warps have added their sums
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -115,6 +116,7 @@ q8_ring_kernel(int M, int N, int K, const int8_t *__restrict__ X,
         mbar_init(smem_u32(&tdone[1]), kQ8Consumers);
         mbar_fence_init();
     }
+    for (int i = threadIdx.x; i < 2 * C::TILE; i += C::THREADS) sums[i] = 0;
     __syncthreads();
     pdl_wait();
 
@@ -150,18 +152,18 @@ q8_ring_kernel(int M, int N, int K, const int8_t *__restrict__ X,
 
     const int g = lane >> 2, t4 = lane & 3;
     const int rt = warp / KW * RW, kpart = warp % KW;   // first row tile, share of the steps
-    const int8_t *x[NB];
+    const int8_t *x[XN];
 #pragma unroll
-    for (int n = 0; n < NB; ++n) x[n] = X + (int64_t)min(m0 + 8 * n + g, M - 1) * ldx + 16 * t4;
+    for (int n = 0; n < XN; ++n) x[n] = X + (int64_t)min(m0 + (DP > 0 ? n : 8 * n + g), M - 1) * ldx + 16 * t4;
     const int8_t *xend = X + (int64_t)(M - 1) * ldx + K;
     // this lane's 16 bytes of rows g and g + 8 in the warp's first step
     const uint32_t wa = (uint32_t)(rt * 16 + g) * S::LD + (uint32_t)(kpart * STEPS * kQ8Step + 16 * t4);
     const uint32_t wb = wa + 8 * S::LD;
     // tokens do not depend on the tile: the same steps come round every time
-    uint4 xnext[STEPS][NB];
+    uint4 xnext[STEPS][XN];
     auto xload = [&](int u, int step) {
 #pragma unroll
-        for (int n = 0; n < NB; ++n) {
+        for (int n = 0; n < XN; ++n) {
             const int8_t *p = x[n] + (int64_t)step * kQ8Step;
             if (step < blocks)
                 xnext[u][n] = xvec ? __ldg(reinterpret_cast<const uint4 *>(p)) : load16_unaligned(p, X, xend);
@@ -170,13 +172,13 @@ q8_ring_kernel(int M, int N, int K, const int8_t *__restrict__ X,
 #pragma unroll
     for (int u = 0; u < STEPS; ++u) {
 #pragma unroll
-        for (int n = 0; n < NB; ++n) xnext[u][n] = make_uint4(0u, 0u, 0u, 0u);
+        for (int n = 0; n < XN; ++n) xnext[u][n] = make_uint4(0u, 0u, 0u, 0u);
         xload(u, kpart * STEPS + u);
     }
     uint32_t used = 0;      // stages read
     uint32_t count = 0;     // tiles finished
     for (int t = blockIdx.x; t < tiles; t += gridDim.x, ++count) {
-        int sum[RW][NB][4];
+        int sum[RW][NB][4], dsum[XN][2];
         float acc[RW][NB][4];
 #pragma unroll
         for (int r = 0; r < RW; ++r)
@@ -187,17 +189,19 @@ q8_ring_kernel(int M, int N, int K, const int8_t *__restrict__ X,
                     sum[r][n][i] = 0;
                     acc[r][n][i] = 0.0f;
                 }
+#pragma unroll
+        for (int j = 0; j < XN; ++j) dsum[j][0] = dsum[j][1] = 0;
         auto flush = [&] {
 #pragma unroll
             for (int r = 0; r < RW; ++r) q8_flush<NB>(sum[r], acc[r]);
         };
-        // This thread's results of the tile: word e of the sums' layout, where
-        // words follow the fragments (lane, then 4 words: rows g, g, g + 8, g + 8,
-        // tokens 2 t4, + 1, 2 t4, + 1).  Their scales are asked for now.
+        // This thread's results of the tile: word e of the sums' layout, which
+        // follows the fragments (4 words of 32 lanes: rows g, g, g + 8, g + 8, tokens
+        // 2 t4, + 1, 2 t4, + 1).  Their scales are asked for now.
         constexpr int OUTS = C::TILE, PER = (OUTS + kQ8Consumers * 32 - 1) / (kQ8Consumers * 32);
         const int n0 = t * ROWS;
         auto place = [&](int e, int &row, int &tok) {
-            const int i = e & 3, l = (e >> 2) & 31, frag = e >> 7;      // frag: (tile of the stage, token block)
+            const int l = e & 31, i = (e >> 5) & 3, frag = e >> 7;      // frag: (tile of the stage, token block)
             row = frag / NB * 16 + (l >> 2) + 8 * (i >> 1);
             tok = frag % NB * 8 + 2 * (l & 3) + (i & 1);
         };
@@ -233,7 +237,8 @@ q8_ring_kernel(int M, int N, int K, const int8_t *__restrict__ X,
                         a[w] = lds128(stage + wa + (uint32_t)w * 16 * S::LD + (uint32_t)u * kQ8Step);
                         b[w] = lds128(stage + wb + (uint32_t)w * 16 * S::LD + (uint32_t)u * kQ8Step);
                     }
-                    if constexpr (NB == 1 && RW == 1) q8_step_s8(sum[0][0], a[0], b[0], xnext[u][0]);
+                    if constexpr (DP > 0) q8_step_dp<XN>(dsum, a[0], b[0], xnext[u]);
+                    else if constexpr (NB == 1) q8_step_s8(sum[0][0], a[0], b[0], xnext[u][0]);
                     else q8_step_rows<RW, NB>(acc, a, b, xnext[u]);
                 }
                 xload(u, bn + u);
@@ -249,26 +254,47 @@ q8_ring_kernel(int M, int N, int K, const int8_t *__restrict__ X,
         if (K % kQ8Step != 0 && kpart == 0) {   // the last values of each row
             const int valid = min(16, max(0, K - blocks * kQ8Step - 16 * t4));
             const int64_t k = (int64_t)blocks * kQ8Step + 16 * t4;
-            uint4 xt[NB], a[RW], b[RW];
+            uint4 xt[XN], a[RW], b[RW];
 #pragma unroll
-            for (int n = 0; n < NB; ++n) xt[n] = load16_bytes(x[n] + (int64_t)blocks * kQ8Step, valid);
+            for (int n = 0; n < XN; ++n) xt[n] = load16_bytes(x[n] + (int64_t)blocks * kQ8Step, valid);
 #pragma unroll
             for (int w = 0; w < RW; ++w) {
                 const int row = n0 + (rt + w) * 16 + g;
                 a[w] = load16_bytes(W + (int64_t)min(row, N - 1) * ldw + k, valid);
                 b[w] = load16_bytes(W + (int64_t)min(row + 8, N - 1) * ldw + k, valid);
             }
-            flush();      // a chunk of its own
-            q8_step_rows<RW, NB>(acc, a, b, xt);
+            if constexpr (DP > 0) {
+                q8_step_dp<XN>(dsum, a[0], b[0], xt);
+            } else if constexpr (NB == 1) {
+                q8_step_s8(sum[0][0], a[0], b[0], xt[0]);
+            } else {
+                flush();      // a chunk of its own
+                q8_step_rows<RW, NB>(acc, a, b, xt);
+            }
         }
         flush();
-        int4 *tile = sums + (count & 1) * C::PART;
+        // whole numbers: the order of these additions does not matter
+        int *tile = sums + (count & 1) * C::TILE;
+        if constexpr (DP > 0) {
 #pragma unroll
-        for (int w = 0; w < RW; ++w)
+            for (int j = 0; j < XN; ++j)
 #pragma unroll
-            for (int n = 0; n < NB; ++n)
-                tile[((warp * RW + w) * NB + n) * 32 + lane] =
-                    make_int4(sum[w][n][0], sum[w][n][1], sum[w][n][2], sum[w][n][3]);
+                for (int i = 0; i < 2; ++i) {
+                    int v = dsum[j][i];
+                    v += __shfl_xor_sync(0xffffffffu, v, 1);
+                    v += __shfl_xor_sync(0xffffffffu, v, 2);
+                    // one lane of the quad: where the MMA would leave (row, token j)
+                    if (t4 == (j >> 1)) atomicAdd(&tile[(rt * 4 + 2 * i + (j & 1)) * 32 + lane], v);
+                }
+        } else {
+#pragma unroll
+            for (int w = 0; w < RW; ++w)
+#pragma unroll
+                for (int n = 0; n < NB; ++n)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        atomicAdd(&tile[(((rt + w) * NB + n) * 4 + i) * 32 + lane], sum[w][n][i]);
+        }
         __syncwarp();
         const uint32_t bar = smem_u32(&tdone[count & 1]);
         if (lane == 0) mbar_arrive(bar);
@@ -282,15 +308,10 @@ q8_ring_kernel(int M, int N, int K, const int8_t *__restrict__ X,
             const int e = (int)threadIdx.x + i * kQ8Consumers * 32;
             place(e, row, tok);
             const int n = n0 + row, m = m0 + tok;
-            if (e < OUTS && n < N && m < M) {
-                // the KW warps that share this tile's steps (whole numbers: any order)
-                const int frag = e >> 7, rtile = frag / NB;
-                const int *v = reinterpret_cast<const int *>(tile) +
-                               ((rtile / RW * KW * RW + rtile % RW) * NB + frag % NB) * 128 + (e & 127);
-                int total = 0;
-#pragma unroll
-                for (int w = 0; w < KW; ++w) total += v[w * RW * NB * 128];
-                out[(int64_t)m * ldc + n] = from_f32<OutT>(epilogue_tail(ep, (float)total * sx[i] * sw[i], n));
+            if (e < OUTS) {
+                if (n < N && m < M)
+                    out[(int64_t)m * ldc + n] = from_f32<OutT>(epilogue_tail(ep, (float)tile[e] * sx[i] * sw[i], n));
+                tile[e] = 0;
             }
         }
     }
@@ -341,12 +362,19 @@ cudaError_t launch_ring(const Q8LinearArgs &a) {
 }
 
 // Rows per stage: as many k as the row has, up to 4096 (1024 for 16 tokens).
+template <int DP, typename OutT>
+cudaError_t launch_8(const Q8LinearArgs &a) {
+    if (a.K <= 1024) return launch_ring<RingCfg<DP, 1, 4, 1, 2, 5>, OutT>(a);
+    if (a.K <= 2048) return launch_ring<RingCfg<DP, 1, 2, 1, 4, 3>, OutT>(a);
+    return launch_ring<RingCfg<DP, 1, 1, 1, 4, 3>, OutT>(a);
+}
+
 template <typename OutT>
 cudaError_t launch_r(const Q8LinearArgs &a) {
-    if (a.M > 8) return launch_ring<RingCfg<2, 2, 2, 1, 4>, OutT>(a);
-    if (a.K <= 1024) return launch_ring<RingCfg<1, 4, 1, 2, 5>, OutT>(a);
-    if (a.K <= 2048) return launch_ring<RingCfg<1, 2, 1, 4, 3>, OutT>(a);
-    return launch_ring<RingCfg<1, 1, 1, 4, 3>, OutT>(a);
+    if (a.M == 1) return launch_8<1, OutT>(a);
+    if (a.M == 2) return launch_8<2, OutT>(a);   // 4 tokens' bytes no longer fit the registers
+    if (a.M <= 8) return launch_8<0, OutT>(a);
+    return launch_ring<RingCfg<0, 2, 2, 2, 1, 5>, OutT>(a);
 }
 
 template <typename OutT>

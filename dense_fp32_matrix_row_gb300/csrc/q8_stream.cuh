@@ -195,16 +195,16 @@ __device__ __forceinline__ void q8_dot(int (&sum)[NB][4], const int8_t *wa, cons
 // tile's are issued by a warp of their own.  Rows lie 64 bytes further apart
 // than they are long, so that the 128-bit reads of a fragment, rows g and g + 1
 // together, meet no bank conflict.  Sixteen consumer warps take STEPS steps
-// each, of RW tiles.  Their sums of a tile, integers, meet in shared memory
-// (as 16-byte stores and one pass of reads: 256 shared-memory atomics a tile
-// took as long as its products).
+// each, of RW tiles.  Their sums of a tile, integers, are added in shared memory,
+// a word per lane of each fragment (no bank conflict).
 //
 // Up to 8 tokens the products are 8-bit MMAs (mma.sync m16n8k32 s8): exact
 // without any expansion, and although sm_103a runs them at a sixteenth of the
 // FP16 rate per byte, 31 bytes of W per cycle and SM is more than memory brings
-// (23).  For 16 tokens that halves, and the FP16 form takes over; there a warp
-// takes RW = 2 row tiles, so that the tokens' bytes, which would otherwise be as
-// many as W's, are fetched and expanded half as often.
+// (23).  For 16 tokens that halves, and the FP16 form takes over (alternate steps
+// by one and the other ran 35% slower than FP16 alone).  There a warp takes RW = 2
+// row tiles, so that the tokens' bytes, which would otherwise be as many as W's,
+// are fetched half as often.  For one or two tokens dp4a is cheaper still.
 constexpr int kQ8Consumers = 16;
 template <int RT, int RW, int STEPS_>
 struct Q8Stage {
