@@ -10,8 +10,19 @@ using namespace sgemm_gb300;
 namespace {
 
 constexpr int64_t kMaxElems = int64_t(1) << 40;
-// Products of at most this many tokens run the streaming kernel.
+// Which products stream W past 16 tokens at a time instead of running on the
+// tensor cores' tiles: up to 16 tokens (16 x 8192 x 4096: 10.8 against 13.3 us),
+// and as long as blocks of 16 tokens x 32 channels give every SM at most two,
+// where the tiles' set-up counts for more than reading W again (128 x 512 x 512
+// 3.3 against 8.4 us, 64 x 2048 x 4096 11.5 either way; at four to an SM, 64 x
+// 4096 x 1024, 11.8 against 8.4).  The latter needs the fast streaming kernel,
+// for which W is 16-byte aligned.
 constexpr int64_t kStreamTokens = 16;
+bool streams(const Q8LinearArgs &a) {
+    if (a.M <= kStreamTokens) return true;
+    const bool aligned = reinterpret_cast<uintptr_t>(a.W) % 16 == 0 && a.ldw % 16 == 0 && a.K >= 64;
+    return aligned && ((a.M + 15) / 16) * ((a.N + 31) / 32) <= 2 * (int64_t)a.sm_count;
+}
 
 size_t type_size(int type) { return type == SGEMM_TYPE_BF16 ? 2 : 4; }
 bool known_type(int type) { return type == SGEMM_TYPE_FP32 || type == SGEMM_TYPE_BF16; }
@@ -148,7 +159,7 @@ int sgemm_q8_linear(int64_t M, int64_t N, int64_t K, const int8_t *X, int64_t ld
     a.stream = static_cast<cudaStream_t>(stream);
     rc = device_args(&a.err, &a.wait_ns, &a.sm_count, &a.encode);
     if (rc != SGEMM_OK) return rc;
-    if (M <= kStreamTokens || !q8_mma_can_run(a)) return launch_status(launch_q8_stream(a));
+    if (streams(a) || !q8_mma_can_run(a)) return launch_status(launch_q8_stream(a));
     void *work = nullptr;
     rc = stream_workspace(q8_mma_workspace_bytes(a), a.stream, &work);
     if (rc != SGEMM_OK) return rc;

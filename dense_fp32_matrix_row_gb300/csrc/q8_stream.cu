@@ -81,7 +81,8 @@ struct RingCfg {
     static_assert(DP == 0 || (NB == 1 && RW == 1 && DP <= 8), "dp4a takes one block of tokens");
     static constexpr int TOK = NB * 8, TILE = S::ROWS * TOK;
     static constexpr int THREADS = (kQ8Consumers + RT) * 32;         // RT producer warps
-    static constexpr size_t SMEM = 128 + (size_t)RING * S::BYTES + 2 * (size_t)TILE * 4 + 256;
+    static constexpr int PART = kQ8Consumers * RW * NB * 32;         // int4 of one tile's sums
+    static constexpr size_t SMEM = 128 + (size_t)RING * S::BYTES + 2 * (size_t)PART * 16 + 256;
     static_assert(SMEM <= 227 * 1024, "shared memory per block");
 };
 
@@ -97,8 +98,8 @@ q8_ring_kernel(int M, int N, int K, const int8_t *__restrict__ X,
     extern __shared__ unsigned char smem_raw[];
     const uintptr_t base = (reinterpret_cast<uintptr_t>(smem_raw) + 127) & ~uintptr_t(127);
     unsigned char *ring = reinterpret_cast<unsigned char *>(base);
-    int *sums = reinterpret_cast<int *>(ring + (size_t)RING * S::BYTES);   // [2][row tile][NB][word][lane]
-    uint64_t *full = reinterpret_cast<uint64_t *>(sums + 2 * C::TILE);
+    int4 *sums = reinterpret_cast<int4 *>(ring + (size_t)RING * S::BYTES);   // [2][warp][RW][NB][lane]
+    uint64_t *full = reinterpret_cast<uint64_t *>(sums + 2 * C::PART);
     uint64_t *empty = full + RING;
     uint64_t *tdone = empty + RING;                       // [2] all warps have added their sums
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -116,7 +117,6 @@ q8_ring_kernel(int M, int N, int K, const int8_t *__restrict__ X,
         mbar_init(smem_u32(&tdone[1]), kQ8Consumers);
         mbar_fence_init();
     }
-    for (int i = threadIdx.x; i < 2 * C::TILE; i += C::THREADS) sums[i] = 0;
     __syncthreads();
     pdl_wait();
 
@@ -195,13 +195,13 @@ q8_ring_kernel(int M, int N, int K, const int8_t *__restrict__ X,
 #pragma unroll
             for (int r = 0; r < RW; ++r) q8_flush<NB>(sum[r], acc[r]);
         };
-        // This thread's results of the tile: word e of the sums' layout, which
-        // follows the fragments (4 words of 32 lanes: rows g, g, g + 8, g + 8, tokens
-        // 2 t4, + 1, 2 t4, + 1).  Their scales are asked for now.
+        // This thread's results of the tile: word e of the sums' layout, where
+        // words follow the fragments (lane, then 4 words: rows g, g, g + 8, g + 8,
+        // tokens 2 t4, + 1, 2 t4, + 1).  Their scales are asked for now.
         constexpr int OUTS = C::TILE, PER = (OUTS + kQ8Consumers * 32 - 1) / (kQ8Consumers * 32);
         const int n0 = t * ROWS;
         auto place = [&](int e, int &row, int &tok) {
-            const int l = e & 31, i = (e >> 5) & 3, frag = e >> 7;      // frag: (tile of the stage, token block)
+            const int i = e & 3, l = (e >> 2) & 31, frag = e >> 7;      // frag: (tile of the stage, token block)
             row = frag / NB * 16 + (l >> 2) + 8 * (i >> 1);
             tok = frag % NB * 8 + 2 * (l & 3) + (i & 1);
         };
@@ -273,8 +273,7 @@ q8_ring_kernel(int M, int N, int K, const int8_t *__restrict__ X,
             }
         }
         flush();
-        // whole numbers: the order of these additions does not matter
-        int *tile = sums + (count & 1) * C::TILE;
+        int4 *tile = sums + (count & 1) * C::PART;
         if constexpr (DP > 0) {
 #pragma unroll
             for (int j = 0; j < XN; ++j)
@@ -284,16 +283,15 @@ q8_ring_kernel(int M, int N, int K, const int8_t *__restrict__ X,
                     v += __shfl_xor_sync(0xffffffffu, v, 1);
                     v += __shfl_xor_sync(0xffffffffu, v, 2);
                     // one lane of the quad: where the MMA would leave (row, token j)
-                    if (t4 == (j >> 1)) atomicAdd(&tile[(rt * 4 + 2 * i + (j & 1)) * 32 + lane], v);
+                    if (t4 == (j >> 1)) reinterpret_cast<int *>(tile + warp * 32 + lane)[2 * i + (j & 1)] = v;
                 }
         } else {
 #pragma unroll
             for (int w = 0; w < RW; ++w)
 #pragma unroll
                 for (int n = 0; n < NB; ++n)
-#pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        atomicAdd(&tile[(((rt + w) * NB + n) * 4 + i) * 32 + lane], sum[w][n][i]);
+                    tile[((warp * RW + w) * NB + n) * 32 + lane] =
+                        make_int4(sum[w][n][0], sum[w][n][1], sum[w][n][2], sum[w][n][3]);
         }
         __syncwarp();
         const uint32_t bar = smem_u32(&tdone[count & 1]);
@@ -308,10 +306,15 @@ q8_ring_kernel(int M, int N, int K, const int8_t *__restrict__ X,
             const int e = (int)threadIdx.x + i * kQ8Consumers * 32;
             place(e, row, tok);
             const int n = n0 + row, m = m0 + tok;
-            if (e < OUTS) {
-                if (n < N && m < M)
-                    out[(int64_t)m * ldc + n] = from_f32<OutT>(epilogue_tail(ep, (float)tile[e] * sx[i] * sw[i], n));
-                tile[e] = 0;
+            if (e < OUTS && n < N && m < M) {
+                // the KW warps that share this tile's steps (whole numbers: any order)
+                const int frag = e >> 7, rtile = frag / NB;
+                const int *v = reinterpret_cast<const int *>(tile) +
+                               ((rtile / RW * KW * RW + rtile % RW) * NB + frag % NB) * 128 + (e & 127);
+                int total = 0;
+#pragma unroll
+                for (int w = 0; w < KW; ++w) total += v[w * RW * NB * 128];
+                out[(int64_t)m * ldc + n] = from_f32<OutT>(epilogue_tail(ep, (float)total * sx[i] * sw[i], n));
             }
         }
     }
@@ -372,9 +375,8 @@ cudaError_t launch_8(const Q8LinearArgs &a) {
 template <typename OutT>
 cudaError_t launch_r(const Q8LinearArgs &a) {
     if (a.M == 1) return launch_8<1, OutT>(a);
-    if (a.M == 2) return launch_8<2, OutT>(a);   // 4 tokens' bytes no longer fit the registers
     if (a.M <= 8) return launch_8<0, OutT>(a);
-    return launch_ring<RingCfg<0, 2, 2, 2, 1, 5>, OutT>(a);
+    return launch_ring<RingCfg<0, 2, 2, 2, 1, 4>, OutT>(a);
 }
 
 template <typename OutT>

@@ -227,12 +227,15 @@ def run_linear(M, N, K, dt="fp32", bias=False, act="none", pads=(0, 0, 0), offse
     (1, 1, 1), (1, 17, 3), (2, 100, 64), (3, 33, 65), (7, 129, 130), (8, 256, 512), (9, 255, 513), (16, 300, 1000),
     (1, 512, 4096), (16, 130, 4096), (17, 64, 256), (31, 200, 96), (33, 257, 1024), (64, 128, 1040), (65, 384, 2048),
     (100, 500, 200), (128, 130, 1025), (129, 129, 129), (200, 640, 4096), (256, 256, 64), (257, 513, 1100),
-    (300, 1000, 48), (520, 260, 3000), (1, 40, 14336), (40, 24, 14336), (700, 16, 272)])
+    (300, 1000, 48), (520, 260, 3000), (1, 40, 14336), (40, 24, 14336), (700, 16, 272),
+    # enough blocks of 16 tokens x 32 channels that the tensor-core tiles take over
+    (40, 4100, 256), (70, 4096, 528), (130, 2500, 1040), (200, 2300, 96), (300, 1100, 2080), (513, 700, 80),
+    (260, 1300, 4096), (1030, 300, 144), (18, 9800, 64)])
 def test_linear(M, N, K, dt):
     run_linear(M, N, K, dt)
 
 
-@pytest.mark.parametrize("M", [1, 8, 16, 24, 48, 130, 300])
+@pytest.mark.parametrize("M", [1, 8, 16, 24, 48, 130, 300, 1100])
 @pytest.mark.parametrize("pads,offsets", [
     ((1, 0, 0), (0, 0, 0)), ((0, 1, 0), (0, 0, 0)), ((0, 0, 1), (0, 0, 1)), ((0, 0, 0), (1, 0, 0)),
     ((0, 0, 0), (0, 3, 0)), ((16, 16, 8), (16, 32, 8)), ((4, 8, 4), (4, 8, 4)), ((5, 7, 3), (2, 9, 5))])
@@ -240,24 +243,26 @@ def test_linear_strides_and_offsets(M, pads, offsets):
     run_linear(M, 144, 272, "bf16", True, "none", pads, offsets)
 
 
-@pytest.mark.parametrize("M", [1, 16, 40, 128, 280])
+@pytest.mark.parametrize("M,N", [(1, 200), (16, 200), (40, 200), (128, 200), (20, 8000), (40, 4500), (128, 2000),
+                                 (280, 1200)])
 @pytest.mark.parametrize("act", ["none", "relu", "gelu", "silu"])
 @pytest.mark.parametrize("bias", [False, True])
-def test_linear_epilogue(M, act, bias):
-    run_linear(M, 200, 320, "fp32", bias, act)
+def test_linear_epilogue(M, N, act, bias):
+    run_linear(M, N, 320, "fp32", bias, act)
 
 
 @pytest.mark.parametrize("M,N,K", [(1, 40, 1024), (5, 40, 4096), (16, 20, 20000), (33, 40, 1024), (70, 130, 4096),
-                                   (300, 140, 8192), (20, 130, 131071)])
+                                   (300, 140, 8192), (20, 130, 131071), (70, 2600, 4096), (40, 5000, 1024),
+                                   (300, 1100, 2048), (1040, 260, 5000)])
 def test_linear_extreme_values(M, N, K):
     run_linear(M, N, K, extremes=True)
 
 
-@pytest.mark.parametrize("M", [1, 12, 40, 260])
-def test_linear_exact_sums(M):
+@pytest.mark.parametrize("M,N", [(1, 70), (3, 70), (12, 70), (40, 70), (260, 70), (40, 4900), (100, 2600), (270, 1100)])
+def test_linear_exact_sums(M, N):
     """Sums below 2^24 are whole numbers: scales of one give them exactly."""
     rng = np.random.default_rng(M)
-    K, N = 5000, 70
+    K = 5000
     xq, wq = (rng.integers(-60, 61, (n, K)).astype(np.int8) for n in (M, N))
     out = torch.empty((M, N), device="cuda")
     one = lambda n: torch.ones(n, device="cuda")  # noqa: E731
@@ -267,11 +272,11 @@ def test_linear_exact_sums(M):
     assert np.array_equal(out.cpu().numpy().astype(np.int64), want)
 
 
-@pytest.mark.parametrize("M", [3, 20, 150])
-def test_linear_nan_scale_stays_in_its_row(M):
+@pytest.mark.parametrize("M,N", [(3, 70), (20, 70), (150, 70), (40, 4900), (150, 2400), (300, 1100)])
+def test_linear_nan_scale_stays_in_its_row(M, N):
     xs = np.full(M, 0.02, dtype=np.float32)
     xs[1] = np.nan
-    out = run_linear(M, 70, 96, xs=xs)
+    out = run_linear(M, N, 96, xs=xs)
     assert torch.isnan(out[1]).all() and not torch.isnan(out[0]).any() and not torch.isnan(out[2:]).any()
 
 
@@ -420,7 +425,7 @@ def test_moe_without_tokens():
 
 # ---- shared conduct ------------------------------------------------------------
 
-def chain(stream=None, M=5, H=256, inner=192, seed=3):
+def chain(stream=None, M=5, H=256, inner=192, seed=3, wide=0):
     """norm -> up -> quantise -> down on fixed inputs, then the expert layer."""
     rng = np.random.default_rng(seed)
     dev = {}
@@ -436,19 +441,25 @@ def chain(stream=None, M=5, H=256, inner=192, seed=3):
          "hq": torch.empty((M, inner), dtype=torch.int8, device="cuda"), "hs": torch.empty(M, device="cuda"),
          "o": torch.empty((M, H), dtype=torch.bfloat16, device="cuda"),
          "m": torch.empty((M, H), dtype=torch.bfloat16, device="cuda")}
+    if wide:
+        dev["ww"] = cuda(rng.integers(-127, 128, (wide, H)).astype(np.int8))
+        dev["sw"] = torch.full((wide,), 1e-3, device="cuda")
+        b["wide"] = torch.empty((M, wide), device="cuda")
 
     def go():
         sg.rmsnorm_q8(dev["x"], dev["w"], b["q"], b["s"], residual=dev["r"], h=b["h"], y=b["y"], stream=stream)
         sg.linear_q8(b["q"], b["s"], up, sup, b["hid"], activation="silu", stream=stream)
         sg.quantize_q8(b["hid"][:, :inner], b["hq"], b["hs"], stream=stream)
         sg.linear_q8(b["hq"], b["hs"], dn, sdn, b["o"], stream=stream)
+        if wide:        # enough output for the tensor-core tiles
+            sg.linear_q8(b["q"], b["s"], dev["ww"], dev["sw"], b["wide"], stream=stream)
         sg.moe_q8(b["y"], *moe, b["m"], 2, stream=stream)
     return go, b
 
 
-@pytest.mark.parametrize("M", [1, 16, 50])
-def test_repeats_are_the_same_bits(M):
-    go, b = chain(M=M)
+@pytest.mark.parametrize("M,wide", [(1, 0), (16, 0), (50, 3500), (60, 9000)])
+def test_repeats_are_the_same_bits(M, wide):
+    go, b = chain(M=M, wide=wide)
     go()
     first = {n: t.clone() for n, t in b.items()}
     for _ in range(3):
@@ -457,14 +468,14 @@ def test_repeats_are_the_same_bits(M):
     assert all(torch.equal(first[n], t) for n, t in b.items())
 
 
-@pytest.mark.parametrize("M", [2, 40])
-def test_side_stream_and_graph(M):
-    go, b = chain(M=M)
+@pytest.mark.parametrize("M,wide", [(2, 0), (40, 4500)])
+def test_side_stream_and_graph(M, wide):
+    go, b = chain(M=M, wide=wide)
     go()
     torch.cuda.synchronize()
     want = {n: t.clone() for n, t in b.items()}
     side = torch.cuda.Stream()
-    go2, b2 = chain(stream=side, M=M)
+    go2, b2 = chain(stream=side, M=M, wide=wide)
     side.wait_stream(torch.cuda.current_stream())
     go2()
     assert sg.status(side) == sg.OK
@@ -485,7 +496,7 @@ def test_side_stream_and_graph(M):
 def test_two_streams_at_once():
     """Calls of two streams overlap on the GPU and keep apart."""
     streams = [torch.cuda.Stream() for _ in range(2)]
-    runs = [chain(stream=s, M=16, seed=5 + i) for i, s in enumerate(streams)]
+    runs = [chain(stream=s, M=40, seed=5 + i, wide=4500) for i, s in enumerate(streams)]
     torch.cuda.synchronize()
     for go, _ in runs:
         go()
