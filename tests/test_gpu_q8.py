@@ -251,6 +251,23 @@ def test_linear_epilogue(M, N, act, bias):
     run_linear(M, N, 320, "fp32", bias, act)
 
 
+@pytest.mark.parametrize("act", ["gelu", "silu"])
+@pytest.mark.parametrize("M,N", [(3, 200), (40, 200), (40, 4500), (280, 1200)])
+def test_linear_bf16_activations_of_large_values(M, N, act):
+    """Both tails and beyond: products from 0 to about 200 in size.  A fast
+    exponential is off by (2 + 1.2 |x|) units in the last place, of a value that is
+    negligible or 1 where |x| is large: below 2^-17 of the result."""
+    rng = np.random.default_rng(M)
+    K = 96
+    xq, wq = (rng.integers(-127, 128, (n, K)).astype(np.int8) for n in (M, N))
+    xs = (10.0 ** rng.uniform(-4, 0.5, M) / 127).astype(np.float32)
+    ws = (np.ones(N) * 60 / (127 * K ** 0.5)).astype(np.float32)
+    out = torch.empty((M, N), dtype=torch.bfloat16, device="cuda")
+    sg.linear_q8(*[torch.from_numpy(a).cuda() for a in (xq, xs, wq, ws)], out, activation=act)
+    want, size = ref.linear(xq, xs, wq, ws, None, act)
+    close(out, want, LINEAR_TOL * size + 2.0 ** -17 * np.abs(want), "bf16")
+
+
 @pytest.mark.parametrize("M,N,K", [(1, 40, 1024), (5, 40, 4096), (16, 20, 20000), (33, 40, 1024), (70, 130, 4096),
                                    (300, 140, 8192), (20, 130, 131071), (70, 2600, 4096), (40, 5000, 1024),
                                    (300, 1100, 2048), (1040, 260, 5000)])
