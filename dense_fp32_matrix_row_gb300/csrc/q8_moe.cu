@@ -29,7 +29,7 @@ namespace sgemm_gb300 {
 namespace {
 
 constexpr int RTHREADS = 256;
-constexpr int kRouteTokens = 16;       // tokens a router block takes at a time
+constexpr int kRouteTokens = 4;        // tokens of a router block
 constexpr int MWARPS = 8, MTHREADS = MWARPS * 32;
 constexpr int kMaxPairs = kMoeMaxTokens * kMoeMaxTopK;
 
@@ -62,9 +62,10 @@ struct MoeLayout {
     }
 };
 
-// Blocks 0 .. E-1: one expert's logits for every token.  Blocks E .. E+T-1:
-// one token's 8-bit row; the first of them also clears the second kernel's
-// counters.
+// The first E * ceil(T / 4) blocks: one expert's logits for four tokens (with all
+// tokens in one block, 16 of them over 16 experts left most SMs idle and took 19 us
+// cold).  The T blocks after them: one token's 8-bit row; the first of those also
+// clears the second kernel's counters.
 template <typename T>
 __global__ void __launch_bounds__(RTHREADS)
 q8_route_kernel(int ntok, int E, int top_k, int H, int I, const T *__restrict__ x, int64_t ldx,
@@ -75,52 +76,53 @@ q8_route_kernel(int ntok, int E, int top_k, int H, int I, const T *__restrict__ 
     pdl_wait();
     pdl_trigger();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    if ((int)blockIdx.x < E) {
-        const int e = (int)blockIdx.x;
+    const int chunks = (ntok + kRouteTokens - 1) / kRouteTokens;
+    if ((int)blockIdx.x < E * chunks) {
+        const int e = (int)blockIdx.x / chunks, t0 = ((int)blockIdx.x - e * chunks) * kRouteTokens;
         const float *w = router + (int64_t)e * ldr;
         float *logits = reinterpret_cast<float *>(ws + L.logits);
-        for (int t0 = 0; t0 < ntok; t0 += kRouteTokens) {
-            float acc[kRouteTokens];
+        const T *xr[kRouteTokens];      // tokens past the last read the last one
+        float acc[kRouteTokens];
 #pragma unroll
-            for (int j = 0; j < kRouteTokens; ++j) acc[j] = 0.0f;
-            if (vec) {
-                for (int k = 4 * (int)threadIdx.x; k < H; k += 4 * RTHREADS) {
-                    const float4 w4 = __ldg(reinterpret_cast<const float4 *>(w + k));
+        for (int j = 0; j < kRouteTokens; ++j) {
+            xr[j] = x + (int64_t)min(t0 + j, ntok - 1) * ldx;
+            acc[j] = 0.0f;
+        }
+        if (vec) {
+#pragma unroll 4
+            for (int k = 4 * (int)threadIdx.x; k < H; k += 4 * RTHREADS) {
+                const float4 w4 = __ldg(reinterpret_cast<const float4 *>(w + k));
 #pragma unroll
-                    for (int j = 0; j < kRouteTokens; ++j)
-                        if (t0 + j < ntok) {
-                            float v[4];
-                            load_vec<T, 4>(x + (int64_t)(t0 + j) * ldx + k, v);
-                            acc[j] = fmaf(v[0], w4.x, fmaf(v[1], w4.y, fmaf(v[2], w4.z, fmaf(v[3], w4.w, acc[j]))));
-                        }
-                }
-            } else {
-                for (int k = threadIdx.x; k < H; k += RTHREADS) {
-                    const float wk = __ldg(w + k);
-#pragma unroll
-                    for (int j = 0; j < kRouteTokens; ++j)
-                        if (t0 + j < ntok) acc[j] = fmaf(to_f32<T>(x[(int64_t)(t0 + j) * ldx + k]), wk, acc[j]);
+                for (int j = 0; j < kRouteTokens; ++j) {
+                    float v[4];
+                    load_vec<T, 4>(xr[j] + k, v);
+                    acc[j] = fmaf(v[0], w4.x, fmaf(v[1], w4.y, fmaf(v[2], w4.z, fmaf(v[3], w4.w, acc[j]))));
                 }
             }
+        } else {
+            for (int k = threadIdx.x; k < H; k += RTHREADS) {
+                const float wk = __ldg(w + k);
 #pragma unroll
-            for (int j = 0; j < kRouteTokens; ++j)
-#pragma unroll
-                for (int o = 16; o > 0; o >>= 1) acc[j] += __shfl_xor_sync(0xffffffffu, acc[j], o);
-            __syncthreads();
-            if (lane == 0)
-#pragma unroll
-                for (int j = 0; j < kRouteTokens; ++j) lsum[warp][j] = acc[j];
-            __syncthreads();
-            if (threadIdx.x < kRouteTokens && t0 + (int)threadIdx.x < ntok) {
-                float s = 0.0f;
-#pragma unroll
-                for (int v = 0; v < RTHREADS / 32; ++v) s += lsum[v][threadIdx.x];
-                logits[(int64_t)(t0 + threadIdx.x) * E + e] = s;
+                for (int j = 0; j < kRouteTokens; ++j) acc[j] = fmaf(to_f32<T>(xr[j][k]), wk, acc[j]);
             }
+        }
+#pragma unroll
+        for (int j = 0; j < kRouteTokens; ++j)
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) acc[j] += __shfl_xor_sync(0xffffffffu, acc[j], o);
+        if (lane == 0)
+#pragma unroll
+            for (int j = 0; j < kRouteTokens; ++j) lsum[warp][j] = acc[j];
+        __syncthreads();
+        if (threadIdx.x < kRouteTokens && t0 + (int)threadIdx.x < ntok) {
+            float s = 0.0f;
+#pragma unroll
+            for (int v = 0; v < RTHREADS / 32; ++v) s += lsum[v][threadIdx.x];
+            logits[(int64_t)(t0 + threadIdx.x) * E + e] = s;
         }
         return;
     }
-    const int t = (int)blockIdx.x - E;
+    const int t = (int)blockIdx.x - E * chunks;
     if (t == 0) {
         uint32_t *z = reinterpret_cast<uint32_t *>(ws + L.zero);
         for (int i = threadIdx.x; i < L.nzero; i += RTHREADS) z[i] = 0u;
@@ -1162,7 +1164,7 @@ cudaError_t launch_t(const Q8MoeArgs &a, unsigned char *ws) {
     const int vec = a.H % 4 == 0 && a.ldx % 4 == 0 && a.ldr % 4 == 0 &&
                     reinterpret_cast<uintptr_t>(a.x) % (4 * sizeof(T)) == 0 &&
                     reinterpret_cast<uintptr_t>(a.router) % 16 == 0;
-    cudaError_t e = launch_pdl(q8_route_kernel<T>, a.E + a.T, RTHREADS, 0, a.stream, a.T, a.E, a.top_k, a.H, a.I,
+    cudaError_t e = launch_pdl(q8_route_kernel<T>, a.E * ((a.T + kRouteTokens - 1) / kRouteTokens) + a.T, RTHREADS, 0, a.stream, a.T, a.E, a.top_k, a.H, a.I,
                                (const T *)a.x, a.ldx, a.router, a.ldr, vec, ws);
     if (e != cudaSuccess) return e;
     if (reinterpret_cast<uintptr_t>(a.w_up) % 16 == 0 && reinterpret_cast<uintptr_t>(a.w_down) % 16 == 0) {
