@@ -178,19 +178,19 @@ __device__ __forceinline__ void set_registers() {
     else asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
 }
 
-// The epilogue's activation.  For a bf16 result SiLU and GELU are v times a
-// logistic function (GELU: of 2 sqrt(2/pi) (v + 0.044715 v^3), the same function
-// as the tanh form) with the fast exponential and quotient: good to about 1e-5,
-// where the result keeps 4e-3.  The exact forms cost some 40 instructions for each
+// The epilogue's activation.  SiLU and GELU are v times a logistic function (GELU:
+// of 2 sqrt(2/pi) (v + 0.044715 v^3), the same function as the tanh form) with the
+// short quotient, good to 2 units in the last place (0 for results below 1e-36),
+// and for a bf16 result the short exponential, good to about 1e-5 where the result
+// keeps 4e-3.  tanhf, expf and the exact quotient cost some 40 instructions for each
 // of a thread's 128 values, more than the MMAs give it time for: 2048 x 14336 x 4096
-// takes 125 us without an activation, 132 with GELU (150 exact), 128 with SiLU (an
-// FP32 result, whose precision needs the exact form, 188).
+// took 188 us with SiLU and an FP32 result, 150 with GELU and bf16, and takes 125
+// without an activation.
 template <int ACT, typename OutT>
 __device__ __forceinline__ float finish_value(float v) {
-    if constexpr (sizeof(OutT) == 2 && ACT == kActSilu) {
-        return __fdividef(v, 1.0f + __expf(-v));
-    } else if constexpr (sizeof(OutT) == 2 && ACT == kActGelu) {
-        return __fdividef(v, 1.0f + __expf(-1.5957691216057308f * fmaf(0.044715f * v, v * v, v)));
+    if constexpr (ACT == kActSilu || ACT == kActGelu) {
+        const float x = ACT == kActSilu ? -v : -1.5957691216057308f * fmaf(0.044715f * v, v * v, v);
+        return __fdividef(v, 1.0f + (sizeof(OutT) == 2 ? __expf(x) : expf(x)));
     } else {
         return activate<ACT>(v);
     }
