@@ -17,10 +17,17 @@
 // first, then all down units.  A down unit waits (bounded) until its expert's
 // hidden rows are there; since every gate/up unit has been drawn by then, by
 // a block that waits for nothing, that wait always ends, whatever else runs
-// on the GPU.  The block that finishes an expert's last gate/up unit turns
-// the hidden rows into 8 bits, and the one that finishes the last down unit
-// of an output range adds the experts' results, in slot order: nothing
-// depends on timing, and results repeat bit for bit.
+// on the GPU.  Between and after them, hidden rows are turned into 8 bits and the
+// experts' results added, in slot order: by units of their own
+// (q8_expert_ring_kernel) or by the block that finishes the last unit they need
+// (q8_expert_kernel, for arrays of any alignment).  Nothing depends on timing, and
+// results repeat bit for bit.
+//
+// Measured (bf16): one token, 2 of 8 experts of 4096 x 14336, 353 MB, 73 us, 4.8
+// TB/s; 16 tokens, 6 of 64 experts of 2048 x 1408, 440 MB, 133 us, 3.3 TB/s; 5 FP32
+// tokens, 4 of 16 experts of 1024 x 1000, 38 MB, 40 us.  What is above memory's time
+// is a chain of hand-overs that each take 1 to 2 us (logits, routing, the first
+// weights, hidden rows, 8 bits, results, sums): 17 us for a layer without work.
 #include <type_traits>
 
 #include "q8_stream.cuh"

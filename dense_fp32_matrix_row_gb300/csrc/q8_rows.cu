@@ -19,6 +19,9 @@
 //   q8_rows        longer rows, few rows, any alignment: a block a row, all its
 //                  loads issued at once;
 //   q8_rows_long   rows beyond registers: read twice.
+// Measured (bf16): 8192 x 4096 with residual, h and y, 302 MB, 51.7 us, 5.8 TB/s,
+// memory; 2048 x 14336 alone, 88 MB, 21.5 us, 4.1 TB/s, instruction issue and the
+// barrier between a row's loads and its stores; one row of 4096 2.3 us, the launch.
 // Measured and not kept for long rows (8192 x 4096, 4096 x 8192 in FP32, 2048 x
 // 16384, with residual: 46, 69 and 42 us with a block a row): persistent blocks
 // that prefetch the next row into registers 46, 89 and 44 us, into shared memory

@@ -284,6 +284,10 @@ int sgemm_q8_rmsnorm(int64_t M, int64_t K, const void *x, int64_t ldx, const voi
  * in magnitude (always up to K = 1024, and for ordinary data far beyond), and
  * rounded to FP32 from there.  K <= 131071 (SGEMM_ERR_BAD_DIM).  K == 0 gives
  * act(bias).
+ * Past 16 tokens it uses the stream's workspace (X in 16 bits; W once more when
+ * its rows are not 16-byte aligned; partial sums when K is divided), grown like
+ * sgemm()'s; the same rule for stream capture holds.  Its kernels' waits on
+ * their own copies are bounded (see sgemm_status).
  */
 int sgemm_q8_linear(int64_t M, int64_t N, int64_t K, const int8_t *X, int64_t ldx, const float *xs,
                     const int8_t *W, int64_t ldw, const float *ws, const float *bias, int activation,
@@ -422,8 +426,8 @@ int64_t sgemm_host_panel_rows(int64_t M, int64_t N, int64_t K);
 
 /*
  * sgemm_release_workspaces -- free the library's cached device workspaces
- * (the transposed copy of A that the FFMA kernel stages from; one buffer per
- * device and stream, grown with cudaMallocAsync on the call's stream) and
+ * (the transposed copy of A that the FFMA kernel stages from, the 8-bit
+ * operators' intermediate rows; one buffer per device and stream, grown with cudaMallocAsync on the call's stream) and
  * sgemm_host's device buffers, copy streams and events.
  * Waits for every stream that owns a workspace.  Call it only while no other
  * host thread is inside an sgemm call; later calls allocate again as needed.
