@@ -644,16 +644,41 @@ __device__ __forceinline__ bool unit_products(EShared &S, uint32_t ring, int *su
     const uint32_t ld = G.ld;
     const int tl = cw / G.kw, kpart = cw % G.kw;      // this warp's tile of a stage, its share of the steps
     const int step0 = kpart * ESTEPS;
-    const int8_t *x[NT];
+    // Rows g and g + 1 lie in the same banks.  With dp4a every lane has its own sum, so
+    // odd rows take their steps in the order 1, 0, 3, 2 and meet no conflict.
+    static_assert(ESTEPS % 4 == 0 || ESTEPS == 2, "pairs of steps");
+    const int odd = DP ? g & 1 : 0;
+    const int8_t *xbase = (up ? A.xq : A.hq) + 16 * t4;
+    int x[NT];                                        // offsets: at most 1024 rows of 131072 bytes
 #pragma unroll
     for (int j = 0; j < NT; ++j) {                    // tokens past the chunk's end: the last one
         const int p = R.list[R.chunk_at[c] + min(DP ? j : 8 * j + g, (int)R.chunk_n[c] - 1)];
-        x[j] = (up ? A.xq + (int64_t)(p / A.top_k) * A.Hp : A.hq + (int64_t)p * A.Ip) + 16 * t4;
+        x[j] = up ? p / A.top_k * A.Hp : p * A.Ip;
     }
-    for (int t = 0; t < sub; ++t) {
-        // the two weight rows of this lane
+    // The tokens of a batch of steps are asked for together, the first ahead of the
+    // wait for the weights.  (A step past the last reads the last one's tokens and is
+    // not used.)  Asked for a stage earlier still, or kept from tile to tile, they
+    // gained nothing (125 against 125 us for 16 tokens, 72.5 against 71.7 for one).
+    constexpr int BATCH = NT <= 2 || ESTEPS <= 2 ? ESTEPS : ESTEPS / 2;
+    uint4 xv[BATCH][NT];
+    auto xload = [&](int first) {
+#pragma unroll
+        for (int k = 0; k < BATCH; ++k)
+#pragma unroll
+            for (int j = 0; j < NT; ++j)
+                xv[k][j] = *reinterpret_cast<const uint4 *>(xbase + (x[j] + max(0, min(first + (k ^ odd), blocks - 1)) * kQ8Step));
+    };
+    auto step = [&](auto &sum, const uint4 &a, const uint4 &d, const uint4 (&xs)[NT]) {
+        if constexpr (DP) {
+            q8_step_dp<NT>(sum, a, d, xs);
+        } else {
+#pragma unroll
+            for (int j = 0; j < NT; ++j) q8_step_s8(sum[j], a, d, xs[j]);
+        }
+    };
+    // this lane's two weight rows of a tile
+    auto rows = [&](int t, const int8_t *&wa, const int8_t *&wb) {
         const int tile = (grp * sub + t) * rt + tl, e = R.chunk_e[c];
-        const int8_t *wa, *wb;
         if (up) {
             wa = A.w_up + ((int64_t)e * 2 * A.I + min(tile * 8 + g, A.I - 1)) * A.ldu;
             wb = wa + (int64_t)A.I * A.ldu;
@@ -661,9 +686,13 @@ __device__ __forceinline__ bool unit_products(EShared &S, uint32_t ring, int *su
             wa = A.w_down + ((int64_t)e * A.H + min(tile * 16 + g, A.H - 1)) * A.ldd;
             wb = A.w_down + ((int64_t)e * A.H + min(tile * 16 + g + 8, A.H - 1)) * A.ldd;
         }
-        // and where they lie in a stage
+    };
+    for (int t = 0; t < sub; ++t) {
+        // where the rows lie in a stage
         uint32_t oa = (uint32_t)(tl * 16 + g) * ld + (uint32_t)(step0 * kQ8Step + 16 * t4), ob = oa + 8 * ld;
         if (SHIFT) {
+            const int8_t *wa, *wb;
+            rows(t, wa, wb);
             oa += (uint32_t)(reinterpret_cast<uintptr_t>(wa) & 15);
             ob += (uint32_t)(reinterpret_cast<uintptr_t>(wb) & 15);
         }
@@ -672,67 +701,58 @@ __device__ __forceinline__ bool unit_products(EShared &S, uint32_t ring, int *su
         for (int j = 0; j < NT; ++j)
 #pragma unroll
             for (int i = 0; i < (DP ? 2 : 4); ++i) sum[j][i] = 0;
-        auto step = [&](const uint4 &a, const uint4 &d, const uint4 (&xv)[NT]) {
-            if constexpr (DP) {
-                q8_step_dp<NT>(sum, a, d, xv);
-            } else {
-#pragma unroll
-                for (int j = 0; j < NT; ++j) q8_step_s8(sum[j], a, d, xv[j]);
-            }
-        };
         for (int s = 0; s < stages; ++s, ++used) {
             const int r = (int)(used % ERING);
             const int first = s * kb + step0;
             const int here = min(ESTEPS, blocks - first);    // this warp's steps of the stage
-            // The tokens of a batch of steps are asked for together, the first ahead of
-            // the wait for the weights.  (A step past the last reads the last one's
-            // tokens and is not used.)
-            constexpr int BATCH = NT <= 2 || ESTEPS <= 2 ? ESTEPS : ESTEPS / 2;
-            uint4 xv[BATCH][NT];
-            auto xload = [&](int k0) {
-#pragma unroll
-                for (int k = 0; k < BATCH; ++k)
-#pragma unroll
-                    for (int j = 0; j < NT; ++j)
-                        xv[k][j] = *reinterpret_cast<const uint4 *>(x[j] + (int64_t)max(0, min(first + k0 + k, blocks - 1)) * kQ8Step);
-            };
-            xload(0);
+            xload(first);
             if (s + t > 0 && !warp_wait(smem_u32(&S.full[r]), (used / ERING) & 1, A.wait_ns)) return false;
             const uint32_t stage = ring + (uint32_t)r * ESTAGE;
 #pragma unroll
             for (int k0 = 0; k0 < ESTEPS; k0 += BATCH) {
-                if (k0 > 0) xload(k0);
+                if (k0 > 0) xload(first + k0);
 #pragma unroll
                 for (int k = 0; k < BATCH; ++k)
-                    if (k0 + k < here) {
-                        const uint32_t o = stage + (uint32_t)(k0 + k) * kQ8Step;
-                        step(SHIFT ? lds_shifted(o + oa) : lds128(o + oa), SHIFT ? lds_shifted(o + ob) : lds128(o + ob), xv[k]);
+                    if (((k0 + k) ^ odd) < here) {
+                        const uint32_t o = stage + (uint32_t)((k0 + k) ^ odd) * kQ8Step;
+                        step(sum, SHIFT ? lds_shifted(o + oa) : lds128(o + oa), SHIFT ? lds_shifted(o + ob) : lds128(o + ob), xv[k]);
                     }
             }
             __syncwarp();
             if (lane == 0) mbar_arrive(smem_u32(&S.empty[r]));
         }
-        if (kpart == 0)
-            for (int k0 = blocks * kQ8Step; k0 < G.K; k0 += kQ8Step) {   // the rows' last values
+        if (kpart == 0 && blocks * kQ8Step < G.K) {   // the rows' last values
+            const int8_t *wa, *wb;
+            rows(t, wa, wb);
+            for (int k0 = blocks * kQ8Step; k0 < G.K; k0 += kQ8Step) {
                 const int valid = min(16, max(0, G.K - k0 - 16 * t4));
-                uint4 xv[NT];
+                uint4 xt[NT];
 #pragma unroll
-                for (int j = 0; j < NT; ++j) xv[j] = *reinterpret_cast<const uint4 *>(x[j] + k0);
-                step(load16_bytes(wa + k0 + 16 * t4, valid), load16_bytes(wb + k0 + 16 * t4, valid), xv);
+                for (int j = 0; j < NT; ++j) xt[j] = *reinterpret_cast<const uint4 *>(xbase + (x[j] + k0));
+                step(sum, load16_bytes(wa + k0 + 16 * t4, valid), load16_bytes(wb + k0 + 16 * t4, valid), xt);
             }
+        }
         // whole numbers: the order of these additions does not matter
         int *to = sums + (t * rt + tl) * 256;
         if constexpr (DP) {
+            // The quad's four parts of every sum, each lane ending with row g + 8 i and
+            // every second token; left where the MMA would leave them.
+            const int i = t4 & 1, odd_tok = t4 >> 1;
+            int m[NT];
 #pragma unroll
             for (int j = 0; j < NT; ++j)
+                m[j] = (i ? sum[j][1] : sum[j][0]) + __shfl_xor_sync(0xffffffffu, i ? sum[j][0] : sum[j][1], 1);
+            if constexpr (NT == 1) {
+                const int v2 = m[0] + __shfl_xor_sync(0xffffffffu, m[0], 2);
+                if (odd_tok == 0) atomicAdd(to + 64 * i + 4 * g, v2);
+            } else {
 #pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    int v2 = sum[j][i];
-                    v2 += __shfl_xor_sync(0xffffffffu, v2, 1);
-                    v2 += __shfl_xor_sync(0xffffffffu, v2, 2);
-                    // one lane of the quad: where the MMA would leave (row, token j)
-                    if (t4 == (j >> 1)) atomicAdd(to + (2 * i + (j & 1)) * 32 + lane, v2);
+                for (int h = 0; h < NT / 2; ++h) {
+                    const int v2 = (odd_tok ? m[2 * h + 1] : m[2 * h]) +
+                                   __shfl_xor_sync(0xffffffffu, odd_tok ? m[2 * h] : m[2 * h + 1], 2);
+                    atomicAdd(to + 64 * i + 32 * odd_tok + 4 * g + h, v2);
                 }
+            }
         } else {
 #pragma unroll
             for (int j = 0; j < NT; ++j)
