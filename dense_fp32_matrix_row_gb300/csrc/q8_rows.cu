@@ -16,14 +16,14 @@
 // kernel a call runs:
 //   q8_rows_warp   rows of at most 64 vectors, many of them: a warp a row, no
 //                  block barriers (at 128 vectors both take 20 us for 16384 rows);
-//   q8_rows        longer rows, few rows, any alignment: a block a row, all its
-//                  loads issued at once;
+//   q8_rows, q8_plain  longer rows, few rows, any alignment: a block a row, all its
+//                  loads issued at once (q8_plain without norm and residual);
 //   q8_rows_long   rows beyond registers: read twice.
-// Measured (bf16): 8192 x 4096 with residual, h and y, 302 MB, 51.7 us, 5.8 TB/s,
-// memory; 2048 x 14336 alone, 88 MB, 21.5 us, 4.1 TB/s, instruction issue and the
-// barrier between a row's loads and its stores; one row of 4096 2.3 us, the launch.
+// Measured (bf16): 8192 x 4096 with residual, h and y, 302 MB, 46.9 us, 6.4 TB/s,
+// memory; 2048 x 14336 alone, 88 MB, 15.0 us, 5.9 TB/s, the same; one row of 4096
+// 2.3 us, the launch.
 // Measured and not kept for long rows (8192 x 4096, 4096 x 8192 in FP32, 2048 x
-// 16384, with residual: 46, 69 and 42 us with a block a row): persistent blocks
+// 16384, with residual: 39, 70 and 45 us with a block a row): persistent blocks
 // that prefetch the next row into registers 46, 89 and 44 us, into shared memory
 // with bulk copies 49, 122 and 64 us.
 #include "q8.cuh"
@@ -82,6 +82,27 @@ struct Raw<T, 1> {
     __device__ __forceinline__ void load(const T *p) { v = *p; }
     __device__ __forceinline__ float operator[](int) const { return to_f32<T>(v); }
 };
+
+// The largest |value| of some vectors, as FP32 bits.  BF16 values are the upper
+// halves of FP32 ones and are compared two at a time.
+template <typename T, int V, int NV>
+__device__ __forceinline__ uint32_t raw_max(const Raw<T, V> (&r)[NV]) {
+    uint32_t mx = 0;
+    if constexpr (sizeof(T) == 2 && V > 1) {
+        uint32_t m2 = 0;
+#pragma unroll
+        for (int i = 0; i < NV; ++i)
+#pragma unroll
+            for (int k = 0; k < V / 2; ++k) m2 = __vmaxu2(m2, r[i].w[k] & 0x7fff7fffu);
+        mx = max(m2 << 16, m2 & 0xffff0000u);
+    } else {
+#pragma unroll
+        for (int i = 0; i < NV; ++i)
+#pragma unroll
+            for (int e = 0; e < V; ++e) mx = max(mx, abs_bits(r[i][e]));
+    }
+    return mx;
+}
 
 // The arrays of a call, and what happens to one row once its sums are known.
 template <typename T>
@@ -282,6 +303,37 @@ q8_rows_long_kernel(int64_t K, const T *x, int64_t ldx, const T *residual, int64
     }
 }
 
+// A block per row without a norm or a residual: the row waits for its maximum in the
+// type it came in (2048 x 14336 in bf16 21.4 us in FP32 registers, 15.0 so).
+template <typename T, int V, int NV>
+__global__ void __launch_bounds__(512) q8_plain_kernel(int64_t K, const T *__restrict__ x, int64_t ldx,
+                                                       int8_t *__restrict__ q, int64_t ldq, float *__restrict__ scale) {
+    __shared__ uint32_t red[64];
+    pdl_wait();
+    const int nvec = (int)(K / V);
+    const T *xr = x + (int64_t)blockIdx.x * ldx;
+    Raw<T, V> r[NV] = {};
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+        const int c = (int)(threadIdx.x + i * blockDim.x);
+        if (c < nvec) r[i].load(xr + (int64_t)c * V);
+    }
+    uint32_t mx = raw_max<T, V, NV>(r);
+    float none = 0.0f;
+    block_max_sum(mx, none, red);
+    const RowQuant rq(mx);
+    if (threadIdx.x == 0) scale[blockIdx.x] = row_scale(rq, 1.0f, 1.0f);
+    int8_t *qr = q + (int64_t)blockIdx.x * ldq;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+        const int c = (int)(threadIdx.x + i * blockDim.x);
+        float v[V];
+#pragma unroll
+        for (int e = 0; e < V; ++e) v[e] = r[i][e];
+        if (c < nvec) store_q<V>(qr + (int64_t)c * V, rq, v);
+    }
+}
+
 template <typename K, typename... A>
 cudaError_t launch_rows_pdl(K kern, dim3 grid, int threads, size_t smem, cudaStream_t s, A... args) {
     cudaLaunchConfig_t cfg = {};
@@ -303,11 +355,30 @@ Rows<T> rows_of(const Q8RowsArgs &a) {
             (T *)a.y, a.ldy, a.q, a.ldq, a.scale};
 }
 
-// Vectors per thread: as few as `most` threads a row allow; 0 if it takes more than 16.
-int vectors_per_thread(int64_t nvec, int most) {
-    for (int nv = 1; nv <= 16; nv *= 2)
+// Vectors per thread: the fewest, from `from` on, that `most` threads a row allow; 0
+// if it takes more than `last`.
+int vectors_per_thread(int64_t nvec, int most, int from, int last) {
+    for (int nv = from; nv <= last; nv *= 2)
         if (nvec <= (int64_t)most * nv) return nv;
     return 0;
+}
+// A block's share.  Few rows: as many threads as there are.  Otherwise a thread keeps
+// several loads in flight, which counts for more than threads do, up to 32 words of
+// input without a norm and 4 vectors with one.
+//   vectors a thread          1     2     4     8    16
+//   no norm, 8192 x 4096     24.2  17.8  16.0
+//     2048 x 14336                       15.7  15.0  19.0
+//     the same in FP32                   23.4  25.4  30.9
+//   norm, 8192 x 2048        24.4  21.7
+//     8192 x 4096 with y     51.6  46.9  48.2
+//     1001 x 4092 in FP32          7.4   6.4   8.2
+//     2048 x 14336                       38.9  50.9  68.6
+// (us, bf16 unless said; with residual but for FP32)
+int block_vectors(int64_t nvec, bool norm, bool few_rows, int words_of_vector) {
+    if (few_rows) return vectors_per_thread(nvec, 512, 1, 16);
+    const int cap = norm ? 4 : words_of_vector > 2 ? 32 / words_of_vector : 16;
+    const int nv = norm ? vectors_per_thread(nvec, 256, 2, cap) : vectors_per_thread(nvec, 128, 1, cap);
+    return nv ? nv : vectors_per_thread(nvec, 512, cap, 16);
 }
 int threads_for(int64_t nvec, int nv) {
     const int t = (int)(((nvec + nv - 1) / nv + 31) / 32 * 32);
@@ -317,8 +388,28 @@ int threads_for(int64_t nvec, int nv) {
 template <typename T, int V>
 cudaError_t launch_block(const Q8RowsArgs &a) {
     const int64_t nvec = a.K / V;
-    const int nv = vectors_per_thread(nvec, 512), threads = threads_for(nvec, nv);
+    const int nv = block_vectors(nvec, a.weight != nullptr, a.M <= 2 * (int64_t)a.sm_count, (V * (int)sizeof(T) + 3) / 4);
+    const int threads = threads_for(nvec, nv);
     const dim3 grid((unsigned)a.M);
+    if (a.weight == nullptr) {
+        const T *x = (const T *)a.x;
+        auto run = [&](auto kernel) {
+            return launch_rows_pdl(kernel, grid, threads, 0, a.stream, a.K, x, a.ldx, a.q, a.ldq, a.scale);
+        };
+        switch (nv) {
+            case 1: return run(q8_plain_kernel<T, V, 1>);
+            case 2: return run(q8_plain_kernel<T, V, 2>);
+            case 4: return run(q8_plain_kernel<T, V, 4>);
+            default: break;
+        }
+        if constexpr (V * sizeof(T) <= 16) {
+            if (nv == 8) return run(q8_plain_kernel<T, V, 8>);
+        }
+        if constexpr (V * sizeof(T) <= 8) {
+            if (nv == 16) return run(q8_plain_kernel<T, V, 16>);
+        }
+        return cudaErrorInvalidValue;
+    }
     const Rows<T> r = rows_of<T>(a);
     switch (nv) {
         case 1: return launch_rows_pdl(q8_rows_kernel<T, V, 1>, grid, threads, 0, a.stream, r);
@@ -340,7 +431,7 @@ cudaError_t launch_warp(const Q8RowsArgs &a) {
     const int64_t blocks = (a.M + WARP_ROWS - 1) / WARP_ROWS, most = (int64_t)a.sm_count * 8;
     const dim3 grid((unsigned)(blocks < most ? blocks : most));
     const Rows<T> r = rows_of<T>(a);
-    switch (vectors_per_thread(a.K / V, 32)) {
+    switch (vectors_per_thread(a.K / V, 32, 1, 2)) {
         case 1: return launch_rows_pdl(q8_rows_warp_kernel<T, V, 1>, grid, WARP_ROWS * 32, 0, a.stream, r);
         default: return launch_rows_pdl(q8_rows_warp_kernel<T, V, 2>, grid, WARP_ROWS * 32, 0, a.stream, r);
     }

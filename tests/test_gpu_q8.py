@@ -172,6 +172,24 @@ def test_rows_of_extreme_values(K, norm):
         run_rows(x, None, w, eps=0.0)
 
 
+@pytest.mark.parametrize("dt", ["fp32", "bf16"])
+@pytest.mark.parametrize("K", [33, 520, 1000, 1028, 2056, 4092, 4100, 5002, 8184, 16384, 16390])
+def test_many_rows(K, dt):
+    """More rows than two an SM, where a thread takes several vectors; some rows are
+    of extreme values."""
+    rng = np.random.default_rng(K)
+    M = 2 * torch.cuda.get_device_properties(0).multi_processor_count + 3
+    x, r = sample(rng, M, K), sample(rng, M, K)
+    x[5, K // 2], x[6, K - 1], x[7, 0] = np.nan, np.inf, -np.inf
+    x[8, :], r[8, :] = 0.0, 0.0
+    x[9] *= 1e-30
+    r[9] = 0.0
+    w = (1.0 + 0.2 * rng.standard_normal(K)).astype(np.float32)
+    run_rows(x, dt=dt)
+    run_rows(x, r, w, dt=dt, with_h=True, with_y=True)
+    run_rows(x, None, w, dt=dt)
+
+
 def test_rows_norm_nan_weight_marks_the_row():
     w = np.ones(64, dtype=np.float32)
     w[3] = np.nan
