@@ -23,11 +23,13 @@
 // (q8_expert_kernel, for arrays of any alignment).  Nothing depends on timing, and
 // results repeat bit for bit.
 //
-// Measured (bf16): one token, 2 of 8 experts of 4096 x 14336, 353 MB, 73 us, 4.8
-// TB/s; 16 tokens, 6 of 64 experts of 2048 x 1408, 440 MB, 133 us, 3.3 TB/s; 5 FP32
+// Measured (bf16): one token, 2 of 8 experts of 4096 x 14336, 353 MB, 72 us, 4.9
+// TB/s; 16 tokens, 6 of 64 experts of 2048 x 1408, 440 MB, 115 us, 3.8 TB/s; 5 FP32
 // tokens, 4 of 16 experts of 1024 x 1000, 38 MB, 40 us.  What is above memory's time
-// is a chain of hand-overs that each take 1 to 2 us (logits, routing, the first
-// weights, hidden rows, 8 bits, results, sums): 17 us for a layer without work.
+// is a chain of hand-overs that each take 1 to 4 us (logits, routing, the first
+// weights, hidden rows, 8 bits, results, sums): 17 us for a layer without work.  A
+// finisher's unit takes 7000 cycles, half of them the fence before its counter;
+// several units to a fence gained nothing.
 #include <type_traits>
 
 #include "q8_stream.cuh"
@@ -504,8 +506,8 @@ q8_expert_kernel(int ntok, int E, int top_k, int H, int I, int renorm, const int
 // size; larger units leave blocks idle at the end of a projection.
 // Eight rows of a stage are one TMA box of 8-byte elements, 2 KB a row at most:
 // as 16 bulk copies, a stage took its warp 2000 cycles to issue, 13 bytes a
-// cycle.  (Rows then lie a multiple of 512 bytes apart and the 128-bit reads of
-// a fragment meet a two-way bank conflict, which costs nothing here.)  Rows whose
+// cycle.  (Rows then lie a multiple of 512 bytes apart; see unit_products on the
+// bank conflicts that this would make.)  Rows whose
 // length is no multiple of 16 (SHIFT) have no TMA map; they are copied one by one
 // from the 16-byte boundary below and shifted as the fragments are read.
 constexpr int FINISHERS = 2;                               // one per consumer group
@@ -541,7 +543,8 @@ struct EGeom {       // one projection's division
         groups = tiles;
     }
     // as many tiles to a unit as leave every block six units (at 8, 12 and 16 the
-    // layer for one token took 74, 82 and 82 us, at 4 73)
+    // layer for one token took 74, 82 and 82 us, at 4 73).  Units of one tile at the end of a
+    // projection, which would even out the blocks' ends, cost more than that (75 us).
     __device__ __forceinline__ void divide(int chunks, int blocks_of_grid) {
         const int64_t all = (int64_t)tiles * chunks;
         sub = rt == 1 ? 4 : rt == 2 ? 2 : 1;
