@@ -37,18 +37,31 @@ std::atomic<int64_t> g_wait_ns{2000000000LL};   // 2 s
 
 EncodeTiledFn g_encode = nullptr;
 
-// Workspace (A^T for the FFMA kernel): one buffer per (device, stream), grown
-// and freed in stream order, so calls on one stream reuse it safely and calls
-// on different streams never share it.
-std::mutex g_ws_mu;
-std::map<std::pair<int, uintptr_t>, std::pair<void *, size_t>> g_ws;
+// Workspaces (A^T for the FFMA kernel, the 8-bit operators' intermediate rows):
+// one buffer per (device, stream), grown and freed in stream order, so calls on
+// one stream reuse it safely and calls on different streams never share it.  A
+// call holds its buffer's lock from here until its last launch: the launches of
+// two calls that host threads make on one stream then stay apart, and neither
+// frees the buffer that the other has yet to use.
+struct Workspace {
+    std::mutex mu;
+    void *p = nullptr;
+    size_t bytes = 0;
+};
+std::mutex g_ws_mu;                                           // the map alone
+std::map<std::pair<int, uintptr_t>, Workspace> g_ws;          // nodes never move or go
 
-int workspace(size_t bytes, cudaStream_t s, float **out) {
+int workspace(size_t bytes, cudaStream_t s, WorkspaceLease &out) {
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess) return SGEMM_ERR_CUDA;
-    std::lock_guard<std::mutex> lock(g_ws_mu);
-    auto &w = g_ws[{dev, reinterpret_cast<uintptr_t>(s)}];
-    if (w.second < bytes) {
+    Workspace *node = nullptr;
+    {
+        std::lock_guard<std::mutex> lock(g_ws_mu);
+        node = &g_ws[{dev, reinterpret_cast<uintptr_t>(s)}];
+    }
+    Workspace &w = *node;
+    std::unique_lock<std::mutex> lock(w.mu);
+    if (w.bytes < bytes) {
         // An allocation made while `s` is captured would belong to the graph.
         cudaStreamCaptureStatus cs = cudaStreamCaptureStatusNone;
         if (cudaStreamIsCapturing(s, &cs) != cudaSuccess) {
@@ -56,20 +69,23 @@ int workspace(size_t bytes, cudaStream_t s, float **out) {
             return SGEMM_ERR_CUDA;
         }
         if (cs != cudaStreamCaptureStatusNone) return SGEMM_ERR_CAPTURE;
-        const size_t grow = std::max(bytes, w.second + w.second / 2);
+        const size_t grow = std::max(bytes, w.bytes + w.bytes / 2);
         const size_t nb = (grow + (size_t(2) << 20) - 1) & ~((size_t(2) << 20) - 1);
-        if (w.first != nullptr) {
-            if (cudaFreeAsync(w.first, s) != cudaSuccess) return SGEMM_ERR_CUDA;
-            w = {nullptr, 0};
+        if (w.p != nullptr) {
+            if (cudaFreeAsync(w.p, s) != cudaSuccess) return SGEMM_ERR_CUDA;
+            w.p = nullptr;
+            w.bytes = 0;
         }
         void *p = nullptr;
         if (cudaMallocAsync(&p, nb, s) != cudaSuccess) {
             (void)cudaGetLastError();
             return SGEMM_ERR_CUDA;
         }
-        w = {p, nb};
+        w.p = p;
+        w.bytes = nb;
     }
-    *out = static_cast<float *>(w.first);
+    out.p = w.p;
+    out.lock = std::move(lock);
     return SGEMM_OK;
 }
 
@@ -254,22 +270,22 @@ int run(int64_t M, int64_t N, int64_t K, float alpha, const float *A, int64_t ld
         case SGEMM_KERNEL_FFMA_GENERIC: e = launch_ffma_generic(g); break;
         case SGEMM_KERNEL_DECODE: e = launch_decode(g); break;
         case SGEMM_KERNEL_FFMA_TMA: {
-            float *ws = nullptr;
+            WorkspaceLease ws;
             const int64_t nf = ffma_tma_workspace_floats(g, INT64_MAX);
-            const int rc = workspace((size_t)nf * sizeof(float), g.stream, &ws);
+            const int rc = workspace((size_t)nf * sizeof(float), g.stream, ws);
             if (rc != SGEMM_OK) return rc;
-            e = launch_ffma_tma(g, ws, nf);
+            e = launch_ffma_tma(g, static_cast<float *>(ws.p), nf);
             break;
         }
         case SGEMM_KERNEL_TF32X3:
         case SGEMM_KERNEL_TF32:
         case SGEMM_KERNEL_BF16: {
             const int terms = kid == SGEMM_KERNEL_TF32X3 ? 3 : kid == SGEMM_KERNEL_TF32 ? 1 : 0;
-            float *ws = nullptr;
+            WorkspaceLease ws;
             const int rc =
-                workspace(tf32_workspace_floats(M, N, K, terms) * sizeof(float), g.stream, &ws);
+                workspace(tf32_workspace_floats(M, N, K, terms) * sizeof(float), g.stream, ws);
             if (rc != SGEMM_OK) return rc;
-            e = launch_tf32(g, ws, terms);
+            e = launch_tf32(g, static_cast<float *>(ws.p), terms);
             break;
         }
         default: return SGEMM_ERR_BAD_ARG;
@@ -338,12 +354,7 @@ int fill_device_args(GemmArgs &g) {
     return SGEMM_OK;
 }
 
-int stream_workspace(size_t bytes, cudaStream_t s, void **out) {
-    float *p = nullptr;
-    const int rc = workspace(bytes, s, &p);
-    if (rc == SGEMM_OK) *out = p;
-    return rc;
-}
+int stream_workspace(size_t bytes, cudaStream_t s, WorkspaceLease &out) { return workspace(bytes, s, out); }
 }  // namespace sgemm_gb300
 
 extern "C" {
@@ -448,13 +459,16 @@ int sgemm_release_workspaces(void) {
     int cur = 0;
     if (cudaGetDevice(&cur) != cudaSuccess) return SGEMM_ERR_CUDA;
     for (auto &kv : g_ws) {
-        if (kv.second.first == nullptr) continue;
+        Workspace &w = kv.second;
+        std::lock_guard<std::mutex> wlock(w.mu);
+        if (w.p == nullptr) continue;
         cudaStream_t s = reinterpret_cast<cudaStream_t>(kv.first.second);
         if (cudaSetDevice(kv.first.first) != cudaSuccess ||
-            cudaStreamSynchronize(s) != cudaSuccess || cudaFree(kv.second.first) != cudaSuccess)
+            cudaStreamSynchronize(s) != cudaSuccess || cudaFree(w.p) != cudaSuccess)
             rc = SGEMM_ERR_CUDA;
+        w.p = nullptr;
+        w.bytes = 0;
     }
-    g_ws.clear();
     if (cudaSetDevice(cur) != cudaSuccess) rc = SGEMM_ERR_CUDA;
     return rc;
 }

@@ -7,6 +7,8 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <mutex>
+
 namespace sgemm_gb300 {
 
 // Bit set in the per-device error word when a bounded wait runs out.
@@ -126,8 +128,15 @@ bool release_host_paths();
 // (setting the device up on first use); returns an SGEMM_* status.
 int fill_device_args(GemmArgs &g);
 // The workspace of (current device, s), at least `bytes` large and 256-byte
-// aligned; returns an SGEMM_* status.
-int stream_workspace(size_t bytes, cudaStream_t s, void **out);
+// aligned, for one call: it stays that call's until the lease goes, which has to be
+// after the last launch that uses it.  Launches of another host thread's call on
+// the stream would otherwise come between this call's.
+struct WorkspaceLease {
+    std::unique_lock<std::mutex> lock;
+    void *p = nullptr;
+};
+// Returns an SGEMM_* status.
+int stream_workspace(size_t bytes, cudaStream_t s, WorkspaceLease &out);
 
 
 #ifdef __CUDACC__

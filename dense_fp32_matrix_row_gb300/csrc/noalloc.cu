@@ -22,6 +22,7 @@ static __device__ __align__(256) float g_noalloc_scratch[kScratchFloats];
 constexpr int kMaxDevices = 64;
 std::mutex g_mu;
 float *g_scratch_ptr[kMaxDevices];   // device address of the array, per device
+std::mutex g_enqueue_mu;             // one call's launches at a time
 
 // The array's device address on the current device.  In host code the array's
 // name is only a host-side stand-in, so the address is looked up once per
@@ -74,5 +75,6 @@ extern "C" int sgemm_noalloc(int64_t M, int64_t N, int64_t K, float alpha, const
     g.stream = static_cast<cudaStream_t>(stream);
     rc = fill_device_args(g);
     if (rc != SGEMM_OK) return rc;
+    std::lock_guard<std::mutex> lock(g_enqueue_mu);
     return launch_ffma_tma(g, scratch, kScratchFloats) == cudaSuccess ? SGEMM_OK : SGEMM_ERR_CUDA;
 }

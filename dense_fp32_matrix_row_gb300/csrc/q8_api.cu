@@ -160,10 +160,10 @@ int sgemm_q8_linear(int64_t M, int64_t N, int64_t K, const int8_t *X, int64_t ld
     rc = device_args(&a.err, &a.wait_ns, &a.sm_count, &a.encode);
     if (rc != SGEMM_OK) return rc;
     if (streams(a) || !q8_mma_can_run(a)) return launch_status(launch_q8_stream(a));
-    void *work = nullptr;
-    rc = stream_workspace(q8_mma_workspace_bytes(a), a.stream, &work);
+    WorkspaceLease work;
+    rc = stream_workspace(q8_mma_workspace_bytes(a), a.stream, work);
     if (rc != SGEMM_OK) return rc;
-    return launch_status(launch_q8_mma(a, work));
+    return launch_status(launch_q8_mma(a, work.p));
 }
 
 int sgemm_q8_moe(int64_t T, int64_t E, int64_t top_k, int64_t H, int64_t I, const void *x, int64_t ldx, int type,
@@ -204,10 +204,10 @@ int sgemm_q8_moe(int64_t T, int64_t E, int64_t top_k, int64_t H, int64_t I, cons
     a.stream = static_cast<cudaStream_t>(stream);
     rc = device_args(&a.err, &a.wait_ns, &a.sm_count, &a.encode);
     if (rc != SGEMM_OK) return rc;
-    void *work = nullptr;
-    rc = stream_workspace(q8_moe_workspace_bytes(a.T, a.E, a.top_k, a.H, a.I), a.stream, &work);
+    WorkspaceLease work;
+    rc = stream_workspace(q8_moe_workspace_bytes(a.T, a.E, a.top_k, a.H, a.I), a.stream, work);
     if (rc != SGEMM_OK) return rc;
-    return launch_status(launch_q8_moe(a, work));
+    return launch_status(launch_q8_moe(a, work.p));
 }
 
 }  // extern "C"

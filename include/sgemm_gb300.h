@@ -46,7 +46,8 @@
  *             enqueued, and nothing is written.  Errors inside a kernel
  *             (a bounded wait that ran out) are recorded in a per-device
  *             word and reported by sgemm_status().
- * Threads     Entry points may be called from several host threads at once.
+ * Threads     Entry points may be called from several host threads at once, on one
+ *             stream too: each call's launches are enqueued together.
  */
 #ifndef SGEMM_GB300_H
 #define SGEMM_GB300_H
