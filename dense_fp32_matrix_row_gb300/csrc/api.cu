@@ -8,6 +8,7 @@
 #include <map>
 #include <mutex>
 #include <utility>
+#include <vector>
 
 #include "common.cuh"
 #include "sgemm_gb300.h"
@@ -47,11 +48,17 @@ struct Workspace {
     std::mutex mu;
     void *p = nullptr;
     size_t bytes = 0;
+    bool in_graph = false;      // a captured call used it: a graph may hold its address
+    std::vector<void *> kept;   // earlier buffers that graphs may hold
 };
 std::mutex g_ws_mu;                                           // the map alone
 std::map<std::pair<int, uintptr_t>, Workspace> g_ws;          // nodes never move or go
 
-int workspace(size_t bytes, cudaStream_t s, WorkspaceLease &out) {
+// The legacy default stream cannot be captured (and may not be asked while
+// another stream is).
+bool may_be_captured(cudaStream_t s) { return s != nullptr && s != cudaStreamLegacy; }
+
+int workspace(size_t bytes, cudaStream_t s, WorkspaceLease &out) try {
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess) return SGEMM_ERR_CUDA;
     Workspace *node = nullptr;
@@ -61,20 +68,25 @@ int workspace(size_t bytes, cudaStream_t s, WorkspaceLease &out) {
     }
     Workspace &w = *node;
     std::unique_lock<std::mutex> lock(w.mu);
-    if (w.bytes < bytes) {
-        // An allocation made while `s` is captured would belong to the graph.
-        cudaStreamCaptureStatus cs = cudaStreamCaptureStatusNone;
+    cudaStreamCaptureStatus cs = cudaStreamCaptureStatusNone;
+    if (w.bytes < bytes || (!w.in_graph && may_be_captured(s)))
         if (cudaStreamIsCapturing(s, &cs) != cudaSuccess) {
             (void)cudaGetLastError();
             return SGEMM_ERR_CUDA;
         }
-        if (cs != cudaStreamCaptureStatusNone) return SGEMM_ERR_CAPTURE;
+    const bool capturing = cs != cudaStreamCaptureStatusNone;
+    if (w.bytes < bytes) {
+        // An allocation made while `s` is captured would belong to the graph.
+        if (capturing) return SGEMM_ERR_CAPTURE;
         const size_t grow = std::max(bytes, w.bytes + w.bytes / 2);
         const size_t nb = (grow + (size_t(2) << 20) - 1) & ~((size_t(2) << 20) - 1);
         if (w.p != nullptr) {
-            if (cudaFreeAsync(w.p, s) != cudaSuccess) return SGEMM_ERR_CUDA;
+            // a graph's replays go on reading and writing what it was captured with
+            if (w.in_graph) w.kept.push_back(w.p);
+            else if (cudaFreeAsync(w.p, s) != cudaSuccess) return SGEMM_ERR_CUDA;
             w.p = nullptr;
             w.bytes = 0;
+            w.in_graph = false;
         }
         void *p = nullptr;
         if (cudaMallocAsync(&p, nb, s) != cudaSuccess) {
@@ -84,9 +96,12 @@ int workspace(size_t bytes, cudaStream_t s, WorkspaceLease &out) {
         w.p = p;
         w.bytes = nb;
     }
+    w.in_graph = w.in_graph || capturing;
     out.p = w.p;
     out.lock = std::move(lock);
     return SGEMM_OK;
+} catch (...) {      // no memory for the map or the list
+    return SGEMM_ERR_CUDA;
 }
 
 // Per-device set-up: check the architecture, find the error word, look up
@@ -461,13 +476,17 @@ int sgemm_release_workspaces(void) {
     for (auto &kv : g_ws) {
         Workspace &w = kv.second;
         std::lock_guard<std::mutex> wlock(w.mu);
-        if (w.p == nullptr) continue;
+        if (w.p == nullptr && w.kept.empty()) continue;
         cudaStream_t s = reinterpret_cast<cudaStream_t>(kv.first.second);
         if (cudaSetDevice(kv.first.first) != cudaSuccess ||
             cudaStreamSynchronize(s) != cudaSuccess || cudaFree(w.p) != cudaSuccess)
             rc = SGEMM_ERR_CUDA;
+        for (void *p : w.kept)
+            if (cudaFree(p) != cudaSuccess) rc = SGEMM_ERR_CUDA;
+        w.kept.clear();
         w.p = nullptr;
         w.bytes = 0;
+        w.in_graph = false;
     }
     if (cudaSetDevice(cur) != cudaSuccess) rc = SGEMM_ERR_CUDA;
     return rc;

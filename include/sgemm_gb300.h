@@ -125,7 +125,12 @@ extern "C" {
  * once a call of the same shape has run eagerly on the same stream and
  * device: that call sets up the device and sizes the stream's workspace.  A
  * captured call never allocates: one that would need a larger workspace
- * returns SGEMM_ERR_CAPTURE with nothing enqueued.
+ * returns SGEMM_ERR_CAPTURE with nothing enqueued.  A workspace that a
+ * captured call used is kept for the graph's replays: a later call that needs
+ * a larger one gets another beside it.  sgemm_release_workspaces frees it, so
+ * destroy such graphs first.  Replays use the capture stream's workspace, so
+ * on another stream they must not overlap with that stream's calls or with
+ * another graph captured on it.
  * Returns SGEMM_OK, or an argument/launch error code (nothing enqueued).
  */
 int sgemm(int64_t M, int64_t N, int64_t K, float alpha,
@@ -431,7 +436,8 @@ int64_t sgemm_host_panel_rows(int64_t M, int64_t N, int64_t K);
  * operators' intermediate rows; one buffer per device and stream, grown with cudaMallocAsync on the call's stream) and
  * sgemm_host's device buffers, copy streams and events.
  * Waits for every stream that owns a workspace.  Call it only while no other
- * host thread is inside an sgemm call; later calls allocate again as needed.
+ * host thread is inside an sgemm call, and after the graphs that captured calls
+ * are gone; later calls allocate again as needed.
  * Returns SGEMM_OK or SGEMM_ERR_CUDA.
  */
 int sgemm_release_workspaces(void);

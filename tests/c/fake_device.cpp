@@ -2,8 +2,8 @@
 // the CUDA runtime and the kernel launchers, so that what the host does with its
 // workspaces can be followed without a GPU.
 //
-// Device memory is host memory from a list of live buffers; a launcher stands for
-// the kernels that it would enqueue: it takes a while, and checks that its
+// Device memory is a list of live buffers, never touched; a launcher stands for the
+// kernels that it would enqueue: it takes a while, and checks that its
 // workspace is live and that no other launcher works with it meanwhile.  The
 // program runs the scenario named on its command line and exits with the number
 // of faults found, each with a line on stderr.
@@ -12,7 +12,6 @@
 #include <atomic>
 #include <chrono>
 #include <cstdio>
-#include <cstdlib>
 #include <cstring>
 #include <map>
 #include <mutex>
@@ -27,11 +26,12 @@
 namespace {
 
 std::mutex mu;
-std::map<void *, size_t> live;              // buffers by address
+std::set<void *> live;                      // buffers
 std::map<void *, std::thread::id> users;    // buffers a launcher works with
 std::set<cudaStream_t> captured;            // streams under capture
 alignas(256) unsigned symbol[64];   // the address of every __device__ variable
 std::atomic<int> faults{0}, launches{0};
+thread_local void *last = nullptr;          // workspace of this thread's last launch
 size_t most_users = 0;                      // launchers at work at one time, at most
 
 void fault(const char *what) {
@@ -57,20 +57,16 @@ cudaError_t launched(void *ws) {
         auto it = users.find(ws);
         if (it != users.end() && it->second == std::this_thread::get_id()) users.erase(it);
     }
+    last = ws;
     ++launches;
     return cudaSuccess;
 }
 
 cudaError_t release(void *p) {
     std::lock_guard<std::mutex> lock(mu);
-    auto it = live.find(p);
-    if (it == live.end()) {
-        fault("a buffer was freed that is not allocated");
-        return cudaErrorInvalidValue;
-    }
-    std::free(p);
-    live.erase(it);
-    return cudaSuccess;
+    if (live.erase(p) != 0) return cudaSuccess;
+    fault("a buffer was freed that is not allocated");
+    return cudaErrorInvalidValue;
 }
 
 }  // namespace
@@ -104,8 +100,9 @@ cudaError_t cudaStreamIsCapturing(cudaStream_t s, cudaStreamCaptureStatus *st) {
 cudaError_t cudaMallocAsync(void **p, size_t, cudaStream_t s) {
     std::lock_guard<std::mutex> lock(mu);
     if (captured.count(s)) fault("an allocation on a stream under capture");
-    *p = std::malloc(256);
-    live[*p] = 1;
+    static uintptr_t next = (uintptr_t)1 << 50;     // an address is given once
+    *p = reinterpret_cast<void *>(next += 256);
+    live.insert(*p);
     return cudaSuccess;
 }
 cudaError_t cudaFreeAsync(void *p, cudaStream_t) { return release(p); }
@@ -211,12 +208,54 @@ void threads_on_their_own_streams() {
     if (most_users < 2) fault("calls on different streams ran one after another");
 }
 
+void capture(cudaStream_t s, bool on) {
+    std::lock_guard<std::mutex> lock(mu);
+    if (on) captured.insert(s);
+    else captured.erase(s);
+}
+
+// A workspace that a captured call used is there for the graph's replays, whatever
+// is called on the stream afterwards.
+void graph_keeps_its_workspace() {
+    const cudaStream_t s = stream(0);
+    std::vector<void *> in_graph;
+    for (int64_t size : {100, 1000, 30000}) {       // a graph on each of three growing workspaces
+        expect(linear(size, s), SGEMM_OK, "eager");
+        expect(moe(8, s), SGEMM_OK, "eager");
+        capture(s, true);
+        expect(moe(8, s), SGEMM_OK, "captured");
+        in_graph.push_back(last);
+        expect(linear(size, s), SGEMM_OK, "captured again");
+        if (last != in_graph.back()) fault("two captured calls got different workspaces");
+        const int before = launches;
+        expect(linear(100 * size, s), SGEMM_ERR_CAPTURE, "a captured call that needs a larger workspace");
+        if (launches != before) fault("a refused call launched something");
+        capture(s, false);
+        expect(moe(8, s), SGEMM_OK, "eager again");
+    }
+    expect(product(20000, s), SGEMM_OK, "a last growth");
+    expect(linear(300000, s), SGEMM_OK, "a last growth");
+    std::lock_guard<std::mutex> lock(mu);
+    for (void *p : in_graph)
+        if (live.count(p) == 0) fault("a graph's workspace was freed");
+}
+
+// Without a capture, growth frees what it replaces.
+void growth_frees_the_old_workspace() {
+    for (int64_t size : {100, 1000, 30000, 200000}) {
+        expect(linear(size, stream(0)), SGEMM_OK, "linear");
+        if (live.size() != 1) fault("a replaced workspace was kept");
+    }
+}
+
 }  // namespace
 
 int main(int argc, char **argv) {
     const struct { const char *name; void (*run)(); } scenarios[] = {
         {"threads_share_a_stream", threads_share_a_stream},
         {"threads_on_their_own_streams", threads_on_their_own_streams},
+        {"graph_keeps_its_workspace", graph_keeps_its_workspace},
+        {"growth_frees_the_old_workspace", growth_frees_the_old_workspace},
     };
     for (const auto &s : scenarios)
         if (argc == 2 && std::strcmp(argv[1], s.name) == 0) {

@@ -1,5 +1,5 @@
 """What the entry points do with their stream workspaces, on a stand-in for the
-CUDA runtime (tests/c/fake_device.cpp): host threads that share a stream."""
+CUDA runtime (tests/c/fake_device.cpp): host threads that share a stream, and graphs."""
 
 import os
 import subprocess
@@ -31,4 +31,9 @@ def run(program, scenario):
 
 @pytest.mark.parametrize("scenario", ["threads_share_a_stream", "threads_on_their_own_streams"])
 def test_host_threads(program, scenario):
+    run(program, scenario)
+
+
+@pytest.mark.parametrize("scenario", ["graph_keeps_its_workspace", "growth_frees_the_old_workspace"])
+def test_capture(program, scenario):
     run(program, scenario)
