@@ -52,7 +52,7 @@ struct Workspace {
     std::vector<void *> kept;   // earlier buffers that graphs may hold
 };
 std::mutex g_ws_mu;                                           // the map alone
-std::map<std::pair<int, uintptr_t>, Workspace> g_ws;          // nodes never move or go
+std::map<StreamKey, Workspace> g_ws;                          // nodes never move or go
 
 // The legacy default stream cannot be captured (and may not be asked while
 // another stream is).
@@ -64,7 +64,7 @@ int workspace(size_t bytes, cudaStream_t s, WorkspaceLease &out) try {
     Workspace *node = nullptr;
     {
         std::lock_guard<std::mutex> lock(g_ws_mu);
-        node = &g_ws[{dev, reinterpret_cast<uintptr_t>(s)}];
+        node = &g_ws[StreamKey(dev, s)];
     }
     Workspace &w = *node;
     std::unique_lock<std::mutex> lock(w.mu);
@@ -477,9 +477,8 @@ int sgemm_release_workspaces(void) {
         Workspace &w = kv.second;
         std::lock_guard<std::mutex> wlock(w.mu);
         if (w.p == nullptr && w.kept.empty()) continue;
-        cudaStream_t s = reinterpret_cast<cudaStream_t>(kv.first.second);
-        if (cudaSetDevice(kv.first.first) != cudaSuccess ||
-            cudaStreamSynchronize(s) != cudaSuccess || cudaFree(w.p) != cudaSuccess)
+        if (cudaSetDevice(kv.first.dev) != cudaSuccess ||
+            kv.first.synchronize() != cudaSuccess || cudaFree(w.p) != cudaSuccess)
             rc = SGEMM_ERR_CUDA;
         for (void *p : w.kept)
             if (cudaFree(p) != cudaSuccess) rc = SGEMM_ERR_CUDA;

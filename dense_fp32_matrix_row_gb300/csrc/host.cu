@@ -46,7 +46,7 @@ struct HostPath {
 };
 
 std::mutex g_mu;
-std::map<std::pair<int, uintptr_t>, HostPath> g_paths;   // nodes never move
+std::map<StreamKey, HostPath> g_paths;                      // nodes never move
 std::atomic<int> g_panels{0};                               // 0: the library's choice
 
 size_t round_up(size_t v, size_t a) { return (v + a - 1) / a * a; }
@@ -168,10 +168,10 @@ bool release_host_paths() {
         HostPath &h = kv.second;
         std::lock_guard<std::mutex> plock(h.mu);
         if (!h.ready) continue;
-        if (cudaSetDevice(kv.first.first) != cudaSuccess ||
+        if (cudaSetDevice(kv.first.dev) != cudaSuccess ||
             cudaStreamSynchronize(h.up) != cudaSuccess ||
             cudaStreamSynchronize(h.down) != cudaSuccess ||
-            cudaStreamSynchronize(reinterpret_cast<cudaStream_t>(kv.first.second)) != cudaSuccess)
+            kv.first.synchronize() != cudaSuccess)
             ok = false;
         destroy(h);
     }
@@ -210,7 +210,7 @@ int sgemm_host(int64_t M, int64_t N, int64_t K, float alpha, const float *A, int
     HostPath *hp = nullptr;
     {
         std::lock_guard<std::mutex> lock(g_mu);
-        hp = &g_paths[{dev, reinterpret_cast<uintptr_t>(S)}];
+        hp = &g_paths[StreamKey(dev, S)];
     }
     HostPath &h = *hp;
     std::lock_guard<std::mutex> plock(h.mu);

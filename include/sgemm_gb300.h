@@ -47,7 +47,9 @@
  *             (a bounded wait that ran out) are recorded in a per-device
  *             word and reported by sgemm_status().
  * Threads     Entry points may be called from several host threads at once, on one
- *             stream too: each call's launches are enqueued together.
+ *             stream too: each call's launches are enqueued together.  A thread
+ *             that uses cudaStreamPerThread has buffers of its own, kept like
+ *             a stream's until sgemm_release_workspaces.
  */
 #ifndef SGEMM_GB300_H
 #define SGEMM_GB300_H

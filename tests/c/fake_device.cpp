@@ -208,6 +208,20 @@ void threads_on_their_own_streams() {
     if (most_users < 2) fault("calls on different streams ran one after another");
 }
 
+// cudaStreamPerThread names another stream in each thread: no buffer is shared.
+void per_thread_streams_share_nothing() {
+    void *seen[3] = {};
+    std::vector<std::thread> all;
+    for (int t = 0; t < 3; ++t)
+        all.emplace_back([t, &seen] {
+            for (int i = 0; i < 20; ++i) expect(moe(8 + i, cudaStreamPerThread), SGEMM_OK, "moe");
+            seen[t] = last;
+        });
+    for (auto &t : all) t.join();
+    if (seen[0] == seen[1] || seen[1] == seen[2] || seen[0] == seen[2])
+        fault("streams of different threads got one workspace");
+}
+
 void capture(cudaStream_t s, bool on) {
     std::lock_guard<std::mutex> lock(mu);
     if (on) captured.insert(s);
@@ -254,6 +268,7 @@ int main(int argc, char **argv) {
     const struct { const char *name; void (*run)(); } scenarios[] = {
         {"threads_share_a_stream", threads_share_a_stream},
         {"threads_on_their_own_streams", threads_on_their_own_streams},
+        {"per_thread_streams_share_nothing", per_thread_streams_share_nothing},
         {"graph_keeps_its_workspace", graph_keeps_its_workspace},
         {"growth_frees_the_old_workspace", growth_frees_the_old_workspace},
     };

@@ -1,4 +1,5 @@
-"""Entry points called from several host threads at once on one stream."""
+"""Entry points called from several host threads at once, on one stream and on the
+stream that each thread has of its own."""
 
 import threading
 
@@ -41,8 +42,13 @@ def calls(seed, stream):
             lambda: sg.sgemm(a, b, out[2], stream=stream)], out
 
 
-def test_threads_on_one_stream_get_their_own_results():
-    stream = torch.cuda.Stream()
+PER_THREAD = 2      # the handle cudaStreamPerThread
+
+
+@pytest.mark.parametrize("stream", ["shared", PER_THREAD])
+def test_threads_get_their_own_results(stream):
+    if stream == "shared":
+        stream = torch.cuda.Stream()
     work = [calls(seed, stream) for seed in range(4)]
     torch.cuda.synchronize()
     for todo, _ in work:
@@ -63,6 +69,7 @@ def test_threads_on_one_stream_get_their_own_results():
             for _ in range(50):
                 for call in todo:
                     call()
+            assert sg.status(stream) == sg.OK
         except Exception as e:      # noqa: BLE001  (reported below)
             errors.append(e)
 
@@ -72,6 +79,7 @@ def test_threads_on_one_stream_get_their_own_results():
     for t in threads:
         t.join()
     assert not errors, errors
-    assert sg.status(stream) == sg.OK
+    torch.cuda.synchronize()
     for (_, out), w in zip(work, want):
         assert all(torch.equal(g, h) for g, h in zip(out, w))
+    assert sg.release_workspaces() == sg.OK

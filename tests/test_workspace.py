@@ -29,7 +29,8 @@ def run(program, scenario):
     assert r.returncode == 0, r.stderr[-2000:]
 
 
-@pytest.mark.parametrize("scenario", ["threads_share_a_stream", "threads_on_their_own_streams"])
+@pytest.mark.parametrize("scenario", ["threads_share_a_stream", "threads_on_their_own_streams",
+                                      "per_thread_streams_share_nothing"])
 def test_host_threads(program, scenario):
     run(program, scenario)
 
