@@ -35,41 +35,45 @@ q8_stream_kernel(int M, int N, int K, const int8_t *__restrict__ X, int64_t ldx,
     const int rt = SWARPS / kw;                     // 16-row tiles per block
     const int tile = warp / kw, kpart = warp % kw;
     const int n0 = ((int)blockIdx.x * rt + tile) * 16;
-    const int m0 = (int)blockIdx.y * TOK;
     pdl_wait();
-    int sum[NB][4];
+    // a grid has 65535 blocks in y at most: beyond, a block takes several blocks of tokens
+    for (int64_t first = (int64_t)blockIdx.y * TOK; first < M; first += (int64_t)gridDim.y * TOK) {
+        const int m0 = (int)first;
+        int sum[NB][4];
 #pragma unroll
-    for (int n = 0; n < NB; ++n)
+        for (int n = 0; n < NB; ++n)
 #pragma unroll
-        for (int i = 0; i < 4; ++i) sum[n][i] = 0;
-    if (n0 < N) {
-        // rows past N and tokens past M read the last one; their results are dropped
-        const int ra = min(n0 + g, N - 1), rb = min(n0 + g + 8, N - 1);
-        const int8_t *x[NB];
+            for (int i = 0; i < 4; ++i) sum[n][i] = 0;
+        if (n0 < N) {
+            // rows past N and tokens past M read the last one; their results are dropped
+            const int ra = min(n0 + g, N - 1), rb = min(n0 + g + 8, N - 1);
+            const int8_t *x[NB];
 #pragma unroll
-        for (int n = 0; n < NB; ++n) x[n] = X + (int64_t)min(m0 + 8 * n + g, M - 1) * ldx;
-        const int steps = (K + kQ8Step - 1) / kQ8Step;
-        const int per = (steps + kw - 1) / kw;
-        const int s0 = min(kpart * per, steps), s1 = min(s0 + per, steps);
-        q8_dot<NB, VEC, 4>(sum, W + (int64_t)ra * ldw, W + (int64_t)rb * ldw, x, K, s0, s1, W,
-                           W + (int64_t)(N - 1) * ldw + K, X, X + (int64_t)(M - 1) * ldx + K);
-    }
+            for (int n = 0; n < NB; ++n) x[n] = X + (int64_t)min(m0 + 8 * n + g, M - 1) * ldx;
+            const int steps = (K + kQ8Step - 1) / kQ8Step;
+            const int per = (steps + kw - 1) / kw;
+            const int s0 = min(kpart * per, steps), s1 = min(s0 + per, steps);
+            q8_dot<NB, VEC, 4>(sum, W + (int64_t)ra * ldw, W + (int64_t)rb * ldw, x, K, s0, s1, W,
+                               W + (int64_t)(N - 1) * ldw + K, X, X + (int64_t)(M - 1) * ldx + K);
+        }
 #pragma unroll
-    for (int n = 0; n < NB; ++n) {
-        part[warp][g][8 * n + 2 * t] = sum[n][0];
-        part[warp][g][8 * n + 2 * t + 1] = sum[n][1];
-        part[warp][g + 8][8 * n + 2 * t] = sum[n][2];
-        part[warp][g + 8][8 * n + 2 * t + 1] = sum[n][3];
-    }
-    __syncthreads();
-    for (int o = threadIdx.x; o < rt * 16 * TOK; o += SWARPS * 32) {
-        const int row = o % 16, tl = (o / 16) % rt, tok = o / (16 * rt);
-        const int n = ((int)blockIdx.x * rt + tl) * 16 + row, m = m0 + tok;
-        if (n >= N || m >= M) continue;
-        int s = 0;
-        for (int w = 0; w < kw; ++w) s += part[tl * kw + w][row][tok];
-        const float v = (float)s * xs[m] * ws[n];
-        C[(int64_t)m * ldc + n] = from_f32<OutT>(epilogue_tail(ep, v, n));
+        for (int n = 0; n < NB; ++n) {
+            part[warp][g][8 * n + 2 * t] = sum[n][0];
+            part[warp][g][8 * n + 2 * t + 1] = sum[n][1];
+            part[warp][g + 8][8 * n + 2 * t] = sum[n][2];
+            part[warp][g + 8][8 * n + 2 * t + 1] = sum[n][3];
+        }
+        __syncthreads();
+        for (int o = threadIdx.x; o < rt * 16 * TOK; o += SWARPS * 32) {
+            const int row = o % 16, tl = (o / 16) % rt, tok = o / (16 * rt);
+            const int n = ((int)blockIdx.x * rt + tl) * 16 + row, m = m0 + tok;
+            if (n >= N || m >= M) continue;
+            int s = 0;
+            for (int w = 0; w < kw; ++w) s += part[tl * kw + w][row][tok];
+            const float v = (float)s * xs[m] * ws[n];
+            C[(int64_t)m * ldc + n] = from_f32<OutT>(epilogue_tail(ep, v, n));
+        }
+        __syncthreads();   // `part` is written again
     }
 }
 
@@ -332,9 +336,8 @@ cudaError_t launch_s(const Q8LinearArgs &a) {
     while (kw < SWARPS && steps >= 8 * kw) kw *= 2;   // at least 4 steps a warp
     const int64_t rows = 16 * (SWARPS / kw);
     const int64_t mb = (a.M + NB * 8 - 1) / (NB * 8);
-    if (mb > 65535) return cudaErrorInvalidConfiguration;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)((a.N + rows - 1) / rows), (unsigned)mb, 1);
+    cfg.gridDim = dim3((unsigned)((a.N + rows - 1) / rows), (unsigned)(mb < 65535 ? mb : 65535), 1);
     cfg.blockDim = dim3(SWARPS * 32, 1, 1);
     cfg.stream = a.stream;
     cudaLaunchAttribute attr[1];
