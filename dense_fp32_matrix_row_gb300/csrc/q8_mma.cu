@@ -40,7 +40,9 @@
 // the parts' sums go to the workspace and the last warp to arrive adds them in
 // part order.
 //
-// Every wait is bounded; on a time-out the roles record it and wind down.
+// Every wait is bounded; on a time-out the roles record it and wind down.  Whichever
+// role gave up, the block ends (and gives tensor memory back) only when its copies
+// have landed and its MMAs are done.
 //
 // Measured: 8192 x 14336 x 4096 492 us in a burst (1950 TFLOP/s of FP16 MMAs, bound
 // by the tensor cores), 534 sustained, with 2 us for X's expansion; 2048 x 4096 x
@@ -160,6 +162,18 @@ __device__ __forceinline__ void arrive_relaxed(uint32_t bar, uint32_t cta) {
                  : "memory");
 }
 
+// Adds to a word in shared memory of CTA `cta` of the cluster.  (With a plain store to
+// the other SM, the 256-token kernel spills 70 registers, with this one 2.)
+__device__ __forceinline__ void add_cta(uint32_t addr, uint32_t cta, uint32_t v) {
+    asm volatile("red.relaxed.cluster.shared::cluster.add.u32 [%0], %1;" ::"r"(cluster_addr(addr, cta)), "r"(v)
+                 : "memory");
+}
+
+// Takes `bytes` off what the barrier's phase still waits for.
+__device__ __forceinline__ void mbar_complete_tx(uint32_t bar, uint32_t bytes) {
+    asm volatile("mbarrier.complete_tx.relaxed.cta.shared::cta.b64 [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
+}
+
 // One stage of X: 128 k of NL tokens as two 64-wide halves, through a map whose
 // dimensions are (k % 64, token, k / 64).
 template <bool PAIR>
@@ -223,6 +237,10 @@ q8_mma_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ C
     uint64_t *dempty = dfull + 2;       // [2] accumulator has been read
     uint64_t *drainbar = dempty + 2;
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(drainbar + 1);
+    // For a pair that gives up (at fixed addresses, which take no registers beside the
+    // epilogue's sums): whether a role of either SM did, the stages of X that each SM issued
+    // (on the even SM), and where xfull is.
+    __shared__ uint32_t gave_up, xcount[2], xfull_at;
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     uint32_t rank = 0;
@@ -248,6 +266,8 @@ q8_mma_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ C
         }
         mbar_init(smem_u32(drainbar), 1);
         mbar_fence_init();
+        gave_up = xcount[0] = xcount[1] = 0u;
+        xfull_at = smem_u32(xfull);
     }
     if (warp == 0) {
         __syncwarp();
@@ -266,6 +286,11 @@ q8_mma_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ C
     if constexpr (PAIR) cluster_sync_all();
     tc_fence_after();
     const uint32_t tmem = *reinterpret_cast<volatile uint32_t *>(tmem_slot);
+    auto fail = [err] {    // one lane of a role that gave up
+        record_error(err, kErrWaitTimeout);
+        if constexpr (PAIR)
+            for (uint32_t cta = 0; cta < 2; ++cta) add_cta(smem_u32(&gave_up), cta, 1u);
+    };
 
     if (warp < EPI_WARPS) {
         // Epilogue warp w: tensor-memory lanes 32 * (w % 4) .. + 31 (a W row
@@ -369,7 +394,7 @@ q8_mma_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ C
                     if (n < N && m0 + at(j) < M) o[(int64_t)at(j) * ldc] = from_f32<OutT>(acc[j]);
             }
         }
-        if (!ok && lane == 0) record_error(err, kErrWaitTimeout);
+        if (!ok && lane == 0) fail();
     } else if (warp < W_WARP) {
         // Converter warp w: W rows (tensor-memory lanes) 32 * (w % 4) .. + 31 of
         // the stages of parity (w / 4) % 2.
@@ -428,7 +453,7 @@ q8_mma_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ C
                 else mbar_arrive(smem_u32(&afull[s]));
             }
         }
-        if (!ok && lane == 0) record_error(err, kErrWaitTimeout);
+        if (!ok && lane == 0) fail();
     } else {
         set_registers<OTHER_REGS, false>();
         if (warp == W_WARP || warp == X_WARP) {
@@ -471,18 +496,14 @@ q8_mma_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ C
                     __syncwarp();
                 }
             }
-            if (!ok && lane == 0) {   // wait for the copies still in flight
-                record_error(err, kErrWaitTimeout);
-                if (is_w || lead) {
+            if (lane == 0) {
+                if (!ok) fail();
+                if (PAIR && !is_w) {      // a pair's X completes on the even SM: see the end
+                    add_cta(smem_u32(&xcount[rank]), 0, g);
+                } else {
                     for (uint32_t q = g > (uint32_t)depth ? g - (uint32_t)depth : 0; q < g; ++q)
                         mbar_wait(smem_u32(&(is_w ? wfull : xfull)[q % (uint32_t)depth]), (q / (uint32_t)depth) & 1,
                                   DRAIN_NS);
-                } else {
-                    // copies of the odd SM complete on the even SM's barriers,
-                    // possibly in phases it gave up on: give them time to land
-                    const uint64_t d0 = globaltimer_ns();
-                    while (globaltimer_ns() - d0 < 200000ull) {
-                    }
                 }
             }
         } else if (warp == MMA_WARP && lead) {
@@ -566,27 +587,46 @@ q8_mma_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ C
                     }
                 }
             }
-            if (!ok) {
-                if (lane == 0) record_error(err, kErrWaitTimeout);
-                if (issued) {
-                    if (elect_one()) {
-                        if constexpr (PAIR)
-                            asm volatile(
-                                "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(
-                                    smem_u32(drainbar)) : "memory");
-                        else
-                            tc_commit(smem_u32(drainbar));
-                    }
-                    __syncwarp();
-                    mbar_wait(smem_u32(drainbar), 0, DRAIN_NS);
+            if (!ok && lane == 0) fail();
+            if (issued) {     // the epilogue may have given up on the last chunks
+                if (elect_one()) {
+                    if constexpr (PAIR)
+                        asm volatile(
+                            "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(
+                                smem_u32(drainbar)) : "memory");
+                    else
+                        tc_commit(smem_u32(drainbar));
                 }
+                __syncwarp();
+                mbar_wait(smem_u32(drainbar), 0, DRAIN_NS);
             }
         }
     }
 
     tc_fence_before();
     __syncthreads();
-    if constexpr (PAIR) cluster_sync_all();
+    if constexpr (PAIR) {
+        cluster_sync_all();
+        if (*const_cast<volatile uint32_t *>(&gave_up) != 0u) {    // as in the other SM: both were told
+            // Both SMs' stages of X complete on the even SM's barriers, and one may have
+            // issued more than the other.  Its barriers get what is missing, then are waited
+            // for: a stage is issued after the MMAs of the stage ST before it, so that only the
+            // last ST can be open.
+            uint32_t cta;
+            asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(cta));
+            if (cta == 0 && threadIdx.x == X_WARP * 32) {
+                const uint32_t own = xcount[0], other = xcount[1], most = max(own, other);
+                for (uint32_t q = most > (uint32_t)ST ? most - ST : 0; q < most; ++q) {
+                    const uint32_t bar = xfull_at + q % ST * 8;
+                    if (q >= own) mbar_arrive_expect_tx(bar, C::X_STAGE);
+                    else if (q >= other) mbar_complete_tx(bar, C::X_STAGE);
+                    mbar_wait(bar, (q / ST) & 1, DRAIN_NS);
+                }
+            }
+            __syncwarp();
+            cluster_sync_all();
+        }
+    }
     if (warp == 0) {
         __syncwarp();
         tc_fence_after();

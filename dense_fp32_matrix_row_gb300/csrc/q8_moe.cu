@@ -851,8 +851,9 @@ __device__ __noinline__ void produce(EShared &S, uint32_t ring, const CUtensorMa
             }
         }
     }
-    if (!ok && lane == 0) {
-        record_error(A.err, kErrWaitTimeout);
+    // The block may not end before its copies have landed, whichever role gave up.
+    if (lane == 0) {
+        if (!ok) record_error(A.err, kErrWaitTimeout);
         for (uint32_t q = g > (uint32_t)ERING ? g - ERING : 0; q < g; ++q)
             mbar_wait(smem_u32(&S.full[q % ERING]), (q / ERING) & 1, 1000000000ull);
     }

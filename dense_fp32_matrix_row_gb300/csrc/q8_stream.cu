@@ -151,8 +151,10 @@ q8_ring_kernel(int M, int N, int K, const int8_t *__restrict__ X,
                               bytes, bar);
                 __syncwarp();
             }
-        if (!ok && lane == 0) {
-            record_error(err, kErrWaitTimeout);
+        // The block may not end before its copies have landed, whichever warp gave up.
+        // (Otherwise they have been waited for already, or are about to be.)
+        if (lane == 0) {
+            if (!ok) record_error(err, kErrWaitTimeout);
             for (uint32_t q = g > (uint32_t)RING ? g - RING : 0; q < g; ++q)
                 mbar_wait(smem_u32(&full[q % RING]), (q / RING) & 1, DRAIN_NS);
         }
