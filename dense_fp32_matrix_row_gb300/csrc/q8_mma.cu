@@ -344,6 +344,7 @@ q8_mma_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ C
                 if (lane == 0) arrived = atomicAdd(counters + (tile * C::R + (int)rank) * EPI_WARPS + warp, 1u);
                 arrived = __shfl_sync(0xffffffffu, arrived, 0);
                 if (arrived != (uint32_t)(plan.ks - 1)) continue;
+                __syncwarp();      // lane 0's count before the other lanes' fences
                 __threadfence();
                 float sum[COLS];
 #pragma unroll

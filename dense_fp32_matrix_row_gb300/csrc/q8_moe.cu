@@ -628,7 +628,10 @@ __device__ __forceinline__ bool warp_poll_all(const uint32_t *p, int count, uint
             ok = ld_acquire(p + lane) >= want;
         } while (!ok && globaltimer_ns() - t0 <= wait_ns);
     }
-    return __all_sync(0xffffffffu, ok) != 0;
+    // the vote orders no memory accesses: what one lane acquired is the others' from here
+    ok = __all_sync(0xffffffffu, ok) != 0;
+    __syncwarp();
+    return ok;
 }
 
 // The products of one unit by one warp of a consumer group, into the buffer

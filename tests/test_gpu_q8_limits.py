@@ -88,3 +88,22 @@ def test_a_wait_that_runs_out_is_reported_and_leaves_nothing_behind(name):
             assert torch.equal(out, want)
     finally:
         sg.set_wait_limit(0)
+
+
+# ---- hand-overs between blocks ------------------------------------------------------
+
+@pytest.mark.parametrize("make", [lambda: moe_case(16, 24, 4, 1096, 520), lambda: moe_case(2, 3, 3, 4096, 200),
+                                  lambda: linear_case(100, 4096, 8192)])
+def test_sums_of_other_blocks_are_complete_every_time(make):
+    """Results that are added from several blocks' parts (experts by one warp whose lanes
+    watch a column group each; parts of K by the last warp to arrive), 200 times."""
+    call, out = make()
+    call()
+    want = out.clone()
+    wrong = torch.zeros((), dtype=torch.int64, device="cuda")
+    for _ in range(200):
+        out.zero_()
+        call()
+        wrong += (out != want).sum()
+    assert sg.status() == sg.OK
+    assert int(wrong) == 0
