@@ -74,6 +74,15 @@ constexpr int kMoeMaxTokens = 64, kMoeMaxTopK = 16, kMoeMaxExperts = 512;
 // Longest dot product whose 8-bit products cannot overflow a 32-bit sum.
 constexpr int64_t kQ8MaxK = 131071;
 
+// Groups of `per` among n > 0 rows, and whether the 32 rows from `first` are all below
+// n, for every n an int holds.
+constexpr int groups_of(int n, int per) { return (n - 1) / per + 1; }
+constexpr bool all_32_below(int first, int n) { return first <= n - 32; }
+static_assert(groups_of(1, 64) == 1 && groups_of(64, 64) == 1 && groups_of(65, 64) == 2, "groups");
+static_assert(groups_of(INT32_MAX, 16) == 1 << 27 && groups_of(INT32_MAX, 64) == 1 << 25, "groups of the most rows");
+static_assert(all_32_below(0, 32) && !all_32_below(0, 31) && !all_32_below(INT32_MAX - 31, INT32_MAX) &&
+              all_32_below(INT32_MAX - 63, INT32_MAX), "32 rows at the end of the most");
+
 #ifdef __CUDACC__
 
 template <typename T>

@@ -383,7 +383,7 @@ q8_mma_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ C
                 default: finish([](float v) { return v; });
             }
             OutT *o = out + (int64_t)m0 * ldc + n;
-            if (n - lane + 32 <= N && m0 + at(COLS - 1) < M) {
+            if (all_32_below(n - lane, N) && m0 + at(COLS - 1) < M) {
 #pragma unroll
                 for (int j = 0; j < COLS; ++j) {
                     *o = from_f32<OutT>(acc[j]);

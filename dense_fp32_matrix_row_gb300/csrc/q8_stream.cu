@@ -114,7 +114,7 @@ q8_ring_kernel(int M, int N, int K, const int8_t *__restrict__ X,
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int blocks = K / kQ8Step;                       // whole steps; the rest is read directly
     const int stages = (blocks + KB - 1) / KB;            // per tile
-    const int tiles = (N + ROWS - 1) / ROWS;
+    const int tiles = groups_of(N, ROWS);
     const int m0 = (int)blockIdx.y * TOK;
 
     if (threadIdx.x == 0) {
