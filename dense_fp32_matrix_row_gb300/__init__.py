@@ -14,6 +14,7 @@ import ctypes
 import os
 
 from .build import LIBRARY, build  # noqa: F401  (build is part of the public API)
+from .q8 import linear_q8, moe_q8, quantize_q8, rmsnorm_q8
 
 __all__ = ["sgemm", "sgemm_host", "host_set_panels", "host_panel_rows", "sgemm_3xtf32", "sgemm_tf32", "sgemm_bf16", "sgemm_ptr", "status", "select_kernel",
            "force_kernel", "ffma_configs", "ffma_config_for", "ffma_force_config", "ffma_force_tail_sum", "ffma_tail_plan", "kernel_timing", "kernel_timing_result", "set_wait_limit", "selftest_wait", "release_workspaces", "status_string",
@@ -341,14 +342,3 @@ def release_workspaces() -> int:
 
 def selftest_wait(ns: int, stream=None) -> int:
     return int(lib().sgemm_selftest_wait(int(ns), _stream_handle(stream)))
-
-
-# The 8-bit operators take torch tensors only; torch is imported on first use,
-# as everywhere in this module.
-def __getattr__(name):
-    if name in ("quantize_q8", "rmsnorm_q8", "linear_q8", "moe_q8"):
-        from . import q8
-        fn = getattr(q8, name)
-        globals()[name] = fn
-        return fn
-    raise AttributeError(f"module {__name__!r} has no attribute {name!r}")

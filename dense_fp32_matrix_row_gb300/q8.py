@@ -11,11 +11,8 @@ from __future__ import annotations
 
 import ctypes
 
-import torch
-
 _i64, _vp, _int, _f32 = ctypes.c_int64, ctypes.c_void_p, ctypes.c_int, ctypes.c_float
 TYPE_FP32, TYPE_BF16 = 0, 1
-_TYPES = {torch.float32: TYPE_FP32, torch.bfloat16: TYPE_BF16}
 ACTIVATIONS = {"none": 0, "relu": 1, "gelu": 2, "silu": 3}
 
 _SIGNATURES = {
@@ -53,10 +50,20 @@ def _launch(index, name, *args):
         raise SgemmError(rc, name)
 
 
-# torch's own accessors behind torch.cuda.current_stream and current_device,
-# without the objects those make (2 us a call); the public ones otherwise
-_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
-_current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+torch = None    # imported by the first call: the package can be imported without it
+
+
+def _load():
+    global torch, _TYPES, _FLOATS, _INT8, _raw_stream, _current_device
+    import torch as t
+    _TYPES = {t.float32: TYPE_FP32, t.bfloat16: TYPE_BF16}
+    _FLOATS = (t.float32, t.bfloat16)
+    _INT8 = (t.int8,)
+    # torch's own accessors behind torch.cuda.current_stream and current_device,
+    # without the objects those make (2 us a call); the public ones otherwise
+    _raw_stream = getattr(t._C, "_cuda_getCurrentRawStream", None)
+    _current_device = getattr(t._C, "_cuda_getDevice", None) or t.cuda.current_device
+    torch = t      # last: the sign that the rest is there
 
 
 def _stream(stream, index):
@@ -119,14 +126,12 @@ def _index(t, name):
     return t.get_device()
 
 
-_FLOATS = (torch.float32, torch.bfloat16)
-_INT8 = (torch.int8,)
-
-
 def quantize_q8(x, q, scale, stream=None) -> None:
     """Each row of ``x`` (M, K; float32 or bfloat16) as 8-bit whole numbers
     ``q`` (M, K; int8) and one ``scale`` (M; float32): x is about q * scale,
     scale = max|row| / 127.  Rows of ``x`` and ``q`` may be strided."""
+    if torch is None:
+        _load()
     dev, shape = _index(q, "q"), _shape2(x, "x")
     M, K = shape
     ldx = _matrix(x, "x", _FLOATS, shape, dev)
@@ -144,6 +149,8 @@ def rmsnorm_q8(x, weight, q, scale, residual=None, h=None, y=None, eps: float = 
     ``x``, ``residual``, ``h`` and ``y`` are (M, K) of one type (float32 or
     bfloat16), ``weight`` K float32 values.  ``residual``, ``h`` and ``y`` may
     be left out; ``h`` may be ``x`` or ``residual`` itself."""
+    if torch is None:
+        _load()
     dev, shape = _index(q, "q"), _shape2(x, "x")
     M, K = shape
     ldx = _matrix(x, "x", _FLOATS, shape, dev)
@@ -170,6 +177,8 @@ def linear_q8(xq, xs, wq, ws, out, bias=None, activation: str = "none", stream=N
     ``xq`` (M, K) and ``wq`` (N, K) are int8 with the float32 scales ``xs``
     (M) and ``ws`` (N); ``out`` (M, N) is float32 or bfloat16; ``bias`` is N
     float32 values or None; ``activation`` is a key of ``ACTIVATIONS``."""
+    if torch is None:
+        _load()
     act = ACTIVATIONS.get(activation)
     if act is None:
         raise ValueError(f"unknown activation {activation!r}; one of {sorted(ACTIVATIONS)}")
@@ -201,6 +210,8 @@ def moe_q8(x, router, w_up, s_up, w_down, s_down, out, top_k: int, renormalize: 
     out[t] = sum over the top_k experts of gate * down(silu(gate) * up), with
     the token and the hidden row in 8 bits.  ``ids`` (T, top_k; int32) and
     ``gates`` (T, top_k; float32) take the routing if given."""
+    if torch is None:
+        _load()
     dev, shape, rshape = _index(out, "out"), _shape2(x, "x"), _shape2(router, "router")
     T, H = shape
     E = rshape[0]
