@@ -19,7 +19,7 @@ sys.meta_path.insert(0, NoTorch())
 from dense_fp32_matrix_row_gb300 import *
 import dense_fp32_matrix_row_gb300 as sg
 sg.build()
-assert version() > 0 and select_kernel(64, 64, 64) > 0
+assert version() > 0 and select_kernel(64, 64, 64, A=1 << 30, B=2 << 30, C=3 << 30) > 0
 for name in sg.__all__:
     assert callable(globals()[name]), name
 for call in (lambda: quantize_q8(None, None, None), lambda: linear_q8(None, None, None, None, None)):
