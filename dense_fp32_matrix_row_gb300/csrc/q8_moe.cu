@@ -310,7 +310,7 @@ __device__ void moe_route(MoeShared &S, int ntok, int E, int top_k, int renorm, 
 }
 
 // One block's sums for 16-row tiles `tile` of a weight matrix into S.part.
-template <int NB, bool VEC, bool COHERENT>
+template <int NB>
 __device__ __forceinline__ void moe_dot(MoeBlock &S, const int8_t *wa, const int8_t *wb, const int8_t *xbase,
                                         const int (&xrow)[2], int64_t xld, int K, int kw, const int8_t *wbegin,
                                         const int8_t *wend, const int8_t *xend) {
@@ -327,7 +327,7 @@ __device__ __forceinline__ void moe_dot(MoeBlock &S, const int8_t *wa, const int
     const int steps = (K + kQ8Step - 1) / kQ8Step;
     const int per = (steps + kw - 1) / kw;
     const int s0 = min(kpart * per, steps), s1 = min(s0 + per, steps);
-    q8_dot<NB, VEC, 4, COHERENT>(sum, wa, wb, x, K, s0, s1, wbegin, wend, xbase, xend);
+    q8_dot<NB, 4, true>(sum, wa, wb, x, K, s0, s1, wbegin, wend, xbase, xend);
 #pragma unroll
     for (int n = 0; n < NB; ++n) {
         S.part[warp][g][8 * n + 2 * t] = sum[n][0];
@@ -391,8 +391,8 @@ q8_expert_kernel(int ntok, int E, int top_k, int H, int I, int renorm, const int
             const int8_t *wb = wa + (int64_t)I * ldu;
             const int xrow[2] = {pa / top_k, pb / top_k};
             const int8_t *xend = xq + (int64_t)ntok * L.Hp;
-            if (n <= 8) moe_dot<1, false, true>(S, wa, wb, xq, xrow, L.Hp, H, kw_up, w_up, up_end, xend);
-            else moe_dot<2, false, true>(S, wa, wb, xq, xrow, L.Hp, H, kw_up, w_up, up_end, xend);
+            if (n <= 8) moe_dot<1>(S, wa, wb, xq, xrow, L.Hp, H, kw_up, w_up, up_end, xend);
+            else moe_dot<2>(S, wa, wb, xq, xrow, L.Hp, H, kw_up, w_up, up_end, xend);
             __syncthreads();
             const int tok = n <= 8 ? 8 : 16;
             for (int o = tid; o < 8 * rt_up * tok; o += MTHREADS) {   // whole warps: 8 * tok * rt_up is a multiple of 32
@@ -454,8 +454,8 @@ q8_expert_kernel(int ntok, int E, int top_k, int H, int I, int renorm, const int
             const int8_t *wb = w_down + ((int64_t)e * H + min(n0 + g + 8, H - 1)) * ldd;
             const int xrow[2] = {pa, pb};
             const int8_t *xend = hq + (int64_t)L.P * L.Ip;
-            if (n <= 8) moe_dot<1, false, true>(S, wa, wb, hq, xrow, L.Ip, I, kw_down, w_down, down_end, xend);
-            else moe_dot<2, false, true>(S, wa, wb, hq, xrow, L.Ip, I, kw_down, w_down, down_end, xend);
+            if (n <= 8) moe_dot<1>(S, wa, wb, hq, xrow, L.Ip, I, kw_down, w_down, down_end, xend);
+            else moe_dot<2>(S, wa, wb, hq, xrow, L.Ip, I, kw_down, w_down, down_end, xend);
             __syncthreads();
             for (int o = tid; o < 16 * rt_down * n; o += MTHREADS) {
                 const int r = o & 15, tl = (o >> 4) % rt_down, j = (o >> 4) / rt_down;

@@ -23,7 +23,7 @@ namespace {
 
 constexpr int SWARPS = 8;
 
-template <int NB, bool VEC, typename OutT>
+template <int NB, typename OutT>
 __global__ void __launch_bounds__(SWARPS * 32)
 q8_stream_kernel(int M, int N, int K, const int8_t *__restrict__ X, int64_t ldx,
                  const float *__restrict__ xs, const int8_t *__restrict__ W, int64_t ldw,
@@ -53,7 +53,7 @@ q8_stream_kernel(int M, int N, int K, const int8_t *__restrict__ X, int64_t ldx,
             const int steps = (K + kQ8Step - 1) / kQ8Step;
             const int per = (steps + kw - 1) / kw;
             const int s0 = min(kpart * per, steps), s1 = min(s0 + per, steps);
-            q8_dot<NB, VEC, 4>(sum, W + (int64_t)ra * ldw, W + (int64_t)rb * ldw, x, K, s0, s1, W,
+            q8_dot<NB, 4>(sum, W + (int64_t)ra * ldw, W + (int64_t)rb * ldw, x, K, s0, s1, W,
                                W + (int64_t)(N - 1) * ldw + K, X, X + (int64_t)(M - 1) * ldx + K);
         }
 #pragma unroll
@@ -331,7 +331,7 @@ q8_ring_kernel(int M, int N, int K, const int8_t *__restrict__ X,
     }
 }
 
-template <int NB, bool VEC, typename OutT>
+template <int NB, typename OutT>
 cudaError_t launch_s(const Q8LinearArgs &a) {
     const int64_t steps = (a.K + kQ8Step - 1) / kQ8Step;
     int kw = 1;
@@ -348,7 +348,7 @@ cudaError_t launch_s(const Q8LinearArgs &a) {
     cfg.attrs = attr;
     cfg.numAttrs = 1;
     const Epilogue ep{1.0f, 0.0f, a.bias, a.act};
-    return cudaLaunchKernelEx(&cfg, q8_stream_kernel<NB, VEC, OutT>, (int)a.M, (int)a.N, (int)a.K, a.X,
+    return cudaLaunchKernelEx(&cfg, q8_stream_kernel<NB, OutT>, (int)a.M, (int)a.N, (int)a.K, a.X,
                               a.ldx, a.xs, a.W, a.ldw, a.ws, ep, (OutT *)a.C, a.ldc, kw);
 }
 
@@ -392,10 +392,8 @@ cudaError_t launch_r(const Q8LinearArgs &a) {
 template <typename OutT>
 cudaError_t launch_o(const Q8LinearArgs &a) {
     const bool wvec = reinterpret_cast<uintptr_t>(a.W) % 16 == 0 && a.ldw % 16 == 0;
-    const bool vec = wvec && reinterpret_cast<uintptr_t>(a.X) % 16 == 0 && a.ldx % 16 == 0;
     if (wvec && a.K >= kQ8Step && (a.M + 7) / 8 <= 65535) return launch_r<OutT>(a);
-    if (a.M <= 8) return vec ? launch_s<1, true, OutT>(a) : launch_s<1, false, OutT>(a);
-    return vec ? launch_s<2, true, OutT>(a) : launch_s<2, false, OutT>(a);
+    return a.M <= 8 ? launch_s<1, OutT>(a) : launch_s<2, OutT>(a);
 }
 
 }  // namespace

@@ -23,14 +23,6 @@ constexpr int kQ8Step = 64;          // k per step
 
 constexpr int kQ8ExactSteps = 16;    // steps per exact FP32 chunk (1024 k)
 
-__device__ __forceinline__ uint4 ldg_stream_u4(const void *p) {
-    uint4 v;
-    asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
-                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-                 : "l"(p));
-    return v;
-}
-
 // Up to 16 bytes from p, byte by byte; bytes at and past `valid` are 0.
 __device__ __forceinline__ uint4 load16_bytes(const int8_t *p, int valid) {
     uint32_t w[4] = {0u, 0u, 0u, 0u};
@@ -115,15 +107,15 @@ __device__ __forceinline__ void q8_flush(int (&sum)[NB][4], float (&acc)[NB][4])
 }
 
 // Adds into `sum` the dot products over steps [s0, s1) of a row of K values.
-//   wa, wb     this lane's two weight rows (g and g + 8 of the 16), at k = 0
-//   x[n]       this lane's token row of block n (token 8n + g), at k = 0
-//   VEC        all those rows are 16-byte aligned; otherwise wbegin/wend and
-//              xbegin/xend bound the two arrays
-//   COHERENT   the token rows were written by other blocks of this kernel (VEC
-//              only): they are read from L2, and are padded with zeros to whole
-//              steps
+//   wa, wb     this lane's two weight rows (g and g + 8 of the 16), at k = 0, of
+//              any alignment; wbegin/wend bound their array
+//   x[n]       this lane's token row of block n (token 8n + g), at k = 0, of any
+//              alignment; xbegin/xend bound their array
+//   COHERENT   the token rows were written by other blocks of this kernel: they
+//              are read from L2, are 16-byte aligned and padded with zeros to
+//              whole steps (xbegin/xend unused)
 // sum[n][0..3]: rows g, g, g+8, g+8 and tokens 8n + 2t, +1, 2t, +1.
-template <int NB, bool VEC, int U, bool COHERENT = false>
+template <int NB, int U, bool COHERENT = false>
 __device__ __forceinline__ void q8_dot(int (&sum)[NB][4], const int8_t *wa, const int8_t *wb,
                                        const int8_t *const (&x)[NB], int64_t K, int s0, int s1,
                                        const int8_t *wbegin, const int8_t *wend,
@@ -138,12 +130,12 @@ __device__ __forceinline__ void q8_dot(int (&sum)[NB][4], const int8_t *wa, cons
         for (int i = 0; i < 4; ++i) acc[n][i] = 0.0f;
     auto wload = [&](const int8_t *row, int s) {
         const int8_t *p = row + (int64_t)s * kQ8Step + 16 * t;
-        return VEC ? ldg_stream_u4(p) : load16_unaligned(p, wbegin, wend);
+        return load16_unaligned(p, wbegin, wend);
     };
     auto xload = [&](const int8_t *row, int s) {
         const int8_t *p = row + (int64_t)s * kQ8Step + 16 * t;
         if (COHERENT) return __ldcg(reinterpret_cast<const uint4 *>(p));
-        return VEC ? __ldg(reinterpret_cast<const uint4 *>(p)) : load16_unaligned(p, xbegin, xend);
+        return load16_unaligned(p, xbegin, xend);
     };
     int s = s0, since = 0;
     static_assert(kQ8ExactSteps % U == 0, "an exact chunk is whole unrolled rounds");
