@@ -9,8 +9,8 @@
 //   hid    = g / (1 + exp(-g)) * u,   hq, hs = 8-bit rows of hid
 //   out[t] = sum_j gate_j * hs * s_down[e_j][.] * (hq . w_down[e_j][.])
 //
-// Bound by memory: the picked experts' weights, read once each (a block of up
-// to 16 of an expert's tokens shares the read).
+// Bound by memory: the picked experts' weights, read once for each 16 of an
+// expert's tokens.
 //
 // The first kernel computes the logits and quantises the tokens.  The second
 // is persistent: blocks draw work units from one counter, all gate/up units
@@ -25,7 +25,8 @@
 //
 // Measured (bf16): one token, 2 of 8 experts of 4096 x 14336, 353 MB, 72 us, 4.9
 // TB/s; 16 tokens, 6 of 64 experts of 2048 x 1408, 440 MB, 115 us, 3.8 TB/s; 5 FP32
-// tokens, 4 of 16 experts of 1024 x 1000, 38 MB, 40 us.  What is above memory's time
+// tokens, 4 of 16 experts of 1024 x 1000, 38 MB, 40 us; 64 tokens over the 64 experts
+// 187 us.  (With weights at an odd address, q8_expert_kernel: 174, 280, 41 and 396 us.)  What is above memory's time
 // is a chain of hand-overs that each take 1 to 4 us (logits, routing, the first
 // weights, hidden rows, 8 bits, results, sums): 17 us for a layer without work.  A
 // finisher's unit takes 7000 cycles, half of them the fence before its counter;

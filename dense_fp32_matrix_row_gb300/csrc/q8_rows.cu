@@ -18,10 +18,12 @@
 //                  block barriers (at 128 vectors both take 20 us for 16384 rows);
 //   q8_rows, q8_plain  longer rows, few rows, any alignment: a block a row, all its
 //                  loads issued at once (q8_plain without norm and residual);
-//   q8_rows_long   rows beyond registers: read twice.
+//   q8_rows_long   rows beyond registers (16384, or 8192 without vector access): read
+//                  twice, an element at a time.
 // Measured (bf16): 8192 x 4096 with residual, h and y, 302 MB, 46.9 us, 6.4 TB/s,
 // memory; 2048 x 14336 alone, 88 MB, 15.0 us, 5.9 TB/s, the same; one row of 4096
-// 2.3 us, the launch.
+// 2.3 us, the launch.  Not taken further: 2048 x 28672, 176 MB, 118 us alone and 126 with
+// a norm (1.4 TB/s, q8_rows_long); 2048 x 8191 22 and 61 us (an element an access).
 // Measured and not kept for long rows (8192 x 4096, 4096 x 8192 in FP32, 2048 x
 // 16384, with residual: 39, 70 and 45 us with a block a row): persistent blocks
 // that prefetch the next row into registers 46, 89 and 44 us, into shared memory

@@ -290,11 +290,16 @@ int sgemm_q8_rmsnorm(int64_t M, int64_t K, const void *x, int64_t ldx, const voi
  *   C           M x N of type `type`
  * The whole-number sums are exact while every partial sum stays within 2^24
  * in magnitude (always up to K = 1024, and for ordinary data far beyond), and
- * rounded to FP32 from there.  K <= 131071 (SGEMM_ERR_BAD_DIM).  K == 0 gives
- * act(bias).
- * Past 16 tokens it uses the stream's workspace (X in 16 bits; W once more when
- * its rows are not 16-byte aligned; partial sums when K is divided), grown like
- * sgemm()'s; the same rule for stream capture holds.  Its kernels' waits on
+ * rounded to FP32 from there (up to 16 tokens they are 32-bit integers,
+ * rounded once).  K <= 131071 (SGEMM_ERR_BAD_DIM).  K == 0 gives act(bias).
+ * Up to 16 tokens, and for small products, W is streamed; the rest runs on the
+ * tensor cores' tiles.  Last bits differ between the two: the tiles take SiLU
+ * and GELU with a quotient good to 2 units in the last place (0 for results below
+ * 1e-36) and, for a BF16 result, an exponential good to 1e-5; streaming uses
+ * CUDA's expf and tanhf and the exact quotient.
+ * The tiles use the stream's workspace (X in 16 bits; W once more when its rows
+ * are not 16-byte aligned; partial sums when K is divided), grown like
+ * sgemm()'s; the same rule for stream capture holds.  The kernels' waits on
  * their own copies are bounded (see sgemm_status).
  */
 int sgemm_q8_linear(int64_t M, int64_t N, int64_t K, const int8_t *X, int64_t ldx, const float *xs,
