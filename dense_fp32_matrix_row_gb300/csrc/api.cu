@@ -12,6 +12,7 @@
 
 #include "common.cuh"
 #include "sgemm_gb300.h"
+#include "workspace.cuh"
 
 using namespace sgemm_gb300;
 

@@ -7,9 +7,6 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
-#include <atomic>
-#include <mutex>
-
 namespace sgemm_gb300 {
 
 // Bit set in the per-device error word when a bounded wait runs out.
@@ -128,63 +125,20 @@ bool release_host_paths();
 // Fills g.err, g.wait_ns, g.sm_count and g.encode for the current device
 // (setting the device up on first use); returns an SGEMM_* status.
 int fill_device_args(GemmArgs &g);
-// What the buffers of a stream are kept under: device, handle and, for
-// cudaStreamPerThread, which names another stream in each host thread, the
-// thread (0 otherwise; a thread's number is never given again).
-struct StreamKey {
-    int dev;
-    uintptr_t stream;
-    uint64_t thread;
-    StreamKey(int d, cudaStream_t s) : dev(d), stream(reinterpret_cast<uintptr_t>(s)), thread(thread_of(s)) {}
-    bool operator<(const StreamKey &o) const {
-        return dev != o.dev ? dev < o.dev : stream != o.stream ? stream < o.stream : thread < o.thread;
-    }
-    // Waits for the stream's work, from any thread (the device current).
-    cudaError_t synchronize() const {
-        return thread != 0 ? cudaDeviceSynchronize() : cudaStreamSynchronize(reinterpret_cast<cudaStream_t>(stream));
-    }
-
-private:
-    static uint64_t thread_of(cudaStream_t s) {
-        if (s != cudaStreamPerThread) return 0;
-        static std::atomic<uint64_t> threads{0};
-        thread_local const uint64_t mine = ++threads;
-        return mine;
-    }
-};
-// The workspace of (current device, s), at least `bytes` large and 256-byte
-// aligned, for one call: it stays that call's until the lease goes, which has to be
-// after the last launch that uses it.  Launches of another host thread's call on
-// the stream would otherwise come between this call's.
-struct WorkspaceLease {
-    std::unique_lock<std::mutex> lock;
-    void *p = nullptr;
-};
-// Returns an SGEMM_* status.
-int stream_workspace(size_t bytes, cudaStream_t s, WorkspaceLease &out);
 
 
 #ifdef __CUDACC__
 
-// The epilogue's activations.  GELU is the tanh form
-// x/2 * (1 + tanh(sqrt(2/pi) * (x + 0.044715 x^3))), SiLU is x / (1 + e^-x);
-// CUDA's tanhf and expf.  ReLU keeps NaN.
-template <int ACT>
-__device__ __forceinline__ float activate(float v) {
-    if constexpr (ACT == kActRelu) return v < 0.0f ? 0.0f : v;
-    else if constexpr (ACT == kActGelu)
-        return 0.5f * v * (1.0f + tanhf(0.7978845608028654f * fmaf(0.044715f * v, v * v, v)));
-    else if constexpr (ACT == kActSilu) return v / (1.0f + expf(-v));
-    else return v;
-}
-
 // act(v + bias[col]): the part of the epilogue after alpha*acc + beta*C.
+// GELU is the tanh form x/2 * (1 + tanh(sqrt(2/pi) * (x + 0.044715 x^3))),
+// SiLU is x / (1 + e^-x); CUDA's tanhf and expf.  ReLU keeps NaN.
 __device__ __forceinline__ float epilogue_tail(const Epilogue &e, float v, int64_t col) {
     if (e.bias != nullptr) v += __ldg(e.bias + col);
     switch (e.act) {
-        case kActRelu: return activate<kActRelu>(v);
-        case kActGelu: return activate<kActGelu>(v);
-        case kActSilu: return activate<kActSilu>(v);
+        case kActRelu: return v < 0.0f ? 0.0f : v;
+        case kActGelu:
+            return 0.5f * v * (1.0f + tanhf(0.7978845608028654f * fmaf(0.044715f * v, v * v, v)));
+        case kActSilu: return v / (1.0f + expf(-v));
         default: return v;
     }
 }

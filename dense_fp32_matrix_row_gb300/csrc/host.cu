@@ -21,6 +21,7 @@
 
 #include "common.cuh"
 #include "sgemm_gb300.h"
+#include "workspace.cuh"
 
 using namespace sgemm_gb300;
 

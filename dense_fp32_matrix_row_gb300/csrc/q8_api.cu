@@ -4,6 +4,7 @@
 
 #include "q8.cuh"
 #include "sgemm_gb300.h"
+#include "workspace.cuh"
 
 using namespace sgemm_gb300;
 

@@ -212,7 +212,7 @@ __device__ __forceinline__ float finish_value(float v) {
         const float x = ACT == kActSilu ? -v : -1.5957691216057308f * fmaf(0.044715f * v, v * v, v);
         return __fdividef(v, 1.0f + (sizeof(OutT) == 2 ? __expf(x) : expf(x)));
     } else {
-        return activate<ACT>(v);
+        return ACT == kActRelu && v < 0.0f ? 0.0f : v;     // ReLU keeps NaN
     }
 }
 
