@@ -167,7 +167,7 @@ __device__ __forceinline__ void finish_row(const Rows<T> &a, int64_t row, int fi
                 }
             uint32_t none = 0;
             reduce(none, s2);
-            r = inv_rms(s2, a.K, lift > 1.0f ? a.eps * lift * lift : 0.0f);
+            r = inv_rms(s2, a.K, a.eps * lift * lift);
         }
     }
     if (first == 0) a.scale[row] = row_scale(rq, lift, r);
@@ -292,7 +292,7 @@ q8_rows_long_kernel(int64_t K, const T *x, int64_t ldx, const T *residual, int64
             }
             uint32_t none = 0;
             block_max_sum(none, s2, red);
-            r = inv_rms(s2, K, lift > 1.0f ? eps * lift * lift : 0.0f);
+            r = inv_rms(s2, K, eps * lift * lift);
         }
     }
     if (threadIdx.x == 0) scale[row] = row_scale(rq, lift, r);

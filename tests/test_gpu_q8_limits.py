@@ -1,5 +1,6 @@
 """The 8-bit operators at the ends of their ranges."""
 
+import numpy as np
 import pytest
 
 pytestmark = pytest.mark.gpu
@@ -9,6 +10,7 @@ if not torch.cuda.is_available():
     pytest.skip("no CUDA device", allow_module_level=True)
 
 import dense_fp32_matrix_row_gb300 as sg  # noqa: E402
+from test_gpu_q8 import run_rows  # noqa: E402
 
 
 @pytest.fixture(scope="module", autouse=True)
@@ -107,3 +109,16 @@ def test_sums_of_other_blocks_are_complete_every_time(make):
         wrong += (out != want).sum()
     assert sg.status() == sg.OK
     assert int(wrong) == 0
+
+
+# ---- rows ------------------------------------------------------------------
+
+@pytest.mark.parametrize("K", [96, 515, 4096, 17000])
+def test_norm_of_the_largest_rows_keeps_eps(K):
+    """Squares that overflow FP32 are summed of scaled values; an eps of their size
+    counts all the same."""
+    rng = np.random.default_rng(K)
+    x = (1e19 * rng.uniform(0.5, 1.5, (5, K))).astype(np.float32)
+    w = np.ones(K, dtype=np.float32)
+    for eps in (1e38, 3e37, 1e-6):
+        run_rows(x, None, w, eps=eps, with_y=True)
