@@ -71,7 +71,7 @@ q8_stream_kernel(int M, int N, int K, const int8_t *__restrict__ X, int64_t ldx,
             if (n >= N || m >= M) continue;
             int s = 0;
             for (int w = 0; w < kw; ++w) s += part[tl * kw + w][row][tok];
-            const float v = (float)s * xs[m] * ws[n];
+            const float v = K > 0 ? (float)s * xs[m] * ws[n] : 0.0f;
             C[(int64_t)m * ldc + n] = from_f32<OutT>(epilogue_tail(ep, v, n));
         }
         __syncthreads();   // `part` is written again

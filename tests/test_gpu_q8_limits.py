@@ -122,3 +122,16 @@ def test_norm_of_the_largest_rows_keeps_eps(K):
     w = np.ones(K, dtype=np.float32)
     for eps in (1e38, 3e37, 1e-6):
         run_rows(x, None, w, eps=eps, with_y=True)
+
+
+@pytest.mark.parametrize("M", [2, 40])
+def test_linear_without_terms_reads_no_scale(M):
+    """K == 0 gives act(bias), whatever the scales hold."""
+    nan = lambda n: torch.full((n,), float("nan"), device="cuda")  # noqa: E731
+    b = torch.tensor([-1.0, 2.0, 0.5], device="cuda")
+    out = torch.full((M, 3), 9.0, device="cuda")
+    for bias, want in ((b, torch.relu(b)), (None, torch.zeros(3, device="cuda"))):
+        sg.linear_q8(torch.empty((M, 0), dtype=torch.int8, device="cuda"), nan(M),
+                     torch.empty((3, 0), dtype=torch.int8, device="cuda"), nan(3), out, bias=bias, activation="relu")
+        assert sg.status() == sg.OK
+        assert torch.equal(out, want.expand(M, 3))
