@@ -74,9 +74,10 @@ constexpr int kMoeMaxTokens = 64, kMoeMaxTopK = 16, kMoeMaxExperts = 512;
 // Longest dot product whose 8-bit products cannot overflow a 32-bit sum.
 constexpr int64_t kQ8MaxK = 131071;
 
-// Groups of `per` among n > 0 rows, and whether the 32 rows from `first` are all below
+// Groups of `per` among n > 0 rows (as (n - 1) / per + 1, the ring kernel for 16 tokens
+// compiled to 18.0 us instead of 17.8), and whether the 32 rows from `first` are all below
 // n, for every n an int holds.
-constexpr int groups_of(int n, int per) { return (n - 1) / per + 1; }
+constexpr int groups_of(int n, int per) { return (int)(((unsigned)n + (unsigned)per - 1u) / (unsigned)per); }
 constexpr bool all_32_below(int first, int n) { return first <= n - 32; }
 static_assert(groups_of(1, 64) == 1 && groups_of(64, 64) == 1 && groups_of(65, 64) == 2, "groups");
 static_assert(groups_of(INT32_MAX, 16) == 1 << 27 && groups_of(INT32_MAX, 64) == 1 << 25, "groups of the most rows");

@@ -162,8 +162,7 @@ __device__ __forceinline__ void arrive_relaxed(uint32_t bar, uint32_t cta) {
                  : "memory");
 }
 
-// Adds to a word in shared memory of CTA `cta` of the cluster.  (With a plain store to
-// the other SM, the 256-token kernel spills 70 registers, with this one 2.)
+// Adds to a word in shared memory of CTA `cta` of the cluster.
 __device__ __forceinline__ void add_cta(uint32_t addr, uint32_t cta, uint32_t v) {
     asm volatile("red.relaxed.cluster.shared::cluster.add.u32 [%0], %1;" ::"r"(cluster_addr(addr, cta)), "r"(v)
                  : "memory");
@@ -236,11 +235,11 @@ q8_mma_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ C
     uint64_t *dfull = empty + ST;       // [2] accumulator holds a finished chunk
     uint64_t *dempty = dfull + 2;       // [2] accumulator has been read
     uint64_t *drainbar = dempty + 2;
-    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(drainbar + 1);
-    // For a pair that gives up (at fixed addresses, which take no registers beside the
-    // epilogue's sums): whether a role of either SM did, the stages of X that each SM issued
-    // (on the even SM), and where xfull is.
-    __shared__ uint32_t gave_up, xcount[2], xfull_at;
+    uint64_t *xdone = drainbar + 1;     // even SM of a pair: the odd one has issued its last X
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(xdone + 1);
+    // Even SM of a pair: stages of X the odd one issued.  (In the dynamic array, as the words
+    // above, it made the 256-token kernel spill 70 registers instead of 2.)
+    __shared__ uint32_t odd_stages;
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     uint32_t rank = 0;
@@ -265,9 +264,9 @@ q8_mma_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ C
             mbar_init(smem_u32(&dempty[b]), C::R * EPI_WARPS / (C::HALVES ? 2 : 1));
         }
         mbar_init(smem_u32(drainbar), 1);
+        mbar_init(smem_u32(xdone), 1);
         mbar_fence_init();
-        gave_up = xcount[0] = xcount[1] = 0u;
-        xfull_at = smem_u32(xfull);
+        odd_stages = 0u;
     }
     if (warp == 0) {
         __syncwarp();
@@ -286,11 +285,6 @@ q8_mma_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ C
     if constexpr (PAIR) cluster_sync_all();
     tc_fence_after();
     const uint32_t tmem = *reinterpret_cast<volatile uint32_t *>(tmem_slot);
-    auto fail = [err] {    // one lane of a role that gave up
-        record_error(err, kErrWaitTimeout);
-        if constexpr (PAIR)
-            for (uint32_t cta = 0; cta < 2; ++cta) add_cta(smem_u32(&gave_up), cta, 1u);
-    };
 
     if (warp < EPI_WARPS) {
         // Epilogue warp w: tensor-memory lanes 32 * (w % 4) .. + 31 (a W row
@@ -395,7 +389,7 @@ q8_mma_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ C
                     if (n < N && m0 + at(j) < M) o[(int64_t)at(j) * ldc] = from_f32<OutT>(acc[j]);
             }
         }
-        if (!ok && lane == 0) fail();
+        if (!ok && lane == 0) record_error(err, kErrWaitTimeout);
     } else if (warp < W_WARP) {
         // Converter warp w: W rows (tensor-memory lanes) 32 * (w % 4) .. + 31 of
         // the stages of parity (w / 4) % 2.
@@ -454,7 +448,7 @@ q8_mma_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ C
                 else mbar_arrive(smem_u32(&afull[s]));
             }
         }
-        if (!ok && lane == 0) fail();
+        if (!ok && lane == 0) record_error(err, kErrWaitTimeout);
     } else {
         set_registers<OTHER_REGS, false>();
         if (warp == W_WARP || warp == X_WARP) {
@@ -497,14 +491,32 @@ q8_mma_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ C
                     __syncwarp();
                 }
             }
+            // The copies have to land before the block ends, whichever role gave up; with no
+            // time-out the MMAs have waited, or are about to wait, for all of them.
             if (lane == 0) {
-                if (!ok) fail();
-                if (PAIR && !is_w) {      // a pair's X completes on the even SM: see the end
-                    add_cta(smem_u32(&xcount[rank]), 0, g);
-                } else {
-                    for (uint32_t q = g > (uint32_t)depth ? g - (uint32_t)depth : 0; q < g; ++q)
-                        mbar_wait(smem_u32(&(is_w ? wfull : xfull)[q % (uint32_t)depth]), (q / (uint32_t)depth) & 1,
-                                  DRAIN_NS);
+                if (!ok) record_error(err, kErrWaitTimeout);
+                uint32_t other = g;     // stages of X that the other SM of a pair issued
+                bool told = true;
+                if (PAIR && !is_w) {
+                    if (lead) {
+                        told = mbar_wait_cluster(smem_u32(xdone), 0, wait_ns + DRAIN_NS);
+                        other = *const_cast<volatile uint32_t *>(&odd_stages);
+                    } else {
+                        add_cta(smem_u32(&odd_stages), 0, g);
+                        mbar_arrive_cta(smem_u32(xdone), 0);
+                    }
+                }
+                if (is_w || lead) {
+                    // Both SMs' X completes on the even SM's barriers.  What one SM issued and
+                    // the other did not is made up for.  (A stage is issued after the MMAs of
+                    // the stage `depth` before it: only the last `depth` can be open.)
+                    const uint32_t most = told && other > g ? other : g;
+                    for (uint32_t q = most > (uint32_t)depth ? most - (uint32_t)depth : 0; q < most; ++q) {
+                        const uint32_t bar = smem_u32(&(is_w ? wfull : xfull)[q % (uint32_t)depth]);
+                        if (told && q >= g) mbar_arrive_expect_tx(bar, C::X_STAGE);
+                        else if (told && q >= other) mbar_complete_tx(bar, C::X_STAGE);
+                        mbar_wait(bar, (q / (uint32_t)depth) & 1, DRAIN_NS);
+                    }
                 }
             }
         } else if (warp == MMA_WARP && lead) {
@@ -588,7 +600,7 @@ q8_mma_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ C
                     }
                 }
             }
-            if (!ok && lane == 0) fail();
+            if (!ok && lane == 0) record_error(err, kErrWaitTimeout);
             if (issued) {     // the epilogue may have given up on the last chunks
                 if (elect_one()) {
                     if constexpr (PAIR)
@@ -606,28 +618,7 @@ q8_mma_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ C
 
     tc_fence_before();
     __syncthreads();
-    if constexpr (PAIR) {
-        cluster_sync_all();
-        if (*const_cast<volatile uint32_t *>(&gave_up) != 0u) {    // as in the other SM: both were told
-            // Both SMs' stages of X complete on the even SM's barriers, and one may have
-            // issued more than the other.  Its barriers get what is missing, then are waited
-            // for: a stage is issued after the MMAs of the stage ST before it, so that only the
-            // last ST can be open.
-            uint32_t cta;
-            asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(cta));
-            if (cta == 0 && threadIdx.x == X_WARP * 32) {
-                const uint32_t own = xcount[0], other = xcount[1], most = max(own, other);
-                for (uint32_t q = most > (uint32_t)ST ? most - ST : 0; q < most; ++q) {
-                    const uint32_t bar = xfull_at + q % ST * 8;
-                    if (q >= own) mbar_arrive_expect_tx(bar, C::X_STAGE);
-                    else if (q >= other) mbar_complete_tx(bar, C::X_STAGE);
-                    mbar_wait(bar, (q / ST) & 1, DRAIN_NS);
-                }
-            }
-            __syncwarp();
-            cluster_sync_all();
-        }
-    }
+    if constexpr (PAIR) cluster_sync_all();
     if (warp == 0) {
         __syncwarp();
         tc_fence_after();
