@@ -47,7 +47,7 @@
 // Measured: 8192 x 14336 x 4096 492 us in a burst (1950 TFLOP/s of FP16 MMAs, bound
 // by the tensor cores), 534 sustained, with 2 us for X's expansion; 2048 x 4096 x
 // 4096 48 us (1420); 512 x 4096 x 4096 20 us (860: tiles for half the GPU, K divided
-// in two); 128 x 14336 x 4096 22.5 us (W alone is 9 us of memory time: one tile of
+// in two); 128 x 14336 x 4096 22.4 us (W alone is 9 us of memory time: one tile of
 // 128 tokens for 112 of the 152 SMs, and the expansion is a launch of its own).
 #include <cuda_fp16.h>
 

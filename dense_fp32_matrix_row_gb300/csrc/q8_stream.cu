@@ -14,7 +14,7 @@
 //
 // Measured at 14336 x 4096 (58.7 MB of W): 12.6 us for one token (4.7 TB/s; the
 // launch and the ring's filling are 4 of them: 57344 x 4096 streams at 6.0 TB/s),
-// 13.8 up to 8 tokens, 17.8 for 16, where the expansion to FP16 and its MMAs
+// 13.8 up to 8 tokens, 17.9 for 16, where the expansion to FP16 and its MMAs
 // have the same length as the copies.  With W at an odd address, q8_stream_kernel takes
 // 29 us for one token (2.0 TB/s), 32 for 4 and 44 for 16; 1 x 4096 x 4095 9.5 us.
 #include "q8_stream.cuh"
