@@ -14,16 +14,18 @@ import ctypes
 import os
 
 from .build import LIBRARY, build  # noqa: F401  (build is part of the public API)
+from .cache import CacheQ8, attend_q8, cache_read_q8, cache_write_q8, norm_rope, norm_rope_write_q8
 from .q8 import linear_q8, moe_q8, quantize_q8, rmsnorm_q8
 
 __all__ = ["sgemm", "sgemm_host", "host_set_panels", "host_panel_rows", "sgemm_3xtf32", "sgemm_tf32", "sgemm_bf16", "sgemm_ptr", "status", "select_kernel",
            "force_kernel", "ffma_configs", "ffma_config_for", "ffma_force_config", "ffma_force_tail_sum", "ffma_tail_plan", "kernel_timing", "kernel_timing_result", "set_wait_limit", "selftest_wait", "release_workspaces", "status_string",
-           "version", "SgemmError", "lib", "quantize_q8", "rmsnorm_q8", "linear_q8", "moe_q8"]
+           "version", "SgemmError", "lib", "quantize_q8", "rmsnorm_q8", "linear_q8", "moe_q8",
+           "CacheQ8", "norm_rope", "norm_rope_write_q8", "cache_write_q8", "cache_read_q8", "attend_q8"]
 
 OK = 0
 ERR_BAD_DIM, ERR_BAD_LD, ERR_NULL_PTR, ERR_ALIAS = -1, -2, -3, -4
 ERR_CUDA, ERR_DEVICE, ERR_TIMEOUT, ERR_BAD_ARG = -5, -6, -7, -8
-ERR_TOO_LARGE, ERR_CAPTURE = -9, -10
+ERR_TOO_LARGE, ERR_CAPTURE, ERR_BAD_INDEX = -9, -10, -11
 
 KERNEL_AUTO, KERNEL_NONE, KERNEL_SCALE_C, KERNEL_FFMA_TMA = 0, 1, 2, 3
 KERNEL_FFMA_GENERIC, KERNEL_DECODE, KERNEL_TF32X3, KERNEL_TF32, KERNEL_BF16 = 4, 5, 6, 7, 8

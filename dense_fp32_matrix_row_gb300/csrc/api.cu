@@ -10,6 +10,7 @@
 #include <utility>
 #include <vector>
 
+#include "cache.cuh"
 #include "common.cuh"
 #include "sgemm_gb300.h"
 #include "workspace.cuh"
@@ -18,8 +19,8 @@ using namespace sgemm_gb300;
 
 namespace {
 
-// Kernels set bits here when a bounded wait runs out; sgemm_status() reads and
-// clears it.  One word per device (a __device__ variable lives in each
+// Kernels set bits here when a bounded wait runs out or an index lies outside its
+// array; sgemm_status() reads and clears it.  One word per device (a __device__ variable lives in each
 // device's copy of this module).
 __device__ unsigned g_err_word;
 
@@ -54,6 +55,7 @@ struct Workspace {
 };
 std::mutex g_ws_mu;                                           // the map alone
 std::map<StreamKey, Workspace> g_ws;                          // nodes never move or go
+std::atomic<bool (*)()> g_release_more{nullptr};              // see on_release
 
 // The legacy default stream cannot be captured (and may not be asked while
 // another stream is).
@@ -371,6 +373,8 @@ int fill_device_args(GemmArgs &g) {
 }
 
 int stream_workspace(size_t bytes, cudaStream_t s, WorkspaceLease &out) { return workspace(bytes, s, out); }
+
+void on_release(bool (*f)()) { g_release_more.store(f); }
 }  // namespace sgemm_gb300
 
 extern "C" {
@@ -413,7 +417,7 @@ int sgemm_status(void *stream) {
         const unsigned zero = 0;
         if (cudaMemcpy(st->err, &zero, sizeof(zero), cudaMemcpyHostToDevice) != cudaSuccess)
             return SGEMM_ERR_CUDA;
-        return SGEMM_ERR_TIMEOUT;
+        return (word & kErrWaitTimeout) != 0 ? SGEMM_ERR_TIMEOUT : SGEMM_ERR_BAD_INDEX;
     }
     return SGEMM_OK;
 }
@@ -429,6 +433,7 @@ const char *sgemm_status_string(int status) {
         case SGEMM_ERR_DEVICE: return "the current device is not an sm_103 GPU";
         case SGEMM_ERR_TIMEOUT: return "a device-side bounded wait ran out";
         case SGEMM_ERR_BAD_ARG: return "invalid argument";
+        case SGEMM_ERR_BAD_INDEX: return "an index in device memory lies outside its array";
         case SGEMM_ERR_CAPTURE:
             return "the stream is being captured and the call needs a larger workspace; "
                    "run one call of this shape eagerly on the stream first";
@@ -471,6 +476,8 @@ int sgemm_selftest_wait(int64_t ns, void *stream) {
 
 int sgemm_release_workspaces(void) {
     int rc = release_host_paths() ? SGEMM_OK : SGEMM_ERR_CUDA;
+    bool (*more)() = g_release_more.load();
+    if (more != nullptr && !more()) rc = SGEMM_ERR_CUDA;
     std::lock_guard<std::mutex> lock(g_ws_mu);
     int cur = 0;
     if (cudaGetDevice(&cur) != cudaSuccess) return SGEMM_ERR_CUDA;

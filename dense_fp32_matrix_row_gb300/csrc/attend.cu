@@ -1,0 +1,63 @@
+// attend.cu -- attention over the paged cache: the choice of a form (attend.cuh)
+// and its parameters.
+#include "attend.cuh"
+
+namespace sgemm_gb300 {
+namespace {
+
+// Up to 8 query heads to a key head take one set of MMA columns, more take two;
+// beyond 16 the cache's strips are read once for each 16.
+int tiles(const AttendArgs &a) { return a.G > 8 ? 2 : 1; }
+int padded(int D) { return D <= 64 ? 64 : D <= 128 ? 128 : 256; }
+
+bool aligned16(const sgemm_heads &h, int es) {
+    return reinterpret_cast<uintptr_t>(h.p) % 16 == 0 && h.ld * es % 16 == 0 && h.hs * es % 16 == 0;
+}
+
+// t / d = (t * mul) >> shift for 0 <= t < 2^31: mul = ceil(2^shift / d), which is off
+// by less than 2^(shift-31) / t of it.
+void divider(uint32_t d, uint32_t *mul, uint32_t *shift) {
+    uint32_t l = 0;
+    while (((uint64_t)1 << l) < d) ++l;
+    *shift = 31 + l;
+    *mul = (uint32_t)((((uint64_t)1 << *shift) + d - 1) / d);
+}
+
+}  // namespace
+
+size_t attend_workspace_bytes(const AttendArgs &a) {
+    const int dt = padded(a.D), nt = tiles(a);
+    return (size_t)a.sm_count * attend_blocks(dt, nt) * 2 * attend_part(dt, nt) * sizeof(float);
+}
+
+cudaError_t launch_attend(const AttendArgs &a, void *workspace, unsigned *tickets) {
+    const int es = a.type == kTypeBf16 ? 2 : 4, dt = padded(a.D), nt = tiles(a);
+    if (3 * a.sm_count * attend_blocks(dt, nt) > kAttendTickets) return cudaErrorInvalidConfiguration;
+    AttendParams p{};
+    p.B = a.B; p.Hk = a.Hk; p.G = a.G; p.D = a.D;
+    p.groups = (a.G + 8 * nt - 1) / (8 * nt);
+    p.page = (int)a.cache.page;
+    p.width = a.width;
+    divider((uint32_t)p.page, &p.page_mul, &p.page_shift);
+    p.whole = p.page % kStrip == 0;
+    p.window = a.window;
+    p.scale_log2 = a.scale * 1.44269504088896341f;
+    p.q = a.q.p; p.q_ld = a.q.ld; p.q_hs = a.q.hs; p.q_vec = aligned16(a.q, es);
+    p.out = a.out.p; p.o_ld = a.out.ld; p.o_hs = a.out.hs; p.o_vec = aligned16(a.out, es);
+    p.k = a.cache.k; p.v = a.cache.v; p.ks = a.cache.k_scale; p.vs = a.cache.v_scale;
+    p.k_stride = a.cache.k_stride; p.v_stride = a.cache.v_stride;
+    p.ks_stride = a.cache.k_scale_stride; p.vs_stride = a.cache.v_scale_stride;
+    p.blocks = a.cache.blocks;
+    p.table = a.table; p.ld_table = a.ld_table; p.lens = a.lens;
+    p.lse = a.lse;
+    p.parts = static_cast<float *>(workspace);
+    p.tickets = tickets;
+    p.err = a.err;
+    switch (dt) {
+        case 64: return launch_attend_64(p, a.type, nt, a.sm_count, a.stream);
+        case 128: return launch_attend_128(p, a.type, nt, a.sm_count, a.stream);
+        default: return launch_attend_256(p, a.type, nt, a.sm_count, a.stream);
+    }
+}
+
+}  // namespace sgemm_gb300

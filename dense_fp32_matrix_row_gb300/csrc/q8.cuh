@@ -235,6 +235,29 @@ __device__ __forceinline__ void block_max_sum(uint32_t &mx, float &sum, uint32_t
     sum = s;
 }
 
+// The norm's factor is r * lift.  lift is 1 unless the sum of squares left
+// FP32's range: squares that overflow (elements above about 1e18) are summed
+// again of h * 2^-100, and a mean (with eps) below 2^-100, whose squares may
+// have underflowed, of h * 2^100.
+constexpr float kLargest = 3.402823466e38f;
+constexpr float kTwo100 = 1.2676506002282294e30f, kTwoM100 = 7.8886090522101181e-31f;
+
+__device__ __forceinline__ float inv_rms(float ss, int64_t K, float eps) {
+    return __fdiv_rn(1.0f, __fsqrt_rn(__fdiv_rn(ss, (float)(K > 0 ? K : 1)) + eps));
+}
+
+// lift for a row with this sum of squares and largest |p| (see above).
+__device__ __forceinline__ float norm_lift(float ss, int64_t K, float eps, uint32_t max_bits) {
+    if (ss > kLargest && max_bits < 0x7f800000u) return kTwoM100;
+    if (ss < kTwoM100 * (float)K && eps < kTwoM100) return kTwo100;
+    return 1.0f;
+}
+
+// scale of a row: step times the norm's factor.
+__device__ __forceinline__ float row_scale(const RowQuant &rq, float lift, float r) {
+    return rq.step == 0.0f ? 0.0f : rq.step * (rq.unpre * lift) * r;
+}
+
 // Four 8-bit whole numbers as four FP16 values, exactly: 0x6400 | u is
 // 1024 + u, and u = b + 128 after flipping the sign bit, so subtracting 1152
 // gives b.  lo: bytes 0 and 1, hi: bytes 2 and 3.

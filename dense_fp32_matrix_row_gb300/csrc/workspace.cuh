@@ -47,4 +47,8 @@ struct WorkspaceLease {
 // Returns an SGEMM_* status.
 int stream_workspace(size_t bytes, cudaStream_t s, WorkspaceLease &out);
 
+// Names a function that sgemm_release_workspaces calls: frees what its file keeps
+// per stream, false if a CUDA call failed.
+void on_release(bool (*f)());
+
 }  // namespace sgemm_gb300

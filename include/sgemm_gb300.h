@@ -72,6 +72,7 @@ extern "C" {
 #define SGEMM_ERR_BAD_ARG    -8   /* any other invalid argument */
 #define SGEMM_ERR_TOO_LARGE  -9   /* beyond sgemm_noalloc's fixed scratch or a limit of sgemm_q8_moe */
 #define SGEMM_ERR_CAPTURE   -10   /* the stream is being captured and the call would allocate */
+#define SGEMM_ERR_BAD_INDEX -11   /* an index in device memory lies outside its array (from sgemm_status) */
 
 /* Kernel identifiers, for sgemm_select_kernel and sgemm_force_kernel. */
 #define SGEMM_KERNEL_AUTO          0   /* library's choice (sgemm_force_kernel only) */
@@ -340,10 +341,148 @@ int sgemm_q8_moe(int64_t T, int64_t E, int64_t top_k, int64_t H, int64_t I, cons
                  float *gates, void *stream);
 
 /*
+ * Attention over an 8-bit key-value cache: the other half of a decoder layer,
+ * between two of the products above.  The conventions of the 8-bit operators
+ * hold, with these additions.
+ * Heads       sgemm_heads names the heads of some tokens: element (t, h, d) is
+ *             at p[t*ld + h*hs + d].  ld and hs are any strides >= 0 of an input
+ *             (views of a joint projection's rows, or stored head by head); in
+ *             an output no two elements may share a place: ld >= (heads-1)*hs +
+ *             dim with hs >= dim, or hs >= (tokens-1)*ld + dim with ld >= dim
+ *             (SGEMM_ERR_BAD_LD).  Outputs do not overlap inputs or other outputs
+ *             (SGEMM_ERR_ALIAS; heads of one token stride may alternate, as
+ *             queries and keys in joint rows do); q_out may be q itself and
+ *             k_out k itself (the same pointer and strides).
+ * Cache       sgemm_q8_cache: `blocks` pages of `page` tokens each.  Token row r
+ *             of page i, head h: dim bytes at k[i*k_stride + (h*page + r)*dim],
+ *             their scale at k_scale[i*k_scale_stride + h*page + r]; v alike.
+ *             slot = i*page + r names a token's place.  dim is a multiple of 16
+ *             up to 256, page >= 1 (SGEMM_ERR_BAD_DIM); strides are at least a
+ *             page's size (SGEMM_ERR_BAD_LD); k and v are 16-byte aligned with
+ *             strides that are multiples of 16 (SGEMM_ERR_BAD_ARG).  The four
+ *             arrays do not overlap, except that pages of arrays with the same
+ *             stride in bytes may alternate.
+ * Indices     Positions, slots, page numbers and lengths are read on the device.
+ *             One that lies outside its array is not followed: what it stands
+ *             for is left out, as said below, and the next sgemm_status()
+ *             returns SGEMM_ERR_BAD_INDEX.
+ */
+typedef struct {
+    void *p;                /* element type: the call's `type`; not written through for an input */
+    int64_t heads, ld, hs;  /* strides in elements */
+} sgemm_heads;
+
+typedef struct {
+    const float *cos, *sin;      /* rows x dims/2, row stride ld */
+    int64_t rows, ld, dims;      /* dims: even, at most the head's size */
+    const int64_t *positions;    /* the tokens' rows of the tables; NULL: token t has row t */
+    int interleaved;             /* pairs (2i, 2i+1) instead of (i, i + dims/2) */
+} sgemm_rotary;
+
+typedef struct {
+    int8_t *k, *v;
+    float *k_scale, *v_scale;
+    int64_t blocks, heads, page, dim;
+    int64_t k_stride, v_stride, k_scale_stride, v_scale_stride;   /* elements from page to page */
+} sgemm_q8_cache;
+
+/*
+ * sgemm_norm_rope -- RMS norm and position rotation of each query and key head
+ * in one pass:
+ *
+ *     p = x * weight                                    (weight NULL: p = x)
+ *     (p_a, p_b) <- (p_a*cos - p_b*sin, p_b*cos + p_a*sin)   for each pair (a, b)
+ *                   among the first `dims` elements, with the table row of the
+ *                   token's position
+ *     y = p / sqrt(mean(x^2) + eps)                     (weight NULL: y = p)
+ *
+ * Products and differences of p are rounded to FP32 one by one.
+ *   D           the heads' size, a multiple of 16 up to 256 (SGEMM_ERR_BAD_DIM)
+ *   q, q_out, q_weight   heads of T tokens, their results, D floats or NULL
+ *   k, k_out, k_weight   the same for the keys; q or k (with its result) may be
+ *               NULL or have no heads
+ *   rotary      NULL: no rotation
+ * Tables of several position axes (time, height, width) are rows of cos and
+ * sin that the caller puts together, one per token, without `positions`.
+ * A token whose position is outside the tables is left out: its results stay
+ * as they were.
+ */
+int sgemm_norm_rope(int64_t T, int64_t D, int type, const sgemm_heads *q, const sgemm_heads *q_out,
+                    const float *q_weight, const sgemm_heads *k, const sgemm_heads *k_out,
+                    const float *k_weight, float eps, const sgemm_rotary *rotary, void *stream);
+
+/*
+ * sgemm_q8_cache_write -- keys and values of T tokens into the cache: each
+ * (token, head) row quantised as above, at slot slots[t].  A negative slot: the
+ * token is not stored.  One past the cache: the same, and reported.  Slots that
+ * are not negative have to differ: of a slot that several tokens name, the
+ * contents are unspecified (other slots are not touched).
+ */
+int sgemm_q8_cache_write(int64_t T, int type, const sgemm_heads *k, const sgemm_heads *v,
+                         const int64_t *slots, const sgemm_q8_cache *cache, void *stream);
+
+/*
+ * sgemm_q8_norm_rope_write -- sgemm_norm_rope and sgemm_q8_cache_write in one
+ * pass over a decoder layer's projections: q_out as sgemm_norm_rope gives it,
+ * the keys' y into the cache without being rounded to `type`:
+ *
+ *     q8 = the whole numbers of p quantised, scale = (m/127) / sqrt(mean(x^2) + eps)
+ *
+ * and the values as they are.  q may be NULL or have no heads.  A token whose
+ * position is outside the tables is left out altogether.
+ */
+int sgemm_q8_norm_rope_write(int64_t T, int type, const sgemm_heads *q, const sgemm_heads *q_out,
+                             const float *q_weight, const sgemm_heads *k, const float *k_weight,
+                             const sgemm_heads *v, float eps, const sgemm_rotary *rotary,
+                             const int64_t *slots, const sgemm_q8_cache *cache, void *stream);
+
+/*
+ * sgemm_q8_cache_read -- the cache's rows as floats: k_out and v_out (either may
+ * be NULL) of N tokens get whole number * scale of slots[0 .. N).  A row whose
+ * slot is negative, or past the cache (reported), stays as it was.
+ */
+int sgemm_q8_cache_read(int64_t N, int type, const sgemm_q8_cache *cache, const int64_t *slots,
+                        const sgemm_heads *k_out, const sgemm_heads *v_out, void *stream);
+
+/*
+ * sgemm_q8_attend -- attention of one new token per sequence over the cache:
+ *
+ *     s_t = scale * q . k_t,   out = sum_t exp(s_t) v_t / sum_t exp(s_t)
+ *     lse = log sum_t exp(s_t)
+ *
+ * over the tokens t in [max(0, lens[b] - window), lens[b]) of sequence b
+ * (window 0: from token 0), token t being row t % page of page
+ * table[b*ld_table + t/page].  Query head h reads key head h / (heads/cache
+ * heads).  A sequence without tokens gives out 0 and lse -inf.
+ *   B           sequences; q and out hold one token of each
+ *   q, out      q->heads == out->heads, a multiple of cache->heads
+ *   table       B x pages, row stride ld_table >= pages; entries of pages that hold
+ *               none of those tokens are not read
+ *   lens        B lengths.  A negative one counts as 0, one beyond pages*page as
+ *               that many (both reported).  Tokens of a page outside the cache
+ *               are left out (reported).
+ *   lse         B x q->heads floats (natural logarithms), or NULL
+ * Several new tokens of a sequence are rows of their own, with a length each.
+ * Scores, sums and results are FP32; the exponentials are rounded to 11 bits
+ * for the product with the values (22 bits for type FP32), the queries for
+ * theirs likewise (a BF16 query is exact).  A row whose scale is NaN gives
+ * NaN to the results that read it; rows that no sequence's tokens lie in may
+ * hold anything.  Sums are taken in an order that depends on `lens` and the
+ * GPU model alone.
+ * Uses the stream's workspace for parts of long sequences, grown like sgemm()'s
+ * with the shape (not with the lengths), and a small array of counters kept
+ * per stream beside it; the same rules for stream capture hold for both.
+ */
+int sgemm_q8_attend(int64_t B, int type, const sgemm_heads *q, const sgemm_q8_cache *cache,
+                    const int32_t *table, int64_t ld_table, int64_t pages, const int32_t *lens,
+                    float scale, int64_t window, const sgemm_heads *out, float *lse, void *stream);
+
+/*
  * sgemm_status -- wait for `stream`, then report and clear the current
  * device's kernel error word.  Returns SGEMM_OK, SGEMM_ERR_TIMEOUT when a
  * kernel's bounded wait ran out since the last call (that kernel skipped its
- * stores and exited; C is unspecified), or SGEMM_ERR_CUDA.
+ * stores and exited; C is unspecified), SGEMM_ERR_BAD_INDEX when a kernel met
+ * an index outside its array (and did not follow it), or SGEMM_ERR_CUDA.
  */
 int sgemm_status(void *stream);
 
