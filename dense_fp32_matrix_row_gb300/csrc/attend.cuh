@@ -140,8 +140,8 @@ __device__ __forceinline__ void pair_tokens(uint32_t a, uint32_t b, uint32_t (&r
 
 // 2^e for -126 <= e <= 127.
 __device__ __forceinline__ float pow2(int e) { return __uint_as_float((uint32_t)(e + 127) << 23); }
-// e with 2^e <= v < 2^(e+1) for a positive finite v, kept in [-120, 127]; -120 for 0.
-__device__ __forceinline__ int exponent(float v) { return max(-120, (int)((__float_as_uint(v) >> 23) & 0xff) - 127); }
+// e with 2^e <= v < 2^(e+1) for a finite v >= 2^-118; -118 below, 128 beyond.
+__device__ __forceinline__ int exponent(float v) { return max(-118, (int)((__float_as_uint(v) >> 23) & 0xff) - 127); }
 
 template <int DT, int NT, int TERMS>
 struct Shape {
@@ -454,12 +454,14 @@ struct Attend {
             if (!on0) v0 = 0.0f;
             if (!on1) v1 = 0.0f;
         }
-        // The scaling by m and vmul is kept until a score passes m + 6 or a value's
-        // scale vcap: probabilities stay below 2^6, their products with the scales
-        // below 2^14 and exact sums in reach of FP16's 65504.
+        // The scaling by m and vmul is kept until a score passes m + 5 or a value's
+        // scale vcap: probabilities stay below 2^5 and their products with the scales,
+        // which vmul takes to [2^8, 2^10], below 2^15, in FP16's range.  FP16 rounds
+        // such a product to 11 bits, or to 2^-24 where it is below 2^-14: 2^-33 of the
+        // largest scale (p = 1), a token.
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
-            grown |= fmaxf(sc[nt][0], sc[nt][2]) > m[nt][0] + 6.0f || fmaxf(sc[nt][1], sc[nt][3]) > m[nt][1] + 6.0f;
+            grown |= fmaxf(sc[nt][0], sc[nt][2]) > m[nt][0] + 5.0f || fmaxf(sc[nt][1], sc[nt][3]) > m[nt][1] + 5.0f;
         const float vm = fmaxf(fabsf(v0), fabsf(v1));
         grown |= vm > vcap;
         if (__any_sync(0xffffffffu, grown)) rescale(sc, vm);
@@ -525,10 +527,10 @@ struct Attend {
         float f = 1.0f;
         if (vm > vcap) {
             const int e = min(exponent(vm), 127);
-            const float to = pow2(5 - e);
+            const float to = pow2(8 - e);
             f = vcap < 0.0f ? 1.0f : to / vmul;
             vmul = to;
-            vcap = e < 124 ? pow2(e + 3) : INFINITY;
+            vcap = e < 126 ? pow2(e + 2) : INFINITY;
         }
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)

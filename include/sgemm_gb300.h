@@ -464,8 +464,9 @@ int sgemm_q8_cache_read(int64_t N, int type, const sgemm_q8_cache *cache, const 
  *   lse         B x q->heads floats (natural logarithms), or NULL
  * Several new tokens of a sequence are rows of their own, with a length each.
  * Scores, sums and results are FP32; the exponentials are rounded to 11 bits
- * for the product with the values (22 bits for type FP32), the queries for
- * theirs likewise (a BF16 query is exact).  A row whose scale is NaN gives
+ * for the product with the values (22 bits for type FP32; those below about
+ * 2^-22 of the largest to 2^-33 of it), the queries for theirs likewise (a BF16
+ * query is exact).  A row whose scale is NaN gives
  * NaN to the results that read it; rows that no sequence's tokens lie in may
  * hold anything.  Sums are taken in an order that depends on `lens` and the
  * GPU model alone.
