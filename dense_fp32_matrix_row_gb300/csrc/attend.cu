@@ -27,12 +27,13 @@ void divider(uint32_t d, uint32_t *mul, uint32_t *shift) {
 
 size_t attend_workspace_bytes(const AttendArgs &a) {
     const int dt = padded(a.D), nt = tiles(a);
-    return (size_t)a.sm_count * attend_blocks(dt, nt) * 2 * attend_part(dt, nt) * sizeof(float);
+    const int terms = a.type == kTypeBf16 ? 1 : 2;
+    return (size_t)a.sm_count * attend_parts(dt, nt, terms) * attend_part(dt, nt) * sizeof(float);
 }
 
 cudaError_t launch_attend(const AttendArgs &a, void *workspace, unsigned *tickets) {
     const int es = a.type == kTypeBf16 ? 2 : 4, dt = padded(a.D), nt = tiles(a);
-    if (3 * a.sm_count * attend_blocks(dt, nt) > kAttendTickets) return cudaErrorInvalidConfiguration;
+    if (3 * a.sm_count > kAttendTickets) return cudaErrorInvalidConfiguration;
     AttendParams p{};
     p.B = a.B; p.Hk = a.Hk; p.G = a.G; p.D = a.D;
     p.groups = (a.G + 8 * nt - 1) / (8 * nt);

@@ -17,21 +17,26 @@
 // reads 16 consecutive bytes of a row.  S^T comes out as P^T goes in except for a
 // transposition of 8 x 8, one instruction (movmatrix).
 //
-// Strips travel through shared memory with cp.async, a ring for each warp, so that
-// no barrier stands between a warp and its data.  The work of all sequences is
-// one list of rounds (a strip for each of the block's warps), divided evenly over
-// the blocks from the lengths as they are on the device: ragged batches balance,
-// and one long sequence spreads over every SM.  A sequence's head that several
-// blocks share is joined by the last of them to finish, in a fixed order.
+// Work: the strips of all sequences' key heads are one list, divided evenly over
+// the blocks (one on an SM) from the lengths as they are on the device, and over
+// a block's warps: ragged batches balance, and one long sequence spreads over
+// every SM.  A warp streams its strips through a ring of its own in shared memory
+// (cp.async) and meets no barrier until its last: what a key head costs besides
+// its strips (queries, results) is latency that the other warps cover.  A key
+// head that several warps share is summed at the end, first within the block,
+// then by the last of the blocks that share it, always in the same order.
 #pragma once
 
 #include "cache.cuh"
 
 namespace sgemm_gb300 {
 
-constexpr int kAttendWarps = 4;
 constexpr int kStrip = 16;                 // tokens
-constexpr int kJoin = 16;                  // parts joined at a time
+constexpr int kJoin = 48;                  // blocks' parts summed at a time
+// A block boundary within so many strips of a key head's first or last strip moves
+// there: joining blocks costs about as long as reading twice as many.
+constexpr int kSnap = 16;
+constexpr int kLeast = 2;                  // strips to a warp, before work goes to another block
 
 struct AttendParams {
     int B, Hk, G, D, groups;               // groups: of 8*NT query heads to a key head
@@ -50,7 +55,7 @@ struct AttendParams {
     const int32_t *table; int64_t ld_table;
     const int32_t *lens;
     float *lse;
-    float *parts;                          // 2 * gridDim.x parts
+    float *parts;                          // attend_parts() for each block
     unsigned *tickets;                     // 2 * gridDim.x for parts, gridDim.x for groups of parts
     unsigned *err;
 };
@@ -58,10 +63,14 @@ struct AttendParams {
 cudaError_t launch_attend_64(const AttendParams &p, int type, int nt, int sms, cudaStream_t stream);
 cudaError_t launch_attend_128(const AttendParams &p, int type, int nt, int sms, cudaStream_t stream);
 cudaError_t launch_attend_256(const AttendParams &p, int type, int nt, int sms, cudaStream_t stream);
-// Blocks on an SM, which the workspace is sized by.
-constexpr int attend_blocks(int dt, int nt) { return dt == 64 ? 4 : dt == 128 ? (nt == 1 ? 4 : 3) : 2; }
+// Warps of a block: what 65536 registers and the rings leave room for (terms: 2 for FP32).
+constexpr int attend_warps(int dt, int nt, int terms) {
+    return dt == 64 ? 16 : dt == 128 ? (nt == 1 ? 16 : terms == 1 ? 12 : 8) : nt * terms == 4 ? 4 : 8;
+}
 // Floats of one part: sums of 8*nt heads, then each head's m and sum of p.
 constexpr int attend_part(int dt, int nt) { return 8 * nt * (dt + 2); }
+// Parts in the workspace: two of each block, one of each warp.
+constexpr int attend_parts(int dt, int nt, int terms) { return 2 + attend_warps(dt, nt, terms); }
 
 #ifdef __CUDACC__
 
@@ -145,24 +154,24 @@ __device__ __forceinline__ int exponent(float v) { return max(-118, (int)((__flo
 
 template <int DT, int NT, int TERMS>
 struct Shape {
+    static constexpr int WARPS = attend_warps(DT, NT, TERMS);
+    static constexpr int THREADS = 32 * WARPS;
     static constexpr int CH = DT / 16;                 // 16-byte chunks of a row
     static constexpr int STEPS = DT / 16;              // MMAs along the head, and dim tiles of O^T
     static constexpr int ROWS = kStrip * DT;           // bytes of a strip's keys
     static constexpr int STAGE = 2 * ROWS + 256;       // keys, values, 16 + 16 scales, the mask
     static constexpr int HEADS = 8 * NT;
-    static constexpr int BLOCKS = attend_blocks(DT, NT);
-    // merge: every warp's sums of DM dims of all heads, padded against bank conflicts
-    static constexpr int DM = (DT * NT > 128) ? 128 / NT : DT;
-    static constexpr int MERGE = kAttendWarps * HEADS * (DM + 4) * 4;
-    // the queries' operands: in registers as long as they take at most 32
-    static constexpr bool Q_SHARED = NT * TERMS * STEPS * 2 > 32;
-    static constexpr int QUERIES = Q_SHARED ? NT * TERMS * STEPS * 256 : 0;
-    static constexpr int FIXED = MERGE + kAttendWarps * HEADS * 8 + 64 + QUERIES;
-    static constexpr int ROOM = (227 * 1024) / BLOCKS - 1024 - 128 - FIXED;
-    static constexpr int MOST = ROOM / (kAttendWarps * STAGE);
+    static constexpr int PART = attend_part(DT, NT);
+    // the queries' operands: in registers as long as they leave room for the sums
+    static constexpr bool Q_SHARED = DT * NT * (TERMS + 1) > 768;
+    static constexpr int QUERIES = Q_SHARED ? NT * TERMS * STEPS * 256 : 0;       // a warp
+    static constexpr int NOTES = WARPS * 64 + 256;        // see the kernel
+    static constexpr int ROOM = 227 * 1024 - 128 - NOTES - WARPS * QUERIES;
+    static constexpr int MOST = ROOM / (WARPS * STAGE);
     static constexpr int STAGES = MOST > 6 ? 6 : MOST;
-    static constexpr int SMEM = kAttendWarps * STAGES * STAGE + FIXED + 128;
+    static constexpr int SMEM = WARPS * (STAGES * STAGE + QUERIES) + NOTES + 128;
     static_assert(STAGES >= 2, "a ring has two strips at least");
+    static_assert(PART * 4 <= STAGES * STAGE, "a ring holds its warp's sums");
 };
 
 // Byte offset of chunk c of row r in a strip, chunks exchanged within 128 bytes so
@@ -199,7 +208,6 @@ __device__ __forceinline__ void load_q16(const T *q, int d, int D, bool vec, flo
 struct Span {
     int first, last;       // tokens [first, last)
     int strip0, strips;    // strips of 16 from token 16*strip0 on
-    __device__ __forceinline__ int rounds() const { return (strips + kAttendWarps - 1) / kAttendWarps; }
 };
 
 __device__ __forceinline__ Span span_of(const AttendParams &p, int b) {
@@ -214,24 +222,107 @@ __device__ __forceinline__ Span span_of(const AttendParams &p, int b) {
     return s;
 }
 
-// A place in the list of rounds: sequence, key head and group of query heads, round.
+// a / b for 0 <= a, 0 < b; mostly both fit 32 bits, where it takes a fifth of the time.
+__device__ __forceinline__ int64_t quotient(int64_t a, int64_t b) {
+    return ((a | b) >> 32) == 0 ? (int64_t)((uint32_t)a / (uint32_t)b) : a / b;
+}
+
+// A place in the list: sequence, key head, group of its query heads, strip.
 struct Cursor {
-    int b, item, round;
+    int b, h, group, strip;
     Span span;
+    // Only where another strip follows in the list.
     __device__ __forceinline__ void step(const AttendParams &p) {
-        if (++round < span.rounds()) return;
-        round = 0;
-        if (++item < p.Hk * p.groups) return;
-        item = 0;
-        do {
-            if (++b >= p.B) { b = p.B - 1; return; }    // past the end: nothing follows
-            span = span_of(p, b);
-        } while (span.strips == 0);
+        if (++strip < span.strips) return;
+        strip = 0;
+        if (++group < p.groups) return;
+        group = 0;
+        if (++h < p.Hk) return;
+        h = 0;
+        do span = span_of(p, ++b);
+        while (span.strips == 0 && b + 1 < p.B);
+    }
+    // The place `off` strips behind the begin of sequence `from`, by a whole warp: 32
+    // sequences at a time.
+    __device__ __forceinline__ void seek(const AttendParams &p, int from, int64_t off) {
+        const int lane = threadIdx.x & 31, items = p.Hk * p.groups;
+        while (true) {
+            const int own = min(from + lane, p.B - 1);
+            const int64_t count = from + lane < p.B ? (int64_t)span_of(p, own).strips * items : 0;
+            int64_t upto = count;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int64_t x = __shfl_up_sync(0xffffffffu, upto, o);
+                if (lane >= o) upto += x;
+            }
+            const uint32_t behind = __ballot_sync(0xffffffffu, upto > off);
+            if (behind != 0 || from + 32 >= p.B) {
+                const int k = behind != 0 ? __ffs(behind) - 1 : 31;
+                off -= __shfl_sync(0xffffffffu, upto - count, k);
+                b = min(from + k, p.B - 1);
+                break;
+            }
+            off -= __shfl_sync(0xffffffffu, upto, 31);
+            from += 32;
+        }
+        span = span_of(p, b);
+        const int64_t n = max(span.strips, 1), item = quotient(off, n);
+        strip = (int)(off - item * n);
+        h = (int)item / p.groups;
+        group = (int)item - h * p.groups;
     }
 };
 
-// The first round of block c among `blocks`.
-__device__ __forceinline__ int64_t block_start(int64_t total, int c, int blocks) { return total * c / blocks; }
+// The list's division: block c begins at strip total*c/blocks, unless that is
+// within kSnap strips of a key head's begin or end.
+struct Division {
+    int64_t total;
+    int blocks;
+    __device__ __forceinline__ int64_t raw(int c) const { return quotient(total * c, blocks); }
+    // Moves a boundary `off` strips into a key head of n strips.
+    static __device__ __forceinline__ int64_t snapped(int64_t at, int off, int n) {
+        if (off > kSnap && n - off > kSnap) return at;
+        return 2 * off < n ? at - off : at + (n - off);
+    }
+    // Of a key head at [at, at + n): the blocks first..last that share it, by the
+    // boundaries that lie within it.  first >= last: one block alone.
+    __device__ __forceinline__ void blocks_of(int64_t at, int n, int &first, int &last) const {
+        // the smallest c with raw(c) > at + kSnap, less one; the largest with raw(c) < at + n - kSnap
+        first = (int)quotient((at + kSnap + 1) * blocks + total - 1, total) - 1;
+        last = n > kSnap ? (int)quotient((at + n - kSnap) * blocks + total - 1, total) - 1 : first;
+    }
+};
+
+// The first of a block's n strips that is warp w's of W: even shares, and one each
+// for the first warps where there are fewer strips than warps.
+template <int W>
+__device__ __forceinline__ int64_t first_of(int64_t n, int w) {
+    return n >= W ? n * w / W : w < n ? w : n;
+}
+
+// A part holds unnormalised sums of all heads, then each head's m and sum of p.  Four
+// dims stay together; they are exchanged within a head so that a warp's stores meet
+// in no bank of shared memory.
+template <int DT>
+__device__ __forceinline__ int part_at(int head, int d) { return head * DT + (d ^ ((head >> 1 & 3) << 2)); }
+
+// Four dims of a head's result; with d == 0 its lse too.
+template <typename T>
+__device__ __forceinline__ void finish_head(const AttendParams &p, int b, int h, int head, int d, float4 o, float top,
+                                            float total) {
+    if (head >= p.G || d >= p.D) return;
+    const float inv = total != 0.0f ? 1.0f / total : 0.0f;
+    const float v[4] = {o.x * inv, o.y * inv, o.z * inv, o.w * inv};
+    T *to = static_cast<T *>(p.out) + b * p.o_ld + ((int64_t)h * p.G + head) * p.o_hs + d;
+    if (p.o_vec) {
+        store_vec<T, 4>(to, v);
+    } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) to[i] = from_f32<T>(v[i]);
+    }
+    if (d == 0 && p.lse)
+        p.lse[((int64_t)b * p.Hk + h) * p.G + head] = total != 0.0f ? (top + log2f(total)) * 0.69314718055994531f : -INFINITY;
+}
 
 template <int DT, int NT, typename T>
 struct Attend {
@@ -241,21 +332,21 @@ struct Attend {
 
     const AttendParams &p;
     uint32_t ring;          // this warp's stages
-    uint32_t queries;       // Q_SHARED: the block's
+    uint32_t queries;       // Q_SHARED: this warp's
     int warp, lane, g, j;
 
     // the strip to be loaded next: its page number is on its way
     Cursor next;
-    int64_t left;           // rounds not yet loaded
+    int64_t left;           // strips not yet loaded
     int next_page;
-    bool next_on;
 
-    __device__ __forceinline__ Attend(const AttendParams &pp, uint32_t smem, uint32_t q) : p(pp), queries(q) {
+    __device__ __forceinline__ Attend(const AttendParams &pp, uint32_t smem) : p(pp) {
         warp = threadIdx.x >> 5;
         lane = threadIdx.x & 31;
         g = lane >> 2;
         j = lane & 3;
         ring = smem + warp * (S::STAGES * S::STAGE);
+        queries = smem + S::WARPS * (S::STAGES * S::STAGE) + warp * S::QUERIES;
     }
 
     __device__ __forceinline__ int page_of(int t) const {
@@ -265,11 +356,9 @@ struct Attend {
     // Asks for the page number of the strip at `next` (of this lane's token of it
     // where a strip may reach over several pages).
     __device__ __forceinline__ void look_up() {
-        const int strip = next.round * kAttendWarps + warp;
-        next_on = left > 0 && strip < next.span.strips;
         next_page = -1;
-        if (next_on) {
-            int t = (next.span.strip0 + strip) * kStrip;
+        if (left > 0) {
+            int t = (next.span.strip0 + next.strip) * kStrip;
             if (!p.whole) t = max(min(t + (lane & 15), next.span.last - 1), next.span.first);
             next_page = __ldg(p.table + next.b * p.ld_table + page_of(t));
         }
@@ -277,10 +366,10 @@ struct Attend {
 
     // Starts the copies of the strip at `next` into stage s, and moves on.
     __device__ __forceinline__ void load(int s) {
-        if (next_on) {
+        if (left > 0) {
             const uint32_t at = ring + s * S::STAGE;
-            const int h = next.item / p.groups;
-            const int t0 = (next.span.strip0 + next.round * kAttendWarps + warp) * kStrip;
+            const int h = next.h;
+            const int t0 = (next.span.strip0 + next.strip) * kStrip;
             const int t = t0 + (lane & 15);
             const bool known = next_page >= 0 && next_page < p.blocks;
             if (!known && lane < 16) record_error(p.err, kErrBadIndex);
@@ -322,9 +411,9 @@ struct Attend {
                 }
             }
             if (lane == 0) asm volatile("st.shared.u32 [%0], %1;" ::"r"(at + 2 * S::ROWS + 128), "r"(mask) : "memory");
+            if (--left > 0) next.step(p);
         }
         cp_commit();
-        if (left > 0 && --left > 0) next.step(p);
         look_up();
     }
 
@@ -335,10 +424,10 @@ struct Attend {
     float vmul, vcap;                   // a power of two that the probabilities carry; the largest scale it is for
     float acc[S::STEPS][NT][4];
 
-    // Queries of group `item` of sequence b as the MMA's B, scaled by a power of two
+    // The queries of the key head at `at` as the MMA's B, scaled by a power of two
     // into FP16's range (below 2^15, so a BF16 query is exact).
-    __device__ __forceinline__ void begin(int b, int item) {
-        const int h = item / p.groups, first = (item % p.groups) * S::HEADS;
+    __device__ __forceinline__ void begin(const Cursor &at) {
+        const int b = at.b, h = at.h, first = at.group * S::HEADS;
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
             const int head = first + nt * 8 + g;
@@ -380,14 +469,12 @@ struct Attend {
         }
         vmul = 1.0f;
         vcap = -1.0f;
-        if constexpr (S::Q_SHARED) __syncthreads();
     }
 
-    // Where they are shared, every warp has computed them and stores a part.
+    // A lane reads what it has written itself.
     __device__ __forceinline__ void put_query(int nt, int term, int step, uint32_t lo, uint32_t hi) {
         if constexpr (S::Q_SHARED) {
-            if (step % kAttendWarps == warp)
-                asm volatile("st.shared.v2.u32 [%0], {%1, %2};" ::"r"(queries + ((nt * TERMS + term) * S::STEPS + step) * 256 + 8 * lane),
+            asm volatile("st.shared.v2.u32 [%0], {%1, %2};" ::"r"(queries + ((nt * TERMS + term) * S::STEPS + step) * 256 + 8 * lane),
                              "r"(lo), "r"(hi)
                              : "memory");
         } else {
@@ -556,120 +643,208 @@ struct Attend {
         const int word = i >> 1, base = DT == 64 ? 8 * g : 16 * (g + 8 * (word >> 2));
         return base + 4 * (DT == 64 ? word : word & 3) + 2 * (i & 1);
     }
+
+    // The sums of p over the warp's lanes (each lane's heads 2j and 2j + 1).
+    __device__ __forceinline__ void total() {
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int k = 0; k < 2; ++k)
+#pragma unroll
+                for (int o = 4; o < 32; o <<= 1) sum[nt][k] += __shfl_xor_sync(0xffffffffu, sum[nt][k], o);
+    }
+
+    // Calls f(head, dim, four sums from dim on, k, nt) for all this lane holds.
+    template <typename F>
+    __device__ __forceinline__ void each(F f) const {
+        const float unscale = 1.0f / vmul;
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int k = 0; k < 2; ++k)
+#pragma unroll
+                for (int i = 0; i < S::STEPS; i += 2)
+                    f(nt * 8 + 2 * j + k, dim_of(i),
+                      make_float4(acc[i][nt][k] * unscale, acc[i][nt][k + 2] * unscale, acc[i + 1][nt][k] * unscale,
+                                  acc[i + 1][nt][k + 2] * unscale),
+                      m[nt][k], sum[nt][k]);
+    }
+
+    // As a part: see part_at.
+    __device__ __forceinline__ void store(float *part) const {
+        each([&](int head, int d, float4 o, float top, float sum_p) {
+            *reinterpret_cast<float4 *>(part + part_at<DT>(head, d)) = o;
+            if (d == 0) *reinterpret_cast<float2 *>(part + S::HEADS * DT + 2 * head) = make_float2(top, sum_p);
+        });
+    }
+    __device__ __forceinline__ void finish(const Cursor &at) const {
+        each([&](int head, int d, float4 o, float top, float sum_p) {
+            finish_head<T>(p, at.b, at.h, at.group * S::HEADS + head, d, o, top, sum_p);
+        });
+    }
 };
 
-// Four dims of a head's result; with d == 0 its lse too.
-template <int DT, int NT, typename T>
-__device__ __forceinline__ void finish(const AttendParams &p, int b, int h, int head, int d, float4 o, float top, float total) {
-    if (head >= p.G || d >= p.D) return;
-    const float inv = total != 0.0f ? 1.0f / total : 0.0f;
-    const float v[4] = {o.x * inv, o.y * inv, o.z * inv, o.w * inv};
-    T *to = static_cast<T *>(p.out) + b * p.o_ld + ((int64_t)h * p.G + head) * p.o_hs + d;
-    if (p.o_vec) {
-        store_vec<T, 4>(to, v);
-    } else {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) to[i] = from_f32<T>(v[i]);
-    }
-    if (d == 0 && p.lse)
-        p.lse[((int64_t)b * p.Hk + h) * p.G + head] = total != 0.0f ? (top + log2f(total)) * 0.69314718055994531f : -INFINITY;
-}
-
-// Counts this block in at a ticket; true in all its threads if it is the last of n.
-__device__ __forceinline__ bool last_of(unsigned *ticket, int n, int *note) {
-    __syncthreads();            // all parts of this block are written
-    if (threadIdx.x == 0) {
-        __threadfence();
-        const bool last = atomicAdd(ticket, 1u) == (unsigned)(n - 1);
-        if (last) *ticket = 0;
-        __threadfence();
-        note[0] = last;
-    }
-    __syncthreads();
-    return note[0] != 0;
-}
-
-// Sums n parts (part i at where(i)) for four dims of a head.
-template <int DT, int NT, typename Where>
+// Sums n parts (part i at where(i)) for four dims of a head; BATCH parts' loads are
+// under way together.
+template <int DT, int NT, bool GLOBAL, typename Where>
 __device__ __forceinline__ void sum_parts(int n, Where where, int head, int d, float4 &o, float &top, float &total) {
+    constexpr int BATCH = 8;
     top = -1e30f;
-    for (int i = 0; i < n; ++i)
-        top = fmaxf(top, __ldcg(reinterpret_cast<const float2 *>(where(i) + 8 * NT * DT + 2 * head)).x);
     o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
     total = 0.0f;
-    for (int i = 0; i < n; ++i) {
-        const float2 y = __ldcg(reinterpret_cast<const float2 *>(where(i) + 8 * NT * DT + 2 * head));
-        const float4 x = __ldcg(reinterpret_cast<const float4 *>(where(i) + head * DT + d));
-        const float f = exp2_fast(y.x - top);
-        total += y.y * f;
-        o.x += x.x * f; o.y += x.y * f; o.z += x.z * f; o.w += x.w * f;
+    for (int i0 = 0; i0 < n; i0 += BATCH) {
+        float2 y[BATCH];
+        float4 x[BATCH];
+#pragma unroll
+        for (int i = 0; i < BATCH; ++i) {
+            const float *from = where(min(i0 + i, n - 1));
+            const float2 *py = reinterpret_cast<const float2 *>(from + 8 * NT * DT + 2 * head);
+            const float4 *px = reinterpret_cast<const float4 *>(from + part_at<DT>(head, d));
+            if constexpr (GLOBAL) {         // other SMs wrote them
+                y[i] = __ldcg(py);
+                x[i] = __ldcg(px);
+            } else {
+                y[i] = *py;
+                x[i] = *px;
+            }
+        }
+        float to = top;
+#pragma unroll
+        for (int i = 0; i < BATCH; ++i) to = fmaxf(to, y[i].x);
+        const float f0 = exp2_fast(top - to);
+        top = to;
+        total *= f0;
+        o.x *= f0; o.y *= f0; o.z *= f0; o.w *= f0;
+#pragma unroll
+        for (int i = 0; i < BATCH; ++i) {
+            const float f = i0 + i < n ? exp2_fast(y[i].x - top) : 0.0f;
+            if (i0 + i < n) {
+                total += y[i].y * f;
+                o.x += x[i].x * f; o.y += x[i].y * f; o.z += x[i].z * f; o.w += x[i].w * f;
+            }
+        }
     }
 }
 
-// Joins the parts of one key head that blocks c0 to c1 have written: the last of
-// each kJoin blocks sums their parts into the first one's place, the last of
-// those sums the sums.
+// What a warp leaves of the key heads that it did not have alone.  head: the one it
+// ended but did not begin; tail: the one it did not end.
+struct Leftover {
+    int has_head, has_tail, through;    // through: the tail was not begun here either
+    struct Item {
+        int b, h, group, n;             // n: strips of the key head
+        int64_t at;                     // its place in the list
+    } head, tail;
+};
+static_assert(sizeof(Leftover) <= 64, "fits the room that Shape::NOTES has");
+
+// A key head that another block has a part of too.
+struct Shared {
+    Leftover::Item item;
+    int first, count;                   // blocks first .. first + count - 1; count 0: none
+};
+
+// Counts this block in; true if it is the last of n.  One thread, behind a fence.
+__device__ __forceinline__ bool last_of(unsigned *ticket, int n) {
+    const bool last = atomicAdd(ticket, 1u) == (unsigned)(n - 1);
+    if (last) *ticket = 0;          // as it was found
+    return last;
+}
+
+// Joins what blocks share, once a block has nothing else to do: its first key head
+// may have been begun by another block (kind 0), its last be ended by another
+// (kind 1).  The last block of each kJoin neighbours to come here sums their parts
+// into the first one's place, the last of those sums the sums.
 template <int DT, int NT, typename T>
-__device__ __forceinline__ void join(const AttendParams &p, int b, int h, int head0, int c0, int c1, bool is_first, int *note) {
-    constexpr int PART = attend_part(DT, NT), HEADS = 8 * NT;
-    const int n = c1 - c0 + 1, group = (int)(blockIdx.x - c0) / kJoin, groups = (n + kJoin - 1) / kJoin;
-    auto where = [&](int i) { return p.parts + (int64_t)(2 * (c0 + i) + (i == 0 ? 1 : 0)) * PART; };
-    const int g0 = group * kJoin, gn = min(kJoin, n - g0);
-    if (!last_of(p.tickets + 2 * (c0 + g0) + (g0 == 0 ? 1 : 0), gn, note)) return;
-    float4 o[(HEADS * DT / 4 + kAttendWarps * 32 - 1) / (kAttendWarps * 32)];
-    if (groups > 1) {
-        // read everything before the first part is written over
-        float2 y[sizeof(o) / sizeof(o[0])];
+__device__ __forceinline__ void join(const AttendParams &p, const Shared *shared, int *note) {
+    using S = typename Attend<DT, NT, T>::S;
+    constexpr int TASKS = S::HEADS * DT / 4, MINE = (TASKS + S::THREADS - 1) / S::THREADS;
+    if (threadIdx.x == 0) {
+        __threadfence();        // the block's parts, which a barrier has put before this
 #pragma unroll
-        for (int k = 0; k < (int)(sizeof(o) / sizeof(o[0])); ++k) {
-            const int i = threadIdx.x + k * kAttendWarps * 32, head = i / (DT / 4), d = (i % (DT / 4)) * 4;
-            sum_parts<DT, NT>(gn, [&](int q) { return where(g0 + q); }, head, d, o[k], y[k].x, y[k].y);
+        for (int kind = 0; kind < 2; ++kind) {
+            const Shared j = shared[kind];
+            bool last = false;
+            if (j.count > 0) {
+                const int g0 = ((int)blockIdx.x - j.first) / kJoin * kJoin;
+                last = last_of(p.tickets + 2 * (j.first + g0) + (g0 == 0 ? 1 : 0), min(kJoin, j.count - g0));
+            }
+            note[kind] = last;
         }
-        __syncthreads();
-#pragma unroll
-        for (int k = 0; k < (int)(sizeof(o) / sizeof(o[0])); ++k) {
-            const int i = threadIdx.x + k * kAttendWarps * 32, head = i / (DT / 4), d = (i % (DT / 4)) * 4;
-            *reinterpret_cast<float4 *>(where(g0) + head * DT + d) = o[k];
-            if (d == 0) *reinterpret_cast<float2 *>(where(g0) + HEADS * DT + 2 * head) = y[k];
-        }
-        if (!last_of(p.tickets + 2 * gridDim.x + c0, groups, note)) return;
+        __threadfence();
     }
-    for (int i = threadIdx.x; i < HEADS * (DT / 4); i += kAttendWarps * 32) {
-        const int head = i / (DT / 4), d = (i % (DT / 4)) * 4;
-        float4 x;
-        float top, total;
-        if (groups > 1) sum_parts<DT, NT>(groups, [&](int q) { return where(q * kJoin); }, head, d, x, top, total);
-        else sum_parts<DT, NT>(n, where, head, d, x, top, total);
-        finish<DT, NT, T>(p, b, h, head0 + head, d, x, top, total);
+    __syncthreads();
+#pragma unroll 1
+    for (int kind = 0; kind < 2; ++kind) {
+        if (note[kind] == 0) continue;
+        const Shared j = shared[kind];
+        const int head0 = j.item.group * S::HEADS;
+        const int g0 = ((int)blockIdx.x - j.first) / kJoin * kJoin, gn = min(kJoin, j.count - g0);
+        const int groups = (j.count + kJoin - 1) / kJoin;
+        // block i's part: the first block's is its kind 1
+        auto where = [&](int i) { return p.parts + ((int64_t)(j.first + i) * (S::WARPS + 2) + (i == 0 ? 1 : 0)) * S::PART; };
+        float4 o[MINE];
+        float2 y[MINE];
+#pragma unroll
+        for (int k = 0; k < MINE; ++k) {
+            const int i = threadIdx.x + k * S::THREADS, head = i / (DT / 4), d = (i % (DT / 4)) * 4;
+            if (i < TASKS) sum_parts<DT, NT, true>(gn, [&](int q) { return where(g0 + q); }, head, d, o[k], y[k].x, y[k].y);
+        }
+        if (groups > 1) {
+            __syncthreads();    // every part has been read before the first one is written over
+#pragma unroll
+            for (int k = 0; k < MINE; ++k) {
+                const int i = threadIdx.x + k * S::THREADS, head = i / (DT / 4), d = (i % (DT / 4)) * 4;
+                if (i >= TASKS) continue;
+                *reinterpret_cast<float4 *>(where(g0) + part_at<DT>(head, d)) = o[k];
+                if (d == 0) *reinterpret_cast<float2 *>(where(g0) + S::HEADS * DT + 2 * head) = y[k];
+            }
+            __syncthreads();
+            if (threadIdx.x == 0) {
+                __threadfence();
+                note[2] = last_of(p.tickets + 2 * gridDim.x + j.first, groups);
+                __threadfence();
+            }
+            __syncthreads();
+            if (note[2] == 0) continue;
+#pragma unroll
+            for (int k = 0; k < MINE; ++k) {
+                const int i = threadIdx.x + k * S::THREADS, head = i / (DT / 4), d = (i % (DT / 4)) * 4;
+                if (i < TASKS) sum_parts<DT, NT, true>(groups, [&](int q) { return where(q * kJoin); }, head, d, o[k], y[k].x, y[k].y);
+            }
+        }
+#pragma unroll
+        for (int k = 0; k < MINE; ++k) {
+            const int i = threadIdx.x + k * S::THREADS, head = i / (DT / 4), d = (i % (DT / 4)) * 4;
+            if (i < TASKS) finish_head<T>(p, j.item.b, j.item.h, head0 + head, d, o[k], y[k].x, y[k].y);
+        }
     }
 }
 
 template <int DT, int NT, typename T>
-__global__ void __launch_bounds__(kAttendWarps * 32, attend_blocks(DT, NT))
+__global__ void __launch_bounds__((Attend<DT, NT, T>::S::THREADS), 1)
 attend_kernel(const __grid_constant__ AttendParams p) {
     using S = typename Attend<DT, NT, T>::S;
     extern __shared__ uint8_t raw[];
     uint8_t *smem = raw + ((128 - (smem_u32(raw) & 127)) & 127);
-    float *merge = reinterpret_cast<float *>(smem + kAttendWarps * S::STAGES * S::STAGE);
-    float2 *ml = reinterpret_cast<float2 *>(merge + S::MERGE / 4);      // [warp][head]: m, sum of p
-    int *note = reinterpret_cast<int *>(ml + kAttendWarps * S::HEADS);
-    uint32_t *queries = reinterpret_cast<uint32_t *>(note + 16);
-    const int tid = threadIdx.x;
+    Leftover *left = reinterpret_cast<Leftover *>(smem + S::WARPS * (S::STAGES * S::STAGE + S::QUERIES));   // of each warp
+    int64_t *bounds = reinterpret_cast<int64_t *>(left + S::WARPS);     // the block's strips, and the list's at sequence
+    Shared *shared = reinterpret_cast<Shared *>(bounds + 4);
+    int *note = reinterpret_cast<int *>(shared + 2);
+    const int tid = threadIdx.x, warp = tid >> 5;
     const int items = p.Hk * p.groups;
+    auto parts = [&](int i) { return p.parts + ((int64_t)blockIdx.x * (S::WARPS + 2) + i) * S::PART; };
 
-    // Rounds of all sequences, and where this block's begin.  A thread counts `per`
-    // consecutive sequences.
-    Cursor start{};
-    int64_t total, mine, r0;
-    int blocks;
+    // Where the block's and its warps' strips begin.  A thread counts `per` consecutive
+    // sequences, whose strips are [before, before + count) of the list.
+    Division div;
+    int64_t begin, end;
     {
-        int64_t *sums = reinterpret_cast<int64_t *>(merge);             // one per thread, then the warps'
-        const int per = (p.B + kAttendWarps * 32 - 1) / (kAttendWarps * 32);
-        const int b0 = min(p.B, tid * per), b1 = min(p.B, b0 + per);
+        int64_t *sums = reinterpret_cast<int64_t *>(smem);      // of the warps
+        const int per = (p.B + S::THREADS - 1) / S::THREADS;
+        const int b0 = (int)min((int64_t)p.B, (int64_t)tid * per), b1 = min(p.B, b0 + per);
         int64_t count = 0;
         for (int b = b0; b < b1; ++b) {
-            const Span s = span_of(p, b);
-            count += s.rounds();
+            count += span_of(p, b).strips;
             if (blockIdx.x == 0) {
                 const int n = p.lens[b];
                 if (n < 0 || n > p.width * p.page) record_error(p.err, kErrBadIndex);
@@ -682,154 +857,153 @@ attend_kernel(const __grid_constant__ AttendParams p) {
             const int64_t x = __shfl_up_sync(0xffffffffu, before, o);
             if ((tid & 31) >= o) before += x;
         }
-        if ((tid & 31) == 31) sums[tid >> 5] = before;
+        if ((tid & 31) == 31) sums[warp] = before;
         __syncthreads();
         before -= count;
-        total = 0;
+        div.total = 0;
 #pragma unroll
-        for (int w = 0; w < kAttendWarps; ++w) {
-            if (w < (tid >> 5)) before += sums[w];
-            total += sums[w];
+        for (int w = 0; w < S::WARPS; ++w) {
+            if (w < warp) before += sums[w];
+            div.total += sums[w];
         }
-        blocks = (int)(total < (int64_t)gridDim.x ? (total > 0 ? total : 1) : gridDim.x);
-        r0 = (int)blockIdx.x < blocks ? block_start(total, blockIdx.x, blocks) : total;
-        mine = (int)blockIdx.x < blocks ? block_start(total, blockIdx.x + 1, blocks) - r0 : 0;
-        if (mine > 0 && r0 >= before && r0 < before + count) {
-            int64_t off = r0 - before;
-            int b = b0;
-            int64_t n = (int64_t)span_of(p, b).rounds() * items;
-            while (off >= n) {
-                off -= n;
-                n = (int64_t)span_of(p, ++b).rounds() * items;
+        const int64_t most = (div.total + S::WARPS * kLeast - 1) / (S::WARPS * kLeast);
+        div.blocks = most < 1 ? 1 : most < (int64_t)gridDim.x ? (int)most : (int)gridDim.x;
+        if ((int)blockIdx.x < div.blocks && div.total > 0) {
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const int c = (int)blockIdx.x + e;
+                const int64_t at = div.raw(c);
+                if (c == div.blocks) {
+                    if (tid == 0) bounds[e] = div.total;
+                } else if (at >= before && at < before + count) {
+                    int64_t off = at - before;
+                    int n = 0, b = b0;
+                    for (; b < b1; ++b) {
+                        n = span_of(p, b).strips;
+                        if (off < (int64_t)n * items) break;
+                        off -= (int64_t)n * items;
+                    }
+                    bounds[e] = Division::snapped(at, (int)(off - quotient(off, n) * n), n);
+                    if (e == 0) {       // the block's strips begin in this sequence or with the next
+                        bounds[2] = at - off;
+                        bounds[3] = b;
+                    }
+                }
             }
-            const int rounds = (int)(n / items);
-            note[0] = b;
-            note[1] = (int)(off / rounds);
-            note[2] = (int)(off % rounds);
+        } else if (tid == 0) {
+            bounds[0] = bounds[1] = 0;
         }
         // rows of sequences without tokens
-        for (int b = blockIdx.x; b < p.B; b += gridDim.x) {
-            if (span_of(p, b).strips > 0) continue;
-            for (int i = tid; i < p.Hk * p.G * p.D; i += blockDim.x)
+        for (int64_t b = blockIdx.x; b < p.B; b += gridDim.x) {
+            if (span_of(p, (int)b).strips > 0) continue;
+            for (int i = tid; i < p.Hk * p.G * p.D; i += S::THREADS)
                 static_cast<T *>(p.out)[b * p.o_ld + (i / p.D) * p.o_hs + i % p.D] = from_f32<T>(0.0f);
             if (p.lse)
-                for (int i = tid; i < p.Hk * p.G; i += blockDim.x) p.lse[(int64_t)b * p.Hk * p.G + i] = -INFINITY;
+                for (int i = tid; i < p.Hk * p.G; i += S::THREADS) p.lse[b * p.Hk * p.G + i] = -INFINITY;
         }
         __syncthreads();
-        if (mine == 0) return;
-        start.b = note[0];
-        start.item = note[1];
-        start.round = note[2];
-        start.span = span_of(p, start.b);
+        begin = bounds[0];
+        end = bounds[1];
+        if (begin >= end) return;
     }
 
-    Attend<DT, NT, T> a(p, smem_u32(smem), smem_u32(queries));
-    if (p.D < DT) {     // chunks past the head's end are never written: zeros in the products
-        uint4 *z = reinterpret_cast<uint4 *>(smem + a.warp * (S::STAGES * S::STAGE));
-        for (int i = a.lane; i < S::STAGES * S::STAGE / 16; i += 32) z[i] = make_uint4(0, 0, 0, 0);
-        __syncwarp();
-    }
-    a.next = start;
-    a.left = mine;
+    Attend<DT, NT, T> a(p, smem_u32(smem));
+    int64_t at = begin + first_of<S::WARPS>(end - begin, warp);
+    int64_t todo = begin + first_of<S::WARPS>(end - begin, warp + 1) - at;
+    Cursor cur{};
+    if (todo > 0) cur.seek(p, (int)bounds[3], at - bounds[2]);
+    Leftover rest{};
+    a.next = cur;
+    a.left = todo;
     a.look_up();
 #pragma unroll
     for (int s = 0; s < S::STAGES - 1; ++s) a.load(s);
 
-    Cursor cur = start;
     int stage = 0, fill = S::STAGES - 1;
-    int64_t todo = mine, at_round = r0;
     while (todo > 0) {
-        // one piece: the rounds of one sequence's key head that are this block's
-        const int rounds = cur.span.rounds();
-        const int n = (int)(todo < rounds - cur.round ? todo : rounds - cur.round);
-        a.begin(cur.b, cur.item);
+        // the strips of one key head that are this warp's
+        const int strips = cur.span.strips;
+        const int n = (int)(todo < strips - cur.strip ? todo : strips - cur.strip);
+        a.begin(cur);
         for (int i = 0; i < n; ++i) {
             cp_wait<S::STAGES - 2>();
             __syncwarp();       // every lane's copies have landed, and the stage filled next has been read
             a.load(fill);
-            if ((cur.round + i) * kAttendWarps + a.warp < cur.span.strips) a.consume(stage);
+            a.consume(stage);
             stage = stage + 1 == S::STAGES ? 0 : stage + 1;
             fill = fill + 1 == S::STAGES ? 0 : fill + 1;
         }
-
-        // the warps' results together
-        const int64_t item0 = at_round - cur.round;         // the key head's rounds in the list
-        const bool whole = n == rounds;
-        const int first_block = (int)(((item0 + 1) * blocks - 1) / total);
-        const int last_block = (int)(((item0 + rounds) * blocks - 1) / total);
-        const bool is_first = first_block == (int)blockIdx.x;
-        float *part = p.parts + (int64_t)(2 * blockIdx.x + (is_first ? 1 : 0)) * attend_part(DT, NT);
-        const int h = cur.item / p.groups, head0 = (cur.item % p.groups) * S::HEADS;
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-            for (int k = 0; k < 2; ++k) {
-                float x = a.sum[nt][k];
-#pragma unroll
-                for (int o = 4; o < 32; o <<= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
-                if (a.g == 0) ml[a.warp * S::HEADS + nt * 8 + 2 * a.j + k] = make_float2(a.m[nt][k], x);
-            }
-        __syncthreads();
-        const float unscale = 1.0f / a.vmul;
-        float factor[NT][2];
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-            for (int k = 0; k < 2; ++k) {
-                float top = -1e30f;
-#pragma unroll
-                for (int w = 0; w < kAttendWarps; ++w) top = fmaxf(top, ml[w * S::HEADS + nt * 8 + 2 * a.j + k].x);
-                factor[nt][k] = exp2_fast(a.m[nt][k] - top) * unscale;
-            }
-        constexpr int PITCH = S::DM + 4;
-#pragma unroll
-        for (int d0 = 0; d0 < DT; d0 += S::DM) {
-            if (d0 > 0) __syncthreads();
-#pragma unroll
-            for (int i = 0; i < S::STEPS; ++i) {
-                const int dim = a.dim_of(i) - d0;
-                if (dim < 0 || dim >= S::DM) continue;
-#pragma unroll
-                for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                    for (int k = 0; k < 2; ++k) {
-                        float *to = merge + (a.warp * S::HEADS + nt * 8 + 2 * a.j + k) * PITCH + dim;
-                        *reinterpret_cast<float2 *>(to) =
-                            make_float2(a.acc[i][nt][k] * factor[nt][k], a.acc[i][nt][k + 2] * factor[nt][k]);
-                    }
-            }
-            __syncthreads();
-            for (int i = tid; i < S::HEADS * (S::DM / 4); i += kAttendWarps * 32) {
-                const int head = i / (S::DM / 4), d = (i % (S::DM / 4)) * 4;
-                float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-                float top = -1e30f;
-                float total_p = 0.0f;
-#pragma unroll
-                for (int w = 0; w < kAttendWarps; ++w) top = fmaxf(top, ml[w * S::HEADS + head].x);
-#pragma unroll
-                for (int w = 0; w < kAttendWarps; ++w) {
-                    const float4 x = *reinterpret_cast<const float4 *>(merge + (w * S::HEADS + head) * PITCH + d);
-                    o.x += x.x; o.y += x.y; o.z += x.z; o.w += x.w;
-                    const float2 y = ml[w * S::HEADS + head];
-                    total_p += y.y * exp2_fast(y.x - top);
-                }
-                if (!whole) {
-                    *reinterpret_cast<float4 *>(part + head * DT + d0 + d) = o;
-                    if (d0 + d == 0) *reinterpret_cast<float2 *>(part + S::HEADS * DT + 2 * head) = make_float2(top, total_p);
-                } else {
-                    finish<DT, NT, T>(p, cur.b, h, head0 + head, d0 + d, o, top, total_p);
-                }
-            }
+        a.total();
+        const bool begun = cur.strip == 0, ended = cur.strip + n == strips;
+        if (begun && ended) {
+            a.finish(cur);
+        } else if (ended) {
+            a.store(parts(2 + warp));
+            rest.has_head = 1;
+            rest.head = {cur.b, cur.h, cur.group, strips, at - cur.strip};
+        } else {
+            rest.has_tail = 1;
+            rest.through = !begun;
+            rest.tail = {cur.b, cur.h, cur.group, strips, at - cur.strip};
         }
-        if (!whole) join<DT, NT, T>(p, cur.b, h, head0, first_block, last_block, is_first, note);
-        __syncthreads();        // ml, merge and note are free again
-        at_round += n;
+        at += n;
         todo -= n;
         if (todo > 0) {
-            cur.round += n - 1;
+            cur.strip += n - 1;
             cur.step(p);
         }
     }
+    cp_wait<0>();
+    __syncwarp();
+    auto ring_of = [&](int w) { return reinterpret_cast<float *>(smem + w * (S::STAGES * S::STAGE)); };
+    if (rest.has_tail) a.store(ring_of(warp));      // nothing is on its way into the ring any more
+    if (a.lane == 0) left[warp] = rest;
+    if (tid < 2) shared[tid].count = 0;
+    __syncthreads();
+
+    // What warps share.  A run is a key head's parts in consecutive warps: tails, and
+    // at its end the head part of the warp that ended it.
+    const int used = (int)min((int64_t)S::WARPS, end - begin);      // warps with strips: the first ones
+    const bool mine = a.lane < used;
+    const uint32_t heads = __ballot_sync(0xffffffffu, mine && left[a.lane].has_head);
+    const uint32_t tails = __ballot_sync(0xffffffffu, mine && left[a.lane].has_tail);
+    const uint32_t through = __ballot_sync(0xffffffffu, mine && left[a.lane].through);
+    const bool from_before = (heads | through) & 1;      // the block's first key head was begun by another
+    const uint32_t begins = tails & ~through;
+    const int runs = __popc(begins) + (from_before ? 1 : 0);
+    constexpr int TASKS = S::HEADS * DT / 4;
+    for (int i = tid; i < runs * TASKS; i += S::THREADS) {
+        const int run = i / TASKS, head = i % TASKS / (DT / 4), d = (i % (DT / 4)) * 4;
+        uint32_t open = begins;
+        for (int k = from_before ? 1 : 0; k < run; ++k) open &= open - 1;
+        const bool early = from_before && run == 0;
+        const int w0 = early ? 0 : __ffs(open) - 1;
+        const uint32_t ends = heads >> w0 >> (early ? 0 : 1) << (early ? 0 : 1) << w0;     // behind the run's begin
+        const int w1 = ends ? __ffs(ends) - 1 : used - 1;
+        float4 o;
+        float top, total_p;
+        sum_parts<DT, NT, false>(w1 - w0 + 1, [&](int k) { return ends && w0 + k == w1 ? parts(2 + w1) : ring_of(w0 + k); },
+                                 head, d, o, top, total_p);
+        // an early run that its first warp ends is that one head part
+        const Leftover::Item &item = early && left[w0].has_head ? left[w0].head : left[w0].tail;
+        if (!early && ends) {
+            finish_head<T>(p, item.b, item.h, item.group * S::HEADS + head, d, o, top, total_p);
+        } else {
+            float *part = parts(early ? 0 : 1);
+            *reinterpret_cast<float4 *>(part + part_at<DT>(head, d)) = o;
+            if (d == 0) *reinterpret_cast<float2 *>(part + S::HEADS * DT + 2 * head) = make_float2(top, total_p);
+            if (i % TASKS == 0) {
+                Shared x{item, 0, 0};
+                int last;
+                div.blocks_of(item.at, item.n, x.first, last);
+                x.count = last - x.first + 1;
+                shared[early ? 0 : 1] = x;
+            }
+        }
+    }
+    __syncthreads();
+    if (shared[0].count == 0 && shared[1].count == 0) return;
+    join<DT, NT, T>(p, shared, note);
 }
 
 template <int DT, int NT, typename T>
@@ -838,7 +1012,7 @@ cudaError_t attend_launch(const AttendParams &p, int sms, cudaStream_t stream) {
     const cudaError_t e =
         cudaFuncSetAttribute(attend_kernel<DT, NT, T>, cudaFuncAttributeMaxDynamicSharedMemorySize, S::SMEM);
     if (e != cudaSuccess) return e;
-    attend_kernel<DT, NT, T><<<sms * S::BLOCKS, kAttendWarps * 32, S::SMEM, stream>>>(p);
+    attend_kernel<DT, NT, T><<<sms, S::THREADS, S::SMEM, stream>>>(p);
     return cudaGetLastError();
 }
 
