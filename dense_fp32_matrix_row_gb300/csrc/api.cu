@@ -439,7 +439,8 @@ const char *sgemm_status_string(int status) {
                    "run one call of this shape eagerly on the stream first";
         case SGEMM_ERR_TOO_LARGE:
             return "problem beyond a fixed limit of the entry point: the fixed scratch of sgemm_noalloc "
-                   "(K * round_up(M, 4) floats > 16777216), or sgemm_q8_moe's tokens, experts or top_k";
+                   "(K * round_up(M, 4) floats > 16777216), sgemm_q8_moe's tokens, experts or top_k, or "
+                   "sgemm_q8_attend's sequences * heads * pages";
         default: return "unknown status";
     }
 }

@@ -37,6 +37,9 @@ constexpr int kJoin = 48;                  // blocks' parts summed at a time
 // there: joining blocks costs about as long as reading twice as many.
 constexpr int kSnap = 16;
 constexpr int kLeast = 2;                  // strips to a warp, before work goes to another block
+// A key head of at most so many strips is one warp's: summing two warps' parts costs
+// about as long as four strips.
+constexpr int kWhole = 10;
 
 struct AttendParams {
     int B, Hk, G, D, groups;               // groups: of 8*NT query heads to a key head
@@ -165,7 +168,7 @@ struct Shape {
     // the queries' operands: in registers as long as they leave room for the sums
     static constexpr bool Q_SHARED = DT * NT * (TERMS + 1) > 768;
     static constexpr int QUERIES = Q_SHARED ? NT * TERMS * STEPS * 256 : 0;       // a warp
-    static constexpr int NOTES = WARPS * 64 + 256;        // see the kernel
+    static constexpr int NOTES = WARPS * (72 + 8) + 128;      // see the kernel
     static constexpr int ROOM = 227 * 1024 - 128 - NOTES - WARPS * QUERIES;
     static constexpr int MOST = ROOM / (WARPS * STAGE);
     static constexpr int STAGES = MOST > 6 ? 6 : MOST;
@@ -183,48 +186,24 @@ __device__ __forceinline__ uint32_t chunk_at(int r, int c) {
     else return (uint32_t)(r * DT + (c >> 3) * 128 + (((c & 7) ^ (r & 7)) << 4));
 }
 
-// 16 values of a query head from element d on, zeros past the head's end.
-template <typename T>
-__device__ __forceinline__ void load_q16(const T *q, int d, int D, bool vec, float (&x)[16]) {
-    if (q == nullptr || d >= D) {
-#pragma unroll
-        for (int i = 0; i < 16; ++i) x[i] = 0.0f;
-    } else if (vec) {
-        constexpr int V = 16 / (int)sizeof(T);
-#pragma unroll
-        for (int i = 0; i < 16 / V; ++i) {
-            float part[V];
-            load_vec<T, V>(q + d + V * i, part);
-#pragma unroll
-            for (int e = 0; e < V; ++e) x[V * i + e] = part[e];
-        }
-    } else {
-#pragma unroll
-        for (int i = 0; i < 16; ++i) x[i] = to_f32<T>(q[d + i]);
-    }
-}
-
 // The strips of a sequence that its new token attends to.
 struct Span {
     int first, last;       // tokens [first, last)
     int strip0, strips;    // strips of 16 from token 16*strip0 on
 };
 
-__device__ __forceinline__ Span span_of(const AttendParams &p, int b) {
-    const int most = p.width * p.page;
-    int n = __ldg(p.lens + b);
-    n = n < 0 ? 0 : n > most ? most : n;
+// Of a sequence of n tokens, 0 <= n.
+__device__ __forceinline__ Span span_of(const AttendParams &p, int n) {
     Span s;
     s.last = n;
     s.first = p.window > 0 && n > p.window ? n - p.window : 0;
     s.strip0 = s.first / kStrip;
-    s.strips = n > 0 ? (n + kStrip - 1) / kStrip - s.strip0 : 0;
+    s.strips = n > 0 ? (n - 1) / kStrip + 1 - s.strip0 : 0;
     return s;
 }
-
-// a / b for 0 <= a, 0 < b; mostly both fit 32 bits, where it takes a fifth of the time.
-__device__ __forceinline__ int64_t quotient(int64_t a, int64_t b) {
-    return ((a | b) >> 32) == 0 ? (int64_t)((uint32_t)a / (uint32_t)b) : a / b;
+// A sequence's length, within what its pages hold.
+__device__ __forceinline__ int tokens_of(const AttendParams &p, int b) {
+    return max(0, min(__ldg(p.lens + b), p.width * p.page));
 }
 
 // A place in the list: sequence, key head, group of its query heads, strip.
@@ -239,72 +218,110 @@ struct Cursor {
         group = 0;
         if (++h < p.Hk) return;
         h = 0;
-        do span = span_of(p, ++b);
+        do span = span_of(p, tokens_of(p, ++b));
         while (span.strips == 0 && b + 1 < p.B);
-    }
-    // The place `off` strips behind the begin of sequence `from`, by a whole warp: 32
-    // sequences at a time.
-    __device__ __forceinline__ void seek(const AttendParams &p, int from, int64_t off) {
-        const int lane = threadIdx.x & 31, items = p.Hk * p.groups;
-        while (true) {
-            const int own = min(from + lane, p.B - 1);
-            const int64_t count = from + lane < p.B ? (int64_t)span_of(p, own).strips * items : 0;
-            int64_t upto = count;
-#pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const int64_t x = __shfl_up_sync(0xffffffffu, upto, o);
-                if (lane >= o) upto += x;
-            }
-            const uint32_t behind = __ballot_sync(0xffffffffu, upto > off);
-            if (behind != 0 || from + 32 >= p.B) {
-                const int k = behind != 0 ? __ffs(behind) - 1 : 31;
-                off -= __shfl_sync(0xffffffffu, upto - count, k);
-                b = min(from + k, p.B - 1);
-                break;
-            }
-            off -= __shfl_sync(0xffffffffu, upto, 31);
-            from += 32;
-        }
-        span = span_of(p, b);
-        const int64_t n = max(span.strips, 1), item = quotient(off, n);
-        strip = (int)(off - item * n);
-        h = (int)item / p.groups;
-        group = (int)item - h * p.groups;
     }
 };
 
-// The list's division: block c begins at strip total*c/blocks, unless that is
-// within kSnap strips of a key head's begin or end.
+// Begins of even shares of n: the first n % shares of them are one longer.
+struct Shares {
+    int q, r;
+    __device__ __forceinline__ Shares(int n, int shares) : q((int)((unsigned)n / (unsigned)shares)), r(n - q * shares) {}
+    __device__ __forceinline__ int begin(int i) const { return q * i + min(i, r); }
+    // The first share that begins behind `at`.
+    __device__ __forceinline__ int behind(int at) const {
+        return 1 + (at < (q + 1) * r ? at / (q + 1) : (at - r) / max(q, 1));
+    }
+};
+
+// Finds places in the list, by a whole warp: it keeps 32 sequences, a lane each.
+// Where there are more, `sums` has the strips of each of a block's warps' runs of
+// `run` sequences, a multiple of 32.
+struct Locator {
+    int from, base;             // the first of the 32 sequences, and its place in the list
+    int tokens;                 // of this lane's sequence
+    int before, upto;           // its strips: [base + before, base + upto) of the list
+    const int *sums;
+    int run;
+
+    __device__ __forceinline__ void load(const AttendParams &p, int first, int at) {
+        const int lane = threadIdx.x & 31;
+        from = first;
+        base = at;
+        tokens = from + lane < p.B ? tokens_of(p, from + lane) : 0;
+        const int count = span_of(p, tokens).strips * (p.Hk * p.groups);
+        upto = count;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int x = __shfl_up_sync(0xffffffffu, upto, o);
+            if (lane >= o) upto += x;
+        }
+        before = upto - count;
+    }
+    __device__ __forceinline__ int all() const { return __shfl_sync(0xffffffffu, upto, 31); }
+
+    // The strip at `at`, which is less than the list's length.
+    __device__ __forceinline__ Cursor find(const AttendParams &p, int at) {
+        if (p.B > 32 && (at < base || at >= base + all())) {
+            int here = 0, w = 0;
+            while (at >= here + sums[w]) here += sums[w++];
+            load(p, w * run, here);
+            while (at >= base + all()) load(p, from + 32, base + all());
+        }
+        const int k = __ffs(__ballot_sync(0xffffffffu, base + upto > at)) - 1;
+        const int off = at - base - __shfl_sync(0xffffffffu, before, k);
+        Cursor c;
+        c.b = from + k;
+        c.span = span_of(p, __shfl_sync(0xffffffffu, tokens, k));
+        const int item = (int)((unsigned)off / (unsigned)c.span.strips);
+        c.strip = off - item * c.span.strips;
+        c.h = p.groups == 1 ? item : item / p.groups;
+        c.group = item - c.h * p.groups;
+        return c;
+    }
+};
+
+// The list's division: block c begins at the c-th even share, unless that is within
+// kSnap strips of a key head's begin or end.
 struct Division {
-    int64_t total;
-    int blocks;
-    __device__ __forceinline__ int64_t raw(int c) const { return quotient(total * c, blocks); }
-    // Moves a boundary `off` strips into a key head of n strips.
-    static __device__ __forceinline__ int64_t snapped(int64_t at, int off, int n) {
-        if (off > kSnap && n - off > kSnap) return at;
-        return 2 * off < n ? at - off : at + (n - off);
+    int total, blocks;
+    // A boundary at `at`, off strips into a key head of n strips, moved to its nearer end.
+    static __device__ __forceinline__ int moved(int at, int off, int n) { return 2 * off < n ? at - off : at + (n - off); }
+    __device__ __forceinline__ int start(const AttendParams &p, Locator &list, int c) const {
+        if (c == blocks) return total;
+        if (c == 0) return 0;
+        const int at = Shares(total, blocks).begin(c);
+        const Cursor x = list.find(p, at);
+        const int off = x.strip, n = x.span.strips;
+        return off > kSnap && n - off > kSnap ? at : moved(at, off, n);
     }
     // Of a key head at [at, at + n): the blocks first..last that share it, by the
     // boundaries that lie within it.  first >= last: one block alone.
-    __device__ __forceinline__ void blocks_of(int64_t at, int n, int &first, int &last) const {
-        // the smallest c with raw(c) > at + kSnap, less one; the largest with raw(c) < at + n - kSnap
-        first = (int)quotient((at + kSnap + 1) * blocks + total - 1, total) - 1;
-        last = n > kSnap ? (int)quotient((at + n - kSnap) * blocks + total - 1, total) - 1 : first;
+    __device__ __forceinline__ void blocks_of(int at, int n, int &first, int &last) const {
+        const Shares s(total, blocks);
+        first = s.behind(at + kSnap) - 1;
+        last = n > kSnap ? s.behind(at + n - kSnap - 1) - 1 : first;
     }
 };
-
-// The first of a block's n strips that is warp w's of W: even shares, and one each
-// for the first warps where there are fewer strips than warps.
-template <int W>
-__device__ __forceinline__ int64_t first_of(int64_t n, int w) {
-    return n >= W ? n * w / W : w < n ? w : n;
-}
 
 // A part holds unnormalised sums of all heads, then each head's m and sum of p.  Four
 // dims stay together; they are exchanged within a head so that a warp's stores meet
 // in no bank of shared memory.
 template <int DT>
 __device__ __forceinline__ int part_at(int head, int d) { return head * DT + (d ^ ((head >> 1 & 3) << 2)); }
+
+template <typename T>
+__device__ __forceinline__ void store_out(const AttendParams &p, T *to, const float (&v)[4]) {
+    if (p.o_vec) {
+        store_vec<T, 4>(to, v);
+    } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) to[i] = from_f32<T>(v[i]);
+    }
+}
+__device__ __forceinline__ float lse_of(float top, float total) {
+    return total != 0.0f ? (top + log2f(total)) * 0.69314718055994531f : -INFINITY;
+}
 
 // Four dims of a head's result; with d == 0 its lse too.
 template <typename T>
@@ -313,16 +330,28 @@ __device__ __forceinline__ void finish_head(const AttendParams &p, int b, int h,
     if (head >= p.G || d >= p.D) return;
     const float inv = total != 0.0f ? 1.0f / total : 0.0f;
     const float v[4] = {o.x * inv, o.y * inv, o.z * inv, o.w * inv};
-    T *to = static_cast<T *>(p.out) + b * p.o_ld + ((int64_t)h * p.G + head) * p.o_hs + d;
-    if (p.o_vec) {
-        store_vec<T, 4>(to, v);
-    } else {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) to[i] = from_f32<T>(v[i]);
-    }
-    if (d == 0 && p.lse)
-        p.lse[((int64_t)b * p.Hk + h) * p.G + head] = total != 0.0f ? (top + log2f(total)) * 0.69314718055994531f : -INFINITY;
+    store_out<T>(p, static_cast<T *>(p.out) + b * p.o_ld + ((int64_t)h * p.G + head) * p.o_hs + d, v);
+    if (d == 0 && p.lse) p.lse[((int64_t)b * p.Hk + h) * p.G + head] = lse_of(top, total);
 }
+
+// Four dims of a head summed over parts.
+struct Sum {
+    float4 o;
+    float top, total;
+    __device__ __forceinline__ Sum() : o(make_float4(0.0f, 0.0f, 0.0f, 0.0f)), top(-1e30f), total(0.0f) {}
+    __device__ __forceinline__ void rise(float to) {
+        const float f = exp2_fast(top - to);
+        top = to;
+        total *= f;
+        o.x *= f; o.y *= f; o.z *= f; o.w *= f;
+    }
+    // A part's m and sum of p, and its dims; m is at most `top`.
+    __device__ __forceinline__ void add(float2 y, float4 x) {
+        const float f = exp2_fast(y.x - top);
+        total += y.y * f;
+        o.x += x.x * f; o.y += x.y * f; o.z += x.z * f; o.w += x.w * f;
+    }
+};
 
 template <int DT, int NT, typename T>
 struct Attend {
@@ -335,9 +364,11 @@ struct Attend {
     uint32_t queries;       // Q_SHARED: this warp's
     int warp, lane, g, j;
 
-    // the strip to be loaded next: its page number is on its way
+    // the strip to be loaded next
     Cursor next;
-    int64_t left;           // strips not yet loaded
+    int left;               // strips not yet loaded
+    // its page number (that of this lane's token, where strips reach over pages), asked
+    // for when the strip before is loaded
     int next_page;
 
     __device__ __forceinline__ Attend(const AttendParams &pp, uint32_t smem) : p(pp) {
@@ -353,15 +384,11 @@ struct Attend {
         return (int)(((uint64_t)(uint32_t)t * p.page_mul) >> p.page_shift);
     }
 
-    // Asks for the page number of the strip at `next` (of this lane's token of it
-    // where a strip may reach over several pages).
     __device__ __forceinline__ void look_up() {
-        next_page = -1;
-        if (left > 0) {
-            int t = (next.span.strip0 + next.strip) * kStrip;
-            if (!p.whole) t = max(min(t + (lane & 15), next.span.last - 1), next.span.first);
-            next_page = __ldg(p.table + next.b * p.ld_table + page_of(t));
-        }
+        const int32_t *row = p.table + next.b * p.ld_table;
+        int t = (next.span.strip0 + next.strip) * kStrip;
+        if (!p.whole) t = max(min(t + (lane & 15), next.span.last - 1), next.span.first);
+        next_page = __ldg(row + page_of(t));
     }
 
     // Starts the copies of the strip at `next` into stage s, and moves on.
@@ -411,10 +438,12 @@ struct Attend {
                 }
             }
             if (lane == 0) asm volatile("st.shared.u32 [%0], %1;" ::"r"(at + 2 * S::ROWS + 128), "r"(mask) : "memory");
-            if (--left > 0) next.step(p);
+            if (--left > 0) {
+                next.step(p);
+                look_up();
+            }
         }
         cp_commit();
-        look_up();
     }
 
     // ---- one key head's running state -------------------------------------------------
@@ -424,36 +453,72 @@ struct Attend {
     float vmul, vcap;                   // a power of two that the probabilities carry; the largest scale it is for
     float acc[S::STEPS][NT][4];
 
-    // The queries of the key head at `at` as the MMA's B, scaled by a power of two
-    // into FP16's range (below 2^15, so a BF16 query is exact).
-    __device__ __forceinline__ void begin(const Cursor &at) {
-        const int b = at.b, h = at.h, first = at.group * S::HEADS;
+    // The queries of the key head at `at`, as they lie: this lane's chunks of one head
+    // of each eight.
+    struct Queries {
+        uint32_t w[NT][S::CH / 4][4 * (int)sizeof(T)];
+    };
+    __device__ __forceinline__ void fetch(Queries &x, const Cursor &at) const {
+        const int first = at.group * S::HEADS;
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
             const int head = first + nt * 8 + g;
-            const T *q = head < p.G ? static_cast<const T *>(p.q) + b * p.q_ld + (h * (int64_t)p.G + head) * p.q_hs : nullptr;
-            float x[S::CH / 4][16];
-            float most = 0.0f;
+            const T *q = static_cast<const T *>(p.q) + at.b * p.q_ld + (at.h * (int64_t)p.G + head) * p.q_hs;
 #pragma unroll
             for (int i = 0; i < S::CH / 4; ++i) {
-                load_q16<T>(q, key_chunk(i) * 16, p.D, p.q_vec != 0, x[i]);
+                const int d = key_chunk(i) * 16;
+                uint32_t(&w)[4 * (int)sizeof(T)] = x.w[nt][i];
+                if (head >= p.G || d >= p.D) {
 #pragma unroll
-                for (int e = 0; e < 16; ++e) most = fmaxf(most, fabsf(x[i][e]));
+                    for (int e = 0; e < 4 * (int)sizeof(T); ++e) w[e] = 0;
+                } else if (p.q_vec) {
+#pragma unroll
+                    for (int e = 0; e < (int)sizeof(T); ++e) {
+                        const uint4 u = *reinterpret_cast<const uint4 *>(q + d + e * (16 / (int)sizeof(T)));
+                        w[4 * e] = u.x; w[4 * e + 1] = u.y; w[4 * e + 2] = u.z; w[4 * e + 3] = u.w;
+                    }
+                } else if constexpr (SPLIT) {
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) w[e] = __float_as_uint(q[d + e]);
+                } else {
+                    const unsigned short *h = reinterpret_cast<const unsigned short *>(q + d);
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) w[e] = (uint32_t)h[2 * e] | (uint32_t)h[2 * e + 1] << 16;
+                }
             }
+        }
+    }
+
+    // The same as the MMA's B, scaled by a power of two into FP16's range (below 2^15, so a
+    // BF16 query is exact).
+    __device__ __forceinline__ void begin(const Cursor &at) {
+        Queries x;
+        fetch(x, at);
+        auto value = [&](int nt, int i, int e) {
+            if constexpr (SPLIT) return __uint_as_float(x.w[nt][i][e]);
+            else return __uint_as_float((e & 1) ? x.w[nt][i][e >> 1] & 0xffff0000u : x.w[nt][i][e >> 1] << 16);
+        };
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+            float most = 0.0f;
+#pragma unroll
+            for (int i = 0; i < S::CH / 4; ++i)
+#pragma unroll
+                for (int e = 0; e < 16; ++e) most = fmaxf(most, fabsf(value(nt, i, e)));
             most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, 1));
             most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, 2));
             const int e = min(exponent(most), 127);
             const float up = pow2(min(14 - e, 127));
-            const float mul = p.scale_log2 / up;
+            const float mul = __fdividef(p.scale_log2, up);     // exact: a power of two
 #pragma unroll
             for (int i = 0; i < S::CH / 4; ++i)
 #pragma unroll
                 for (int w = 0; w < 4; ++w) {
-                    const float a = x[i][4 * w] * up, bb = x[i][4 * w + 1] * up, c = x[i][4 * w + 2] * up,
-                                d = x[i][4 * w + 3] * up;
-                    const uint32_t lo = half_pair(a, bb), hi = half_pair(c, d);
+                    const float a = value(nt, i, 4 * w) * up, b = value(nt, i, 4 * w + 1) * up,
+                                c = value(nt, i, 4 * w + 2) * up, d = value(nt, i, 4 * w + 3) * up;
+                    const uint32_t lo = half_pair(a, b), hi = half_pair(c, d);
                     put_query(nt, 0, 4 * i + w, lo, hi);
-                    if constexpr (SPLIT) put_query(nt, 1, 4 * i + w, half_pair_rest(a, bb, lo), half_pair_rest(c, d, hi));
+                    if constexpr (SPLIT) put_query(nt, 1, 4 * i + w, half_pair_rest(a, b, lo), half_pair_rest(c, d, hi));
                 }
             qmul[nt][0] = __shfl_sync(0xffffffffu, mul, 8 * j);
             qmul[nt][1] = __shfl_sync(0xffffffffu, mul, 8 * j + 4);
@@ -678,52 +743,54 @@ struct Attend {
         });
     }
     __device__ __forceinline__ void finish(const Cursor &at) const {
-        each([&](int head, int d, float4 o, float top, float sum_p) {
-            finish_head<T>(p, at.b, at.h, at.group * S::HEADS + head, d, o, top, sum_p);
-        });
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+                const int head = at.group * S::HEADS + nt * 8 + 2 * j + k;
+                if (head >= p.G) continue;
+                const float total = sum[nt][k], inv = total != 0.0f ? 1.0f / (total * vmul) : 0.0f;
+                T *to = static_cast<T *>(p.out) + at.b * p.o_ld + (at.h * (int64_t)p.G + head) * p.o_hs;
+#pragma unroll
+                for (int i = 0; i < S::STEPS; i += 2) {
+                    const int d = dim_of(i);
+                    const float v[4] = {acc[i][nt][k] * inv, acc[i][nt][k + 2] * inv, acc[i + 1][nt][k] * inv,
+                                        acc[i + 1][nt][k + 2] * inv};
+                    if (d < p.D) store_out<T>(p, to + d, v);
+                }
+                if (g == 0 && p.lse) p.lse[(at.b * (int64_t)p.Hk + at.h) * p.G + head] = lse_of(m[nt][k], total);
+            }
     }
 };
 
-// Sums n parts (part i at where(i)) for four dims of a head; BATCH parts' loads are
-// under way together.
-template <int DT, int NT, bool GLOBAL, typename Where>
-__device__ __forceinline__ void sum_parts(int n, Where where, int head, int d, float4 &o, float &top, float &total) {
+// Adds n parts of other blocks (part i at where(i)); eight parts' loads are under way
+// together.
+template <int DT, int NT, typename Where>
+__device__ __forceinline__ void sum_parts(Sum &sum, int n, Where where, int head, int d) {
     constexpr int BATCH = 8;
-    top = -1e30f;
-    o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-    total = 0.0f;
     for (int i0 = 0; i0 < n; i0 += BATCH) {
         float2 y[BATCH];
         float4 x[BATCH];
 #pragma unroll
         for (int i = 0; i < BATCH; ++i) {
             const float *from = where(min(i0 + i, n - 1));
-            const float2 *py = reinterpret_cast<const float2 *>(from + 8 * NT * DT + 2 * head);
-            const float4 *px = reinterpret_cast<const float4 *>(from + part_at<DT>(head, d));
-            if constexpr (GLOBAL) {         // other SMs wrote them
-                y[i] = __ldcg(py);
-                x[i] = __ldcg(px);
-            } else {
-                y[i] = *py;
-                x[i] = *px;
-            }
+            y[i] = __ldcg(reinterpret_cast<const float2 *>(from + 8 * NT * DT + 2 * head));
+            x[i] = __ldcg(reinterpret_cast<const float4 *>(from + part_at<DT>(head, d)));
         }
-        float to = top;
+        float to = sum.top;
 #pragma unroll
         for (int i = 0; i < BATCH; ++i) to = fmaxf(to, y[i].x);
-        const float f0 = exp2_fast(top - to);
-        top = to;
-        total *= f0;
-        o.x *= f0; o.y *= f0; o.z *= f0; o.w *= f0;
+        sum.rise(to);
 #pragma unroll
-        for (int i = 0; i < BATCH; ++i) {
-            const float f = i0 + i < n ? exp2_fast(y[i].x - top) : 0.0f;
-            if (i0 + i < n) {
-                total += y[i].y * f;
-                o.x += x[i].x * f; o.y += x[i].y * f; o.z += x[i].z * f; o.w += x[i].w * f;
-            }
-        }
+        for (int i = 0; i < BATCH; ++i)
+            if (i0 + i < n) sum.add(y[i], x[i]);
     }
+}
+
+template <int DT, int NT>
+__device__ __forceinline__ void put_part(float *part, int head, int d, const Sum &sum) {
+    *reinterpret_cast<float4 *>(part + part_at<DT>(head, d)) = sum.o;
+    if (d == 0) *reinterpret_cast<float2 *>(part + 8 * NT * DT + 2 * head) = make_float2(sum.top, sum.total);
 }
 
 // What a warp leaves of the key heads that it did not have alone.  head: the one it
@@ -731,17 +798,17 @@ __device__ __forceinline__ void sum_parts(int n, Where where, int head, int d, f
 struct Leftover {
     int has_head, has_tail, through;    // through: the tail was not begun here either
     struct Item {
-        int b, h, group, n;             // n: strips of the key head
-        int64_t at;                     // its place in the list
+        int b, h, group;
+        int n, at;                      // the key head's strips, and its place in the list
     } head, tail;
 };
-static_assert(sizeof(Leftover) <= 64, "fits the room that Shape::NOTES has");
 
 // A key head that another block has a part of too.
 struct Shared {
     Leftover::Item item;
     int first, count;                   // blocks first .. first + count - 1; count 0: none
 };
+static_assert(sizeof(Leftover) <= 72 && 2 * sizeof(Shared) + 12 <= 128, "they fit the room that Shape::NOTES has");
 
 // Counts this block in; true if it is the last of n.  One thread, behind a fence.
 __device__ __forceinline__ bool last_of(unsigned *ticket, int n) {
@@ -782,12 +849,11 @@ __device__ __forceinline__ void join(const AttendParams &p, const Shared *shared
         const int groups = (j.count + kJoin - 1) / kJoin;
         // block i's part: the first block's is its kind 1
         auto where = [&](int i) { return p.parts + ((int64_t)(j.first + i) * (S::WARPS + 2) + (i == 0 ? 1 : 0)) * S::PART; };
-        float4 o[MINE];
-        float2 y[MINE];
+        Sum sum[MINE];
 #pragma unroll
         for (int k = 0; k < MINE; ++k) {
             const int i = threadIdx.x + k * S::THREADS, head = i / (DT / 4), d = (i % (DT / 4)) * 4;
-            if (i < TASKS) sum_parts<DT, NT, true>(gn, [&](int q) { return where(g0 + q); }, head, d, o[k], y[k].x, y[k].y);
+            if (i < TASKS) sum_parts<DT, NT>(sum[k], gn, [&](int q) { return where(g0 + q); }, head, d);
         }
         if (groups > 1) {
             __syncthreads();    // every part has been read before the first one is written over
@@ -795,8 +861,7 @@ __device__ __forceinline__ void join(const AttendParams &p, const Shared *shared
             for (int k = 0; k < MINE; ++k) {
                 const int i = threadIdx.x + k * S::THREADS, head = i / (DT / 4), d = (i % (DT / 4)) * 4;
                 if (i >= TASKS) continue;
-                *reinterpret_cast<float4 *>(where(g0) + part_at<DT>(head, d)) = o[k];
-                if (d == 0) *reinterpret_cast<float2 *>(where(g0) + S::HEADS * DT + 2 * head) = y[k];
+                put_part<DT, NT>(where(g0), head, d, sum[k]);
             }
             __syncthreads();
             if (threadIdx.x == 0) {
@@ -809,14 +874,29 @@ __device__ __forceinline__ void join(const AttendParams &p, const Shared *shared
 #pragma unroll
             for (int k = 0; k < MINE; ++k) {
                 const int i = threadIdx.x + k * S::THREADS, head = i / (DT / 4), d = (i % (DT / 4)) * 4;
-                if (i < TASKS) sum_parts<DT, NT, true>(groups, [&](int q) { return where(q * kJoin); }, head, d, o[k], y[k].x, y[k].y);
+                sum[k] = Sum();
+                if (i < TASKS) sum_parts<DT, NT>(sum[k], groups, [&](int q) { return where(q * kJoin); }, head, d);
             }
         }
 #pragma unroll
         for (int k = 0; k < MINE; ++k) {
             const int i = threadIdx.x + k * S::THREADS, head = i / (DT / 4), d = (i % (DT / 4)) * 4;
-            if (i < TASKS) finish_head<T>(p, j.item.b, j.item.h, head0 + head, d, o[k], y[k].x, y[k].y);
+            if (i < TASKS) finish_head<T>(p, j.item.b, j.item.h, head0 + head, d, sum[k].o, sum[k].top, sum[k].total);
         }
+    }
+}
+
+// The results of sequences without tokens, and complaints about lengths.
+template <int THREADS, typename T>
+__device__ __forceinline__ void nothing(const AttendParams &p) {
+    for (int64_t b = blockIdx.x; b < p.B; b += gridDim.x) {
+        const int n = __ldg(p.lens + b);
+        if ((n < 0 || n > p.width * p.page) && threadIdx.x == 0) record_error(p.err, kErrBadIndex);
+        if (n > 0 && p.width > 0) continue;
+        for (int i = threadIdx.x; i < p.Hk * p.G * p.D; i += THREADS)
+            static_cast<T *>(p.out)[b * p.o_ld + (i / p.D) * p.o_hs + i % p.D] = from_f32<T>(0.0f);
+        if (p.lse)
+            for (int i = threadIdx.x; i < p.Hk * p.G; i += THREADS) p.lse[b * p.Hk * p.G + i] = -INFINITY;
     }
 }
 
@@ -827,103 +907,68 @@ attend_kernel(const __grid_constant__ AttendParams p) {
     extern __shared__ uint8_t raw[];
     uint8_t *smem = raw + ((128 - (smem_u32(raw) & 127)) & 127);
     Leftover *left = reinterpret_cast<Leftover *>(smem + S::WARPS * (S::STAGES * S::STAGE + S::QUERIES));   // of each warp
-    int64_t *bounds = reinterpret_cast<int64_t *>(left + S::WARPS);     // the block's strips, and the list's at sequence
-    Shared *shared = reinterpret_cast<Shared *>(bounds + 4);
+    int *sums = reinterpret_cast<int *>(left + S::WARPS);       // strips of each warp's run of sequences
+    Shared *shared = reinterpret_cast<Shared *>(sums + S::WARPS);
     int *note = reinterpret_cast<int *>(shared + 2);
     const int tid = threadIdx.x, warp = tid >> 5;
-    const int items = p.Hk * p.groups;
     auto parts = [&](int i) { return p.parts + ((int64_t)blockIdx.x * (S::WARPS + 2) + i) * S::PART; };
 
-    // Where the block's and its warps' strips begin.  A thread counts `per` consecutive
-    // sequences, whose strips are [before, before + count) of the list.
+    // The list's length, and where this warp's strips begin and end.
     Division div;
-    int64_t begin, end;
-    {
-        int64_t *sums = reinterpret_cast<int64_t *>(smem);      // of the warps
-        const int per = (p.B + S::THREADS - 1) / S::THREADS;
-        const int b0 = (int)min((int64_t)p.B, (int64_t)tid * per), b1 = min(p.B, b0 + per);
-        int64_t count = 0;
-        for (int b = b0; b < b1; ++b) {
-            count += span_of(p, b).strips;
-            if (blockIdx.x == 0) {
-                const int n = p.lens[b];
-                if (n < 0 || n > p.width * p.page) record_error(p.err, kErrBadIndex);
-            }
-        }
-        count *= items;
-        int64_t before = count;
+    Locator list;
+    list.sums = sums;
+    list.run = ((p.B + S::WARPS - 1) / S::WARPS + 31) & ~31;
+    if (p.B > 32) {
+        int count = 0;
+        const int b1 = min(p.B, (warp + 1) * list.run);
+        for (int b = warp * list.run + (tid & 31); b < b1; b += 32) count += span_of(p, tokens_of(p, b)).strips;
+        count *= p.Hk * p.groups;
 #pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const int64_t x = __shfl_up_sync(0xffffffffu, before, o);
-            if ((tid & 31) >= o) before += x;
-        }
-        if ((tid & 31) == 31) sums[warp] = before;
+        for (int o = 16; o > 0; o >>= 1) count += __shfl_xor_sync(0xffffffffu, count, o);
+        if ((tid & 31) == 0) sums[warp] = count;
         __syncthreads();
-        before -= count;
         div.total = 0;
-#pragma unroll
-        for (int w = 0; w < S::WARPS; ++w) {
-            if (w < warp) before += sums[w];
-            div.total += sums[w];
-        }
-        const int64_t most = (div.total + S::WARPS * kLeast - 1) / (S::WARPS * kLeast);
-        div.blocks = most < 1 ? 1 : most < (int64_t)gridDim.x ? (int)most : (int)gridDim.x;
-        if ((int)blockIdx.x < div.blocks && div.total > 0) {
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                const int c = (int)blockIdx.x + e;
-                const int64_t at = div.raw(c);
-                if (c == div.blocks) {
-                    if (tid == 0) bounds[e] = div.total;
-                } else if (at >= before && at < before + count) {
-                    int64_t off = at - before;
-                    int n = 0, b = b0;
-                    for (; b < b1; ++b) {
-                        n = span_of(p, b).strips;
-                        if (off < (int64_t)n * items) break;
-                        off -= (int64_t)n * items;
-                    }
-                    bounds[e] = Division::snapped(at, (int)(off - quotient(off, n) * n), n);
-                    if (e == 0) {       // the block's strips begin in this sequence or with the next
-                        bounds[2] = at - off;
-                        bounds[3] = b;
-                    }
-                }
-            }
-        } else if (tid == 0) {
-            bounds[0] = bounds[1] = 0;
-        }
-        // rows of sequences without tokens
-        for (int64_t b = blockIdx.x; b < p.B; b += gridDim.x) {
-            if (span_of(p, (int)b).strips > 0) continue;
-            for (int i = tid; i < p.Hk * p.G * p.D; i += S::THREADS)
-                static_cast<T *>(p.out)[b * p.o_ld + (i / p.D) * p.o_hs + i % p.D] = from_f32<T>(0.0f);
-            if (p.lse)
-                for (int i = tid; i < p.Hk * p.G; i += S::THREADS) p.lse[b * p.Hk * p.G + i] = -INFINITY;
-        }
-        __syncthreads();
-        begin = bounds[0];
-        end = bounds[1];
-        if (begin >= end) return;
+        for (int w = 0; w < S::WARPS; ++w) div.total += sums[w];
     }
+    list.load(p, 0, 0);
+    if (p.B <= 32) div.total = list.all();
+    div.blocks = min((int)gridDim.x, max(1, (div.total - 1) / (S::WARPS * kLeast) + 1));
+    nothing<S::THREADS, T>(p);
+    if ((int)blockIdx.x >= div.blocks || div.total == 0) return;
+    const int begin = div.start(p, list, blockIdx.x), end = div.start(p, list, blockIdx.x + 1);
+    if (begin >= end) return;
 
     Attend<DT, NT, T> a(p, smem_u32(smem));
-    int64_t at = begin + first_of<S::WARPS>(end - begin, warp);
-    int64_t todo = begin + first_of<S::WARPS>(end - begin, warp + 1) - at;
-    Cursor cur{};
-    if (todo > 0) cur.seek(p, (int)bounds[3], at - bounds[2]);
-    Leftover rest{};
+    Cursor cur;
+    int at, todo;
+    {
+        const Shares warps(end - begin, S::WARPS);
+        // a boundary between warps, unless it would divide a short key head
+        auto start = [&](int w) {
+            const int x = begin + warps.begin(w);
+            if (x >= end) return end;
+            cur = list.find(p, x);
+            return cur.span.strips > kWhole ? x : Division::moved(x, cur.strip, cur.span.strips);
+        };
+        const int upto = start(warp + 1);
+        at = start(warp);
+        todo = upto - at;
+        if (todo > 0 && cur.span.strips <= kWhole && cur.strip != 0) cur = list.find(p, at);
+    }
+    bool has_tail = false;
+    if (a.lane == 0) left[warp].has_head = left[warp].has_tail = left[warp].through = 0;
+    if (tid < 2) shared[tid].count = 0;
     a.next = cur;
     a.left = todo;
-    a.look_up();
-#pragma unroll
+    if (todo > 0) a.look_up();
+#pragma unroll 1
     for (int s = 0; s < S::STAGES - 1; ++s) a.load(s);
 
     int stage = 0, fill = S::STAGES - 1;
     while (todo > 0) {
         // the strips of one key head that are this warp's
         const int strips = cur.span.strips;
-        const int n = (int)(todo < strips - cur.strip ? todo : strips - cur.strip);
+        const int n = min(todo, strips - cur.strip);
         a.begin(cur);
         for (int i = 0; i < n; ++i) {
             cp_wait<S::STAGES - 2>();
@@ -937,34 +982,38 @@ attend_kernel(const __grid_constant__ AttendParams p) {
         const bool begun = cur.strip == 0, ended = cur.strip + n == strips;
         if (begun && ended) {
             a.finish(cur);
-        } else if (ended) {
-            a.store(parts(2 + warp));
-            rest.has_head = 1;
-            rest.head = {cur.b, cur.h, cur.group, strips, at - cur.strip};
         } else {
-            rest.has_tail = 1;
-            rest.through = !begun;
-            rest.tail = {cur.b, cur.h, cur.group, strips, at - cur.strip};
+            if (ended) a.store(parts(2 + warp));
+            if (a.lane == 0) {
+                const Leftover::Item item{cur.b, cur.h, cur.group, strips, at - cur.strip};
+                if (ended) {
+                    left[warp].has_head = 1;
+                    left[warp].head = item;
+                } else {
+                    left[warp].has_tail = 1;
+                    left[warp].through = !begun;
+                    left[warp].tail = item;
+                }
+            }
         }
         at += n;
         todo -= n;
         if (todo > 0) {
             cur.strip += n - 1;
             cur.step(p);
+        } else if (!ended) {
+            has_tail = true;
         }
     }
     cp_wait<0>();
     __syncwarp();
     auto ring_of = [&](int w) { return reinterpret_cast<float *>(smem + w * (S::STAGES * S::STAGE)); };
-    if (rest.has_tail) a.store(ring_of(warp));      // nothing is on its way into the ring any more
-    if (a.lane == 0) left[warp] = rest;
-    if (tid < 2) shared[tid].count = 0;
+    if (has_tail) a.store(ring_of(warp));       // nothing is on its way into the ring any more
     __syncthreads();
 
     // What warps share.  A run is a key head's parts in consecutive warps: tails, and
     // at its end the head part of the warp that ended it.
-    const int used = (int)min((int64_t)S::WARPS, end - begin);      // warps with strips: the first ones
-    const bool mine = a.lane < used;
+    const bool mine = a.lane < S::WARPS;
     const uint32_t heads = __ballot_sync(0xffffffffu, mine && left[a.lane].has_head);
     const uint32_t tails = __ballot_sync(0xffffffffu, mine && left[a.lane].has_tail);
     const uint32_t through = __ballot_sync(0xffffffffu, mine && left[a.lane].through);
@@ -978,26 +1027,38 @@ attend_kernel(const __grid_constant__ AttendParams p) {
         for (int k = from_before ? 1 : 0; k < run; ++k) open &= open - 1;
         const bool early = from_before && run == 0;
         const int w0 = early ? 0 : __ffs(open) - 1;
-        const uint32_t ends = heads >> w0 >> (early ? 0 : 1) << (early ? 0 : 1) << w0;     // behind the run's begin
-        const int w1 = ends ? __ffs(ends) - 1 : used - 1;
-        float4 o;
-        float top, total_p;
-        sum_parts<DT, NT, false>(w1 - w0 + 1, [&](int k) { return ends && w0 + k == w1 ? parts(2 + w1) : ring_of(w0 + k); },
-                                 head, d, o, top, total_p);
+        const uint32_t ends = heads & (early ? ~0u : ~((2u << w0) - 1));     // behind the run's begin
+        const int w1 = ends ? __ffs(ends) - 1 : 32 - __clz(tails);           // the tails are those of w0 to w1 - 1
+        Sum sum;
+        float4 x;
+        float2 y;
+        if (ends) {
+            const float *from = parts(2 + w1);
+            y = *reinterpret_cast<const float2 *>(from + S::HEADS * DT + 2 * head);
+            x = *reinterpret_cast<const float4 *>(from + part_at<DT>(head, d));
+        }
+#pragma unroll 4
+        for (int w = w0; w < w1; ++w) sum.top = fmaxf(sum.top, ring_of(w)[S::HEADS * DT + 2 * head]);
+        if (ends) sum.top = fmaxf(sum.top, y.x);
+#pragma unroll 4
+        for (int w = w0; w < w1; ++w) {
+            const float *from = ring_of(w);
+            sum.add(*reinterpret_cast<const float2 *>(from + S::HEADS * DT + 2 * head),
+                    *reinterpret_cast<const float4 *>(from + part_at<DT>(head, d)));
+        }
+        if (ends) sum.add(y, x);
         // an early run that its first warp ends is that one head part
         const Leftover::Item &item = early && left[w0].has_head ? left[w0].head : left[w0].tail;
         if (!early && ends) {
-            finish_head<T>(p, item.b, item.h, item.group * S::HEADS + head, d, o, top, total_p);
+            finish_head<T>(p, item.b, item.h, item.group * S::HEADS + head, d, sum.o, sum.top, sum.total);
         } else {
-            float *part = parts(early ? 0 : 1);
-            *reinterpret_cast<float4 *>(part + part_at<DT>(head, d)) = o;
-            if (d == 0) *reinterpret_cast<float2 *>(part + S::HEADS * DT + 2 * head) = make_float2(top, total_p);
+            put_part<DT, NT>(parts(early ? 0 : 1), head, d, sum);
             if (i % TASKS == 0) {
-                Shared x{item, 0, 0};
+                Shared with{item, 0, 0};
                 int last;
-                div.blocks_of(item.at, item.n, x.first, last);
-                x.count = last - x.first + 1;
-                shared[early ? 0 : 1] = x;
+                div.blocks_of(item.at, item.n, with.first, last);
+                with.count = last - with.first + 1;
+                shared[early ? 0 : 1] = with;
             }
         }
     }

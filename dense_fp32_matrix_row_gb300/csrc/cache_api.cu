@@ -1,5 +1,6 @@
 // cache_api.cu -- the attention operators of include/sgemm_gb300.h: argument checks,
 // quick returns, and the counters that a stream's attention calls share.
+#include <algorithm>
 #include <climits>
 #include <cmath>
 #include <cstdint>
@@ -341,6 +342,9 @@ int sgemm_q8_attend(int64_t B, int type, const sgemm_heads *q, const sgemm_q8_ca
     if (B < 0 || B > (1 << 30) || pages < 0 || pages > INT32_MAX / cache->page) return SGEMM_ERR_BAD_DIM;
     if (!known_type(type) || !std::isfinite(scale) || window < 0) return SGEMM_ERR_BAD_ARG;
     if (B == 0) return SGEMM_OK;
+    // the kernel counts all sequences' strips of 16 tokens in 32 bits
+    if (there(q) && q->heads > 0 && (pages * cache->page / 16 + 2) * std::min(q->heads, kMaxHeads) > INT32_MAX / B)
+        return SGEMM_ERR_TOO_LARGE;
     if (!there(q) || !there(out) || lens == nullptr || (table == nullptr && pages > 0)) return SGEMM_ERR_NULL_PTR;
     rc = check_heads(q, B, cache->dim, type, false);
     if (rc == SGEMM_OK) rc = check_heads(out, B, cache->dim, type, true);

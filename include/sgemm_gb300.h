@@ -70,7 +70,7 @@ extern "C" {
 #define SGEMM_ERR_DEVICE     -6   /* the current device is not an sm_103 GPU */
 #define SGEMM_ERR_TIMEOUT    -7   /* a device-side bounded wait ran out (from sgemm_status) */
 #define SGEMM_ERR_BAD_ARG    -8   /* any other invalid argument */
-#define SGEMM_ERR_TOO_LARGE  -9   /* beyond sgemm_noalloc's fixed scratch or a limit of sgemm_q8_moe */
+#define SGEMM_ERR_TOO_LARGE  -9   /* beyond sgemm_noalloc's fixed scratch or a limit of sgemm_q8_moe, sgemm_q8_attend */
 #define SGEMM_ERR_CAPTURE   -10   /* the stream is being captured and the call would allocate */
 #define SGEMM_ERR_BAD_INDEX -11   /* an index in device memory lies outside its array (from sgemm_status) */
 
@@ -462,6 +462,7 @@ int sgemm_q8_cache_read(int64_t N, int type, const sgemm_q8_cache *cache, const 
  *               that many (both reported).  Tokens of a page outside the cache
  *               are left out (reported).
  *   lse         B x q->heads floats (natural logarithms), or NULL
+ * B * q->heads * (pages*page/16 + 2) is below 2^31 (SGEMM_ERR_TOO_LARGE).
  * Several new tokens of a sequence are rows of their own, with a length each.
  * Scores, sums and results are FP32; the exponentials are rounded to 11 bits
  * for the product with the values (22 bits for type FP32; those below about

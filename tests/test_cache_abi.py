@@ -149,6 +149,8 @@ def test_read_refusals(fn):
 def test_attend_refusals(fn):
     assert attend(fn, B=-1) == attend(fn, B=(1 << 30) + 1) == attend(fn, pages=-1) == sg.ERR_BAD_DIM
     assert attend(fn, pages=1 << 28, ldt=1 << 28) == sg.ERR_BAD_DIM
+    # strips of 16 tokens are counted in 32 bits: 4 heads of 2^15 sequences of 2^18 tokens
+    assert attend(fn, B=1 << 15, pages=1 << 14, ldt=1 << 14) == sg.ERR_TOO_LARGE
     assert attend(fn, type_=2) == attend(fn, scale=NAN) == attend(fn, scale=INF) == attend(fn, window=-1) == sg.ERR_BAD_ARG
     for name in ("q", "out", "table", "lens", "c"):
         assert attend(fn, **{name: None}) == sg.ERR_NULL_PTR
