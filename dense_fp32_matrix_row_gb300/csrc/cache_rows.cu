@@ -36,14 +36,17 @@ struct RowsParams {
     bool interleaved;
     Heads q, q_out, k, k_out, v;
     const float *qw, *kw;
-    float eps;
+    float eps, over_dim;   // 1 / D
+    float least;           // sums of squares below it may have lost some
     const float *cos, *sin;
     int64_t rows, ldt;
     const int64_t *positions;
     const int64_t *slots;  // nullptr: no cache
     sgemm_q8_cache cache;
-    int q_units, k_units, units;      // per token: groups of U heads of queries, keys, values
-    int64_t first, count;             // units of this launch, over all tokens
+    // units: groups of U heads; per token, and of this launch over all its tokens
+    int q_units, k_units, float_units, cache_units;
+    int64_t first, float_count, cache_count;
+    int float_blocks;
     unsigned *err;
 };
 
@@ -60,256 +63,324 @@ __device__ __forceinline__ bool place(const sgemm_q8_cache &c, int64_t s, int64_
     return true;
 }
 
-// The elements of four pairs (a, b): both halves of a rotated head, or eight
-// neighbours.
-template <typename T, bool VEC>
-__device__ __forceinline__ void load_pairs(const T *p, int a0, int b0, bool neighbours, float (&a)[4], float (&b)[4]) {
-    if (neighbours) {
-        if constexpr (VEC) {
-            float u[4], w[4];
-            load_vec<T, 4>(p + a0, u);
-            load_vec<T, 4>(p + a0 + 4, w);
+// Four elements as they come from memory.
+template <typename T>
+struct Quad {
+    uint32_t w[sizeof(T)];
+    __device__ __forceinline__ void clear() {
 #pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                a[i] = u[2 * i]; b[i] = u[2 * i + 1];
-                a[i + 2] = w[2 * i]; b[i + 2] = w[2 * i + 1];
-            }
+        for (int i = 0; i < (int)sizeof(T); ++i) w[i] = 0;
+    }
+    __device__ __forceinline__ void load(const T *p) {
+        if constexpr (sizeof(T) == 4) {
+            const uint4 u = *reinterpret_cast<const uint4 *>(p);
+            w[0] = u.x; w[1] = u.y; w[2] = u.z; w[3] = u.w;
         } else {
-#pragma unroll
-            for (int i = 0; i < 4; ++i) { a[i] = to_f32<T>(p[a0 + 2 * i]); b[i] = to_f32<T>(p[a0 + 2 * i + 1]); }
+            const uint2 u = *reinterpret_cast<const uint2 *>(p);
+            w[0] = u.x; w[1] = u.y;
         }
-    } else if constexpr (VEC) {
-        load_vec<T, 4>(p + a0, a);
-        load_vec<T, 4>(p + b0, b);
-    } else {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) { a[i] = to_f32<T>(p[a0 + i]); b[i] = to_f32<T>(p[b0 + i]); }
     }
-}
-
-template <typename T, bool VEC>
-__device__ __forceinline__ void store_pairs(T *p, int a0, int b0, bool neighbours, const float (&a)[4],
-                                            const float (&b)[4]) {
-    if (neighbours) {
-        if constexpr (VEC) {
-            const float u[4] = {a[0], b[0], a[1], b[1]}, w[4] = {a[2], b[2], a[3], b[3]};
-            store_vec<T, 4>(p + a0, u);
-            store_vec<T, 4>(p + a0 + 4, w);
+    // From four places, one by one.
+    __device__ __forceinline__ void gather(const T *p, const int (&at)[4]) {
+        if constexpr (sizeof(T) == 4) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) w[i] = __float_as_uint(p[at[i]]);
         } else {
+            const unsigned short *h = reinterpret_cast<const unsigned short *>(p);
 #pragma unroll
-            for (int i = 0; i < 4; ++i) { p[a0 + 2 * i] = from_f32<T>(a[i]); p[a0 + 2 * i + 1] = from_f32<T>(b[i]); }
-        }
-    } else if constexpr (VEC) {
-        store_vec<T, 4>(p + a0, a);
-        store_vec<T, 4>(p + b0, b);
-    } else {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) { p[a0 + i] = from_f32<T>(a[i]); p[b0 + i] = from_f32<T>(b[i]); }
-    }
-}
-
-// The same as whole numbers (the cache's rows are 16-byte aligned; the halves of
-// a rotated part are 4-byte aligned where VEC says so).
-template <bool VEC>
-__device__ __forceinline__ void store_pairs_q(int8_t *p, int a0, int b0, bool neighbours, const RowQuant &rq,
-                                              const float (&a)[4], const float (&b)[4]) {
-    if (neighbours && VEC) {
-        const float u[8] = {a[0], b[0], a[1], b[1], a[2], b[2], a[3], b[3]};
-        store_q<8>(p + a0, rq, u);
-    } else if (VEC) {
-        store_q<4>(p + a0, rq, a);
-        store_q<4>(p + b0, rq, b);
-    } else {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            p[a0 + (neighbours ? 2 * i : i)] = (int8_t)rq(a[i]);
-            p[neighbours ? a0 + 2 * i + 1 : b0 + i] = (int8_t)rq(b[i]);
+            for (int i = 0; i < 2; ++i) w[i] = (uint32_t)h[at[2 * i]] | (uint32_t)h[at[2 * i + 1]] << 16;
         }
     }
+    // Elements 2i and 2i + 1.
+    __device__ __forceinline__ float2 pair(int i) const {
+        if constexpr (sizeof(T) == 4) return make_float2(__uint_as_float(w[2 * i]), __uint_as_float(w[2 * i + 1]));
+        else return make_float2(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xffff0000u));
+    }
+};
+
+// 1 / sqrt(mean square + eps) from a head's sum of squares: rsqrtf, good to 2 units in
+// the last place.
+__device__ __forceinline__ float norm_factor(float ss, float over_dim, float eps) { return rsqrtf(fmaf(ss, over_dim, eps)); }
+
+// x * c - y * s and y * c + x * s, each product and sum rounded by itself.  (Not two
+// elements at a time: such products came out fused with the sum, whatever their
+// form, which moved one whole number in a million.)
+__device__ __forceinline__ void rotate(float &x, float &y, float c, float s) {
+    const float px = x, py = y;
+    x = __fsub_rn(__fmul_rn(px, c), __fmul_rn(py, s));
+    y = __fadd_rn(__fmul_rn(py, c), __fmul_rn(px, s));
 }
 
-// LANES lanes to a head, U heads of one kind and token to a group.  Without VEC
-// a lane's pairs may straddle the end of the rotated part, and are taken one by
-// one (elem says where).
-template <typename T, bool VEC, int LANES, int U>
-__global__ void __launch_bounds__(kThreads) head_rows_kernel(const __grid_constant__ RowsParams a) {
+// LANES lanes to a head, U heads of one kind and token to a group.  A lane has two
+// quads of a head's elements.  INTER false: the first elements of four rotated
+// pairs, and the second ones; true: four pairs, one behind another.  Lanes behind
+// the rotated part have eight neighbours.  Without VEC the rotated part may end
+// within a quad, and elements are taken one by one.  CACHED: keys and values into
+// the cache; otherwise queries and keys to floats.
+template <typename T, bool VEC, bool INTER, bool CACHED, int LANES, int U>
+__device__ __forceinline__ void head_rows(const RowsParams &a, uint32_t idx, uint32_t count, int units, int first_units) {
+    constexpr uint32_t ALL = 0xffffffffu;
     const int lane = threadIdx.x % LANES;
-    const int64_t idx = (int64_t)blockIdx.x * (kThreads / LANES) + threadIdx.x / LANES;
-    const bool here = idx < a.count;
-    const uint32_t local = here ? (uint32_t)idx : 0u;
-    const uint32_t tok = local / (uint32_t)a.units;
+    const bool here = idx < count;
+    const uint32_t tok = here ? idx / (uint32_t)units : 0u;
     const int64_t t = a.first + tok;
-    int unit = (int)(local - tok * (uint32_t)a.units);
-    // which heads: queries, keys or values
-    const bool is_q = unit < a.q_units, is_k = !is_q && unit < a.q_units + a.k_units;
-    if (!is_q) unit -= is_k ? a.q_units : a.q_units + a.k_units;
-    const Heads in = is_q ? a.q : is_k ? a.k : a.v;
-    const float *weight = is_q ? a.qw : is_k ? a.kw : nullptr;
+    int unit = here ? (int)(idx - tok * (uint32_t)units) : 0;
+    // the first kind: queries, or keys for the cache; the second: keys, or values
+    const bool one = unit < first_units;
+    if (!one) unit -= first_units;
     const int h0 = unit * U;
     const bool active = here && 8 * lane < a.D;
 
-    // the lane's pairs
+    // the token's places, asked for first
+    int64_t pos = t, slot = -1;
+    if (a.pairs > 0 && a.positions && here) pos = a.positions[t];
+    if (CACHED && here) slot = a.slots[t];
+
+    // where the lane's elements are, and whether they are rotated
     const int p0 = 4 * lane;
-    const bool turned = (is_q || is_k) && a.pairs > 0;
-    const bool neighbours = !turned || a.interleaved || p0 >= a.pairs;
-    int ea[4], eb[4];
-    if constexpr (!VEC) {
+    const bool rotates = (one || !CACHED) && a.pairs > 0;
+    int at0[4], at1[4];         // VEC: the quads' first elements alone
+    bool turn[4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const bool nb = !turned || a.interleaved || p0 + i >= a.pairs;
-            ea[i] = nb ? 2 * (p0 + i) : p0 + i;
-            eb[i] = nb ? 2 * (p0 + i) + 1 : p0 + i + a.pairs;
+    for (int i = 0; i < 4; ++i) {
+        if (INTER || VEC) {
+            turn[i] = rotates && p0 + (VEC ? 0 : i) < a.pairs;
+            const bool halves = !INTER && turn[i];
+            at0[i] = (halves ? p0 : 2 * p0) + i;
+            at1[i] = (halves ? p0 + a.pairs : 2 * p0 + 4) + i;
+        } else {                // a pair of neighbours stands for a pair behind the rotated part
+            turn[i] = rotates && p0 + i < a.pairs;
+            at0[i] = turn[i] ? p0 + i : 2 * (p0 + i);
+            at1[i] = turn[i] ? p0 + i + a.pairs : 2 * (p0 + i) + 1;
         }
     }
-    const int a0 = neighbours ? 2 * p0 : p0, b0 = p0 + a.pairs;
 
-    float xa[U][4], xb[U][4];
+    const Heads &in = CACHED ? (one ? a.k : a.v) : (one ? a.q : a.k);
+    const int heads = min(in.n - h0, U);
+    Quad<T> x0[U], x1[U];
+    {
+        const T *src = in.at<T>(t, h0);
+        const int64_t hs = in.hs;
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-        const bool on = active && h0 + u < in.n;
-        if (on) {
-            const T *src = in.at<T>(t, h0 + u);
-            if constexpr (VEC) {
-                load_pairs<T, true>(src, a0, b0, neighbours, xa[u], xb[u]);
+        for (int u = 0; u < U; ++u) {
+            if (active && u < heads) {
+                if constexpr (VEC) {
+                    x0[u].load(src + u * hs + at0[0]);
+                    x1[u].load(src + u * hs + at1[0]);
+                } else {
+                    x0[u].gather(src + u * hs, at0);
+                    x1[u].gather(src + u * hs, at1);
+                }
             } else {
-#pragma unroll
-                for (int i = 0; i < 4; ++i) { xa[u][i] = to_f32<T>(src[ea[i]]); xb[u][i] = to_f32<T>(src[eb[i]]); }
+                x0[u].clear();
+                x1[u].clear();
             }
-        } else {
-#pragma unroll
-            for (int i = 0; i < 4; ++i) xa[u][i] = xb[u][i] = 0.0f;
         }
     }
-
-    // the token's place in the tables and in the cache
     bool fine = here;
-    int64_t pos = t;
-    if (a.pairs > 0) {
-        if (here && a.positions) pos = a.positions[t];
-        if ((uint64_t)pos >= (uint64_t)a.rows) {
-            if (here && lane == 0) record_error(a.err, kErrBadIndex);
-            fine = false;
-        }
+    if (a.pairs > 0 && (uint64_t)pos >= (uint64_t)a.rows) {
+        if (here && lane == 0) record_error(a.err, kErrBadIndex);
+        fine = false;
     }
-    float c[4], s[4];
-    if (turned && fine && active) {
-        const float *pc = a.cos + pos * a.ldt, *ps = a.sin + pos * a.ldt;
+    Quad<float> c, s;
+    if (rotates && fine && active) {
+        const float *pc = a.cos + pos * a.ldt + p0, *ps = a.sin + pos * a.ldt + p0;
         if constexpr (VEC) {
-            if (p0 < a.pairs) {
-                load_vec<float, 4>(pc + p0, c);
-                load_vec<float, 4>(ps + p0, s);
+            if (turn[0]) {
+                c.load(pc);
+                s.load(ps);
             }
         } else {
 #pragma unroll
             for (int i = 0; i < 4; ++i)
-                if (p0 + i < a.pairs) { c[i] = pc[p0 + i]; s[i] = ps[p0 + i]; }
+                if (turn[i]) { c.w[i] = __float_as_uint(pc[i]); s.w[i] = __float_as_uint(ps[i]); }
         }
     }
-    float wa[4], wb[4];
+    const float *weight = CACHED ? (one ? a.kw : nullptr) : (one ? a.qw : a.kw);
+    Quad<float> w0, w1;
     if (weight && active) {
         if constexpr (VEC) {
-            load_pairs<float, true>(weight, a0, b0, neighbours, wa, wb);
+            w0.load(weight + at0[0]);
+            w1.load(weight + at1[0]);
         } else {
-#pragma unroll
-            for (int i = 0; i < 4; ++i) { wa[i] = weight[ea[i]]; wb[i] = weight[eb[i]]; }
+            w0.gather(weight, at0);
+            w1.gather(weight, at1);
         }
     }
-    const bool cached = a.slots != nullptr && !is_q;
-    int64_t page = 0;
-    int row = 0;
-    bool stored = false;
-    if (cached && fine) {
-        const int64_t slot = a.slots[t];
-        stored = place(a.cache, slot, page, row);
-        if (!stored && slot >= 0 && lane == 0) record_error(a.err, kErrBadIndex);
+
+    // the norms' factors
+    float r[U];
+    bool lifted = false;
+    uint32_t huge = 0, tiny = 0;        // heads, a bit each
+#pragma unroll
+    for (int u = 0; u < U; ++u) r[u] = 1.0f;
+    if (__any_sync(ALL, weight != nullptr)) {
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            r[u] = 0.0f;
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                r[u] = fmaf(x0[u].pair(i).x, x0[u].pair(i).x, r[u]);
+                r[u] = fmaf(x0[u].pair(i).y, x0[u].pair(i).y, r[u]);
+                r[u] = fmaf(x1[u].pair(i).x, x1[u].pair(i).x, r[u]);
+                r[u] = fmaf(x1[u].pair(i).y, x1[u].pair(i).y, r[u]);
+            }
+        }
+#pragma unroll
+        for (int o = LANES / 2; o > 0; o >>= 1)
+#pragma unroll
+            for (int u = 0; u < U; ++u) r[u] += __shfl_xor_sync(ALL, r[u], o);
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            huge |= (uint32_t)(weight && r[u] > kLargest) << u;
+            tiny |= (uint32_t)(weight && r[u] < a.least) << u;
+            r[u] = weight ? norm_factor(r[u], a.over_dim, a.eps) : 1.0f;
+        }
+        lifted = __any_sync(ALL, huge | tiny);
+        if (lifted) {           // squares beyond FP32's range: rare
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                const float lift = huge >> u & 1 ? kTwoM100 : tiny >> u & 1 ? kTwo100 : 1.0f;
+                float s2 = 0.0f;
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    const float2 v0 = x0[u].pair(i), v1 = x1[u].pair(i);
+                    s2 = fmaf(v0.x * lift, v0.x * lift, s2);
+                    s2 = fmaf(v0.y * lift, v0.y * lift, s2);
+                    s2 = fmaf(v1.x * lift, v1.x * lift, s2);
+                    s2 = fmaf(v1.y * lift, v1.y * lift, s2);
+                }
+#pragma unroll
+                for (int o = LANES / 2; o > 0; o >>= 1) s2 += __shfl_xor_sync(ALL, s2, o);
+                if (lift != 1.0f) r[u] = norm_factor(s2, a.over_dim, a.eps * lift * lift);
+            }
+        }
     }
+
+    // where the results go
+    bool stored = active && fine;
+    int8_t *rows = nullptr;
+    float *scales = nullptr;
+    T *dst = nullptr;
+    if constexpr (CACHED) {
+        if (fine) {
+            int64_t page = 0;
+            int row = 0;
+            if (place(a.cache, slot, page, row)) {
+                const int64_t at = (int64_t)h0 * a.cache.page + row;
+                rows = (one ? a.cache.k + page * a.cache.k_stride : a.cache.v + page * a.cache.v_stride) + at * a.D;
+                scales = (one ? a.cache.k_scale + page * a.cache.k_scale_stride
+                              : a.cache.v_scale + page * a.cache.v_scale_stride) + at;
+            } else {
+                stored = false;
+                if (slot >= 0 && lane == 0) record_error(a.err, kErrBadIndex);
+            }
+        }
+    } else {
+        dst = (one ? a.q_out : a.k_out).at<T>(t, h0);
+    }
+    const int64_t step = CACHED ? a.cache.page * a.D : (one ? a.q_out : a.k_out).hs;
 
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-        float ss = 0.0f;
+        float2 f0[2], f1[2];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            f0[i] = x0[u].pair(i);
+            f1[i] = x1[u].pair(i);
+        }
         if (weight) {
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                ss = fmaf(xa[u][i], xa[u][i], ss);
-                ss = fmaf(xb[u][i], xb[u][i], ss);
+            for (int i = 0; i < 2; ++i) {
+                f0[i] = __fmul2_rn(f0[i], w0.pair(i));
+                f1[i] = __fmul2_rn(f1[i], w1.pair(i));
             }
         }
-        float pa[4], pb[4];
-        uint32_t mx = 0;
+        if constexpr (INTER) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            pa[i] = xa[u][i];
-            pb[i] = xb[u][i];
-            if (weight && active) {
-                pa[i] = __fmul_rn(pa[i], wa[i]);
-                pb[i] = __fmul_rn(pb[i], wb[i]);
+            for (int i = 0; i < 2; ++i) {
+                if (turn[i]) rotate(f0[i].x, f0[i].y, __uint_as_float(c.w[i]), __uint_as_float(s.w[i]));
+                if (turn[i + 2]) rotate(f1[i].x, f1[i].y, __uint_as_float(c.w[i + 2]), __uint_as_float(s.w[i + 2]));
             }
-            if (turned && active && p0 + i < a.pairs) {
-                const float x = pa[i], y = pb[i];
-                pa[i] = __fsub_rn(__fmul_rn(x, c[i]), __fmul_rn(y, s[i]));
-                pb[i] = __fadd_rn(__fmul_rn(y, c[i]), __fmul_rn(x, s[i]));
-            }
-            mx = max(mx, max(abs_bits(pa[i]), abs_bits(pb[i])));
-        }
+        } else if constexpr (VEC) {
+            if (turn[0]) {
 #pragma unroll
-        for (int o = LANES / 2; o > 0; o >>= 1) {
-            ss += __shfl_xor_sync(0xffffffffu, ss, o);
-            mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-        }
-        float r = 1.0f, lift = 1.0f;
-        if (weight) {
-            r = inv_rms(ss, a.D, a.eps);
-            lift = norm_lift(ss, a.D, a.eps, mx);
-        }
-        if (__any_sync(0xffffffffu, lift != 1.0f)) {   // squares beyond FP32's range: rare
-            float s2 = 0.0f;
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const float va = xa[u][i] * lift, vb = xb[u][i] * lift;
-                s2 = fmaf(va, va, s2);
-                s2 = fmaf(vb, vb, s2);
-            }
-#pragma unroll
-            for (int o = LANES / 2; o > 0; o >>= 1) s2 += __shfl_xor_sync(0xffffffffu, s2, o);
-            if (lift != 1.0f) r = inv_rms(s2, a.D, a.eps * lift * lift);
-        }
-        const int h = h0 + u;
-        if (!active || !fine || h >= in.n) continue;
-        if (cached) {
-            if (!stored) continue;
-            const RowQuant rq(mx);
-            const int64_t at = (int64_t)h * a.cache.page + row;
-            int8_t *dst = is_k ? a.cache.k + page * a.cache.k_stride : a.cache.v + page * a.cache.v_stride;
-            dst += at * a.D;
-            if constexpr (VEC) {
-                store_pairs_q<true>(dst, a0, b0, neighbours, rq, pa, pb);
-            } else {
-#pragma unroll
-                for (int i = 0; i < 4; ++i) { dst[ea[i]] = (int8_t)rq(pa[i]); dst[eb[i]] = (int8_t)rq(pb[i]); }
-            }
-            if (lane == 0) {
-                float *scale = is_k ? a.cache.k_scale + page * a.cache.k_scale_stride
-                                    : a.cache.v_scale + page * a.cache.v_scale_stride;
-                scale[at] = row_scale(rq, lift, r);
-            }
-        } else {
-            const Heads o = is_q ? a.q_out : a.k_out;
-            T *dst = o.at<T>(t, h);
-            if (weight) {
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    pa[i] = lift == 1.0f ? pa[i] * r : pa[i] * lift * r;
-                    pb[i] = lift == 1.0f ? pb[i] * r : pb[i] * lift * r;
+                for (int i = 0; i < 2; ++i) {
+                    rotate(f0[i].x, f1[i].x, c.pair(i).x, s.pair(i).x);
+                    rotate(f0[i].y, f1[i].y, c.pair(i).y, s.pair(i).y);
                 }
             }
-            if constexpr (VEC) {
-                store_pairs<T, true>(dst, a0, b0, neighbours, pa, pb);
-            } else {
+        } else {
 #pragma unroll
-                for (int i = 0; i < 4; ++i) { dst[ea[i]] = from_f32<T>(pa[i]); dst[eb[i]] = from_f32<T>(pb[i]); }
+            for (int i = 0; i < 2; ++i) {
+                if (turn[2 * i]) rotate(f0[i].x, f1[i].x, c.pair(i).x, s.pair(i).x);
+                if (turn[2 * i + 1]) rotate(f0[i].y, f1[i].y, c.pair(i).y, s.pair(i).y);
+            }
+        }
+        const float lift = !lifted ? 1.0f : huge >> u & 1 ? kTwoM100 : tiny >> u & 1 ? kTwo100 : 1.0f;
+        if constexpr (CACHED) {
+            uint32_t mx = 0;
+            if (active) {
+#pragma unroll
+                for (int i = 0; i < 2; ++i)
+                    mx = max(max(mx, max(abs_bits(f0[i].x), abs_bits(f0[i].y))), max(abs_bits(f1[i].x), abs_bits(f1[i].y)));
+            }
+#pragma unroll
+            for (int o = LANES / 2; o > 0; o >>= 1) mx = max(mx, __shfl_xor_sync(ALL, mx, o));
+            if (stored && u < heads) {
+                const RowQuant rq(mx);
+                const float v0[4] = {f0[0].x, f0[0].y, f0[1].x, f0[1].y};
+                const float v1[4] = {f1[0].x, f1[0].y, f1[1].x, f1[1].y};
+                int8_t *to = rows + u * step;
+                if constexpr (VEC) {
+                    store_q<4>(to + at0[0], rq, v0);
+                    store_q<4>(to + at1[0], rq, v1);
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) { to[at0[i]] = (int8_t)rq(v0[i]); to[at1[i]] = (int8_t)rq(v1[i]); }
+                }
+                if (lane == 0) scales[u * a.cache.page] = row_scale(rq, lift, r[u]);
+            }
+        } else {
+            if (lifted) {
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    f0[i] = __fmul2_rn(f0[i], make_float2(lift, lift));
+                    f1[i] = __fmul2_rn(f1[i], make_float2(lift, lift));
+                }
+            }
+            if (weight) {
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    f0[i] = __fmul2_rn(f0[i], make_float2(r[u], r[u]));
+                    f1[i] = __fmul2_rn(f1[i], make_float2(r[u], r[u]));
+                }
+            }
+            if (stored && u < heads) {
+                const float v0[4] = {f0[0].x, f0[0].y, f0[1].x, f0[1].y};
+                const float v1[4] = {f1[0].x, f1[0].y, f1[1].x, f1[1].y};
+                T *to = dst + u * step;
+                if constexpr (VEC) {
+                    store_vec<T, 4>(to + at0[0], v0);
+                    store_vec<T, 4>(to + at1[0], v1);
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) { to[at0[i]] = from_f32<T>(v0[i]); to[at1[i]] = from_f32<T>(v1[i]); }
+                }
             }
         }
     }
+}
+
+// The first float_blocks blocks write floats, the rest write the cache.
+template <typename T, bool VEC, bool INTER, int LANES, int U>
+__global__ void __launch_bounds__(kThreads, 4) head_rows_kernel(const __grid_constant__ RowsParams a) {
+    const uint32_t group = threadIdx.x / LANES, per = kThreads / LANES;
+    if (blockIdx.x < (unsigned)a.float_blocks)
+        head_rows<T, VEC, INTER, false, LANES, U>(a, blockIdx.x * per + group, (uint32_t)a.float_count, a.float_units, a.q_units);
+    else
+        head_rows<T, VEC, INTER, true, LANES, U>(a, (blockIdx.x - a.float_blocks) * per + group, (uint32_t)a.cache_count,
+                                                 a.cache_units, a.k_units);
 }
 
 struct ReadParams {
@@ -323,60 +394,85 @@ struct ReadParams {
     unsigned *err;
 };
 
-// LANES lanes to a row, 16 elements a lane; U heads of one token to a group.
-template <typename T, bool VEC, int LANES, int U>
+// Four bytes times sc, rounded once: a byte in the last bits of 2^23 makes 2^23 + itself.
+__device__ __forceinline__ void bytes_to_f32(uint32_t w, float sc, float *v) {
+    const uint32_t u = w ^ 0x80808080u;
+    const float2 back = make_float2(-8388736.0f, -8388736.0f), by = make_float2(sc, sc);
+#pragma unroll
+    for (int i = 0; i < 4; i += 2) {
+        float2 x = make_float2(__uint_as_float(__byte_perm(u, 0x4b000000u, 0x7440 + i)),
+                               __uint_as_float(__byte_perm(u, 0x4b000000u, 0x7441 + i)));
+        x = __fmul2_rn(__fadd2_rn(x, back), by);
+        v[i] = x.x;
+        v[i + 1] = x.y;
+    }
+}
+
+// LANES lanes to a row, 16 bytes of result a lane (IT times); U heads of one token to
+// a group.
+template <typename T, bool VEC, int LANES, int IT, int U>
 __global__ void __launch_bounds__(kThreads) cache_read_kernel(const __grid_constant__ ReadParams a) {
+    constexpr int V = 16 / (int)sizeof(T);
     const int lane = threadIdx.x % LANES;
-    const int64_t idx = (int64_t)blockIdx.x * (kThreads / LANES) + threadIdx.x / LANES;
-    if (idx >= a.count) return;
-    const uint32_t tok = (uint32_t)idx / (uint32_t)a.units;
-    const int64_t n = a.first + tok;
-    int unit = (int)((uint32_t)idx - tok * (uint32_t)a.units);
+    const uint32_t idx = blockIdx.x * (uint32_t)(kThreads / LANES) + threadIdx.x / LANES;
+    if (idx >= (uint32_t)a.count) return;
+    // 16 tokens, then the next heads of the same 16: a page's rows of one head lie together
+    const uint32_t tile = idx / 16 / (uint32_t)a.units;
+    const int64_t n = a.first + tile * 16 + idx % 16;
+    int unit = (int)(idx / 16 - tile * (uint32_t)a.units);
+    if (n >= a.N) return;
+    const int64_t slot = a.slots[n];
     const bool is_k = unit < a.k_units;
     if (!is_k) unit -= a.k_units;
-    const int64_t slot = a.slots[n];
     int64_t page;
     int row;
     if (!place(a.cache, slot, page, row)) {
         if (slot >= 0 && lane == 0) record_error(a.err, kErrBadIndex);
         return;
     }
-    if (16 * lane >= a.D) return;
     const int h0 = unit * U, heads = (int)a.cache.heads;
     const int8_t *src = (is_k ? a.cache.k + page * a.cache.k_stride : a.cache.v + page * a.cache.v_stride);
     const float *scales = is_k ? a.cache.k_scale + page * a.cache.k_scale_stride
                                : a.cache.v_scale + page * a.cache.v_scale_stride;
-    uint4 w[U];
+    uint32_t w[U][IT][V / 4];
     float sc[U];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-        if (h0 + u < heads) {
-            const int64_t at = (int64_t)(h0 + u) * a.cache.page + row;
-            w[u] = *reinterpret_cast<const uint4 *>(src + at * a.D + 16 * lane);
-            sc[u] = scales[at];
+        if (h0 + u >= heads) continue;
+        const int64_t at = (int64_t)(h0 + u) * a.cache.page + row;
+        sc[u] = scales[at];
+#pragma unroll
+        for (int i = 0; i < IT; ++i) {
+            const int e = (lane + i * LANES) * V;
+            if (e >= a.D) continue;
+            const int8_t *p = src + at * a.D + e;
+            if constexpr (V == 8) {
+                const uint2 x = *reinterpret_cast<const uint2 *>(p);
+                w[u][i][0] = x.x;
+                w[u][i][1] = x.y;
+            } else {
+                w[u][i][0] = *reinterpret_cast<const uint32_t *>(p);
+            }
         }
     }
     const Heads out = is_k ? a.k_out : a.v_out;
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-        if (h0 + u >= heads) break;
-        const uint32_t word[4] = {w[u].x, w[u].y, w[u].z, w[u].w};
-        float v[16];
+        if (h0 + u >= heads) continue;
+        T *dst = out.at<T>(n, h0 + u);
 #pragma unroll
-        for (int i = 0; i < 16; ++i) v[i] = (float)(int8_t)(word[i / 4] >> (8 * (i % 4))) * sc[u];
-        T *dst = out.at<T>(n, h0 + u) + 16 * lane;
-        if constexpr (VEC) {
-            constexpr int V = 16 / (int)sizeof(T);
+        for (int i = 0; i < IT; ++i) {
+            const int e = (lane + i * LANES) * V;
+            if (e >= a.D) continue;
+            float v[V];
 #pragma unroll
-            for (int i = 0; i < 16 / V; ++i) {
-                float part[V];
+            for (int k = 0; k < V / 4; ++k) bytes_to_f32(w[u][i][k], sc[u], v + 4 * k);
+            if constexpr (VEC) {
+                store_vec<T, V>(dst + e, v);
+            } else {
 #pragma unroll
-                for (int e = 0; e < V; ++e) part[e] = v[V * i + e];
-                store_vec<T, V>(dst + V * i, part);
+                for (int k = 0; k < V; ++k) dst[e + k] = from_f32<T>(v[k]);
             }
-        } else {
-#pragma unroll
-            for (int i = 0; i < 16; ++i) dst[i] = from_f32<T>(v[i]);
         }
     }
 }
@@ -393,76 +489,85 @@ bool aligned(const void *p, int bytes) { return reinterpret_cast<uintptr_t>(p) %
 // Tokens of one launch: its units are counted in 32 bits.
 constexpr int64_t kMostUnits = int64_t(1) << 30;
 
-template <typename T, bool VEC, int LANES, int U>
+template <typename T, bool VEC, bool INTER, int LANES, int U>
 cudaError_t rows_launch(RowsParams p, cudaStream_t stream) {
-    const int64_t step = kMostUnits / p.units;
+    const bool cached = p.slots != nullptr;
+    p.q_units = (p.q.n + U - 1) / U;
+    p.k_units = (p.k.n + U - 1) / U;
+    p.float_units = p.q_units + (cached ? 0 : p.k_units);
+    p.cache_units = cached ? 2 * p.k_units : 0;         // as many values as keys
+    const int64_t step = kMostUnits / (p.float_units > p.cache_units ? p.float_units : p.cache_units);
     for (int64_t t = 0; t < p.T; t += step) {
-        const int64_t n = p.T - t < step ? p.T - t : step;
+        const int64_t n = p.T - t < step ? p.T - t : step, per = kThreads / LANES;
         p.first = t;
-        p.count = n * p.units;
-        const int64_t per = kThreads / LANES;
-        head_rows_kernel<T, VEC, LANES, U><<<(unsigned)((p.count + per - 1) / per), kThreads, 0, stream>>>(p);
+        p.float_count = n * p.float_units;
+        p.cache_count = n * p.cache_units;
+        p.float_blocks = (int)((p.float_count + per - 1) / per);
+        const unsigned blocks = (unsigned)(p.float_blocks + (p.cache_count + per - 1) / per);
+        head_rows_kernel<T, VEC, INTER, LANES, U><<<blocks, kThreads, 0, stream>>>(p);
         const cudaError_t e = cudaGetLastError();
         if (e != cudaSuccess) return e;
     }
     return cudaSuccess;
 }
 
-template <typename T, bool VEC, int U>
+template <typename T, bool VEC, bool INTER, int U>
 cudaError_t rows_lanes(const RowsParams &p, cudaStream_t stream) {
-    if (p.D <= 64) return rows_launch<T, VEC, 8, U>(p, stream);
-    if (p.D <= 128) return rows_launch<T, VEC, 16, U>(p, stream);
-    return rows_launch<T, VEC, 32, U>(p, stream);
+    if (p.D <= 64) return rows_launch<T, VEC, INTER, 8, U>(p, stream);
+    if (p.D <= 128) return rows_launch<T, VEC, INTER, 16, U>(p, stream);
+    return rows_launch<T, VEC, INTER, 32, U>(p, stream);
 }
 
-template <typename T>
+template <typename T, bool INTER>
 cudaError_t rows_type(RowsParams p, cudaStream_t stream, int sm_count) {
     constexpr int es = sizeof(T), bytes = 4 * es;
     const bool vec = p.pairs % 4 == 0 && aligned(p.q, es, bytes) && aligned(p.k, es, bytes) && aligned(p.v, es, bytes) &&
                      aligned(p.q_out, es, bytes) && aligned(p.k_out, es, bytes) && aligned(p.cos, 16) &&
                      aligned(p.sin, 16) && p.ldt % 4 == 0 && aligned(p.qw, 16) && aligned(p.kw, 16);
-    auto split = [&](int u) {
-        p.q_units = (p.q.n + u - 1) / u;
-        p.k_units = (p.k.n + u - 1) / u;
-        p.units = p.q_units + p.k_units + (p.v.n + u - 1) / u;
-    };
-    if (!vec) {
-        split(1);
-        return rows_lanes<T, false, 1>(p, stream);
-    }
-    // Four heads to a group once single ones would fill every SM: a token's angles
-    // are then loaded once for four heads, and four heads' loads are under way together.
+    if (!vec) return rows_lanes<T, false, INTER, 1>(p, stream);
+    // Several heads to a group once single ones would fill every SM: a token's angles
+    // are then loaded once for them, and 32 bytes' loads of a lane are under way together.
     const int lanes = p.D <= 64 ? 8 : p.D <= 128 ? 16 : 32;
-    split(1);
-    if (p.T * p.units * lanes <= (int64_t)sm_count * 2048) return rows_lanes<T, true, 1>(p, stream);
-    split(4);
-    return rows_lanes<T, true, 4>(p, stream);
+    if (p.T * (p.q.n + p.k.n + p.v.n) * lanes <= (int64_t)sm_count * 2048) return rows_lanes<T, true, INTER, 1>(p, stream);
+    return rows_lanes<T, true, INTER, 8 / es>(p, stream);
 }
 
-template <typename T, bool VEC, int LANES, int U>
+template <typename T>
+cudaError_t rows_of(const RowsParams &p, cudaStream_t stream, int sm_count) {
+    return p.interleaved && p.pairs > 0 ? rows_type<T, true>(p, stream, sm_count) : rows_type<T, false>(p, stream, sm_count);
+}
+
+template <typename T, bool VEC, int LANES, int IT, int U>
 cudaError_t read_launch(ReadParams p, cudaStream_t stream) {
     const int per_kind = ((int)p.cache.heads + U - 1) / U;
     p.k_units = p.k_out.n > 0 ? per_kind : 0;
     p.units = p.k_units + (p.v_out.n > 0 ? per_kind : 0);
-    const int64_t step = kMostUnits / p.units;
+    const int64_t step = kMostUnits / p.units / 16 * 16;
     for (int64_t t = 0; t < p.N; t += step) {
         const int64_t n = p.N - t < step ? p.N - t : step;
         p.first = t;
-        p.count = n * p.units;
+        p.count = (n + 15) / 16 * 16 * p.units;
         const int64_t per = kThreads / LANES;
-        cache_read_kernel<T, VEC, LANES, U><<<(unsigned)((p.count + per - 1) / per), kThreads, 0, stream>>>(p);
+        cache_read_kernel<T, VEC, LANES, IT, U><<<(unsigned)((p.count + per - 1) / per), kThreads, 0, stream>>>(p);
         const cudaError_t e = cudaGetLastError();
         if (e != cudaSuccess) return e;
     }
     return cudaSuccess;
 }
 
+template <typename T, bool VEC>
+cudaError_t read_lanes(const ReadParams &p, cudaStream_t stream) {
+    const int chunks = p.D * (int)sizeof(T) / 16;
+    if (chunks <= 8) return read_launch<T, VEC, 4, 2, 2>(p, stream);
+    if (chunks <= 16) return read_launch<T, VEC, 8, 2, 2>(p, stream);
+    if (chunks <= 32) return read_launch<T, VEC, 16, 2, 2>(p, stream);
+    return read_launch<T, VEC, 32, 2, 2>(p, stream);
+}
+
 template <typename T>
 cudaError_t read_type(const ReadParams &p, cudaStream_t stream) {
     const bool vec = aligned(p.k_out, sizeof(T), 16) && aligned(p.v_out, sizeof(T), 16);
-    if (p.D <= 64) return vec ? read_launch<T, true, 4, 2>(p, stream) : read_launch<T, false, 4, 1>(p, stream);
-    if (p.D <= 128) return vec ? read_launch<T, true, 8, 2>(p, stream) : read_launch<T, false, 8, 1>(p, stream);
-    return vec ? read_launch<T, true, 16, 2>(p, stream) : read_launch<T, false, 16, 1>(p, stream);
+    return vec ? read_lanes<T, true>(p, stream) : read_lanes<T, false>(p, stream);
 }
 
 }  // namespace
@@ -477,12 +582,14 @@ cudaError_t launch_head_rows(const HeadRowsArgs &a) {
     p.k = heads_of(a.k); p.k_out = heads_of(a.k_out);
     p.v = heads_of(a.v);
     p.qw = a.q_weight; p.kw = a.k_weight; p.eps = a.eps;
+    p.over_dim = 1.0f / (float)a.D;
+    p.least = a.eps < kTwoM100 ? kTwoM100 * (float)a.D : 0.0f;      // see norm_lift
     p.cos = a.rotary.cos; p.sin = a.rotary.sin;
     p.rows = a.rotary.rows; p.ldt = a.rotary.ld; p.positions = a.rotary.positions;
     p.slots = a.slots; p.cache = a.cache;
     p.err = a.err;
-    return a.type == kTypeBf16 ? rows_type<__nv_bfloat16>(p, a.stream, a.sm_count)
-                               : rows_type<float>(p, a.stream, a.sm_count);
+    return a.type == kTypeBf16 ? rows_of<__nv_bfloat16>(p, a.stream, a.sm_count)
+                               : rows_of<float>(p, a.stream, a.sm_count);
 }
 
 cudaError_t launch_cache_read(const CacheReadArgs &a) {
