@@ -34,8 +34,11 @@ namespace sgemm_gb300 {
 constexpr int kStrip = 16;                 // tokens
 constexpr int kJoin = 48;                  // blocks' parts summed at a time
 // A block boundary within so many strips of a key head's first or last strip moves
-// there: joining blocks costs about as long as reading twice as many.
-constexpr int kSnap = 16;
+// there: joining blocks costs about as long as reading twice as many.  So does one
+// anywhere in a key head of at most kFew strips or, where there is too little work
+// for all SMs, kUnshared (half as many of FP32, whose strips take twice as long): a
+// block takes those alone in about the time that joining would add.
+constexpr int kSnap = 16, kFew = 48, kUnshared = 96;
 constexpr int kLeast = 2;                  // strips to a warp, before work goes to another block
 // A key head of at most so many strips is one warp's: summing two warps' parts costs
 // about as long as four strips.
@@ -284,7 +287,10 @@ struct Locator {
 // The list's division: block c begins at the c-th even share, unless that is within
 // kSnap strips of a key head's begin or end.
 struct Division {
-    int total, blocks;
+    int total, blocks, unshared;
+    __device__ __forceinline__ Division(int strips, int per_block, int terms)
+        : total(strips), blocks(min((int)gridDim.x, max(1, (strips - 1) / per_block + 1))),
+          unshared((blocks < (int)gridDim.x ? kUnshared : kFew) / terms) {}
     // A boundary at `at`, off strips into a key head of n strips, moved to its nearer end.
     static __device__ __forceinline__ int moved(int at, int off, int n) { return 2 * off < n ? at - off : at + (n - off); }
     __device__ __forceinline__ int start(const AttendParams &p, Locator &list, int c) const {
@@ -293,14 +299,14 @@ struct Division {
         const int at = Shares(total, blocks).begin(c);
         const Cursor x = list.find(p, at);
         const int off = x.strip, n = x.span.strips;
-        return off > kSnap && n - off > kSnap ? at : moved(at, off, n);
+        return n > unshared && off > kSnap && n - off > kSnap ? at : moved(at, off, n);
     }
     // Of a key head at [at, at + n): the blocks first..last that share it, by the
     // boundaries that lie within it.  first >= last: one block alone.
     __device__ __forceinline__ void blocks_of(int at, int n, int &first, int &last) const {
         const Shares s(total, blocks);
         first = s.behind(at + kSnap) - 1;
-        last = n > kSnap ? s.behind(at + n - kSnap - 1) - 1 : first;
+        last = n > unshared ? s.behind(at + n - kSnap - 1) - 1 : first;
     }
 };
 
@@ -808,7 +814,7 @@ struct Shared {
     Leftover::Item item;
     int first, count;                   // blocks first .. first + count - 1; count 0: none
 };
-static_assert(sizeof(Leftover) <= 72 && 2 * sizeof(Shared) + 12 <= 128, "they fit the room that Shape::NOTES has");
+static_assert(sizeof(Leftover) <= 72 && 2 * sizeof(Shared) + 72 <= 128, "they fit the room that Shape::NOTES has");
 
 // Counts this block in; true if it is the last of n.  One thread, behind a fence.
 __device__ __forceinline__ bool last_of(unsigned *ticket, int n) {
@@ -914,8 +920,8 @@ attend_kernel(const __grid_constant__ AttendParams p) {
     auto parts = [&](int i) { return p.parts + ((int64_t)blockIdx.x * (S::WARPS + 2) + i) * S::PART; };
 
     // The list's length, and where this warp's strips begin and end.
-    Division div;
     Locator list;
+    int total = 0;
     list.sums = sums;
     list.run = ((p.B + S::WARPS - 1) / S::WARPS + 31) & ~31;
     if (p.B > 32) {
@@ -927,34 +933,44 @@ attend_kernel(const __grid_constant__ AttendParams p) {
         for (int o = 16; o > 0; o >>= 1) count += __shfl_xor_sync(0xffffffffu, count, o);
         if ((tid & 31) == 0) sums[warp] = count;
         __syncthreads();
-        div.total = 0;
-        for (int w = 0; w < S::WARPS; ++w) div.total += sums[w];
+        for (int w = 0; w < S::WARPS; ++w) total += sums[w];
     }
     list.load(p, 0, 0);
-    if (p.B <= 32) div.total = list.all();
-    div.blocks = min((int)gridDim.x, max(1, (div.total - 1) / (S::WARPS * kLeast) + 1));
+    if (p.B <= 32) total = list.all();
+    const Division div(total, S::WARPS * kLeast, Attend<DT, NT, T>::TERMS);
     nothing<S::THREADS, T>(p);
-    if ((int)blockIdx.x >= div.blocks || div.total == 0) return;
-    const int begin = div.start(p, list, blockIdx.x), end = div.start(p, list, blockIdx.x + 1);
+    if ((int)blockIdx.x >= div.blocks || total == 0) return;
+    int *bounds = note, *starts = note + 2;     // of the block, of its warps
+    if (warp < 2) {
+        const int x = div.start(p, list, blockIdx.x + warp);
+        if ((tid & 31) == 0) bounds[warp] = x;
+    }
+    __syncthreads();
+    const int begin = bounds[0], end = bounds[1];
     if (begin >= end) return;
 
     Attend<DT, NT, T> a(p, smem_u32(smem));
+    // This warp's even share of the block's strips, but for a begin that would divide a
+    // short key head.
     Cursor cur;
-    int at, todo;
-    {
-        const Shares warps(end - begin, S::WARPS);
-        // a boundary between warps, unless it would divide a short key head
-        auto start = [&](int w) {
-            const int x = begin + warps.begin(w);
-            if (x >= end) return end;
-            cur = list.find(p, x);
-            return cur.span.strips > kWhole ? x : Division::moved(x, cur.strip, cur.span.strips);
-        };
-        const int upto = start(warp + 1);
-        at = start(warp);
-        todo = upto - at;
-        if (todo > 0 && cur.span.strips <= kWhole && cur.strip != 0) cur = list.find(p, at);
+    int at = begin + Shares(end - begin, S::WARPS).begin(warp);
+    if (at < end) {
+        cur = list.find(p, at);
+        const int n = cur.span.strips;
+        if (n <= kWhole && cur.strip > 0) {
+            const int to = Division::moved(at, cur.strip, n);
+            if (to < at) {
+                cur.strip = 0;
+            } else if (to < end) {
+                cur.strip = n - 1;
+                cur.step(p);
+            }
+            at = to;
+        }
     }
+    if (a.lane == 0) starts[warp] = at;
+    __syncthreads();
+    int todo = (warp + 1 < S::WARPS ? starts[warp + 1] : end) - at;
     bool has_tail = false;
     if (a.lane == 0) left[warp].has_head = left[warp].has_tail = left[warp].through = 0;
     if (tid < 2) shared[tid].count = 0;
@@ -1037,14 +1053,17 @@ attend_kernel(const __grid_constant__ AttendParams p) {
             y = *reinterpret_cast<const float2 *>(from + S::HEADS * DT + 2 * head);
             x = *reinterpret_cast<const float4 *>(from + part_at<DT>(head, d));
         }
-#pragma unroll 4
-        for (int w = w0; w < w1; ++w) sum.top = fmaxf(sum.top, ring_of(w)[S::HEADS * DT + 2 * head]);
+        const uint32_t rings = smem_u32(smem), at_m = 4 * (S::HEADS * DT + 2 * head), at_o = 4 * part_at<DT>(head, d);
+#pragma unroll 8
+        for (int w = w0; w < w1; ++w) sum.top = fmaxf(sum.top, __uint_as_float(lds4(rings + w * (S::STAGES * S::STAGE) + at_m)));
         if (ends) sum.top = fmaxf(sum.top, y.x);
 #pragma unroll 4
         for (int w = w0; w < w1; ++w) {
-            const float *from = ring_of(w);
-            sum.add(*reinterpret_cast<const float2 *>(from + S::HEADS * DT + 2 * head),
-                    *reinterpret_cast<const float4 *>(from + part_at<DT>(head, d)));
+            const uint32_t from = rings + w * (S::STAGES * S::STAGE);
+            const uint2 m = lds8(from + at_m);
+            const uint4 o = lds16(from + at_o);
+            sum.add(make_float2(__uint_as_float(m.x), __uint_as_float(m.y)),
+                    make_float4(__uint_as_float(o.x), __uint_as_float(o.y), __uint_as_float(o.z), __uint_as_float(o.w)));
         }
         if (ends) sum.add(y, x);
         // an early run that its first warp ends is that one head part
