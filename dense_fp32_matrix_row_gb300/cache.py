@@ -33,10 +33,24 @@ q8._SIGNATURES.update({
 })
 
 
+_Tensor = None      # and the types below: set by the first call, like q8.torch
+
+
+def _load():
+    global _Tensor, _F32, _I32, _I64, _FLOATS, _TYPES
+    if q8.torch is None:
+        q8._load()
+    t = q8.torch
+    _F32, _I32, _I64, _FLOATS, _TYPES = t.float32, t.int32, t.int64, q8._FLOATS, q8._TYPES
+    _Tensor = t.Tensor
+
+
+# The helpers take a call's eight or ten tensors apart in the time that its launch
+# leaves: each asks a tensor only for what it needs, at 0.1 us an answer.
+
 def _heads(t, name, dtype, shape, index):
     """Checks heads of this type and shape on CUDA device `index`; their sgemm_heads."""
-    torch = q8.torch
-    if not isinstance(t, torch.Tensor):
+    if not isinstance(t, _Tensor):
         raise TypeError(f"{name} must be a torch tensor")
     if t.dtype is not dtype:
         raise TypeError(f"{name} must be of type {dtype}, not {t.dtype}")
@@ -45,7 +59,7 @@ def _heads(t, name, dtype, shape, index):
     T, H, D = shape
     if T == 0 or H == 0:
         return _HEADS(0, 0, 0, 0)
-    if index < 0 or t.get_device() != index:
+    if t.get_device() != index or index < 0:
         raise TypeError(f"{name} must live on the same CUDA device as the output")
     ld, hs, ds = t.stride()
     if ds != 1 and D > 1:
@@ -57,33 +71,40 @@ def _heads(t, name, dtype, shape, index):
     return _HEADS(t.data_ptr(), H, ld, hs)
 
 
-def _vector(t, name, dtype, n, index):
-    """Checks a contiguous vector (None: NULL); its address."""
-    if t is None:
-        return None
-    q8._packed(t, name, dtype, (n,), index)
+def _vector(t, name, dtype, shape, index):
+    """Checks a contiguous array of this shape; its address."""
+    if not (isinstance(t, _Tensor) and t.dtype is dtype and t.shape == shape and t.get_device() == index >= 0
+            and t.is_contiguous()):
+        q8._packed(t, name, dtype, shape, index)        # says what is wrong (or lets an empty one pass)
     return t.data_ptr()
 
 
 def _shape3(t, name):
-    if not isinstance(t, q8.torch.Tensor):
+    if not isinstance(t, _Tensor):
         raise TypeError(f"{name} must be a torch tensor")
-    if t.dim() != 3:
+    shape = t.shape
+    if len(shape) != 3:
         raise ValueError(f"{name} must be 3-D (tokens, heads, dim)")
-    return t.shape
+    return shape
+
+
+def _type(t, name):
+    dtype = t.dtype
+    if dtype not in _FLOATS:
+        raise TypeError(f"{name} must be of type float32 or bfloat16, not {dtype}")
+    return dtype
 
 
 def _rotary(cos, sin, positions, interleaved, T, index):
     """The tables' sgemm_rotary (None without them)."""
-    torch = q8.torch
     if cos is None and sin is None:
         return None
     shape = q8._shape2(cos, "cos")
-    ld = q8._matrix(cos, "cos", (torch.float32,), shape, index)
-    if q8._matrix(sin, "sin", (torch.float32,), shape, index) != ld:
+    ld = q8._matrix(cos, "cos", (_F32,), shape, index)
+    if q8._matrix(sin, "sin", (_F32,), shape, index) != ld:
         raise ValueError("cos and sin must have the same row stride")
-    return _ROTARY(cos.data_ptr(), sin.data_ptr(), shape[0], ld, 2 * shape[1],
-                   _vector(positions, "positions", torch.int64, T, index) or 0, 1 if interleaved else 0)
+    at = 0 if positions is None else _vector(positions, "positions", _I64, (T,), index)
+    return _ROTARY(cos.data_ptr(), sin.data_ptr(), shape[0], ld, 2 * shape[1], at, 1 if interleaved else 0)
 
 
 class CacheQ8:
@@ -98,8 +119,8 @@ class CacheQ8:
     __slots__ = ("k", "v", "k_scale", "v_scale", "heads", "page", "dim", "slots", "_device", "_c", "_at")
 
     def __init__(self, k, v, k_scale, v_scale):
-        if q8.torch is None:
-            q8._load()
+        if _Tensor is None:
+            _load()
         torch = q8.torch
         for t, name in ((k, "k"), (v, "v"), (k_scale, "k_scale"), (v_scale, "v_scale")):
             if not isinstance(t, torch.Tensor):
@@ -133,7 +154,9 @@ class CacheQ8:
 
     def _struct(self):
         """The sgemm_q8_cache; made again if a tensor was given another storage."""
-        if (self.k.data_ptr(), self.v.data_ptr(), self.k_scale.data_ptr(), self.v_scale.data_ptr()) != self._at:
+        at = self._at
+        if (self.k.data_ptr() != at[0] or self.v.data_ptr() != at[1] or self.k_scale.data_ptr() != at[2]
+                or self.v_scale.data_ptr() != at[3]):
             self._check()
         return self._c
 
@@ -156,27 +179,27 @@ def norm_rope(q, k, cos, sin, q_out, k_out, positions=None, q_weight=None, k_wei
     ``positions``; both None: no rotation.  Pairs are (i, i + R/2), or (2i, 2i+1)
     with ``interleaved``.  ``q_weight`` and ``k_weight`` (D; float32): None: no norm.
     A token whose position is outside the tables is left out."""
-    if q8.torch is None:
-        q8._load()
+    if _Tensor is None:
+        _load()
     if q is None and k is None:
         raise ValueError("norm_rope needs q or k")
     lead, result, name = (q, q_out, "q") if q is not None else (k, k_out, "k")
-    shape, dev, dt = _shape3(lead, name), q8._index(result, name + "_out"), lead.dtype
-    if dt not in q8._FLOATS:
-        raise TypeError(f"{name} must be of type float32 or bfloat16, not {dt}")
+    shape, dev, dt = _shape3(lead, name), q8._index(result, name + "_out"), _type(lead, name)
     T, _, D = shape
     cq = cqo = ck = cko = pq = pk = None
     if q is not None:
         cq, cqo = _heads(q, "q", dt, shape, dev), _heads(q_out, "q_out", dt, shape, dev)
-        pq = _vector(q_weight, "q_weight", q8.torch.float32, D, dev)
+        if q_weight is not None:
+            pq = _vector(q_weight, "q_weight", _F32, (D,), dev)
     if k is not None:
         kshape = _shape3(k, "k")
         if kshape[0] != T or kshape[2] != D:
             raise ValueError(f"k must have shape ({T}, heads, {D}), not {tuple(kshape)}")
         ck, cko = _heads(k, "k", dt, kshape, dev), _heads(k_out, "k_out", dt, kshape, dev)
-        pk = _vector(k_weight, "k_weight", q8.torch.float32, D, dev)
+        if k_weight is not None:
+            pk = _vector(k_weight, "k_weight", _F32, (D,), dev)
     rotary = _rotary(cos, sin, positions, interleaved, T, dev)
-    q8._launch(dev, "sgemm_norm_rope", T, D, q8._TYPES[dt], cq, cqo, pq, ck, cko, pk, eps, rotary,
+    q8._launch(dev, "sgemm_norm_rope", T, D, _TYPES[dt], cq, cqo, pq, ck, cko, pk, eps, rotary,
                q8._stream(stream, dev))
 
 
@@ -195,28 +218,26 @@ def norm_rope_write_q8(q, k, v, cos, sin, q_out, cache, slots, positions=None, q
     attention.  The keys are not rounded to ``k``'s type on their way into 8 bits.
     ``q`` and ``q_out`` may be None; the other arguments are those of ``norm_rope``
     and ``cache_write_q8``."""
-    if q8.torch is None:
-        q8._load()
+    if _Tensor is None:
+        _load()
     c = _cache(cache)
-    shape, dev, dt = _shape3(k, "k"), cache._device, k.dtype
-    if dt not in q8._FLOATS:
-        raise TypeError(f"k must be of type float32 or bfloat16, not {dt}")
+    shape, dev, dt = _shape3(k, "k"), cache._device, _type(k, "k")
     T = shape[0]
     want = (T, cache.heads, cache.dim)
     ck, cv = _heads(k, "k", dt, want, dev), _heads(v, "v", dt, want, dev)
-    at = _vector(slots, "slots", q8.torch.int64, T, dev)
-    if at is None:
-        raise TypeError("slots must be a torch tensor of type torch.int64")
-    cq = cqo = pq = None
+    at = _vector(slots, "slots", _I64, (T,), dev)
+    cq = cqo = pq = pk = None
     if q is not None:
         qshape = _shape3(q, "q")
         if qshape[0] != T or qshape[2] != cache.dim:
             raise ValueError(f"q must have shape ({T}, heads, {cache.dim}), not {tuple(qshape)}")
         cq, cqo = _heads(q, "q", dt, qshape, dev), _heads(q_out, "q_out", dt, qshape, dev)
-        pq = _vector(q_weight, "q_weight", q8.torch.float32, cache.dim, dev)
-    pk = _vector(k_weight, "k_weight", q8.torch.float32, cache.dim, dev)
+        if q_weight is not None:
+            pq = _vector(q_weight, "q_weight", _F32, (cache.dim,), dev)
+    if k_weight is not None:
+        pk = _vector(k_weight, "k_weight", _F32, (cache.dim,), dev)
     rotary = _rotary(cos, sin, positions, interleaved, T, dev)
-    q8._launch(dev, "sgemm_q8_norm_rope_write", T, q8._TYPES[dt], cq, cqo, pq, ck, pk, cv, eps, rotary, at, c,
+    q8._launch(dev, "sgemm_q8_norm_rope_write", T, _TYPES[dt], cq, cqo, pq, ck, pk, cv, eps, rotary, at, c,
                q8._stream(stream, dev))
 
 
@@ -224,22 +245,20 @@ def cache_read_q8(cache, slots, k_out=None, v_out=None, stream=None) -> None:
     """The rows at ``slots`` (N; int64) as floats, whole number * scale, into ``k_out``
     and ``v_out`` (N, heads, dim; float32 or bfloat16 alike; either may be None).  A
     row whose slot is negative stays as it was."""
-    if q8.torch is None:
-        q8._load()
+    if _Tensor is None:
+        _load()
     c = _cache(cache)
     lead = k_out if k_out is not None else v_out
     if lead is None:
         raise ValueError("cache_read_q8 needs k_out or v_out")
-    dev, dt, N = q8._index(lead, "k_out" if k_out is not None else "v_out"), lead.dtype, _shape3(lead, "the output")[0]
-    if dt not in q8._FLOATS:
-        raise TypeError(f"the outputs must be of type float32 or bfloat16, not {dt}")
+    N, dev, dt = _shape3(lead, "the output")[0], lead.get_device(), _type(lead, "the output")
     want = (N, cache.heads, cache.dim)
     if N and cache._device != dev:
         raise TypeError("the cache must live on the same CUDA device as the output")
     ck = None if k_out is None else _heads(k_out, "k_out", dt, want, dev)
     cv = None if v_out is None else _heads(v_out, "v_out", dt, want, dev)
-    at = _vector(slots, "slots", q8.torch.int64, N, dev)
-    q8._launch(dev, "sgemm_q8_cache_read", N, q8._TYPES[dt], c, at, ck, cv, q8._stream(stream, dev))
+    at = _vector(slots, "slots", _I64, (N,), dev)
+    q8._launch(dev, "sgemm_q8_cache_read", N, _TYPES[dt], c, at, ck, cv, q8._stream(stream, dev))
 
 
 def attend_q8(q, cache, table, lens, out, scale=None, window: int = 0, lse=None, stream=None) -> None:
@@ -252,13 +271,10 @@ def attend_q8(q, cache, table, lens, out, scale=None, window: int = 0, lse=None,
     (B, pages) and ``lens`` (B) are int32.  ``window`` > 0: only the last ``window``
     tokens.  ``scale`` defaults to 1 / sqrt(dim).  ``lse`` (B, heads; float32) takes the
     logarithm of the sum of exp(scores).  A sequence of length 0 gives zeros and -inf."""
-    if q8.torch is None:
-        q8._load()
-    torch = q8.torch
+    if _Tensor is None:
+        _load()
     c = _cache(cache)
-    dev, shape, dt = q8._index(out, "out"), _shape3(q, "q"), q.dtype
-    if dt not in q8._FLOATS:
-        raise TypeError(f"q must be of type float32 or bfloat16, not {dt}")
+    shape, dev, dt = _shape3(q, "q"), q8._index(out, "out"), _type(q, "q")
     B, H, D = shape
     if D != cache.dim or H % cache.heads != 0 or H == 0:
         raise ValueError(f"q must have shape (sequences, a multiple of {cache.heads} heads, {cache.dim}), not {tuple(shape)}")
@@ -268,10 +284,9 @@ def attend_q8(q, cache, table, lens, out, scale=None, window: int = 0, lse=None,
     tshape = q8._shape2(table, "table")
     if tshape[0] != B:
         raise ValueError(f"table must have shape ({B}, pages), not {tuple(tshape)}")
-    ldt = q8._matrix(table, "table", (torch.int32,), tshape, dev)
-    pl = _vector(lens, "lens", torch.int32, B, dev)
-    if lse is not None:
-        q8._packed(lse, "lse", torch.float32, (B, H), dev)
-    q8._launch(dev, "sgemm_q8_attend", B, q8._TYPES[dt], cq, c, table.data_ptr(), ldt, tshape[1], pl,
-               1.0 / math.sqrt(D) if scale is None else scale, window, co, None if lse is None else lse.data_ptr(),
+    ldt = q8._matrix(table, "table", (_I32,), tshape, dev)
+    pl = _vector(lens, "lens", _I32, (B,), dev)
+    ps = None if lse is None else _vector(lse, "lse", _F32, (B, H), dev)
+    q8._launch(dev, "sgemm_q8_attend", B, _TYPES[dt], cq, c, table.data_ptr(), ldt, tshape[1], pl,
+               1.0 / math.sqrt(D) if scale is None else scale, window, co, ps,
                q8._stream(stream, dev))

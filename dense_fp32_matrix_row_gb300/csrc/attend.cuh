@@ -27,6 +27,8 @@
 // then by the last of the blocks that share it, always in the same order.
 #pragma once
 
+#include <atomic>
+
 #include "cache.cuh"
 
 namespace sgemm_gb300 {
@@ -513,9 +515,8 @@ struct Attend {
                 for (int e = 0; e < 16; ++e) most = fmaxf(most, fabsf(value(nt, i, e)));
             most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, 1));
             most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, 2));
-            const int e = min(exponent(most), 127);
-            const float up = pow2(min(14 - e, 127));
-            const float mul = __fdividef(p.scale_log2, up);     // exact: a power of two
+            const int k = min(14 - min(exponent(most), 127), 126);
+            const float up = pow2(k), mul = p.scale_log2 * pow2(-k);
 #pragma unroll
             for (int i = 0; i < S::CH / 4; ++i)
 #pragma unroll
@@ -1089,9 +1090,16 @@ attend_kernel(const __grid_constant__ AttendParams p) {
 template <int DT, int NT, typename T>
 cudaError_t attend_launch(const AttendParams &p, int sms, cudaStream_t stream) {
     using S = typename Attend<DT, NT, T>::S;
-    const cudaError_t e =
-        cudaFuncSetAttribute(attend_kernel<DT, NT, T>, cudaFuncAttributeMaxDynamicSharedMemorySize, S::SMEM);
+    static std::atomic<uint64_t> allowed{0};        // a bit for each device that has been told
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
+    const uint64_t bit = dev < 64 ? uint64_t(1) << dev : 0;
+    if ((allowed.load(std::memory_order_relaxed) & bit) == 0) {
+        e = cudaFuncSetAttribute(attend_kernel<DT, NT, T>, cudaFuncAttributeMaxDynamicSharedMemorySize, S::SMEM);
+        if (e != cudaSuccess) return e;
+        allowed.fetch_or(bit, std::memory_order_relaxed);
+    }
     attend_kernel<DT, NT, T><<<sms, S::THREADS, S::SMEM, stream>>>(p);
     return cudaGetLastError();
 }

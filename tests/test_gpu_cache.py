@@ -370,7 +370,7 @@ def test_read(D, page, dt):
 # ---- attention --------------------------------------------------------------------------
 
 def check_attend(lens, Hk, G, D, page, dt, window=0, scale=None, q_scale=2.0, pad=0, lead=0, offset=0, seed=0, pool=None,
-                 table=None, q=None, width=None, by_head=False):
+                 table=None, q=None, width=None, by_head=False, heads=None):
     torch.manual_seed(seed)
     B = len(lens)
     if pool is None:
@@ -385,12 +385,14 @@ def check_attend(lens, Hk, G, D, page, dt, window=0, scale=None, q_scale=2.0, pa
     assert sg.status() == sg.OK
     scale = D ** -0.5 if scale is None else scale
     want, tol, want_lse, lse_tol = ref.attend(q.view, pool, table, lens, scale, window, dt == "bf16")
-    close(out.view, want, tol, dt)
-    close(lse, want_lse, lse_tol, "fp32")
+    if heads is None:
+        heads = list(range(Hk * G))
+    close(out.view[:, heads], want[:, heads], tol[:, heads], dt)
+    close(lse[:, heads], want_lse[:, heads], lse_tol[:, heads], "fp32")
     assert out.intact() and q.intact()
     again = torch.empty_like(out.view)
     sg.attend_q8(q.view, cache, table, ln, again, scale=scale, window=window)
-    assert torch.equal(again, out.view), "the same call gives other bits"
+    assert torch.equal(again[:, heads], out.view[:, heads]), "the same call gives other bits"
     return out.view
 
 
@@ -467,10 +469,24 @@ def test_attend_strides(lead, offset, by_head, dt):
 
 
 @pytest.mark.parametrize("dt", ["fp32", "bf16"])
-@pytest.mark.parametrize("scale,q_scale", [(1.0, 1.0), (0.0, 2.0), (-0.3, 1.0), (1e-20, 1e10), (1e-3, 3e4), (1e20, 1e-21)])
+@pytest.mark.parametrize("scale,q_scale", [(1.0, 1.0), (0.0, 2.0), (-0.3, 1.0), (1e-20, 1e10), (1e-3, 3e4), (1e20, 1e-21),
+                                           (1e36, 1e-36), (1e-37, 3e36)])
 def test_attend_scales(scale, q_scale, dt):
     """Sharp, flat and turned distributions; queries far outside FP16's range."""
     check_attend([200, 33], 2, 4, 64, 16, dt, scale=scale, q_scale=q_scale)
+
+
+@pytest.mark.parametrize("dt", ["fp32", "bf16"])
+def test_attend_queries_of_unequal_size(dt):
+    """Each head's queries are scaled by themselves; small elements beside large ones."""
+    q = np.random.default_rng(2).standard_normal((2, 12, 64)).astype(np.float32)
+    q *= (10.0 ** np.arange(-30, 30, 5))[None, :, None].astype(np.float32)
+    q[:, :, ::2] *= np.float32(1e-4)
+    pool = ref.Pool(20, 3, 16, 64)
+    table, _ = pool.table([150, 40])
+    for h in range(12):          # one head's scale at a time
+        check_attend([150, 40], 3, 4, 64, 16, dt, pool=pool, table=table, q=q, scale=float(10.0 ** (29 - 5 * h)),
+                     heads=[h])
 
 
 @pytest.mark.parametrize("dt", ["fp32", "bf16"])
@@ -589,6 +605,28 @@ def test_offsets_past_32_bits():
     sg.attend_q8(q, cache, torch.tensor([[last]], dtype=torch.int32, device="cuda"), n, got)
     sg.attend_q8(q, small, torch.tensor([[0]], dtype=torch.int32, device="cuda"), n, want)
     assert sg.status() == sg.OK and torch.equal(got, want)
+
+
+def test_more_tokens_than_a_launch_takes():
+    """2^29 and some tokens without a slot (2^30 groups of heads fill a launch), a few
+    with one behind them."""
+    T, few = (1 << 29) + 77, 5
+    pool = ref.Pool(2, 1, 8, 16)
+    x = torch.randn((1, 1, 16), device="cuda").bfloat16()
+    slots = torch.full((T,), -1, dtype=torch.int64, device="cuda")
+    slots[-few:] = torch.arange(few, device="cuda")
+    sg.cache_write_q8(x.expand(T, 1, 16), x.expand(T, 1, 16), pool.cache(), slots)
+    want = ref.Pool(2, 1, 8, 16)
+    sg.cache_write_q8(x.expand(few, 1, 16).contiguous(), x.expand(few, 1, 16), want.cache(), slots[-few:].contiguous())
+    assert sg.status() == sg.OK
+    for n in ("k", "v", "k_scale", "v_scale"):
+        assert torch.equal(getattr(pool, n), getattr(want, n))
+    out = torch.zeros((T, 1, 16), dtype=torch.bfloat16, device="cuda")
+    sg.cache_read_q8(pool.cache(), slots, out, None)
+    less = torch.empty((few, 1, 16), dtype=torch.bfloat16, device="cuda")
+    sg.cache_read_q8(pool.cache(), slots[-few:].contiguous(), less, None)
+    assert sg.status() == sg.OK
+    assert torch.equal(out[-few:], less) and float(out[:-few].abs().max()) == 0
 
 
 # ---- together, streams, graphs, threads ---------------------------------------------------
