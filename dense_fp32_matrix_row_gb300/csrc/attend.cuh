@@ -921,6 +921,8 @@ attend_kernel(const __grid_constant__ AttendParams p) {
     auto parts = [&](int i) { return p.parts + ((int64_t)blockIdx.x * (S::WARPS + 2) + i) * S::PART; };
 
     // The list's length, and where this warp's strips begin and end.
+    pdl_wait();
+    pdl_trigger();
     Locator list;
     int total = 0;
     list.sums = sums;
@@ -1100,8 +1102,7 @@ cudaError_t attend_launch(const AttendParams &p, int sms, cudaStream_t stream) {
         if (e != cudaSuccess) return e;
         allowed.fetch_or(bit, std::memory_order_relaxed);
     }
-    attend_kernel<DT, NT, T><<<sms, S::THREADS, S::SMEM, stream>>>(p);
-    return cudaGetLastError();
+    return launch_dependent(attend_kernel<DT, NT, T>, sms, S::THREADS, S::SMEM, stream, p);
 }
 
 template <int DT>

@@ -58,6 +58,25 @@ cudaError_t launch_head_rows(const HeadRowsArgs &a);
 cudaError_t launch_cache_read(const CacheReadArgs &a);
 // Bytes of partial results that a call may write.
 size_t attend_workspace_bytes(const AttendArgs &a);
+#ifdef __CUDACC__
+// Launches `kernel` as a programmatic dependent of the work before it: its blocks may
+// be set up while that finishes, and wait (pdl_wait) before they touch memory.
+template <typename Params>
+cudaError_t launch_dependent(void (*kernel)(Params), unsigned blocks, unsigned threads, size_t smem, cudaStream_t stream,
+                             const Params &params) {
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(blocks);
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cudaLaunchAttribute at{};
+    at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at.val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = &at;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, params);
+}
+#endif
 // `tickets`: kAttendTickets words that are zero, and zero again once the call has run.
 constexpr int kAttendTickets = 4096;
 cudaError_t launch_attend(const AttendArgs &a, void *workspace, unsigned *tickets);

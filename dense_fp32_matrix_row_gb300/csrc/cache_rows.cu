@@ -375,6 +375,8 @@ __device__ __forceinline__ void head_rows(const RowsParams &a, uint32_t idx, uin
 // The first float_blocks blocks write floats, the rest write the cache.
 template <typename T, bool VEC, bool INTER, int LANES, int U>
 __global__ void __launch_bounds__(kThreads, 4) head_rows_kernel(const __grid_constant__ RowsParams a) {
+    pdl_wait();
+    pdl_trigger();
     const uint32_t group = threadIdx.x / LANES, per = kThreads / LANES;
     if (blockIdx.x < (unsigned)a.float_blocks)
         head_rows<T, VEC, INTER, false, LANES, U>(a, blockIdx.x * per + group, (uint32_t)a.float_count, a.float_units, a.q_units);
@@ -413,6 +415,8 @@ __device__ __forceinline__ void bytes_to_f32(uint32_t w, float sc, float *v) {
 template <typename T, bool VEC, int LANES, int IT, int U>
 __global__ void __launch_bounds__(kThreads) cache_read_kernel(const __grid_constant__ ReadParams a) {
     constexpr int V = 16 / (int)sizeof(T);
+    pdl_wait();
+    pdl_trigger();
     const int lane = threadIdx.x % LANES;
     const uint32_t idx = blockIdx.x * (uint32_t)(kThreads / LANES) + threadIdx.x / LANES;
     if (idx >= (uint32_t)a.count) return;
@@ -504,8 +508,7 @@ cudaError_t rows_launch(RowsParams p, cudaStream_t stream) {
         p.cache_count = n * p.cache_units;
         p.float_blocks = (int)((p.float_count + per - 1) / per);
         const unsigned blocks = (unsigned)(p.float_blocks + (p.cache_count + per - 1) / per);
-        head_rows_kernel<T, VEC, INTER, LANES, U><<<blocks, kThreads, 0, stream>>>(p);
-        const cudaError_t e = cudaGetLastError();
+        const cudaError_t e = launch_dependent(head_rows_kernel<T, VEC, INTER, LANES, U>, blocks, kThreads, 0, stream, p);
         if (e != cudaSuccess) return e;
     }
     return cudaSuccess;
@@ -548,8 +551,8 @@ cudaError_t read_launch(ReadParams p, cudaStream_t stream) {
         p.first = t;
         p.count = (n + 15) / 16 * 16 * p.units;
         const int64_t per = kThreads / LANES;
-        cache_read_kernel<T, VEC, LANES, IT, U><<<(unsigned)((p.count + per - 1) / per), kThreads, 0, stream>>>(p);
-        const cudaError_t e = cudaGetLastError();
+        const cudaError_t e = launch_dependent(cache_read_kernel<T, VEC, LANES, IT, U>, (unsigned)((p.count + per - 1) / per),
+                                               kThreads, 0, stream, p);
         if (e != cudaSuccess) return e;
     }
     return cudaSuccess;
