@@ -19,7 +19,7 @@
 namespace sgemm_gb300 {
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 128;     // 256: 3% longer, 512: 8%
 
 // Element (t, h, d) at p[t*ld + h*hs + d].
 struct Heads {
@@ -374,7 +374,7 @@ __device__ __forceinline__ void head_rows(const RowsParams &a, uint32_t idx, uin
 
 // The first float_blocks blocks write floats, the rest write the cache.
 template <typename T, bool VEC, bool INTER, int LANES, int U>
-__global__ void __launch_bounds__(kThreads, 4) head_rows_kernel(const __grid_constant__ RowsParams a) {
+__global__ void __launch_bounds__(kThreads, 8) head_rows_kernel(const __grid_constant__ RowsParams a) {
     pdl_wait();
     pdl_trigger();
     const uint32_t group = threadIdx.x / LANES, per = kThreads / LANES;
