@@ -102,6 +102,11 @@ struct Quad {
 // the last place.
 __device__ __forceinline__ float norm_factor(float ss, float over_dim, float eps) { return rsqrtf(fmaf(ss, over_dim, eps)); }
 
+// What a head's squares are lifted by, with its bit in `huge` or `tiny`.
+__device__ __forceinline__ float lift_of(uint32_t huge, uint32_t tiny, int u) {
+    return huge >> u & 1 ? kTwoM100 : tiny >> u & 1 ? kTwo100 : 1.0f;
+}
+
 // x * c - y * s and y * c + x * s, each product and sum rounded by itself.  (Not two
 // elements at a time: such products came out fused with the sum, whatever their
 // form, which moved one whole number in a million.)
@@ -115,9 +120,11 @@ __device__ __forceinline__ void rotate(float &x, float &y, float c, float s) {
 // quads of a head's elements.  INTER false: the first elements of four rotated
 // pairs, and the second ones; true: four pairs, one behind another.  Lanes behind
 // the rotated part have eight neighbours.  Without VEC the rotated part may end
-// within a quad, and elements are taken one by one.  CACHED: keys and values into
-// the cache; otherwise queries and keys to floats.
-template <typename T, bool VEC, bool INTER, bool CACHED, int LANES, int U>
+// within a quad, and elements are taken one by one.  FULL: no lane is without
+// elements, and heads that are not there are loaded as the last one, rather than
+// asked for one by one.  CACHED: keys and values into the cache; otherwise queries
+// and keys to floats.
+template <typename T, bool VEC, bool FULL, bool INTER, bool CACHED, int LANES, int U>
 __device__ __forceinline__ void head_rows(const RowsParams &a, uint32_t idx, uint32_t count, int units, int first_units) {
     constexpr uint32_t ALL = 0xffffffffu;
     const int lane = threadIdx.x % LANES;
@@ -129,7 +136,7 @@ __device__ __forceinline__ void head_rows(const RowsParams &a, uint32_t idx, uin
     const bool one = unit < first_units;
     if (!one) unit -= first_units;
     const int h0 = unit * U;
-    const bool active = here && 8 * lane < a.D;
+    const bool active = FULL || (here && 8 * lane < a.D);
 
     // the token's places, asked for first
     int64_t pos = t, slot = -1;
@@ -156,14 +163,18 @@ __device__ __forceinline__ void head_rows(const RowsParams &a, uint32_t idx, uin
     }
 
     const Heads &in = CACHED ? (one ? a.k : a.v) : (one ? a.q : a.k);
-    const int heads = min(in.n - h0, U);
+    const int heads = here ? min(in.n - h0, U) : 0;
     Quad<T> x0[U], x1[U];
     {
         const T *src = in.at<T>(t, h0);
         const int64_t hs = in.hs;
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-            if (active && u < heads) {
+            if constexpr (FULL) {
+                const T *from = src + min(u, max(heads - 1, 0)) * hs;
+                x0[u].load(from + at0[0]);
+                x1[u].load(from + at1[0]);
+            } else if (active && u < heads) {
                 if constexpr (VEC) {
                     x0[u].load(src + u * hs + at0[0]);
                     x1[u].load(src + u * hs + at1[0]);
@@ -211,9 +222,7 @@ __device__ __forceinline__ void head_rows(const RowsParams &a, uint32_t idx, uin
     // the norms' factors
     float r[U];
     bool lifted = false;
-    uint32_t huge = 0, tiny = 0;        // heads, a bit each
-#pragma unroll
-    for (int u = 0; u < U; ++u) r[u] = 1.0f;
+    uint32_t huge = 0, tiny = 0;        // of `lifted`: heads, a bit each
     if (__any_sync(ALL, weight != nullptr)) {
 #pragma unroll
         for (int u = 0; u < U; ++u) {
@@ -230,17 +239,16 @@ __device__ __forceinline__ void head_rows(const RowsParams &a, uint32_t idx, uin
         for (int o = LANES / 2; o > 0; o >>= 1)
 #pragma unroll
             for (int u = 0; u < U; ++u) r[u] += __shfl_xor_sync(ALL, r[u], o);
+        bool odd = false;
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-            huge |= (uint32_t)(weight && r[u] > kLargest) << u;
-            tiny |= (uint32_t)(weight && r[u] < a.least) << u;
-            r[u] = weight ? norm_factor(r[u], a.over_dim, a.eps) : 1.0f;
-        }
-        lifted = __any_sync(ALL, huge | tiny);
+        for (int u = 0; u < U; ++u) odd |= r[u] > kLargest || r[u] < a.least;
+        lifted = __any_sync(ALL, odd && weight != nullptr);
         if (lifted) {           // squares beyond FP32's range: rare
 #pragma unroll
             for (int u = 0; u < U; ++u) {
-                const float lift = huge >> u & 1 ? kTwoM100 : tiny >> u & 1 ? kTwo100 : 1.0f;
+                huge |= (uint32_t)(weight && r[u] > kLargest) << u;
+                tiny |= (uint32_t)(weight && r[u] < a.least) << u;
+                const float lift = lift_of(huge, tiny, u);
                 float s2 = 0.0f;
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
@@ -252,8 +260,11 @@ __device__ __forceinline__ void head_rows(const RowsParams &a, uint32_t idx, uin
                 }
 #pragma unroll
                 for (int o = LANES / 2; o > 0; o >>= 1) s2 += __shfl_xor_sync(ALL, s2, o);
-                if (lift != 1.0f) r[u] = norm_factor(s2, a.over_dim, a.eps * lift * lift);
+                r[u] = norm_factor(s2, a.over_dim, a.eps * lift * lift);
             }
+        } else {
+#pragma unroll
+            for (int u = 0; u < U; ++u) r[u] = norm_factor(r[u], a.over_dim, a.eps);
         }
     }
 
@@ -317,7 +328,6 @@ __device__ __forceinline__ void head_rows(const RowsParams &a, uint32_t idx, uin
                 if (turn[2 * i + 1]) rotate(f0[i].y, f1[i].y, c.pair(i).y, s.pair(i).y);
             }
         }
-        const float lift = !lifted ? 1.0f : huge >> u & 1 ? kTwoM100 : tiny >> u & 1 ? kTwo100 : 1.0f;
         if constexpr (CACHED) {
             uint32_t mx = 0;
             if (active) {
@@ -339,12 +349,13 @@ __device__ __forceinline__ void head_rows(const RowsParams &a, uint32_t idx, uin
 #pragma unroll
                     for (int i = 0; i < 4; ++i) { to[at0[i]] = (int8_t)rq(v0[i]); to[at1[i]] = (int8_t)rq(v1[i]); }
                 }
-                if (lane == 0) scales[u * a.cache.page] = row_scale(rq, lift, r[u]);
+                if (lane == 0) scales[u * a.cache.page] = row_scale(rq, lifted ? lift_of(huge, tiny, u) : 1.0f, weight ? r[u] : 1.0f);
             }
         } else {
             if (lifted) {
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
+                    const float lift = lift_of(huge, tiny, u);
                     f0[i] = __fmul2_rn(f0[i], make_float2(lift, lift));
                     f1[i] = __fmul2_rn(f1[i], make_float2(lift, lift));
                 }
@@ -373,16 +384,16 @@ __device__ __forceinline__ void head_rows(const RowsParams &a, uint32_t idx, uin
 }
 
 // The first float_blocks blocks write floats, the rest write the cache.
-template <typename T, bool VEC, bool INTER, int LANES, int U>
+template <typename T, bool VEC, bool FULL, bool INTER, int LANES, int U>
 __global__ void __launch_bounds__(kThreads, 8) head_rows_kernel(const __grid_constant__ RowsParams a) {
     pdl_wait();
     pdl_trigger();
     const uint32_t group = threadIdx.x / LANES, per = kThreads / LANES;
     if (blockIdx.x < (unsigned)a.float_blocks)
-        head_rows<T, VEC, INTER, false, LANES, U>(a, blockIdx.x * per + group, (uint32_t)a.float_count, a.float_units, a.q_units);
+        head_rows<T, VEC, FULL, INTER, false, LANES, U>(a, blockIdx.x * per + group, (uint32_t)a.float_count, a.float_units, a.q_units);
     else
-        head_rows<T, VEC, INTER, true, LANES, U>(a, (blockIdx.x - a.float_blocks) * per + group, (uint32_t)a.cache_count,
-                                                 a.cache_units, a.k_units);
+        head_rows<T, VEC, FULL, INTER, true, LANES, U>(a, (blockIdx.x - a.float_blocks) * per + group, (uint32_t)a.cache_count,
+                                                       a.cache_units, a.k_units);
 }
 
 struct ReadParams {
@@ -493,7 +504,7 @@ bool aligned(const void *p, int bytes) { return reinterpret_cast<uintptr_t>(p) %
 // Tokens of one launch: its units are counted in 32 bits.
 constexpr int64_t kMostUnits = int64_t(1) << 30;
 
-template <typename T, bool VEC, bool INTER, int LANES, int U>
+template <typename T, bool VEC, bool FULL, bool INTER, int LANES, int U>
 cudaError_t rows_launch(RowsParams p, cudaStream_t stream) {
     const bool cached = p.slots != nullptr;
     p.q_units = (p.q.n + U - 1) / U;
@@ -508,17 +519,25 @@ cudaError_t rows_launch(RowsParams p, cudaStream_t stream) {
         p.cache_count = n * p.cache_units;
         p.float_blocks = (int)((p.float_count + per - 1) / per);
         const unsigned blocks = (unsigned)(p.float_blocks + (p.cache_count + per - 1) / per);
-        const cudaError_t e = launch_dependent(head_rows_kernel<T, VEC, INTER, LANES, U>, blocks, kThreads, 0, stream, p);
+        const cudaError_t e = launch_dependent(head_rows_kernel<T, VEC, FULL, INTER, LANES, U>, blocks, kThreads, 0, stream, p);
         if (e != cudaSuccess) return e;
     }
     return cudaSuccess;
 }
 
+template <typename T, bool VEC, bool INTER, int U, int LANES>
+cudaError_t rows_full(const RowsParams &p, cudaStream_t stream) {
+    if constexpr (U > 1) {      // for a few heads it makes no difference
+        if (p.D == 8 * LANES) return rows_launch<T, VEC, true, INTER, LANES, U>(p, stream);
+    }
+    return rows_launch<T, VEC, false, INTER, LANES, U>(p, stream);
+}
+
 template <typename T, bool VEC, bool INTER, int U>
 cudaError_t rows_lanes(const RowsParams &p, cudaStream_t stream) {
-    if (p.D <= 64) return rows_launch<T, VEC, INTER, 8, U>(p, stream);
-    if (p.D <= 128) return rows_launch<T, VEC, INTER, 16, U>(p, stream);
-    return rows_launch<T, VEC, INTER, 32, U>(p, stream);
+    if (p.D <= 64) return rows_full<T, VEC, INTER, U, 8>(p, stream);
+    if (p.D <= 128) return rows_full<T, VEC, INTER, U, 16>(p, stream);
+    return rows_full<T, VEC, INTER, U, 32>(p, stream);
 }
 
 template <typename T, bool INTER>
