@@ -383,17 +383,19 @@ __device__ __forceinline__ void head_rows(const RowsParams &a, uint32_t idx, uin
     }
 }
 
-// The first float_blocks blocks write floats, the rest write the cache.
-template <typename T, bool VEC, bool FULL, bool INTER, int LANES, int U>
-__global__ void __launch_bounds__(kThreads, 8) head_rows_kernel(const __grid_constant__ RowsParams a) {
+// The first float_blocks blocks write floats, the rest (with MIXED) write the cache.
+template <typename T, bool VEC, bool FULL, bool INTER, bool MIXED, int LANES, int U>
+__global__ void __launch_bounds__(kThreads, MIXED ? 8 : 9) head_rows_kernel(const __grid_constant__ RowsParams a) {
     pdl_wait();
     pdl_trigger();
     const uint32_t group = threadIdx.x / LANES, per = kThreads / LANES;
-    if (blockIdx.x < (unsigned)a.float_blocks)
-        head_rows<T, VEC, FULL, INTER, false, LANES, U>(a, blockIdx.x * per + group, (uint32_t)a.float_count, a.float_units, a.q_units);
-    else
-        head_rows<T, VEC, FULL, INTER, true, LANES, U>(a, (blockIdx.x - a.float_blocks) * per + group, (uint32_t)a.cache_count,
-                                                       a.cache_units, a.k_units);
+    if (!MIXED || blockIdx.x < (unsigned)a.float_blocks) {
+        head_rows<T, VEC, FULL, INTER, false, LANES, U>(a, blockIdx.x * per + group, (uint32_t)a.float_count, a.float_units,
+                                                        a.q_units);
+    } else if constexpr (MIXED) {
+        head_rows<T, VEC, FULL, INTER, true, LANES, U>(a, (blockIdx.x - a.float_blocks) * per + group,
+                                                       (uint32_t)a.cache_count, a.cache_units, a.k_units);
+    }
 }
 
 struct ReadParams {
@@ -519,7 +521,9 @@ cudaError_t rows_launch(RowsParams p, cudaStream_t stream) {
         p.cache_count = n * p.cache_units;
         p.float_blocks = (int)((p.float_count + per - 1) / per);
         const unsigned blocks = (unsigned)(p.float_blocks + (p.cache_count + per - 1) / per);
-        const cudaError_t e = launch_dependent(head_rows_kernel<T, VEC, FULL, INTER, LANES, U>, blocks, kThreads, 0, stream, p);
+        const cudaError_t e =
+            launch_dependent(cached ? head_rows_kernel<T, VEC, FULL, INTER, true, LANES, U>
+                                    : head_rows_kernel<T, VEC, FULL, INTER, false, LANES, U>, blocks, kThreads, 0, stream, p);
         if (e != cudaSuccess) return e;
     }
     return cudaSuccess;
