@@ -41,7 +41,7 @@ constexpr int kJoin = 48;                  // blocks' parts summed at a time
 // for all SMs, kUnshared (half as many of FP32, whose strips take twice as long): a
 // block takes those alone in about the time that joining would add.
 constexpr int kSnap = 16, kFew = 48, kUnshared = 96;
-constexpr int kLeast = 2;                  // strips to a warp, before work goes to another block
+constexpr int kLeast = 1;                  // strips to a warp, before work goes to another block
 // A key head of at most so many strips is one warp's: summing two warps' parts costs
 // about as long as four strips.
 constexpr int kWhole = 10;
