@@ -73,7 +73,7 @@ cudaError_t launch_attend_128(const AttendParams &p, int type, int nt, int sms, 
 cudaError_t launch_attend_256(const AttendParams &p, int type, int nt, int sms, cudaStream_t stream);
 // Warps of a block: what 65536 registers and the rings leave room for (terms: 2 for FP32).
 constexpr int attend_warps(int dt, int nt, int terms) {
-    return dt == 64 ? 16 : dt == 128 ? (nt == 1 ? 16 : terms == 1 ? 12 : 8) : nt * terms == 4 ? 4 : 8;
+    return dt == 64 ? 16 : dt == 128 ? (nt * terms == 1 ? 16 : nt * terms == 2 ? 12 : 8) : nt * terms == 4 ? 4 : 8;
 }
 // Floats of one part: sums of 8*nt heads, then each head's m and sum of p.
 constexpr int attend_part(int dt, int nt) { return 8 * nt * (dt + 2); }
@@ -673,11 +673,22 @@ struct Attend {
 #pragma unroll
         for (int half = 0; half < 2; ++half)
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
+            for (int nt = 0; nt < NT; ++nt) {
+                float(&sum_of)[4] = acc[2 * word + half][nt];
+                if constexpr (SPLIT) {
+                    // An MMA cuts off what its sum has no room for: over hundreds of strips that
+                    // is several units in FP32's last place (64 x 16384 tokens: 3.9e-6 off instead
+                    // of 1e-6), so strips are added up outside.
+                    float strip[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-                for (int t = 0; t < TERMS; ++t)
-                    mma_f16(acc[2 * word + half][nt], lo[2 * half], lo[2 * half + 1], hi[2 * half], hi[2 * half + 1],
-                            pf[nt][t][0], pf[nt][t][1]);
+                    for (int t = TERMS - 1; t >= 0; --t)
+                        mma_f16(strip, lo[2 * half], lo[2 * half + 1], hi[2 * half], hi[2 * half + 1], pf[nt][t][0], pf[nt][t][1]);
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) sum_of[k] += strip[k];
+                } else {
+                    mma_f16(sum_of, lo[2 * half], lo[2 * half + 1], hi[2 * half], hi[2 * half + 1], pf[nt][0][0], pf[nt][0][1]);
+                }
+            }
     }
 
     __device__ __forceinline__ void rescale(const float (&sc)[NT][4], float vm) {
