@@ -99,12 +99,18 @@ def _rotary(cos, sin, positions, interleaved, T, index):
     """The tables' sgemm_rotary (None without them)."""
     if cos is None and sin is None:
         return None
-    shape = q8._shape2(cos, "cos")
-    ld = q8._matrix(cos, "cos", (_F32,), shape, index)
-    if q8._matrix(sin, "sin", (_F32,), shape, index) != ld:
-        raise ValueError("cos and sin must have the same row stride")
+    if (isinstance(cos, _Tensor) and isinstance(sin, _Tensor) and cos.dtype is _F32 and sin.dtype is _F32
+            and cos.get_device() == index == sin.get_device() and index >= 0 and cos.is_contiguous()
+            and sin.is_contiguous() and cos.dim() == 2 and cos.shape == sin.shape):
+        rows, ld = cos.shape
+        half = ld
+    else:                   # strided, empty, or wrong: says what
+        rows, half = q8._shape2(cos, "cos")
+        ld = q8._matrix(cos, "cos", (_F32,), (rows, half), index)
+        if q8._matrix(sin, "sin", (_F32,), (rows, half), index) != ld:
+            raise ValueError("cos and sin must have the same row stride")
     at = 0 if positions is None else _vector(positions, "positions", _I64, (T,), index)
-    return _ROTARY(cos.data_ptr(), sin.data_ptr(), shape[0], ld, 2 * shape[1], at, 1 if interleaved else 0)
+    return _ROTARY(cos.data_ptr(), sin.data_ptr(), rows, ld, 2 * half, at, 1 if interleaved else 0)
 
 
 class CacheQ8:
