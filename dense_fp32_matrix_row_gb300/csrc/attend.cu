@@ -5,10 +5,14 @@
 namespace sgemm_gb300 {
 namespace {
 
-// Up to 8 query heads to a key head take one set of MMA columns, more take two;
-// beyond 16 the cache's strips are read once for each 16.
-int tiles(const AttendArgs &a) { return a.G > 8 ? 2 : 1; }
 int padded(int D) { return D <= 64 ? 64 : D <= 128 ? 128 : 256; }
+
+// Sets of 8 MMA columns.  More than 8 query heads to a key head take two sets, which
+// read a strip once for 16 heads (16 heads to a key head, 32 sequences of 16384: heads of 64
+// 139 us against 226 for two sets of 8 one after the other, 128: 213 and 343, 256: 109 and 171;
+// FP32, 128: 313 and 397).  FP32 heads beyond 128 take one: two leave room for 4 warps
+// alone (256: 213 us against 200).
+int tiles(const AttendArgs &a) { return a.G > 8 && !(a.type != kTypeBf16 && padded(a.D) == 256) ? 2 : 1; }
 
 bool aligned16(const sgemm_heads &h, int es) {
     return reinterpret_cast<uintptr_t>(h.p) % 16 == 0 && h.ld * es % 16 == 0 && h.hs * es % 16 == 0;

@@ -12,7 +12,7 @@
 //     S^T (tokens x heads) = K (16 x D) . Q^T (D x 8)      K's rows are the MMA's A as they lie
 //     O^T (dims x heads) += V^T (D x 16) . P^T (16 x 8)    A: bytes of two tokens paired
 //
-// up to 8 heads that share a key head as the MMA's 8 columns (NT of those).  The
+// up to 8 heads that share a key head as the MMA's 8 columns (NT sets of those).  The
 // order of an MMA's inner index is free as long as A and B agree, so every lane
 // reads 16 consecutive bytes of a row.  S^T comes out as P^T goes in except for a
 // transposition of 8 x 8, one instruction (movmatrix).
@@ -25,6 +25,21 @@
 // its strips (queries, results) is latency that the other warps cover.  A key
 // head that several warps share is summed at the end, first within the block,
 // then by the last of the blocks that share it, always in the same order.
+//
+// Bound by memory as long as sequences are long.  Measured (bf16, 8 key heads of 128, 8
+// query heads to each; copies alone, without any arithmetic, stream at 7.0 TB/s):
+//   64 sequences of 16384 tokens, 2.2 GB, 330 us, 6.7 TB/s;
+//   64 of 1024 to 8192, 602 MB, 107 us: 3 us until the first copies, 5 to 8 of sums
+//     at the end, while other SMs still load memory;
+//   one of 131072 (4 heads to each), 277 MB, 52 us, the same;
+//   one of 500, 8.1 us: two strips a warp (1.1 us each), four dependent loads before
+//     them (length, page number, queries, strip), two sums behind them.
+// Other divisions, measured with those four: rounds of a strip for each of a block's
+// warps, with barriers where key heads end, by 4 warps (4 blocks an SM) 380, 119, 63 and 9.5
+// us, 8 warps 367, 125, 58 and 8.7, 16 warps 363, 151, 59 and 10.2; joining blocks where a
+// key head ends instead of at the end, 26 us more for the first.  No gain: queries
+// loaded before the first strips (registers, or through the ring), page numbers by 32,
+// one loop for the ring's filling and its use, deeper batches in the joins.
 #pragma once
 
 #include <atomic>
@@ -71,9 +86,10 @@ struct AttendParams {
 cudaError_t launch_attend_64(const AttendParams &p, int type, int nt, int sms, cudaStream_t stream);
 cudaError_t launch_attend_128(const AttendParams &p, int type, int nt, int sms, cudaStream_t stream);
 cudaError_t launch_attend_256(const AttendParams &p, int type, int nt, int sms, cudaStream_t stream);
-// Warps of a block: what 65536 registers and the rings leave room for (terms: 2 for FP32).
+// Warps of a block, as many as 65536 registers hold (terms: 2 for FP32; 16 warps of 128
+// registers instead of 12 for FP32 heads of 128: 218 us against 206 for 32 sequences of 16384).
 constexpr int attend_warps(int dt, int nt, int terms) {
-    return dt == 64 ? 16 : dt == 128 ? (nt * terms == 1 ? 16 : nt * terms == 2 ? 12 : 8) : nt * terms == 4 ? 4 : 8;
+    return dt == 64 ? 16 : dt == 256 ? 8 : nt * terms == 1 ? 16 : nt * terms == 2 ? 12 : 8;
 }
 // Floats of one part: sums of 8*nt heads, then each head's m and sum of p.
 constexpr int attend_part(int dt, int nt) { return 8 * nt * (dt + 2); }
@@ -1120,7 +1136,9 @@ template <int DT>
 cudaError_t attend_of_dim(const AttendParams &p, int type, int nt, int sms, cudaStream_t stream) {
     if (type == kTypeBf16)
         return nt == 1 ? attend_launch<DT, 1, __nv_bfloat16>(p, sms, stream) : attend_launch<DT, 2, __nv_bfloat16>(p, sms, stream);
-    return nt == 1 ? attend_launch<DT, 1, float>(p, sms, stream) : attend_launch<DT, 2, float>(p, sms, stream);
+    if constexpr (DT < 256)
+        if (nt == 2) return attend_launch<DT, 2, float>(p, sms, stream);
+    return attend_launch<DT, 1, float>(p, sms, stream);
 }
 
 }  // namespace

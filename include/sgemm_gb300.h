@@ -366,6 +366,9 @@ int sgemm_q8_moe(int64_t T, int64_t E, int64_t top_k, int64_t H, int64_t I, cons
  *             One that lies outside its array is not followed: what it stands
  *             for is left out, as said below, and the next sgemm_status()
  *             returns SGEMM_ERR_BAD_INDEX.
+ * Stream order  The kernels are launched as programmatic dependents, like
+ *             sgemm()'s decode kernel: they wait for the work before them on `stream`
+ *             before touching memory.
  */
 typedef struct {
     void *p;                /* element type: the call's `type`; not written through for an input */
@@ -471,9 +474,10 @@ int sgemm_q8_cache_read(int64_t N, int type, const sgemm_q8_cache *cache, const 
  * NaN to the results that read it; rows that no sequence's tokens lie in may
  * hold anything.  Sums are taken in an order that depends on `lens` and the
  * GPU model alone.
- * Uses the stream's workspace for parts of long sequences, grown like sgemm()'s
- * with the shape (not with the lengths), and a small array of counters kept
- * per stream beside it; the same rules for stream capture hold for both.
+ * Uses the stream's workspace for parts of long sequences (up to 25 MB, by the head
+ * size and the heads to a key head, not by lengths), grown like sgemm()'s, and a
+ * small array of counters kept per stream beside it; the same rules for stream
+ * capture and for graphs that share a capture stream hold for both.
  */
 int sgemm_q8_attend(int64_t B, int type, const sgemm_heads *q, const sgemm_q8_cache *cache,
                     const int32_t *table, int64_t ld_table, int64_t pages, const int32_t *lens,
@@ -581,8 +585,9 @@ int64_t sgemm_host_panel_rows(int64_t M, int64_t N, int64_t K);
 /*
  * sgemm_release_workspaces -- free the library's cached device workspaces
  * (the transposed copy of A that the FFMA kernel stages from, the 8-bit
- * operators' intermediate rows; one buffer per device and stream, grown with cudaMallocAsync on the call's stream) and
- * sgemm_host's device buffers, copy streams and events.
+ * operators' intermediate rows; one buffer per device and stream, grown with cudaMallocAsync on the call's stream),
+ * sgemm_q8_attend's counters (16 KiB per device and stream) and sgemm_host's
+ * device buffers, copy streams and events.
  * Waits for every stream that owns a workspace.  Call it only while no other
  * host thread is inside an sgemm call, and after the graphs that captured calls
  * are gone; later calls allocate again as needed.
