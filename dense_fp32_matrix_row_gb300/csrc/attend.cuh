@@ -222,9 +222,10 @@ __device__ __forceinline__ Span span_of(const AttendParams &p, int n) {
     s.strips = n > 0 ? (n - 1) / kStrip + 1 - s.strip0 : 0;
     return s;
 }
-// A sequence's length, within what its pages hold.
+// A sequence's length, within what its pages hold.  (Read by plain loads, as page
+// numbers are: a load through the read-only path might be moved before pdl_wait.)
 __device__ __forceinline__ int tokens_of(const AttendParams &p, int b) {
-    return max(0, min(__ldg(p.lens + b), p.width * p.page));
+    return max(0, min(p.lens[b], p.width * p.page));
 }
 
 // A place in the list: sequence, key head, group of its query heads, strip.
@@ -362,7 +363,7 @@ __device__ __forceinline__ void finish_head(const AttendParams &p, int b, int h,
 struct Sum {
     float4 o;
     float top, total;
-    __device__ __forceinline__ Sum() : o(make_float4(0.0f, 0.0f, 0.0f, 0.0f)), top(-1e30f), total(0.0f) {}
+    __device__ __forceinline__ Sum() : o(make_float4(0.0f, 0.0f, 0.0f, 0.0f)), top(-kLargest), total(0.0f) {}
     __device__ __forceinline__ void rise(float to) {
         const float f = exp2_fast(top - to);
         top = to;
@@ -412,7 +413,7 @@ struct Attend {
         const int32_t *row = p.table + next.b * p.ld_table;
         int t = (next.span.strip0 + next.strip) * kStrip;
         if (!p.whole) t = max(min(t + (lane & 15), next.span.last - 1), next.span.first);
-        next_page = __ldg(row + page_of(t));
+        next_page = row[page_of(t)];
     }
 
     // Starts the copies of the strip at `next` into stage s, and moves on.
@@ -547,7 +548,7 @@ struct Attend {
             qmul[nt][1] = __shfl_sync(0xffffffffu, mul, 8 * j + 4);
 #pragma unroll
             for (int k = 0; k < 2; ++k) {
-                m[nt][k] = -1e30f;
+                m[nt][k] = -kLargest;
                 sum[nt][k] = 0.0f;
             }
 #pragma unroll
@@ -777,19 +778,20 @@ struct Attend {
         });
     }
     __device__ __forceinline__ void finish(const Cursor &at) const {
+        const float unscale = 1.0f / vmul;
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
             for (int k = 0; k < 2; ++k) {
                 const int head = at.group * S::HEADS + nt * 8 + 2 * j + k;
                 if (head >= p.G) continue;
-                const float total = sum[nt][k], inv = total != 0.0f ? 1.0f / (total * vmul) : 0.0f;
+                const float total = sum[nt][k], inv = total != 0.0f ? 1.0f / total : 0.0f;
                 T *to = static_cast<T *>(p.out) + at.b * p.o_ld + (at.h * (int64_t)p.G + head) * p.o_hs;
 #pragma unroll
                 for (int i = 0; i < S::STEPS; i += 2) {
                     const int d = dim_of(i);
-                    const float v[4] = {acc[i][nt][k] * inv, acc[i][nt][k + 2] * inv, acc[i + 1][nt][k] * inv,
-                                        acc[i + 1][nt][k + 2] * inv};
+                    const float v[4] = {acc[i][nt][k] * unscale * inv, acc[i][nt][k + 2] * unscale * inv,
+                                        acc[i + 1][nt][k] * unscale * inv, acc[i + 1][nt][k + 2] * unscale * inv};
                     if (d < p.D) store_out<T>(p, to + d, v);
                 }
                 if (g == 0 && p.lse) p.lse[(at.b * (int64_t)p.Hk + at.h) * p.G + head] = lse_of(m[nt][k], total);
@@ -920,17 +922,32 @@ __device__ __forceinline__ void join(const AttendParams &p, const Shared *shared
     }
 }
 
-// The results of sequences without tokens, and complaints about lengths.
+// The results of sequences without tokens, and complaints about lengths.  A thread
+// looks at one sequence of each gridDim.x; `found` has a word for each warp.
 template <int THREADS, typename T>
-__device__ __forceinline__ void nothing(const AttendParams &p) {
-    for (int64_t b = blockIdx.x; b < p.B; b += gridDim.x) {
-        const int n = __ldg(p.lens + b);
-        if ((n < 0 || n > p.width * p.page) && threadIdx.x == 0) record_error(p.err, kErrBadIndex);
-        if (n > 0 && p.width > 0) continue;
-        for (int i = threadIdx.x; i < p.Hk * p.G * p.D; i += THREADS)
-            static_cast<T *>(p.out)[b * p.o_ld + (i / p.D) * p.o_hs + i % p.D] = from_f32<T>(0.0f);
-        if (p.lse)
-            for (int i = threadIdx.x; i < p.Hk * p.G; i += THREADS) p.lse[b * p.Hk * p.G + i] = -INFINITY;
+__device__ __forceinline__ void nothing(const AttendParams &p, uint32_t *found) {
+    for (int64_t first = blockIdx.x; first < p.B; first += (int64_t)gridDim.x * THREADS) {
+        const int64_t own = first + (int64_t)gridDim.x * threadIdx.x;
+        bool empty = false;
+        if (own < p.B) {
+            const int n = p.lens[own];
+            if (n < 0 || n > p.width * p.page) record_error(p.err, kErrBadIndex);
+            empty = n <= 0 || p.width == 0;
+        }
+        const uint32_t some = __ballot_sync(0xffffffffu, empty);
+        if (!__syncthreads_or(some != 0)) continue;
+        if (threadIdx.x % 32 == 0) found[threadIdx.x / 32] = some;
+        __syncthreads();
+        for (int w = 0; w < THREADS / 32; ++w) {
+            for (uint32_t left = found[w]; left != 0; left &= left - 1) {
+                const int64_t b = first + (int64_t)gridDim.x * (32 * w + __ffs(left) - 1);
+                for (int i = threadIdx.x; i < p.Hk * p.G * p.D; i += THREADS)
+                    static_cast<T *>(p.out)[b * p.o_ld + (i / p.D) * p.o_hs + i % p.D] = from_f32<T>(0.0f);
+                if (p.lse)
+                    for (int i = threadIdx.x; i < p.Hk * p.G; i += THREADS) p.lse[b * p.Hk * p.G + i] = -INFINITY;
+            }
+        }
+        __syncthreads();
     }
 }
 
@@ -968,7 +985,7 @@ attend_kernel(const __grid_constant__ AttendParams p) {
     list.load(p, 0, 0);
     if (p.B <= 32) total = list.all();
     const Division div(total, S::WARPS * kLeast, Attend<DT, NT, T>::TERMS);
-    nothing<S::THREADS, T>(p);
+    nothing<S::THREADS, T>(p, reinterpret_cast<uint32_t *>(note));
     if ((int)blockIdx.x >= div.blocks || total == 0) return;
     int *bounds = note, *starts = note + 2;     // of the block, of its warps
     if (warp < 2) {

@@ -457,6 +457,28 @@ def test_attend_many(dt):
     check_attend([0] * 400 + [77] + [0] * 400, 1, 2, 64, 16, dt)
 
 
+def test_attend_very_many():
+    """More sequences than a block looks at in one step, most without tokens, the last
+    lengths outside the table."""
+    B = 152 * 512 + 1000
+    pool = ref.Pool(8, 1, 16, 64)
+    lens = torch.zeros(B, dtype=torch.int32, device="cuda")
+    lens[::1000] = 20
+    lens[-2:] = torch.tensor([33, -1], device="cuda")
+    table = torch.arange(2, dtype=torch.int32, device="cuda").repeat(B, 1)
+    q = torch.randn((1, 2, 64), device="cuda")
+    out, lse = torch.full((B, 2, 64), 9.0, device="cuda"), torch.full((B, 2), 9.0, device="cuda")
+    sg.attend_q8(q.expand(B, 2, 64), pool.cache(), table, lens, out, lse=lse)
+    assert sg.status() == sg.ERR_BAD_INDEX
+    want, tol, want_lse, lse_tol = ref.attend(q.repeat(2, 1, 1), pool, table[:2], [20, 32], 0.125, 0, False)
+    full = lens == 20
+    close(out[full], want[:1].expand(int(full.sum()), 2, 64), tol[:1].expand(int(full.sum()), 2, 64), "fp32")
+    close(out[-2:-1], want[1:], tol[1:], "fp32")
+    close(lse[-2:-1], want_lse[1:], lse_tol[1:], "fp32")
+    none = (lens == 0) | (lens < 0)
+    assert float(out[none].abs().max()) == 0 and bool((lse[none] == -float("inf")).all())
+
+
 def test_attend_no_tokens():
     check_attend([0, 0, 0], 2, 4, 64, 16, "bf16")
     check_attend([0], 1, 1, 128, 8, "fp32", width=0)
@@ -470,7 +492,7 @@ def test_attend_strides(lead, offset, by_head, dt):
 
 @pytest.mark.parametrize("dt", ["fp32", "bf16"])
 @pytest.mark.parametrize("scale,q_scale", [(1.0, 1.0), (0.0, 2.0), (-0.3, 1.0), (1e-20, 1e10), (1e-3, 3e4), (1e20, 1e-21),
-                                           (1e36, 1e-36), (1e-37, 3e36)])
+                                           (1e36, 1e-36), (1e-37, 3e36), (-1e15, 1e15)])
 def test_attend_scales(scale, q_scale, dt):
     """Sharp, flat and turned distributions; queries far outside FP16's range."""
     check_attend([200, 33], 2, 4, 64, 16, dt, scale=scale, q_scale=q_scale)
@@ -517,6 +539,11 @@ def test_attend_values_of_unequal_size(dt):
         t = 199 - t if flip else t
         pool.v_scale[:] = (10.0 ** (t.clamp(0, 199) * 0.3 - 30)).float()[:, None]
         check_attend([200], 1, 2, 64, 16, dt, pool=pool, table=table, q=np.ones((1, 2, 64), np.float32) * 0.1)
+    for size in (1e-35, 1e-37, 1e33):       # one warp's and several warps' sequences
+        pool = ref.Pool(15, 1, 16, 64)
+        table, _ = pool.table([200, 30])
+        pool.v_scale.fill_(size)
+        check_attend([200, 30], 1, 2, 64, 16, dt, pool=pool, table=table)
     pool = ref.Pool(13, 1, 16, 64)
     table, _ = pool.table([200])
     sink = int(table[0, 0])
