@@ -140,6 +140,8 @@ class CacheQ8:
         torch = q8.torch
         shape = self.k.shape
         blocks, self.heads, self.page, self.dim = shape
+        if 0 in shape[1:]:
+            raise ValueError(f"a cache has heads, rows and elements: k of shape {tuple(shape)}")
         self.slots = blocks * self.page
         self._device = self.k.get_device()
         strides = []

@@ -865,6 +865,13 @@ def test_python_refusals():
     assert bool((y == 0).all())
 
 
+@pytest.mark.parametrize("heads,page,dim", [(0, 16, 64), (2, 0, 64), (2, 16, 0)])
+def test_a_cache_without_elements(heads, page, dim):
+    k, v = (torch.zeros((4, heads, page, dim), dtype=torch.int8, device="cuda") for _ in range(2))
+    with pytest.raises(ValueError):
+        sg.CacheQ8(k, v, *(torch.zeros((4, heads, page), device="cuda") for _ in range(2)))
+
+
 def test_empty_calls():
     pool = ref.Pool(4, 2, 16, 64)
     none = torch.zeros((0, 2, 64), device="cuda")
