@@ -7,12 +7,22 @@ namespace {
 
 int padded(int D) { return D <= 64 ? 64 : D <= 128 ? 128 : 256; }
 
-// Sets of 8 MMA columns.  More than 8 query heads to a key head take two sets, which
-// read a strip once for 16 heads (16 heads to a key head, 32 sequences of 16384: heads of 64
-// 139 us against 226 for two sets of 8 one after the other, 128: 213 and 343, 256: 109 and 171;
-// FP32, 128: 313 and 397).  FP32 heads beyond 128 take one: two leave room for 4 warps
-// alone (256: 213 us against 200).
-int tiles(const AttendArgs &a) { return a.G > 8 && !(a.type != kTypeBf16 && padded(a.D) == 256) ? 2 : 1; }
+// Sets of 8 MMA columns.  More than 8 query heads to a key head take up to four sets,
+// which read a strip once for all (8 key heads, 16 sequences of 16384: 16 heads of 64 76 us against
+// 113 for two sets of 8 one after the other, 128: 112 and 172; 24 heads of 64 93 against 139 for two
+// times two sets, 128: 150 and 214; 32 heads 107 and 139, 172 and 214; FP32, three sets against two
+// times two, 64: 125 and 199, 128: 209 and 306).  Heads beyond 128 take two, in FP32 one: more
+// leave too few registers or warps (24 heads of 256 in three sets 398 us, in two times two 362;
+// FP32, two sets 213, two times one 200).
+int most_tiles(const AttendArgs &a) {
+    const bool bf16 = a.type == kTypeBf16;
+    return padded(a.D) == 256 ? (bf16 ? 2 : 1) : bf16 ? 4 : 3;
+}
+// As few times as that allows, alike.
+int tiles(const AttendArgs &a) {
+    const int sets = (a.G + 7) / 8, times = (sets - 1) / most_tiles(a) + 1;
+    return (sets + times - 1) / times;
+}
 
 bool aligned16(const sgemm_heads &h, int es) {
     return reinterpret_cast<uintptr_t>(h.p) % 16 == 0 && h.ld * es % 16 == 0 && h.hs * es % 16 == 0;

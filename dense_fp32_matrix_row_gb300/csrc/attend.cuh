@@ -86,10 +86,12 @@ struct AttendParams {
 cudaError_t launch_attend_64(const AttendParams &p, int type, int nt, int sms, cudaStream_t stream);
 cudaError_t launch_attend_128(const AttendParams &p, int type, int nt, int sms, cudaStream_t stream);
 cudaError_t launch_attend_256(const AttendParams &p, int type, int nt, int sms, cudaStream_t stream);
-// Warps of a block, as many as 65536 registers hold (terms: 2 for FP32; 16 warps of 128
-// registers instead of 12 for FP32 heads of 128: 218 us against 206 for 32 sequences of 16384).
+// Warps of a block, as many as 65536 registers hold, as many on each quarter of an SM
+// (terms: 2 for FP32; 16 sequences of 16384, 8 key heads: 3 sets of heads of 64 with 8 warps 205
+// us, with 12 173; of 128 with 8 150, with 10 178.  FP32 heads of 128 with 12 109, with 16 106,
+// but 7 short sequences 12.7 and 13.5).
 constexpr int attend_warps(int dt, int nt, int terms) {
-    return dt == 64 ? 16 : dt == 256 ? 8 : nt * terms == 1 ? 16 : nt * terms == 2 ? 12 : 8;
+    return dt == 64 ? (nt > 2 ? 12 : 16) : dt == 256 ? 8 : nt * terms == 1 ? 16 : nt <= 2 ? 12 : 8;
 }
 // Floats of one part: sums of 8*nt heads, then each head's m and sum of p.
 constexpr int attend_part(int dt, int nt) { return 8 * nt * (dt + 2); }
@@ -186,8 +188,10 @@ struct Shape {
     static constexpr int STAGE = 2 * ROWS + 256;       // keys, values, 16 + 16 scales, the mask
     static constexpr int HEADS = 8 * NT;
     static constexpr int PART = attend_part(DT, NT);
-    // the queries' operands: in registers as long as they leave room for the sums
-    static constexpr bool Q_SHARED = DT * NT * (TERMS + 1) > 768;
+    // The queries' operands: in registers as long as they leave room for the sums (16 sequences
+    // of 16384, registers against shared memory: bf16 heads of 128, 16 to a key head, 115 and 112
+    // us, of 256, 8, 174 and 177; FP32 heads of 64, 16, 108 and 94, of 128, 8, 111 and 108).
+    static constexpr bool Q_SHARED = NT * TERMS > 1 && DT * NT * TERMS >= 256;
     static constexpr int QUERIES = Q_SHARED ? NT * TERMS * STEPS * 256 : 0;       // a warp
     static constexpr int NOTES = WARPS * (72 + 8) + 128;      // see the kernel
     static constexpr int ROOM = 227 * 1024 - 128 - NOTES - WARPS * QUERIES;
@@ -1169,11 +1173,16 @@ cudaError_t attend_launch(const AttendParams &p, int sms, cudaStream_t stream) {
 
 template <int DT>
 cudaError_t attend_of_dim(const AttendParams &p, int type, int nt, int sms, cudaStream_t stream) {
-    if (type == kTypeBf16)
-        return nt == 1 ? attend_launch<DT, 1, __nv_bfloat16>(p, sms, stream) : attend_launch<DT, 2, __nv_bfloat16>(p, sms, stream);
-    if constexpr (DT < 256)
+    using B = __nv_bfloat16;
+    const bool b = type == kTypeBf16;
+    if (nt == 1) return b ? attend_launch<DT, 1, B>(p, sms, stream) : attend_launch<DT, 1, float>(p, sms, stream);
+    if (b && nt == 2) return attend_launch<DT, 2, B>(p, sms, stream);
+    if constexpr (DT < 256) {
         if (nt == 2) return attend_launch<DT, 2, float>(p, sms, stream);
-    return attend_launch<DT, 1, float>(p, sms, stream);
+        if (nt == 3) return b ? attend_launch<DT, 3, B>(p, sms, stream) : attend_launch<DT, 3, float>(p, sms, stream);
+        if (b && nt == 4) return attend_launch<DT, 4, B>(p, sms, stream);
+    }
+    return cudaErrorInvalidConfiguration;       // not one of most_tiles()
 }
 
 }  // namespace

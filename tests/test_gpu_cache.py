@@ -421,6 +421,16 @@ def test_attend_groups(Hk, G, dt):
 
 
 @pytest.mark.parametrize("dt", ["fp32", "bf16"])
+@pytest.mark.parametrize("G", [18, 25, 32, 33, 47, 100])
+def test_attend_many_heads_of_a_key_head(G, dt):
+    """Up to 32 at a time, in one block and joined from many."""
+    for D in (64, 80, 128, 256):
+        check_attend([1, 0, 16, 333], 2, G, D, 16, dt)
+    check_attend([33, 5000, 70], 1, G, 64, 20, dt, q_scale=1.0)
+    check_attend([20000, 3], 1, G, 128, 16, dt, q_scale=1.0, window=17000)
+
+
+@pytest.mark.parametrize("dt", ["fp32", "bf16"])
 @pytest.mark.parametrize("window", [1, 2, 15, 16, 17, 64, 100, 5000])
 def test_attend_window(window, dt):
     check_attend(LENS + [700], 2, 4, 64, 16, dt, window=window)
