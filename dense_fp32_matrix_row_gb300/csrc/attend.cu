@@ -5,13 +5,15 @@
 namespace sgemm_gb300 {
 namespace {
 
-int padded(int D) { return D <= 64 ? 64 : D <= 128 ? 128 : 256; }
+// The form that heads of D run in.  96: 16 sequences of 16384, heads of 96 86 us in 128, 75 here,
+// of 80 95 and 82; FP32 108 and 91, 116 and 94.
+int padded(int D) { return D <= 64 ? 64 : D <= 96 ? 96 : D <= 128 ? 128 : 256; }
 
 // Sets of 8 MMA columns.  More than 8 query heads to a key head take up to four sets,
-// which read a strip once for all (8 key heads, 16 sequences of 16384: 16 heads of 64 76 us against
-// 113 for two sets of 8 one after the other, 128: 112 and 172; 24 heads of 64 93 against 139 for two
-// times two sets, 128: 150 and 214; 32 heads 107 and 139, 172 and 214; FP32, three sets against two
-// times two, 64: 125 and 199, 128: 209 and 306).  Heads beyond 128 take two, in FP32 one: more
+// which read a strip once for all (8 key heads, 16 sequences of 16384: 16 heads of 64 71 us against
+// 113 for two sets of 8 one after the other, 128: 106 and 172; 24 heads of 64 89 against 139 for two
+// times two sets, 128: 140 and 214; 32 heads 102 and 139, 164 and 214; FP32, three sets against two
+// times two, 64: 120 and 199, 128: 200 and 306).  Heads beyond 128 take two, in FP32 one: more
 // leave too few registers or warps (24 heads of 256 in three sets 398 us, in two times two 362;
 // FP32, two sets 213, two times one 200).
 int most_tiles(const AttendArgs &a) {
@@ -54,6 +56,7 @@ cudaError_t launch_attend(const AttendArgs &a, void *workspace, unsigned *ticket
     p.page = (int)a.cache.page;
     p.width = a.width;
     divider((uint32_t)p.page, &p.page_mul, &p.page_shift);
+    p.chunk_mul = 65536 / (a.D / 16) + 1;      // above 2^16 / chunks by at most 1
     p.whole = p.page % kStrip == 0;
     p.window = a.window;
     p.scale_log2 = a.scale * 1.44269504088896341f;
@@ -70,6 +73,7 @@ cudaError_t launch_attend(const AttendArgs &a, void *workspace, unsigned *ticket
     p.err = a.err;
     switch (dt) {
         case 64: return launch_attend_64(p, a.type, nt, a.sm_count, a.stream);
+        case 96: return launch_attend_96(p, a.type, nt, a.sm_count, a.stream);
         case 128: return launch_attend_128(p, a.type, nt, a.sm_count, a.stream);
         default: return launch_attend_256(p, a.type, nt, a.sm_count, a.stream);
     }

@@ -65,6 +65,7 @@ struct AttendParams {
     int B, Hk, G, D, groups;               // groups: of 8*NT query heads to a key head
     int page, width;
     uint32_t page_mul, page_shift;         // t / page = (t * page_mul) >> page_shift (host: divider())
+    uint32_t chunk_mul;                    // q / chunks of a row = (q * chunk_mul) >> 16 for q < 128
     int whole;                             // a strip lies within a page
     int window;
     float scale_log2;                      // scale * log2(e)
@@ -84,6 +85,7 @@ struct AttendParams {
 };
 
 cudaError_t launch_attend_64(const AttendParams &p, int type, int nt, int sms, cudaStream_t stream);
+cudaError_t launch_attend_96(const AttendParams &p, int type, int nt, int sms, cudaStream_t stream);
 cudaError_t launch_attend_128(const AttendParams &p, int type, int nt, int sms, cudaStream_t stream);
 cudaError_t launch_attend_256(const AttendParams &p, int type, int nt, int sms, cudaStream_t stream);
 // Warps of a block, as many as 65536 registers hold, as many on each quarter of an SM
@@ -91,7 +93,7 @@ cudaError_t launch_attend_256(const AttendParams &p, int type, int nt, int sms, 
 // us, with 12 173; of 128 with 8 150, with 10 178.  FP32 heads of 128 with 12 109, with 16 106,
 // but 7 short sequences 12.7 and 13.5).
 constexpr int attend_warps(int dt, int nt, int terms) {
-    return dt == 64 ? (nt > 2 ? 12 : 16) : dt == 256 ? 8 : nt * terms == 1 ? 16 : nt <= 2 ? 12 : 8;
+    return dt == 64 ? (nt > 2 ? 12 : 16) : dt == 256 ? 8 : nt * terms == 1 ? 16 : nt <= 2 || (dt == 96 && nt * terms == 3) ? 12 : 8;
 }
 // Floats of one part: sums of 8*nt heads, then each head's m and sum of p.
 constexpr int attend_part(int dt, int nt) { return 8 * nt * (dt + 2); }
@@ -184,14 +186,23 @@ struct Shape {
     static constexpr int THREADS = 32 * WARPS;
     static constexpr int CH = DT / 16;                 // 16-byte chunks of a row
     static constexpr int STEPS = DT / 16;              // MMAs along the head, and dim tiles of O^T
-    static constexpr int ROWS = kStrip * DT;           // bytes of a strip's keys
+    static constexpr int ROWS = kStrip * (DT == 96 ? 128 : DT);        // bytes of a strip's keys
+    // What a lane reads of a key row, as the MMAs' inner index: 16 bytes of each 64, and
+    // 8 of the last 32 of 96.
+    static constexpr int PIECES = (CH + 3) / 4;
+    static constexpr int words(int piece) { return DT / 16 - 4 * piece < 4 ? DT / 16 - 4 * piece : 4; }
     static constexpr int STAGE = 2 * ROWS + 256;       // keys, values, 16 + 16 scales, the mask
     static constexpr int HEADS = 8 * NT;
     static constexpr int PART = attend_part(DT, NT);
     // The queries' operands: in registers as long as they leave room for the sums (16 sequences
     // of 16384, registers against shared memory: bf16 heads of 128, 16 to a key head, 115 and 112
-    // us, of 256, 8, 174 and 177; FP32 heads of 64, 16, 108 and 94, of 128, 8, 111 and 108).
-    static constexpr bool Q_SHARED = NT * TERMS > 1 && DT * NT * TERMS >= 256;
+    // us, of 256, 8, 174 and 177; FP32 heads of 64, 16, 108 and 94, of 128, 8, 111 and 108; 96: sums
+    // take less, heads of 80, 16, 99 and 106).
+    static constexpr bool Q_SHARED = NT * TERMS > 1 && !(DT == 96 && NT * TERMS == 2);
+    // Where a strip's chunks go is kept, rather than found for each strip, where registers
+    // are left for it (heads of 128, 16 to a key head 109 -> 107 us, FP32, 8, 107 -> 104, but bf16,
+    // 8, 91 -> 94).
+    static constexpr bool PLACES = DT < 256 && NT * TERMS > 1;
     static constexpr int QUERIES = Q_SHARED ? NT * TERMS * STEPS * 256 : 0;       // a warp
     static constexpr int NOTES = WARPS * (72 + 8) + 128;      // see the kernel
     static constexpr int ROOM = 227 * 1024 - 128 - NOTES - WARPS * QUERIES;
@@ -204,10 +215,13 @@ struct Shape {
 
 // Byte offset of chunk c of row r in a strip, chunks exchanged within 128 bytes so
 // that neither the keys' reads (8 lanes: 2 rows, 4 chunks of each) nor the values'
-// (8 lanes: 4 rows, 2 chunks) meet in a bank.
+// (8 lanes: 4 rows, 2 chunks) meet in a bank.  96: rows lie as 128 do; 16 lanes read
+// halves of chunks (keys: 4 rows, 2 chunks of each; values: every other of 8 rows).
+// Packed closer, with one more stage, four chunks of a row apart from its other two: 75 -> 79 us.
 template <int DT>
 __device__ __forceinline__ uint32_t chunk_at(int r, int c) {
     if constexpr (DT == 64) return (uint32_t)((r >> 1) * 128 + ((((r & 1) * 4 + c) ^ (r & 6)) << 4));
+    else if constexpr (DT == 96) return (uint32_t)(r * 128 + ((c ^ (((r ^ r >> 2) & 1) << 2 | (r & 2))) << 4));
     else return (uint32_t)(r * DT + (c >> 3) * 128 + (((c & 7) ^ (r & 7)) << 4));
 }
 
@@ -392,6 +406,7 @@ struct Attend {
     uint32_t ring;          // this warp's stages
     uint32_t queries;       // Q_SHARED: this warp's
     int warp, lane, g, j;
+    uint32_t places[S::PLACES ? S::PIECES : 1];     // find_place() of 2 * i and 2 * i + 1
 
     // the strip to be loaded next
     Cursor next;
@@ -406,7 +421,21 @@ struct Attend {
         g = lane >> 2;
         j = lane & 3;
         ring = smem + warp * (S::STAGES * S::STAGE);
+        if constexpr (S::PLACES) {
+#pragma unroll
+            for (int i = 0; i < S::PIECES; ++i) places[i] = find_place(2 * i) | find_place(2 * i + 1) << 16;
+        }
         queries = smem + S::WARPS * (S::STAGES * S::STAGE) + warp * S::QUERIES;
+    }
+
+    // Where the strip's chunk number lane + 32 * i goes.
+    __device__ __forceinline__ uint32_t find_place(int i) const {
+        const int q = lane + 32 * i, r = (int)((uint32_t)q * p.chunk_mul >> 16) & (kStrip - 1);
+        return chunk_at<DT>(r, q - r * (p.D >> 4));
+    }
+    __device__ __forceinline__ uint32_t place_of(int i) const {
+        if constexpr (S::PLACES) return places[i / 2] >> 16 * (i % 2) & 0xffff;
+        else return find_place(i);
     }
 
     __device__ __forceinline__ int page_of(int t) const {
@@ -440,10 +469,15 @@ struct Attend {
                     const int8_t *v = p.v + page * p.v_stride + row * p.D;
 #pragma unroll
                     for (int i = 0; i < S::CH / 2; ++i) {
+                        // one chunk behind another, whatever the rows' size (16 sequences of 16384,
+                        // heads of 64: 64 -> 61 us, of 112: 101 -> 98; 256, with twice the divisions,
+                        // 175 -> 178)
                         const int q = lane + 32 * i, r = q / S::CH, c = q % S::CH;
-                        if (c < chunks) {
-                            cp_async16(at + chunk_at<DT>(r, c), k + r * p.D + c * 16);
-                            cp_async16(at + S::ROWS + chunk_at<DT>(r, c), v + r * p.D + c * 16);
+                        if (DT == 256 ? c < chunks : q < 16 * chunks) {
+                            const uint32_t to = at + (DT == 256 ? chunk_at<DT>(r, c) : place_of(i));
+                            const int from = DT == 256 ? r * p.D + c * 16 : q * 16;
+                            cp_async16(to, k + from);
+                            cp_async16(to + S::ROWS, v + from);
                         }
                     }
                     const float *scale = lane < 16 ? p.ks + page * p.ks_stride : p.vs + page * p.vs_stride;
@@ -485,7 +519,7 @@ struct Attend {
     // The queries of the key head at `at`, as they lie: this lane's chunks of one head
     // of each eight.
     struct Queries {
-        uint32_t w[NT][S::CH / 4][4 * (int)sizeof(T)];
+        uint32_t w[NT][S::PIECES][4 * (int)sizeof(T)];
     };
     __device__ __forceinline__ void fetch(Queries &x, const Cursor &at) const {
         const int first = at.group * S::HEADS;
@@ -494,25 +528,25 @@ struct Attend {
             const int head = first + nt * 8 + g;
             const T *q = static_cast<const T *>(p.q) + at.b * p.q_ld + (at.h * (int64_t)p.G + head) * p.q_hs;
 #pragma unroll
-            for (int i = 0; i < S::CH / 4; ++i) {
-                const int d = key_chunk(i) * 16;
+            for (int i = 0; i < S::PIECES; ++i) {
+                const int d = key_dim(i), n = S::words(i);       // 4 * n elements
                 uint32_t(&w)[4 * (int)sizeof(T)] = x.w[nt][i];
                 if (head >= p.G || d >= p.D) {
 #pragma unroll
-                    for (int e = 0; e < 4 * (int)sizeof(T); ++e) w[e] = 0;
+                    for (int e = 0; e < n * (int)sizeof(T); ++e) w[e] = 0;
                 } else if (p.q_vec) {
 #pragma unroll
-                    for (int e = 0; e < (int)sizeof(T); ++e) {
+                    for (int e = 0; e < n * (int)sizeof(T) / 4; ++e) {
                         const uint4 u = *reinterpret_cast<const uint4 *>(q + d + e * (16 / (int)sizeof(T)));
                         w[4 * e] = u.x; w[4 * e + 1] = u.y; w[4 * e + 2] = u.z; w[4 * e + 3] = u.w;
                     }
                 } else if constexpr (SPLIT) {
 #pragma unroll
-                    for (int e = 0; e < 16; ++e) w[e] = __float_as_uint(q[d + e]);
+                    for (int e = 0; e < 4 * n; ++e) w[e] = __float_as_uint(q[d + e]);
                 } else {
                     const unsigned short *h = reinterpret_cast<const unsigned short *>(q + d);
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) w[e] = (uint32_t)h[2 * e] | (uint32_t)h[2 * e + 1] << 16;
+                    for (int e = 0; e < 2 * n; ++e) w[e] = (uint32_t)h[2 * e] | (uint32_t)h[2 * e + 1] << 16;
                 }
             }
         }
@@ -531,17 +565,17 @@ struct Attend {
         for (int nt = 0; nt < NT; ++nt) {
             float most = 0.0f;
 #pragma unroll
-            for (int i = 0; i < S::CH / 4; ++i)
+            for (int i = 0; i < S::PIECES; ++i)
 #pragma unroll
-                for (int e = 0; e < 16; ++e) most = fmaxf(most, fabsf(value(nt, i, e)));
+                for (int e = 0; e < 4 * S::words(i); ++e) most = fmaxf(most, fabsf(value(nt, i, e)));
             most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, 1));
             most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, 2));
             const int k = min(14 - min(exponent(most), 127), 126);
             const float up = pow2(k), mul = p.scale_log2 * pow2(-k);
 #pragma unroll
-            for (int i = 0; i < S::CH / 4; ++i)
+            for (int i = 0; i < S::PIECES; ++i)
 #pragma unroll
-                for (int w = 0; w < 4; ++w) {
+                for (int w = 0; w < S::words(i); ++w) {
                     const float a = value(nt, i, 4 * w) * up, b = value(nt, i, 4 * w + 1) * up,
                                 c = value(nt, i, 4 * w + 2) * up, d = value(nt, i, 4 * w + 3) * up;
                     const uint32_t lo = half_pair(a, b), hi = half_pair(c, d);
@@ -580,10 +614,10 @@ struct Attend {
         else return make_uint2(qf[nt][term][step][0], qf[nt][term][step][1]);
     }
 
-    // The i-th chunk of a key row that this lane reads.
-    __device__ __forceinline__ int key_chunk(int i) const {
-        if constexpr (DT == 64) return j;
-        else return (i >> 1) * 8 + 2 * j + (i & 1);
+    // The first dim of this lane's i-th piece of a key row.
+    __device__ __forceinline__ int key_dim(int i) const {
+        if constexpr (DT <= 96) return i == 0 ? 16 * j : 64 + 8 * j;
+        else return ((i >> 1) * 8 + 2 * j + (i & 1)) * 16;
     }
 
     __device__ __forceinline__ void consume(int s) {
@@ -598,17 +632,28 @@ struct Attend {
 #pragma unroll
             for (int k = 0; k < 4; ++k) sc[nt][k] = rest[nt][k] = 0.0f;
 #pragma unroll
-        for (int i = 0; i < S::CH / 4; ++i) {
+        for (int i = 0; i < S::PIECES; ++i) {
             float dims[NT][4];
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                 for (int k = 0; k < 4; ++k) dims[nt][k] = 0.0f;
-            const int c = key_chunk(i);
-            const uint4 lo = lds16(at + chunk_at<DT>(g, c)), hi = lds16(at + chunk_at<DT>(g + 8, c));
+            const int c = key_dim(i) >> 4;
+            uint4 lo, hi;
+            if constexpr (DT == 96) {
+                if (i == 1) {
+                    const uint2 l = lds8(at + chunk_at<DT>(g, c) + 8 * (j & 1)), h = lds8(at + chunk_at<DT>(g + 8, c) + 8 * (j & 1));
+                    lo = make_uint4(l.x, l.y, 0, 0);
+                    hi = make_uint4(h.x, h.y, 0, 0);
+                }
+            }
+            if (S::words(i) == 4) {
+                lo = lds16(at + chunk_at<DT>(g, c));
+                hi = lds16(at + chunk_at<DT>(g + 8, c));
+            }
             const uint32_t wl[4] = {lo.x, lo.y, lo.z, lo.w}, wh[4] = {hi.x, hi.y, hi.z, hi.w};
 #pragma unroll
-            for (int w = 0; w < 4; ++w) {
+            for (int w = 0; w < S::words(i); ++w) {
                 uint32_t a0, a1, a2, a3;
                 q8_to_f16(wl[w], a0, a2);
                 q8_to_f16(wh[w], a1, a3);
@@ -681,13 +726,20 @@ struct Attend {
             }
         }
         const uint32_t vals = at + S::ROWS;
-        if constexpr (DT == 64) {
-            // 8 dims a lane: half a chunk of each of its four tokens
+        if constexpr (DT <= 96) {
+            // 8 dims of 64 a lane: half a chunk of each of its four tokens; of 96, 4 more
             uint2 r[4];
 #pragma unroll
             for (int k = 0; k < 4; ++k) r[k] = lds8(vals + chunk_at<DT>(2 * j + (k & 1) + (k >> 1) * 8, g >> 1) + (g & 1) * 8);
             values(0, r[0].x, r[1].x, r[2].x, r[3].x, pf);
             values(1, r[0].y, r[1].y, r[2].y, r[3].y, pf);
+            if constexpr (DT == 96) {
+                uint32_t w[4];
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                    w[k] = lds4(vals + chunk_at<DT>(2 * j + (k & 1) + (k >> 1) * 8, 4 + (g >> 2)) + (g & 3) * 4);
+                values(2, w[0], w[1], w[2], w[3], pf);
+            }
         } else {
 #pragma unroll
             for (int i = 0; i < S::CH / 8; ++i) {
@@ -762,8 +814,9 @@ struct Attend {
 
     // The dim of acc[i][.][0 or 1]; [2 or 3] is the next one.
     __device__ __forceinline__ int dim_of(int i) const {
-        const int word = i >> 1, base = DT == 64 ? 8 * g : 16 * (g + 8 * (word >> 2));
-        return base + 4 * (DT == 64 ? word : word & 3) + 2 * (i & 1);
+        const int word = i >> 1;
+        if (DT <= 96) return (word < 2 ? 8 * g + 4 * word : 64 + 4 * g) + 2 * (i & 1);
+        return 16 * (g + 8 * (word >> 2)) + 4 * (word & 3) + 2 * (i & 1);
     }
 
     // The sums of p over the warp's lanes (each lane's heads 2j and 2j + 1).

@@ -1,4 +1,4 @@
-// attend_128.cu -- attend.cuh for heads of 80 to 128 elements.
+// attend_128.cu -- attend.cuh for heads of 112 and 128 elements.
 #include "attend.cuh"
 
 namespace sgemm_gb300 {
