@@ -5,24 +5,21 @@
 namespace sgemm_gb300 {
 namespace {
 
-// The form that heads of D run in.  96: 16 sequences of 16384, heads of 96 86 us in 128, 75 here,
-// of 80 95 and 82; FP32 108 and 91, 116 and 94.
-int padded(int D) { return D <= 64 ? 64 : D <= 96 ? 96 : D <= 128 ? 128 : 256; }
+// The form that heads of D run in (8 key heads of 8, 16 sequences of 16384: heads of 96 in 128 86
+// us, in 96 75; of 80 95 and 82; of 192 in 256 154, in 192 139; of 144 154 and 121; FP32 96 108 and 91,
+// 192 187 and 147).
+int padded(int D) { return D <= 64 ? 64 : D <= 96 ? 96 : D <= 128 ? 128 : D <= 192 ? 192 : 256; }
 
 // Sets of 8 MMA columns.  More than 8 query heads to a key head take up to four sets,
 // which read a strip once for all (8 key heads, 16 sequences of 16384: 16 heads of 64 71 us against
 // 113 for two sets of 8 one after the other, 128: 106 and 172; 24 heads of 64 89 against 139 for two
 // times two sets, 128: 140 and 214; 32 heads 102 and 139, 164 and 214; FP32, three sets against two
-// times two, 64: 120 and 199, 128: 200 and 306).  Heads beyond 128 take two, in FP32 one: more
-// leave too few registers or warps (24 heads of 256 in three sets 398 us, in two times two 362;
-// FP32, two sets 213, two times one 200).
-int most_tiles(const AttendArgs &a) {
-    const bool bf16 = a.type == kTypeBf16;
-    return padded(a.D) == 256 ? (bf16 ? 2 : 1) : bf16 ? 4 : 3;
-}
+// times two, 64: 120 and 199, 128: 200 and 306).  Heads of 192 take two (16 heads
+// 155 us, 8 139; FP32 217 and 147), of 256 two, in FP32 one: more leave too few registers or warps (24
+// heads of 256 in three sets 398 us, in two times two 362; FP32, two sets 213, two times one 200).
 // As few times as that allows, alike.
 int tiles(const AttendArgs &a) {
-    const int sets = (a.G + 7) / 8, times = (sets - 1) / most_tiles(a) + 1;
+    const int sets = (a.G + 7) / 8, times = (sets - 1) / attend_sets(padded(a.D), a.type == kTypeBf16) + 1;
     return (sets + times - 1) / times;
 }
 
@@ -75,6 +72,7 @@ cudaError_t launch_attend(const AttendArgs &a, void *workspace, unsigned *ticket
         case 64: return launch_attend_64(p, a.type, nt, a.sm_count, a.stream);
         case 96: return launch_attend_96(p, a.type, nt, a.sm_count, a.stream);
         case 128: return launch_attend_128(p, a.type, nt, a.sm_count, a.stream);
+        case 192: return launch_attend_192(p, a.type, nt, a.sm_count, a.stream);
         default: return launch_attend_256(p, a.type, nt, a.sm_count, a.stream);
     }
 }

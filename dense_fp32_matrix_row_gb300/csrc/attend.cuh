@@ -65,7 +65,7 @@ struct AttendParams {
     int B, Hk, G, D, groups;               // groups: of 8*NT query heads to a key head
     int page, width;
     uint32_t page_mul, page_shift;         // t / page = (t * page_mul) >> page_shift (host: divider())
-    uint32_t chunk_mul;                    // q / chunks of a row = (q * chunk_mul) >> 16 for q < 128
+    uint32_t chunk_mul;                    // q / chunks of a row = (q * chunk_mul) >> 16 for q < 192
     int whole;                             // a strip lies within a page
     int window;
     float scale_log2;                      // scale * log2(e)
@@ -87,13 +87,18 @@ struct AttendParams {
 cudaError_t launch_attend_64(const AttendParams &p, int type, int nt, int sms, cudaStream_t stream);
 cudaError_t launch_attend_96(const AttendParams &p, int type, int nt, int sms, cudaStream_t stream);
 cudaError_t launch_attend_128(const AttendParams &p, int type, int nt, int sms, cudaStream_t stream);
+cudaError_t launch_attend_192(const AttendParams &p, int type, int nt, int sms, cudaStream_t stream);
 cudaError_t launch_attend_256(const AttendParams &p, int type, int nt, int sms, cudaStream_t stream);
+// The most sets of 8 query heads that a form takes (see attend.cu).
+constexpr int attend_sets(int dt, bool bf16) { return dt <= 128 ? (bf16 ? 4 : 3) : dt == 192 ? 2 : bf16 ? 2 : 1; }
 // Warps of a block, as many as 65536 registers hold, as many on each quarter of an SM
 // (terms: 2 for FP32; 16 sequences of 16384, 8 key heads: 3 sets of heads of 64 with 8 warps 205
 // us, with 12 173; of 128 with 8 150, with 10 178.  FP32 heads of 128 with 12 109, with 16 106,
 // but 7 short sequences 12.7 and 13.5).
 constexpr int attend_warps(int dt, int nt, int terms) {
-    return dt == 64 ? (nt > 2 ? 12 : 16) : dt == 256 ? 8 : nt * terms == 1 ? 16 : nt <= 2 || (dt == 96 && nt * terms == 3) ? 12 : 8;
+    const int n = nt * terms;
+    return dt == 64 ? (nt > 2 ? 12 : 16) : dt == 96 ? (n == 1 ? 16 : n <= 3 || nt == 2 ? 12 : 8)
+         : dt == 128 ? (n == 1 ? 16 : nt <= 2 ? 12 : 8) : dt == 192 && n == 1 ? 12 : 8;
 }
 // Floats of one part: sums of 8*nt heads, then each head's m and sum of p.
 constexpr int attend_part(int dt, int nt) { return 8 * nt * (dt + 2); }
@@ -202,7 +207,7 @@ struct Shape {
     // Where a strip's chunks go is kept, rather than found for each strip, where registers
     // are left for it (heads of 128, 16 to a key head 109 -> 107 us, FP32, 8, 107 -> 104, but bf16,
     // 8, 91 -> 94).
-    static constexpr bool PLACES = DT < 256 && NT * TERMS > 1;
+    static constexpr bool PLACES = DT < 256 && (DT == 192 || NT * TERMS > 1);
     static constexpr int QUERIES = Q_SHARED ? NT * TERMS * STEPS * 256 : 0;       // a warp
     static constexpr int NOTES = WARPS * (72 + 8) + 128;      // see the kernel
     static constexpr int ROOM = 227 * 1024 - 128 - NOTES - WARPS * QUERIES;
@@ -217,11 +222,13 @@ struct Shape {
 // that neither the keys' reads (8 lanes: 2 rows, 4 chunks of each) nor the values'
 // (8 lanes: 4 rows, 2 chunks) meet in a bank.  96: rows lie as 128 do; 16 lanes read
 // halves of chunks (keys: 4 rows, 2 chunks of each; values: every other of 8 rows).
+// 192: eight chunks of each row as 128, then four as 64.
 // Packed closer, with one more stage, four chunks of a row apart from its other two: 75 -> 79 us.
 template <int DT>
 __device__ __forceinline__ uint32_t chunk_at(int r, int c) {
     if constexpr (DT == 64) return (uint32_t)((r >> 1) * 128 + ((((r & 1) * 4 + c) ^ (r & 6)) << 4));
     else if constexpr (DT == 96) return (uint32_t)(r * 128 + ((c ^ (((r ^ r >> 2) & 1) << 2 | (r & 2))) << 4));
+    else if constexpr (DT == 192) return c < 8 ? chunk_at<128>(r, c) : 2048 + chunk_at<64>(r, c - 8);
     else return (uint32_t)(r * DT + (c >> 3) * 128 + (((c & 7) ^ (r & 7)) << 4));
 }
 
@@ -406,7 +413,7 @@ struct Attend {
     uint32_t ring;          // this warp's stages
     uint32_t queries;       // Q_SHARED: this warp's
     int warp, lane, g, j;
-    uint32_t places[S::PLACES ? S::PIECES : 1];     // find_place() of 2 * i and 2 * i + 1
+    uint32_t places[S::PLACES ? (S::CH + 3) / 4 : 1];     // find_place() of 2 * i and 2 * i + 1
 
     // the strip to be loaded next
     Cursor next;
@@ -423,7 +430,7 @@ struct Attend {
         ring = smem + warp * (S::STAGES * S::STAGE);
         if constexpr (S::PLACES) {
 #pragma unroll
-            for (int i = 0; i < S::PIECES; ++i) places[i] = find_place(2 * i) | find_place(2 * i + 1) << 16;
+            for (int i = 0; i < (S::CH + 3) / 4; ++i) places[i] = find_place(2 * i) | find_place(2 * i + 1) << 16;
         }
         queries = smem + S::WARPS * (S::STAGES * S::STAGE) + warp * S::QUERIES;
     }
@@ -619,6 +626,7 @@ struct Attend {
     // The first dim of this lane's i-th piece of a key row.
     __device__ __forceinline__ int key_dim(int i) const {
         if constexpr (DT <= 96) return i == 0 ? 16 * j : 64 + 8 * j;
+        else if (DT == 192 && i == 2) return 128 + 16 * j;
         else return ((i >> 1) * 8 + 2 * j + (i & 1)) * 16;
     }
 
@@ -753,6 +761,13 @@ struct Attend {
                 values(4 * i + 2, r[0].z, r[1].z, r[2].z, r[3].z, pf);
                 values(4 * i + 3, r[0].w, r[1].w, r[2].w, r[3].w, pf);
             }
+            if constexpr (DT == 192) {
+                uint2 r[4];
+#pragma unroll
+                for (int k = 0; k < 4; ++k) r[k] = lds8(vals + chunk_at<DT>(2 * j + (k & 1) + (k >> 1) * 8, 8 + (g >> 1)) + (g & 1) * 8);
+                values(4, r[0].x, r[1].x, r[2].x, r[3].x, pf);
+                values(5, r[0].y, r[1].y, r[2].y, r[3].y, pf);
+            }
         }
     }
 
@@ -818,6 +833,7 @@ struct Attend {
     __device__ __forceinline__ int dim_of(int i) const {
         const int word = i >> 1;
         if (DT <= 96) return (word < 2 ? 8 * g + 4 * word : 64 + 4 * g) + 2 * (i & 1);
+        if (DT == 192 && word >= 4) return 128 + 8 * g + 4 * (word & 3) + 2 * (i & 1);
         return 16 * (g + 8 * (word >> 2)) + 4 * (word & 3) + 2 * (i & 1);
     }
 
@@ -1232,12 +1248,15 @@ cudaError_t attend_of_dim(const AttendParams &p, int type, int nt, int sms, cuda
     const bool b = type == kTypeBf16;
     if (nt == 1) return b ? attend_launch<DT, 1, B>(p, sms, stream) : attend_launch<DT, 1, float>(p, sms, stream);
     if (b && nt == 2) return attend_launch<DT, 2, B>(p, sms, stream);
-    if constexpr (DT < 256) {
-        if (nt == 2) return attend_launch<DT, 2, float>(p, sms, stream);
-        if (nt == 3) return b ? attend_launch<DT, 3, B>(p, sms, stream) : attend_launch<DT, 3, float>(p, sms, stream);
+    if constexpr (attend_sets(DT, false) >= 2)
+        if (!b && nt == 2) return attend_launch<DT, 2, float>(p, sms, stream);
+    if constexpr (attend_sets(DT, false) >= 3)
+        if (!b && nt == 3) return attend_launch<DT, 3, float>(p, sms, stream);
+    if constexpr (attend_sets(DT, true) >= 3)
+        if (b && nt == 3) return attend_launch<DT, 3, B>(p, sms, stream);
+    if constexpr (attend_sets(DT, true) >= 4)
         if (b && nt == 4) return attend_launch<DT, 4, B>(p, sms, stream);
-    }
-    return cudaErrorInvalidConfiguration;       // not one of most_tiles()
+    return cudaErrorInvalidConfiguration;       // more than attend_sets()
 }
 
 }  // namespace

@@ -1,4 +1,4 @@
-// attend_256.cu -- attend.cuh for heads of 144 to 256 elements.
+// attend_256.cu -- attend.cuh for heads of 208 to 256 elements.
 #include "attend.cuh"
 
 namespace sgemm_gb300 {

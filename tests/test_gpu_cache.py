@@ -431,6 +431,16 @@ def test_attend_many_heads_of_a_key_head(G, dt):
 
 
 @pytest.mark.parametrize("dt", ["fp32", "bf16"])
+@pytest.mark.parametrize("D", [80, 96, 144, 160, 176, 192, 208])
+def test_attend_head_sizes_between(D, dt):
+    """Sizes that their form has more room than: chunks and dims behind the head's."""
+    for G in (1, 9, 17):
+        check_attend([1, 0, 16, 333], 2, G, D, 16, dt)
+        check_attend([50, 18], 1, G, D, 20, dt, pad=1)
+    check_attend([9000, 3], 2, 5, D, 32, dt, q_scale=1.0)
+
+
+@pytest.mark.parametrize("dt", ["fp32", "bf16"])
 @pytest.mark.parametrize("window", [1, 2, 15, 16, 17, 64, 100, 5000])
 def test_attend_window(window, dt):
     check_attend(LENS + [700], 2, 4, 64, 16, dt, window=window)
