@@ -205,9 +205,9 @@ struct Shape {
     // take less, heads of 80, 16, 99 and 106).
     static constexpr bool Q_SHARED = NT * TERMS > 1 && !(DT == 96 && NT * TERMS == 2);
     // Where a strip's chunks go is kept, rather than found for each strip, where registers
-    // are left for it (heads of 128, 16 to a key head 109 -> 107 us, FP32, 8, 107 -> 104, but bf16,
-    // 8, 91 -> 94).
-    static constexpr bool PLACES = DT < 256 && (DT == 192 || NT * TERMS > 1);
+    // are left for it (heads of 96 78 -> 75 us, of 128, 16 to a key head, 109 -> 107, FP32, 8, 107 -> 104,
+    // but bf16, 8, 91 -> 94).
+    static constexpr bool PLACES = DT < 256 && (DT != 128 || NT * TERMS > 1);
     static constexpr int QUERIES = Q_SHARED ? NT * TERMS * STEPS * 256 : 0;       // a warp
     static constexpr int NOTES = WARPS * (72 + 8) + 128;      // see the kernel
     static constexpr int ROOM = 227 * 1024 - 128 - NOTES - WARPS * QUERIES;
