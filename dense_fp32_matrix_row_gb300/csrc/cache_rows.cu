@@ -18,7 +18,7 @@
 //
 // Measured: 8192 tokens of 32 + 8 heads of 128, bf16, 172 MB, 31.5 us, 5.5 TB/s (82% of
 // a copy's; issue slots 73% taken); in FP32, 340 MB, 51.2 us, 6.6 TB/s.  With keys and
-// 8 heads of values into the cache, 190 MB, 43.5 us.  18432 tokens of 8 + 8 heads read
+// 8 heads of values into the cache, 190 MB, 40.6 us.  18432 tokens of 8 + 8 heads read
 // back, 114 MB, 20.1 us, 5.7 TB/s.  One token 1.5 us.  Not kept (first case): 16 elements
 // a lane 40 us, eight heads to a group one half after the other 44, one kernel for
 // floats and cache 33.0, a question for each load whether its head is there 34.8.
@@ -54,7 +54,8 @@ struct RowsParams {
     // units: groups of U heads; per token, and of this launch over all its tokens
     int q_units, k_units, float_units, cache_units;
     int64_t first, float_count, cache_count;
-    int float_blocks;
+    unsigned cache_begin, cache_blocks;
+    int sms;
     unsigned *err;
 };
 
@@ -391,17 +392,20 @@ __device__ __forceinline__ void head_rows(const RowsParams &a, uint32_t idx, uin
     }
 }
 
-// The first float_blocks blocks write floats, the rest (with MIXED) write the cache.
+// With MIXED, cache_blocks blocks from cache_begin on write the cache, the others floats:
+// those alone without it.  The cache first where there is more than a wave, as its blocks
+// take longer and the end is short (8192 tokens 40.6 us, floats first 43.1, both kinds mixed
+// 42.2), otherwise last (777 FP32 tokens of 20 heads of 96, read back as well: 6.8 us, first 7.7).
 template <typename T, bool VEC, bool FULL, bool INTER, bool MIXED, int LANES, int U>
 __global__ void __launch_bounds__(kThreads, MIXED ? 8 : 9) head_rows_kernel(const __grid_constant__ RowsParams a) {
     pdl_wait();
     pdl_trigger();
     const uint32_t group = threadIdx.x / LANES, per = kThreads / LANES;
-    if (!MIXED || blockIdx.x < (unsigned)a.float_blocks) {
-        head_rows<T, VEC, FULL, INTER, false, LANES, U>(a, blockIdx.x * per + group, (uint32_t)a.float_count, a.float_units,
-                                                        a.q_units);
+    if (!MIXED || blockIdx.x - a.cache_begin >= a.cache_blocks) {
+        const uint32_t at = MIXED && a.cache_begin == 0 ? blockIdx.x - a.cache_blocks : blockIdx.x;
+        head_rows<T, VEC, FULL, INTER, false, LANES, U>(a, at * per + group, (uint32_t)a.float_count, a.float_units, a.q_units);
     } else if constexpr (MIXED) {
-        head_rows<T, VEC, FULL, INTER, true, LANES, U>(a, (blockIdx.x - a.float_blocks) * per + group,
+        head_rows<T, VEC, FULL, INTER, true, LANES, U>(a, (blockIdx.x - a.cache_begin) * per + group,
                                                        (uint32_t)a.cache_count, a.cache_units, a.k_units);
     }
 }
@@ -527,8 +531,10 @@ cudaError_t rows_launch(RowsParams p, cudaStream_t stream) {
         p.first = t;
         p.float_count = n * p.float_units;
         p.cache_count = n * p.cache_units;
-        p.float_blocks = (int)((p.float_count + per - 1) / per);
-        const unsigned blocks = (unsigned)(p.float_blocks + (p.cache_count + per - 1) / per);
+        const unsigned float_blocks = (unsigned)((p.float_count + per - 1) / per);
+        p.cache_blocks = (unsigned)((p.cache_count + per - 1) / per);
+        const unsigned blocks = float_blocks + p.cache_blocks;
+        p.cache_begin = blocks > 8u * p.sms ? 0 : float_blocks;
         const cudaError_t e =
             launch_dependent(cached ? head_rows_kernel<T, VEC, FULL, INTER, true, LANES, U>
                                     : head_rows_kernel<T, VEC, FULL, INTER, false, LANES, U>, blocks, kThreads, 0, stream, p);
@@ -553,7 +559,7 @@ cudaError_t rows_lanes(const RowsParams &p, cudaStream_t stream) {
 }
 
 template <typename T, bool INTER>
-cudaError_t rows_type(RowsParams p, cudaStream_t stream, int sm_count) {
+cudaError_t rows_type(const RowsParams &p, cudaStream_t stream) {
     constexpr int es = sizeof(T), bytes = 4 * es;
     const bool vec = p.pairs % 4 == 0 && aligned(p.q, es, bytes) && aligned(p.k, es, bytes) && aligned(p.v, es, bytes) &&
                      aligned(p.q_out, es, bytes) && aligned(p.k_out, es, bytes) && aligned(p.cos, 16) &&
@@ -564,13 +570,13 @@ cudaError_t rows_type(RowsParams p, cudaStream_t stream, int sm_count) {
     // (tokens of 32 + 8 heads of 128 in bf16: 128 tokens 2.3 us against 2.0 with single heads,
     // 256 2.5 and 2.7, 1024 4.7 and 6.9, 4096 17.7 and 26.7).
     const int lanes = p.D <= 64 ? 8 : p.D <= 128 ? 16 : 32;
-    if (p.T * (p.q.n + p.k.n + p.v.n) * lanes <= (int64_t)sm_count * 1024) return rows_lanes<T, true, INTER, 1>(p, stream);
+    if (p.T * (p.q.n + p.k.n + p.v.n) * lanes <= (int64_t)p.sms * 1024) return rows_lanes<T, true, INTER, 1>(p, stream);
     return rows_lanes<T, true, INTER, 8 / es>(p, stream);
 }
 
 template <typename T>
-cudaError_t rows_of(const RowsParams &p, cudaStream_t stream, int sm_count) {
-    return p.interleaved && p.pairs > 0 ? rows_type<T, true>(p, stream, sm_count) : rows_type<T, false>(p, stream, sm_count);
+cudaError_t rows_of(const RowsParams &p, cudaStream_t stream) {
+    return p.interleaved && p.pairs > 0 ? rows_type<T, true>(p, stream) : rows_type<T, false>(p, stream);
 }
 
 template <typename T, bool VEC, int LANES, int IT, int U>
@@ -623,9 +629,10 @@ cudaError_t launch_head_rows(const HeadRowsArgs &a) {
     p.cos = a.rotary.cos; p.sin = a.rotary.sin;
     p.rows = a.rotary.rows; p.ldt = a.rotary.ld; p.positions = a.rotary.positions;
     p.slots = a.slots; p.cache = a.cache;
+    p.sms = a.sm_count;
     p.err = a.err;
-    return a.type == kTypeBf16 ? rows_of<__nv_bfloat16>(p, a.stream, a.sm_count)
-                               : rows_of<float>(p, a.stream, a.sm_count);
+    return a.type == kTypeBf16 ? rows_of<__nv_bfloat16>(p, a.stream)
+                               : rows_of<float>(p, a.stream);
 }
 
 cudaError_t launch_cache_read(const CacheReadArgs &a) {
