@@ -59,7 +59,7 @@ Range range_of(const sgemm_heads *h, int64_t T, int64_t D, size_t es) {
 // In place: the same elements in the same places.
 bool same(const Range &a, const Range &b) {
     return a.heads && b.heads && a.heads->p == b.heads->p && a.heads->heads == b.heads->heads &&
-           a.heads->ld == b.heads->ld && a.heads->hs == b.heads->hs;
+           a.heads->ld == b.heads->ld && (a.heads->heads == 1 || a.heads->hs == b.heads->hs);
 }
 
 // Heads of T > 0 tokens.
@@ -68,7 +68,9 @@ int check_heads(const sgemm_heads *h, int64_t T, int64_t D, int type, bool outpu
     if (h->heads < 0 || h->heads > kMaxHeads) return SGEMM_ERR_BAD_DIM;
     if (h->p == nullptr) return SGEMM_ERR_NULL_PTR;
     if (h->ld < 0 || h->hs < 0) return SGEMM_ERR_BAD_LD;
-    if (h->ld > kMaxElems || h->hs > kMaxElems / kMaxHeads || (h->ld > 0 && T > kMaxElems / h->ld)) return SGEMM_ERR_BAD_DIM;
+    // hs leads from head to head: of a single one it is not used
+    if (h->ld > kMaxElems || (h->heads > 1 && h->hs > kMaxElems / h->heads) || (h->ld > 0 && T > kMaxElems / h->ld))
+        return SGEMM_ERR_BAD_DIM;
     if (output) {
         const bool by_token = (h->heads == 1 || h->hs >= D) && (T == 1 || h->ld >= (h->heads - 1) * h->hs + D);
         const bool by_head = (T == 1 || h->ld >= D) && (h->heads == 1 || h->hs >= (T - 1) * h->ld + D);
@@ -152,7 +154,10 @@ int launch_status(cudaError_t e) {
     return SGEMM_ERR_CUDA;
 }
 
-sgemm_heads value(const sgemm_heads *h) { return there(h) ? *h : sgemm_heads{nullptr, 0, 0, 0}; }
+sgemm_heads value(const sgemm_heads *h) {
+    if (!there(h)) return sgemm_heads{nullptr, 0, 0, 0};
+    return sgemm_heads{h->p, h->heads, h->ld, h->heads > 1 ? h->hs : 0};
+}
 
 // The three calls on new tokens' heads; `cache` nullptr: float results alone.
 int head_rows(int64_t T, int64_t D, int type, const sgemm_heads *q, const sgemm_heads *q_out, const float *q_weight,
@@ -363,7 +368,7 @@ int sgemm_q8_attend(int64_t B, int type, const sgemm_heads *q, const sgemm_q8_ca
     if (o.overlaps(l) || c.overlaps(o) || c.overlaps(l)) return SGEMM_ERR_ALIAS;
     AttendArgs a{};
     a.B = (int)B; a.Hk = (int)cache->heads; a.G = (int)(q->heads / cache->heads); a.D = (int)cache->dim; a.type = type;
-    a.q = *q; a.out = *out;
+    a.q = value(q); a.out = value(out);
     a.cache = *cache;
     a.table = table; a.ld_table = ld_table; a.width = (int)pages; a.lens = lens;
     a.scale = scale;

@@ -349,10 +349,12 @@ int sgemm_q8_moe(int64_t T, int64_t E, int64_t top_k, int64_t H, int64_t I, cons
  *             (views of a joint projection's rows, or stored head by head); in
  *             an output no two elements may share a place: ld >= (heads-1)*hs +
  *             dim with hs >= dim, or hs >= (tokens-1)*ld + dim with ld >= dim
- *             (SGEMM_ERR_BAD_LD).  Outputs do not overlap inputs or other outputs
- *             (SGEMM_ERR_ALIAS; heads of one token stride may alternate, as
- *             queries and keys in joint rows do); q_out may be q itself and
- *             k_out k itself (the same pointer and strides).
+ *             (SGEMM_ERR_BAD_LD).  tokens * ld and, of several heads, heads * hs are
+ *             at most 2^40 (SGEMM_ERR_BAD_DIM); the hs of a single head is not used.
+ *             Outputs do not overlap inputs or other outputs (SGEMM_ERR_ALIAS;
+ *             heads of one token stride may alternate, as queries and keys in
+ *             joint rows do); q_out may be q itself and k_out k itself (the same
+ *             pointer and strides).
  * Cache       sgemm_q8_cache: `blocks` pages of `page` tokens each.  Token row r
  *             of page i, head h: dim bytes at k[i*k_stride + (h*page + r)*dim],
  *             their scale at k_scale[i*k_scale_stride + h*page + r]; v alike.
