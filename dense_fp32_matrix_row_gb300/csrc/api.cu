@@ -440,7 +440,7 @@ const char *sgemm_status_string(int status) {
         case SGEMM_ERR_TOO_LARGE:
             return "problem beyond a fixed limit of the entry point: the fixed scratch of sgemm_noalloc "
                    "(K * round_up(M, 4) floats > 16777216), sgemm_q8_moe's tokens, experts or top_k, or "
-                   "sgemm_q8_attend's sequences * heads * pages";
+                   "sgemm_q8_attend's sequences * key heads * pages";
         default: return "unknown status";
     }
 }

@@ -347,14 +347,15 @@ int sgemm_q8_attend(int64_t B, int type, const sgemm_heads *q, const sgemm_q8_ca
     if (B < 0 || B > (1 << 30) || pages < 0 || pages > INT32_MAX / cache->page) return SGEMM_ERR_BAD_DIM;
     if (!known_type(type) || !std::isfinite(scale) || window < 0) return SGEMM_ERR_BAD_ARG;
     if (B == 0) return SGEMM_OK;
-    // the kernel counts all sequences' strips of 16 tokens in 32 bits
-    if (there(q) && q->heads > 0 && (pages * cache->page / 16 + 2) * std::min(q->heads, kMaxHeads) > INT32_MAX / B)
-        return SGEMM_ERR_TOO_LARGE;
     if (!there(q) || !there(out) || lens == nullptr || (table == nullptr && pages > 0)) return SGEMM_ERR_NULL_PTR;
     rc = check_heads(q, B, cache->dim, type, false);
     if (rc == SGEMM_OK) rc = check_heads(out, B, cache->dim, type, true);
     if (rc != SGEMM_OK) return rc;
     if (q->heads != out->heads || q->heads % cache->heads != 0) return SGEMM_ERR_BAD_DIM;
+    // The kernel counts the strips of 16 tokens of all sequences, key heads and groups of query
+    // heads in 32 bits.  A group takes 8 heads at least.
+    const int64_t G = q->heads / cache->heads;
+    if (cache->heads * std::min(G, 2 * ((G + 7) / 8)) * (pages * cache->page / 16 + 2) > INT32_MAX / B) return SGEMM_ERR_TOO_LARGE;
     if (ld_table < pages) return SGEMM_ERR_BAD_LD;
     if (ld_table > 0 && B > kMaxElems / ld_table) return SGEMM_ERR_BAD_DIM;
     if (misaligned(table, 4) || misaligned(lens, 4) || misaligned(lse, 4)) return SGEMM_ERR_BAD_ARG;
@@ -367,7 +368,7 @@ int sgemm_q8_attend(int64_t B, int type, const sgemm_heads *q, const sgemm_q8_ca
     const CacheRanges c(*cache);
     if (o.overlaps(l) || c.overlaps(o) || c.overlaps(l)) return SGEMM_ERR_ALIAS;
     AttendArgs a{};
-    a.B = (int)B; a.Hk = (int)cache->heads; a.G = (int)(q->heads / cache->heads); a.D = (int)cache->dim; a.type = type;
+    a.B = (int)B; a.Hk = (int)cache->heads; a.G = (int)G; a.D = (int)cache->dim; a.type = type;
     a.q = value(q); a.out = value(out);
     a.cache = *cache;
     a.table = table; a.ld_table = ld_table; a.width = (int)pages; a.lens = lens;

@@ -467,7 +467,8 @@ int sgemm_q8_cache_read(int64_t N, int type, const sgemm_q8_cache *cache, const 
  *               that many (both reported).  Tokens of a page outside the cache
  *               are left out (reported).
  *   lse         B x q->heads floats (natural logarithms), or NULL
- * B * q->heads * (pages*page/16 + 2) is below 2^31 (SGEMM_ERR_TOO_LARGE).
+ * B * cache->heads * g * (pages*page/16 + 2) is below 2^31 (SGEMM_ERR_TOO_LARGE), where g is
+ * G = q->heads/cache->heads, but at most 2 * ceil(G/8): 2 for up to 8 query heads to a key head.
  * Several new tokens of a sequence are rows of their own, with a length each.
  * Scores, sums and results are FP32; the exponentials are rounded to 11 bits
  * for the product with the values (22 bits for type FP32; those below about

@@ -41,3 +41,22 @@ def test_the_head_stride_of_a_single_head(fn):
         assert attend(fn, q=q, out=q, c=one) == sg.ERR_ALIAS
         # in its own place, which is allowed: what ends the call is the table in the result's place
         assert rope(fn, q=q, qo=heads(A[2], 1, ld=64, hs=64), qw=None, k=None, ko=None, rot=rotary(cos=A[2])) == sg.ERR_ALIAS
+
+
+@pytest.mark.parametrize("B,n,key_heads,pages", [(32768, 32, 8, 2048), (256, 128, 8, 65536), (4096, 64, 8, 1000), (33000, 64, 4, 2063),
+                                                 (32767, 8, 8, 512), (1, 65535, 1, 8191)])
+def test_strips_that_fit_the_list(fn, B, n, key_heads, pages):
+    """The list holds a strip of 16 tokens once for a key head's group of 8 query heads or
+    more, not once for each query head: rows of a prompt of 32768 tokens and 256
+    sequences with tables for a million tokens."""
+    q = heads(A[0], n)
+    strips = pages + 2
+    g = min(n // key_heads, 2 * -(-n // key_heads // 8))
+    assert B * key_heads * -(-n // key_heads // 8) * strips < B * key_heads * g * strips < 1 << 31 or n == key_heads
+    assert attend(fn, B=B, q=q, out=q, c=pool(heads=key_heads), pages=pages, ldt=pages) == sg.ERR_ALIAS
+
+
+@pytest.mark.parametrize("B,n,key_heads,pages", [(65536, 32, 8, 4096), (65536, 8, 8, 4096), (1 << 27, 64, 1, 0), (131072, 64, 8, 1022)])
+def test_strips_that_do_not(fn, B, n, key_heads, pages):
+    q = heads(A[0], n, ld=0)
+    assert attend(fn, B=B, q=q, out=heads(A[1], n), c=pool(heads=key_heads), pages=pages, ldt=pages) == sg.ERR_TOO_LARGE

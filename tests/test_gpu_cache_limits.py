@@ -67,3 +67,31 @@ def test_long_arrays_stored_head_by_head(dt):
     sg.norm_rope(x[-1:], None, None, None, got[-1:], None, q_weight=w)
     sg.norm_rope(rows[-1:], None, None, None, want[-1:], None, q_weight=w)
     assert sg.status() == sg.OK and torch.equal(got[-1:], want[-1:])
+
+
+@pytest.mark.parametrize("dt", [torch.bfloat16, torch.float32])
+def test_rows_of_a_long_prompt(dt):
+    """33000 tokens of a prompt, a row each, 8 query heads to a key head and a table for
+    32768 tokens: 2^31 strips, were they counted for each query head."""
+    B, Hk, G, D, page, pages = 33000, 2, 16, 64, 16, 2048
+    pool = ref.Pool(40, Hk, page, D)
+    own = torch.randperm(40, device="cuda").to(torch.int32)
+    table = torch.full((B, pages), -1, dtype=torch.int32, device="cuda")
+    table[:, :40] = own
+    lens = (torch.arange(B, device="cuda") % 60 + 1).to(torch.int32)
+    lens[-1], lens[1000] = 40 * page, 0
+    gen = torch.Generator(device="cuda")
+    gen.manual_seed(1)
+    q = torch.randn((B, Hk * G, D), device="cuda", generator=gen).to(dt)
+    out, lse = torch.full_like(q, 9.0), torch.full((B, Hk * G), 9.0, device="cuda")
+    assert B * Hk * G * (pages + 2) > 1 << 31
+    sg.attend_q8(q, pool.cache(), table, lens, out, lse=lse)
+    assert sg.status() == sg.OK
+    some = [0, 1, 59, 999, 1000, 1001, 16384, 32767, 32768, B - 2, B - 1]
+    want, tol, want_lse, lse_tol = ref.attend(q[some], pool, table[some], lens[some].tolist(), D ** -0.5, 0, dt == torch.bfloat16)
+    # (a bf16 result is rounded by half a unit in its last place)
+    tol = tol + (2.0 ** -8 * (1 + 2.0 ** -6) * want.abs() if dt == torch.bfloat16 else 0)
+    assert bool(((out[some].double() - want).abs() <= tol + 2.0 ** -140).all())
+    none = want_lse.isinf()
+    assert torch.equal(lse[some].isinf(), none) and bool(((lse[some].double() - want_lse).abs() <= lse_tol)[~none].all())
+    assert bool(out.isfinite().all()) and not bool((out == 9.0).all(-1).any())
