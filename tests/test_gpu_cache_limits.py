@@ -95,3 +95,96 @@ def test_rows_of_a_long_prompt(dt):
     none = want_lse.isinf()
     assert torch.equal(lse[some].isinf(), none) and bool(((lse[some].double() - want_lse).abs() <= lse_tol)[~none].all())
     assert bool(out.isfinite().all()) and not bool((out == 9.0).all(-1).any())
+
+
+# ---- tensors of a cache that change ---------------------------------------------------
+
+def four(blocks, heads, page, dim, more=0):
+    """Zeroed tensors of a cache; pages `more` rows of all heads further apart."""
+    def one(tail, dtype):
+        t = torch.zeros((blocks, heads * (page + more)) + tail, dtype=dtype, device="cuda")
+        return t[:, :heads * page].view(blocks, heads, page, *tail)
+    return [one((dim,), torch.int8), one((dim,), torch.int8), one((), torch.float32), one((), torch.float32)]
+
+
+def stored(cache, slots, x):
+    sg.cache_write_q8(x, x, cache, slots)
+    out = torch.zeros_like(x)
+    sg.cache_read_q8(cache, slots, None, out)
+    assert sg.status() == sg.OK
+    return out
+
+
+def give(tensors, others):
+    for t, other in zip(tensors, others):
+        t.data = other
+
+
+@pytest.mark.parametrize("kind", ["pages", "strides", "heads"])
+def test_a_cache_follows_its_tensors_layout(kind):
+    """Tensors that get another shape or other strides at the same address are used as
+    they then are: what a new CacheQ8 around them would give."""
+    gen = torch.Generator(device="cuda")
+    gen.manual_seed(2)
+    old = four(6, 2, 16, 64, more=8)
+    cache = sg.CacheQ8(*old)
+    x = torch.randn((30, 2, 64), device="cuda", generator=gen)
+    slots = torch.randperm(48, device="cuda", generator=gen)[:30]
+    stored(cache, slots, x)
+    whole = [t.as_strided((6 * 2 * 24,) + t.shape[3:], (t.stride(2),) + t.stride()[3:]) for t in old]   # all rows there are
+    shape, strided = {"pages": ((12, 2, 8), 24), "strides": ((6, 2, 16), 40), "heads": ((6, 1, 16), 48)}[kind]
+    new = [w.as_strided(shape + w.shape[1:], tuple(n * w.stride(0) for n in (strided, shape[2], 1)) + w.stride()[1:])
+           for w in whole]
+    if kind == "heads":
+        x = x[:, :1].contiguous()
+    for w in whole:
+        w.zero_()
+    give(old, new)
+    assert old[0].data_ptr() == whole[0].data_ptr()
+    got = stored(cache, slots, x)
+    seen = [w.clone() for w in whole]
+    for w in whole:
+        w.zero_()
+    want = stored(sg.CacheQ8(*new), slots, x)
+    assert torch.equal(got, want) and bool(got.any())
+    for a, b in zip(seen, whole):
+        assert torch.equal(a, b)
+    assert (cache.heads, cache.page, cache.slots) == (shape[1], shape[2], shape[0] * shape[2])
+
+
+def test_a_cache_that_has_shrunk():
+    """Slots and pages behind its end are outside it, though their memory is still there."""
+    tensors = four(8, 1, 16, 64)
+    kept = [t.detach() for t in tensors]
+    cache = sg.CacheQ8(*tensors)
+    x = torch.randn((2, 1, 64), device="cuda")
+    stored(cache, torch.tensor([3, 100], device="cuda"), x)
+    give(tensors, [t[:2] for t in kept])
+    before = [t.clone() for t in kept]
+    sg.cache_write_q8(x + 1, x, cache, torch.tensor([32, 127], device="cuda"))
+    assert sg.status() == sg.ERR_BAD_INDEX
+    q, out = torch.randn((1, 2, 64), device="cuda"), torch.full((1, 2, 64), 9.0, device="cuda")
+    sg.attend_q8(q, cache, torch.tensor([[6]], dtype=torch.int32, device="cuda"), torch.tensor([5], dtype=torch.int32, device="cuda"), out)
+    assert sg.status() == sg.ERR_BAD_INDEX and float(out.abs().max()) == 0
+    for a, b in zip(before, kept):
+        assert torch.equal(a, b)
+
+
+def test_a_cache_with_a_tensor_replaced():
+    a, b = four(4, 2, 16, 64), four(9, 2, 16, 64)
+    cache = sg.CacheQ8(*a)
+    x = torch.randn((5, 2, 64), device="cuda")
+    slots = torch.arange(60, 65, device="cuda")         # the second pool alone has them all
+    cache.k, cache.v = b[0], b[1]
+    with pytest.raises(ValueError):                     # scales of another number of pages
+        sg.cache_write_q8(x, x, cache, slots)
+    with pytest.raises(ValueError):
+        sg.cache_write_q8(x, x, cache, slots)
+    cache.k_scale, cache.v_scale = b[2], b[3]
+    got = stored(cache, slots, x)
+    assert cache.slots == 9 * 16
+    want = stored(sg.CacheQ8(*four(9, 2, 16, 64)), slots, x)
+    assert torch.equal(got, want) and bool((b[0] != 0).any()) and not bool(a[0].any())
+    cache.k = cache.v = cache.k_scale = cache.v_scale = None
+    with pytest.raises(TypeError):
+        sg.cache_write_q8(x, x, cache, slots)
