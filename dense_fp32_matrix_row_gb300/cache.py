@@ -49,13 +49,15 @@ def _load():
 # leaves: each asks a tensor only for what it needs, at 0.1 us an answer.
 
 def _heads(t, name, dtype, shape, index):
-    """Checks heads of this type and shape on CUDA device `index`; their sgemm_heads."""
-    if not isinstance(t, _Tensor):
-        raise TypeError(f"{name} must be a torch tensor")
-    if t.dtype is not dtype:
-        raise TypeError(f"{name} must be of type {dtype}, not {t.dtype}")
-    if t.shape != shape:
-        raise ValueError(f"{name} must have shape {tuple(shape)}, not {tuple(t.shape)}")
+    """Checks heads of this type (None: type and shape are known to be right) and shape on
+    CUDA device `index`; their sgemm_heads."""
+    if dtype is not None:
+        if not isinstance(t, _Tensor):
+            raise TypeError(f"{name} must be a torch tensor")
+        if t.dtype is not dtype:
+            raise TypeError(f"{name} must be of type {dtype}, not {t.dtype}")
+        if t.shape != shape:
+            raise ValueError(f"{name} must have shape {tuple(shape)}, not {tuple(t.shape)}")
     T, H, D = shape
     if T == 0 or H == 0:
         return _HEADS(0, 0, 0, 0)
@@ -206,14 +208,14 @@ def norm_rope(q, k, cos, sin, q_out, k_out, positions=None, q_weight=None, k_wei
     T, _, D = shape
     cq = cqo = ck = cko = pq = pk = None
     if q is not None:
-        cq, cqo = _heads(q, "q", dt, shape, dev), _heads(q_out, "q_out", dt, shape, dev)
+        cq, cqo = _heads(q, "q", None, shape, dev), _heads(q_out, "q_out", dt, shape, dev)
         if q_weight is not None:
             pq = _vector(q_weight, "q_weight", _F32, (D,), dev)
     if k is not None:
         kshape = _shape3(k, "k")
         if kshape[0] != T or kshape[2] != D:
             raise ValueError(f"k must have shape ({T}, heads, {D}), not {tuple(kshape)}")
-        ck, cko = _heads(k, "k", dt, kshape, dev), _heads(k_out, "k_out", dt, kshape, dev)
+        ck, cko = _heads(k, "k", dt if k is not lead else None, kshape, dev), _heads(k_out, "k_out", dt, kshape, dev)
         if k_weight is not None:
             pk = _vector(k_weight, "k_weight", _F32, (D,), dev)
     rotary = _rotary(cos, sin, positions, interleaved, T, dev)
@@ -242,7 +244,9 @@ def norm_rope_write_q8(q, k, v, cos, sin, q_out, cache, slots, positions=None, q
     shape, dev, dt = _shape3(k, "k"), cache._device, _type(k, "k")
     T = shape[0]
     want = (T, cache.heads, cache.dim)
-    ck, cv = _heads(k, "k", dt, want, dev), _heads(v, "v", dt, want, dev)
+    if shape != want:
+        raise ValueError(f"k must have shape {want}, not {tuple(shape)}")
+    ck, cv = _heads(k, "k", None, want, dev), _heads(v, "v", dt, want, dev)
     at = _vector(slots, "slots", _I64, (T,), dev)
     cq = cqo = pq = pk = None
     if q is not None:
@@ -269,12 +273,16 @@ def cache_read_q8(cache, slots, k_out=None, v_out=None, stream=None) -> None:
     lead = k_out if k_out is not None else v_out
     if lead is None:
         raise ValueError("cache_read_q8 needs k_out or v_out")
-    N, dev, dt = _shape3(lead, "the output")[0], lead.get_device(), _type(lead, "the output")
+    name = "k_out" if k_out is not None else "v_out"
+    shape, dev, dt = _shape3(lead, name), lead.get_device(), _type(lead, name)
+    N = shape[0]
     want = (N, cache.heads, cache.dim)
+    if shape != want:
+        raise ValueError(f"{name} must have shape {want}, not {tuple(shape)}")
     if N and cache._device != dev:
         raise TypeError("the cache must live on the same CUDA device as the output")
-    ck = None if k_out is None else _heads(k_out, "k_out", dt, want, dev)
-    cv = None if v_out is None else _heads(v_out, "v_out", dt, want, dev)
+    ck = None if k_out is None else _heads(k_out, "k_out", None, want, dev)
+    cv = None if v_out is None else _heads(v_out, "v_out", None if k_out is None else dt, want, dev)
     at = _vector(slots, "slots", _I64, (N,), dev)
     q8._launch(dev, "sgemm_q8_cache_read", N, _TYPES[dt], c, at, ck, cv, q8._stream(stream, dev))
 
@@ -298,11 +306,14 @@ def attend_q8(q, cache, table, lens, out, scale=None, window: int = 0, lse=None,
         raise ValueError(f"q must have shape (sequences, a multiple of {cache.heads} heads, {cache.dim}), not {tuple(shape)}")
     if B and cache._device != dev:
         raise TypeError("the cache must live on the same CUDA device as the output")
-    cq, co = _heads(q, "q", dt, shape, dev), _heads(out, "out", dt, shape, dev)
+    cq, co = _heads(q, "q", None, shape, dev), _heads(out, "out", dt, shape, dev)
     tshape = q8._shape2(table, "table")
     if tshape[0] != B:
         raise ValueError(f"table must have shape ({B}, pages), not {tuple(tshape)}")
-    ldt = q8._matrix(table, "table", (_I32,), tshape, dev)
+    if table.dtype is _I32 and table.get_device() == dev >= 0 and table.is_contiguous():
+        ldt = tshape[1] or 1
+    else:                   # strided, empty, or wrong: says what
+        ldt = q8._matrix(table, "table", (_I32,), tshape, dev)
     pl = _vector(lens, "lens", _I32, (B,), dev)
     ps = None if lse is None else _vector(lse, "lse", _F32, (B, H), dev)
     q8._launch(dev, "sgemm_q8_attend", B, _TYPES[dt], cq, c, table.data_ptr(), ldt, tshape[1], pl,
