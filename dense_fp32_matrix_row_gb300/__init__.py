@@ -253,7 +253,8 @@ def sgemm_bf16(A, B, C, alpha: float = 1.0, beta: float = 0.0, stream=None) -> N
 
 
 def status(stream=None) -> int:
-    """Wait for ``stream`` and return (and clear) the device's kernel error status."""
+    """Wait for ``stream`` and return (and clear) the device's kernel error status: of two
+    kinds, a time-out first and an index outside its array by the next call."""
     return int(lib().sgemm_status(_stream_handle(stream)))
 
 

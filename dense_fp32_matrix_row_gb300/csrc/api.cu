@@ -344,6 +344,8 @@ namespace {
 
 // One thread waits on a barrier that nothing completes, with the library's
 // bounded wait, and records the time-out.
+__global__ void clear_error_kernel(unsigned *err, unsigned bits) { atomicAnd(err, ~bits); }
+
 __global__ void selftest_wait_kernel(unsigned *err, uint64_t wait_ns) {
     __shared__ uint64_t bar;
     if (threadIdx.x == 0) {
@@ -413,13 +415,14 @@ int sgemm_status(void *stream) {
     unsigned word = 0;
     if (cudaMemcpy(&word, st->err, sizeof(word), cudaMemcpyDeviceToHost) != cudaSuccess)
         return SGEMM_ERR_CUDA;
-    if (word != 0) {
-        const unsigned zero = 0;
-        if (cudaMemcpy(st->err, &zero, sizeof(zero), cudaMemcpyHostToDevice) != cudaSuccess)
-            return SGEMM_ERR_CUDA;
-        return (word & kErrWaitTimeout) != 0 ? SGEMM_ERR_TIMEOUT : SGEMM_ERR_BAD_INDEX;
-    }
-    return SGEMM_OK;
+    if (word == 0) return SGEMM_OK;
+    // What is reported is cleared, and nothing else: the other kind is the next call's, and
+    // kernels on other streams may be setting bits meanwhile.
+    const bool timeout = (word & kErrWaitTimeout) != 0;
+    clear_error_kernel<<<1, 1, 0, static_cast<cudaStream_t>(stream)>>>(st->err, timeout ? kErrWaitTimeout : ~kErrWaitTimeout);
+    if (cudaGetLastError() != cudaSuccess || cudaStreamSynchronize(static_cast<cudaStream_t>(stream)) != cudaSuccess)
+        return SGEMM_ERR_CUDA;
+    return timeout ? SGEMM_ERR_TIMEOUT : SGEMM_ERR_BAD_INDEX;
 }
 
 const char *sgemm_status_string(int status) {

@@ -492,6 +492,8 @@ int sgemm_q8_attend(int64_t B, int type, const sgemm_heads *q, const sgemm_q8_ca
  * kernel's bounded wait ran out since the last call (that kernel skipped its
  * stores and exited; C is unspecified), SGEMM_ERR_BAD_INDEX when a kernel met
  * an index outside its array (and did not follow it), or SGEMM_ERR_CUDA.
+ * Where both are to be told, this call returns (and clears) SGEMM_ERR_TIMEOUT
+ * and the next one SGEMM_ERR_BAD_INDEX.
  */
 int sgemm_status(void *stream);
 

@@ -188,3 +188,28 @@ def test_a_cache_with_a_tensor_replaced():
     cache.k = cache.v = cache.k_scale = cache.v_scale = None
     with pytest.raises(TypeError):
         sg.cache_write_q8(x, x, cache, slots)
+
+
+# ---- what is reported -----------------------------------------------------------------
+
+def test_status_tells_both_kinds():
+    """A time-out and an index outside its array, whichever came first."""
+    x = torch.randn((1, 2, 64), device="cuda")
+    tables = torch.ones((4, 32), device="cuda")
+    out = torch.empty_like(x)
+
+    def bad_index():
+        sg.norm_rope(x, None, tables, tables, out, None, positions=torch.tensor([9], device="cuda"))
+
+    def timeout():
+        assert sg.selftest_wait(1000) == sg.OK
+
+    for calls in ((bad_index, timeout), (timeout, bad_index), (timeout, bad_index, bad_index, timeout)):
+        for call in calls:
+            call()
+        assert [sg.status() for _ in range(3)] == [sg.ERR_TIMEOUT, sg.ERR_BAD_INDEX, sg.OK]
+    bad_index()
+    assert [sg.status() for _ in range(2)] == [sg.ERR_BAD_INDEX, sg.OK]
+    timeout()
+    other = torch.cuda.Stream()
+    assert [sg.status(other) for _ in range(2)] == [sg.ERR_TIMEOUT, sg.OK]
