@@ -1,7 +1,7 @@
 // attend.cuh -- attention of one new token per sequence over the 8-bit paged
 // cache, as a template over the heads' size (instantiated in attend_*.cu).
 //
-//     s_t = scale * q . k_t        p_t = 2^(s_t*log2(e) - m)        m: about the largest so far
+//     s_t = scale * q . k_t        p_t = 2^(s_t*log2(e) - m)        m: see consume()
 //     out = sum_t p_t v_t / sum_t p_t
 //
 // One pass over the cache.  Keys and values are whole numbers times a scale per
@@ -153,6 +153,12 @@ __device__ __forceinline__ uint32_t transpose8(uint32_t v) {
 __device__ __forceinline__ float exp2_fast(float x) {      // 2 units in the last place; 0 below 2^-126
     float y;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+__device__ __forceinline__ float log2_fast(float x) {      // -infinity for 0
+    float y;
+    asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
 }
 
@@ -369,8 +375,11 @@ __device__ __forceinline__ void store_out(const AttendParams &p, T *to, const fl
         for (int i = 0; i < 4; ++i) to[i] = from_f32<T>(v[i]);
     }
 }
+// (The logarithm of the mantissa alone: top may lie far from it.)
 __device__ __forceinline__ float lse_of(float top, float total) {
-    return total != 0.0f ? (top + log2f(total)) * 0.69314718055994531f : -INFINITY;
+    if (total == 0.0f) return -INFINITY;
+    const int e = min(exponent(total), 126);
+    return ((top + (float)e) + log2f(total * pow2(-e))) * 0.69314718055994531f;
 }
 
 // Four dims of a head's result; with d == 0 its lse too.
@@ -522,7 +531,7 @@ struct Attend {
     uint32_t qf[S::Q_SHARED ? 1 : NT][TERMS][S::STEPS][2];
     float qmul[NT][2];                  // turns a product into a score in base 2, without the key's scale
     float m[NT][2], sum[NT][2];         // of heads 2j and 2j + 1; sum: of this lane's tokens
-    float vmul, vcap;                   // a power of two that the probabilities carry; the largest scale it is for
+    float vmul, vcap;                   // a power of two that the value scales carry; the largest scale it is for
     float acc[S::STEPS][NT][4];
 
     // The queries of the key head at `at`, as they lie: this lane's chunks of one head
@@ -561,8 +570,8 @@ struct Attend {
         }
     }
 
-    // The same as the MMA's B, scaled by a power of two into FP16's range (below 2^15, so a
-    // BF16 query is exact).
+    // The same as the MMA's B, scaled by a power of two into FP16's range (below 2^15: a
+    // BF16 query is exact but for elements below 2^-31 of its largest).
     __device__ __forceinline__ void begin(const Cursor &at) {
         Queries x;
         fetch(x, at);
@@ -685,7 +694,7 @@ struct Attend {
         const uint32_t scales = at + 2 * S::ROWS;
         const float k0 = __uint_as_float(lds4(scales + 4 * g)), k1 = __uint_as_float(lds4(scales + 4 * g + 32));
         float v0 = __uint_as_float(lds4(scales + 64 + 4 * g)), v1 = __uint_as_float(lds4(scales + 64 + 4 * g + 32));
-        bool grown = false;
+        bool look = false;
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
             if constexpr (SPLIT) {
@@ -707,17 +716,17 @@ struct Attend {
             if (!on0) v0 = 0.0f;
             if (!on1) v1 = 0.0f;
         }
-        // The scaling by m and vmul is kept until a score passes m + 5 or a value's
-        // scale vcap: probabilities stay below 2^5 and their products with the scales,
-        // which vmul takes to [2^8, 2^10], below 2^15, in FP16's range.  FP16 rounds
-        // such a product to 11 bits, or to 2^-24 where it is below 2^-14: 2^-33 of the
-        // largest scale (p = 1), a token.
+        // FP16 takes the products p * (value scale) as x = p * u, u = scale * vmul.  vmul brings
+        // the largest scale so far to [2^8, 2^10]; m is the head's, and such that its largest x
+        // is between 2^8 and 2^15: both are kept until a scale passes vcap or an x 2^15.  FP16
+        // rounds an x to 11 bits, or to 2^-24 where it is below 2^-14: by 2^-33 of the head's
+        // largest product at most, whatever other tokens' scales are.  As u is at most 2^10,
+        // scores up to m + 5 need no closer look (one at every strip: 2% of the time).
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
-            grown |= fmaxf(sc[nt][0], sc[nt][2]) > m[nt][0] + 5.0f || fmaxf(sc[nt][1], sc[nt][3]) > m[nt][1] + 5.0f;
-        const float vm = fmaxf(fabsf(v0), fabsf(v1));
-        grown |= vm > vcap;
-        if (__any_sync(0xffffffffu, grown)) rescale(sc, vm);
+            look |= fmaxf(sc[nt][0], sc[nt][2]) > m[nt][0] + 5.0f || fmaxf(sc[nt][1], sc[nt][3]) > m[nt][1] + 5.0f;
+        look |= fmaxf(fabsf(v0), fabsf(v1)) > vcap;
+        if (__any_sync(0xffffffffu, look) && (vcap < 0.0f || grown(sc, v0, v1))) rescale(sc, v0, v1);
         const float u0 = v0 * vmul, u1 = v1 * vmul;
         uint32_t pf[NT][TERMS][2];
 #pragma unroll
@@ -799,33 +808,68 @@ struct Attend {
             }
     }
 
-    __device__ __forceinline__ void rescale(const float (&sc)[NT][4], float vm) {
+    // log2 of u's size, as m goes by it: at most 10, which no finite u passes, and at least -45,
+    // so that p stays below 2^60 where the values are (next to) nothing.
+    static __device__ __forceinline__ float size_of(float u) { return fminf(fmaxf(log2_fast(fabsf(u)), -45.0f), 10.0f); }
+
+    // Whether the scales that products carry have to change for this strip, by its largest ones.
+    __device__ __forceinline__ bool grown(const float (&sc)[NT][4], float v0, float v1) const {
+        const float l0 = size_of(v0 * vmul), l1 = size_of(v1 * vmul);
+        bool more = fmaxf(fabsf(v0), fabsf(v1)) > vcap;
 #pragma unroll
-        for (int o = 1; o < 32; o <<= 1) vm = fmaxf(vm, __shfl_xor_sync(0xffffffffu, vm, o));
-        float f = 1.0f;
-        if (vm > vcap) {
-            const int e = min(exponent(vm), 127);
-            const float to = pow2(8 - e);
-            f = vcap < 0.0f ? 1.0f : to / vmul;
-            vmul = to;
-            vcap = e < 126 ? pow2(e + 2) : INFINITY;
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int k = 0; k < 2; ++k) more |= fmaxf(sc[nt][k] + l0, sc[nt][k + 2] + l1) > m[nt][k] + 15.0f;
+        return __any_sync(0xffffffffu, more);
+    }
+
+    // A head's sums taken from m to another one, products' times f besides.
+    __device__ __forceinline__ void move(int nt, int k, float to, float f) {
+        const float d = exp2_fast(m[nt][k] - to);
+        m[nt][k] = to;
+        sum[nt][k] *= d;
+#pragma unroll
+        for (int i = 0; i < S::STEPS; ++i) {
+            acc[i][nt][k] *= d * f;
+            acc[i][nt][k + 2] *= d * f;
         }
+    }
+
+    // vmul for a larger scale than those so far.  What is there shrinks with it, and m goes
+    // down by as much, or later tokens like those would be rounded by the new scale's size.  (By
+    // less where sums of p would pass 2^60.)
+    __device__ __forceinline__ void take_scale(float vm) {
+        const int e = min(exponent(vm), 127);
+        const int down = vcap < 0.0f ? 0 : (int)(__float_as_uint(vmul) >> 23) - 127 - (8 - e);
+        vmul = pow2(8 - e);
+        vcap = e < 126 ? pow2(e + 2) : INFINITY;
+        if (down == 0) return;
+        const float f = down <= 126 ? pow2(-down) : 0.0f;
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
             for (int k = 0; k < 2; ++k) {
-                float x = fmaxf(sc[nt][k], sc[nt][k + 2]);
+                float s = sum[nt][k];
+#pragma unroll
+                for (int o = 4; o < 32; o <<= 1) s = fmaxf(s, __shfl_xor_sync(0xffffffffu, s, o));
+                move(nt, k, m[nt][k] - (float)min(down, max(60 - exponent(s), 0)), f);
+            }
+    }
+
+    __device__ __forceinline__ void rescale(const float (&sc)[NT][4], float v0, float v1) {
+        float vm = fmaxf(fabsf(v0), fabsf(v1));
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) vm = fmaxf(vm, __shfl_xor_sync(0xffffffffu, vm, o));
+        if (vm > vcap) take_scale(vm);
+        const float l0 = size_of(v0 * vmul) - 8.0f, l1 = size_of(v1 * vmul) - 8.0f;
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+                float x = fmaxf(sc[nt][k] + l0, sc[nt][k + 2] + l1);
 #pragma unroll
                 for (int o = 4; o < 32; o <<= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, o));
-                const float to = fmaxf(x, m[nt][k]);
-                const float d = exp2_fast(m[nt][k] - to);
-                m[nt][k] = to;
-                sum[nt][k] *= d;
-#pragma unroll
-                for (int i = 0; i < S::STEPS; ++i) {
-                    acc[i][nt][k] *= d * f;
-                    acc[i][nt][k + 2] *= d * f;
-                }
+                move(nt, k, fmaxf(x, m[nt][k]), 1.0f);
             }
     }
 

@@ -470,11 +470,13 @@ int sgemm_q8_cache_read(int64_t N, int type, const sgemm_q8_cache *cache, const 
  * B * cache->heads * g * (pages*page/16 + 2) is below 2^31 (SGEMM_ERR_TOO_LARGE), where g is
  * G = q->heads/cache->heads, but at most 2 * ceil(G/8): 2 for up to 8 query heads to a key head.
  * Several new tokens of a sequence are rows of their own, with a length each.
- * Scores, sums and results are FP32; the exponentials are rounded to 11 bits
- * for the product with the values (22 bits for type FP32; those below about
- * 2^-22 of the largest to 2^-33 of it), the queries for theirs likewise (a BF16
- * query is exact).  A row whose scale is NaN gives
- * NaN to the results that read it; rows that no sequence's tokens lie in may
+ * Scores, sums and results are FP32.  For the product with the values' whole
+ * numbers each exp(s_t) times its value scale is rounded to 11 bits (type FP32:
+ * 22), those below 2^-22 (FP32: 2^-11) of the head's largest such product by up
+ * to 2^-33 of that instead (or 2^-93 of the largest value scale, if that is more).
+ * Queries are taken exactly (FP32: to 22 bits), but for elements below 2^-31
+ * (FP32: 2^-17) of their head's largest, which are rounded by up to 2^-39 of it.
+ * A row whose scale is NaN gives NaN to the results that read it; rows that no sequence's tokens lie in may
  * hold anything.  Sums are taken in an order that depends on `lens` and the
  * GPU model alone.
  * Uses the stream's workspace for parts of long sequences (up to 25 MB, by the head

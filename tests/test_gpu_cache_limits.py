@@ -213,3 +213,117 @@ def test_status_tells_both_kinds():
     timeout()
     other = torch.cuda.Stream()
     assert [sg.status(other) for _ in range(2)] == [sg.ERR_TIMEOUT, sg.OK]
+
+
+# ---- values of unequal size -----------------------------------------------------------
+
+def products_bound(q, pool, table, lens, scale, bf16):
+    """(out, tol, lse, lse_tol) as cache_ref.attend gives them (its bounds are derived there),
+    but for the last term of tol: what FP16's smallest step leaves off a product
+    p * (value scale) goes by the head's largest such product, not by the largest scale.  In
+    the kernel's units the largest is at 2^8 or more and the step 2^-24, so each product is
+    off by at most 2^-33 of the largest, times a whole number of up to 127.  Where products
+    are below 2^-53 of (largest p) * (largest scale), sums of p end that: p is held up to
+    2^60, scales up to 2^8 or more, and the step is 2^-93 of them."""
+    _, _, lse, lse_tol = ref.attend(q, pool, table, lens, scale, 0, bf16)
+    B, H, D = q.shape
+    Hk, u, d = pool.heads, 2.0 ** -23, torch.float64
+    out, tol = (torch.zeros((B, H, D), dtype=d, device="cuda") for _ in range(2))
+    for b, n in enumerate(lens):
+        t = torch.arange(n, device="cuda")
+        block, row = table[b].long()[t // pool.page], t % pool.page
+        k = pool.k[block, :, row].to(d) * pool.k_scale[block, :, row].to(d)[..., None]
+        steps = pool.v_scale[block, :, row].to(d)                           # (n, Hk)
+        v = pool.v[block, :, row].to(d) * steps[..., None]
+        x = q[b].to(d).view(Hk, H // Hk, D)
+        s = torch.einsum("hgd,nhd->hgn", x, k) * scale
+        size = torch.einsum("hgd,nhd->hgn", x.abs(), k.abs()) * abs(scale)
+        p = torch.softmax(s, -1)
+        out[b] = torch.einsum("hgn,nhd->hgd", p, v).reshape(H, D)
+        eps = (10 + D / 8) * u * size.amax(-1) + 6 * u
+        weight = torch.einsum("hgn,nhd->hgd", p, v.abs())
+        product = (p * steps.abs().T[:, None]).amax(-1)                     # (Hk, G)
+        least = 127 * n * (2.0 ** -33 * product + 2.0 ** -93 * steps.abs().amax(0)[:, None])
+        tol[b] = (weight * (2 * eps + 2 * (n / 16 + 24) * u + (2.0 ** -11 if bf16 else 2.0 ** -21))[..., None]
+                  + least[..., None]).reshape(H, D)
+    return out, tol, lse, lse_tol
+
+
+def check_products(q, pool, table, lens, scale):
+    bf16 = q.dtype == torch.bfloat16
+    out, lse = torch.full_like(q, 9.0), torch.zeros(q.shape[:2], device="cuda")
+    sg.attend_q8(q, pool.cache(), table, torch.tensor(lens, dtype=torch.int32, device="cuda"), out, scale=scale, lse=lse)
+    assert sg.status() == sg.OK
+    want, tol, want_lse, lse_tol = products_bound(q, pool, table, lens, scale, bf16)
+    tol = tol + (2.0 ** -8 * (1 + 2.0 ** -6) * want.abs() if bf16 else 0) + 2.0 ** -140
+    over = (out.double() - want).abs() / tol
+    assert bool((over <= 1).all()), f"{int((over > 1).sum())} of {over.numel()} off, worst {float(over.max()):.3g}x the bound"
+    assert bool(((lse.double() - want_lse).abs() <= lse_tol).all())
+
+
+def scored(pool, table, lens, score, size):
+    """Gives token t of sequence b the score score[b][t] for a query of ones (in its first
+    dim alone) and scale 1, and the value scale size[b][t], for each key head."""
+    pool.k.zero_()
+    pool.k[..., 0] = 100
+    for b, n in enumerate(lens):
+        t = torch.arange(n, device="cuda")
+        block, row = table[b].long()[t // pool.page], t % pool.page
+        pool.k_scale[block, :, row] = (score[b].to("cuda") / 100).float()[:, None]
+        pool.v_scale[block, :, row] = size[b].to("cuda").float()[:, None]
+
+
+@pytest.mark.parametrize("dt", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("D,G", [(64, 4), (64, 12), (96, 7), (128, 8), (128, 24), (192, 5), (256, 8), (256, 3)])
+def test_small_values_of_large_weight(D, G, dt):
+    """Value scales over fifty powers of two, the smaller the more weight: heads that turn
+    the scores up, down or off."""
+    lens = [200, 90, 5000, 16, 7]
+    gen = torch.Generator()
+    gen.manual_seed(D + G)
+    pool = ref.Pool(sum(-(-n // 16) for n in lens) + 1, 2, 16, D, seed=G)
+    table, kept = pool.table(lens)
+    fall = [50 * torch.rand(n, generator=gen, dtype=torch.float64) for n in lens]
+    turn = [0.8 + 0.4 * torch.rand(n, generator=gen, dtype=torch.float64) for n in lens]
+    scored(pool, table, lens, [0.6931 * a * w for a, w in zip(fall, turn)], [2.0 ** -a for a in fall])
+    pool.poison(kept)
+    q = torch.zeros((len(lens), 2 * G, D), device="cuda")
+    q[..., 0] = torch.linspace(-0.5, 1.0, 2 * G, device="cuda")
+    check_products(q.to(dt), pool, table, lens, 1.0)
+
+
+@pytest.mark.parametrize("dt", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("ratio", [2.0 ** -11, 2.0 ** -16, 2.0 ** -24, 2.0 ** -36, 2.0 ** -44, 0.0])
+@pytest.mark.parametrize("at", [(0, 3), (3, 0), (2, 40), (40, 2), (17, 150)])
+def test_one_small_value_beside_a_large_one(at, ratio, dt):
+    """All weight on a token whose values are `ratio` of another's, which comes before it,
+    behind it, or in its strip of 16; more tokens like it follow."""
+    n = 160         # ten strips: one warp's
+    pool = ref.Pool(12, 1, 16, 64, seed=3)
+    table, _ = pool.table([n])
+    score, size = torch.zeros(n, dtype=torch.float64), torch.full((n,), ratio / 2, dtype=torch.float64)
+    small, large = at
+    score[small], size[small] = 50.0, ratio
+    score[100:103], size[100:103] = 50.0, ratio
+    size[large] = 1.0
+    scored(pool, table, [n], [score], [size])
+    q = torch.zeros((1, 4, 64), device="cuda")
+    q[..., 0] = torch.tensor([1.0, 0.9, 0.0, -1.0], device="cuda")
+    check_products(q.to(dt), pool, table, [n], 1.0)
+
+
+@pytest.mark.parametrize("dt", [torch.bfloat16, torch.float32])
+def test_values_that_grow_while_scores_fall(dt):
+    """Each strip's values are larger and its scores lower than the last one's, and the
+    other way round: every strip changes how products are scaled."""
+    n = 160
+    for sign in (1, -1):
+        for slope in (0.5, 1.0, 1.5):
+            pool = ref.Pool(12, 1, 16, 128, seed=4)
+            table, _ = pool.table([n])
+            t = torch.arange(n, dtype=torch.float64)
+            t = t if sign > 0 else n - 1 - t
+            scored(pool, table, [n], [-0.6931 * slope * t], [2.0 ** (t - 100)])
+            q = torch.zeros((1, 3, 128), device="cuda")
+            q[..., 0] = torch.tensor([1.0, 0.75, 0.25], device="cuda")
+            check_products(q.to(dt), pool, table, [n], 1.0)
