@@ -188,6 +188,8 @@ __device__ __forceinline__ void pair_tokens(uint32_t a, uint32_t b, uint32_t (&r
 
 // 2^e for -126 <= e <= 127.
 __device__ __forceinline__ float pow2(int e) { return __uint_as_float((uint32_t)(e + 127) << 23); }
+// 1 / v for a power of two from 2^-126 to 2^126.
+__device__ __forceinline__ float inverse_pow2(float v) { return __uint_as_float(0x7f000000u - __float_as_uint(v)); }
 // e with 2^e <= v < 2^(e+1) for a finite v >= 2^-118; -118 below, 128 beyond.
 __device__ __forceinline__ int exponent(float v) { return max(-118, (int)((__float_as_uint(v) >> 23) & 0xff) - 127); }
 
@@ -869,7 +871,7 @@ struct Attend {
                 float x = fmaxf(sc[nt][k] + l0, sc[nt][k + 2] + l1);
 #pragma unroll
                 for (int o = 4; o < 32; o <<= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, o));
-                move(nt, k, fmaxf(x, m[nt][k]), 1.0f);
+                move(nt, k, fmaxf(floorf(x), m[nt][k]), 1.0f);      // a whole number, for lower()
             }
     }
 
@@ -891,31 +893,48 @@ struct Attend {
                 for (int o = 4; o < 32; o <<= 1) sum[nt][k] += __shfl_xor_sync(0xffffffffu, sum[nt][k], o);
     }
 
-    // Calls f(head, dim, four sums from dim on, k, nt) for all this lane holds.
-    template <typename F>
-    __device__ __forceinline__ void each(F f) const {
-        const float unscale = 1.0f / vmul;
+    // For sums that are to be joined with others' and might pass FP32's range then (the values
+    // beyond 2^40, or p far beyond 1): sums over 2^k, with m + k, exactly (both are whole
+    // numbers).  The sum of p becomes 1/2 to 1, times 2^-12, as several thousand parts may be joined.
+    __device__ __forceinline__ void lower() {
+        bool far = vmul < pow2(-40);
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) far |= fmaxf(sum[nt][0], sum[nt][1]) > pow2(30);
+        if (!__any_sync(0xffffffffu, far)) return;
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-            for (int k = 0; k < 2; ++k)
+            for (int k = 0; k < 2; ++k) {
+                const int over = min(exponent(sum[nt][k]) + 13, 126);
+                const float down = pow2(-over);
+                m[nt][k] += (float)over;
+                sum[nt][k] *= down;
 #pragma unroll
-                for (int i = 0; i < S::STEPS; i += 2)
-                    f(nt * 8 + 2 * j + k, dim_of(i),
-                      make_float4(acc[i][nt][k] * unscale, acc[i][nt][k + 2] * unscale, acc[i + 1][nt][k] * unscale,
-                                  acc[i + 1][nt][k + 2] * unscale),
-                      m[nt][k], sum[nt][k]);
+                for (int i = 0; i < S::STEPS; ++i) {
+                    acc[i][nt][k] *= down;
+                    acc[i][nt][k + 2] *= down;
+                }
+            }
     }
 
     // As a part: see part_at.
-    __device__ __forceinline__ void store(float *part) const {
-        each([&](int head, int d, float4 o, float top, float sum_p) {
-            *reinterpret_cast<float4 *>(part + part_at<DT>(head, d)) = o;
-            if (d == 0) *reinterpret_cast<float2 *>(part + S::HEADS * DT + 2 * head) = make_float2(top, sum_p);
-        });
+    __device__ __forceinline__ void store(float *part) {
+        lower();
+        const float w = inverse_pow2(vmul);
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+                const int head = nt * 8 + 2 * j + k;
+#pragma unroll
+                for (int i = 0; i < S::STEPS; i += 2)
+                    *reinterpret_cast<float4 *>(part + part_at<DT>(head, dim_of(i))) =
+                        make_float4(acc[i][nt][k] * w, acc[i][nt][k + 2] * w, acc[i + 1][nt][k] * w, acc[i + 1][nt][k + 2] * w);
+                if (g == 0) *reinterpret_cast<float2 *>(part + S::HEADS * DT + 2 * head) = make_float2(m[nt][k], sum[nt][k]);
+            }
     }
     __device__ __forceinline__ void finish(const Cursor &at) const {
-        const float unscale = 1.0f / vmul;
+        const float w = inverse_pow2(vmul);
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -927,8 +946,8 @@ struct Attend {
 #pragma unroll
                 for (int i = 0; i < S::STEPS; i += 2) {
                     const int d = dim_of(i);
-                    const float v[4] = {acc[i][nt][k] * unscale * inv, acc[i][nt][k + 2] * unscale * inv,
-                                        acc[i + 1][nt][k] * unscale * inv, acc[i + 1][nt][k + 2] * unscale * inv};
+                    const float v[4] = {acc[i][nt][k] * inv * w, acc[i][nt][k + 2] * inv * w, acc[i + 1][nt][k] * inv * w,
+                                        acc[i + 1][nt][k + 2] * inv * w};
                     if (d < p.D) store_out<T>(p, to + d, v);
                 }
                 if (g == 0 && p.lse) p.lse[(at.b * (int64_t)p.Hk + at.h) * p.G + head] = lse_of(m[nt][k], total);

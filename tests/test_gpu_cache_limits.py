@@ -327,3 +327,37 @@ def test_values_that_grow_while_scores_fall(dt):
             q = torch.zeros((1, 3, 128), device="cuda")
             q[..., 0] = torch.tensor([1.0, 0.75, 0.25], device="cuda")
             check_products(q.to(dt), pool, table, [n], 1.0)
+
+
+@pytest.mark.parametrize("dt", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("G,D,lens", [(4, 64, [30, 1]), (9, 96, [200, 17]), (8, 128, [5000, 160]), (20, 128, [40, 9000]),
+                                      (8, 192, [3000]), (4, 256, [16000]), (1, 64, [60000])])
+def test_values_near_the_end_of_the_range(G, D, lens, dt):
+    """Sums of values that pass FP32's range, whose mean does not: one warp's, several
+    warps', several blocks'."""
+    pool = ref.Pool(sum(-(-n // 16) for n in lens) + 1, 1, 16, D, seed=D)
+    table, kept = pool.table(lens)
+    pool.v.copy_(pool.v // 16 + 100)            # 92 to 107
+    pool.v_scale.copy_(3e36 * (0.9 + 0.1 * torch.rand_like(pool.v_scale)))
+    pool.poison(kept)
+    gen = torch.Generator(device="cuda")
+    gen.manual_seed(5)
+    q = torch.randn((len(lens), G, D), device="cuda", generator=gen).to(dt)
+    check_products(q, pool, table, lens, D ** -0.5)
+
+
+@pytest.mark.parametrize("dt", [torch.bfloat16, torch.float32])
+def test_values_of_all_sizes_in_one_sequence(dt):
+    """Runs of 300 tokens from 1e-33 to 3e36, in several blocks: parts that are scaled
+    differently are joined, whichever have the weight."""
+    lens, D = [9000], 128
+    n = lens[0]
+    for slope in (0.0, 1.0, -1.0):
+        pool = ref.Pool(570, 2, 16, D, seed=8)
+        table, _ = pool.table(lens)
+        run = (torch.arange(n) // 300).double()         # 0 to 29
+        size = 3e36 * 10.0 ** (-69 * run / 29)
+        scored(pool, table, lens, [slope * 2.0 * run], [size])
+        q = torch.zeros((1, 10, D), device="cuda")
+        q[..., 0] = torch.linspace(0.2, 1.0, 10, device="cuda")
+        check_products(q.to(dt), pool, table, lens, 1.0)
