@@ -1,6 +1,8 @@
 """The attention operators over the 8-bit cache at the ends of their ranges: strides,
 counts and magnitudes, and what they report."""
 
+import threading
+
 import pytest
 
 pytestmark = pytest.mark.gpu
@@ -361,3 +363,48 @@ def test_values_of_all_sizes_in_one_sequence(dt):
         q = torch.zeros((1, 10, D), device="cuda")
         q[..., 0] = torch.linspace(0.2, 1.0, 10, device="cuda")
         check_products(q.to(dt), pool, table, lens, 1.0)
+
+
+# ---- host threads ---------------------------------------------------------------------
+
+def test_every_call_of_several_threads():
+    """Threads on one stream and on streams of their own, sequences that many blocks share
+    (parts and counters in the streams' workspaces): each call's own result, in arrays of
+    its own, is compared."""
+    calls, lens = 40, [[5990, 3000], [11, 7000], [6000, 1], [2500, 2500]]
+    shared = torch.cuda.Stream()
+    streams = [shared, shared, torch.cuda.Stream(), torch.cuda.Stream()]
+    work, want = [], []
+    for i in range(4):
+        Hk, G, D = (2, 4, 64) if i % 2 else (1, 12, 128)
+        pool = ref.Pool(sum(-(-n // 16) for n in lens[i]), Hk, 16, D, seed=i)
+        table, _ = pool.table(lens[i], seed=i)
+        q = torch.randn((2, Hk * G, D), device="cuda").bfloat16()
+        outs = torch.full((calls,) + q.shape, float("nan"), device="cuda", dtype=q.dtype)
+        lses = torch.full((calls,) + q.shape[:2], float("nan"), device="cuda")
+        args = (q, pool.cache(), table, torch.tensor(lens[i], dtype=torch.int32, device="cuda"))
+        out, lse = torch.empty_like(q), torch.empty(q.shape[:2], device="cuda")
+        sg.attend_q8(*args, out, lse=lse)
+        work.append((args, outs, lses))
+        want.append((out, lse))
+    torch.cuda.synchronize()
+    begin, faults = threading.Barrier(4), []
+
+    def run(i):
+        try:
+            args, outs, lses = work[i]
+            begin.wait(60)
+            for k in range(calls):
+                sg.attend_q8(*args, outs[k], lse=lses[k], stream=streams[i])
+            streams[i].synchronize()
+        except Exception as e:      # noqa: BLE001
+            faults.append(repr(e))
+
+    threads = [threading.Thread(target=run, args=(i,)) for i in range(4)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not faults and sg.status() == sg.OK
+    for (_, outs, lses), (out, lse) in zip(work, want):
+        assert torch.equal(outs, out.expand_as(outs)) and torch.equal(lses, lse.expand_as(lses))
