@@ -265,7 +265,7 @@ __device__ __forceinline__ int tokens_of(const AttendParams &p, int b) {
 struct Cursor {
     int b, h, group, strip;
     Span span;
-    // Only where another strip follows in the list.
+    // Only where another strip follows in the list, by the whole warp.
     __device__ __forceinline__ void step(const AttendParams &p) {
         if (++strip < span.strips) return;
         strip = 0;
@@ -273,8 +273,17 @@ struct Cursor {
         group = 0;
         if (++h < p.Hk) return;
         h = 0;
-        do span = span_of(p, tokens_of(p, ++b));
-        while (span.strips == 0 && b + 1 < p.B);
+        // the next sequence with tokens: the warp looks at 32 at a time
+        const int lane = threadIdx.x & 31;
+        for (++b;; b += 32) {
+            const int n = b + lane < p.B ? tokens_of(p, b + lane) : 0;
+            const uint32_t some = __ballot_sync(0xffffffffu, n > 0);
+            if (some == 0 && b + 32 < p.B) continue;
+            const int k = max(__ffs(some) - 1, 0);
+            b += k;
+            span = span_of(p, __shfl_sync(0xffffffffu, n, k));
+            return;
+        }
     }
 };
 
