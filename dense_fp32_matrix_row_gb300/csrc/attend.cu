@@ -56,7 +56,7 @@ cudaError_t launch_attend(const AttendArgs &a, void *workspace, unsigned *ticket
     p.chunk_mul = 65536 / (a.D / 16) + 1;      // above 2^16 / chunks by at most 1
     p.whole = p.page % kStrip == 0;
     p.window = a.window;
-    p.scale_log2 = a.scale * 1.44269504088896341f;
+    p.scale_log2 = a.scale * kLog2e;
     p.q = a.q.p; p.q_ld = a.q.ld; p.q_hs = a.q.hs; p.q_vec = aligned16(a.q, es);
     p.out = a.out.p; p.o_ld = a.out.ld; p.o_hs = a.out.hs; p.o_vec = aligned16(a.out, es);
     p.k = a.cache.k; p.v = a.cache.v; p.ks = a.cache.k_scale; p.vs = a.cache.v_scale;

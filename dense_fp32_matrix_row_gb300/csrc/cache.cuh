@@ -13,6 +13,9 @@ constexpr unsigned kErrBadIndex = 2u;
 // Heads whose keys and values the operators take: multiples of 16 elements.
 constexpr int64_t kCacheMaxDim = 256;
 
+// Attention takes its scores in base 2: a scale times this has to be finite.
+constexpr float kLog2e = 1.44269504088896341f;
+
 struct HeadRowsArgs {
     int64_t T;
     int D, type;

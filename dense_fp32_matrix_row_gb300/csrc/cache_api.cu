@@ -345,7 +345,7 @@ int sgemm_q8_attend(int64_t B, int type, const sgemm_heads *q, const sgemm_q8_ca
     int rc = check_cache(cache);
     if (rc != SGEMM_OK) return rc;
     if (B < 0 || B > (1 << 30) || pages < 0 || pages > INT32_MAX / cache->page) return SGEMM_ERR_BAD_DIM;
-    if (!known_type(type) || !std::isfinite(scale) || window < 0) return SGEMM_ERR_BAD_ARG;
+    if (!known_type(type) || !std::isfinite(scale * kLog2e) || window < 0) return SGEMM_ERR_BAD_ARG;
     if (B == 0) return SGEMM_OK;
     if (!there(q) || !there(out) || lens == nullptr || (table == nullptr && pages > 0)) return SGEMM_ERR_NULL_PTR;
     rc = check_heads(q, B, cache->dim, type, false);

@@ -466,6 +466,7 @@ int sgemm_q8_cache_read(int64_t N, int type, const sgemm_q8_cache *cache, const 
  *   lens        B lengths.  A negative one counts as 0, one beyond pages*page as
  *               that many (both reported).  Tokens of a page outside the cache
  *               are left out (reported).
+ *   scale       finite, and so in base 2: up to 2.35e38 in size (SGEMM_ERR_BAD_ARG)
  *   lse         B x q->heads floats (natural logarithms), or NULL
  * B * cache->heads * g * (pages*page/16 + 2) is below 2^31 (SGEMM_ERR_TOO_LARGE), where g is
  * G = q->heads/cache->heads, but at most 2 * ceil(G/8): 2 for up to 8 query heads to a key head.

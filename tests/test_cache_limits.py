@@ -60,3 +60,11 @@ def test_strips_that_fit_the_list(fn, B, n, key_heads, pages):
 def test_strips_that_do_not(fn, B, n, key_heads, pages):
     q = heads(A[0], n, ld=0)
     assert attend(fn, B=B, q=q, out=heads(A[1], n), c=pool(heads=key_heads), pages=pages, ldt=pages) == sg.ERR_TOO_LARGE
+
+
+def test_scales_that_are_finite_in_base_2_too(fn):
+    """Scores are taken in base 2: a scale that is not finite times log2(e) would make them NaN."""
+    for scale in (2.359e38, 2.36e38, 3.4e38, -2.36e38, -3.4e38):
+        assert attend(fn, q=heads(A[1], 4), scale=scale) == sg.ERR_BAD_ARG
+    for scale in (2.358e38, -2.35e38, 0.0, 1e-45):
+        assert attend(fn, q=heads(A[1], 4), scale=scale) == sg.ERR_ALIAS
