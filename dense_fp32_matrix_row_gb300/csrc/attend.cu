@@ -11,9 +11,9 @@ namespace {
 int padded(int D) { return D <= 64 ? 64 : D <= 96 ? 96 : D <= 128 ? 128 : D <= 192 ? 192 : 256; }
 
 // Sets of 8 MMA columns.  More than 8 query heads to a key head take up to four sets,
-// which read a strip once for all (8 key heads, 16 sequences of 16384: 16 heads of 64 71 us against
-// 113 for two sets of 8 one after the other, 128: 106 and 172; 24 heads of 64 89 against 139 for two
-// times two sets, 128: 140 and 214; 32 heads 102 and 139, 164 and 214; FP32, three sets against two
+// which read a strip once for all (8 key heads, 16 sequences of 16384: 16 heads of 64 73 us against
+// 113 for two sets of 8 one after the other, 128: 107 and 172; 24 heads of 64 91 against 139 for two
+// times two sets, 128: 141 and 214; 32 heads 106 and 139, 168 and 214; FP32, three sets against two
 // times two, 64: 120 and 199, 128: 200 and 306).  Heads of 192 take two (16 heads
 // 155 us, 8 139; FP32 217 and 147), of 256 two, in FP32 one: more leave too few registers or warps (24
 // heads of 256 in three sets 398 us, in two times two 362; FP32, two sets 213, two times one 200).

@@ -26,20 +26,15 @@
 // head that several warps share is summed at the end, first within the block,
 // then by the last of the blocks that share it, always in the same order.
 //
-// Bound by memory as long as sequences are long.  Measured (bf16, 8 key heads of 128, 8
+// Bound by memory as long as sequences are long, by latency where they are short, and by
+// issue slots with many query heads to a key head.  Measured (bf16, 8 key heads of 128, 8
 // query heads to each; copies alone, without any arithmetic, stream at 7.0 TB/s):
-//   64 sequences of 16384 tokens, 2.2 GB, 330 us, 6.7 TB/s;
+//   64 sequences of 16384 tokens, 2.2 GB, 328 us, 6.8 TB/s;
 //   64 of 1024 to 8192, 602 MB, 107 us: 3 us until the first copies, 5 to 8 of sums
 //     at the end, while other SMs still load memory;
-//   one of 131072 (4 heads to each), 277 MB, 52 us, the same;
-//   one of 500, 8.1 us: two strips a warp (1.1 us each), four dependent loads before
+//   one of 131072 (4 heads to each), 277 MB, 52 us, the same; one of 8192, 17 MB, 14 us;
+//   one of 500, 8.2 us: two strips a warp (1.1 us each), four dependent loads before
 //     them (length, page number, queries, strip), two sums behind them.
-// Other divisions, measured with those four: rounds of a strip for each of a block's
-// warps, with barriers where key heads end, by 4 warps (4 blocks an SM) 380, 119, 63 and 9.5
-// us, 8 warps 367, 125, 58 and 8.7, 16 warps 363, 151, 59 and 10.2; joining blocks where a
-// key head ends instead of at the end, 26 us more for the first.  No gain: queries
-// loaded before the first strips (registers, or through the ring), page numbers by 32,
-// one loop for the ring's filling and its use, deeper batches in the joins.
 #pragma once
 
 #include <atomic>
@@ -806,7 +801,8 @@ struct Attend {
                 if constexpr (SPLIT) {
                     // An MMA cuts off what its sum has no room for: over hundreds of strips that
                     // is several units in FP32's last place, so strips are added up outside (which
-                    // took 64 x 16384 tokens from 3.9e-6 to 0.9e-6 off).
+                    // took 64 x 16384 tokens from 3.9e-6 to 0.9e-6 off; a BF16 result is rounded
+                    // by a thousand times that).
                     float strip[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
                     for (int t = TERMS - 1; t >= 0; --t)

@@ -11,15 +11,18 @@
 // of a rotation is rounded by itself (no fused multiply-add), which makes q the
 // same whole numbers wherever they are computed.
 //
-// Bound by memory, and in bf16 nearly by instructions: every head is read and
-// written once.  A group of 8, 16 or 32 lanes holds a head, 8 elements a lane: four
+// Every head is read and written once.  FP32 is bound by memory; in bf16 neither memory
+// nor the issue slots are full (67% of them taken, a quarter of a warp's time spent
+// waiting for loads, and a quarter ready behind another warp).  A group of 8, 16 or 32 lanes holds a head, 8 elements a lane: four
 // pairs, whose angles belong to the lane and serve all the heads that the group
 // takes of a token.
 //
 // Measured: 8192 tokens of 32 + 8 heads of 128, bf16, 172 MB, 31.5 us, 5.5 TB/s (82% of
-// a copy's; issue slots 73% taken); in FP32, 340 MB, 51.2 us, 6.6 TB/s.  With keys and
-// 8 heads of values into the cache, 190 MB, 40.6 us.  18432 tokens of 8 + 8 heads read
-// back, 114 MB, 20.1 us, 5.7 TB/s.  One token 1.5 us.  Not kept (first case): 16 elements
+// a copy's); in FP32, 340 MB, 51.2 us, 6.6 TB/s.  With keys and 8 heads of values into
+// the cache, 189 MB, 41.2 us, 4.6 TB/s (69%; FP32, 357 MB, 61.5 us, 87%): its blocks hold
+// more registers, eight to an SM instead of nine.  Keys and values alone, 32768 tokens of
+// 8 + 8 heads, 204 MB, 58.3 us (52%).  18432 tokens of 8 + 8 heads read back, 114 MB, 20.1
+// us, 5.7 TB/s (85%).  One token 1.5 us.  Not kept (first case): 16 elements
 // a lane 40 us, eight heads to a group one half after the other 44, one kernel for
 // floats and cache 33.0, a question for each load whether its head is there 34.8.
 #include "cache.cuh"

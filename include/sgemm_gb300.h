@@ -480,8 +480,9 @@ int sgemm_q8_cache_read(int64_t N, int type, const sgemm_q8_cache *cache, const 
  * A row whose scale is NaN gives NaN to the results that read it; rows that no sequence's tokens lie in may
  * hold anything.  Sums are taken in an order that depends on `lens` and the
  * GPU model alone.
- * Uses the stream's workspace for parts of long sequences (up to 25 MB, by the head
- * size and the heads to a key head, not by lengths), grown like sgemm()'s, and a
+ * Uses the stream's workspace for parts of long sequences (by the head size and the
+ * heads to a key head, not by lengths; at most 25.3 MB on 152 SMs, in a buffer of whole
+ * 2 MiB that grows by half at least), grown like sgemm()'s, and a
  * small array of counters kept per stream beside it; the same rules for stream
  * capture and for graphs that share a capture stream hold for both.
  */
