@@ -727,7 +727,7 @@ struct Attend {
         // is between 2^8 and 2^15: both are kept until a scale passes vcap or an x 2^15.  FP16
         // rounds an x to 11 bits, or to 2^-24 where it is below 2^-14: by 2^-33 of the head's
         // largest product at most, whatever other tokens' scales are.  As u is at most 2^10,
-        // scores up to m + 5 need no closer look (one at every strip: 2% of the time).
+        // scores up to m + 5 need no closer look (one at every strip: 2 to 4% of the time).
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
             look |= fmaxf(sc[nt][0], sc[nt][2]) > m[nt][0] + 5.0f || fmaxf(sc[nt][1], sc[nt][3]) > m[nt][1] + 5.0f;
